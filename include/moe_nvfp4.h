@@ -10,7 +10,14 @@
  *   moe_finalize            ordered FP32 combine of unfinalized rows (standalone)
  *   moe_routed_forward      all of the above in one call, from BF16 hidden states
  *
- * plus one-time weight preparation (moe_quantize_weights, moe_prepare_weights).
+ * plus one-time weight preparation (moe_quantize_weights, moe_prepare_weights), and the
+ * operators around the routed experts in a decoder layer, in the same formats:
+ *
+ *   moe_add_rmsnorm         residual addition, RMS norm, BF16 and scaled E4M3 outputs
+ *   moe_linear_fp4          a few tokens times one dense NVFP4 matrix (projections, shared
+ *                           experts, the output head), with an optional activation
+ *   moe_kv_append           BF16 keys and values -> a paged NVFP4 cache
+ *   moe_kv_attend           queries of a decode step against that cache
  *
  * Conventions shared by every entry point:
  *  - Every pointer argument is a DEVICE pointer unless stated otherwise, owned by
@@ -71,6 +78,8 @@ typedef enum {
 #define MOE_DEV_DUPLICATE_EXPERT 1 /* a token names the same local expert twice ([CUDNN] "distinct experts") */
 #define MOE_DEV_TIMEOUT 2          /* a bounded wait in a GEMM kernel gave up after 2 s; the kernel
                                       abandoned its remaining tiles and returned (outputs undefined) */
+#define MOE_DEV_BAD_INDEX 4        /* a cache slot, page id or sequence length outside the cache; what it
+                                      names is skipped */
 
 /* Expert activations. [MCORE] flashinfer_routed_nvfp4_moe(activation_type): squared-ReLU or
  * SwiGLU experts; [CUDNN] Activation functions: SwiGLU with default scalars, GeGLU, GELU, ReLU,
@@ -349,6 +358,133 @@ MOE_API moe_status_t moe_routed_forward(const uint16_t* x, int32_t M, int64_t ld
                                         int32_t* token_to_row, void* workspace, size_t workspace_bytes,
                                         int32_t* dev_status, void* const* step_events, int32_t num_step_events,
                                         moe_stream_t stream);
+
+/* ========================================================================================
+ * Operators around the routed experts in a decoder layer. They share the conventions at the
+ * top of this file; every call below is one kernel launch unless it says otherwise.
+ * ======================================================================================== */
+
+/* Scales of an E4M3 matrix [M, H]: none (not an E4M3 matrix), one FP32 scale per row ([M]), or
+ * one per MOE_FP8_GROUP consecutive columns ([M, ceil(H / 128)], the last group may be short).
+ * A stored value stands for code * scale. */
+typedef enum { MOE_FP8_NONE = 0, MOE_FP8_PER_TOKEN = 1, MOE_FP8_PER_GROUP = 2 } moe_fp8_scale_t;
+#define MOE_FP8_GROUP 128
+
+/* ----------------------------------------------------------------------------------------
+ * moe_add_rmsnorm - root-mean-square norm with the residual's addition, per row:
+ *   h = x (+ residual)                        FP32, not rounded before the norm
+ *   f = h * rsqrt(mean(h^2) + eps) * weight   FP32 throughout
+ *   residual_out = bf16(h), y = bf16(f), and for the E4M3 output, per scale group,
+ *   scale = amax|f| / 448 (1 when amax is 0), y8 = e4m3(f * (448 / amax)), rounded to nearest
+ *   even and saturated.
+ *   x            [M, ld_x] BF16 (first H columns used), ld_x >= H
+ *   residual     [M, ld_r] BF16 or NULL (no addition; residual_out must then be NULL)
+ *   weight       [H] BF16
+ *   eps          finite, >= 0
+ *   fp8_scale    moe_fp8_scale_t of y8; MOE_FP8_NONE when y8 and y8_scale are NULL
+ *   y            [M, H] BF16 (out) or NULL;  y8 [M, H] E4M3 (out) or NULL, one of them is needed
+ *   y8_scale     [M] or [M, ceil(H / 128)] FP32 (out), with y8
+ *   residual_out [M, H] BF16 (out) or NULL; may be `residual` itself when ld_r == H
+ * 1 <= H <= 32768, any H (rows of odd sizes take a scalar path). M == 0 is a no-op. NaN and
+ * infinite inputs make NaN (or infinite) outputs and scales in their own row.
+ * ---------------------------------------------------------------------------------------- */
+MOE_API moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ld_x, const uint16_t* residual, int64_t ld_r,
+                                     const uint16_t* weight, int32_t M, int32_t H, float eps, int32_t fp8_scale,
+                                     uint16_t* y, uint16_t* residual_out, uint8_t* y8, float* y8_scale,
+                                     moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * moe_linear_fp4 - y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]) for a few tokens, the
+ * weights read once per 16 tokens:
+ *   x          [M, ld_x] BF16 (x_scale_mode MOE_FP8_NONE; ld_x % 8 == 0) or E4M3 (MOE_FP8_PER_TOKEN
+ *              or MOE_FP8_PER_GROUP; ld_x % 16 == 0), first K columns used. The activations are
+ *              not rounded any further; E4M3 values are multiplied by their scale in FP32
+ *   x_scale    [M] or [M, ceil(K / 128)] FP32, NULL for BF16
+ *   w, w_sf    [N, K/2] packed E2M1 and [N, K/16] E4M3, linear, as moe_quantize_weights writes them
+ *   alpha      device scalar (FP32), the matrix's global decode scale
+ *   activation moe_activation_t. The gated kinds take w rows [gate; up] (N even) and write N/2
+ *              columns; MOE_ACT_IDENTITY is a plain product
+ *   out        [M, N] (gated: [M, N/2]) BF16, contiguous: FP32 sums, one rounding at the end
+ * K % 16 == 0, 16 <= K <= 65536, N >= 1. Rows of w are read in 16-byte pieces when K % 32 == 0
+ * and in 8-byte pieces otherwise. Any M; M <= 16 is what it is made for. M == 0 is a no-op.
+ * ---------------------------------------------------------------------------------------- */
+MOE_API moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode,
+                                    int32_t M, int32_t K, const uint8_t* w, const uint8_t* w_sf, const float* alpha,
+                                    int32_t N, int32_t activation, uint16_t* out, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * A paged key/value cache in NVFP4. Per page and kv head the codes and the scales of
+ * page_size tokens are contiguous:
+ *   k, v        [num_pages, num_kv_heads, page_size, head_dim/2]  packed E2M1
+ *   k_sf, v_sf  [num_pages, num_kv_heads, page_size, head_dim/16] E4M3
+ * with data_page_stride / sf_page_stride BYTES between pages (at least one page, multiples of
+ * 16), so keys and values may share one allocation. k_scale and v_scale are the static FP32
+ * encode scales g of the block rule of moe_quantize_input (finite, > 0): a stored value stands for
+ * code * scale / g. head_dim is 64 or 128; page_size a power of two, 16 to 256. A slot is
+ * page * page_size + place in the page.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* k;
+  uint8_t* k_sf;
+  uint8_t* v;
+  uint8_t* v_sf;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int64_t data_page_stride;
+  int64_t sf_page_stride;
+  float k_scale;
+  float v_scale;
+} moe_kv_cache_t;
+
+/* ----------------------------------------------------------------------------------------
+ * moe_kv_append - encodes N new tokens' keys and values with the block rule of
+ * moe_quantize_input and stores them.
+ *   k_new, v_new  [N, ld_k / ld_v] BF16, the num_kv_heads * head_dim values of a token
+ *                 contiguous; ld % 8 == 0 (slices of one projection's output will do)
+ *   slots         [N] int64 distinct slots; negative: the token is not stored. A slot past the
+ *                 cache is skipped and sets MOE_DEV_BAD_INDEX
+ *   k_seen, v_seen  [N, num_kv_heads, head_dim] BF16 (out, both or neither): what the cache holds
+ *                 for each token, bf16(code * scale / g), for callers that go on with the values
+ *                 later steps will see; written for tokens without a slot too
+ *   dev_status    may be NULL
+ * N == 0 is a no-op.
+ * ---------------------------------------------------------------------------------------- */
+MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const uint16_t* k_new, int64_t ld_k,
+                                   const uint16_t* v_new, int64_t ld_v, const int64_t* slots, int32_t N,
+                                   uint16_t* k_seen, uint16_t* v_seen, int32_t* dev_status, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * moe_kv_attend - attention of a decode step over the cache. Sequence b holds
+ * seq_lens[b] tokens, its q_len new ones last; query row t of sequence b sees its first
+ * seq_lens[b] - (q_len - 1) + t tokens (causal among the new ones):
+ *   s_j = softmax_scale * q . k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = ln sum_j exp(s_j)
+ * for query head h with the keys and values of kv head h / (num_q_heads / num_kv_heads). A row
+ * that sees nothing gets out = 0 and lse = -inf. Whatever the cache holds past a sequence's
+ * end is never used.
+ *   q           [batch * q_len, ld_q] BF16, the num_q_heads * head_dim values of a row contiguous;
+ *               ld_q % 8 == 0
+ *   page_table  [batch, ld_table] int32: page i of sequence b; entries past its length are not
+ *               read. A page outside the cache is skipped and sets MOE_DEV_BAD_INDEX
+ *   max_pages   columns of page_table in use, <= ld_table: lengths above max_pages * page_size
+ *               are cut there and set MOE_DEV_BAD_INDEX
+ *   seq_lens    [batch] int32 (negative: empty)
+ *   out         [batch * q_len, num_q_heads, head_dim] BF16;  lse [batch * q_len, num_q_heads]
+ *               FP32 or NULL
+ *   workspace   moe_kv_attend_workspace_bytes(...) bytes (may be NULL when 0), no contents kept
+ *   dev_status  may be NULL
+ * Long sequences are split over thread blocks and joined by a second launch in a fixed order,
+ * so results repeat bit for bit. num_q_heads % num_kv_heads == 0; batch == 0 is a no-op.
+ * ---------------------------------------------------------------------------------------- */
+MOE_API size_t moe_kv_attend_workspace_bytes(const moe_kv_cache_t* cache, int32_t batch, int32_t q_len,
+                                             int32_t num_q_heads, int32_t max_pages);
+MOE_API moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch,
+                                   int32_t q_len, int32_t num_q_heads, const int32_t* page_table, int64_t ld_table,
+                                   int32_t max_pages, const int32_t* seq_lens, float softmax_scale, uint16_t* out,
+                                   float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                   moe_stream_t stream);
 
 #ifdef __cplusplus
 }

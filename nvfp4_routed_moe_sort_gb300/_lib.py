@@ -22,10 +22,12 @@ MOE_ACT_SWIGLU, MOE_ACT_RELU2, MOE_ACT_GEGLU, MOE_ACT_GELU, MOE_ACT_RELU, MOE_AC
 ACTIVATIONS = {"swiglu": MOE_ACT_SWIGLU, "relu2": MOE_ACT_RELU2, "geglu": MOE_ACT_GEGLU, "gelu": MOE_ACT_GELU,
                "relu": MOE_ACT_RELU, "silu": MOE_ACT_SILU, "identity": MOE_ACT_IDENTITY}
 MOE_SCALE_GLOBAL_ONE, MOE_SCALE_PER_TOKEN = 0, 1
-MOE_DEV_DUPLICATE_EXPERT, MOE_DEV_TIMEOUT = 1, 2
+MOE_DEV_DUPLICATE_EXPERT, MOE_DEV_TIMEOUT, MOE_DEV_BAD_INDEX = 1, 2, 4
 MOE_WEIGHTS_F32, MOE_WEIGHTS_BF16, MOE_WEIGHTS_PACKED = 0, 1, 2
 MOE_IDS_INT32, MOE_IDS_PACKED = 0, 1
 MOE_OUTPUT_UNFINALIZED, MOE_OUTPUT_FINALIZED, MOE_OUTPUT_ACCUMULATE = 0, 1, 2
+MOE_FP8_NONE, MOE_FP8_PER_TOKEN, MOE_FP8_PER_GROUP = 0, 1, 2
+MOE_FP8_GROUP = 128
 
 EXPORTED = [
     "moe_status_string", "moe_abi_version", "moe_quantize_input", "moe_plan_capacity",
@@ -33,6 +35,7 @@ EXPORTED = [
     "moe_prepare_weights", "moe_forward_workspace_bytes", "moe_forward_workspace_layout",
     "moe_grouped_fp4_forward", "moe_finalize", "moe_plan_noalloc",
     "moe_routed_forward_workspace_bytes", "moe_routed_forward",
+    "moe_add_rmsnorm", "moe_linear_fp4", "moe_kv_append", "moe_kv_attend_workspace_bytes", "moe_kv_attend",
 ]
 # the test build's extra entry points (include/moe_nvfp4_test.h)
 TEST_EXPORTED = ["moe_test_default_options", "moe_test_routed_forward", "moe_test_gemm1"]
@@ -50,6 +53,15 @@ class WeightsT(ctypes.Structure):
         ("w2", c_void_p), ("w2_sf", c_void_p), ("w2_alpha", c_void_p),
         ("num_local_experts", c_int32), ("hidden", c_int32), ("inter", c_int32),
         ("activation", c_int32), ("w1_gate_alpha", c_void_p),
+    ]
+
+
+class KVCacheT(ctypes.Structure):
+    """moe_kv_cache_t"""
+    _fields_ = [
+        ("k", c_void_p), ("k_sf", c_void_p), ("v", c_void_p), ("v_sf", c_void_p),
+        ("num_pages", c_int32), ("page_size", c_int32), ("num_kv_heads", c_int32), ("head_dim", c_int32),
+        ("data_page_stride", c_int64), ("sf_page_stride", c_int64), ("k_scale", c_float), ("v_scale", c_float),
     ]
 
 
@@ -89,6 +101,12 @@ def _declare(lib, test=False):
         "moe_finalize": (c_int32, [P, P, c_int32, c_float, P, c_int32, c_int32, c_int32, P, P]),
         "moe_routed_forward_workspace_bytes": (c_size_t, [c_int32, c_int32, ctypes.POINTER(WeightsT), c_int32]),
         "moe_routed_forward": (c_int32, routed + [P]),
+        "moe_add_rmsnorm": (c_int32, [P, c_int64, P, c_int64, P, c_int32, c_int32, c_float, c_int32, P, P, P, P, P]),
+        "moe_linear_fp4": (c_int32, [P, c_int64, P, c_int32, c_int32, c_int32, P, P, P, c_int32, c_int32, P, P]),
+        "moe_kv_append": (c_int32, [ctypes.POINTER(KVCacheT), P, c_int64, P, c_int64, P, c_int32, P, P, P, P]),
+        "moe_kv_attend_workspace_bytes": (c_size_t, [ctypes.POINTER(KVCacheT), c_int32, c_int32, c_int32, c_int32]),
+        "moe_kv_attend": (c_int32, [ctypes.POINTER(KVCacheT), P, c_int64, c_int32, c_int32, c_int32, P, c_int64,
+                                    c_int32, P, c_float, P, P, P, c_size_t, P, P]),
     }
     if test:
         sig.update({
@@ -301,6 +319,50 @@ def moe_finalize(gemm2_out, topk_weights, token_to_row, out, stream=None, routed
     _check(lib().moe_finalize(_ptr(gemm2_out), _ptr(topk_weights), _weights_dtype(topk_weights),
                               float(routed_scaling_factor), _ptr(token_to_row), M, k, H, _ptr(out),
                               _stream(stream)), "moe_finalize")
+
+
+def _ld(t, width):
+    """Values between the rows of t (a single row's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def moe_add_rmsnorm(x, residual, weight, eps, fp8_scale, y, residual_out, y8, y8_scale, stream=None):
+    """x [M, H] and residual [M, H] (or None) may have a row stride; the outputs are contiguous."""
+    M, H = x.shape
+    _check(lib().moe_add_rmsnorm(_ptr(x), _ld(x, H), _ptr(residual), _ld(residual, H) if residual is not None else 0,
+                                 _ptr(weight), M, H, eps, fp8_scale, _ptr(y), _ptr(residual_out), _ptr(y8),
+                                 _ptr(y8_scale), _stream(stream)), "moe_add_rmsnorm")
+
+
+def moe_linear_fp4(x, x_scale, x_scale_mode, w, w_sf, alpha, activation, out, stream=None):
+    """x [M, K] bf16 or float8_e4m3fn (it may have a row stride); w [N, K/2], w_sf [N, K/16], alpha [1]."""
+    M, K = x.shape
+    _check(lib().moe_linear_fp4(_ptr(x), _ld(x, K), _ptr(x_scale), x_scale_mode, M, K, _ptr(w), _ptr(w_sf),
+                                _ptr(alpha), w.shape[0], activation, _ptr(out), _stream(stream)), "moe_linear_fp4")
+
+
+def moe_kv_append(cache: KVCacheT, k_new, v_new, slots, k_seen, v_seen, dev_status, stream=None):
+    """k_new, v_new [N, num_kv_heads, head_dim] bf16 (a token stride is fine), slots [N] int64."""
+    N, n = k_new.shape[0], cache.num_kv_heads * cache.head_dim
+    _check(lib().moe_kv_append(cache, _ptr(k_new), _ld(k_new, n), _ptr(v_new), _ld(v_new, n), _ptr(slots), N, _ptr(k_seen), _ptr(v_seen), _ptr(dev_status), _stream(stream)),
+           "moe_kv_append")
+
+
+def moe_kv_attend_workspace_bytes(cache: KVCacheT, batch, q_len, num_q_heads, max_pages) -> int:
+    return lib().moe_kv_attend_workspace_bytes(cache, batch, q_len, num_q_heads, max_pages)
+
+
+def moe_kv_attend(cache: KVCacheT, q, ld_q, page_table, seq_lens, softmax_scale, out, lse, workspace, dev_status,
+                  stream=None):
+    """q [batch, q_len, num_q_heads, head_dim] bf16 with ld_q values between rows (b, t) and (b, t + 1) and
+    between the last row of a sequence and the first of the next; page_table [batch, max_pages] int32."""
+    B, T, Hq, D = q.shape
+    if B * T == 1:
+        ld_q = Hq * D
+    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().moe_kv_attend(cache, _ptr(q), ld_q, B, T, Hq, _ptr(page_table), _ld(page_table, page_table.shape[1]),
+                               page_table.shape[1], _ptr(seq_lens), softmax_scale, _ptr(out), _ptr(lse),
+                               _ptr(workspace), wsb, _ptr(dev_status), _stream(stream)), "moe_kv_attend")
 
 
 def moe_test_gemm1(padded_offsets, row_to_slot, M, top_k, xq, xsf, xs, w: WeightsT, prepared, mode,

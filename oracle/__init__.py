@@ -16,7 +16,9 @@ what the pages define:
   expert matrix);
 * ``plan``     - the expert-sorted plan with segments padded to 128 rows;
 * ``moe``      - block-scaled GEMM1, SwiGLU / squared-ReLU, requantisation of
-  the intermediate, GEMM2, and the ordered FP32 finalize.
+  the intermediate, GEMM2, and the ordered FP32 finalize;
+* ``decoder``  - the operators around the routed experts: RMS norm with the
+  residual's addition, the NVFP4 linear, the NVFP4 cache and its attention.
 
 Precision: a floating-point step that decides an integer (a quantised code or
 scale) runs in IEEE float32, the precision of the kernel; sums and
@@ -24,4 +26,4 @@ activations run in float64 unless the pages fix FP32 (the combine). Every
 function is pinned by the ``-m "not gpu"`` tests under ``tests/`` against
 closed forms, library routines, invariants or brute force.
 """
-from . import formats, quantize, plan, moe  # noqa: F401
+from . import formats, quantize, plan, moe, decoder  # noqa: F401
