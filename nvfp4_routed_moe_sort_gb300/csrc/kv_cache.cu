@@ -72,91 +72,447 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
   }
 }
 
+// ---------------------------------------------------------------------------
+// attention of a decode step
+// ---------------------------------------------------------------------------
+// One block per (run of a sequence's tokens, kv head and up to 8 * NT of its query rows,
+// sequence). Query rows are q_len * group many per kv head, row = t * group + g. Both
+// products run transposed on mma.m16n8k16 (FP16 in, FP32 sums), so that the cached side is
+// the 16-row operand and eight query rows fill its 8 columns:
+//   S^T[token, row] = K[token, :] . Q[row, :]     per 16 tokens, D / 16 steps
+//   O^T[dim, row]  += V^T[dim, token] . P^T       per 16 tokens, D / 16 tiles
+// A cached value is code * scale with 6 significant bits, exact in FP16. The dimensions of an
+// MMA step and the rows of an MMA tile are numbered so that a lane's operand bytes lie side
+// by side in the cache: with r = lane / 4 and c = lane % 4, lane (r, c) reads bytes
+// [c * D/8, +D/8) of the keys of tokens r and r + 8 (step j uses its dimensions c * D/4 + 4j to
+// 4j + 3), and bytes [r * D/16, +D/16) of the values of tokens 2c, 2c+1, 2c+8 and 2c+9 (tile i
+// has dimension r * D/8 + 2i as its row r and the next as its row r + 8). No shared memory is
+// read in the loop. P^T's fragment is S^T's, transposed in 8 x 8 pieces (movmatrix).
+//
+// Softmax in base 2 with a running maximum per query row; p = 2^(s - m + 15) is rounded to
+// FP16 for the second product (11 significant bits down to 2^-29 of the largest weight), its
+// sum is FP32. Query rows are scaled by a power of two to a largest value in [2^14, 2^15) so
+// that BF16's exponents fit FP16.
+constexpr int kAttWarps = 4;
+constexpr int kAttGroup = 32;                       // tokens of one step of a warp
+constexpr int kAttStep = kAttWarps * kAttGroup;     // tokens of one step of a block
+constexpr float kPShift = 15.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 struct AttendArgs {
   const uint16_t* q;
   const int32_t* table;
   const int32_t* lens;
   uint16_t* out;
   float* lse;
+  float* part_o;   // [rows, splits, D]
+  float2* part_ml; // [rows, splits]: maximum (base 2) and sum
   int32_t* dev_status;
   int64_t ld_q, ld_table;
-  int q_len, q_heads, max_pages;
+  int q_len, q_heads, group, row_blocks, max_pages, splits, chunk;
   float scale;
 };
 
-constexpr int kAttWarps = 8;
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
+  uint32_t r;
+  asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(r) : "r"(byte));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 
-// One block per query row and head: warps take tokens in turn, each with its own running
-// maximum and sum; lanes hold D / 32 neighbouring dimensions.
-template <int D>
-__global__ void __launch_bounds__(kAttWarps * 32) kv_attend_kernel(Cache c, AttendArgs a) {
+// N 32-bit words of cached bytes (read once, kept out of L1)
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
+  if constexpr (N == 4)
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+  else if constexpr (N == 2)
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  else
+    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+}
+
+// first token position that query row `row` of a sequence of `len` tokens does not see
+__device__ __forceinline__ int row_limit(const AttendArgs& a, int len, int row) {
+  return len - (a.q_len - 1) + row / a.group;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_kernel(Cache c, AttendArgs a) {
+  constexpr int KS = D / 16;       // MMA steps of S, MMA tiles of O
+  constexpr int KW = D / 32;       // words of one token's keys per lane
+  constexpr int VW = D / 64;       // words of one token's values per lane
+  constexpr int R = 8 * NT;        // query rows of the block
   pdl_wait();
   pdl_trigger();
-  constexpr int P = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int head = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-  const int kvh = head / (a.q_heads / c.heads);
-  const int64_t row = static_cast<int64_t>(b) * a.q_len + t;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, cc = lane & 3;
+  const int split = blockIdx.x, kvh = blockIdx.y / a.row_blocks, b = blockIdx.z;
+  const int row0 = (blockIdx.y - kvh * a.row_blocks) * R;
+  const int rows_here = min(R, a.q_len * a.group - row0);
   int len = max(a.lens[b], 0);
   const int64_t most = static_cast<int64_t>(a.max_pages) << c.page_shift;
   if (len > most) {
     len = static_cast<int>(most);
-    if (a.dev_status && threadIdx.x == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
+    if (a.dev_status && tid == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
   }
-  const int limit = len - (a.q_len - 1) + t;
-  float q[P], o[P], m = -INFINITY, l = 0.0f;
+  const int first = split * a.chunk;
+  const int seen = max(row_limit(a, len, row0 + rows_here - 1), 0);  // by the block's last row
+  if (split > 0 && first >= seen) return;                            // the join does not read these parts
+  const int end = min(seen, first + a.chunk);
+  const int all_see = row_limit(a, len, row0);                       // every row sees the tokens before it
+
+  // Q^T fragments and each row's factor from raw sums to base-2 scores
+  uint32_t q[NT][KS][2];
+  float to_log2[NT][2];
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    q[i] = __uint_as_float(static_cast<uint32_t>(a.q[row * a.ld_q + head * D + lane * P + i]) << 16);
-    o[i] = 0.0f;
-  }
-  for (int j = warp; j < limit; j += kAttWarps) {
-    const int page = a.table[b * a.ld_table + (j >> c.page_shift)];
-    if (page < 0 || page >= c.pages) {
-      if (a.dev_status && lane == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
-      continue;
+  for (int t = 0; t < NT; ++t) {
+    const int row = row0 + 8 * t + r;
+    uint32_t raw[D / 8];
+    float amax = 0.0f;
+    if (8 * t + r < rows_here) {
+      const int tok = row / a.group, g = row - tok * a.group;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + (static_cast<int64_t>(b) * a.q_len + tok) * a.ld_q + (kvh * a.group + g) * D + cc * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 u = src[i];
+        raw[4 * i] = u.x, raw[4 * i + 1] = u.y, raw[4 * i + 2] = u.z, raw[4 * i + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) raw[i] = 0;
     }
-    const int64_t place = (static_cast<int64_t>(kvh) << c.page_shift) + (j & ((1 << c.page_shift) - 1));
-    float kv[2][P];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint8_t* d = c.data[w] + page * c.data_page + place * (D / 2) + lane * P / 2;
-      const float s = e4m3_to_f32(c.sf[w][page * c.sf_page + place * (D / 16) + lane * P / 16]) / c.g[w];
+    for (int i = 0; i < D / 8; ++i)
+      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[i] << 16)), fabsf(__uint_as_float(raw[i] & 0xFFFF0000u))));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // 2^shift * amax in [2^14, 2^15); zero and the smallest rows take the largest shift
+    const int shift = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
+    const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
 #pragma unroll
-      for (int i = 0; i < P; ++i) kv[w][i] = e2m1_to_f32((d[i / 2] >> (4 * (i & 1))) & 15) * s;
+    for (int i = 0; i < D / 8; ++i)
+      q[t][i >> 1][i & 1] = pack_f16x2(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xFFFF0000u) * up);
+    const float f = a.scale * kLog2e / c.g[0] * down;
+    to_log2[t][0] = __shfl_sync(0xffffffffu, f, 8 * cc);
+    to_log2[t][1] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
+  }
+
+  float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int i = 0; i < KS; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
+    m[t][0] = m[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.0f;
+  }
+
+  uint32_t kw[2][2][KW], ksf[2][2], vw[2][4][VW], vsf[2][4];
+  int page[2] = {-1, -1}, next_page[2] = {-1, -1};
+  const int32_t* table = a.table + b * a.ld_table;
+  const int in_page = (1 << c.page_shift) - 1;
+
+  auto load_pages = [&](int* p, int tok) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      p[u] = -1;
+      if (tok + 16 * u < end) p[u] = table[(tok + 16 * u) >> c.page_shift];
     }
-    float s = 0.0f;
+  };
+  // 16 tokens of a page: every address lies inside the page, whatever the sequence's length
+  auto load_k = [&](const int* p, int tok) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) s += q[i] * kv[0][i];
+    for (int u = 0; u < 2; ++u) {
+      if (static_cast<unsigned>(p[u]) < static_cast<unsigned>(c.pages)) {
+        const int64_t at = (static_cast<int64_t>(kvh) << c.page_shift) + ((tok + 16 * u) & in_page) + r;
+        const uint8_t* d = c.data[0] + p[u] * c.data_page + at * (D / 2) + cc * (D / 8);
+        const uint8_t* s = c.sf[0] + p[u] * c.sf_page + at * (D / 16) + cc * (D / 64);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale;
-    const float top = fmaxf(m, s), keep = expf(m - top), p = expf(s - top);
-    l = l * keep + p;
+        for (int h = 0; h < 2; ++h) {
+          load_words<KW>(kw[u][h], d + h * 8 * (D / 2));
+          ksf[u][h] = D == 128 ? *reinterpret_cast<const uint16_t*>(s + h * 8 * (D / 16)) : s[h * 8 * (D / 16)];
+        }
+      }
+    }
+  };
+  auto load_v = [&](const int* p, int tok) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) o[i] = o[i] * keep + p * kv[1][i];
-    m = top;
+    for (int u = 0; u < 2; ++u) {
+      if (static_cast<unsigned>(p[u]) < static_cast<unsigned>(c.pages)) {
+        const int64_t at = (static_cast<int64_t>(kvh) << c.page_shift) + ((tok + 16 * u) & in_page) + 2 * cc;
+        const uint8_t* d = c.data[1] + p[u] * c.data_page + at * (D / 2) + r * (D / 16);
+        const uint8_t* s = c.sf[1] + p[u] * c.sf_page + at * (D / 16) + r * (D / 16) / 8;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int row = (h & 1) + 8 * (h >> 1);
+          load_words<VW>(vw[u][h], d + row * (D / 2));
+          vsf[u][h] = s[row * (D / 16)];
+        }
+      }
+    }
+  };
+
+  int tok = first + warp * kAttGroup;
+  load_pages(page, tok);
+  load_k(page, tok);
+  load_v(page, tok);
+  load_pages(next_page, tok + kAttStep);
+  for (; tok < end; tok += kAttStep) {
+    // ---- scores of 32 tokens
+    float s[2][NT][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.0f;
+      uint32_t sc[2][2];  // [token half][block], a scale in both halves
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t two = e4m3x2_to_f16x2(ksf[u][h]);
+        sc[h][0] = __byte_perm(two, two, 0x1010);
+        sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
+      }
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        uint32_t f[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w = kw[u][h][j >> 1] >> (16 * (j & 1));
+          const uint32_t x = sc[h][j / 4];
+          f[h] = mul_f16x2(e2m1x2_to_f16x2(w & 0xFF), x);
+          f[2 + h] = mul_f16x2(e2m1x2_to_f16x2((w >> 8) & 0xFF), x);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_f16(s[u][t], f, q[t][j]);
+      }
+    }
+    const bool more = tok + kAttStep < end;
+    bool held[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) held[u] = static_cast<unsigned>(page[u]) < static_cast<unsigned>(c.pages);
+    if (more) load_k(next_page, tok + kAttStep);
+
+    // ---- running maximum, weights
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][t][i] *= to_log2[t][i & 1];
+    if (tok + kAttGroup > min(all_see, end) || !held[0] || !held[1]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (!held[u] && tok + 16 * u < end && a.dev_status && lane == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = tok + 16 * u + r + 8 * (i >> 1);
+            const int lim = min(end, row_limit(a, len, row0 + 8 * t + 2 * cc + (i & 1)));
+            if (!held[u] || at >= lim) s[u][t][i] = -INFINITY;
+          }
+        // values past the sequence's end may be anything: a zero scale keeps them out
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const bool out = !held[u] || tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1) >= end;
+          if (out) vsf[u][h] = 0;
+        }
+      }
+    }
+    uint32_t p[2][NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float top[2], keep[2];
+      bool grew = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = fmaxf(fmaxf(s[0][t][i], s[0][t][i + 2]), fmaxf(s[1][t][i], s[1][t][i + 2]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        top[i] = fmaxf(m[t][i], x);
+        grew |= top[i] > m[t][i];
+        keep[i] = top[i] == -INFINITY ? 0.0f : top[i];
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float f = ex2(m[t][i] - keep[i]);
+          l[t][i] *= f;
+#pragma unroll
+          for (int j = 0; j < KS; ++j) o[t][j][i] *= f, o[t][j][i + 2] *= f;
+          m[t][i] = top[i];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[u][t][i] = ex2(s[u][t][i] - keep[i & 1] + kPShift);
+          l[t][i & 1] += s[u][t][i];
+        }
+        p[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
+        p[u][t][1] = transpose8x8(pack_f16x2(s[u][t][2], s[u][t][3]));
+      }
+    }
+
+    // ---- weighted values of 32 tokens
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t s01 = e4m3x2_to_f16x2(vsf[u][0] | vsf[u][1] << 8);
+      const uint32_t s89 = e4m3x2_to_f16x2(vsf[u][2] | vsf[u][3] << 8);
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        // bytes that pair one dimension's codes of two neighbouring tokens
+        const uint32_t low = 0x0F0F0F0Fu;
+        const uint32_t e01 = (vw[u][0][w] & low) | (vw[u][1][w] << 4 & ~low);
+        const uint32_t o01 = (vw[u][0][w] >> 4 & low) | (vw[u][1][w] & ~low);
+        const uint32_t e89 = (vw[u][2][w] & low) | (vw[u][3][w] << 4 & ~low);
+        const uint32_t o89 = (vw[u][2][w] >> 4 & low) | (vw[u][3][w] & ~low);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t f[4];
+          f[0] = mul_f16x2(e2m1x2_to_f16x2(e01 >> (8 * i) & 0xFF), s01);
+          f[1] = mul_f16x2(e2m1x2_to_f16x2(o01 >> (8 * i) & 0xFF), s01);
+          f[2] = mul_f16x2(e2m1x2_to_f16x2(e89 >> (8 * i) & 0xFF), s89);
+          f[3] = mul_f16x2(e2m1x2_to_f16x2(o89 >> (8 * i) & 0xFF), s89);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * w + i], f, p[u][t]);
+        }
+      }
+    }
+    if (more) load_v(next_page, tok + kAttStep);
+    page[0] = next_page[0], page[1] = next_page[1];
+    load_pages(next_page, tok + 2 * kAttStep);
   }
-  __shared__ float sm[kAttWarps], sl[kAttWarps], so[kAttWarps][D];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
+
+  // ---- join the warps
+  constexpr int ST = D + 4;
+  __shared__ float sm[kAttWarps][R], sl[kAttWarps][R];
+  __shared__ float so[kAttWarps][R][ST];
 #pragma unroll
-  for (int i = 0; i < P; ++i) so[warp][lane * P + i] = o[i];
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float x = l[t][i];
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      const int row = 8 * t + 2 * cc + i;
+      if (r == 0) {
+        sm[warp][row] = m[t][i];
+        sl[warp][row] = x;
+      }
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+        *reinterpret_cast<float2*>(&so[warp][row][r * (D / 8) + 2 * j]) = make_float2(o[t][j][i], o[t][j][i + 2]);
+    }
   __syncthreads();
-  float top = -INFINITY;
-  for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, sm[w]);
-  float total = 0.0f;
-  for (int w = 0; w < kAttWarps; ++w) total += sl[w] == 0.0f ? 0.0f : sl[w] * expf(sm[w] - top);
-  const int64_t at = row * a.q_heads + head;
-  for (int i = threadIdx.x; i < D; i += kAttWarps * 32) {
-    float v = 0.0f;
-    for (int w = 0; w < kAttWarps; ++w)
-      if (sl[w] != 0.0f) v += so[w][i] * expf(sm[w] - top);
-    a.out[at * D + i] = __bfloat16_as_ushort(__float2bfloat16_rn(total == 0.0f ? 0.0f : v / total));
+  for (int i = tid; i < rows_here * (D / 4); i += kAttWarps * 32) {
+    const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
+    float top = sm[0][row];
+#pragma unroll
+    for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sm[w][row]);
+    float total = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) {
+      if (sl[w][row] == 0.0f) continue;  // saw nothing (its maximum may be -inf)
+      const float f = ex2(sm[w][row] - top);
+      total += sl[w][row] * f;
+      const float4 x = *reinterpret_cast<const float4*>(&so[w][row][d]);
+      v[0] += x.x * f, v[1] += x.y * f, v[2] += x.z * f, v[3] += x.w * f;
+    }
+    const int grow = row0 + row, t = grow / a.group, g = grow - t * a.group;
+    const int64_t at = (static_cast<int64_t>(b) * a.q_len + t) * a.q_heads + kvh * a.group + g;
+    if (a.splits > 1) {
+      *reinterpret_cast<float4*>(a.part_o + (at * a.splits + split) * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+      if (d == 0) a.part_ml[at * a.splits + split] = make_float2(top, total);
+    } else {
+      const float f = total == 0.0f ? 0.0f : 1.0f / (total * c.g[1]);
+      ushort4 h;
+      h.x = __bfloat16_as_ushort(__float2bfloat16_rn(v[0] * f));
+      h.y = __bfloat16_as_ushort(__float2bfloat16_rn(v[1] * f));
+      h.z = __bfloat16_as_ushort(__float2bfloat16_rn(v[2] * f));
+      h.w = __bfloat16_as_ushort(__float2bfloat16_rn(v[3] * f));
+      *reinterpret_cast<ushort4*>(a.out + at * D + d) = h;
+      if (a.lse && d == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top - kPShift + log2f(total)) * kLn2;
+    }
   }
-  if (a.lse && threadIdx.x == 0) a.lse[at] = total == 0.0f ? -INFINITY : top + logf(total);
+}
+
+// Joins the parts of one query row: a thread per dimension, parts in ascending order.
+template <int D>
+__global__ void __launch_bounds__(D) kv_join_kernel(Cache c, AttendArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t at = blockIdx.x;
+  const int64_t tok = at / a.q_heads;
+  const int b = static_cast<int>(tok / a.q_len), t = static_cast<int>(tok % a.q_len);
+  const int len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), static_cast<int64_t>(a.max_pages) << c.page_shift));
+  const int seen = max(len - (a.q_len - 1) + t, 0);
+  const int n = (seen + a.chunk - 1) / a.chunk;
+  const float2* ml = a.part_ml + at * a.splits;
+  const float* po = a.part_o + at * a.splits * D + threadIdx.x;
+  float top = -INFINITY;
+  for (int i = 0; i < n; ++i) top = fmaxf(top, ml[i].x);
+  float total = 0.0f, v = 0.0f;
+  for (int i = 0; i < n; ++i) {
+    const float2 x = ml[i];
+    if (x.y == 0.0f) continue;
+    const float f = ex2(x.x - top);
+    total += x.y * f;
+    v += po[static_cast<int64_t>(i) * D] * f;
+  }
+  a.out[at * D + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(total == 0.0f ? 0.0f : v / (total * c.g[1])));
+  if (a.lse && threadIdx.x == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top - kPShift + log2f(total)) * kLn2;
+}
+
+// How a call is cut: rows of a block, and runs of the sequences. Enough blocks to fill every
+// SM twice over (sequences differ in length), no run shorter than four steps of a block.
+struct Cut {
+  int row_tiles, row_blocks, splits, chunk;
+};
+
+Cut cut_attend(int batch, int kv_heads, int rows, int64_t most) {
+  Cut k;
+  k.row_tiles = rows > 8 ? 2 : 1;
+  k.row_blocks = (rows + 8 * k.row_tiles - 1) / (8 * k.row_tiles);
+  const int64_t blocks = static_cast<int64_t>(batch) * kv_heads * k.row_blocks;
+  const int64_t want = (static_cast<int64_t>(num_sms()) * 8 + blocks - 1) / blocks;
+  int64_t chunk = (most + want - 1) / want;
+  if (chunk < 4 * kAttStep) chunk = 4 * kAttStep;
+  chunk = roundup64(chunk, kAttStep);
+  k.chunk = static_cast<int>(chunk < (1 << 30) ? chunk : (1 << 30));
+  k.splits = most > 0 ? static_cast<int>((most + k.chunk - 1) / k.chunk) : 1;
+  return k;
 }
 
 moe_status_t check_cache(const moe_kv_cache_t* c, Cache* out) {
@@ -222,10 +578,34 @@ extern "C" moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const uint16_
                     static_cast<int64_t>(N), k_seen, v_seen, dev_status);
 }
 
+namespace {
+
+// checks the sizes that the workspace and the launches are made from
+moe_status_t attend_cut(const moe_kv_cache_t* cache, Cache* c, int32_t batch, int32_t q_len, int32_t num_q_heads,
+                        int32_t max_pages, Cut* cut, size_t* bytes) {
+  const moe_status_t st = check_cache(cache, c);
+  if (st != MOE_OK) return st;
+  MOE_CHECK(batch >= 0 && q_len >= 1 && num_q_heads >= 1 && num_q_heads % c->heads == 0 && max_pages >= 0,
+            MOE_ERR_INVALID_ARGUMENT);
+  const int64_t most = static_cast<int64_t>(max_pages) << c->page_shift;
+  const int64_t rows = static_cast<int64_t>(q_len) * (num_q_heads / c->heads);
+  MOE_CHECK(batch <= 65535 && most < (int64_t(1) << 30) && q_len <= 65535 && rows * c->heads <= 65535 &&
+                rows * c->heads * (batch > 0 ? batch : 1) < (int64_t(1) << 31),
+            MOE_ERR_UNSUPPORTED_SHAPE);
+  *cut = cut_attend(batch > 0 ? batch : 1, c->heads, static_cast<int>(rows), most);
+  const int64_t parts = cut->splits > 1 ? static_cast<int64_t>(batch) * q_len * num_q_heads * cut->splits : 0;
+  *bytes = static_cast<size_t>(roundup64(parts * c->dim * 4, 16) + parts * 8);
+  return MOE_OK;
+}
+
+}  // namespace
+
 extern "C" size_t moe_kv_attend_workspace_bytes(const moe_kv_cache_t* cache, int32_t batch, int32_t q_len,
                                                 int32_t num_q_heads, int32_t max_pages) {
-  (void)cache, (void)batch, (void)q_len, (void)num_q_heads, (void)max_pages;
-  return 0;
+  Cache c;
+  Cut cut;
+  size_t bytes;
+  return attend_cut(cache, &c, batch, q_len, num_q_heads, max_pages, &cut, &bytes) == MOE_OK ? bytes : 0;
 }
 
 extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch,
@@ -234,14 +614,12 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
                                       float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                       moe_stream_t stream) {
   Cache c;
-  moe_status_t st = check_cache(cache, &c);
+  Cut cut;
+  size_t need;
+  const moe_status_t st = attend_cut(cache, &c, batch, q_len, num_q_heads, max_pages, &cut, &need);
   if (st != MOE_OK) return st;
-  MOE_CHECK(batch >= 0 && q_len >= 1 && num_q_heads >= 1 && num_q_heads % c.heads == 0 && max_pages >= 0 &&
-                ld_table >= max_pages && ld_q >= static_cast<int64_t>(num_q_heads) * c.dim && isfinite(softmax_scale),
+  MOE_CHECK(ld_table >= max_pages && ld_q >= static_cast<int64_t>(num_q_heads) * c.dim && isfinite(softmax_scale),
             MOE_ERR_INVALID_ARGUMENT);
-  MOE_CHECK(batch <= 65535 && q_len <= 65535 && (static_cast<int64_t>(max_pages) << c.page_shift) < (int64_t(1) << 31),
-            MOE_ERR_UNSUPPORTED_SHAPE);
-  const size_t need = moe_kv_attend_workspace_bytes(cache, batch, q_len, num_q_heads, max_pages);
   MOE_CHECK(workspace_bytes >= need, MOE_ERR_WORKSPACE_TOO_SMALL);
   if (batch == 0) return MOE_OK;
   MOE_CHECK(q && seq_lens && out && (page_table || max_pages == 0) && (workspace || need == 0),
@@ -260,9 +638,18 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
     for (int j = 0; j < i; ++j) MOE_CHECK(!overlaps(to[i], to_bytes[i], to[j], to_bytes[j]), MOE_ERR_OVERLAP);
     MOE_CHECK(!touches_cache(cache, to[i], to_bytes[i]), MOE_ERR_OVERLAP);
   }
-  AttendArgs a = {q, page_table, seq_lens, out, lse, dev_status, ld_q, ld_table, q_len, num_q_heads, max_pages,
-                  softmax_scale};
-  const dim3 grid(num_q_heads, q_len, batch);
-  return launch_pdl(c.dim == 64 ? kv_attend_kernel<64> : kv_attend_kernel<128>, grid, dim3(kAttWarps * 32), 0,
-                    as_stream(stream), c, a);
+  const size_t parts = cut.splits > 1 ? rows * num_q_heads * cut.splits : 0;
+  float* part_o = parts ? static_cast<float*>(workspace) : nullptr;
+  float2* part_ml = parts ? reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + roundup64(parts * c.dim * 4, 16))
+                          : nullptr;
+  const AttendArgs a = {q, page_table, seq_lens, out, lse, part_o, part_ml, dev_status, ld_q, ld_table, q_len,
+                        num_q_heads, num_q_heads / c.heads, cut.row_blocks, max_pages, cut.splits, cut.chunk,
+                        softmax_scale};
+  const dim3 grid(cut.splits, c.heads * cut.row_blocks, batch);
+  auto* kern = c.dim == 64 ? (cut.row_tiles == 1 ? kv_attend_kernel<64, 1> : kv_attend_kernel<64, 2>)
+                           : (cut.row_tiles == 1 ? kv_attend_kernel<128, 1> : kv_attend_kernel<128, 2>);
+  const moe_status_t ran = launch_pdl(kern, grid, dim3(kAttWarps * 32), 0, as_stream(stream), c, a);
+  if (ran != MOE_OK || cut.splits == 1) return ran;
+  return launch_pdl(c.dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>,
+                    dim3(static_cast<unsigned>(rows * num_q_heads)), dim3(c.dim), 0, as_stream(stream), c, a);
 }
