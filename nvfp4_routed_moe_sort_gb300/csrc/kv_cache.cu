@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 constexpr int kAttWarps = 4;
 constexpr int kAttGroup = 32;                       // tokens of one step of a warp
 constexpr int kAttStep = kAttWarps * kAttGroup;     // tokens of one step of a block
+constexpr int kAttFill = 8, kAttLeast = 2;
 constexpr float kPShift = 15.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -113,10 +114,13 @@ struct AttendArgs {
   float scale;
 };
 
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(r) : "r"(byte));
-  return r;
+// the eight codes of a word, a byte's two to one register. Naming the word's bytes costs nothing;
+// shifting and masking them out costs two more instructions of the pipe that converts.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t* f) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(w));
 }
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t r;
@@ -165,6 +169,20 @@ __device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
 // first token position that query row `row` of a sequence of `len` tokens does not see
 __device__ __forceinline__ int row_limit(const AttendArgs& a, int len, int row) {
   return len - (a.q_len - 1) + row / a.group;
+}
+
+// four dimensions of a finished row (zeros when it saw nothing), and its log sum
+__device__ __forceinline__ void store_row(const AttendArgs& a, int64_t at, float4 v, float total, float g) {
+  const float f = total == 0.0f ? 0.0f : 1.0f / (total * g);
+  ushort4 h;
+  h.x = __bfloat16_as_ushort(__float2bfloat16_rn(v.x * f));
+  h.y = __bfloat16_as_ushort(__float2bfloat16_rn(v.y * f));
+  h.z = __bfloat16_as_ushort(__float2bfloat16_rn(v.z * f));
+  h.w = __bfloat16_as_ushort(__float2bfloat16_rn(v.w * f));
+  *reinterpret_cast<ushort4*>(a.out + at) = h;
+}
+__device__ __forceinline__ float row_lse(float top, float total) {
+  return total == 0.0f ? -INFINITY : (top - kPShift + log2f(total)) * kLn2;
 }
 
 template <int D, int NT>
@@ -303,17 +321,17 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
         sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
       }
 #pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        uint32_t f[4];
+      for (int w = 0; w < KW; ++w) {  // a word is two steps
+        uint32_t f[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t w = kw[u][h][j >> 1] >> (16 * (j & 1));
-          const uint32_t x = sc[h][j / 4];
-          f[h] = mul_f16x2(e2m1x2_to_f16x2(w & 0xFF), x);
-          f[2 + h] = mul_f16x2(e2m1x2_to_f16x2((w >> 8) & 0xFF), x);
+        for (int h = 0; h < 2; ++h) e2m1x8_to_f16x2(kw[u][h][w], f[h]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t x[4] = {mul_f16x2(f[0][2 * j], sc[0][w / 2]), mul_f16x2(f[1][2 * j], sc[1][w / 2]),
+                                 mul_f16x2(f[0][2 * j + 1], sc[0][w / 2]), mul_f16x2(f[1][2 * j + 1], sc[1][w / 2])};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(s[u][t], x, q[t][2 * w + j]);
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma_f16(s[u][t], f, q[t][j]);
       }
     }
     const bool more = tok + kAttStep < end;
@@ -394,19 +412,17 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
       for (int w = 0; w < VW; ++w) {
         // bytes that pair one dimension's codes of two neighbouring tokens
         const uint32_t low = 0x0F0F0F0Fu;
-        const uint32_t e01 = (vw[u][0][w] & low) | (vw[u][1][w] << 4 & ~low);
-        const uint32_t o01 = (vw[u][0][w] >> 4 & low) | (vw[u][1][w] & ~low);
-        const uint32_t e89 = (vw[u][2][w] & low) | (vw[u][3][w] << 4 & ~low);
-        const uint32_t o89 = (vw[u][2][w] >> 4 & low) | (vw[u][3][w] & ~low);
+        uint32_t f[4][4];
+        e2m1x8_to_f16x2((vw[u][0][w] & low) | (vw[u][1][w] << 4 & ~low), f[0]);
+        e2m1x8_to_f16x2((vw[u][0][w] >> 4 & low) | (vw[u][1][w] & ~low), f[1]);
+        e2m1x8_to_f16x2((vw[u][2][w] & low) | (vw[u][3][w] << 4 & ~low), f[2]);
+        e2m1x8_to_f16x2((vw[u][2][w] >> 4 & low) | (vw[u][3][w] & ~low), f[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t f[4];
-          f[0] = mul_f16x2(e2m1x2_to_f16x2(e01 >> (8 * i) & 0xFF), s01);
-          f[1] = mul_f16x2(e2m1x2_to_f16x2(o01 >> (8 * i) & 0xFF), s01);
-          f[2] = mul_f16x2(e2m1x2_to_f16x2(e89 >> (8 * i) & 0xFF), s89);
-          f[3] = mul_f16x2(e2m1x2_to_f16x2(o89 >> (8 * i) & 0xFF), s89);
+          const uint32_t x[4] = {mul_f16x2(f[0][i], s01), mul_f16x2(f[1][i], s01), mul_f16x2(f[2][i], s89),
+                                 mul_f16x2(f[3][i], s89)};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * w + i], f, p[u][t]);
+          for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * w + i], x, p[u][t]);
         }
       }
     }
@@ -441,58 +457,95 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
     float top = sm[0][row];
 #pragma unroll
     for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sm[w][row]);
-    float total = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float total = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kAttWarps; ++w) {
       if (sl[w][row] == 0.0f) continue;  // saw nothing (its maximum may be -inf)
       const float f = ex2(sm[w][row] - top);
       total += sl[w][row] * f;
       const float4 x = *reinterpret_cast<const float4*>(&so[w][row][d]);
-      v[0] += x.x * f, v[1] += x.y * f, v[2] += x.z * f, v[3] += x.w * f;
+      v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
     }
     const int grow = row0 + row, t = grow / a.group, g = grow - t * a.group;
     const int64_t at = (static_cast<int64_t>(b) * a.q_len + t) * a.q_heads + kvh * a.group + g;
     if (a.splits > 1) {
-      *reinterpret_cast<float4*>(a.part_o + (at * a.splits + split) * D + d) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(a.part_o + (at * a.splits + split) * D + d) = v;
       if (d == 0) a.part_ml[at * a.splits + split] = make_float2(top, total);
     } else {
-      const float f = total == 0.0f ? 0.0f : 1.0f / (total * c.g[1]);
-      ushort4 h;
-      h.x = __bfloat16_as_ushort(__float2bfloat16_rn(v[0] * f));
-      h.y = __bfloat16_as_ushort(__float2bfloat16_rn(v[1] * f));
-      h.z = __bfloat16_as_ushort(__float2bfloat16_rn(v[2] * f));
-      h.w = __bfloat16_as_ushort(__float2bfloat16_rn(v[3] * f));
-      *reinterpret_cast<ushort4*>(a.out + at * D + d) = h;
-      if (a.lse && d == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top - kPShift + log2f(total)) * kLn2;
+      store_row(a, at * D + d, v, total, c.g[1]);
+      if (a.lse && d == 0) a.lse[at] = row_lse(top, total);
     }
   }
 }
 
-// Joins the parts of one query row: a thread per dimension, parts in ascending order.
+// Joins the parts of one query row. The block first turns the parts' maxima and sums into weights
+// (shared memory, kJoinParts at a time), then kJoinThreads / (D / 4) groups of threads each add every
+// so-manieth part, four dimensions to a thread, and the groups' sums are added in order.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 1024;
+
 template <int D>
-__global__ void __launch_bounds__(D) kv_join_kernel(Cache c, AttendArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(Cache c, AttendArgs a) {
+  constexpr int L = D / 4, G = kJoinThreads / L;
+  __shared__ float weight[kJoinParts], red[2][kJoinThreads / 32];
+  __shared__ float4 acc[G][L];
   pdl_wait();
   pdl_trigger();
-  const int64_t at = blockIdx.x;
-  const int64_t tok = at / a.q_heads;
-  const int b = static_cast<int>(tok / a.q_len), t = static_cast<int>(tok % a.q_len);
-  const int len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), static_cast<int64_t>(a.max_pages) << c.page_shift));
-  const int seen = max(len - (a.q_len - 1) + t, 0);
-  const int n = (seen + a.chunk - 1) / a.chunk;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t at = blockIdx.x, tok = at / a.q_heads;
+  const int b = static_cast<int>(tok / a.q_len), t = static_cast<int>(tok - static_cast<int64_t>(b) * a.q_len);
+  const int64_t most = static_cast<int64_t>(a.max_pages) << c.page_shift;
+  const int len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), most));
+  const int n = (max(len - (a.q_len - 1) + t, 0) + a.chunk - 1) / a.chunk;  // parts that the row sees
   const float2* ml = a.part_ml + at * a.splits;
-  const float* po = a.part_o + at * a.splits * D + threadIdx.x;
   float top = -INFINITY;
-  for (int i = 0; i < n; ++i) top = fmaxf(top, ml[i].x);
-  float total = 0.0f, v = 0.0f;
-  for (int i = 0; i < n; ++i) {
-    const float2 x = ml[i];
-    if (x.y == 0.0f) continue;
-    const float f = ex2(x.x - top);
-    total += x.y * f;
-    v += po[static_cast<int64_t>(i) * D] * f;
+  for (int i = tid; i < n; i += kJoinThreads) top = fmaxf(top, ml[i].x);
+  top = warp_max(top);
+  if (lane == 0) red[0][warp] = top;
+  __syncthreads();
+  top = red[0][0];
+#pragma unroll
+  for (int w = 1; w < kJoinThreads / 32; ++w) top = fmaxf(top, red[0][w]);
+
+  const int g = tid / L, d = tid - g * L;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float total = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += kJoinParts) {
+    const int here = min(n - i0, kJoinParts);
+    __syncthreads();
+    for (int i = tid; i < here; i += kJoinThreads) {
+      const float2 x = ml[i0 + i];
+      const float f = x.y == 0.0f ? 0.0f : ex2(x.x - top);  // a part may have seen nothing
+      weight[i] = f;
+      total += f * x.y;
+    }
+    __syncthreads();
+    const float4* po = reinterpret_cast<const float4*>(a.part_o + (at * a.splits + i0) * D) + d;
+#pragma unroll 4
+    for (int i = g; i < here; i += G) {
+      const float f = weight[i];
+      if (f == 0.0f) continue;
+      const float4 x = po[i * L];
+      v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+    }
   }
-  a.out[at * D + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(total == 0.0f ? 0.0f : v / (total * c.g[1])));
-  if (a.lse && threadIdx.x == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top - kPShift + log2f(total)) * kLn2;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) red[1][warp] = total;
+  acc[g][d] = v;
+  __syncthreads();
+  if (g > 0) return;
+  total = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) total += red[1][w];
+#pragma unroll
+  for (int i = 1; i < G; ++i) {
+    const float4 x = acc[i][d];
+    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  }
+  store_row(a, at * D + 4 * d, v, total, c.g[1]);
+  if (a.lse && d == 0) a.lse[at] = row_lse(top, total);
 }
 
 // How a call is cut: rows of a block, and runs of the sequences. Enough blocks to fill every
@@ -506,9 +559,9 @@ Cut cut_attend(int batch, int kv_heads, int rows, int64_t most) {
   k.row_tiles = rows > 8 ? 2 : 1;
   k.row_blocks = (rows + 8 * k.row_tiles - 1) / (8 * k.row_tiles);
   const int64_t blocks = static_cast<int64_t>(batch) * kv_heads * k.row_blocks;
-  const int64_t want = (static_cast<int64_t>(num_sms()) * 8 + blocks - 1) / blocks;
+  const int64_t want = (static_cast<int64_t>(num_sms()) * kAttFill + blocks - 1) / blocks;
   int64_t chunk = (most + want - 1) / want;
-  if (chunk < 4 * kAttStep) chunk = 4 * kAttStep;
+  if (chunk < kAttLeast * kAttStep) chunk = kAttLeast * kAttStep;
   chunk = roundup64(chunk, kAttStep);
   k.chunk = static_cast<int>(chunk < (1 << 30) ? chunk : (1 << 30));
   k.splits = most > 0 ? static_cast<int>((most + k.chunk - 1) / k.chunk) : 1;
@@ -651,5 +704,5 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   const moe_status_t ran = launch_pdl(kern, grid, dim3(kAttWarps * 32), 0, as_stream(stream), c, a);
   if (ran != MOE_OK || cut.splits == 1) return ran;
   return launch_pdl(c.dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>,
-                    dim3(static_cast<unsigned>(rows * num_q_heads)), dim3(c.dim), 0, as_stream(stream), c, a);
+                    dim3(static_cast<unsigned>(rows * num_q_heads)), dim3(kJoinThreads), 0, as_stream(stream), c, a);
 }
