@@ -86,8 +86,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 // by side in the cache: with r = lane / 4 and c = lane % 4, lane (r, c) reads bytes
 // [c * D/8, +D/8) of the keys of tokens r and r + 8 (step j uses its dimensions c * D/4 + 4j to
 // 4j + 3), and bytes [r * D/16, +D/16) of the values of tokens 2c, 2c+1, 2c+8 and 2c+9 (tile i
-// has dimension r * D/8 + 2i as its row r and the next as its row r + 8). No shared memory is
-// read in the loop. P^T's fragment is S^T's, transposed in 8 x 8 pieces (movmatrix).
+// has dimension r * D/8 + 2i as its row r and the next as its row r + 8). P^T's fragment is
+// S^T's, transposed in 8 x 8 pieces (movmatrix).
+//
+// Each warp takes every kAttWarps-th group of 32 tokens and feeds itself through a ring of
+// kAttStages groups in shared memory (bulk copies of 16 or 32 tokens, one mbarrier per stage), so
+// the warps of a block never wait for one another before the end.
 //
 // Softmax in base 2 with a running maximum per query row; p = 2^(s - m + 15) is rounded to
 // FP16 for the second product (11 significant bits down to 2^-29 of the largest weight), its
@@ -97,6 +101,7 @@ constexpr int kAttWarps = 4;
 constexpr int kAttGroup = 32;                       // tokens of one step of a warp
 constexpr int kAttStep = kAttWarps * kAttGroup;     // tokens of one step of a block
 constexpr int kAttFill = 8, kAttLeast = 2;
+constexpr int kAttStages = 3;
 constexpr float kPShift = 15.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -154,16 +159,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return r;
 }
 
-// N 32-bit words of cached bytes (read once, kept out of L1)
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
-  if constexpr (N == 4)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-  else if constexpr (N == 2)
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  else
-    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+  if constexpr (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 // first token position that query row `row` of a sequence of `len` tokens does not see
@@ -191,9 +197,19 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
   constexpr int KW = D / 32;       // words of one token's keys per lane
   constexpr int VW = D / 64;       // words of one token's values per lane
   constexpr int R = 8 * NT;        // query rows of the block
+  // a stage: keys and values of 32 tokens, then their scales
+  constexpr int kData = kAttGroup * D / 2, kSf = kAttGroup * D / 16, kStage = 2 * (kData + kSf);
+  extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage][kStage]; the warps' sums at the end
+  __shared__ __align__(8) uint64_t full[kAttWarps][kAttStages];
+  __shared__ int held_by[kAttWarps][kAttStages];    // which 16-token halves of a stage were copied
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, cc = lane & 3;
+  if (lane < kAttStages) mbar_init(&full[warp][lane], 1);
+  if (tid == 0) abort_flag = 0;
+  fence_mbar_init();
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, cc = lane & 3;
   const int split = blockIdx.x, kvh = blockIdx.y / a.row_blocks, b = blockIdx.z;
   const int row0 = (blockIdx.y - kvh * a.row_blocks) * R;
   const int rows_here = min(R, a.q_len * a.group - row0);
@@ -208,6 +224,42 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
   if (split > 0 && first >= seen) return;                            // the join does not read these parts
   const int end = min(seen, first + a.chunk);
   const int all_see = row_limit(a, len, row0);                       // every row sees the tokens before it
+
+  // Lane 4u + w copies array w (keys, values, their scales) of the stage's u-th 16 tokens, or of all
+  // 32 where a page holds them (u = 0). Copies stay inside a page whatever the sequence's length.
+  uint8_t* const my_ring = ring + warp * (kAttStages * kStage);
+  const int32_t* table = a.table + b * a.ld_table;
+  const bool wide = c.page_shift >= 5;
+  const int half = (lane >> 2) & 1, arr = lane & 3;
+  const uint32_t row_bytes = arr < 2 ? D / 2 : D / 16;
+  const uint8_t* const from = (arr == 0 ? c.data[0] : arr == 1 ? c.data[1] : arr == 2 ? c.sf[0] : c.sf[1]) +
+                              (static_cast<int64_t>(kvh) << c.page_shift) * row_bytes;
+  const int64_t from_page = arr < 2 ? c.data_page : c.sf_page;
+  const uint32_t to = (arr < 2 ? arr * kData : 2 * kData + (arr - 2) * kSf) + half * 16 * row_bytes;
+  auto page_of = [&](int tok) { return tok + 16 * half < end ? table[(tok + 16 * half) >> c.page_shift] : -1; };
+  auto issue = [&](int stage, int tok, int page) {
+    const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(c.pages);
+    const uint32_t held = __ballot_sync(0xffffffffu, ok) & 0x11;  // lanes 0 and 4
+    if (lane == 0) {
+      held_by[warp][stage] = held;
+      mbar_arrive_expect_tx(&full[warp][stage], ((held & 1) + (held >> 4)) * (kStage / 2));
+    }
+    __syncwarp();
+    const int tokens = wide && held == 0x11 ? 32 : 16;
+    if (lane < 8 && ok && (half == 0 || tokens == 16))
+      bulk_load(my_ring + stage * kStage + to, from + page * from_page + ((tok + 16 * half) & ((1 << c.page_shift) - 1)) * row_bytes,
+                tokens * row_bytes, &full[warp][stage]);
+  };
+  int tok = first + warp * kAttGroup, page = -1;
+  {
+    int p[kAttStages + 1];
+#pragma unroll
+    for (int i = 0; i <= kAttStages; ++i) p[i] = page_of(tok + i * kAttStep);
+#pragma unroll
+    for (int i = 0; i < kAttStages; ++i)
+      if (tok + i * kAttStep < end) issue(i, tok + i * kAttStep, p[i]);
+    page = p[kAttStages];
+  }
 
   // Q^T fragments and each row's factor from raw sums to base-2 scores
   uint32_t q[NT][KS][2];
@@ -256,67 +308,25 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
     l[t][0] = l[t][1] = 0.0f;
   }
 
-  uint32_t kw[2][2][KW], ksf[2][2], vw[2][4][VW], vsf[2][4];
-  int page[2] = {-1, -1}, next_page[2] = {-1, -1};
-  const int32_t* table = a.table + b * a.ld_table;
-  const int in_page = (1 << c.page_shift) - 1;
-
-  auto load_pages = [&](int* p, int tok) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      p[u] = -1;
-      if (tok + 16 * u < end) p[u] = table[(tok + 16 * u) >> c.page_shift];
-    }
-  };
-  // 16 tokens of a page: every address lies inside the page, whatever the sequence's length
-  auto load_k = [&](const int* p, int tok) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (static_cast<unsigned>(p[u]) < static_cast<unsigned>(c.pages)) {
-        const int64_t at = (static_cast<int64_t>(kvh) << c.page_shift) + ((tok + 16 * u) & in_page) + r;
-        const uint8_t* d = c.data[0] + p[u] * c.data_page + at * (D / 2) + cc * (D / 8);
-        const uint8_t* s = c.sf[0] + p[u] * c.sf_page + at * (D / 16) + cc * (D / 64);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          load_words<KW>(kw[u][h], d + h * 8 * (D / 2));
-          ksf[u][h] = D == 128 ? *reinterpret_cast<const uint16_t*>(s + h * 8 * (D / 16)) : s[h * 8 * (D / 16)];
-        }
-      }
-    }
-  };
-  auto load_v = [&](const int* p, int tok) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (static_cast<unsigned>(p[u]) < static_cast<unsigned>(c.pages)) {
-        const int64_t at = (static_cast<int64_t>(kvh) << c.page_shift) + ((tok + 16 * u) & in_page) + 2 * cc;
-        const uint8_t* d = c.data[1] + p[u] * c.data_page + at * (D / 2) + r * (D / 16);
-        const uint8_t* s = c.sf[1] + p[u] * c.sf_page + at * (D / 16) + r * (D / 16) / 8;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int row = (h & 1) + 8 * (h >> 1);
-          load_words<VW>(vw[u][h], d + row * (D / 2));
-          vsf[u][h] = s[row * (D / 16)];
-        }
-      }
-    }
-  };
-
-  int tok = first + warp * kAttGroup;
-  load_pages(page, tok);
-  load_k(page, tok);
-  load_v(page, tok);
-  load_pages(next_page, tok + kAttStep);
+  int stage = 0;
+  uint32_t parity = 0;
   for (; tok < end; tok += kAttStep) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &abort_flag, a.dev_status, kWaitLimitNs))) break;
+    const uint8_t* const st = my_ring + stage * kStage;
+    const int held = held_by[warp][stage];
     // ---- scores of 32 tokens
     float s[2][NT][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.0f;
-      uint32_t sc[2][2];  // [token half][block], a scale in both halves
+      uint32_t kw[2][KW], sc[2][2];  // [token r or r + 8][...]; a block's scale in both halves
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t two = e4m3x2_to_f16x2(ksf[u][h]);
+        const int row = 16 * u + 8 * h + r;
+        load_words<KW>(kw[h], st + row * (D / 2) + cc * (D / 8));
+        const uint8_t* f = st + 2 * kData + row * (D / 16) + cc * (D / 64);
+        const uint32_t two = e4m3x2_to_f16x2(D == 128 ? *reinterpret_cast<const uint16_t*>(f) : *f);
         sc[h][0] = __byte_perm(two, two, 0x1010);
         sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
       }
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
       for (int w = 0; w < KW; ++w) {  // a word is two steps
         uint32_t f[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) e2m1x8_to_f16x2(kw[u][h][w], f[h]);
+        for (int h = 0; h < 2; ++h) e2m1x8_to_f16x2(kw[h][w], f[h]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t x[4] = {mul_f16x2(f[0][2 * j], sc[0][w / 2]), mul_f16x2(f[1][2 * j], sc[1][w / 2]),
@@ -334,12 +344,6 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
         }
       }
     }
-    const bool more = tok + kAttStep < end;
-    bool held[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) held[u] = static_cast<unsigned>(page[u]) < static_cast<unsigned>(c.pages);
-    if (more) load_k(next_page, tok + kAttStep);
-
     // ---- running maximum, weights
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -347,24 +351,29 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[u][t][i] *= to_log2[t][i & 1];
-    if (tok + kAttGroup > min(all_see, end) || !held[0] || !held[1]) {
+    uint32_t vsf[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        vsf[u][h] = st[2 * kData + kSf + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 16) + r * (D / 16) / 8];
+    if (tok + kAttGroup > min(all_see, end) || held != 0x11) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if (!held[u] && tok + 16 * u < end && a.dev_status && lane == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
+        const bool here = held >> (4 * u) & 1;
+        if (!here && tok + 16 * u < end && a.dev_status && lane == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = tok + 16 * u + r + 8 * (i >> 1);
             const int lim = min(end, row_limit(a, len, row0 + 8 * t + 2 * cc + (i & 1)));
-            if (!held[u] || at >= lim) s[u][t][i] = -INFINITY;
+            if (!here || at >= lim) s[u][t][i] = -INFINITY;
           }
         // values past the sequence's end may be anything: a zero scale keeps them out
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const bool out = !held[u] || tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1) >= end;
-          if (out) vsf[u][h] = 0;
-        }
+        for (int h = 0; h < 4; ++h)
+          if (!here || tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1) >= end) vsf[u][h] = 0;
       }
     }
     uint32_t p[2][NT][2];
@@ -408,15 +417,19 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
     for (int u = 0; u < 2; ++u) {
       const uint32_t s01 = e4m3x2_to_f16x2(vsf[u][0] | vsf[u][1] << 8);
       const uint32_t s89 = e4m3x2_to_f16x2(vsf[u][2] | vsf[u][3] << 8);
+      uint32_t vw[4][VW];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        load_words<VW>(vw[h], st + kData + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 2) + r * (D / 16));
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
         // bytes that pair one dimension's codes of two neighbouring tokens
         const uint32_t low = 0x0F0F0F0Fu;
         uint32_t f[4][4];
-        e2m1x8_to_f16x2((vw[u][0][w] & low) | (vw[u][1][w] << 4 & ~low), f[0]);
-        e2m1x8_to_f16x2((vw[u][0][w] >> 4 & low) | (vw[u][1][w] & ~low), f[1]);
-        e2m1x8_to_f16x2((vw[u][2][w] & low) | (vw[u][3][w] << 4 & ~low), f[2]);
-        e2m1x8_to_f16x2((vw[u][2][w] >> 4 & low) | (vw[u][3][w] & ~low), f[3]);
+        e2m1x8_to_f16x2((vw[0][w] & low) | (vw[1][w] << 4 & ~low), f[0]);
+        e2m1x8_to_f16x2((vw[0][w] >> 4 & low) | (vw[1][w] & ~low), f[1]);
+        e2m1x8_to_f16x2((vw[2][w] & low) | (vw[3][w] << 4 & ~low), f[2]);
+        e2m1x8_to_f16x2((vw[2][w] >> 4 & low) | (vw[3][w] & ~low), f[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t x[4] = {mul_f16x2(f[0][i], s01), mul_f16x2(f[1][i], s01), mul_f16x2(f[2][i], s89),
@@ -426,15 +439,28 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
         }
       }
     }
-    if (more) load_v(next_page, tok + kAttStep);
-    page[0] = next_page[0], page[1] = next_page[1];
-    load_pages(next_page, tok + 2 * kAttStep);
+    __syncwarp();  // every lane has read the stage
+    const int next = tok + kAttStages * kAttStep;
+    if (next < end) {
+      issue(stage, next, page);
+      page = page_of(next + kAttStep);
+    }
+    if (++stage == kAttStages) stage = 0, parity ^= 1;
   }
+  // after a wait that gave up: the stages still in flight, before their memory is used again
+  for (int i = 0; i < kAttStages && tok < end; ++i, tok += kAttStep) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(&full[warp][stage], parity) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    }
+    if (++stage == kAttStages) stage = 0, parity ^= 1;
+  }
+  __syncthreads();
 
   // ---- join the warps
   constexpr int ST = D + 4;
   __shared__ float sm[kAttWarps][R], sl[kAttWarps][R];
-  __shared__ float so[kAttWarps][R][ST];
+  static_assert(R * ST * 4 <= kAttStages * kStage, "a warp's sums fit its ring");
+  auto so = reinterpret_cast<float(*)[R][ST]>(ring);  // [warp][row][dim]
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -701,7 +727,9 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   const dim3 grid(cut.splits, c.heads * cut.row_blocks, batch);
   auto* kern = c.dim == 64 ? (cut.row_tiles == 1 ? kv_attend_kernel<64, 1> : kv_attend_kernel<64, 2>)
                            : (cut.row_tiles == 1 ? kv_attend_kernel<128, 1> : kv_attend_kernel<128, 2>);
-  const moe_status_t ran = launch_pdl(kern, grid, dim3(kAttWarps * 32), 0, as_stream(stream), c, a);
+  const int smem = kAttWarps * kAttStages * kAttGroup * c.dim * 9 / 8;
+  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const moe_status_t ran = launch_pdl(kern, grid, dim3(kAttWarps * 32), smem, as_stream(stream), c, a);
   if (ran != MOE_OK || cut.splits == 1) return ran;
   return launch_pdl(c.dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>,
                     dim3(static_cast<unsigned>(rows * num_q_heads)), dim3(kJoinThreads), 0, as_stream(stream), c, a);
