@@ -1,0 +1,54 @@
+// FP4 operands on mma.m16n8k16 (FP16 in, FP32 sums): the conversions and instructions that the
+// dense linear and the cache's attention share. Both read each 4-bit value once, for at most 16
+// tokens or query rows, and are bound by HBM; the legacy warp-level MMA takes its operands from
+// registers, where the codes are converted, and its rate is not what limits them. An E2M1 code
+// times an E4M3 scale has 6 significant bits between 2^-10 and 2688: exact in FP16.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// the eight codes of a word, a byte's two to one register. Naming the word's bytes costs nothing;
+// shifting and masking them out costs two more instructions of the pipe that converts.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t* f) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t two) { return __uint_as_float(two << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t two) { return __uint_as_float(two & 0xFFFF0000u); }
+
+// The power of two that takes a largest magnitude `amax` into [2^14, 2^15), and its inverse: BF16
+// values so scaled fit FP16 with their own bits down to 2^-28 of the largest. Zero and the
+// smallest take 2^126; infinity and NaN (whose amax is that of the rest) stay what they are.
+__device__ __forceinline__ void f16_range(float amax, float* up, float* down) {
+  const int shift = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
+  *up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+  *down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+}
+
+}  // namespace moe

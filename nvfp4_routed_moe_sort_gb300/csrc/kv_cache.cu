@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "fp4_mma.cuh"
 #include "host_util.h"
 
 namespace moe {
@@ -119,39 +120,10 @@ struct AttendArgs {
   float scale;
 };
 
-// the eight codes of a word, a byte's two to one register. Naming the word's bytes costs nothing;
-// shifting and masking them out costs two more instructions of the pipe that converts.
-__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t* f) {
-  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
-      : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
@@ -284,16 +256,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
     }
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
-      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[i] << 16)), fabsf(__uint_as_float(raw[i] & 0xFFFF0000u))));
+      amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[i])), fabsf(bf16_hi(raw[i]))));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // 2^shift * amax in [2^14, 2^15); zero and the smallest rows take the largest shift
-    const int shift = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
-    const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+    float up, down;
+    f16_range(amax, &up, &down);
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
-      q[t][i >> 1][i & 1] = pack_f16x2(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xFFFF0000u) * up);
+      q[t][i >> 1][i & 1] = pack_f16x2(bf16_lo(raw[i]) * up, bf16_hi(raw[i]) * up);
     const float f = a.scale * kLog2e / c.g[0] * down;
     to_log2[t][0] = __shfl_sync(0xffffffffu, f, 8 * cc);
     to_log2[t][1] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);

@@ -1,16 +1,33 @@
 // A few tokens times one dense NVFP4 matrix: y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]).
 //
-// A weight is code * scale of its 16-value block, both read in their linear layout. Products
-// with bf16 or e4m3 activations are exact in FP32, sums are FP32, and alpha, the activation
+// Bound by HBM: 9/16 byte per weight, read once per 16 tokens. One block takes kLinRows rows of w
+// and a slice of K, one warp 16 of its rows: mma.m16n8k16 with the 16 weight rows as one operand
+// and eight tokens as the other. Per 128 values of K (a chunk) lane (r, c) = (lane / 4, lane % 4)
+// reads bytes [16c, 16c + 16) of rows r and r + 8 and their two scales each, kLinAhead chunks
+// ahead in registers; MMA step j of the chunk takes its values 32c + 4j to 32c + 4j + 3.
+//
+// The block first lays its slice of x out in shared memory as FP16 in fragment order. Each
+// (token, chunk) has an FP32 factor: the tokens' own scales for E4M3 (exact in FP16), a power of two
+// that brings the chunk's values into FP16's range for BF16. A chunk is summed on its own and
+// enters the FP32 sum times its factor.
+//
+// Blocks that share rows (slices of K) form a cluster; each adds a share of the rows over the
+// cluster's shared memory in rank order, so sums do not depend on timing. alpha, the activation
 // and the BF16 rounding come once at the end.
 #include "common.cuh"
+#include "fp4_mma.cuh"
 #include "host_util.h"
 
 namespace moe {
 namespace {
 
-constexpr int kLinThreads = 256;
+constexpr int kLinWarps = 8;
+constexpr int kLinThreads = kLinWarps * 32;
+constexpr int kLinRows = kLinWarps * 16;  // rows of w per block; gated: half gate, half up rows
 constexpr int kLinTokens = 16;
+constexpr int kLinChunk = 128;            // = MOE_FP8_GROUP
+constexpr int kLinAhead = 4;
+static_assert(kLinChunk == MOE_FP8_GROUP, "one E4M3 scale per chunk");
 
 struct LinArgs {
   const void* x;
@@ -20,7 +37,9 @@ struct LinArgs {
   const float* alpha;
   uint16_t* out;
   int64_t ld_x;
-  int x_mode, M, K, N, n_out, act, x_groups;  // N: rows of w; n_out: columns of out
+  int x_mode, M, K, n_out, act, x_groups;  // n_out: columns of out
+  int slices, slice;                       // blocks of a cluster, chunks of each
+  int tokens;                              // tokens of a block
   bool gated;
 };
 
@@ -45,46 +64,216 @@ __device__ __forceinline__ float activate(int act, float g, float u) {
   }
 }
 
-__device__ __forceinline__ float e2m1_to_f32(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3, m = c & 1;
-  const float v = e == 0 ? 0.5f * m : (1.0f + 0.5f * m) * static_cast<float>(1u << (e - 1));
-  return (c & 8) ? -v : v;
+__device__ __forceinline__ float load_cluster_f32(const float* p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float load_x(const LinArgs& a, int64_t m, int k) {
-  if (a.x_mode == MOE_FP8_NONE)
-    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.x)[m * a.ld_x + k]) << 16);
-  const uint32_t b = static_cast<const uint8_t*>(a.x)[m * a.ld_x + k];
-  const float v = (b & 0x7F) == 0x7F ? __uint_as_float(0x7FFFFFFFu) : e4m3_to_f32(b);
-  return v * a.x_scale[m * a.x_groups + (a.x_mode == MOE_FP8_PER_GROUP ? k / MOE_FP8_GROUP : 0)];
+// 32 codes (16 bytes) of a row at byte `at`, and their two scales
+struct Codes {
+  uint32_t w[4], sf;
+};
+
+// WIDE: rows are multiples of 16 bytes; otherwise of 8. Codes past the row's end read as zero.
+template <bool WIDE>
+__device__ __forceinline__ void load_codes(Codes& d, const uint8_t* w, const uint8_t* sf, int k, int K) {
+  if constexpr (WIDE) {
+    if (k < K) {
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(d.w[0]), "=r"(d.w[1]), "=r"(d.w[2]), "=r"(d.w[3]) : "l"(w + k / 2));
+      d.sf = *reinterpret_cast<const uint16_t*>(sf + k / kBlock);
+    } else {
+      d.w[0] = d.w[1] = d.w[2] = d.w[3] = d.sf = 0;
+    }
+  } else {
+    d.w[0] = d.w[1] = d.w[2] = d.w[3] = d.sf = 0;
+    if (k < K) {
+      const uint2 a = *reinterpret_cast<const uint2*>(w + k / 2);
+      d.w[0] = a.x, d.w[1] = a.y;
+      d.sf = sf[k / kBlock];
+    }
+    if (k + kBlock < K) {
+      const uint2 a = *reinterpret_cast<const uint2*>(w + k / 2 + 8);
+      d.w[2] = a.x, d.w[3] = a.y;
+      d.sf |= static_cast<uint32_t>(sf[k / kBlock + 1]) << 8;
+    }
+  }
 }
 
-// one warp per output column and token, lanes over the 16-value blocks of its weight rows
-__global__ void __launch_bounds__(kLinThreads) linear_kernel(LinArgs a) {
+// NT: groups of eight tokens
+template <int NT, bool WIDE>
+__global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(LinArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kLinThreads + threadIdx.x) >> 5;
-  const int m = blockIdx.y;
-  if (i >= a.n_out) return;
-  float y[2] = {0.0f, 0.0f};
-  for (int h = 0; h < (a.gated ? 2 : 1); ++h) {
-    const int64_t n = i + (h ? a.n_out : 0);
-    float acc = 0.0f;
-    for (int b = lane; b < a.K / kBlock; b += 32) {
-      const float s = e4m3_to_f32(a.sf[n * (a.K / kBlock) + b]);
-      for (int k = 0; k < kBlock; ++k) {
-        const uint32_t c = a.w[n * (a.K / 2) + b * 8 + k / 2] >> (4 * (k & 1));
-        acc += load_x(a, m, b * kBlock + k) * (e2m1_to_f32(c & 15) * s);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+  const int rank = blockIdx.x % a.slices;
+  const int64_t block = blockIdx.x / a.slices;
+  const int m0 = blockIdx.y * a.tokens, M = min(a.M - m0, a.tokens);
+  const int chunk0 = rank * a.slice;
+  const int chunks = max(0, min(a.slice, (a.K + kLinChunk - 1) / kLinChunk - chunk0));
+  // shared memory: x [M][chunks * 256 + 64 bytes], factors [slice][8 * NT], sums [kLinRows][8 * NT + 1]
+  const int x_row = a.slice * (kLinChunk * 2) + 64;
+  float* const factor = reinterpret_cast<float*>(smem + M * x_row);
+  float* const sums = factor + a.slice * 8 * NT;
+  constexpr int kSumRow = 8 * NT + 1;
+
+  // this warp's 16 rows: rows of the block are output columns block * n_per + i, first as gate (or
+  // plain) rows, then, for the gated kinds, the same columns' up rows
+  const int n_per = a.gated ? kLinRows / 2 : kLinRows;
+  const bool up = a.gated && warp >= kLinWarps / 2;
+  const int i0 = (up ? warp - kLinWarps / 2 : warp) * 16;
+  const uint8_t *w[2], *sf[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int64_t n = block * n_per + i0 + r + 8 * h;
+    if (n >= a.n_out) n = a.n_out - 1;  // computed and dropped
+    if (up) n += a.n_out;
+    w[h] = a.w + n * (a.K / 2);
+    sf[h] = a.sf + n * (a.K / kBlock);
+  }
+  const int k_lane = chunk0 * kLinChunk + 32 * c, k_end = min(a.K, (chunk0 + chunks) * kLinChunk);
+  Codes buf[kLinAhead][2];
+#pragma unroll
+  for (int u = 0; u < kLinAhead; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_codes<WIDE>(buf[u][h], w[h], sf[h], k_lane + u * kLinChunk, k_end);
+
+  // x: half a warp per (token, chunk), eight values a lane
+  for (int i = tid >> 4; i < M * chunks; i += kLinThreads / 16) {
+    const int m = i / chunks, ch = i - m * chunks, piece = tid & 15;
+    const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
+    uint4 f = make_uint4(0, 0, 0, 0);
+    float scale;
+    if (a.x_mode == MOE_FP8_NONE) {
+      if (k < a.K) f = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (m0 + m) * a.ld_x + k);
+      const uint32_t raw[4] = {f.x, f.y, f.z, f.w};
+      float amax = 0.0f, grow;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[j])), fabsf(bf16_hi(raw[j]))));
+      const uint32_t half_warp = 0xFFFFu << (lane & 16);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half_warp, amax, o));
+      f16_range(amax, &grow, &scale);
+      f = make_uint4(pack_f16x2(bf16_lo(raw[0]) * grow, bf16_hi(raw[0]) * grow),
+                     pack_f16x2(bf16_lo(raw[1]) * grow, bf16_hi(raw[1]) * grow),
+                     pack_f16x2(bf16_lo(raw[2]) * grow, bf16_hi(raw[2]) * grow),
+                     pack_f16x2(bf16_lo(raw[3]) * grow, bf16_hi(raw[3]) * grow));
+    } else {
+      uint2 e = make_uint2(0, 0);
+      if (k < a.K) e = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + (m0 + m) * a.ld_x + k);
+      f = make_uint4(e4m3x2_to_f16x2(e.x & 0xFFFF), e4m3x2_to_f16x2(e.x >> 16), e4m3x2_to_f16x2(e.y & 0xFFFF),
+                     e4m3x2_to_f16x2(e.y >> 16));
+      scale = a.x_scale[static_cast<int64_t>(m0 + m) * a.x_groups + (a.x_mode == MOE_FP8_PER_GROUP ? chunk0 + ch : 0)];
+    }
+    // values 8 * piece + ... belong to lane column piece / 4, steps 2 * (piece % 4) and the next
+    *reinterpret_cast<uint4*>(smem + m * x_row + ch * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16) = f;
+    if (piece == 0) factor[ch * 8 * NT + m] = scale;
+  }
+  for (int i = tid; i < chunks * 8 * NT; i += kLinThreads)
+    if (i % (8 * NT) >= M) factor[i] = 0.0f;  // columns of no token
+  __syncthreads();
+
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+  for (int ch0 = 0; ch0 < chunks; ch0 += kLinAhead) {
+#pragma unroll
+    for (int u = 0; u < kLinAhead; ++u) {
+      const int ch = ch0 + u;
+      if (ch >= chunks) break;
+      uint32_t f[2][4][4];  // [row half][word][byte]
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t two = e4m3x2_to_f16x2(buf[u][h].sf);
+        const uint32_t s[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          e2m1x8_to_f16x2(buf[u][h].w[j], f[h][j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[h][j][i] = mul_f16x2(f[h][j][i], s[j / 2]);
+        }
+        load_codes<WIDE>(buf[u][h], w[h], sf[h], k_lane + (ch + kLinAhead) * kLinChunk, k_end);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (8 * t + r < M) x = *reinterpret_cast<const uint4*>(smem + (8 * t + r) * x_row + ch * 256 + (4 * j + c) * 16);
+          const uint32_t b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t A[4] = {f[0][j][2 * i], f[1][j][2 * i], f[0][j][2 * i + 1], f[1][j][2 * i + 1]};
+            mma_f16(part, A, b + 2 * i);
+          }
+        }
+        const float2 s = *reinterpret_cast<const float2*>(factor + (ch * NT + t) * 8 + 2 * c);
+        acc[t][0] += part[0] * s.x, acc[t][1] += part[1] * s.y, acc[t][2] += part[2] * s.x, acc[t][3] += part[3] * s.y;
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    y[h] = acc * *a.alpha;
   }
-  if (lane == 0)
-    a.out[static_cast<int64_t>(m) * a.n_out + i] =
+
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sums[(warp * 16 + r + 8 * (i >> 1)) * kSumRow + 8 * t + 2 * c + (i & 1)] = acc[t][i];
+  if (a.slices > 1) cluster_sync();
+  else __syncthreads();
+  const float alpha = *a.alpha;
+  for (int i = rank * kLinThreads + tid; i < n_per * M; i += a.slices * kLinThreads) {
+    const int m = i / n_per, col = i - m * n_per;
+    const int64_t n = block * n_per + col;
+    if (n >= a.n_out) continue;
+    float y[2] = {0.0f, 0.0f};
+    for (int g = 0; g < (a.gated ? 2 : 1); ++g) {
+      const float* p = sums + (col + g * n_per) * kSumRow + m;
+      if (a.slices == 1) y[g] = *p;
+      else
+        for (int s = 0; s < a.slices; ++s) y[g] += load_cluster_f32(p, s);
+      y[g] *= alpha;
+    }
+    a.out[static_cast<int64_t>(m0 + m) * a.n_out + n] =
         __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0], y[1])));
+  }
+  if (a.slices > 1) cluster_sync();  // the others may still read this block's sums
+}
+
+template <int NT, bool WIDE>
+moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.slices;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (smem > 48 * 1024)
+    MOE_CUDA(cudaFuncSetAttribute(linear_kernel<NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+  return cudaLaunchKernelEx(&cfg, linear_kernel<NT, WIDE>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+constexpr size_t kLinSmem = 100 * 1024, kLinSmemMost = 227 * 1024;  // two blocks per SM; the most of one
+
+size_t linear_smem(int tokens, int slice) {
+  const int columns = tokens > 8 ? 16 : 8;
+  return static_cast<size_t>(tokens) * (slice * kLinChunk * 2 + 64) + static_cast<size_t>(slice) * columns * 4 +
+         static_cast<size_t>(kLinRows) * (columns + 1) * 4;
 }
 
 }  // namespace
@@ -108,14 +297,36 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
   MOE_CHECK(aligned16(x) && aligned16(x_scale) && aligned16(w) && aligned16(w_sf) && aligned16(alpha) &&
                 aligned16(out) && ld_x % (fp8 ? 16 : 8) == 0,
             MOE_ERR_MISALIGNED);
-  LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, N, gated ? N / 2 : N, activation,
-               x_scale_mode == MOE_FP8_PER_GROUP ? (K + MOE_FP8_GROUP - 1) / MOE_FP8_GROUP : 1, gated};
+  const int chunks = (K + kLinChunk - 1) / kLinChunk;
+  LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, gated ? N / 2 : N, activation,
+               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, gated};
   const size_t ob = static_cast<size_t>(M) * a.n_out * 2;
   MOE_CHECK(!overlaps(out, ob, x, (static_cast<size_t>(M - 1) * ld_x + K) * (fp8 ? 1 : 2)) &&
                 !overlaps(out, ob, w, static_cast<size_t>(N) * K / 2) &&
                 !overlaps(out, ob, w_sf, static_cast<size_t>(N) * K / kBlock) && !overlaps(out, ob, alpha, 4) &&
                 !overlaps(out, ob, x_scale, static_cast<size_t>(M) * a.x_groups * 4),
             MOE_ERR_OVERLAP);
-  const unsigned warps = kLinThreads / 32;
-  return launch_pdl(linear_kernel, dim3((a.n_out + warps - 1) / warps, M), dim3(kLinThreads), 0, as_stream(stream), a);
+  // Slices of K: as many as fill two blocks per SM, and as x's share of shared memory asks for.
+  const int n_per = gated ? kLinRows / 2 : kLinRows;
+  const int64_t blocks = (static_cast<int64_t>(a.n_out) + n_per - 1) / n_per;
+  auto cut = [&](int most) {  // blocks of at most `most` tokens
+    a.tokens = M < most ? M : most;
+    a.slices = 1, a.slice = chunks;
+    const int64_t groups = (static_cast<int64_t>(M) + a.tokens - 1) / a.tokens;
+    while (a.slices < 8 && a.slices < chunks &&
+           (blocks * groups * a.slices < 2 * num_sms() || linear_smem(a.tokens, a.slice) > kLinSmem)) {
+      a.slices *= 2;
+      a.slice = (chunks + a.slices - 1) / a.slices;
+    }
+    return groups;
+  };
+  int64_t groups = cut(kLinTokens);
+  if (linear_smem(a.tokens, a.slice) > kLinSmemMost) groups = cut(8);  // the longest K
+  const size_t smem = linear_smem(a.tokens, a.slice);
+  MOE_CHECK(blocks * a.slices < (int64_t(1) << 31) && groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
+  const dim3 grid(static_cast<unsigned>(blocks * a.slices), static_cast<unsigned>(groups));
+  const bool wide = K % 32 == 0;
+  cudaStream_t s = as_stream(stream);
+  if (a.tokens <= 8) return wide ? launch_linear<1, true>(a, grid, smem, s) : launch_linear<1, false>(a, grid, smem, s);
+  return wide ? launch_linear<2, true>(a, grid, smem, s) : launch_linear<2, false>(a, grid, smem, s);
 }
