@@ -11,9 +11,11 @@
 // that brings the chunk's values into FP16's range for BF16. A chunk is summed on its own and
 // enters the FP32 sum times its factor.
 //
-// Blocks that share rows (slices of K) form a cluster; each adds a share of the rows over the
-// cluster's shared memory in rank order, so sums do not depend on timing. alpha, the activation
-// and the BF16 rounding come once at the end.
+// Blocks that share rows (slices of K) form a cluster. A row belongs to one of them: the others
+// store their sums into its shared memory, and after one cluster barrier it adds them in rank
+// order, so results do not depend on timing. alpha, the activation and the BF16 rounding come
+// once at the end. A block goes on to further rows while there are any, its first chunks of them
+// already in flight.
 #include "common.cuh"
 #include "fp4_mma.cuh"
 #include "host_util.h"
@@ -64,16 +66,13 @@ __device__ __forceinline__ float activate(int act, float g, float u) {
   }
 }
 
-__device__ __forceinline__ float load_cluster_f32(const float* p, uint32_t rank) {
+__device__ __forceinline__ void store_cluster_f32(float* p, uint32_t rank, float v) {
   uint32_t at;
-  float v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // 32 codes (16 bytes) of a row at byte `at`, and their two scales
 struct Codes {
@@ -114,137 +113,178 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(LinArgs a) {
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   const int rank = blockIdx.x % a.slices;
-  const int64_t block = blockIdx.x / a.slices;
+  if (a.slices > 1) cluster_arrive();  // this block has started: its shared memory may be written
   const int m0 = blockIdx.y * a.tokens, M = min(a.M - m0, a.tokens);
   const int chunk0 = rank * a.slice;
   const int chunks = max(0, min(a.slice, (a.K + kLinChunk - 1) / kLinChunk - chunk0));
-  // shared memory: x [M][chunks * 256 + 64 bytes], factors [slice][8 * NT], sums [kLinRows][8 * NT + 1]
+  const int steps = (chunks + kLinAhead - 1) / kLinAhead * kLinAhead;
+  // shared memory: x [M][slice * 256 + 64 bytes], factors [slice][8 * NT], sums (twice) [kLinRows][8 * NT + 1]
   const int x_row = a.slice * (kLinChunk * 2) + 64;
   float* const factor = reinterpret_cast<float*>(smem + M * x_row);
-  float* const sums = factor + a.slice * 8 * NT;
   constexpr int kSumRow = 8 * NT + 1;
+  float* sums = factor + a.slice * 8 * NT;
+  float* sums_next = sums + kLinRows * kSumRow;
 
-  // this warp's 16 rows: rows of the block are output columns block * n_per + i, first as gate (or
-  // plain) rows, then, for the gated kinds, the same columns' up rows
+  // A row block is n_per output columns: their rows of w, or for the gated kinds their gate rows
+  // (first half of the warps) and up rows (second half)
   const int n_per = a.gated ? kLinRows / 2 : kLinRows;
   const bool up = a.gated && warp >= kLinWarps / 2;
-  const int i0 = (up ? warp - kLinWarps / 2 : warp) * 16;
-  const uint8_t *w[2], *sf[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    int64_t n = block * n_per + i0 + r + 8 * h;
-    if (n >= a.n_out) n = a.n_out - 1;  // computed and dropped
-    if (up) n += a.n_out;
-    w[h] = a.w + n * (a.K / 2);
-    sf[h] = a.sf + n * (a.K / kBlock);
-  }
+  const int i0 = (up ? warp - kLinWarps / 2 : warp) * 16 + r;
+  const int blocks = (a.n_out + n_per - 1) / n_per, stride = gridDim.x / a.slices;
+  int block = blockIdx.x / a.slices;
   const int k_lane = chunk0 * kLinChunk + 32 * c, k_end = min(a.K, (chunk0 + chunks) * kLinChunk);
+  const uint8_t *w[2], *sf[2];
+  auto rows_of = [&](int b) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      int64_t n = min(static_cast<int64_t>(b) * n_per + i0 + 8 * h, static_cast<int64_t>(a.n_out) - 1);  // spare rows are dropped
+      if (up) n += a.n_out;
+      w[h] = a.w + n * (a.K / 2);
+      sf[h] = a.sf + n * (a.K / kBlock);
+    }
+  };
+  rows_of(block);
   Codes buf[kLinAhead][2];
 #pragma unroll
   for (int u = 0; u < kLinAhead; ++u)
 #pragma unroll
     for (int h = 0; h < 2; ++h) load_codes<WIDE>(buf[u][h], w[h], sf[h], k_lane + u * kLinChunk, k_end);
 
-  // x: half a warp per (token, chunk), eight values a lane
-  for (int i = tid >> 4; i < M * chunks; i += kLinThreads / 16) {
-    const int m = i / chunks, ch = i - m * chunks, piece = tid & 15;
-    const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
-    uint4 f = make_uint4(0, 0, 0, 0);
-    float scale;
-    if (a.x_mode == MOE_FP8_NONE) {
-      if (k < a.K) f = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (m0 + m) * a.ld_x + k);
-      const uint32_t raw[4] = {f.x, f.y, f.z, f.w};
-      float amax = 0.0f, grow;
+  // x: half a warp per (token, chunk), eight values a lane, four loads in flight
+  constexpr int kPairs = kLinThreads / 16;
+  for (int i = tid >> 4; i < M * chunks; i += 4 * kPairs) {
+    const int piece = tid & 15;
+    uint4 raw[4];
+    float scale[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[j])), fabsf(bf16_hi(raw[j]))));
-      const uint32_t half_warp = 0xFFFFu << (lane & 16);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half_warp, amax, o));
-      f16_range(amax, &grow, &scale);
-      f = make_uint4(pack_f16x2(bf16_lo(raw[0]) * grow, bf16_hi(raw[0]) * grow),
-                     pack_f16x2(bf16_lo(raw[1]) * grow, bf16_hi(raw[1]) * grow),
-                     pack_f16x2(bf16_lo(raw[2]) * grow, bf16_hi(raw[2]) * grow),
-                     pack_f16x2(bf16_lo(raw[3]) * grow, bf16_hi(raw[3]) * grow));
-    } else {
-      uint2 e = make_uint2(0, 0);
-      if (k < a.K) e = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + (m0 + m) * a.ld_x + k);
-      f = make_uint4(e4m3x2_to_f16x2(e.x & 0xFFFF), e4m3x2_to_f16x2(e.x >> 16), e4m3x2_to_f16x2(e.y & 0xFFFF),
-                     e4m3x2_to_f16x2(e.y >> 16));
-      scale = a.x_scale[static_cast<int64_t>(m0 + m) * a.x_groups + (a.x_mode == MOE_FP8_PER_GROUP ? chunk0 + ch : 0)];
+    for (int u = 0; u < 4; ++u) {
+      const int m = (i + u * kPairs) / chunks, ch = i + u * kPairs - m * chunks;
+      const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (m >= M) continue;
+      if (a.x_mode == MOE_FP8_NONE) {
+        if (k < a.K) raw[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (m0 + m) * a.ld_x + k);
+      } else {
+        if (k < a.K) {
+          const uint2 e = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + (m0 + m) * a.ld_x + k);
+          raw[u].x = e.x, raw[u].y = e.y;
+        }
+        scale[u] = a.x_scale[static_cast<int64_t>(m0 + m) * a.x_groups + (a.x_mode == MOE_FP8_PER_GROUP ? chunk0 + ch : 0)];
+      }
     }
-    // values 8 * piece + ... belong to lane column piece / 4, steps 2 * (piece % 4) and the next
-    *reinterpret_cast<uint4*>(smem + m * x_row + ch * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16) = f;
-    if (piece == 0) factor[ch * 8 * NT + m] = scale;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int m = (i + u * kPairs) / chunks, ch = i + u * kPairs - m * chunks;
+      if (m >= M) break;
+      const uint32_t v[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      uint4 f;
+      if (a.x_mode == MOE_FP8_NONE) {
+        float amax = 0.0f, grow;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(v[j])), fabsf(bf16_hi(v[j]))));
+        const uint32_t half_warp = 0xFFFFu << (lane & 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half_warp, amax, o));
+        f16_range(amax, &grow, &scale[u]);
+        f = make_uint4(pack_f16x2(bf16_lo(v[0]) * grow, bf16_hi(v[0]) * grow),
+                       pack_f16x2(bf16_lo(v[1]) * grow, bf16_hi(v[1]) * grow),
+                       pack_f16x2(bf16_lo(v[2]) * grow, bf16_hi(v[2]) * grow),
+                       pack_f16x2(bf16_lo(v[3]) * grow, bf16_hi(v[3]) * grow));
+      } else {
+        f = make_uint4(e4m3x2_to_f16x2(v[0] & 0xFFFF), e4m3x2_to_f16x2(v[0] >> 16), e4m3x2_to_f16x2(v[1] & 0xFFFF),
+                       e4m3x2_to_f16x2(v[1] >> 16));
+      }
+      // piece p is half of lane column p / 4's share: its steps 2 * (p % 4) and the next
+      *reinterpret_cast<uint4*>(smem + m * x_row + ch * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16) = f;
+      if (piece == 0) factor[ch * 8 * NT + m] = scale[u];
+    }
   }
   for (int i = tid; i < chunks * 8 * NT; i += kLinThreads)
     if (i % (8 * NT) >= M) factor[i] = 0.0f;  // columns of no token
   __syncthreads();
 
-  float acc[NT][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-  for (int ch0 = 0; ch0 < chunks; ch0 += kLinAhead) {
-#pragma unroll
-    for (int u = 0; u < kLinAhead; ++u) {
-      const int ch = ch0 + u;
-      if (ch >= chunks) break;
-      uint32_t f[2][4][4];  // [row half][word][byte]
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t two = e4m3x2_to_f16x2(buf[u][h].sf);
-        const uint32_t s[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          e2m1x8_to_f16x2(buf[u][h].w[j], f[h][j]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[h][j][i] = mul_f16x2(f[h][j][i], s[j / 2]);
-        }
-        load_codes<WIDE>(buf[u][h], w[h], sf[h], k_lane + (ch + kLinAhead) * kLinChunk, k_end);
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (8 * t + r < M) x = *reinterpret_cast<const uint4*>(smem + (8 * t + r) * x_row + ch * 256 + (4 * j + c) * 16);
-          const uint32_t b[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t A[4] = {f[0][j][2 * i], f[1][j][2 * i], f[0][j][2 * i + 1], f[1][j][2 * i + 1]};
-            mma_f16(part, A, b + 2 * i);
-          }
-        }
-        const float2 s = *reinterpret_cast<const float2*>(factor + (ch * NT + t) * 8 + 2 * c);
-        acc[t][0] += part[0] * s.x, acc[t][1] += part[1] * s.y, acc[t][2] += part[2] * s.x, acc[t][3] += part[3] * s.y;
-      }
-    }
-  }
-
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sums[(warp * 16 + r + 8 * (i >> 1)) * kSumRow + 8 * t + 2 * c + (i & 1)] = acc[t][i];
-  if (a.slices > 1) cluster_sync();
-  else __syncthreads();
+  const int share = n_per / a.slices, kinds = a.gated ? 2 : 1;
   const float alpha = *a.alpha;
-  for (int i = rank * kLinThreads + tid; i < n_per * M; i += a.slices * kLinThreads) {
-    const int m = i / n_per, col = i - m * n_per;
-    const int64_t n = block * n_per + col;
-    if (n >= a.n_out) continue;
-    float y[2] = {0.0f, 0.0f};
-    for (int g = 0; g < (a.gated ? 2 : 1); ++g) {
-      const float* p = sums + (col + g * n_per) * kSumRow + m;
-      if (a.slices == 1) y[g] = *p;
-      else
-        for (int s = 0; s < a.slices; ++s) y[g] += load_cluster_f32(p, s);
-      y[g] *= alpha;
+  if (a.slices > 1) cluster_wait();
+  for (; block < blocks; block += stride) {
+    float acc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+    for (int ch0 = 0; ch0 < steps; ch0 += kLinAhead) {
+      // what is loaded while this step's chunks are computed: the row block's next, or the next block's first
+      const bool last = ch0 + kLinAhead >= steps;
+      const int k_next = last ? k_lane : k_lane + (ch0 + kLinAhead) * kLinChunk;
+      const int k_stop = last && block + stride >= blocks ? 0 : k_end;
+      if (last) rows_of(block + stride);
+#pragma unroll
+      for (int u = 0; u < kLinAhead; ++u) {
+        const int ch = ch0 + u;
+        uint32_t f[2][4][4];  // [row half][word][byte]
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t two = e4m3x2_to_f16x2(buf[u][h].sf);
+          const uint32_t s[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e2m1x8_to_f16x2(buf[u][h].w[j], f[h][j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[h][j][i] = mul_f16x2(f[h][j][i], s[j / 2]);
+          }
+          load_codes<WIDE>(buf[u][h], w[h], sf[h], k_next + u * kLinChunk, k_stop);
+        }
+        if (ch >= chunks) continue;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (8 * t + r < M) x = *reinterpret_cast<const uint4*>(smem + (8 * t + r) * x_row + ch * 256 + (4 * j + c) * 16);
+            const uint32_t b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t A[4] = {f[0][j][2 * i], f[1][j][2 * i], f[0][j][2 * i + 1], f[1][j][2 * i + 1]};
+              mma_f16(part, A, b + 2 * i);
+            }
+          }
+          const float2 s = *reinterpret_cast<const float2*>(factor + (ch * NT + t) * 8 + 2 * c);
+          acc[t][0] += part[0] * s.x, acc[t][1] += part[1] * s.y, acc[t][2] += part[2] * s.x, acc[t][3] += part[3] * s.y;
+        }
+      }
     }
-    a.out[static_cast<int64_t>(m0 + m) * a.n_out + n] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0], y[1])));
+
+    // sums [rank][kind][column of the owner's share][token], in the owner's shared memory
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int owner = (i0 + 8 * h) / share;
+      float* const to = sums + ((rank * kinds + (up ? 1 : 0)) * share + i0 + 8 * h - owner * share) * kSumRow + 2 * c;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (a.slices > 1) store_cluster_f32(to + 8 * t + i, owner, acc[t][2 * h + i]);
+          else to[8 * t + i] = acc[t][2 * h + i];
+        }
+    }
+    if (a.slices > 1) cluster_arrive(), cluster_wait();
+    else __syncthreads();
+    for (int i = tid; i < share * M; i += kLinThreads) {
+      const int m = i / share, col = i - m * share;
+      const int64_t n = static_cast<int64_t>(block) * n_per + rank * share + col;
+      if (n >= a.n_out) continue;
+      float y[2] = {0.0f, 0.0f};
+      for (int s = 0; s < a.slices; ++s) {
+        y[0] += sums[(s * kinds * share + col) * kSumRow + m];
+        if (a.gated) y[1] += sums[((s * 2 + 1) * share + col) * kSumRow + m];
+      }
+      a.out[static_cast<int64_t>(m0 + m) * a.n_out + n] =
+          __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0] * alpha, y[1] * alpha)));
+    }
+    // The other buffer is free: what it held was added before the barrier above.
+    float* const t = sums;
+    sums = sums_next;
+    sums_next = t;
   }
-  if (a.slices > 1) cluster_sync();  // the others may still read this block's sums
 }
 
 template <int NT, bool WIDE>
@@ -273,7 +313,7 @@ constexpr size_t kLinSmem = 100 * 1024, kLinSmemMost = 227 * 1024;  // two block
 size_t linear_smem(int tokens, int slice) {
   const int columns = tokens > 8 ? 16 : 8;
   return static_cast<size_t>(tokens) * (slice * kLinChunk * 2 + 64) + static_cast<size_t>(slice) * columns * 4 +
-         static_cast<size_t>(kLinRows) * (columns + 1) * 4;
+         2 * static_cast<size_t>(kLinRows) * (columns + 1) * 4;
 }
 
 }  // namespace
@@ -306,7 +346,7 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
                 !overlaps(out, ob, w_sf, static_cast<size_t>(N) * K / kBlock) && !overlaps(out, ob, alpha, 4) &&
                 !overlaps(out, ob, x_scale, static_cast<size_t>(M) * a.x_groups * 4),
             MOE_ERR_OVERLAP);
-  // Slices of K: as many as fill two blocks per SM, and as x's share of shared memory asks for.
+  // Slices of K: as long as all blocks run at once, two to an SM, and as x's share of shared memory asks for.
   const int n_per = gated ? kLinRows / 2 : kLinRows;
   const int64_t blocks = (static_cast<int64_t>(a.n_out) + n_per - 1) / n_per;
   auto cut = [&](int most) {  // blocks of at most `most` tokens
@@ -314,7 +354,7 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
     a.slices = 1, a.slice = chunks;
     const int64_t groups = (static_cast<int64_t>(M) + a.tokens - 1) / a.tokens;
     while (a.slices < 8 && a.slices < chunks &&
-           (blocks * groups * a.slices < 2 * num_sms() || linear_smem(a.tokens, a.slice) > kLinSmem)) {
+           (blocks * groups * a.slices <= num_sms() || linear_smem(a.tokens, a.slice) > kLinSmem)) {
       a.slices *= 2;
       a.slice = (chunks + a.slices - 1) / a.slices;
     }
@@ -323,8 +363,10 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
   int64_t groups = cut(kLinTokens);
   if (linear_smem(a.tokens, a.slice) > kLinSmemMost) groups = cut(8);  // the longest K
   const size_t smem = linear_smem(a.tokens, a.slice);
-  MOE_CHECK(blocks * a.slices < (int64_t(1) << 31) && groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
-  const dim3 grid(static_cast<unsigned>(blocks * a.slices), static_cast<unsigned>(groups));
+  MOE_CHECK(groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
+  // two blocks per SM; they take row blocks in turn
+  const int64_t at_once = 2 * num_sms() / a.slices;
+  const dim3 grid(static_cast<unsigned>((blocks < at_once ? blocks : at_once) * a.slices), static_cast<unsigned>(groups));
   const bool wide = K % 32 == 0;
   cudaStream_t s = as_stream(stream);
   if (a.tokens <= 8) return wide ? launch_linear<1, true>(a, grid, smem, s) : launch_linear<1, false>(a, grid, smem, s);
