@@ -1,7 +1,7 @@
 // A few tokens times one dense NVFP4 matrix: y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]).
 //
-// Bound by HBM: 9/16 byte per weight, read once per 16 tokens. One block takes kLinRows rows of w
-// and a slice of K, one warp 16 of its rows: mma.m16n8k16 with the 16 weight rows as one operand
+// Bound by HBM: 9/16 byte per weight, read once per 16 tokens. A block of warps takes 16 rows
+// of w each and a slice of K: mma.m16n8k16 with the 16 weight rows as one operand
 // and eight tokens as the other. Per 128 values of K (a chunk) lane (r, c) = (lane / 4, lane % 4)
 // reads bytes [16c, 16c + 16) of rows r and r + 8 and their two scales each, kLinAhead chunks
 // ahead in registers; MMA step j of the chunk takes its values 32c + 4j to 32c + 4j + 3.
@@ -23,9 +23,7 @@
 namespace moe {
 namespace {
 
-constexpr int kLinWarps = 8;
-constexpr int kLinThreads = kLinWarps * 32;
-constexpr int kLinRows = kLinWarps * 16;  // rows of w per block; gated: half gate, half up rows
+constexpr int kLinWarps = 8;              // most warps of a block, 16 rows of w each
 constexpr int kLinTokens = 16;
 constexpr int kLinChunk = 128;            // = MOE_FP8_GROUP
 constexpr int kLinAhead = 4;
@@ -42,6 +40,7 @@ struct LinArgs {
   int x_mode, M, K, n_out, act, x_groups;  // n_out: columns of out
   int slices, slice;                       // blocks of a cluster, chunks of each
   int tokens;                              // tokens of a block
+  int warps;                               // of a block; gated: half gate, half up rows
   bool gated;
 };
 
@@ -79,60 +78,61 @@ struct Codes {
   uint32_t w[4], sf;
 };
 
-// WIDE: rows are multiples of 16 bytes; otherwise of 8. Codes past the row's end read as zero.
+// One chunk's share of a lane: w and sf point at it. WIDE: rows are multiples of 16 bytes, otherwise
+// of 8 (a lane's two blocks are loaded one by one).
 template <bool WIDE>
-__device__ __forceinline__ void load_codes(Codes& d, const uint8_t* w, const uint8_t* sf, int k, int K) {
+__device__ __forceinline__ void load_codes(Codes& d, const uint8_t* w, const uint8_t* sf) {
   if constexpr (WIDE) {
-    if (k < K) {
-      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(d.w[0]), "=r"(d.w[1]), "=r"(d.w[2]), "=r"(d.w[3]) : "l"(w + k / 2));
-      d.sf = *reinterpret_cast<const uint16_t*>(sf + k / kBlock);
-    } else {
-      d.w[0] = d.w[1] = d.w[2] = d.w[3] = d.sf = 0;
-    }
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(d.w[0]), "=r"(d.w[1]), "=r"(d.w[2]), "=r"(d.w[3]) : "l"(w));
+    d.sf = *reinterpret_cast<const uint16_t*>(sf);
   } else {
-    d.w[0] = d.w[1] = d.w[2] = d.w[3] = d.sf = 0;
-    if (k < K) {
-      const uint2 a = *reinterpret_cast<const uint2*>(w + k / 2);
-      d.w[0] = a.x, d.w[1] = a.y;
-      d.sf = sf[k / kBlock];
-    }
-    if (k + kBlock < K) {
-      const uint2 a = *reinterpret_cast<const uint2*>(w + k / 2 + 8);
-      d.w[2] = a.x, d.w[3] = a.y;
-      d.sf |= static_cast<uint32_t>(sf[k / kBlock + 1]) << 8;
-    }
+    const uint2 a = *reinterpret_cast<const uint2*>(w), b = *reinterpret_cast<const uint2*>(w + 8);
+    d.w[0] = a.x, d.w[1] = a.y, d.w[2] = b.x, d.w[3] = b.y;
+    d.sf = sf[0] | static_cast<uint32_t>(sf[1]) << 8;
+  }
+}
+// A chunk that K ends in: a block past the end repeats the row's last one. Those meet zeros of x, but
+// have to be numbers where the row holds numbers.
+template <bool WIDE>
+__device__ __forceinline__ void load_last_codes(Codes& d, const uint8_t* w, const uint8_t* sf, int k, int K) {
+  if constexpr (WIDE) {
+    k = min(k, K - 32);
+    load_codes<true>(d, w + k / 2, sf + k / kBlock);
+  } else {
+    const int k0 = min(k, K - kBlock), k1 = min(k + kBlock, K - kBlock);
+    const uint2 a = *reinterpret_cast<const uint2*>(w + k0 / 2), b = *reinterpret_cast<const uint2*>(w + k1 / 2);
+    d.w[0] = a.x, d.w[1] = a.y, d.w[2] = b.x, d.w[3] = b.y;
+    d.sf = sf[k0 / kBlock] | static_cast<uint32_t>(sf[k1 / kBlock]) << 8;
   }
 }
 
 // NT: groups of eight tokens
 template <int NT, bool WIDE>
-__global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(LinArgs a) {
+__global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+  const int tid = threadIdx.x, threads = 32 * a.warps, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   const int rank = blockIdx.x % a.slices;
   if (a.slices > 1) cluster_arrive();  // this block has started: its shared memory may be written
   const int m0 = blockIdx.y * a.tokens, M = min(a.M - m0, a.tokens);
   const int chunk0 = rank * a.slice;
   const int chunks = max(0, min(a.slice, (a.K + kLinChunk - 1) / kLinChunk - chunk0));
-  const int steps = (chunks + kLinAhead - 1) / kLinAhead * kLinAhead;
-  // shared memory: x [M][slice * 256 + 64 bytes], factors [slice][8 * NT], sums (twice) [kLinRows][8 * NT + 1]
+  // shared memory: x [M][slice * 256 + 64 bytes], factors [slice][8 * NT], sums (twice) [16 * warps][8 * NT + 1]
   const int x_row = a.slice * (kLinChunk * 2) + 64;
   float* const factor = reinterpret_cast<float*>(smem + M * x_row);
   constexpr int kSumRow = 8 * NT + 1;
   float* sums = factor + a.slice * 8 * NT;
-  float* sums_next = sums + kLinRows * kSumRow;
+  float* sums_next = sums + 16 * a.warps * kSumRow;
 
   // A row block is n_per output columns: their rows of w, or for the gated kinds their gate rows
   // (first half of the warps) and up rows (second half)
-  const int n_per = a.gated ? kLinRows / 2 : kLinRows;
-  const bool up = a.gated && warp >= kLinWarps / 2;
-  const int i0 = (up ? warp - kLinWarps / 2 : warp) * 16 + r;
+  const int n_per = a.gated ? 8 * a.warps : 16 * a.warps;
+  const bool up = a.gated && warp >= a.warps / 2;
+  const int i0 = (up ? warp - a.warps / 2 : warp) * 16 + r;
   const int blocks = (a.n_out + n_per - 1) / n_per, stride = gridDim.x / a.slices;
   int block = blockIdx.x / a.slices;
-  const int k_lane = chunk0 * kLinChunk + 32 * c, k_end = min(a.K, (chunk0 + chunks) * kLinChunk);
   const uint8_t *w[2], *sf[2];
   auto rows_of = [&](int b) {
 #pragma unroll
@@ -143,22 +143,32 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(LinArgs a) {
       sf[h] = a.sf + n * (a.K / kBlock);
     }
   };
-  rows_of(block);
   Codes buf[kLinAhead][2];
+  // chunks ch to ch + kLinAhead - 1 of the slice; those past its end stay what they were
+  auto load_step = [&](int u, int ch) {
+    const int k = (chunk0 + ch) * kLinChunk + 32 * c;
+    if ((chunk0 + ch + u + 1) * kLinChunk <= a.K && ch + u < chunks) {
 #pragma unroll
-  for (int u = 0; u < kLinAhead; ++u)
+      for (int h = 0; h < 2; ++h)
+        load_codes<WIDE>(buf[u][h], w[h] + k / 2 + u * (kLinChunk / 2), sf[h] + k / kBlock + u * (kLinChunk / kBlock));
+    } else if (ch + u < chunks) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) load_codes<WIDE>(buf[u][h], w[h], sf[h], k_lane + u * kLinChunk, k_end);
+      for (int h = 0; h < 2; ++h) load_last_codes<WIDE>(buf[u][h], w[h], sf[h], k + u * kLinChunk, a.K);
+    }
+  };
+  rows_of(block);
+#pragma unroll
+  for (int u = 0; u < kLinAhead; ++u) load_step(u, 0);
 
   // x: half a warp per (token, chunk), eight values a lane, four loads in flight
-  constexpr int kPairs = kLinThreads / 16;
-  for (int i = tid >> 4; i < M * chunks; i += 4 * kPairs) {
+  const int pairs = threads / 16;
+  for (int i = tid >> 4; i < M * chunks; i += 4 * pairs) {
     const int piece = tid & 15;
     uint4 raw[4];
     float scale[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int m = (i + u * kPairs) / chunks, ch = i + u * kPairs - m * chunks;
+      const int m = (i + u * pairs) / chunks, ch = i + u * pairs - m * chunks;
       const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
       raw[u] = make_uint4(0, 0, 0, 0);
       if (m >= M) continue;
@@ -174,7 +184,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(LinArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int m = (i + u * kPairs) / chunks, ch = i + u * kPairs - m * chunks;
+      const int m = (i + u * pairs) / chunks, ch = i + u * pairs - m * chunks;
       if (m >= M) break;
       const uint32_t v[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
       uint4 f;
@@ -199,57 +209,60 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(LinArgs a) {
       if (piece == 0) factor[ch * 8 * NT + m] = scale[u];
     }
   }
-  for (int i = tid; i < chunks * 8 * NT; i += kLinThreads)
-    if (i % (8 * NT) >= M) factor[i] = 0.0f;  // columns of no token
   __syncthreads();
 
   const int share = n_per / a.slices, kinds = a.gated ? 2 : 1;
   const float alpha = *a.alpha;
   if (a.slices > 1) cluster_wait();
+  const uint8_t* x_lane[NT];  // columns of no token repeat the last one and are dropped
+#pragma unroll
+  for (int t = 0; t < NT; ++t) x_lane[t] = smem + min(8 * t + r, M - 1) * x_row + c * 16;
   for (; block < blocks; block += stride) {
     float acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-    for (int ch0 = 0; ch0 < steps; ch0 += kLinAhead) {
+    for (int ch0 = 0; ch0 < chunks; ch0 += kLinAhead) {
       // what is loaded while this step's chunks are computed: the row block's next, or the next block's first
-      const bool last = ch0 + kLinAhead >= steps;
-      const int k_next = last ? k_lane : k_lane + (ch0 + kLinAhead) * kLinChunk;
-      const int k_stop = last && block + stride >= blocks ? 0 : k_end;
+      const bool last = ch0 + kLinAhead >= chunks;
+      const bool more = !last || block + stride < blocks;
+      const int next = last ? 0 : ch0 + kLinAhead;
       if (last) rows_of(block + stride);
 #pragma unroll
       for (int u = 0; u < kLinAhead; ++u) {
         const int ch = ch0 + u;
-        uint32_t f[2][4][4];  // [row half][word][byte]
+        if (ch < chunks) {
+          float part[NT][4];
+          const uint32_t two[2] = {e4m3x2_to_f16x2(buf[u][0].sf), e4m3x2_to_f16x2(buf[u][1].sf)};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t two = e4m3x2_to_f16x2(buf[u][h].sf);
-          const uint32_t s[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+          for (int j = 0; j < 4; ++j) {  // a word of either row: two MMA steps
+            uint32_t f[2][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            e2m1x8_to_f16x2(buf[u][h].w[j], f[h][j]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t s = __byte_perm(two[h], two[h], j < 2 ? 0x1010 : 0x3232);
+              e2m1x8_to_f16x2(buf[u][h].w[j], f[h]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[h][j][i] = mul_f16x2(f[h][j][i], s[j / 2]);
-          }
-          load_codes<WIDE>(buf[u][h], w[h], sf[h], k_next + u * kLinChunk, k_stop);
-        }
-        if (ch >= chunks) continue;
+              for (int i = 0; i < 4; ++i) f[h][i] = mul_f16x2(f[h][i], s);
+            }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int t = 0; t < NT; ++t) {
+              const uint4 x = *reinterpret_cast<const uint4*>(x_lane[t] + ch * 256 + j * 64);
+              const uint32_t b[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (8 * t + r < M) x = *reinterpret_cast<const uint4*>(smem + (8 * t + r) * x_row + ch * 256 + (4 * j + c) * 16);
-            const uint32_t b[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t A[4] = {f[0][j][2 * i], f[1][j][2 * i], f[0][j][2 * i + 1], f[1][j][2 * i + 1]};
-              mma_f16(part, A, b + 2 * i);
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t A[4] = {f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1]};
+                if (j == 0 && i == 0) mma_f16_first(part[t], A, b);
+                else mma_f16(part[t], A, b + 2 * i);
+              }
             }
           }
-          const float2 s = *reinterpret_cast<const float2*>(factor + (ch * NT + t) * 8 + 2 * c);
-          acc[t][0] += part[0] * s.x, acc[t][1] += part[1] * s.y, acc[t][2] += part[2] * s.x, acc[t][3] += part[3] * s.y;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float2 s = *reinterpret_cast<const float2*>(factor + (ch * NT + t) * 8 + 2 * c);
+            acc[t][0] += part[t][0] * s.x, acc[t][1] += part[t][1] * s.y;
+            acc[t][2] += part[t][2] * s.x, acc[t][3] += part[t][3] * s.y;
+          }
         }
+        if (more) load_step(u, next);
       }
     }
 
@@ -268,7 +281,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(LinArgs a) {
     }
     if (a.slices > 1) cluster_arrive(), cluster_wait();
     else __syncthreads();
-    for (int i = tid; i < share * M; i += kLinThreads) {
+    for (int i = tid; i < share * M; i += threads) {
       const int m = i / share, col = i - m * share;
       const int64_t n = static_cast<int64_t>(block) * n_per + rank * share + col;
       if (n >= a.n_out) continue;
@@ -291,7 +304,7 @@ template <int NT, bool WIDE>
 moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kLinThreads);
+  cfg.blockDim = dim3(32 * a.warps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -310,10 +323,10 @@ moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_
 
 constexpr size_t kLinSmem = 100 * 1024, kLinSmemMost = 227 * 1024;  // two blocks per SM; the most of one
 
-size_t linear_smem(int tokens, int slice) {
+size_t linear_smem(int tokens, int slice, int warps) {
   const int columns = tokens > 8 ? 16 : 8;
   return static_cast<size_t>(tokens) * (slice * kLinChunk * 2 + 64) + static_cast<size_t>(slice) * columns * 4 +
-         2 * static_cast<size_t>(kLinRows) * (columns + 1) * 4;
+         2 * static_cast<size_t>(16 * warps) * (columns + 1) * 4;
 }
 
 }  // namespace
@@ -339,34 +352,40 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
             MOE_ERR_MISALIGNED);
   const int chunks = (K + kLinChunk - 1) / kLinChunk;
   LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, gated ? N / 2 : N, activation,
-               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, gated};
+               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, kLinWarps, gated};
   const size_t ob = static_cast<size_t>(M) * a.n_out * 2;
   MOE_CHECK(!overlaps(out, ob, x, (static_cast<size_t>(M - 1) * ld_x + K) * (fp8 ? 1 : 2)) &&
                 !overlaps(out, ob, w, static_cast<size_t>(N) * K / 2) &&
                 !overlaps(out, ob, w_sf, static_cast<size_t>(N) * K / kBlock) && !overlaps(out, ob, alpha, 4) &&
                 !overlaps(out, ob, x_scale, static_cast<size_t>(M) * a.x_groups * 4),
             MOE_ERR_OVERLAP);
-  // Slices of K: as long as all blocks run at once, two to an SM, and as x's share of shared memory asks for.
-  const int n_per = gated ? kLinRows / 2 : kLinRows;
-  const int64_t blocks = (static_cast<int64_t>(a.n_out) + n_per - 1) / n_per;
-  auto cut = [&](int most) {  // blocks of at most `most` tokens
+  // Slices of K (a cluster barrier each row block) while a warp keeps the chunks that it has in flight
+  // anyway and all blocks run at once, two to an SM; more where x's share of shared memory asks for it.
+  auto blocks = [&] {
+    const int64_t n_per = gated ? 8 * a.warps : 16 * a.warps;
+    return (a.n_out + n_per - 1) / n_per;
+  };
+  auto cut = [&](int most) {  // for blocks of at most `most` tokens
     a.tokens = M < most ? M : most;
     a.slices = 1, a.slice = chunks;
     const int64_t groups = (static_cast<int64_t>(M) + a.tokens - 1) / a.tokens;
     while (a.slices < 8 && a.slices < chunks &&
-           (blocks * groups * a.slices <= num_sms() || linear_smem(a.tokens, a.slice) > kLinSmem)) {
+           ((a.slice > kLinAhead && blocks() * groups * a.slices <= num_sms()) ||
+            linear_smem(a.tokens, a.slice, a.warps) > kLinSmem)) {
       a.slices *= 2;
       a.slice = (chunks + a.slices - 1) / a.slices;
     }
     return groups;
   };
   int64_t groups = cut(kLinTokens);
-  if (linear_smem(a.tokens, a.slice) > kLinSmemMost) groups = cut(8);  // the longest K
-  const size_t smem = linear_smem(a.tokens, a.slice);
+  if (linear_smem(a.tokens, a.slice, a.warps) > kLinSmemMost) groups = cut(8);  // the longest K
+  // smaller blocks where whole ones leave SMs idle
+  while (a.warps > 2 && blocks() * groups * a.slices < num_sms()) a.warps /= 2;
+  const size_t smem = linear_smem(a.tokens, a.slice, a.warps);
   MOE_CHECK(groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
   // two blocks per SM; they take row blocks in turn
   const int64_t at_once = 2 * num_sms() / a.slices;
-  const dim3 grid(static_cast<unsigned>((blocks < at_once ? blocks : at_once) * a.slices), static_cast<unsigned>(groups));
+  const dim3 grid(static_cast<unsigned>((blocks() < at_once ? blocks() : at_once) * a.slices), static_cast<unsigned>(groups));
   const bool wide = K % 32 == 0;
   cudaStream_t s = as_stream(stream);
   if (a.tokens <= 8) return wide ? launch_linear<1, true>(a, grid, smem, s) : launch_linear<1, false>(a, grid, smem, s);
