@@ -1,21 +1,27 @@
 // A few tokens times one dense NVFP4 matrix: y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]).
 //
-// Bound by HBM: 9/16 byte per weight, read once per 16 tokens. A block of warps takes 16 rows
-// of w each and a slice of K: mma.m16n8k16 with the 16 weight rows as one operand
-// and eight tokens as the other. Per 128 values of K (a chunk) lane (r, c) = (lane / 4, lane % 4)
-// reads bytes [16c, 16c + 16) of rows r and r + 8 and their two scales each, kLinAhead chunks
-// ahead in registers; MMA step j of the chunk takes its values 32c + 4j to 32c + 4j + 3.
+// Bound by HBM: 9/16 byte per weight, read once per 16 tokens. A warp takes 16 rows of w and a run
+// of K: mma.m16n8k16 with the 16 weight rows as one operand and eight tokens as the other. K
+// goes by chunks of 128 values. In a chunk lane (r, c) = (lane / 4, lane % 4) holds the values 32c
+// to 32c + 31 of rows r and r + 8, and MMA step j takes its values 32c + 4j to 32c + 4j + 3.
+//
+// The codes come through a ring in shared memory that belongs to the warp (cp.async; two chunks a
+// stage, kLinStages of them): copied as 128 contiguous bytes per row, a quarter of the L1 lines
+// that fetching them in fragment order would touch, and swizzled so that reading them in that
+// order meets no bank twice.
 //
 // The block first lays its slice of x out in shared memory as FP16 in fragment order. Each
 // (token, chunk) has an FP32 factor: the tokens' own scales for E4M3 (exact in FP16), a power of two
 // that brings the chunk's values into FP16's range for BF16. A chunk is summed on its own and
 // enters the FP32 sum times its factor.
 //
-// Blocks that share rows (slices of K) form a cluster. A row belongs to one of them: the others
-// store their sums into its shared memory, and after one cluster barrier it adds them in rank
-// order, so results do not depend on timing. alpha, the activation and the BF16 rounding come
-// once at the end. A block goes on to further rows while there are any, its first chunks of them
-// already in flight.
+// Two ways of sharing K. Warps of one block (`across` of them) take neighbouring runs of the same
+// rows, so that a block reads whole rows: DRAM gives 128 rows at a time read along K 4.8 TB/s, whole
+// rows 5.9 (302 MB, read alone). Blocks of a cluster take slices of K where there are too few
+// rows for the SMs, or too much x for shared memory. A row's sums belong to one block: the
+// others store theirs into its shared memory, and after one barrier it adds all in a fixed order, so
+// results do not depend on timing. alpha, the activation and the BF16 rounding come once at the
+// end. A block goes on to further rows while there are any, their first chunks already in flight.
 #include "common.cuh"
 #include "fp4_mma.cuh"
 #include "host_util.h"
@@ -26,7 +32,7 @@ namespace {
 constexpr int kLinWarps = 8;              // most warps of a block, 16 rows of w each
 constexpr int kLinTokens = 16;
 constexpr int kLinChunk = 128;            // = MOE_FP8_GROUP
-constexpr int kLinAhead = 4;
+constexpr int kLinStages = 3, kLinStage = 16 * 128 + 16 * 20;  // of two chunks: codes, scales
 static_assert(kLinChunk == MOE_FP8_GROUP, "one E4M3 scale per chunk");
 
 struct LinArgs {
@@ -40,7 +46,7 @@ struct LinArgs {
   int x_mode, M, K, n_out, act, x_groups;  // n_out: columns of out
   int slices, slice;                       // blocks of a cluster, chunks of each
   int tokens;                              // tokens of a block
-  int warps;                               // of a block; gated: half gate, half up rows
+  int warps, across;                       // warps of a block, and how many of them share rows
   bool gated;
 };
 
@@ -73,42 +79,25 @@ __device__ __forceinline__ void store_cluster_f32(float* p, uint32_t rank, float
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// 32 codes (16 bytes) of a row at byte `at`, and their two scales
-struct Codes {
-  uint32_t w[4], sf;
-};
+// N bytes of global memory into shared memory, asynchronously; fewer `bytes` leave zeros behind them
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, uint32_t bytes = N) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-// One chunk's share of a lane: w and sf point at it. WIDE: rows are multiples of 16 bytes, otherwise
-// of 8 (a lane's two blocks are loaded one by one).
-template <bool WIDE>
-__device__ __forceinline__ void load_codes(Codes& d, const uint8_t* w, const uint8_t* sf) {
-  if constexpr (WIDE) {
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(d.w[0]), "=r"(d.w[1]), "=r"(d.w[2]), "=r"(d.w[3]) : "l"(w));
-    d.sf = *reinterpret_cast<const uint16_t*>(sf);
-  } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(w), b = *reinterpret_cast<const uint2*>(w + 8);
-    d.w[0] = a.x, d.w[1] = a.y, d.w[2] = b.x, d.w[3] = b.y;
-    d.sf = sf[0] | static_cast<uint32_t>(sf[1]) << 8;
-  }
-}
-// A chunk that K ends in: a block past the end repeats the row's last one. Those meet zeros of x, but
-// have to be numbers where the row holds numbers.
-template <bool WIDE>
-__device__ __forceinline__ void load_last_codes(Codes& d, const uint8_t* w, const uint8_t* sf, int k, int K) {
-  if constexpr (WIDE) {
-    k = min(k, K - 32);
-    load_codes<true>(d, w + k / 2, sf + k / kBlock);
-  } else {
-    const int k0 = min(k, K - kBlock), k1 = min(k + kBlock, K - kBlock);
-    const uint2 a = *reinterpret_cast<const uint2*>(w + k0 / 2), b = *reinterpret_cast<const uint2*>(w + k1 / 2);
-    d.w[0] = a.x, d.w[1] = a.y, d.w[2] = b.x, d.w[3] = b.y;
-    d.sf = sf[k0 / kBlock] | static_cast<uint32_t>(sf[k1 / kBlock]) << 8;
-  }
-}
+// How rows of codes and of scales are aligned: K % 256 == 0, K % 32 == 0, or only K % 16 == 0
+enum Align : int { kAlign256, kAlign32, kAlign16 };
 
 // NT: groups of eight tokens
-template <int NT, bool WIDE>
+template <int NT, int ALIGN>
 __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
@@ -119,46 +108,95 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
   const int m0 = blockIdx.y * a.tokens, M = min(a.M - m0, a.tokens);
   const int chunk0 = rank * a.slice;
   const int chunks = max(0, min(a.slice, (a.K + kLinChunk - 1) / kLinChunk - chunk0));
-  // shared memory: x [M][slice * 256 + 64 bytes], factors [slice][8 * NT], sums (twice) [16 * warps][8 * NT + 1]
+  // shared memory: rings [warps][kLinStages * kLinStage], x [M][slice * 256 + 64 bytes],
+  // factors [slice][8 * NT], sums (twice) [16 * warps][8 * NT + 1]
+  uint8_t* const xs = smem + a.warps * (kLinStages * kLinStage);
   const int x_row = a.slice * (kLinChunk * 2) + 64;
-  float* const factor = reinterpret_cast<float*>(smem + M * x_row);
+  float* const factor = reinterpret_cast<float*>(xs + M * x_row);
   constexpr int kSumRow = 8 * NT + 1;
   float* sums = factor + a.slice * 8 * NT;
   float* sums_next = sums + 16 * a.warps * kSumRow;
 
   // A row block is n_per output columns: their rows of w, or for the gated kinds their gate rows
-  // (first half of the warps) and up rows (second half)
-  const int n_per = a.gated ? 8 * a.warps : 16 * a.warps;
-  const bool up = a.gated && warp >= a.warps / 2;
-  const int i0 = (up ? warp - a.warps / 2 : warp) * 16 + r;
+  // (first half of the row tiles) and up rows (second half). Warp (tile, part) takes 16 of the rows
+  // and the chunks [first, last) of the slice.
+  const int tiles = a.warps / a.across, tile = warp / a.across, part = warp - tile * a.across;
+  const int n_per = a.gated ? 8 * tiles : 16 * tiles;
+  const bool up = a.gated && tile >= tiles / 2;
+  const int i0 = (up ? tile - tiles / 2 : tile) * 16;
   const int blocks = (a.n_out + n_per - 1) / n_per, stride = gridDim.x / a.slices;
-  int block = blockIdx.x / a.slices;
-  const uint8_t *w[2], *sf[2];
-  auto rows_of = [&](int b) {
+  const int run = ((chunks + a.across - 1) / a.across + 1) & ~1;  // whole stages
+  const int first = min(part * run, chunks), last = min(first + run, chunks);
+
+  // ---- the ring. Lane (q, p) = (lane / 8, lane % 8) copies piece p (16 bytes) of rows q, q + 4, ...
+  const uint32_t ring = smem_u32(smem) + warp * (kLinStages * kLinStage);
+  const uint8_t* const ring_at = smem + warp * (kLinStages * kLinStage);
+  const int q = lane >> 3, p = lane & 7;
+  const uint32_t to = q * 128 + ((p ^ (q & 1) << 2) << 4);
+  const int sf_ld = a.K / kBlock;
+  const uint8_t *w_from, *sf_from;  // this lane's first piece of codes, and of scales, of the next stage
+  int load_block = blockIdx.x / a.slices, load_ch = first, load_rows;
+  auto rows_of = [&] {
+    const int64_t n = static_cast<int64_t>(load_block) * n_per + i0;
+    load_rows = load_block < blocks ? static_cast<int>(min(static_cast<int64_t>(a.n_out) - n, int64_t(16))) : 0;
+    const int64_t row = n + (up ? a.n_out : 0);
+    w_from = a.w + (row + q) * (a.K / 2) + (chunk0 + first) * (kLinChunk / 2) + 16 * p;
+    sf_from = a.sf + (row + (ALIGN == kAlign256 ? lane : q)) * sf_ld + (chunk0 + first) * (kLinChunk / kBlock);
+  };
+  const uint8_t* const sf_end = a.sf + static_cast<int64_t>(a.gated ? 2 : 1) * a.n_out * sf_ld;
+  auto load_stage = [&](int stage) {
+    const uint32_t at = ring + stage * kLinStage;
+    if (load_ch < last && load_rows > 0) {
+      const int k = (chunk0 + load_ch) * kLinChunk;
+      const bool whole = load_rows == 16 && load_ch + 2 <= last && k + 2 * kLinChunk <= a.K;
+      if (whole) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      int64_t n = min(static_cast<int64_t>(b) * n_per + i0 + 8 * h, static_cast<int64_t>(a.n_out) - 1);  // spare rows are dropped
-      if (up) n += a.n_out;
-      w[h] = a.w + n * (a.K / 2);
-      sf[h] = a.sf + n * (a.K / kBlock);
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (ALIGN != kAlign16) {
+            copy_async<16>(at + to + i * 512, w_from + i * 2 * a.K);
+          } else {
+            copy_async<8>(at + to + i * 512, w_from + i * 2 * a.K);
+            copy_async<8>(at + to + i * 512 + 8, w_from + i * 2 * a.K + 8);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // rows past the matrix, pieces past K: zeros
+          const bool row = q + 4 * i < load_rows && (p < 4 || load_ch + 1 < last);
+          const bool in0 = row && k + 32 * p < a.K, in1 = row && k + 32 * p + kBlock < a.K;
+          const uint8_t* const from = w_from + i * 2 * static_cast<int64_t>(a.K);
+          if constexpr (ALIGN != kAlign16) {
+            copy_async<16>(at + to + i * 512, in0 ? from : a.w, in0 ? 16 : 0);
+          } else {
+            copy_async<8>(at + to + i * 512, in0 ? from : a.w, in0 ? 8 : 0);
+            copy_async<8>(at + to + i * 512 + 8, in1 ? from + 8 : a.w, in1 ? 8 : 0);
+          }
+        }
+      }
+      if constexpr (ALIGN == kAlign256) {  // one row's 16 scales a lane
+        if (lane < 16) copy_async<16>(at + 2048 + lane * 16, lane < load_rows ? sf_from : a.sf, lane < load_rows ? 16 : 0);
+      } else {  // the (up to five) words that hold a row's 16 scales, four rows at a time
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* const s = sf_from + 4 * i * static_cast<int64_t>(sf_ld);
+          const uint8_t* const from = s - (reinterpret_cast<uintptr_t>(s) & 3) + 4 * p;
+          const bool in = q + 4 * i < load_rows && from < sf_end;
+          const int left = in ? static_cast<int>(min(sf_end - from, static_cast<ptrdiff_t>(4))) : 0;
+          if (p < 5) copy_async<4>(at + 2048 + (q + 4 * i) * 20 + 4 * p, in ? from : a.sf, left);
+        }
+      }
+    }
+    copies_commit();
+    load_ch += 2;
+    w_from += kLinChunk, sf_from += 2 * kLinChunk / kBlock;
+    if (load_ch >= last) {
+      load_ch = first, load_block += stride;
+      rows_of();
     }
   };
-  Codes buf[kLinAhead][2];
-  // chunks ch to ch + kLinAhead - 1 of the slice; those past its end stay what they were
-  auto load_step = [&](int u, int ch) {
-    const int k = (chunk0 + ch) * kLinChunk + 32 * c;
-    if ((chunk0 + ch + u + 1) * kLinChunk <= a.K && ch + u < chunks) {
+  rows_of();
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        load_codes<WIDE>(buf[u][h], w[h] + k / 2 + u * (kLinChunk / 2), sf[h] + k / kBlock + u * (kLinChunk / kBlock));
-    } else if (ch + u < chunks) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) load_last_codes<WIDE>(buf[u][h], w[h], sf[h], k + u * kLinChunk, a.K);
-    }
-  };
-  rows_of(block);
-#pragma unroll
-  for (int u = 0; u < kLinAhead; ++u) load_step(u, 0);
+  for (int u = 0; u < kLinStages - 1; ++u) load_stage(u);
 
   // x: half a warp per (token, chunk), eight values a lane, four loads in flight
   const int pairs = threads / 16;
@@ -205,78 +243,99 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
                        e4m3x2_to_f16x2(v[1] >> 16));
       }
       // piece p is half of lane column p / 4's share: its steps 2 * (p % 4) and the next
-      *reinterpret_cast<uint4*>(smem + m * x_row + ch * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16) = f;
+      *reinterpret_cast<uint4*>(xs + m * x_row + ch * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16) = f;
       if (piece == 0) factor[ch * 8 * NT + m] = scale[u];
     }
   }
   __syncthreads();
 
-  const int share = n_per / a.slices, kinds = a.gated ? 2 : 1;
+  const int share = n_per / a.slices, kinds = a.gated ? 2 : 1, parts = a.slices * a.across;
   const float alpha = *a.alpha;
   if (a.slices > 1) cluster_wait();
   const uint8_t* x_lane[NT];  // columns of no token repeat the last one and are dropped
 #pragma unroll
-  for (int t = 0; t < NT; ++t) x_lane[t] = smem + min(8 * t + r, M - 1) * x_row + c * 16;
-  for (; block < blocks; block += stride) {
+  for (int t = 0; t < NT; ++t) x_lane[t] = xs + min(8 * t + r, M - 1) * x_row + c * 16;
+  int stage = 0;
+  for (int block = blockIdx.x / a.slices; block < blocks; block += stride) {
     float acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-    for (int ch0 = 0; ch0 < chunks; ch0 += kLinAhead) {
-      // what is loaded while this step's chunks are computed: the row block's next, or the next block's first
-      const bool last = ch0 + kLinAhead >= chunks;
-      const bool more = !last || block + stride < blocks;
-      const int next = last ? 0 : ch0 + kLinAhead;
-      if (last) rows_of(block + stride);
+    uint32_t shift[2] = {0, 0};  // of a row's scales in their first word
+    if constexpr (ALIGN != kAlign256) {
+      const int64_t row = static_cast<int64_t>(block) * n_per + i0 + (up ? a.n_out : 0) + r;
+      shift[0] = (row * sf_ld) & 3, shift[1] = ((row + 8) * sf_ld) & 3;
+    }
+    for (int ch0 = first; ch0 < last; ch0 += 2) {
+      copies_wait<kLinStages - 2>();
+      __syncwarp();  // every lane's copies of this stage are there, and the stage before it has been read
+      load_stage(stage == 0 ? kLinStages - 1 : stage - 1);
+      const uint8_t* const at = ring_at + stage * kLinStage;
 #pragma unroll
-      for (int u = 0; u < kLinAhead; ++u) {
+      for (int u = 0; u < 2; ++u) {
         const int ch = ch0 + u;
-        if (ch < chunks) {
-          float part[NT][4];
-          const uint32_t two[2] = {e4m3x2_to_f16x2(buf[u][0].sf), e4m3x2_to_f16x2(buf[u][1].sf)};
+        if (u == 1 && ch >= last) break;
+        uint32_t codes[2][4], two[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // a word of either row: two MMA steps
-            uint32_t f[2][4];
+        for (int h = 0; h < 2; ++h) {
+          const int row = r + 8 * h;
+          const uint4 x = *reinterpret_cast<const uint4*>(at + row * 128 + ((4 * u + c) ^ (r & 1) << 2) * 16);
+          codes[h][0] = x.x, codes[h][1] = x.y, codes[h][2] = x.z, codes[h][3] = x.w;
+          if constexpr (ALIGN == kAlign256) {
+            two[h] = *reinterpret_cast<const uint16_t*>(at + 2048 + row * 16 + 8 * u + 2 * c);
+          } else {
+            const uint8_t* const s = at + 2048 + row * 20 + shift[h] + 8 * u + 2 * c;
+            two[h] = s[0] | static_cast<uint32_t>(s[1]) << 8;
+            // past K lie the next row's scales, which may be no numbers
+            const int k = (chunk0 + ch) * kLinChunk + 32 * c;
+            if (k + 32 > a.K) two[h] = k < a.K ? two[h] & 0xFF : 0;
+          }
+          two[h] = e4m3x2_to_f16x2(two[h]);
+        }
+        float sum[NT][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t s = __byte_perm(two[h], two[h], j < 2 ? 0x1010 : 0x3232);
-              e2m1x8_to_f16x2(buf[u][h].w[j], f[h]);
+        for (int j = 0; j < 4; ++j) {  // a word of either row: two MMA steps
+          uint32_t f[2][4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) f[h][i] = mul_f16x2(f[h][i], s);
-            }
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t s = __byte_perm(two[h], two[h], j < 2 ? 0x1010 : 0x3232);
+            e2m1x8_to_f16x2(codes[h][j], f[h]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint4 x = *reinterpret_cast<const uint4*>(x_lane[t] + ch * 256 + j * 64);
-              const uint32_t b[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t A[4] = {f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1]};
-                if (j == 0 && i == 0) mma_f16_first(part[t], A, b);
-                else mma_f16(part[t], A, b + 2 * i);
-              }
-            }
+            for (int i = 0; i < 4; ++i) f[h][i] = mul_f16x2(f[h][i], s);
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const float2 s = *reinterpret_cast<const float2*>(factor + (ch * NT + t) * 8 + 2 * c);
-            acc[t][0] += part[t][0] * s.x, acc[t][1] += part[t][1] * s.y;
-            acc[t][2] += part[t][2] * s.x, acc[t][3] += part[t][3] * s.y;
+            const uint4 x = *reinterpret_cast<const uint4*>(x_lane[t] + ch * 256 + j * 64);
+            const uint32_t b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t A[4] = {f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1]};
+              if (j == 0 && i == 0) mma_f16_first(sum[t], A, b);
+              else mma_f16(sum[t], A, b + 2 * i);
+            }
           }
         }
-        if (more) load_step(u, next);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float2 s = *reinterpret_cast<const float2*>(factor + (ch * NT + t) * 8 + 2 * c);
+          acc[t][0] += sum[t][0] * s.x, acc[t][1] += sum[t][1] * s.y;
+          acc[t][2] += sum[t][2] * s.x, acc[t][3] += sum[t][3] * s.y;
+        }
       }
+      if (++stage == kLinStages) stage = 0;
     }
 
-    // sums [rank][kind][column of the owner's share][token], in the owner's shared memory
+    // sums [part of K][kind][column of the owner's share][token], in the owner's shared memory
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int owner = (i0 + 8 * h) / share;
-      float* const to = sums + ((rank * kinds + (up ? 1 : 0)) * share + i0 + 8 * h - owner * share) * kSumRow + 2 * c;
+      const int col = i0 + r + 8 * h, owner = col / share;
+      float* const to_sum =
+          sums + (((rank * a.across + part) * kinds + (up ? 1 : 0)) * share + col - owner * share) * kSumRow + 2 * c;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (a.slices > 1) store_cluster_f32(to + 8 * t + i, owner, acc[t][2 * h + i]);
-          else to[8 * t + i] = acc[t][2 * h + i];
+          if (a.slices > 1) store_cluster_f32(to_sum + 8 * t + i, owner, acc[t][2 * h + i]);
+          else to_sum[8 * t + i] = acc[t][2 * h + i];
         }
     }
     if (a.slices > 1) cluster_arrive(), cluster_wait();
@@ -286,7 +345,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
       const int64_t n = static_cast<int64_t>(block) * n_per + rank * share + col;
       if (n >= a.n_out) continue;
       float y[2] = {0.0f, 0.0f};
-      for (int s = 0; s < a.slices; ++s) {
+      for (int s = 0; s < parts; ++s) {
         y[0] += sums[(s * kinds * share + col) * kSumRow + m];
         if (a.gated) y[1] += sums[((s * 2 + 1) * share + col) * kSumRow + m];
       }
@@ -300,7 +359,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
   }
 }
 
-template <int NT, bool WIDE>
+template <int NT, int ALIGN>
 moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -317,16 +376,17 @@ moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (smem > 48 * 1024)
-    MOE_CUDA(cudaFuncSetAttribute(linear_kernel<NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
-  return cudaLaunchKernelEx(&cfg, linear_kernel<NT, WIDE>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    MOE_CUDA(cudaFuncSetAttribute(linear_kernel<NT, ALIGN>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+  return cudaLaunchKernelEx(&cfg, linear_kernel<NT, ALIGN>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-constexpr size_t kLinSmem = 100 * 1024, kLinSmemMost = 227 * 1024;  // two blocks per SM; the most of one
+// shared memory of a block: two to an SM; the most of one; an SM's, 1 KB of it taken by each block
+constexpr size_t kLinSmem = 113 * 1024, kLinSmemMost = 227 * 1024, kLinSmemSm = 228 * 1024;
 
 size_t linear_smem(int tokens, int slice, int warps) {
   const int columns = tokens > 8 ? 16 : 8;
   return static_cast<size_t>(tokens) * (slice * kLinChunk * 2 + 64) + static_cast<size_t>(slice) * columns * 4 +
-         2 * static_cast<size_t>(16 * warps) * (columns + 1) * 4;
+         2 * static_cast<size_t>(16 * warps) * (columns + 1) * 4 + static_cast<size_t>(warps) * kLinStages * kLinStage;
 }
 
 }  // namespace
@@ -352,42 +412,48 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
             MOE_ERR_MISALIGNED);
   const int chunks = (K + kLinChunk - 1) / kLinChunk;
   LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, gated ? N / 2 : N, activation,
-               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, kLinWarps, gated};
+               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, kLinWarps, 1, gated};
   const size_t ob = static_cast<size_t>(M) * a.n_out * 2;
   MOE_CHECK(!overlaps(out, ob, x, (static_cast<size_t>(M - 1) * ld_x + K) * (fp8 ? 1 : 2)) &&
                 !overlaps(out, ob, w, static_cast<size_t>(N) * K / 2) &&
                 !overlaps(out, ob, w_sf, static_cast<size_t>(N) * K / kBlock) && !overlaps(out, ob, alpha, 4) &&
                 !overlaps(out, ob, x_scale, static_cast<size_t>(M) * a.x_groups * 4),
             MOE_ERR_OVERLAP);
-  // Slices of K (a cluster barrier each row block) while a warp keeps the chunks that it has in flight
-  // anyway and all blocks run at once, two to an SM; more where x's share of shared memory asks for it.
+  // Slices of K (a cluster barrier each row block) while a warp keeps two stages to itself and all blocks
+  // run at once, two to an SM; more where x's share of shared memory asks for it.
   auto blocks = [&] {
-    const int64_t n_per = gated ? 8 * a.warps : 16 * a.warps;
+    const int64_t n_per = (gated ? 8 : 16) * (a.warps / a.across);
     return (a.n_out + n_per - 1) / n_per;
   };
   auto cut = [&](int most) {  // for blocks of at most `most` tokens
     a.tokens = M < most ? M : most;
-    a.slices = 1, a.slice = chunks;
+    a.slices = 1, a.slice = (chunks + 1) & ~1;
     const int64_t groups = (static_cast<int64_t>(M) + a.tokens - 1) / a.tokens;
     while (a.slices < 8 && a.slices < chunks &&
-           ((a.slice > kLinAhead && blocks() * groups * a.slices <= num_sms()) ||
+           ((a.slice > 4 && blocks() * groups * a.slices <= num_sms()) ||
             linear_smem(a.tokens, a.slice, a.warps) > kLinSmem)) {
       a.slices *= 2;
-      a.slice = (chunks + a.slices - 1) / a.slices;
+      a.slice = ((chunks + a.slices - 1) / a.slices + 1) & ~1;  // whole stages
     }
     return groups;
   };
   int64_t groups = cut(kLinTokens);
   if (linear_smem(a.tokens, a.slice, a.warps) > kLinSmemMost) groups = cut(8);  // the longest K
-  // smaller blocks where whole ones leave SMs idle
+  // whole rows where there are rows enough; smaller blocks where whole ones leave SMs idle
+  if (blocks() * groups >= 2 * num_sms() && a.slice >= 8) a.across = 4;
   while (a.warps > 2 && blocks() * groups * a.slices < num_sms()) a.warps /= 2;
   const size_t smem = linear_smem(a.tokens, a.slice, a.warps);
   MOE_CHECK(groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
-  // two blocks per SM; they take row blocks in turn
-  const int64_t at_once = 2 * num_sms() / a.slices;
+  // as many blocks as run at once; they take row blocks in turn
+  const int64_t at_once = (kLinSmemSm / (smem + 1024) < 2 ? 1 : 2) * num_sms() / a.slices;
   const dim3 grid(static_cast<unsigned>((blocks() < at_once ? blocks() : at_once) * a.slices), static_cast<unsigned>(groups));
-  const bool wide = K % 32 == 0;
   cudaStream_t s = as_stream(stream);
-  if (a.tokens <= 8) return wide ? launch_linear<1, true>(a, grid, smem, s) : launch_linear<1, false>(a, grid, smem, s);
-  return wide ? launch_linear<2, true>(a, grid, smem, s) : launch_linear<2, false>(a, grid, smem, s);
+  const int align = K % 256 == 0 ? kAlign256 : K % 32 == 0 ? kAlign32 : kAlign16;
+  if (a.tokens <= 8)
+    return align == kAlign256  ? launch_linear<1, kAlign256>(a, grid, smem, s)
+           : align == kAlign32 ? launch_linear<1, kAlign32>(a, grid, smem, s)
+                               : launch_linear<1, kAlign16>(a, grid, smem, s);
+  return align == kAlign256  ? launch_linear<2, kAlign256>(a, grid, smem, s)
+         : align == kAlign32 ? launch_linear<2, kAlign32>(a, grid, smem, s)
+                             : launch_linear<2, kAlign16>(a, grid, smem, s);
 }
