@@ -11,6 +11,8 @@ import ctypes
 import os
 from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
 
+from torch import _C
+
 from .build import LIB as LIB_PATH
 from .build import TEST_LIB as TEST_LIB_PATH
 
@@ -173,10 +175,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
-    from torch import _C  # the raw handle: a Stream object costs 3 us of host time per call
-    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    if stream is None:  # the raw handle: a Stream object costs 3 us of host time per call
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def make_weights(num_local_experts: int, hidden: int, inter: int, activation: int,
@@ -321,31 +322,42 @@ def moe_finalize(gemm2_out, topk_weights, token_to_row, out, stream=None, routed
                               _stream(stream)), "moe_finalize")
 
 
-def _ld(t, width):
-    """Values between the rows of t (a single row's stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else width
-
-
+# The operators around the experts run for microseconds at decode sizes: their wrappers take plain
+# numbers from the caller where it has them and make one pass over the tensors. A single row's stride
+# says nothing: it counts as contiguous.
 def moe_add_rmsnorm(x, residual, weight, eps, fp8_scale, y, residual_out, y8, y8_scale, stream=None):
     """x [M, H] and residual [M, H] (or None) may have a row stride; the outputs are contiguous."""
     M, H = x.shape
-    _check(lib().moe_add_rmsnorm(_ptr(x), _ld(x, H), _ptr(residual), _ld(residual, H) if residual is not None else 0,
-                                 _ptr(weight), M, H, eps, fp8_scale, _ptr(y), _ptr(residual_out), _ptr(y8),
-                                 _ptr(y8_scale), _stream(stream)), "moe_add_rmsnorm")
+    st = lib().moe_add_rmsnorm(
+        x.data_ptr(), x.stride(0) if M > 1 else H, residual.data_ptr() if residual is not None else None,
+        H if residual is None or M == 1 else residual.stride(0), weight.data_ptr(), M, H, eps, fp8_scale,
+        y.data_ptr() if y is not None else None, residual_out.data_ptr() if residual_out is not None else None,
+        y8.data_ptr() if y8 is not None else None, y8_scale.data_ptr() if y8_scale is not None else None,
+        _stream(stream))
+    if st:
+        _check(st, "moe_add_rmsnorm")
 
 
 def moe_linear_fp4(x, x_scale, x_scale_mode, w, w_sf, alpha, activation, out, stream=None):
     """x [M, K] bf16 or float8_e4m3fn (it may have a row stride); w [N, K/2], w_sf [N, K/16], alpha [1]."""
     M, K = x.shape
-    _check(lib().moe_linear_fp4(_ptr(x), _ld(x, K), _ptr(x_scale), x_scale_mode, M, K, _ptr(w), _ptr(w_sf),
-                                _ptr(alpha), w.shape[0], activation, _ptr(out), _stream(stream)), "moe_linear_fp4")
+    st = lib().moe_linear_fp4(
+        x.data_ptr(), x.stride(0) if M > 1 else K, x_scale.data_ptr() if x_scale is not None else None, x_scale_mode,
+        M, K, w.data_ptr(), w_sf.data_ptr(), alpha.data_ptr(), w.shape[0], activation, out.data_ptr(), _stream(stream))
+    if st:
+        _check(st, "moe_linear_fp4")
 
 
 def moe_kv_append(cache: KVCacheT, k_new, v_new, slots, k_seen, v_seen, dev_status, stream=None):
     """k_new, v_new [N, num_kv_heads, head_dim] bf16 (a token stride is fine), slots [N] int64."""
-    N, n = k_new.shape[0], cache.num_kv_heads * cache.head_dim
-    _check(lib().moe_kv_append(cache, _ptr(k_new), _ld(k_new, n), _ptr(v_new), _ld(v_new, n), _ptr(slots), N, _ptr(k_seen), _ptr(v_seen), _ptr(dev_status), _stream(stream)),
-           "moe_kv_append")
+    N, heads, dim = k_new.shape
+    st = lib().moe_kv_append(
+        cache, k_new.data_ptr(), k_new.stride(0) if N > 1 else heads * dim, v_new.data_ptr(),
+        v_new.stride(0) if N > 1 else heads * dim, slots.data_ptr(), N,
+        k_seen.data_ptr() if k_seen is not None else None, v_seen.data_ptr() if v_seen is not None else None,
+        dev_status.data_ptr() if dev_status is not None else None, _stream(stream))
+    if st:
+        _check(st, "moe_kv_append")
 
 
 def moe_kv_attend_workspace_bytes(cache: KVCacheT, batch, q_len, num_q_heads, max_pages) -> int:
@@ -357,12 +369,15 @@ def moe_kv_attend(cache: KVCacheT, q, ld_q, page_table, seq_lens, softmax_scale,
     """q [batch, q_len, num_q_heads, head_dim] bf16 with ld_q values between rows (b, t) and (b, t + 1) and
     between the last row of a sequence and the first of the next; page_table [batch, max_pages] int32."""
     B, T, Hq, D = q.shape
-    if B * T == 1:
-        ld_q = Hq * D
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().moe_kv_attend(cache, _ptr(q), ld_q, B, T, Hq, _ptr(page_table), _ld(page_table, page_table.shape[1]),
-                               page_table.shape[1], _ptr(seq_lens), softmax_scale, _ptr(out), _ptr(lse),
-                               _ptr(workspace), wsb, _ptr(dev_status), _stream(stream)), "moe_kv_attend")
+    pages = page_table.shape[1]
+    st = lib().moe_kv_attend(
+        cache, q.data_ptr(), ld_q if B * T > 1 else Hq * D, B, T, Hq, page_table.data_ptr(),
+        page_table.stride(0) if B > 1 else pages, pages, seq_lens.data_ptr(), softmax_scale, out.data_ptr(),
+        lse.data_ptr() if lse is not None else None, workspace.data_ptr() if workspace is not None else None,
+        workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        dev_status.data_ptr() if dev_status is not None else None, _stream(stream))
+    if st:
+        _check(st, "moe_kv_attend")
 
 
 def moe_test_gemm1(padded_offsets, row_to_slot, M, top_k, xq, xsf, xs, w: WeightsT, prepared, mode,

@@ -2,6 +2,13 @@
 //
 // Per row: h = x + r, f = h * rsqrt(sum(h^2) / H + eps) * w; bf16(h), bf16(f), and per scale
 // group scale = amax|f| / 448, e4m3(f * (448 / amax)).
+//
+// Bound by HBM (9 bytes per value with every output); few rows by the chain load - sum - store. A
+// row stays in the registers of its warps between its one read and its one write. An item of a
+// warp is 256 columns, eight neighbouring ones a lane, so that 16 lanes hold a scale group. Rows that are
+// not whole 16-byte pieces are read and written by the value (or by pairs) side by side and change
+// hands in shared memory, so that every alignment adds in the same order. Sums and scales meet
+// in shared memory only where a row has several warps.
 #include <math.h>
 
 #include "common.cuh"
@@ -10,7 +17,6 @@
 namespace moe {
 namespace {
 
-constexpr int kNormThreads = 256;
 constexpr int kNormMaxCols = 32768;
 
 // maximum that lets a NaN through (fmaxf drops it)
@@ -19,9 +25,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-
-__device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
-__device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
 struct NormArgs {
   const uint16_t* x;
@@ -32,50 +35,224 @@ struct NormArgs {
   uint8_t* y8;
   float* scale;
   int64_t ld_x, ld_r;
-  int M, H, groups, group;  // group: columns of one scale
+  int M, H, fp8, groups, warps;  // warps: of one row
   float eps;
 };
 
-__global__ void __launch_bounds__(kNormThreads) norm_rows_kernel(NormArgs a) {
-  extern __shared__ float row[];  // h, then f
-  __shared__ float red[kNormThreads / 32];
+constexpr int kItem = 256;
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void unpack8(float* v, uint4 u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+
+template <int V> struct Piece;  // V values of BF16, and of E4M3
+template <> struct Piece<2> { using Bf16 = uint32_t; using Fp8 = uint16_t; };
+template <> struct Piece<1> { using Bf16 = uint16_t; using Fp8 = uint8_t; };
+
+// One item as a lane reads it: its eight values (V == 8), or pieces of V values 32 pieces apart
+template <int V>
+struct Raw {
+  using T = typename Piece<V>::Bf16;
+  T v[8 / V];
+  __device__ __forceinline__ void load(const uint16_t* p, int lane, int left) {
+#pragma unroll
+    for (int i = 0; i < 8 / V; ++i) {
+      v[i] = 0;
+      if ((i * 32 + lane) * V < left) v[i] = *reinterpret_cast<const T*>(p + (i * 32 + lane) * V);
+    }
+  }
+  __device__ __forceinline__ uint4 mine(uint8_t* turn, int lane) const {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8 / V; ++i) reinterpret_cast<T*>(turn)[i * 32 + lane] = v[i];
+    __syncwarp();
+    return reinterpret_cast<const uint4*>(turn)[lane];
+  }
+};
+template <>
+struct Raw<8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p, int lane, int left) {
+    v = make_uint4(0, 0, 0, 0);
+    if (8 * lane < left) v = *reinterpret_cast<const uint4*>(p + 8 * lane);
+  }
+  __device__ __forceinline__ uint4 mine(uint8_t*, int) const { return v; }
+};
+
+// An item's `left` first values, eight to a lane in u, to memory
+template <int V>
+__device__ __forceinline__ void store_bf16(uint16_t* p, uint4 u, uint8_t* turn, int lane, int left) {
+  if constexpr (V == 8) {
+    if (8 * lane < left) *reinterpret_cast<uint4*>(p + 8 * lane) = u;
+  } else {
+    using T = typename Piece<V>::Bf16;
+    __syncwarp();
+    reinterpret_cast<uint4*>(turn)[lane] = u;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8 / V; ++i)
+      if ((i * 32 + lane) * V < left) *reinterpret_cast<T*>(p + (i * 32 + lane) * V) = reinterpret_cast<const T*>(turn)[i * 32 + lane];
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_fp8(uint8_t* p, uint2 u, uint8_t* turn, int lane, int left) {
+  if constexpr (V == 8) {
+    if (8 * lane < left) *reinterpret_cast<uint2*>(p + 8 * lane) = u;
+  } else {
+    using T = typename Piece<V>::Fp8;
+    __syncwarp();
+    reinterpret_cast<uint2*>(turn)[lane] = u;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8 / V; ++i)
+      if ((i * 32 + lane) * V < left) *reinterpret_cast<T*>(p + (i * 32 + lane) * V) = reinterpret_cast<const T*>(turn)[i * 32 + lane];
+  }
+}
+
+// The sum (or NaN-keeping maximum) of v over a row: its warp's lanes, then its warps in order.
+template <bool MAX>
+__device__ __forceinline__ float over_row(float v, float* red, int warps, int lane, int warp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? max_nan(v, u) : v + u;
+  }
+  if (warps == 1) return v;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  v = red[0];
+  for (int i = 1; i < warps; ++i) v = MAX ? max_nan(v, red[i]) : v + red[i];
+  return v;
+}
+
+// V: values read at once (8, 2 or 1, by the rows' alignment); ITEMS: items of a warp
+template <int V, int ITEMS>
+__global__ void __launch_bounds__(ITEMS > 2 ? 512 : 1024) norm_kernel(NormArgs a) {
+  __shared__ float red[2][32];
+  __shared__ __align__(16) uint8_t turns[V == 8 ? 1 : (ITEMS > 2 ? 16 : 32)][V == 8 ? 16 : 2 * kItem];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t m = blockIdx.x;
+  const int lane = threadIdx.x & 31, in_block = threadIdx.x >> 5;
+  // several rows to a block only where a row is one warp's
+  const int row = a.warps == 1 ? in_block : 0, warp = a.warps == 1 ? 0 : in_block;
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * (a.warps == 1 ? blockDim.x >> 5 : 1) + row;
+  if (m >= a.M) return;
+  uint8_t* const turn = turns[V == 8 ? 0 : in_block];
+  const int64_t out = m * a.H;
+  float h[ITEMS][8];
+  {
+    Raw<V> x[ITEMS], r[ITEMS];  // all of the row's loads before any of them is used
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int col = (warp + i * a.warps) * kItem;
+      x[i].load(a.x + m * a.ld_x + col, lane, a.H - col);
+      if (a.r) r[i].load(a.r + m * a.ld_r + col, lane, a.H - col);
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int col = (warp + i * a.warps) * kItem;
+      unpack8(h[i], x[i].mine(turn, lane));
+      if (a.r) {
+        float t[8];
+        unpack8(t, r[i].mine(turn, lane));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = __fadd_rn(h[i][e], t[e]);
+        if (a.r_out)
+          store_bf16<V>(a.r_out + out + col, make_uint4(bf16x2(h[i][0], h[i][1]), bf16x2(h[i][2], h[i][3]),
+                                                        bf16x2(h[i][4], h[i][5]), bf16x2(h[i][6], h[i][7])),
+                        turn, lane, a.H - col);
+      }
+    }
+  }
   float sum = 0.0f;
-  for (int i = tid; i < a.H; i += kNormThreads) {
-    float h = bf16_to_f32(a.x[m * a.ld_x + i]);
-    if (a.r) h = __fadd_rn(h, bf16_to_f32(a.r[m * a.ld_r + i]));
-    if (a.r_out) a.r_out[m * a.H + i] = f32_to_bf16(h);
-    row[i] = h;
-    sum += h * h;
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) red[warp] = sum;
-  __syncthreads();
-  sum = 0.0f;
+  for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-  for (int i = 0; i < kNormThreads / 32; ++i) sum += red[i];
+    for (int e = 0; e < 8; ++e) sum += h[i][e] * h[i][e];
+  sum = over_row<false>(sum, red[0], a.warps, lane, warp);
   const float rstd = rsqrtf(sum / static_cast<float>(a.H) + a.eps);
-  for (int i = tid; i < a.H; i += kNormThreads) {
-    const float f = __fmul_rn(__fmul_rn(row[i], rstd), bf16_to_f32(a.w[i]));
-    row[i] = f;
-    if (a.y) a.y[m * a.H + i] = f32_to_bf16(f);
-  }
-  if (!a.y8) return;
-  __syncthreads();
-  for (int g = warp; g < a.groups; g += kNormThreads / 32) {
-    const int end = min(a.H, (g + 1) * a.group);
-    float amax = 0.0f;
-    for (int i = g * a.group + lane; i < end; i += 32) amax = max_nan(amax, fabsf(row[i]));
+
+  float amax[ITEMS], most = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float inv = amax == 0.0f ? 1.0f : __fdiv_rn(448.0f, amax);
-    if (lane == 0) a.scale[m * a.groups + g] = amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f);
-    for (int i = g * a.group + lane; i < end; i += 32)
-      a.y8[m * a.H + i] = static_cast<uint8_t>(f32_to_e4m3(__fmul_rn(row[i], inv)));
+  for (int i = 0; i < ITEMS; ++i) {
+    const int col = (warp + i * a.warps) * kItem;
+    float w[8];
+    Raw<8> raw;  // the weight itself is aligned; its last piece may be short
+    if (V == 8 || col + 8 * lane + 8 <= a.H) {
+      raw.load(a.w + col, lane, a.H - col);
+      unpack8(w, raw.v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        w[e] = 0.0f;
+        if (col + 8 * lane + e < a.H) w[e] = __uint_as_float(static_cast<uint32_t>(a.w[col + 8 * lane + e]) << 16);
+      }
+    }
+    amax[i] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      h[i][e] = __fmul_rn(__fmul_rn(h[i][e], rstd), w[e]);
+      if (V == 8 ? col + 8 * lane < a.H : col + 8 * lane + e < a.H) amax[i] = max_nan(amax[i], fabsf(h[i][e]));
+    }
+    if (a.y)
+      store_bf16<V>(a.y + out + col, make_uint4(bf16x2(h[i][0], h[i][1]), bf16x2(h[i][2], h[i][3]),
+                                                bf16x2(h[i][4], h[i][5]), bf16x2(h[i][6], h[i][7])),
+                    turn, lane, a.H - col);
+    most = max_nan(most, amax[i]);
+  }
+  if (a.fp8 == MOE_FP8_NONE) return;
+  if (a.fp8 == MOE_FP8_PER_TOKEN) {
+    most = over_row<true>(most, red[1], a.warps, lane, warp);
+    if (lane == 0 && warp == 0) a.scale[m] = most == 0.0f ? 1.0f : __fdiv_rn(most, 448.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int col = (warp + i * a.warps) * kItem;
+    float top = most;
+    if (a.fp8 == MOE_FP8_PER_GROUP) {
+      top = amax[i];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if ((lane & 15) == 0 && col + 8 * lane < a.H)
+        a.scale[m * a.groups + (col + 8 * lane) / MOE_FP8_GROUP] = top == 0.0f ? 1.0f : __fdiv_rn(top, 448.0f);
+    }
+    const float inv = top == 0.0f ? 1.0f : __fdiv_rn(448.0f, top);
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = __fmul_rn(h[i][e], inv);
+    store_fp8<V>(a.y8 + out + col, make_uint2(e4m3x2(t[0], t[1]) | e4m3x2(t[2], t[3]) << 16,
+                                              e4m3x2(t[4], t[5]) | e4m3x2(t[6], t[7]) << 16),
+                 turn, lane, a.H - col);
+  }
+}
+
+template <int V>
+moe_status_t launch_norm(NormArgs a, cudaStream_t s) {
+  const int items = (a.H + kItem - 1) / kItem;
+  // A warp's items: one while the rows leave SMs idle (the shortest chain), otherwise enough to keep a
+  // warp's loads in flight and a block's warps few; a block has at most 32 warps, or 16 of over two items.
+  int per = a.M <= num_sms() ? 1 : 4;
+  while ((items + per - 1) / per > (per > 2 ? 16 : 32)) per *= 2;
+  while (per > 1 && items <= per / 2) per /= 2;
+  a.warps = (items + per - 1) / per;
+  const int rows = a.warps == 1 ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.M) + rows - 1) / rows)), block(32 * a.warps * rows);
+  switch (per) {
+    case 1: return launch_pdl(norm_kernel<V, 1>, grid, block, 0, s, a);
+    case 2: return launch_pdl(norm_kernel<V, 2>, grid, block, 0, s, a);
+    case 4: return launch_pdl(norm_kernel<V, 4>, grid, block, 0, s, a);
+    default: return launch_pdl(norm_kernel<V, 8>, grid, block, 0, s, a);
   }
 }
 
@@ -113,9 +290,9 @@ extern "C" moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ld_x, const u
     }
     for (int j = 0; j < i; ++j) MOE_CHECK(!overlaps(out[i], out_bytes[i], out[j], out_bytes[j]), MOE_ERR_OVERLAP);
   }
-  NormArgs a = {x, residual, weight, y, residual_out, y8, y8_scale, ld_x, ld_r, M, H, groups,
-                fp8_scale == MOE_FP8_PER_GROUP ? MOE_FP8_GROUP : H, eps};
-  const size_t smem = static_cast<size_t>(H) * 4;
-  MOE_CUDA(cudaFuncSetAttribute(norm_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4));
-  return launch_pdl(norm_rows_kernel, dim3(M), dim3(kNormThreads), smem, as_stream(stream), a);
+  const NormArgs a = {x, residual, weight, y, residual_out, y8, y8_scale, ld_x, ld_r, M, H, fp8_scale, groups, 1, eps};
+  cudaStream_t s = as_stream(stream);
+  if (((H | ld_x | (residual ? ld_r : 0)) & 7) == 0) return launch_norm<8>(a, s);
+  if (((H | ld_x | (residual ? ld_r : 0)) & 1) == 0) return launch_norm<2>(a, s);
+  return launch_norm<1>(a, s);
 }

@@ -22,18 +22,14 @@ def _need(cond, what: str):
 
 
 def _dense(t, dtype, shape, what: str):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on the GPU")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the GPU")
 
 
 def _rows(t, dtype, shape, what: str):
     """t: rows of `shape` whose values lie side by side (any row stride)."""
-    if t.dtype is not dtype or t.shape != shape or (t.stride(1) != 1 and shape[1] != 1):
-        raise ValueError(f"{what} must be {dtype} rows of shape {tuple(shape)} with their values side by side")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on the GPU")
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or (t.stride(1) != 1 and shape[1] != 1):
+        raise ValueError(f"{what} must be {dtype} rows of shape {tuple(shape)} on the GPU, their values side by side")
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
