@@ -40,6 +40,7 @@ struct NormArgs {
 };
 
 constexpr int kItem = 256;
+constexpr int kNormWarps = 32;
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -240,9 +241,11 @@ __global__ void __launch_bounds__(ITEMS > 2 ? 512 : 1024) norm_kernel(NormArgs a
 template <int V>
 moe_status_t launch_norm(NormArgs a, cudaStream_t s) {
   const int items = (a.H + kItem - 1) / kItem;
-  // A warp's items: one while the rows leave SMs idle (the shortest chain), otherwise enough to keep a
-  // warp's loads in flight and a block's warps few; a block has at most 32 warps, or 16 of over two items.
-  int per = a.M <= num_sms() ? 1 : 4;
+  // A warp's items: up to four, its loads in flight together, while that leaves kNormWarps warps to every
+  // SM; fewer, so that a row's chain gets shorter, for fewer rows. A block has at most 32 warps,
+  // or 16 of over two items.
+  int per = 4;
+  while (per > 1 && a.M * static_cast<int64_t>((items + per - 1) / per) < kNormWarps * num_sms()) per /= 2;
   while ((items + per - 1) / per > (per > 2 ? 16 : 32)) per *= 2;
   while (per > 1 && items <= per / 2) per /= 2;
   a.warps = (items + per - 1) / per;
