@@ -446,7 +446,7 @@ typedef struct {
  *   slots         [N] int64 distinct slots; negative: the token is not stored. A slot past the
  *                 cache is skipped and sets MOE_DEV_BAD_INDEX
  *   k_seen, v_seen  [N, num_kv_heads, head_dim] BF16 (out, both or neither): what the cache holds
- *                 for each token, bf16(code * scale / g), for callers that go on with the values
+ *                 for each token, bf16(code * (scale / g)), for callers that go on with the values
  *                 later steps will see; written for tokens without a slot too
  *   dev_status    may be NULL
  * N == 0 is a no-op.

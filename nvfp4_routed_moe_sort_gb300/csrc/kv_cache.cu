@@ -1,5 +1,7 @@
 // A paged key/value cache in NVFP4: the append that encodes new tokens into it and the
 // attention of a decode step that reads it.
+#include <cuda_fp16.h>
+#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -19,55 +21,54 @@ struct Cache {
   int pages, page_shift, heads, dim;
 };
 
-__device__ __forceinline__ float e2m1_to_f32(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3, m = c & 1;
-  const float v = e == 0 ? 0.5f * m : (1.0f + 0.5f * m) * static_cast<float>(1u << (e - 1));
-  return (c & 8) ? -v : v;
-}
-
-// One thread per 16-value block of one token's keys or values.
+// One thread per 16-value block of one token's keys (blockIdx.y 0) or values (1): bound by its chain of
+// load, block maximum, two divisions and stores. The held value is code * (scale / g).
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, const uint16_t* __restrict__ k_new,
                                                                    int64_t ld_k, const uint16_t* __restrict__ v_new,
                                                                    int64_t ld_v, const int64_t* __restrict__ slots,
-                                                                   int64_t N, uint16_t* k_seen, uint16_t* v_seen,
+                                                                   int N, uint16_t* k_seen, uint16_t* v_seen,
                                                                    int32_t* dev_status) {
   pdl_wait();
   pdl_trigger();
+  const bool vals = blockIdx.y != 0;
   const int per_head = c.dim / kBlock, per_token = c.heads * per_head;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x;
-  if (i >= N * 2 * per_token) return;
-  const int64_t n = i / (2 * per_token);
-  const int in_token = static_cast<int>(i - n * 2 * per_token);
-  const int which = in_token >= per_token;
-  const int b = in_token - which * per_token;
+  const int64_t n = i / per_token;
+  if (n >= N) return;
+  const int b = static_cast<int>(i - n * per_token);
   const int head = b / per_head, blk = b - head * per_head;
-  float v[16];
-  load_block16(which ? v_new + n * ld_v + b * kBlock : k_new + n * ld_k + b * kBlock, v);
-  uint32_t codes[2];
-  const float g = c.g[which];
-  const uint32_t q = quantize_block16(v, g, codes);
   const int64_t slot = slots[n];
+  float v[16];
+  load_block16((vals ? v_new + n * ld_v : k_new + n * ld_k) + b * kBlock, v);
+  uint32_t codes[2];
+  const float g = vals ? c.g[1] : c.g[0];
+  const uint32_t q = quantize_block16(v, g, codes);
   const int64_t page = slot >> c.page_shift;
   if (slot >= 0 && page < c.pages) {
     const int64_t row = (static_cast<int64_t>(head) << c.page_shift) + (slot & ((1 << c.page_shift) - 1));
-    *reinterpret_cast<uint2*>(c.data[which] + page * c.data_page + row * (c.dim / 2) + blk * 8) =
-        make_uint2(codes[0], codes[1]);
-    c.sf[which][page * c.sf_page + row * per_head + blk] = static_cast<uint8_t>(q);
-  } else if (slot >= 0 && dev_status && in_token == 0) {
+    uint8_t* const data = (vals ? c.data[1] : c.data[0]) + page * c.data_page + row * (c.dim / 2) + blk * 8;
+    uint8_t* const sf = (vals ? c.sf[1] : c.sf[0]) + page * c.sf_page + row * per_head + blk;
+    *reinterpret_cast<uint2*>(data) = make_uint2(codes[0], codes[1]);
+    *sf = static_cast<uint8_t>(q);
+  } else if (slot >= 0 && dev_status && b == 0 && !vals) {
     atomicOr(dev_status, MOE_DEV_BAD_INDEX);
   }
-  uint16_t* seen = which ? v_seen : k_seen;
+  uint16_t* const seen = vals ? v_seen : k_seen;
   if (seen) {
-    const float s = e4m3_to_f32(q);
+    const float s = __fdiv_rn(e4m3_to_f32(q), g);
     uint32_t o[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t byte = codes[j >> 2] >> (8 * (j & 3));
-      const float lo = __fdiv_rn(e2m1_to_f32(byte & 15) * s, g), hi = __fdiv_rn(e2m1_to_f32((byte >> 4) & 15) * s, g);
-      o[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(lo))) |
-             static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16;
+    for (int w = 0; w < 2; ++w) {
+      uint32_t f[4];
+      e2m1x8_to_f16x2(codes[w], f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
+        const __nv_bfloat162 y = __floats2bfloat162_rn(x.x * s, x.y * s);
+        o[4 * w + j] = *reinterpret_cast<const uint32_t*>(&y);
+      }
     }
-    uint4* dst = reinterpret_cast<uint4*>(seen + (n * per_token + b) * kBlock);
+    uint4* const dst = reinterpret_cast<uint4*>(seen + (n * per_token + b) * kBlock);
     dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
@@ -173,7 +174,6 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
   constexpr int kData = kAttGroup * D / 2, kSf = kAttGroup * D / 16, kStage = 2 * (kData + kSf);
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage][kStage]; the warps' sums at the end
   __shared__ __align__(8) uint64_t full[kAttWarps][kAttStages];
-  __shared__ int held_by[kAttWarps][kAttStages];    // which 16-token halves of a stage were copied
   __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, cc = lane & 3;
   if (lane < kAttStages) mbar_init(&full[warp][lane], 1);
@@ -209,13 +209,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
   const int64_t from_page = arr < 2 ? c.data_page : c.sf_page;
   const uint32_t to = (arr < 2 ? arr * kData : 2 * kData + (arr - 2) * kSf) + half * 16 * row_bytes;
   auto page_of = [&](int tok) { return tok + 16 * half < end ? table[(tok + 16 * half) >> c.page_shift] : -1; };
+  uint32_t held_next = 0;  // which 16-token halves of the stages in flight were copied, the oldest in bits 0 and 4
   auto issue = [&](int stage, int tok, int page) {
     const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(c.pages);
     const uint32_t held = __ballot_sync(0xffffffffu, ok) & 0x11;  // lanes 0 and 4
-    if (lane == 0) {
-      held_by[warp][stage] = held;
-      mbar_arrive_expect_tx(&full[warp][stage], ((held & 1) + (held >> 4)) * (kStage / 2));
-    }
+    held_next = held_next >> 8 | held << (8 * (kAttStages - 1));
+    if (lane == 0) mbar_arrive_expect_tx(&full[warp][stage], ((held & 1) + (held >> 4)) * (kStage / 2));
     __syncwarp();
     const int tokens = wide && held == 0x11 ? 32 : 16;
     if (lane < 8 && ok && (half == 0 || tokens == 16))
@@ -230,6 +229,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
 #pragma unroll
     for (int i = 0; i < kAttStages; ++i)
       if (tok + i * kAttStep < end) issue(i, tok + i * kAttStep, p[i]);
+      else held_next >>= 8;
     page = p[kAttStages];
   }
 
@@ -261,10 +261,11 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     float up, down;
     f16_range(amax, &up, &down);
+    if (a.scale < 0.0f) up = -up;  // the factor below is never negative
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
       q[t][i >> 1][i & 1] = pack_f16x2(bf16_lo(raw[i]) * up, bf16_hi(raw[i]) * up);
-    const float f = a.scale * kLog2e / c.g[0] * down;
+    const float f = fmaxf(fabsf(a.scale) * kLog2e / c.g[0] * down, FLT_MIN);  // above 0: -inf stays -inf
     to_log2[t][0] = __shfl_sync(0xffffffffu, f, 8 * cc);
     to_log2[t][1] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
   }
@@ -283,13 +284,11 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
   for (; tok < end; tok += kAttStep) {
     if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &abort_flag, a.dev_status, kWaitLimitNs))) break;
     const uint8_t* const st = my_ring + stage * kStage;
-    const int held = held_by[warp][stage];
+    const uint32_t held = held_next & 0xFF;
     // ---- scores of 32 tokens
     float s[2][NT][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.0f;
       uint32_t kw[2][KW], sc[2][2];  // [token r or r + 8][...]; a block's scale in both halves
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -310,17 +309,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
           const uint32_t x[4] = {mul_f16x2(f[0][2 * j], sc[0][w / 2]), mul_f16x2(f[1][2 * j], sc[1][w / 2]),
                                  mul_f16x2(f[0][2 * j + 1], sc[0][w / 2]), mul_f16x2(f[1][2 * j + 1], sc[1][w / 2])};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(s[u][t], x, q[t][2 * w + j]);
+          for (int t = 0; t < NT; ++t) {
+            if (w == 0 && j == 0) mma_f16_first(s[u][t], x, q[t][0]);
+            else mma_f16(s[u][t], x, q[t][2 * w + j]);
+          }
         }
       }
     }
     // ---- running maximum, weights
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][t][i] *= to_log2[t][i & 1];
     uint32_t vsf[2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -349,16 +345,17 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
     uint32_t p[2][NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float top[2], keep[2];
+      float top[2], keep[2], base[2];
       bool grew = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x = fmaxf(fmaxf(s[0][t][i], s[0][t][i + 2]), fmaxf(s[1][t][i], s[1][t][i + 2]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-        top[i] = fmaxf(m[t][i], x);
+        top[i] = fmaxf(m[t][i], x * to_log2[t][i]);
         grew |= top[i] > m[t][i];
         keep[i] = top[i] == -INFINITY ? 0.0f : top[i];
+        base[i] = kPShift - keep[i];
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -374,7 +371,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[u][t][i] = ex2(s[u][t][i] - keep[i & 1] + kPShift);
+          s[u][t][i] = ex2(fmaf(s[u][t][i], to_log2[t][i & 1], base[i & 1]));
           l[t][i & 1] += s[u][t][i];
         }
         p[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
@@ -414,6 +411,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
     if (next < end) {
       issue(stage, next, page);
       page = page_of(next + kAttStep);
+    } else {
+      held_next >>= 8;
     }
     if (++stage == kAttStages) stage = 0, parity ^= 1;
   }
@@ -621,10 +620,10 @@ extern "C" moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const uint16_
                 !overlaps(k_seen, sb, v_seen, sb) && !overlaps(k_seen, sb, k_new, kb) &&
                 !overlaps(k_seen, sb, v_new, vb) && !overlaps(v_seen, sb, k_new, kb) && !overlaps(v_seen, sb, v_new, vb),
             MOE_ERR_OVERLAP);
-  const int64_t blocks = static_cast<int64_t>(N) * 2 * (width / kBlock);
-  return launch_pdl(kv_append_kernel, dim3(static_cast<unsigned>((blocks + kAppendThreads - 1) / kAppendThreads)),
+  const int64_t blocks = static_cast<int64_t>(N) * (width / kBlock);
+  return launch_pdl(kv_append_kernel, dim3(static_cast<unsigned>((blocks + kAppendThreads - 1) / kAppendThreads), 2),
                     dim3(kAppendThreads), 0, as_stream(stream), c, k_new, ld_k, v_new, ld_v, slots,
-                    static_cast<int64_t>(N), k_seen, v_seen, dev_status);
+                    static_cast<int>(N), k_seen, v_seen, dev_status);
 }
 
 namespace {
