@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 constexpr int kAttWarps = 4;
 constexpr int kAttGroup = 32;                       // tokens of one step of a warp
 constexpr int kAttStep = kAttWarps * kAttGroup;     // tokens of one step of a block
-constexpr int kAttFill = 8, kAttLeast = 2;
+constexpr int kAttFill = 8, kAttMost = 1536;
 constexpr int kAttStages = 3;
 constexpr float kPShift = 15.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -165,7 +165,7 @@ __device__ __forceinline__ float row_lse(float top, float total) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_kernel(Cache c, AttendArgs a) {
+__global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : NT <= 3 ? 3 : 2) kv_attend_kernel(Cache c, AttendArgs a) {
   constexpr int KS = D / 16;       // MMA steps of S, MMA tiles of O
   constexpr int KW = D / 32;       // words of one token's keys per lane
   constexpr int VW = D / 64;       // words of one token's values per lane
@@ -193,7 +193,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
   }
   const int first = split * a.chunk;
   const int seen = max(row_limit(a, len, row0 + rows_here - 1), 0);  // by the block's last row
-  if (split > 0 && first >= seen) return;                            // the join does not read these parts
+  if (split > 0 && first >= seen) {  // nothing to see here: the join skips parts of sum 0
+    if (tid < rows_here) {
+      const int row = row0 + tid, t = row / a.group, g = row - t * a.group;
+      const int64_t at = (static_cast<int64_t>(b) * a.q_len + t) * a.q_heads + kvh * a.group + g;
+      a.part_ml[at * a.splits + split] = make_float2(-INFINITY, 0.0f);
+    }
+    return;
+  }
   const int end = min(seen, first + a.chunk);
   const int all_see = row_limit(a, len, row0);                       // every row sees the tokens before it
 
@@ -428,7 +435,6 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
   // ---- join the warps
   constexpr int ST = D + 4;
   __shared__ float sm[kAttWarps][R], sl[kAttWarps][R];
-  static_assert(R * ST * 4 <= kAttStages * kStage, "a warp's sums fit its ring");
   auto so = reinterpret_cast<float(*)[R][ST]>(ring);  // [warp][row][dim]
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -474,89 +480,85 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : 3) kv_attend_ker
   }
 }
 
-// Joins the parts of one query row. The block first turns the parts' maxima and sums into weights
-// (shared memory, kJoinParts at a time), then kJoinThreads / (D / 4) groups of threads each add every
-// so-manieth part, four dimensions to a thread, and the groups' sums are added in order.
+// Joins the parts of query rows, W warps to a row. Every warp weighs all parts (a lane a part; those
+// that saw nothing have weight 0 and are not read), then adds every so-manieth part with D / 4 lanes
+// of four dimensions each; the groups of lanes are added in order.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinParts = 1024;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(Cache c, AttendArgs a) {
-  constexpr int L = D / 4, G = kJoinThreads / L;
-  __shared__ float weight[kJoinParts], red[2][kJoinThreads / 32];
-  __shared__ float4 acc[G][L];
+template <int D, int W>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, float g, int64_t rows) {
+  constexpr int L = D / 4, P = 32 / L;  // lanes of a part, parts of a warp
+  __shared__ float4 acc[W > 1 ? kJoinThreads / 32 : 1][L];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t at = blockIdx.x, tok = at / a.q_heads;
-  const int b = static_cast<int>(tok / a.q_len), t = static_cast<int>(tok - static_cast<int64_t>(b) * a.q_len);
-  const int64_t most = static_cast<int64_t>(a.max_pages) << c.page_shift;
-  const int len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), most));
-  const int n = (max(len - (a.q_len - 1) + t, 0) + a.chunk - 1) / a.chunk;  // parts that the row sees
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32 / W) + warp / W;
+  const bool row = at < rows;
   const float2* ml = a.part_ml + at * a.splits;
   float top = -INFINITY;
-  for (int i = tid; i < n; i += kJoinThreads) top = fmaxf(top, ml[i].x);
+  if (row)
+    for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
   top = warp_max(top);
-  if (lane == 0) red[0][warp] = top;
-  __syncthreads();
-  top = red[0][0];
-#pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) top = fmaxf(top, red[0][w]);
-
-  const int g = tid / L, d = tid - g * L;
+  const int part = lane / L, d = lane - part * L;
+  const float4* po = reinterpret_cast<const float4*>(a.part_o + at * a.splits * D) + d;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float total = 0.0f;
-  for (int i0 = 0; i0 < n; i0 += kJoinParts) {
-    const int here = min(n - i0, kJoinParts);
-    __syncthreads();
-    for (int i = tid; i < here; i += kJoinThreads) {
-      const float2 x = ml[i0 + i];
-      const float f = x.y == 0.0f ? 0.0f : ex2(x.x - top);  // a part may have seen nothing
-      weight[i] = f;
-      total += f * x.y;
+  for (int i0 = 0; i0 < a.splits; i0 += 32) {
+    float mine = 0.0f;
+    if (row && i0 + lane < a.splits) {
+      const float2 x = ml[i0 + lane];
+      if (x.y != 0.0f) mine = ex2(x.x - top);
+      total += mine * x.y;
     }
-    __syncthreads();
-    const float4* po = reinterpret_cast<const float4*>(a.part_o + (at * a.splits + i0) * D) + d;
+    const int here = min(a.splits - i0, 32);
 #pragma unroll 4
-    for (int i = g; i < here; i += G) {
-      const float f = weight[i];
-      if (f == 0.0f) continue;
-      const float4 x = po[i * L];
-      v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+    for (int j = w * P; j < here; j += W * P) {
+      const float f = __shfl_sync(0xffffffffu, mine, (j + part) & 31);
+      if (j + part < here && f != 0.0f) {
+        const float4 x = po[static_cast<int64_t>(i0 + j + part) * L];
+        v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+      }
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) red[1][warp] = total;
-  acc[g][d] = v;
-  __syncthreads();
-  if (g > 0) return;
-  total = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) total += red[1][w];
-#pragma unroll
-  for (int i = 1; i < G; ++i) {
-    const float4 x = acc[i][d];
-    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  if constexpr (P == 2) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, 16), v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, 16), v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
   }
-  store_row(a, at * D + 4 * d, v, total, c.g[1]);
+  if constexpr (W > 1) {
+    if (part == 0) acc[warp][d] = v;
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      const float4 x = acc[warp + i][d];
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+  }
+  if (!row || part != 0) return;
+  store_row(a, at * D + 4 * d, v, total, g);
   if (a.lse && d == 0) a.lse[at] = row_lse(top, total);
 }
 
-// How a call is cut: rows of a block, and runs of the sequences. Enough blocks to fill every
-// SM twice over (sequences differ in length), no run shorter than four steps of a block.
+// How a call is cut: rows of a block, and runs of the sequences. A block takes as many row tiles as
+// its registers hold, since all of them share one conversion of the cache.
 struct Cut {
   int row_tiles, row_blocks, splits, chunk;
 };
 
-Cut cut_attend(int batch, int kv_heads, int rows, int64_t most) {
+Cut cut_attend(int batch, int kv_heads, int head_dim, int rows, int64_t most) {
   Cut k;
-  k.row_tiles = rows > 8 ? 2 : 1;
-  k.row_blocks = (rows + 8 * k.row_tiles - 1) / (8 * k.row_tiles);
+  const int tiles = (rows + 7) / 8, most_tiles = head_dim == 64 ? 4 : 2;
+  k.row_blocks = (tiles + most_tiles - 1) / most_tiles;
+  k.row_tiles = (tiles + k.row_blocks - 1) / k.row_blocks;
   const int64_t blocks = static_cast<int64_t>(batch) * kv_heads * k.row_blocks;
-  const int64_t want = (static_cast<int64_t>(num_sms()) * kAttFill + blocks - 1) / blocks;
+  const int fill = batch == 1 ? 4 : kAttFill;
+  const int64_t want = (static_cast<int64_t>(num_sms()) * fill + blocks - 1) / blocks;
   int64_t chunk = (most + want - 1) / want;
-  if (chunk < kAttLeast * kAttStep) chunk = kAttLeast * kAttStep;
+  if (batch > 1 && chunk > kAttMost) chunk = kAttMost;
+  const int least = k.row_tiles == 1 ? 2 : 3;  // steps of a block: joining its warps costs by the rows
+  if (chunk < least * kAttStep) chunk = least * kAttStep;
   chunk = roundup64(chunk, kAttStep);
   k.chunk = static_cast<int>(chunk < (1 << 30) ? chunk : (1 << 30));
   k.splits = most > 0 ? static_cast<int>((most + k.chunk - 1) / k.chunk) : 1;
@@ -640,7 +642,7 @@ moe_status_t attend_cut(const moe_kv_cache_t* cache, Cache* c, int32_t batch, in
   MOE_CHECK(batch <= 65535 && most < (int64_t(1) << 30) && q_len <= 65535 && rows * c->heads <= 65535 &&
                 rows * c->heads * (batch > 0 ? batch : 1) < (int64_t(1) << 31),
             MOE_ERR_UNSUPPORTED_SHAPE);
-  *cut = cut_attend(batch > 0 ? batch : 1, c->heads, static_cast<int>(rows), most);
+  *cut = cut_attend(batch > 0 ? batch : 1, c->heads, c->dim, static_cast<int>(rows), most);
   const int64_t parts = cut->splits > 1 ? static_cast<int64_t>(batch) * q_len * num_q_heads * cut->splits : 0;
   *bytes = static_cast<size_t>(roundup64(parts * c->dim * 4, 16) + parts * 8);
   return MOE_OK;
@@ -694,12 +696,26 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
                         num_q_heads, num_q_heads / c.heads, cut.row_blocks, max_pages, cut.splits, cut.chunk,
                         softmax_scale};
   const dim3 grid(cut.splits, c.heads * cut.row_blocks, batch);
-  auto* kern = c.dim == 64 ? (cut.row_tiles == 1 ? kv_attend_kernel<64, 1> : kv_attend_kernel<64, 2>)
-                           : (cut.row_tiles == 1 ? kv_attend_kernel<128, 1> : kv_attend_kernel<128, 2>);
-  const int smem = kAttWarps * kAttStages * kAttGroup * c.dim * 9 / 8;
+  decltype(&kv_attend_kernel<64, 1>) kern;
+  if (c.dim == 64)
+    kern = cut.row_tiles == 1   ? kv_attend_kernel<64, 1>
+           : cut.row_tiles == 2 ? kv_attend_kernel<64, 2>
+           : cut.row_tiles == 3 ? kv_attend_kernel<64, 3>
+                                : kv_attend_kernel<64, 4>;
+  else
+    kern = cut.row_tiles == 1 ? kv_attend_kernel<128, 1> : kv_attend_kernel<128, 2>;
+  // the warps' rings, and after them their sums in the same place
+  const int rings = kAttWarps * kAttStages * kAttGroup * c.dim * 9 / 8;
+  const int sums = kAttWarps * 8 * cut.row_tiles * (c.dim + 4) * static_cast<int>(sizeof(float));
+  const int smem = rings > sums ? rings : sums;
   MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const moe_status_t ran = launch_pdl(kern, grid, dim3(kAttWarps * 32), smem, as_stream(stream), c, a);
   if (ran != MOE_OK || cut.splits == 1) return ran;
-  return launch_pdl(c.dim == 64 ? kv_join_kernel<64> : kv_join_kernel<128>,
-                    dim3(static_cast<unsigned>(rows * num_q_heads)), dim3(kJoinThreads), 0, as_stream(stream), c, a);
+  // a warp to a row while there are rows enough, or too few parts to share
+  const bool one = cut.splits <= 16 || rows * num_q_heads >= static_cast<size_t>(num_sms()) * 16;
+  auto* join = c.dim == 64 ? (one ? kv_join_kernel<64, 1> : kv_join_kernel<64, 8>)
+                           : (one ? kv_join_kernel<128, 1> : kv_join_kernel<128, 8>);
+  const int64_t all = static_cast<int64_t>(rows) * num_q_heads, per_block = one ? 8 : 1;
+  return launch_pdl(join, dim3(static_cast<unsigned>((all + per_block - 1) / per_block)), dim3(kJoinThreads), 0,
+                    as_stream(stream), a, c.g[1], all);
 }
