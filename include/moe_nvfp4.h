@@ -467,7 +467,7 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const uint16_t* 
  *   q           [batch * q_len, ld_q] BF16, the num_q_heads * head_dim values of a row contiguous;
  *               ld_q % 8 == 0
  *   page_table  [batch, ld_table] int32: page i of sequence b; entries past its length are not
- *               read. A page outside the cache is skipped and sets MOE_DEV_BAD_INDEX
+ *               used. A page outside the cache is skipped and sets MOE_DEV_BAD_INDEX
  *   max_pages   columns of page_table in use, <= ld_table: lengths above max_pages * page_size
  *               are cut there and set MOE_DEV_BAD_INDEX
  *   seq_lens    [batch] int32 (negative: empty)

@@ -185,13 +185,36 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : NT <= 3 ? 3 : 2)
   const int split = blockIdx.x, kvh = blockIdx.y / a.row_blocks, b = blockIdx.z;
   const int row0 = (blockIdx.y - kvh * a.row_blocks) * R;
   const int rows_here = min(R, a.q_len * a.group - row0);
-  int len = max(a.lens[b], 0);
+  // Everything the block's first copies and its queries wait for is fetched at once; pages past the
+  // sequence's end are fetched too and not used.
+  const int32_t* table = a.table + b * a.ld_table;
+  const int half = (lane >> 2) & 1, first = split * a.chunk;
+  int tok = first + warp * kAttGroup;
+  int len = a.lens[b], pages[kAttStages + 1];
+#pragma unroll
+  for (int i = 0; i <= kAttStages; ++i) {
+    const int at = (tok + i * kAttStep + 16 * half) >> c.page_shift;
+    pages[i] = at < a.max_pages ? table[at] : -1;
+  }
+  uint32_t raw[NT][D / 8];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = row0 + 8 * t + r, at = row / a.group, g = row - at * a.group;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        a.q + (static_cast<int64_t>(b) * a.q_len + at) * a.ld_q + (kvh * a.group + g) * D + cc * (D / 4));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (8 * t + r < rows_here) u = src[i];
+      raw[t][4 * i] = u.x, raw[t][4 * i + 1] = u.y, raw[t][4 * i + 2] = u.z, raw[t][4 * i + 3] = u.w;
+    }
+  }
+  len = max(len, 0);
   const int64_t most = static_cast<int64_t>(a.max_pages) << c.page_shift;
   if (len > most) {
     len = static_cast<int>(most);
     if (a.dev_status && tid == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
   }
-  const int first = split * a.chunk;
   const int seen = max(row_limit(a, len, row0 + rows_here - 1), 0);  // by the block's last row
   if (split > 0 && first >= seen) {  // nothing to see here: the join skips parts of sum 0
     if (tid < rows_here) {
@@ -207,9 +230,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : NT <= 3 ? 3 : 2)
   // Lane 4u + w copies array w (keys, values, their scales) of the stage's u-th 16 tokens, or of all
   // 32 where a page holds them (u = 0). Copies stay inside a page whatever the sequence's length.
   uint8_t* const my_ring = ring + warp * (kAttStages * kStage);
-  const int32_t* table = a.table + b * a.ld_table;
   const bool wide = c.page_shift >= 5;
-  const int half = (lane >> 2) & 1, arr = lane & 3;
+  const int arr = lane & 3;
   const uint32_t row_bytes = arr < 2 ? D / 2 : D / 16;
   const uint8_t* const from = (arr == 0 ? c.data[0] : arr == 1 ? c.data[1] : arr == 2 ? c.sf[0] : c.sf[1]) +
                               (static_cast<int64_t>(kvh) << c.page_shift) * row_bytes;
@@ -228,42 +250,20 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : NT <= 3 ? 3 : 2)
       bulk_load(my_ring + stage * kStage + to, from + page * from_page + ((tok + 16 * half) & ((1 << c.page_shift) - 1)) * row_bytes,
                 tokens * row_bytes, &full[warp][stage]);
   };
-  int tok = first + warp * kAttGroup, page = -1;
-  {
-    int p[kAttStages + 1];
 #pragma unroll
-    for (int i = 0; i <= kAttStages; ++i) p[i] = page_of(tok + i * kAttStep);
-#pragma unroll
-    for (int i = 0; i < kAttStages; ++i)
-      if (tok + i * kAttStep < end) issue(i, tok + i * kAttStep, p[i]);
-      else held_next >>= 8;
-    page = p[kAttStages];
-  }
+  for (int i = 0; i < kAttStages; ++i)
+    if (tok + i * kAttStep < end) issue(i, tok + i * kAttStep, tok + i * kAttStep + 16 * half < end ? pages[i] : -1);
+    else held_next >>= 8;
+  int page = tok + kAttStages * kAttStep + 16 * half < end ? pages[kAttStages] : -1;
 
   // Q^T fragments and each row's factor from raw sums to base-2 scores
   uint32_t q[NT][KS][2];
   float to_log2[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int row = row0 + 8 * t + r;
-    uint32_t raw[D / 8];
     float amax = 0.0f;
-    if (8 * t + r < rows_here) {
-      const int tok = row / a.group, g = row - tok * a.group;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<int64_t>(b) * a.q_len + tok) * a.ld_q + (kvh * a.group + g) * D + cc * (D / 4));
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 u = src[i];
-        raw[4 * i] = u.x, raw[4 * i + 1] = u.y, raw[4 * i + 2] = u.z, raw[4 * i + 3] = u.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) raw[i] = 0;
-    }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-      amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[i])), fabsf(bf16_hi(raw[i]))));
+    for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[t][i])), fabsf(bf16_hi(raw[t][i]))));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     float up, down;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? 4 : NT <= 3 ? 3 : 2)
     if (a.scale < 0.0f) up = -up;  // the factor below is never negative
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
-      q[t][i >> 1][i & 1] = pack_f16x2(bf16_lo(raw[i]) * up, bf16_hi(raw[i]) * up);
+      q[t][i >> 1][i & 1] = pack_f16x2(bf16_lo(raw[t][i]) * up, bf16_hi(raw[t][i]) * up);
     const float f = fmaxf(fabsf(a.scale) * kLog2e / c.g[0] * down, FLT_MIN);  // above 0: -inf stays -inf
     to_log2[t][0] = __shfl_sync(0xffffffffu, f, 8 * cc);
     to_log2[t][1] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
@@ -708,7 +708,7 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   const int rings = kAttWarps * kAttStages * kAttGroup * c.dim * 9 / 8;
   const int sums = kAttWarps * 8 * cut.row_tiles * (c.dim + 4) * static_cast<int>(sizeof(float));
   const int smem = rings > sums ? rings : sums;
-  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if (smem > 48 * 1024) MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const moe_status_t ran = launch_pdl(kern, grid, dim3(kAttWarps * 32), smem, as_stream(stream), c, a);
   if (ran != MOE_OK || cut.splits == 1) return ran;
   // a warp to a row while there are rows enough, or too few parts to share
