@@ -103,7 +103,7 @@ constexpr int kAttWarps = 4;
 constexpr int kAttGroup = 32;                       // tokens of one step of a warp
 constexpr int kAttStep = kAttWarps * kAttGroup;     // tokens of one step of a block
 constexpr int kAttFill = 8, kAttMost = 1536;
-constexpr int kAttStages = 3;
+constexpr int kAttStages = 2;
 constexpr float kPShift = 15.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 

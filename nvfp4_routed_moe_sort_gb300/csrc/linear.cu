@@ -22,6 +22,7 @@
 // others store theirs into its shared memory, and after one barrier it adds all in a fixed order, so
 // results do not depend on timing. alpha, the activation and the BF16 rounding come once at the
 // end. A block goes on to further rows while there are any, their first chunks already in flight.
+#include "cluster.cuh"
 #include "common.cuh"
 #include "fp4_mma.cuh"
 #include "host_util.h"
@@ -70,14 +71,6 @@ __device__ __forceinline__ float activate(int act, float g, float u) {
     default: return g;
   }
 }
-
-__device__ __forceinline__ void store_cluster_f32(float* p, uint32_t rank, float v) {
-  uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // N bytes of global memory into shared memory, asynchronously; fewer `bytes` leave zeros behind them
 template <int N>
@@ -330,11 +323,12 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
       const int col = i0 + r + 8 * h, owner = col / share;
       float* const to_sum =
           sums + (((rank * a.across + part) * kinds + (up ? 1 : 0)) * share + col - owner * share) * kSumRow + 2 * c;
+      const uint32_t to_cluster = a.slices > 1 ? cluster_address(to_sum, owner) : 0;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (a.slices > 1) store_cluster_f32(to_sum + 8 * t + i, owner, acc[t][2 * h + i]);
+          if (a.slices > 1) store_cluster(to_cluster + 4 * (8 * t + i), acc[t][2 * h + i]);
           else to_sum[8 * t + i] = acc[t][2 * h + i];
         }
     }
@@ -361,23 +355,9 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
 
 template <int NT, int ALIGN>
 moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(32 * a.warps);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.slices;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
   if (smem > 48 * 1024)
     MOE_CUDA(cudaFuncSetAttribute(linear_kernel<NT, ALIGN>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
-  return cudaLaunchKernelEx(&cfg, linear_kernel<NT, ALIGN>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_clusters(linear_kernel<NT, ALIGN>, a.slices, grid, dim3(32 * a.warps), smem, s, a);
 }
 
 // shared memory of a block: two to an SM; the most of one; an SM's, 1 KB of it taken by each block

@@ -7,6 +7,8 @@ caller did not bring.
 """
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import _lib as L
@@ -30,6 +32,23 @@ def _rows(t, dtype, shape, what: str):
     """t: rows of `shape` whose values lie side by side (any row stride)."""
     if t.dtype is not dtype or t.shape != shape or not t.is_cuda or (t.stride(1) != 1 and shape[1] != 1):
         raise ValueError(f"{what} must be {dtype} rows of shape {tuple(shape)} on the GPU, their values side by side")
+
+
+_scratch: dict = {}
+
+
+def _workspace(nbytes: int, device) -> torch.Tensor | None:
+    """Scratch of one call. Outside graph capture it is kept for the next call of the same host thread on
+    the same stream, which runs after this one (a fresh tensor costs 5 us of host time a call)."""
+    if nbytes == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=_U8, device=device)
+    key = device, L.current_stream(), threading.get_ident()
+    t = _scratch.get(key)
+    if t is None or t.numel() < nbytes:
+        t = _scratch[key] = torch.empty(nbytes, dtype=_U8, device=device)
+    return t
 
 
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -200,8 +219,7 @@ class NVFP4KVCache:
         else:
             _dense(lse, _F32, (B, T, Hq), "lse")
         if workspace is None:
-            n = L.moe_kv_attend_workspace_bytes(self.c, B, T, Hq, page_table.shape[1])
-            workspace = torch.empty(n, dtype=_U8, device=q.device) if n else None
+            workspace = _workspace(L.moe_kv_attend_workspace_bytes(self.c, B, T, Hq, page_table.shape[1]), q.device)
         L.moe_kv_attend(self.c, q, ld, page_table, seq_lens, D ** -0.5 if softmax_scale is None else softmax_scale,
                         out, lse, workspace, self.dev_status)
         return out, lse
