@@ -30,7 +30,7 @@
 namespace moe {
 namespace {
 
-constexpr int kLinWarps = 8;              // most warps of a block, 16 rows of w each
+constexpr int kLinWarps = 16;             // most warps of a block, 16 rows of w each
 constexpr int kLinTokens = 16;
 constexpr int kLinChunk = 128;            // = MOE_FP8_GROUP
 constexpr int kLinStages = 3, kLinStage = 16 * 128 + 16 * 20;  // of two chunks: codes, scales
@@ -91,7 +91,7 @@ enum Align : int { kAlign256, kAlign32, kAlign16 };
 
 // NT: groups of eight tokens
 template <int NT, int ALIGN>
-__global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
+__global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
   pdl_trigger();
@@ -191,14 +191,14 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
 #pragma unroll
   for (int u = 0; u < kLinStages - 1; ++u) load_stage(u);
 
-  // x: half a warp per (token, chunk), eight values a lane, four loads in flight
+  // x: half a warp per (token, chunk), eight values a lane, eight loads in flight
   const int pairs = threads / 16;
-  for (int i = tid >> 4; i < M * chunks; i += 4 * pairs) {
+  for (int i = tid >> 4; i < M * chunks; i += 8 * pairs) {
     const int piece = tid & 15;
-    uint4 raw[4];
-    float scale[4];
+    uint4 raw[8];
+    float scale[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 8; ++u) {
       const int m = (i + u * pairs) / chunks, ch = i + u * pairs - m * chunks;
       const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
       raw[u] = make_uint4(0, 0, 0, 0);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 8; ++u) {
       const int m = (i + u * pairs) / chunks, ch = i + u * pairs - m * chunks;
       if (m >= M) break;
       const uint32_t v[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
@@ -332,10 +332,20 @@ __global__ void __launch_bounds__(kLinWarps * 32, 2) linear_kernel(LinArgs a) {
           else to_sum[8 * t + i] = acc[t][2 * h + i];
         }
     }
-    if (a.slices > 1) cluster_arrive(), cluster_wait();
-    else __syncthreads();
-    for (int i = tid; i < share * M; i += threads) {
-      const int m = i / share, col = i - m * share;
+    // What meets at the barrier: the cluster, or the warps of one tile (and of its up rows), which then
+    // add the tile's columns
+    int at_col = 0, cols = share, member = tid, members = threads;
+    if (a.slices > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      const int own = tiles / kinds, group = tile % own;
+      at_col = group * 16, cols = 16;
+      member = ((tile / own) * a.across + part) * 32 + lane, members = a.across * kinds * 32;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(members) : "memory");
+    }
+    for (int i = member; i < cols * M; i += members) {
+      const int m = i / cols, col = at_col + i - m * cols;
       const int64_t n = static_cast<int64_t>(block) * n_per + rank * share + col;
       if (n >= a.n_out) continue;
       float y[2] = {0.0f, 0.0f};
@@ -392,40 +402,50 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
             MOE_ERR_MISALIGNED);
   const int chunks = (K + kLinChunk - 1) / kLinChunk;
   LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, gated ? N / 2 : N, activation,
-               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, kLinWarps, 1, gated};
+               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, 8, 1, gated};
   const size_t ob = static_cast<size_t>(M) * a.n_out * 2;
   MOE_CHECK(!overlaps(out, ob, x, (static_cast<size_t>(M - 1) * ld_x + K) * (fp8 ? 1 : 2)) &&
                 !overlaps(out, ob, w, static_cast<size_t>(N) * K / 2) &&
                 !overlaps(out, ob, w_sf, static_cast<size_t>(N) * K / kBlock) && !overlaps(out, ob, alpha, 4) &&
                 !overlaps(out, ob, x_scale, static_cast<size_t>(M) * a.x_groups * 4),
             MOE_ERR_OVERLAP);
-  // Slices of K (a cluster barrier each row block) while a warp keeps two stages to itself and all blocks
-  // run at once, two to an SM; more where x's share of shared memory asks for it.
   auto blocks = [&] {
     const int64_t n_per = (gated ? 8 : 16) * (a.warps / a.across);
     return (a.n_out + n_per - 1) / n_per;
   };
-  auto cut = [&](int most) {  // for blocks of at most `most` tokens
-    a.tokens = M < most ? M : most;
-    a.slices = 1, a.slice = (chunks + 1) & ~1;
-    const int64_t groups = (static_cast<int64_t>(M) + a.tokens - 1) / a.tokens;
-    while (a.slices < 8 && a.slices < chunks &&
-           ((a.slice > 4 && blocks() * groups * a.slices <= num_sms()) ||
-            linear_smem(a.tokens, a.slice, a.warps) > kLinSmem)) {
-      a.slices *= 2;
-      a.slice = ((chunks + a.slices - 1) / a.slices + 1) & ~1;  // whole stages
+  const int64_t sms = num_sms();
+  a.tokens = M < kLinTokens ? M : kLinTokens;
+  int64_t groups = (static_cast<int64_t>(M) + a.tokens - 1) / a.tokens;
+  auto slice = [&](int n) { a.slices = n, a.slice = ((chunks + n - 1) / n + 1) & ~1; };  // whole stages
+  auto smem_of = [&] { return linear_smem(a.tokens, a.slice, a.warps); };
+  slice(1);
+  if (blocks() * groups >= 2 * sms) {
+    // Rows for many turns of every SM: one block of 16 warps to an SM, so that it lays x out once, four warps
+    // to whole rows. Where x does not fit beside their rings, slices of K, and more rows to each of the
+    // cluster's barriers as long as every cluster has four turns.
+    a.warps = 16;
+    while (a.slices < 8 && smem_of() > kLinSmemMost) slice(2 * a.slices);
+    if (smem_of() > kLinSmemMost) {  // the longest K
+      a.tokens = 8, groups = (static_cast<int64_t>(M) + 7) / 8;
     }
-    return groups;
-  };
-  int64_t groups = cut(kLinTokens);
-  if (linear_smem(a.tokens, a.slice, a.warps) > kLinSmemMost) groups = cut(8);  // the longest K
-  // whole rows where there are rows enough; smaller blocks where whole ones leave SMs idle
-  if (blocks() * groups >= 2 * num_sms() && a.slice >= 8) a.across = 4;
-  while (a.warps > 2 && blocks() * groups * a.slices < num_sms()) a.warps /= 2;
-  const size_t smem = linear_smem(a.tokens, a.slice, a.warps);
+    a.across = a.slice >= 8 ? 4 : 1;
+    if (a.slices > 1)
+      while (a.across > 1 && blocks() / 2 * a.slices >= 4 * sms) a.across /= 2;
+  } else {
+    // Fewer rows: slices of K while a warp keeps two stages to itself and all blocks run at once, two to an SM,
+    // and as x asks for; then smaller blocks where whole ones leave SMs idle.
+    while (a.slices < 8 && a.slices < chunks &&
+           ((a.slice > 4 && blocks() * groups * a.slices <= sms) || smem_of() > kLinSmem))
+      slice(2 * a.slices);
+    if (smem_of() > kLinSmemMost) {
+      a.tokens = 8, groups = (static_cast<int64_t>(M) + 7) / 8;
+    }
+    while (a.warps > 2 && blocks() * groups * a.slices < sms) a.warps /= 2;
+  }
+  const size_t smem = smem_of();
   MOE_CHECK(groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
   // as many blocks as run at once; they take row blocks in turn
-  const int64_t at_once = (kLinSmemSm / (smem + 1024) < 2 ? 1 : 2) * num_sms() / a.slices;
+  const int64_t at_once = (a.warps > 8 || kLinSmemSm / (smem + 1024) < 2 ? 1 : 2) * sms / a.slices;
   const dim3 grid(static_cast<unsigned>((blocks() < at_once ? blocks() : at_once) * a.slices), static_cast<unsigned>(groups));
   cudaStream_t s = as_stream(stream);
   const int align = K % 256 == 0 ? kAlign256 : K % 32 == 0 ? kAlign32 : kAlign16;
