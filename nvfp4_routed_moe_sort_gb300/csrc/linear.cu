@@ -6,7 +6,7 @@
 // to 32c + 31 of rows r and r + 8, and MMA step j takes its values 32c + 4j to 32c + 4j + 3.
 //
 // The codes come through a ring in shared memory that belongs to the warp (cp.async; two chunks a
-// stage, kLinStages of them): copied as 128 contiguous bytes per row, a quarter of the L1 lines
+// stage, two or three of them): copied as 128 contiguous bytes per row, a quarter of the L1 lines
 // that fetching them in fragment order would touch, and swizzled so that reading them in that
 // order meets no bank twice.
 //
@@ -33,7 +33,6 @@ namespace {
 constexpr int kLinWarps = 16;             // most warps of a block, 16 rows of w each
 constexpr int kLinTokens = 16;
 constexpr int kLinChunk = 128;            // = MOE_FP8_GROUP
-constexpr int kLinStages = 3, kLinStage = 16 * 128 + 16 * 20;  // of two chunks: codes, scales
 static_assert(kLinChunk == MOE_FP8_GROUP, "one E4M3 scale per chunk");
 
 struct LinArgs {
@@ -48,6 +47,8 @@ struct LinArgs {
   int slices, slice;                       // blocks of a cluster, chunks of each
   int tokens;                              // tokens of a block
   int warps, across;                       // warps of a block, and how many of them share rows
+  int stages;                              // of a warp's ring, two chunks each: 3 or 2
+  int buffers;                             // of sums: 2, or 1 where memory is short
   bool gated;
 };
 
@@ -86,8 +87,13 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// How rows of codes and of scales are aligned: K % 256 == 0, K % 32 == 0, or only K % 16 == 0
+// How rows are aligned: K % 256 == 0 (codes and scales to 16 bytes), K % 32 == 0 (codes to 16, scales to
+// 2), or only K % 16 == 0 (codes to 8, scales to 1). Copies are of 16 aligned bytes; where a row
+// starts inside such a piece, one more of them is copied and the row is read at its offset.
 enum Align : int { kAlign256, kAlign32, kAlign16 };
+__host__ __device__ constexpr int code_row(int align) { return align == kAlign16 ? 144 : 128; }
+__host__ __device__ constexpr int scale_row(int align) { return align == kAlign256 ? 16 : 48; }
+__host__ __device__ constexpr int stage_bytes(int align) { return 16 * (code_row(align) + scale_row(align)); }
 
 // NT: groups of eight tokens
 template <int NT, int ALIGN>
@@ -101,14 +107,15 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   const int m0 = blockIdx.y * a.tokens, M = min(a.M - m0, a.tokens);
   const int chunk0 = rank * a.slice;
   const int chunks = max(0, min(a.slice, (a.K + kLinChunk - 1) / kLinChunk - chunk0));
-  // shared memory: rings [warps][kLinStages * kLinStage], x [M][slice * 256 + 64 bytes],
-  // factors [slice][8 * NT], sums (twice) [16 * warps][8 * NT + 1]
-  uint8_t* const xs = smem + a.warps * (kLinStages * kLinStage);
+  constexpr int kRow = code_row(ALIGN), kSfRow = scale_row(ALIGN), kStage = stage_bytes(ALIGN);
+  // shared memory: rings [warps][stages][kStage], x [M][slice * 256 + 64 bytes],
+  // factors [slice][8 * NT], sums [buffers][16 * warps][8 * NT + 1]
+  uint8_t* const xs = smem + a.warps * a.stages * kStage;
   const int x_row = a.slice * (kLinChunk * 2) + 64;
   float* const factor = reinterpret_cast<float*>(xs + M * x_row);
   constexpr int kSumRow = 8 * NT + 1;
   float* sums = factor + a.slice * 8 * NT;
-  float* sums_next = sums + 16 * a.warps * kSumRow;
+  float* sums_next = a.buffers == 2 ? sums + 16 * a.warps * kSumRow : sums;
 
   // A row block is n_per output columns: their rows of w, or for the gated kinds their gate rows
   // (first half of the row tiles) and up rows (second half). Warp (tile, part) takes 16 of the rows
@@ -121,85 +128,96 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   const int run = ((chunks + a.across - 1) / a.across + 1) & ~1;  // whole stages
   const int first = min(part * run, chunks), last = min(first + run, chunks);
 
-  // ---- the ring. Lane (q, p) = (lane / 8, lane % 8) copies piece p (16 bytes) of rows q, q + 4, ...
-  const uint32_t ring = smem_u32(smem) + warp * (kLinStages * kLinStage);
-  const uint8_t* const ring_at = smem + warp * (kLinStages * kLinStage);
+  // ---- the ring. Lane (q, p) = (lane / 8, lane % 8) copies piece p (16 bytes) of the codes of rows q, q + 4,
+  // ..., lane 2i + j piece j of row i's scales. Past K lies the next row, which is copied along (zeros of x
+  // meet its codes, its scales are cleared when read); past the matrix nothing is read.
+  const uint32_t ring = smem_u32(smem) + warp * a.stages * kStage;
+  const uint8_t* const ring_at = smem + warp * a.stages * kStage;
   const int q = lane >> 3, p = lane & 7;
-  const uint32_t to = q * 128 + ((p ^ (q & 1) << 2) << 4);
-  const int sf_ld = a.K / kBlock;
-  const uint8_t *w_from, *sf_from;  // this lane's first piece of codes, and of scales, of the next stage
+  const uint32_t to = q * kRow + (ALIGN == kAlign16 ? p : p ^ (q & 1) << 2) * 16;
+  const uint32_t sf_to = 16 * kRow + (lane >> 1) * kSfRow + (lane & 1) * 16;
+  const int row_bytes = a.K / 2, sf_bytes = a.K / kBlock;
+  const int64_t rows = static_cast<int64_t>(a.gated ? 2 : 1) * a.n_out;
+  const uint8_t* const w_end = a.w + rows * row_bytes;
+  const uint8_t* const sf_end = a.sf + rows * sf_bytes;
+  const uint8_t *w_from, *w_ninth = nullptr, *sf_from;  // this lane's pieces of the next stage
+  bool sf_mine;
+  int64_t behind;  // bytes of the matrix from the tile's last row on
   int load_block = blockIdx.x / a.slices, load_ch = first, load_rows;
   auto rows_of = [&] {
     const int64_t n = static_cast<int64_t>(load_block) * n_per + i0;
     load_rows = load_block < blocks ? static_cast<int>(min(static_cast<int64_t>(a.n_out) - n, int64_t(16))) : 0;
     const int64_t row = n + (up ? a.n_out : 0);
-    w_from = a.w + (row + q) * (a.K / 2) + (chunk0 + first) * (kLinChunk / 2) + 16 * p;
-    sf_from = a.sf + (row + (ALIGN == kAlign256 ? lane : q)) * sf_ld + (chunk0 + first) * (kLinChunk / kBlock);
+    behind = (rows - row - 15) * row_bytes;
+    const int64_t at = static_cast<int64_t>(chunk0 + first) * (kLinChunk / 2);
+    const int64_t mine = (row + q) * row_bytes;
+    w_from = a.w + mine + at + 16 * p - (ALIGN == kAlign16 ? mine & 8 : 0);
+    if constexpr (ALIGN == kAlign16) {
+      const int64_t ninth = (row + lane) * row_bytes;  // of lanes below 16, where the row starts inside a piece
+      w_ninth = lane < 16 && (ninth & 8) ? a.w + ninth + at + 120 : nullptr;
+    }
+    const int64_t sf_at = (row + (lane >> 1)) * sf_bytes;
+    sf_mine = (lane & 1) == 0 || (ALIGN != kAlign256 && (sf_at & 15) != 0);
+    sf_from = a.sf + (sf_at & ~int64_t(15)) + at / 8 + 16 * (lane & 1);
   };
-  const uint8_t* const sf_end = a.sf + static_cast<int64_t>(a.gated ? 2 : 1) * a.n_out * sf_ld;
+  auto left = [](const uint8_t* from, const uint8_t* end) {
+    return static_cast<uint32_t>(max(min(end - from, static_cast<ptrdiff_t>(16)), static_cast<ptrdiff_t>(0)));
+  };
   auto load_stage = [&](int stage) {
-    const uint32_t at = ring + stage * kLinStage;
+    const uint32_t at = ring + stage * kStage;
     if (load_ch < last && load_rows > 0) {
-      const int k = (chunk0 + load_ch) * kLinChunk;
-      const bool whole = load_rows == 16 && load_ch + 2 <= last && k + 2 * kLinChunk <= a.K;
-      if (whole) {
+      if (load_rows == 16 && (chunk0 + load_ch + 2) * (kLinChunk / 2) <= behind) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (ALIGN != kAlign16) {
-            copy_async<16>(at + to + i * 512, w_from + i * 2 * a.K);
-          } else {
-            copy_async<8>(at + to + i * 512, w_from + i * 2 * a.K);
-            copy_async<8>(at + to + i * 512 + 8, w_from + i * 2 * a.K + 8);
-          }
-        }
+        for (int i = 0; i < 4; ++i) copy_async<16>(at + to + i * 4 * kRow, w_from + i * 4 * row_bytes);
+        if (ALIGN == kAlign16 && w_ninth) copy_async<16>(at + lane * kRow + 128, w_ninth, left(w_ninth, w_end));
+        if (sf_mine) copy_async<16>(at + sf_to, sf_from, ALIGN == kAlign256 ? 16 : left(sf_from, sf_end));
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // rows past the matrix, pieces past K: zeros
-          const bool row = q + 4 * i < load_rows && (p < 4 || load_ch + 1 < last);
-          const bool in0 = row && k + 32 * p < a.K, in1 = row && k + 32 * p + kBlock < a.K;
-          const uint8_t* const from = w_from + i * 2 * static_cast<int64_t>(a.K);
-          if constexpr (ALIGN != kAlign16) {
-            copy_async<16>(at + to + i * 512, in0 ? from : a.w, in0 ? 16 : 0);
-          } else {
-            copy_async<8>(at + to + i * 512, in0 ? from : a.w, in0 ? 8 : 0);
-            copy_async<8>(at + to + i * 512 + 8, in1 ? from + 8 : a.w, in1 ? 8 : 0);
-          }
-        }
-      }
-      if constexpr (ALIGN == kAlign256) {  // one row's 16 scales a lane
-        if (lane < 16) copy_async<16>(at + 2048 + lane * 16, lane < load_rows ? sf_from : a.sf, lane < load_rows ? 16 : 0);
-      } else {  // the (up to five) words that hold a row's 16 scales, four rows at a time
-#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint8_t* const s = sf_from + 4 * i * static_cast<int64_t>(sf_ld);
-          const uint8_t* const from = s - (reinterpret_cast<uintptr_t>(s) & 3) + 4 * p;
-          const bool in = q + 4 * i < load_rows && from < sf_end;
-          const int left = in ? static_cast<int>(min(sf_end - from, static_cast<ptrdiff_t>(4))) : 0;
-          if (p < 5) copy_async<4>(at + 2048 + (q + 4 * i) * 20 + 4 * p, in ? from : a.sf, left);
+          const uint8_t* const from = w_from + i * 4 * static_cast<int64_t>(row_bytes);
+          const uint32_t n = q + 4 * i < load_rows ? left(from, w_end) : 0;
+          copy_async<16>(at + to + i * 4 * kRow, n ? from : a.w, n);
+        }
+        if (ALIGN == kAlign16 && w_ninth) {
+          const uint32_t n = lane < load_rows ? left(w_ninth, w_end) : 0;
+          copy_async<16>(at + lane * kRow + 128, n ? w_ninth : a.w, n);
+        }
+        if (sf_mine) {
+          const uint32_t n = (lane >> 1) < load_rows ? left(sf_from, sf_end) : 0;
+          copy_async<16>(at + sf_to, n ? sf_from : a.sf, n);
         }
       }
     }
     copies_commit();
     load_ch += 2;
     w_from += kLinChunk, sf_from += 2 * kLinChunk / kBlock;
+    if (ALIGN == kAlign16 && w_ninth) w_ninth += kLinChunk;
     if (load_ch >= last) {
       load_ch = first, load_block += stride;
       rows_of();
     }
   };
   rows_of();
-#pragma unroll
-  for (int u = 0; u < kLinStages - 1; ++u) load_stage(u);
+  load_stage(0);
+  if (a.stages == 3) load_stage(1);
 
-  // x: half a warp per (token, chunk), eight values a lane, eight loads in flight
-  const int pairs = threads / 16;
-  for (int i = tid >> 4; i < M * chunks; i += 8 * pairs) {
-    const int piece = tid & 15;
-    uint4 raw[8];
-    float scale[8];
+  // x: half a warp per (token, chunk), eight values a lane, four loads in flight
+  const int pairs = threads / 16, piece = tid & 15;
+  int m_next = chunks ? (tid >> 4) / chunks : M, ch_next = (tid >> 4) - m_next * chunks;
+  const int m_step = chunks ? pairs / chunks : 0, ch_step = pairs - m_step * chunks;
+  while (m_next < M) {
+    uint4 raw[4];
+    float scale[4];
+    int ms[4], chs[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int m = (i + u * pairs) / chunks, ch = i + u * pairs - m * chunks;
+    for (int u = 0; u < 4; ++u) {
+      ms[u] = m_next, chs[u] = ch_next;
+      m_next += m_step, ch_next += ch_step;
+      if (ch_next >= chunks) ch_next -= chunks, ++m_next;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int m = ms[u], ch = chs[u];
       const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
       raw[u] = make_uint4(0, 0, 0, 0);
       if (m >= M) continue;
@@ -214,8 +232,8 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int m = (i + u * pairs) / chunks, ch = i + u * pairs - m * chunks;
+    for (int u = 0; u < 4; ++u) {
+      const int m = ms[u], ch = chs[u];
       if (m >= M) break;
       const uint32_t v[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
       uint4 f;
@@ -253,16 +271,19 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
     float acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-    uint32_t shift[2] = {0, 0};  // of a row's scales in their first word
+    // where rows r and r + 8 start in their first piece of codes, and of scales
+    int code_at = 0, scale_at[2] = {0, 0};
     if constexpr (ALIGN != kAlign256) {
       const int64_t row = static_cast<int64_t>(block) * n_per + i0 + (up ? a.n_out : 0) + r;
-      shift[0] = (row * sf_ld) & 3, shift[1] = ((row + 8) * sf_ld) & 3;
+      if (ALIGN == kAlign16) code_at = (row * row_bytes) & 8;
+      scale_at[0] = (row * sf_bytes) & 15, scale_at[1] = ((row + 8) * sf_bytes) & 15;
     }
     for (int ch0 = first; ch0 < last; ch0 += 2) {
-      copies_wait<kLinStages - 2>();
+      if (a.stages == 3) copies_wait<1>();
+      else copies_wait<0>();
       __syncwarp();  // every lane's copies of this stage are there, and the stage before it has been read
-      load_stage(stage == 0 ? kLinStages - 1 : stage - 1);
-      const uint8_t* const at = ring_at + stage * kLinStage;
+      load_stage(stage == 0 ? a.stages - 1 : stage - 1);
+      const uint8_t* const at = ring_at + stage * kStage;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int ch = ch0 + u;
@@ -271,16 +292,20 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int row = r + 8 * h;
-          const uint4 x = *reinterpret_cast<const uint4*>(at + row * 128 + ((4 * u + c) ^ (r & 1) << 2) * 16);
-          codes[h][0] = x.x, codes[h][1] = x.y, codes[h][2] = x.z, codes[h][3] = x.w;
-          if constexpr (ALIGN == kAlign256) {
-            two[h] = *reinterpret_cast<const uint16_t*>(at + 2048 + row * 16 + 8 * u + 2 * c);
+          if constexpr (ALIGN == kAlign16) {
+            const uint2* const w = reinterpret_cast<const uint2*>(at + row * kRow + code_at + (4 * u + c) * 16);
+            const uint2 x = w[0], y = w[1];
+            codes[h][0] = x.x, codes[h][1] = x.y, codes[h][2] = y.x, codes[h][3] = y.y;
           } else {
-            const uint8_t* const s = at + 2048 + row * 20 + shift[h] + 8 * u + 2 * c;
-            two[h] = s[0] | static_cast<uint32_t>(s[1]) << 8;
-            // past K lie the next row's scales, which may be no numbers
+            const uint4 x = *reinterpret_cast<const uint4*>(at + row * kRow + ((4 * u + c) ^ (r & 1) << 2) * 16);
+            codes[h][0] = x.x, codes[h][1] = x.y, codes[h][2] = x.z, codes[h][3] = x.w;
+          }
+          const uint8_t* const s = at + 16 * kRow + row * kSfRow + scale_at[h] + 8 * u + 2 * c;
+          if constexpr (ALIGN == kAlign16) two[h] = s[0] | static_cast<uint32_t>(s[1]) << 8;
+          else two[h] = *reinterpret_cast<const uint16_t*>(s);
+          if (ALIGN != kAlign256 && (chunk0 + ch + 1) * kLinChunk > a.K) {  // the next row's may be no numbers
             const int k = (chunk0 + ch) * kLinChunk + 32 * c;
-            if (k + 32 > a.K) two[h] = k < a.K ? two[h] & 0xFF : 0;
+            two[h] = k >= a.K ? 0 : k + kBlock >= a.K ? two[h] & 0xFF : two[h];
           }
           two[h] = e4m3x2_to_f16x2(two[h]);
         }
@@ -314,7 +339,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
           acc[t][2] += sum[t][2] * s.x, acc[t][3] += sum[t][3] * s.y;
         }
       }
-      if (++stage == kLinStages) stage = 0;
+      if (++stage == a.stages) stage = 0;
     }
 
     // sums [part of K][kind][column of the owner's share][token], in the owner's shared memory
@@ -356,10 +381,13 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
       a.out[static_cast<int64_t>(m0 + m) * a.n_out + n] =
           __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0] * alpha, y[1] * alpha)));
     }
-    // The other buffer is free: what it held was added before the barrier above.
-    float* const t = sums;
-    sums = sums_next;
-    sums_next = t;
+    if (a.buffers == 2) {  // the other buffer is free: what it held was added before the barrier above
+      float* const t = sums;
+      sums = sums_next;
+      sums_next = t;
+    } else {
+      asm volatile("bar.sync %0, %1;" ::"r"(tile % (tiles / kinds) + 1), "r"(members) : "memory");
+    }
   }
 }
 
@@ -373,10 +401,11 @@ moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_
 // shared memory of a block: two to an SM; the most of one; an SM's, 1 KB of it taken by each block
 constexpr size_t kLinSmem = 113 * 1024, kLinSmemMost = 227 * 1024, kLinSmemSm = 228 * 1024;
 
-size_t linear_smem(int tokens, int slice, int warps) {
-  const int columns = tokens > 8 ? 16 : 8;
-  return static_cast<size_t>(tokens) * (slice * kLinChunk * 2 + 64) + static_cast<size_t>(slice) * columns * 4 +
-         2 * static_cast<size_t>(16 * warps) * (columns + 1) * 4 + static_cast<size_t>(warps) * kLinStages * kLinStage;
+size_t linear_smem(const LinArgs& a, int align) {
+  const int columns = a.tokens > 8 ? 16 : 8;
+  return static_cast<size_t>(a.tokens) * (a.slice * kLinChunk * 2 + 64) + static_cast<size_t>(a.slice) * columns * 4 +
+         static_cast<size_t>(a.buffers) * 16 * a.warps * (columns + 1) * 4 +
+         static_cast<size_t>(a.warps) * a.stages * stage_bytes(align);
 }
 
 }  // namespace
@@ -402,13 +431,14 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
             MOE_ERR_MISALIGNED);
   const int chunks = (K + kLinChunk - 1) / kLinChunk;
   LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, gated ? N / 2 : N, activation,
-               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, 8, 1, gated};
+               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, 8, 1, 3, 2, gated};
   const size_t ob = static_cast<size_t>(M) * a.n_out * 2;
   MOE_CHECK(!overlaps(out, ob, x, (static_cast<size_t>(M - 1) * ld_x + K) * (fp8 ? 1 : 2)) &&
                 !overlaps(out, ob, w, static_cast<size_t>(N) * K / 2) &&
                 !overlaps(out, ob, w_sf, static_cast<size_t>(N) * K / kBlock) && !overlaps(out, ob, alpha, 4) &&
                 !overlaps(out, ob, x_scale, static_cast<size_t>(M) * a.x_groups * 4),
             MOE_ERR_OVERLAP);
+  const int align = K % 256 == 0 ? kAlign256 : K % 32 == 0 ? kAlign32 : kAlign16;
   auto blocks = [&] {
     const int64_t n_per = (gated ? 8 : 16) * (a.warps / a.across);
     return (a.n_out + n_per - 1) / n_per;
@@ -417,16 +447,22 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
   a.tokens = M < kLinTokens ? M : kLinTokens;
   int64_t groups = (static_cast<int64_t>(M) + a.tokens - 1) / a.tokens;
   auto slice = [&](int n) { a.slices = n, a.slice = ((chunks + n - 1) / n + 1) & ~1; };  // whole stages
-  auto smem_of = [&] { return linear_smem(a.tokens, a.slice, a.warps); };
+  auto smem_of = [&] { return linear_smem(a, align); };
   slice(1);
   if (blocks() * groups >= 2 * sms) {
-    // Rows for many turns of every SM: one block of 16 warps to an SM, so that it lays x out once, four warps
-    // to whole rows. Where x does not fit beside their rings, slices of K, and more rows to each of the
-    // cluster's barriers as long as every cluster has four turns.
-    a.warps = 16;
-    while (a.slices < 8 && smem_of() > kLinSmemMost) slice(2 * a.slices);
+    // Rows for many turns of every SM: four warps to whole rows, and where x is large one block of 16 warps to an
+    // SM, so that it is laid out once. Where it does not fit beside their rings, shorter rings; then slices of
+    // K, with as many rows to each of the cluster's barriers as leave every cluster four turns.
+    if (smem_of() > kLinSmem) a.warps = 16;
+    if (smem_of() > kLinSmemMost) a.stages = 2;
+    if (smem_of() > kLinSmemMost) a.buffers = 1;
+    while (a.slices < 8 && smem_of() > kLinSmemMost) a.buffers = 2, slice(2 * a.slices);
     if (smem_of() > kLinSmemMost) {  // the longest K
-      a.tokens = 8, groups = (static_cast<int64_t>(M) + 7) / 8;
+      a.tokens = 8, a.warps = 8, groups = (static_cast<int64_t>(M) + 7) / 8;
+    }
+    if (a.slices > 1) {  // a cluster needs both buffers
+      a.stages = 3;
+      if (smem_of() > kLinSmemMost) a.stages = 2;
     }
     a.across = a.slice >= 8 ? 4 : 1;
     if (a.slices > 1)
@@ -441,6 +477,9 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
       a.tokens = 8, groups = (static_cast<int64_t>(M) + 7) / 8;
     }
     while (a.warps > 2 && blocks() * groups * a.slices < sms) a.warps /= 2;
+    // SMs idle all the same: more warps to a row tile, as long as each has a stage
+    while (a.warps < 16 && a.slice > 2 * a.across && blocks() * groups * a.slices < sms && smem_of() * 2 < kLinSmemMost)
+      a.warps *= 2, a.across *= 2;
   }
   const size_t smem = smem_of();
   MOE_CHECK(groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
@@ -448,7 +487,6 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
   const int64_t at_once = (a.warps > 8 || kLinSmemSm / (smem + 1024) < 2 ? 1 : 2) * sms / a.slices;
   const dim3 grid(static_cast<unsigned>((blocks() < at_once ? blocks() : at_once) * a.slices), static_cast<unsigned>(groups));
   cudaStream_t s = as_stream(stream);
-  const int align = K % 256 == 0 ? kAlign256 : K % 32 == 0 ? kAlign32 : kAlign16;
   if (a.tokens <= 8)
     return align == kAlign256  ? launch_linear<1, kAlign256>(a, grid, smem, s)
            : align == kAlign32 ? launch_linear<1, kAlign32>(a, grid, smem, s)

@@ -194,6 +194,29 @@ def test_linear_activations(act, M, N, K):
     check_linear(run_linear(*c, act), *c, act)
 
 
+@pytest.mark.parametrize("act", ["identity", "swiglu"])
+@pytest.mark.parametrize("M,N,K,mode", [(15, 44008, 4672, "group"), (16, 40016, 4720, None), (8, 50010, 1040, "token"),
+                                        (4, 30002, 8208, None), (12, 60000, 256, None), (1, 39000, 2048, "group"),
+                                        (20, 41000, 512, None)])
+def test_linear_many_rows(M, N, K, mode, act):
+    """Matrices of many turns per SM: every kind of row alignment, and x from small to more than an SM holds.
+    A sample of the columns, the first and last tiles among them, is compared."""
+    x, scale, data, sf, alpha = linear_case(M, N, K, mode)
+    got = run_linear(x, scale, data, sf, alpha, act)
+    n_out = N // 2 if act == "swiglu" else N
+    cols = np.unique(np.r_[0:20, n_out - 20:n_out, np.random.default_rng(1).integers(0, n_out, 400)])
+    rows = np.r_[cols, cols + n_out] if act == "swiglu" else cols
+    check_linear(got[:, torch.from_numpy(cols).to(DEV)], x, scale, data[rows], sf[rows], alpha, act)
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 300, 65536), (9, 40, 65520), (2, 33, 40000), (16, 20000, 32784)])
+def test_linear_longest_k(M, N, K):
+    x, scale, data, sf, alpha = linear_case(M, N, K, None)
+    got = run_linear(x, scale, data, sf, alpha)
+    cols = np.unique(np.r_[0:min(N, 20), max(N - 20, 0):N, np.random.default_rng(1).integers(0, N, 60)])
+    check_linear(got[:, torch.from_numpy(cols).to(DEV)], x, scale, data[cols], sf[cols], alpha)
+
+
 def test_linear_row_stride_and_no_rows():
     x, scale, data, sf, alpha = linear_case(5, 60, 256, None)
     wide = torch.full((5, 256 + 40), float("nan"), dtype=torch.bfloat16, device=DEV)
