@@ -76,8 +76,8 @@ typedef enum {
 
 /* Bits OR-ed into *dev_status by the kernels. */
 #define MOE_DEV_DUPLICATE_EXPERT 1 /* a token names the same local expert twice ([CUDNN] "distinct experts") */
-#define MOE_DEV_TIMEOUT 2          /* a bounded wait in a GEMM kernel gave up after 2 s; the kernel
-                                      abandoned its remaining tiles and returned (outputs undefined) */
+#define MOE_DEV_TIMEOUT 2          /* a bounded wait in a GEMM or attention kernel gave up after 2 s; the
+                                      kernel abandoned its remaining tiles and returned (outputs undefined) */
 #define MOE_DEV_BAD_INDEX 4        /* a cache slot, page id or sequence length outside the cache; what it
                                       names is skipped */
 
@@ -405,8 +405,8 @@ MOE_API moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ld_x, const uint
  *   activation moe_activation_t. The gated kinds take w rows [gate; up] (N even) and write N/2
  *              columns; MOE_ACT_IDENTITY is a plain product
  *   out        [M, N] (gated: [M, N/2]) BF16, contiguous: FP32 sums, one rounding at the end
- * K % 16 == 0, 16 <= K <= 65536, N >= 1. Rows of w are read in 16-byte pieces when K % 32 == 0
- * and in 8-byte pieces otherwise. Any M; M <= 16 is what it is made for. M == 0 is a no-op.
+ * K % 16 == 0, 16 <= K <= 65536, 1 <= N <= 2^30; K % 256 == 0 is fastest. Any M; M <= 16 is what it
+ * is made for. M == 0 is a no-op.
  * ---------------------------------------------------------------------------------------- */
 MOE_API moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode,
                                     int32_t M, int32_t K, const uint8_t* w, const uint8_t* w_sf, const float* alpha,

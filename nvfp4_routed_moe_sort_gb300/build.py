@@ -1,10 +1,11 @@
-"""Builds libmoe_nvfp4.so (the product library) and libmoe_nvfp4_test.so (the test build)
-in-tree with nvcc for sm_103a.
+"""Builds libmoe_nvfp4.so (the product library), libmoe_nvfp4_test.so (the test build) and the
+Python module _native in-tree, with nvcc for sm_103a and g++.
 
 Each .cu file compiles to an object in parallel. The product library links the objects of
 csrc/*.cu (CUDA runtime linked statically); the test library links the same objects plus
 those of csrc/testbuild/*.cu, the entry points of include/moe_nvfp4_test.h, which only
-tests load. The build is skipped when both libraries are newer than every source.
+tests load. _native (csrc/binding/native.cpp, against the installed torch's headers) calls the
+product library beside it. The build is skipped when all three are newer than every source.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 TESTBUILD = os.path.join(CSRC, "testbuild")
 LIB = os.path.join(PKG, "libmoe_nvfp4.so")
 TEST_LIB = os.path.join(PKG, "libmoe_nvfp4_test.so")
+BINDING = os.path.join(CSRC, "binding")
+NATIVE = os.path.join(PKG, "_native.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -47,14 +51,15 @@ def test_sources() -> list[str]:
 def _deps() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if os.path.isfile(os.path.join(CSRC, f))]
     files += [os.path.join(TESTBUILD, f) for f in os.listdir(TESTBUILD)]
+    files += [os.path.join(BINDING, f) for f in os.listdir(BINDING)]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return files
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(TEST_LIB)):
+    if not all(os.path.exists(f) for f in (LIB, TEST_LIB, NATIVE)):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TEST_LIB))
+    t = min(os.path.getmtime(f) for f in (LIB, TEST_LIB, NATIVE))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -75,9 +80,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout, r.stderr)
         return obj
 
+    def compile_binding() -> str:
+        import torch
+        base = os.path.dirname(torch.__file__)
+        obj = os.path.join(BUILD, "native.o")
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", "-I", sysconfig.get_paths()["include"],
+               "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               "-I", os.path.join(cuda, "include"), "-I", INCLUDE, "-c", os.path.join(BINDING, "native.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for the _native module:\n{r.stdout}\n{r.stderr}")
+        return obj
+
     product, extra = sources(), test_sources()
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, product + extra))
+        native_obj = binding.result()
     prod_objs, test_objs = objs[:len(product)], objs[len(product):]
 
     def link(out: str, objects: list[str]):
@@ -90,6 +110,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     link(LIB, prod_objs)
     link(TEST_LIB, prod_objs + test_objs)
+    import torch
+    tmp = NATIVE + ".tmp"
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    r = subprocess.run(["g++", "-shared", "-o", tmp, native_obj, "-L", PKG, "-lmoe_nvfp4", "-Wl,-rpath,$ORIGIN", "-L", libs,
+                        "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {NATIVE} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
     return LIB
 
 

@@ -623,6 +623,7 @@ extern "C" moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const uint16_
                 !overlaps(k_seen, sb, v_new, vb) && !overlaps(v_seen, sb, k_new, kb) && !overlaps(v_seen, sb, v_new, vb),
             MOE_ERR_OVERLAP);
   const int64_t blocks = static_cast<int64_t>(N) * (width / kBlock);
+  MOE_CHECK(blocks < (int64_t(1) << 31) * kAppendThreads - kAppendThreads, MOE_ERR_UNSUPPORTED_SHAPE);
   return launch_pdl(kv_append_kernel, dim3(static_cast<unsigned>((blocks + kAppendThreads - 1) / kAppendThreads), 2),
                     dim3(kAppendThreads), 0, as_stream(stream), c, k_new, ld_k, v_new, ld_v, slots,
                     static_cast<int>(N), k_seen, v_seen, dev_status);

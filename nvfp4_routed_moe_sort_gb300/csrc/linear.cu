@@ -422,7 +422,7 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
   MOE_CHECK(activation >= MOE_ACT_SWIGLU && activation <= MOE_ACT_IDENTITY, MOE_ERR_INVALID_ARGUMENT);
   const bool gated = activation == MOE_ACT_SWIGLU || activation == MOE_ACT_GEGLU;
   MOE_CHECK(!gated || N % 2 == 0, MOE_ERR_INVALID_ARGUMENT);
-  MOE_CHECK(K % kBlock == 0 && K <= 65536, MOE_ERR_UNSUPPORTED_SHAPE);
+  MOE_CHECK(K % kBlock == 0 && K <= 65536 && N <= (1 << 30), MOE_ERR_UNSUPPORTED_SHAPE);
   if (M == 0) return MOE_OK;
   const bool fp8 = x_scale_mode != MOE_FP8_NONE;
   MOE_CHECK(x && w && w_sf && alpha && out && fp8 == (x_scale != nullptr), MOE_ERR_INVALID_ARGUMENT);

@@ -228,10 +228,11 @@ __global__ void __launch_bounds__(ITEMS > 2 ? 512 : 1024) norm_kernel(NormArgs a
       if ((lane & 15) == 0 && col + 8 * lane < a.H)
         a.scale[m * a.groups + (col + 8 * lane) / MOE_FP8_GROUP] = top == 0.0f ? 1.0f : __fdiv_rn(top, 448.0f);
     }
-    const float inv = top == 0.0f ? 1.0f : __fdiv_rn(448.0f, top);
+    const float up = top < 0x1p-64f ? 0x1p64f : 1.0f;  // exact, and keeps 448 / amax finite
+    const float inv = top == 0.0f ? 1.0f : __fdiv_rn(448.0f, top * up);
     float t[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = __fmul_rn(h[i][e], inv);
+    for (int e = 0; e < 8; ++e) t[e] = __fmul_rn(h[i][e] * up, inv);
     store_fp8<V>(a.y8 + out + col, make_uint2(e4m3x2(t[0], t[1]) | e4m3x2(t[2], t[3]) << 16,
                                               e4m3x2(t[4], t[5]) | e4m3x2(t[6], t[7]) << 16),
                  turn, lane, a.H - col);

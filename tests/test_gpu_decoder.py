@@ -483,6 +483,66 @@ def test_attend_writes_nothing_else():
     assert torch.equal(again[0], ref[0])
 
 
+def test_the_c_entry_points_by_name():
+    """The ctypes calls of the C names give what the torch layer gives."""
+    x, res, w = norm_case(5, 256, True, "group")
+    ref = pkg.add_rms_norm(x, w, res, fp8="group")
+    got = [torch.empty_like(t) for t in ref]
+    pkg.moe_add_rmsnorm(x, res, w, 1e-6, pkg.MOE_FP8_PER_GROUP, *got)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(ref, got))
+    x, scale, data, sf, alpha = linear_case(5, 64, 256, "group")
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)  # noqa: E731
+    out = torch.empty(5, 64, dtype=torch.bfloat16, device=DEV)
+    pkg.moe_linear_fp4(x, up(scale), pkg.MOE_FP8_PER_GROUP, up(data), up(sf), torch.tensor([alpha], device=DEV),
+                       pkg.MOE_ACT_IDENTITY, out)
+    assert torch.equal(out, run_linear(x, scale, data, sf, alpha))
+    lens = [3, 700]
+    a, b = Pool(50, 16, 2, 64), Pool(50, 16, 2, 64)
+    table, ln, _ = sequences(a, lens)
+    for s, d in zip(a.t, b.t):
+        d.copy_(s)
+    k, v = queries(2, 1, 2, 64, seed=4)[:, 0], queries(2, 1, 2, 64, seed=5)[:, 0]
+    slots = torch.tensor([int(table[0, 0]) * 16 + 2, int(table[1, 43]) * 16 + 11], device=DEV)
+    a.kv.append(k, v, slots)
+    pkg.moe_kv_append(b.kv.c, k, v, slots, None, None, b.status)
+    assert all(torch.equal(s, d) for s, d in zip(a.t, b.t))
+    q = queries(2, 1, 8, 64)
+    ref = a.kv.attend(q, table, ln)
+    out, lse = torch.empty_like(ref[0]), torch.empty_like(ref[1])
+    n = pkg.moe_kv_attend_workspace_bytes(b.kv.c, 2, 1, 8, table.shape[1])
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV) if n else None
+    pkg.moe_kv_attend(b.kv.c, q, 8 * 64, table, ln, 0.125, out, lse, ws, b.status)
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_empty_batches_tables_and_caches():
+    p = Pool(4, 16, 2, 64)
+    q = queries(2, 1, 4, 64)
+    none = torch.empty(2, 0, dtype=torch.int32, device=DEV)
+    for lens, status in (([0, 0], 0), ([5, 0], pkg.MOE_DEV_BAD_INDEX)):   # no page at all for a length above 0
+        out, lse = p.kv.attend(q, none, torch.tensor(lens, dtype=torch.int32, device=DEV))
+        assert (out == 0).all() and torch.isneginf(lse).all() and int(p.status[0]) == status
+    out, lse = p.kv.attend(q[:0], none[:0], torch.empty(0, dtype=torch.int32, device=DEV))
+    assert out.shape == (0, 1, 4, 64) and lse.shape == (0, 1, 4)
+    empty = pkg.NVFP4KVCache.allocate(0, 16, 2, 64, DEV)
+    table = torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+    out, lse = empty.attend(q, table, torch.tensor([40, 1], dtype=torch.int32, device=DEV))
+    assert (out == 0).all() and torch.isneginf(lse).all() and int(empty.dev_status[0]) == pkg.MOE_DEV_BAD_INDEX
+
+
+def test_norm_of_subnormal_rows_stays_finite():
+    x = torch.zeros(3, 256, dtype=torch.bfloat16, device=DEV)
+    x[0, ::2] = 2.0 ** -130
+    x[1, 5] = 2.0 ** -126
+    w = torch.full((256,), 2.0 ** -4, dtype=torch.bfloat16, device=DEV)
+    for fp8 in ("token", "group"):
+        y, _, y8, scale = pkg.add_rms_norm(x, w, fp8=fp8)
+        assert all(torch.isfinite(t.float()).all() for t in (y, y8, scale)) and (scale >= 0).all()
+        want = x.double() / np.sqrt(1e-6) * 2.0 ** -4
+        # scales this small are subnormal: a few bits are left of them
+        assert (y8.double() * scale[:, :1].double() - want).abs().max() <= want.abs().max() * 0.25
+
+
 def test_operators_run_on_the_callers_stream_and_in_a_graph():
     """One decode step (norm, projection, append, attention) captured, then replayed on new values."""
     H, Hkv, G, Dh, page = 256, 2, 2, 64, 16
