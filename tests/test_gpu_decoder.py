@@ -388,6 +388,42 @@ def test_attend_long(B, Hkv, G, T, Dh, page, n):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("B,Hkv,G,T,Dh,page,n", [(20, 16, 4, 1, 128, 64, 4300), (22, 14, 4, 2, 64, 16, 5000), (1, 8, 8, 1, 128, 32, 70000),
+                                               (1, 24, 3, 1, 64, 128, 33333), (300, 2, 1, 1, 128, 256, 2600)])
+def test_attend_long_runs(B, Hkv, G, T, Dh, page, n):
+    """Blocks that walk long runs (four 16-token runs a step), over caches of random bytes whose free places
+    hold no numbers; a sample of the sequences and heads is compared."""
+    r = np.random.default_rng(n)
+    lens = [n] + [int(v) for v in r.integers(0, n + 1, B - 1)]
+    if B > 3:
+        lens[1], lens[2], lens[3] = 0, 1, 17
+    used = [-(-m // page) for m in lens]
+    p = Pool(sum(used) + 1, page, Hkv, Dh)
+    for i in (0, 2):
+        p.t[i].copy_(torch.randint(0, 256, p.t[i].shape, device=DEV).to(torch.uint8))
+        p.t[i + 1].copy_(torch.randint(0x20, 0x38, p.t[i + 1].shape, device=DEV).to(torch.uint8))
+    order = r.permutation(p.pages)
+    table, at = np.full((B, max(used)), -1, np.int32), 0
+    for b, m in enumerate(used):
+        table[b, :m] = order[at:at + m]
+        at += m
+        if lens[b] % page:
+            for i in (1, 3):
+                p.t[i][int(table[b, m - 1]), :, lens[b] % page:] = 0x7F
+    q = queries(B, T, Hkv * G, Dh, size=1.0)
+    out, lse = p.kv.attend(q, torch.from_numpy(table).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+    assert int(p.status[0]) == 0 and torch.isfinite(out.float()).all()
+    again = p.kv.attend(q, torch.from_numpy(table).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    for b in {0, min(1, B - 1), min(2, B - 1), min(3, B - 1), *(int(v) for v in r.integers(0, B, 4))}:
+        h = int(r.integers(0, Hkv))
+        pages = torch.from_numpy(table[b, :used[b]]).long().to(DEV)
+        k, v = (D.nvfp4_values(to_np(p.t[i][pages, h].flatten(0, 1))[:lens[b]], to_np(p.t[i + 1][pages, h].flatten(0, 1))[:lens[b]])
+                for i in (0, 2))
+        sl = slice(h * G, (h + 1) * G)
+        check_attend(out[b:b + 1, :, sl], lse[b:b + 1, :, sl], q[b:b + 1, :, sl], [(k[:, None], v[:, None])], 1, Dh ** -0.5)
+
+
 def test_attend_spikes_far_scores_and_large_queries():
     """One score far above a long tail, scores of both signs past any exponent's range, zero queries."""
     lens, page, Dh = [3000, 3000, 3000, 3000], 64, 128
