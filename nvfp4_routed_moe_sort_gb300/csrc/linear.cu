@@ -73,13 +73,13 @@ __device__ __forceinline__ float activate(int act, float g, float u) {
   }
 }
 
-// N bytes of global memory into shared memory, asynchronously; fewer `bytes` leave zeros behind them
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from, uint32_t bytes = N) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N), "r"(bytes) : "memory");
+// 16 bytes of global memory into shared memory, asynchronously and past L1; fewer `bytes` leave zeros
+// behind them
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -140,64 +140,65 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   const int64_t rows = static_cast<int64_t>(a.gated ? 2 : 1) * a.n_out;
   const uint8_t* const w_end = a.w + rows * row_bytes;
   const uint8_t* const sf_end = a.sf + rows * sf_bytes;
-  const uint8_t *w_from, *w_ninth = nullptr, *sf_from;  // this lane's pieces of the next stage
-  bool sf_mine;
-  int64_t behind;  // bytes of the matrix from the tile's last row on
-  int load_block = blockIdx.x / a.slices, load_ch = first, load_rows;
-  auto rows_of = [&] {
-    const int64_t n = static_cast<int64_t>(load_block) * n_per + i0;
-    load_rows = load_block < blocks ? static_cast<int>(min(static_cast<int64_t>(a.n_out) - n, int64_t(16))) : 0;
-    const int64_t row = n + (up ? a.n_out : 0);
-    behind = (rows - row - 15) * row_bytes;
-    const int64_t at = static_cast<int64_t>(chunk0 + first) * (kLinChunk / 2);
-    const int64_t mine = (row + q) * row_bytes;
-    w_from = a.w + mine + at + 16 * p - (ALIGN == kAlign16 ? mine & 8 : 0);
-    if constexpr (ALIGN == kAlign16) {
-      const int64_t ninth = (row + lane) * row_bytes;  // of lanes below 16, where the row starts inside a piece
-      w_ninth = lane < 16 && (ninth & 8) ? a.w + ninth + at + 120 : nullptr;
-    }
-    const int64_t sf_at = (row + (lane >> 1)) * sf_bytes;
-    sf_mine = (lane & 1) == 0 || (ALIGN != kAlign256 && (sf_at & 15) != 0);
-    sf_from = a.sf + (sf_at & ~int64_t(15)) + at / 8 + 16 * (lane & 1);
-  };
+  // The tile to load next: its first column, its rows, and this lane's pieces of its first stage; the pieces
+  // of the stage to load next. Tiles are 16 * so many rows apart, so that where a row starts in a
+  // piece is the same for all of them.
+  int load_col = static_cast<int>(blockIdx.x / a.slices) * n_per + i0, load_ch = first;
+  const int64_t row_first = load_col + (up ? a.n_out : 0);
+  const int64_t k_at = static_cast<int64_t>(chunk0 + first) * (kLinChunk / 2);
+  const int64_t w_at = (row_first + q) * row_bytes, sf_at = (row_first + (lane >> 1)) * sf_bytes;
+  const int64_t w_step = static_cast<int64_t>(stride) * n_per * row_bytes, sf_step = static_cast<int64_t>(stride) * n_per * sf_bytes;
+  const uint8_t* w_tile = a.w + w_at + k_at + 16 * p - (ALIGN == kAlign16 ? w_at & 8 : 0);
+  const uint8_t* sf_tile = a.sf + (sf_at & ~int64_t(15)) + k_at / 8 + 16 * (lane & 1);
+  const bool sf_mine = (lane & 1) == 0 || (ALIGN != kAlign256 && (sf_at & 15) != 0);
+  // a ninth piece of row `lane`'s codes, where it starts inside one
+  const bool ninth = ALIGN == kAlign16 && lane < 16 && (((row_first + lane) * row_bytes) & 8) != 0;
+  const int64_t to_ninth = (static_cast<int64_t>(lane) * row_bytes + 120) - (w_tile - (a.w + row_first * row_bytes + k_at));
+  const uint8_t *w_from = w_tile, *sf_from = sf_tile;
+  // a tile is whole, 16 rows and every piece of them inside the matrix, up to this column
+  const int past_rows = static_cast<int>((static_cast<int64_t>(chunk0 + last + 2) * (kLinChunk / 2) + row_bytes - 1) / row_bytes);
+  const int whole_to = static_cast<int>(min(rows - (up ? a.n_out : 0) - 15 - past_rows, static_cast<int64_t>(a.n_out) - 16));
   auto left = [](const uint8_t* from, const uint8_t* end) {
     return static_cast<uint32_t>(max(min(end - from, static_cast<ptrdiff_t>(16)), static_cast<ptrdiff_t>(0)));
   };
   auto load_stage = [&](int stage) {
     const uint32_t at = ring + stage * kStage;
-    if (load_ch < last && load_rows > 0) {
-      if (load_rows == 16 && (chunk0 + load_ch + 2) * (kLinChunk / 2) <= behind) {
+    if (load_ch < last && load_col < a.n_out) {
+      if (load_col <= whole_to) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) copy_async<16>(at + to + i * 4 * kRow, w_from + i * 4 * row_bytes);
-        if (ALIGN == kAlign16 && w_ninth) copy_async<16>(at + lane * kRow + 128, w_ninth, left(w_ninth, w_end));
-        if (sf_mine) copy_async<16>(at + sf_to, sf_from, ALIGN == kAlign256 ? 16 : left(sf_from, sf_end));
+        for (int i = 0; i < 4; ++i) copy_async(at + to + i * 4 * kRow, w_from + i * 4 * row_bytes);
+        if (ninth) copy_async(at + lane * kRow + 128, w_from + to_ninth);
+        if (ALIGN == kAlign256) {
+          if (sf_mine) copy_async(at + sf_to, sf_from);
+        } else if (sf_mine) {
+          copy_async(at + sf_to, sf_from, left(sf_from, sf_end));
+        }
       } else {
+        const int load_rows = min(a.n_out - load_col, 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint8_t* const from = w_from + i * 4 * static_cast<int64_t>(row_bytes);
           const uint32_t n = q + 4 * i < load_rows ? left(from, w_end) : 0;
-          copy_async<16>(at + to + i * 4 * kRow, n ? from : a.w, n);
+          copy_async(at + to + i * 4 * kRow, n ? from : a.w, n);
         }
-        if (ALIGN == kAlign16 && w_ninth) {
-          const uint32_t n = lane < load_rows ? left(w_ninth, w_end) : 0;
-          copy_async<16>(at + lane * kRow + 128, n ? w_ninth : a.w, n);
+        if (ninth) {
+          const uint32_t n = lane < load_rows ? left(w_from + to_ninth, w_end) : 0;
+          copy_async(at + lane * kRow + 128, n ? w_from + to_ninth : a.w, n);
         }
         if (sf_mine) {
           const uint32_t n = (lane >> 1) < load_rows ? left(sf_from, sf_end) : 0;
-          copy_async<16>(at + sf_to, n ? sf_from : a.sf, n);
+          copy_async(at + sf_to, n ? sf_from : a.sf, n);
         }
       }
     }
     copies_commit();
     load_ch += 2;
     w_from += kLinChunk, sf_from += 2 * kLinChunk / kBlock;
-    if (ALIGN == kAlign16 && w_ninth) w_ninth += kLinChunk;
     if (load_ch >= last) {
-      load_ch = first, load_block += stride;
-      rows_of();
+      load_ch = first, load_col += stride * n_per;
+      w_from = w_tile += w_step, sf_from = sf_tile += sf_step;
     }
   };
-  rows_of();
   load_stage(0);
   if (a.stages == 3) load_stage(1);
 
@@ -265,19 +266,36 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   if (a.slices > 1) cluster_wait();
   const uint8_t* x_lane[NT];  // columns of no token repeat the last one and are dropped
 #pragma unroll
-  for (int t = 0; t < NT; ++t) x_lane[t] = xs + min(8 * t + r, M - 1) * x_row + c * 16;
+  for (int t = 0; t < NT; ++t) x_lane[t] = xs + min(8 * t + r, M - 1) * x_row + c * 16 + first * 256;
+  const float* const factor_lane = factor + first * 8 * NT + 2 * c;
+  // where rows r and r + 8 start in their first piece of codes, and of scales
+  int code_at = 0, scale_at[2] = {0, 0};
+  if constexpr (ALIGN != kAlign256) {
+    if (ALIGN == kAlign16) code_at = ((row_first + r) * row_bytes) & 8;
+    scale_at[0] = ((row_first + r) * sf_bytes) & 15, scale_at[1] = ((row_first + r + 8) * sf_bytes) & 15;
+  }
+  // Sums [part of K][kind][column of the owner's share][token], in the owner's shared memory: where this lane's
+  // go. What meets at the barrier is the cluster, or the warps of one tile (and of its up rows), which
+  // then add the tile's columns.
+  int sum_at[2], owner[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int col = i0 + r + 8 * h;
+    owner[h] = col / share;
+    sum_at[h] = (((rank * a.across + part) * kinds + (up ? 1 : 0)) * share + col - owner[h] * share) * kSumRow + 2 * c;
+  }
+  const int own = tiles / kinds, group = tile % own;
+  const int cols = a.slices > 1 ? share : 16, at_col = a.slices > 1 ? 0 : group * 16;
+  const int member = a.slices > 1 ? tid : ((tile / own) * a.across + part) * 32 + lane;
+  const int members = a.slices > 1 ? threads : a.across * kinds * 32;
+  const int m_member = member / cols, col_member = at_col + member - m_member * cols;
   int stage = 0;
   for (int block = blockIdx.x / a.slices; block < blocks; block += stride) {
     float acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-    // where rows r and r + 8 start in their first piece of codes, and of scales
-    int code_at = 0, scale_at[2] = {0, 0};
-    if constexpr (ALIGN != kAlign256) {
-      const int64_t row = static_cast<int64_t>(block) * n_per + i0 + (up ? a.n_out : 0) + r;
-      if (ALIGN == kAlign16) code_at = (row * row_bytes) & 8;
-      scale_at[0] = (row * sf_bytes) & 15, scale_at[1] = ((row + 8) * sf_bytes) & 15;
-    }
+    const float* scale_of = factor_lane;
+    int x_at = 0;
     for (int ch0 = first; ch0 < last; ch0 += 2) {
       if (a.stages == 3) copies_wait<1>();
       else copies_wait<0>();
@@ -322,7 +340,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const uint4 x = *reinterpret_cast<const uint4*>(x_lane[t] + ch * 256 + j * 64);
+            const uint4 x = *reinterpret_cast<const uint4*>(x_lane[t] + x_at + u * 256 + j * 64);
             const uint32_t b[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -334,21 +352,19 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float2 s = *reinterpret_cast<const float2*>(factor + (ch * NT + t) * 8 + 2 * c);
+          const float2 s = *reinterpret_cast<const float2*>(scale_of + (u * NT + t) * 8);
           acc[t][0] += sum[t][0] * s.x, acc[t][1] += sum[t][1] * s.y;
           acc[t][2] += sum[t][2] * s.x, acc[t][3] += sum[t][3] * s.y;
         }
       }
+      x_at += 512, scale_of += 16 * NT;
       if (++stage == a.stages) stage = 0;
     }
 
-    // sums [part of K][kind][column of the owner's share][token], in the owner's shared memory
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int col = i0 + r + 8 * h, owner = col / share;
-      float* const to_sum =
-          sums + (((rank * a.across + part) * kinds + (up ? 1 : 0)) * share + col - owner * share) * kSumRow + 2 * c;
-      const uint32_t to_cluster = a.slices > 1 ? cluster_address(to_sum, owner) : 0;
+      float* const to_sum = sums + sum_at[h];
+      const uint32_t to_cluster = a.slices > 1 ? cluster_address(to_sum, owner[h]) : 0;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -357,36 +373,33 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
           else to_sum[8 * t + i] = acc[t][2 * h + i];
         }
     }
-    // What meets at the barrier: the cluster, or the warps of one tile (and of its up rows), which then
-    // add the tile's columns
-    int at_col = 0, cols = share, member = tid, members = threads;
     if (a.slices > 1) {
       cluster_arrive();
       cluster_wait();
     } else {
-      const int own = tiles / kinds, group = tile % own;
-      at_col = group * 16, cols = 16;
-      member = ((tile / own) * a.across + part) * 32 + lane, members = a.across * kinds * 32;
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(members) : "memory");
     }
-    for (int i = member; i < cols * M; i += members) {
-      const int m = i / cols, col = at_col + i - m * cols;
-      const int64_t n = static_cast<int64_t>(block) * n_per + rank * share + col;
-      if (n >= a.n_out) continue;
-      float y[2] = {0.0f, 0.0f};
-      for (int s = 0; s < parts; ++s) {
-        y[0] += sums[(s * kinds * share + col) * kSumRow + m];
-        if (a.gated) y[1] += sums[((s * 2 + 1) * share + col) * kSumRow + m];
+    const int left_cols = a.n_out - (block * n_per + rank * share);
+    for (int i = member, m = m_member, col = col_member; i < cols * M;) {
+      if (col < left_cols) {
+        const float* at = sums + col * kSumRow + m;
+        float y[2] = {0.0f, 0.0f};
+        for (int s = 0; s < parts; ++s) {
+          y[0] += *at, at += share * kSumRow;
+          if (a.gated) y[1] += *at, at += share * kSumRow;
+        }
+        a.out[static_cast<int64_t>(m0 + m) * a.n_out + block * n_per + rank * share + col] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0] * alpha, y[1] * alpha)));
       }
-      a.out[static_cast<int64_t>(m0 + m) * a.n_out + n] =
-          __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0] * alpha, y[1] * alpha)));
+      i += members;
+      if (i < cols * M) m = i / cols, col = at_col + i - m * cols;
     }
     if (a.buffers == 2) {  // the other buffer is free: what it held was added before the barrier above
       float* const t = sums;
       sums = sums_next;
       sums_next = t;
     } else {
-      asm volatile("bar.sync %0, %1;" ::"r"(tile % (tiles / kinds) + 1), "r"(members) : "memory");
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(members) : "memory");
     }
   }
 }
