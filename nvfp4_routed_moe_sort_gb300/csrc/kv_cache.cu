@@ -99,6 +99,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 // FP16 for the second product (11 significant bits down to 2^-29 of the largest weight), its
 // sum is FP32. Query rows are scaled by a power of two to a largest value in [2^14, 2^15) so
 // that BF16's exponents fit FP16.
+//
+// Bound by the conversion (ALU pipe 55 %, issue slots 60 % in use; 17.5 instructions per token and kv head), not by
+// HBM: 64 sequences of 4000 to 8191 tokens, 8 kv heads, 86 us (5.1 TB/s; the copies alone 73 us), one of
+// 131071 tokens 34 us. Short ones by the chain of length, pages, first copies, two steps and the join.
 constexpr int kAttWarps = 4;
 constexpr int kAttStages = 2;
 constexpr float kPShift = 15.0f;
