@@ -449,7 +449,8 @@ typedef struct {
  *                 for each token, bf16(code * (scale / g)), for callers that go on with the values
  *                 later steps will see; written for tokens without a slot too
  *   dev_status    may be NULL
- * N == 0 is a no-op.
+ * N == 0 is a no-op. The cache holds no infinities and no NaN: an infinite value becomes the largest
+ * one of its block's scale, a NaN some finite one.
  * ---------------------------------------------------------------------------------------- */
 MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const uint16_t* k_new, int64_t ld_k,
                                    const uint16_t* v_new, int64_t ld_v, const int64_t* slots, int32_t N,

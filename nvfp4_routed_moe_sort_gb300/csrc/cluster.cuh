@@ -16,13 +16,6 @@ __device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank
 __device__ __forceinline__ void store_cluster(uint32_t at, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
-__device__ __forceinline__ void store_cluster(uint32_t at, float2 v) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
-}
-__device__ __forceinline__ void store_cluster(uint32_t at, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
-}
 
 // Whole warps only. Every block of the cluster arrives at every barrier that one of them waits at.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }

@@ -1,8 +1,9 @@
 // FP4 operands on mma.m16n8k16 (FP16 in, FP32 sums): the conversions and instructions that the
 // dense linear and the cache's attention share. Both read each 4-bit value once, for at most 16
-// tokens or query rows, and are bound by HBM; the legacy warp-level MMA takes its operands from
-// registers, where the codes are converted, and its rate is not what limits them. An E2M1 code
-// times an E4M3 scale has 6 significant bits between 2^-10 and 2688: exact in FP16.
+// tokens or 32 query rows, and convert it in registers, where the legacy warp-level MMA takes its
+// operands from. Per two values that is one conversion and one multiplication by the scale, either at
+// half rate; the MMA pipe itself is busy a quarter of the time. An E2M1 code times an E4M3 scale
+// has 6 significant bits between 2^-10 and 2688: exact in FP16.
 #pragma once
 
 #include "common.cuh"

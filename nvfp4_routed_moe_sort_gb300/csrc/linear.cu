@@ -1,6 +1,6 @@
 // A few tokens times one dense NVFP4 matrix: y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]).
 //
-// Bound by HBM: 9/16 byte per weight, read once per 16 tokens. A warp takes 16 rows of w and a run
+// 9/16 byte per weight, read once per 16 tokens: bound by the weights' conversion, close behind it by HBM. A warp takes 16 rows of w and a run
 // of K: mma.m16n8k16 with the 16 weight rows as one operand and eight tokens as the other. K
 // goes by chunks of 128 values. In a chunk lane (r, c) = (lane / 4, lane % 4) holds the values 32c
 // to 32c + 31 of rows r and r + 8, and MMA step j takes its values 32c + 4j to 32c + 4j + 3.
@@ -17,7 +17,7 @@
 //
 // Two ways of sharing K. Warps of one block (`across` of them) take neighbouring runs of the same
 // rows, so that a block reads whole rows: DRAM gives 128 rows at a time read along K 4.8 TB/s, whole
-// rows 5.9 (302 MB, read alone). Blocks of a cluster take slices of K where there are too few
+// rows 5.9 (264 MB, read alone). Blocks of a cluster take slices of K where there are too few
 // rows for the SMs, or too much x for shared memory. A row's sums belong to one block: the
 // others store theirs into its shared memory, and after one barrier it adds all in a fixed order, so
 // results do not depend on timing. alpha, the activation and the BF16 rounding come once at the
@@ -481,7 +481,8 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
       a.stages = 3;
       if (smem_of() > kLinSmemMost) a.stages = 2;
     }
-    a.across = a.slice >= 8 ? 4 : 1;
+    // The tiles of a block meet at barriers 1 to 8, so 16 warps are never 16 tiles.
+    a.across = a.slice >= 8 ? 4 : a.warps / 8;
     if (a.slices > 1)
       while (a.across > 1 && blocks() / 2 * a.slices >= 4 * sms) a.across /= 2;
   } else {

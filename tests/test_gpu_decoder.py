@@ -209,6 +209,18 @@ def test_linear_many_rows(M, N, K, mode, act):
     check_linear(got[:, torch.from_numpy(cols).to(DEV)], x, scale, data[rows], sf[rows], alpha, act)
 
 
+@pytest.mark.parametrize("act", ["identity", "geglu"])
+@pytest.mark.parametrize("M,N,K", [(16, 40006, 528), (40, 40006, 752), (16, 80010, 720)])
+def test_linear_short_unaligned_rows(M, N, K, act):
+    """Rows so short that a warp takes them whole, and so aligned that only one block of 16 warps fits an SM."""
+    x, scale, data, sf, alpha = linear_case(M, N, K, None)
+    got = run_linear(x, scale, data, sf, alpha, act)
+    n_out = N // 2 if act == "geglu" else N
+    cols = np.unique(np.r_[0:300, n_out - 300:n_out])
+    rows = np.r_[cols, cols + n_out] if act == "geglu" else cols
+    check_linear(got[:, torch.from_numpy(cols).to(DEV)], x, scale, data[rows], sf[rows], alpha, act)
+
+
 @pytest.mark.parametrize("M,N,K", [(16, 300, 65536), (9, 40, 65520), (2, 33, 40000), (16, 20000, 32784)])
 def test_linear_longest_k(M, N, K):
     x, scale, data, sf, alpha = linear_case(M, N, K, None)
