@@ -34,7 +34,7 @@
 namespace moe {
 namespace {
 
-constexpr int kLinWarps = 16;             // most warps of a block, 16 rows of w each
+constexpr int kLinWarps = 16;             // most warps of a block, and of an SM: 128 registers a thread
 constexpr int kLinTokens = 16;
 constexpr int kLinChunk = 128;            // = MOE_FP8_GROUP
 static_assert(kLinChunk == MOE_FP8_GROUP, "one E4M3 scale per chunk");
@@ -415,14 +415,104 @@ moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_
   return launch_clusters(linear_kernel<NT, ALIGN>, a.slices, grid, dim3(32 * a.warps), smem, s, a);
 }
 
-// shared memory of a block: two to an SM; the most of one; an SM's, 1 KB of it taken by each block
-constexpr size_t kLinSmem = 113 * 1024, kLinSmemMost = 227 * 1024, kLinSmemSm = 228 * 1024;
+// How a product is cut.
+struct LinCut {
+  int tokens, warps, across, slices, slice, stages, buffers;
+  int at_once;  // clusters that run at once
+  int64_t groups;
+};
 
-size_t linear_smem(const LinArgs& a, int align) {
-  const int columns = a.tokens > 8 ? 16 : 8;
-  return static_cast<size_t>(a.tokens) * (a.slice * kLinChunk * 2 + 64) + static_cast<size_t>(a.slice) * columns * 4 +
-         static_cast<size_t>(a.buffers) * 16 * a.warps * (columns + 1) * 4 +
-         static_cast<size_t>(a.warps) * a.stages * stage_bytes(align);
+constexpr int kLinSmem = 227 * 1024, kLinSmemSm = 228 * 1024;  // of a block; of an SM, 1 KB taken by each block
+
+int linear_smem(const LinCut& k, int align) {
+  const int columns = k.tokens > 8 ? 16 : 8;
+  return k.tokens * (k.slice * kLinChunk * 2 + 64) + k.slice * columns * 4 + k.buffers * 16 * k.warps * (columns + 1) * 4 +
+         k.warps * k.stages * stage_bytes(align);
+}
+
+// The cut whose estimated time is least, of blocks of 2 to 16 warps, 1 to 8 of them on the same rows, in clusters
+// of 1 to 8. The estimate (in us, less the launch) adds up what a block does:
+//   1.0    per round of a warp's loads of x (four for either half), 0.005 per token and chunk laid out on an SM;
+//   0.47   per turn (the sums), 0.7 more where a cluster meets; shared where an SM has several blocks and turns;
+//   a warp's chunks one after the other at 0.18 each, or all of an SM's at 0.024 (up to 8 tokens) or 0.038, the
+//   issue slots' rate, whichever is longer; 3 % more with a ring of two stages, and over several turns 23 % more
+//   where one warp takes a run of K alone and 13 % where two or three do (DRAM: whole rows 5.9 TB/s, one run 4.8).
+// Of that and the weights' bytes at 6 TB/s the longer counts, and a fifth of the shorter. Constants fitted to 61 shapes from
+// 1 x 200 x 8192 to 4 x 129021 x 4096 and 16 x 60000 x 7168, each timed in every cut: the cut chosen is on average 2 %
+// off the best of them (worst 12 %). Halving and doubling blocks and slices until they filled the SMs was 15 %
+// off (worst 52 %): 12 x 10240 x 7168 30.2 us against 21.6, 1 x 4096 x 4096 7.2 against 5.7.
+bool cut_linear(int64_t M, int K, int n_out, bool gated, int align, int sms, LinCut* cut) {
+  // warps and across: all of a block's to one tile of rows for little work, whole tiles for much
+  static constexpr signed char kBlocks[][2] = {{2, 2},  {3, 3},  {4, 1},  {4, 2},  {4, 4},  {5, 5},  {6, 1},  {6, 2},  {6, 3},
+                                               {7, 1},  {8, 1},  {8, 2},  {8, 4},  {8, 8},  {10, 1}, {10, 2}, {12, 1}, {12, 2},
+                                               {12, 3}, {12, 4}, {14, 1}, {14, 2}, {16, 1}, {16, 2}, {16, 4}, {16, 8}};
+  const int chunks = (K + kLinChunk - 1) / kLinChunk, kinds = gated ? 2 : 1;
+  const float copy = static_cast<float>(n_out) * kinds * K * (9.0f / 16) / 6e6f;
+  LinCut k;
+  k.tokens = static_cast<int>(M < kLinTokens ? M : kLinTokens);
+  float best = 0.0f;
+  bool found = false;
+  while (true) {
+    k.groups = (M + k.tokens - 1) / k.tokens;
+    const float unit = k.tokens > 8 ? 0.038f : 0.024f;
+    for (k.slices = 1; k.slices <= 8; k.slices *= 2) {
+      k.slice = ((chunks + k.slices - 1) / k.slices + 1) & ~1;  // whole stages
+      if ((k.slices - 1) * k.slice >= chunks) break;
+      const int pairs = k.tokens * (k.slice < chunks ? k.slice : chunks);
+      for (const auto& b : kBlocks) {
+        k.warps = b[0], k.across = b[1];
+        const int tiles = k.warps / k.across, n_per = (gated ? 8 : 16) * tiles;
+        if (tiles % kinds != 0 || n_per % k.slices != 0 || (k.across > 1 && 2 * k.across > k.slice + 1)) continue;
+        if (k.slices == 1 && tiles / kinds > 15) continue;  // a barrier for each, and one for all
+        k.stages = 3, k.buffers = 2;
+        int smem = linear_smem(k, align);
+        if (smem > kLinSmem) k.stages = 2, smem = linear_smem(k, align);
+        if (smem > kLinSmem && k.slices == 1) k.buffers = 1, smem = linear_smem(k, align);  // a cluster needs both
+        if (smem > kLinSmem) continue;
+        const int fit = kLinSmemSm / (smem + 1024), most = kLinWarps / k.warps, per_sm = fit < most ? fit : most;
+        // SMs that clusters of 4 and 8 leave over: 8 and 32 of 152 at one block to an SM, half to a quarter of that otherwise
+        const int odd = k.slices == 8 ? (per_sm == 1 ? 32 : 8) : k.slices == 4 ? (per_sm == 1 ? 8 : 4) : 0;
+        k.at_once = (sms - odd) * per_sm / k.slices;
+        if (k.at_once < 1) continue;
+        const int64_t blocks = (static_cast<int64_t>(n_out) + n_per - 1) / n_per * k.groups;
+        const int first = static_cast<int>(blocks < k.at_once ? blocks : k.at_once) * k.slices;
+        const int spread = sms - (k.slices == 8 ? 32 : k.slices == 4 ? 8 : 0);
+        const int on_sm = (first + spread - 1) / spread < per_sm ? (first + spread - 1) / spread : per_sm;
+        const float turns = static_cast<float>((blocks + k.at_once - 1) / k.at_once);
+        int run = ((k.slice + k.across - 1) / k.across + 1) & ~1;
+        run = run < chunks ? run : chunks;
+        const float ends = turns * (k.slices > 1 ? 1.17f : 0.47f);
+        const float alone = turns * 0.18f * run + ends;
+        const float shared = turns * unit * (on_sm * k.warps * run) * (k.stages == 2 ? 1.03f : 1.0f) +
+                             (turns > 1.0f ? ends / on_sm : ends);
+        const float rows = turns == 1.0f || k.across >= 4 ? 1.0f : k.across > 1 ? 1.13f : 1.23f;
+        const float work = (pairs + 8 * k.warps - 1) / (8 * k.warps) + 0.005f * (on_sm * pairs) + (alone > shared ? alone : shared) * rows;
+        const float time = work > copy ? work + 0.2f * copy : copy + 0.2f * work;
+        if (!found || time < best) found = true, best = time, *cut = k;
+      }
+    }
+    if (found || k.tokens <= 8) return found;
+    k.tokens = 8;  // the longest K: x of 16 tokens does not fit
+  }
+}
+
+// The estimates take 2 us of host time, so a thread keeps the cuts of the sizes it last asked for (a decoder's
+// handful); they follow from the sizes alone.
+bool cut_of(int64_t M, int K, int n_out, bool gated, int align, int sms, LinCut* cut) {
+  struct Kept {
+    int64_t M;
+    int K, n_out, gated, sms;
+    LinCut cut;
+  };
+  static thread_local Kept kept[64];
+  const uint64_t hash = (static_cast<uint64_t>(M) * 0x9E3779B97F4A7C15ull ^ static_cast<uint64_t>(K) << 32 ^ n_out) * 0x9E3779B97F4A7C15ull;
+  Kept& c = kept[hash >> 58];
+  if (c.M != M || c.K != K || c.n_out != n_out || c.gated != gated || c.sms != sms) {
+    if (!cut_linear(M, K, n_out, gated, align, sms, cut)) return false;
+    c = {M, K, n_out, gated, sms, *cut};
+  }
+  *cut = c.cut;
+  return true;
 }
 
 }  // namespace
@@ -446,64 +536,23 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
   MOE_CHECK(aligned16(x) && aligned16(x_scale) && aligned16(w) && aligned16(w_sf) && aligned16(alpha) &&
                 aligned16(out) && ld_x % (fp8 ? 16 : 8) == 0,
             MOE_ERR_MISALIGNED);
-  const int chunks = (K + kLinChunk - 1) / kLinChunk;
-  LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, gated ? N / 2 : N, activation,
-               x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, 1, chunks, kLinTokens, 8, 1, 3, 2, gated};
+  const int chunks = (K + kLinChunk - 1) / kLinChunk, n_out = gated ? N / 2 : N;
+  const int align = K % 256 == 0 ? kAlign256 : K % 32 == 0 ? kAlign32 : kAlign16;
+  LinCut cut;
+  MOE_CHECK(cut_of(M, K, n_out, gated, align, num_sms(), &cut) && cut.groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
+  const LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, n_out, activation,
+                     x_scale_mode == MOE_FP8_PER_GROUP ? chunks : 1, cut.slices, cut.slice, cut.tokens, cut.warps,
+                     cut.across, cut.stages, cut.buffers, gated};
   const size_t ob = static_cast<size_t>(M) * a.n_out * 2;
   MOE_CHECK(!overlaps(out, ob, x, (static_cast<size_t>(M - 1) * ld_x + K) * (fp8 ? 1 : 2)) &&
                 !overlaps(out, ob, w, static_cast<size_t>(N) * K / 2) &&
                 !overlaps(out, ob, w_sf, static_cast<size_t>(N) * K / kBlock) && !overlaps(out, ob, alpha, 4) &&
                 !overlaps(out, ob, x_scale, static_cast<size_t>(M) * a.x_groups * 4),
             MOE_ERR_OVERLAP);
-  const int align = K % 256 == 0 ? kAlign256 : K % 32 == 0 ? kAlign32 : kAlign16;
-  auto blocks = [&] {
-    const int64_t n_per = (gated ? 8 : 16) * (a.warps / a.across);
-    return (a.n_out + n_per - 1) / n_per;
-  };
-  const int64_t sms = num_sms();
-  a.tokens = M < kLinTokens ? M : kLinTokens;
-  int64_t groups = (static_cast<int64_t>(M) + a.tokens - 1) / a.tokens;
-  auto slice = [&](int n) { a.slices = n, a.slice = ((chunks + n - 1) / n + 1) & ~1; };  // whole stages
-  auto smem_of = [&] { return linear_smem(a, align); };
-  slice(1);
-  if (blocks() * groups >= 2 * sms) {
-    // Rows for many turns of every SM: four warps to whole rows, and where x is large one block of 16 warps to an
-    // SM, so that it is laid out once. Where it does not fit beside their rings, shorter rings; then slices of
-    // K, with as many rows to each of the cluster's barriers as leave every cluster four turns.
-    if (smem_of() > kLinSmem) a.warps = 16;
-    if (smem_of() > kLinSmemMost) a.stages = 2;
-    if (smem_of() > kLinSmemMost) a.buffers = 1;
-    while (a.slices < 8 && smem_of() > kLinSmemMost) a.buffers = 2, slice(2 * a.slices);
-    if (smem_of() > kLinSmemMost) {  // the longest K
-      a.tokens = 8, a.warps = 8, groups = (static_cast<int64_t>(M) + 7) / 8;
-    }
-    if (a.slices > 1) {  // a cluster needs both buffers
-      a.stages = 3;
-      if (smem_of() > kLinSmemMost) a.stages = 2;
-    }
-    // The tiles of a block meet at barriers 1 to 8, so 16 warps are never 16 tiles.
-    a.across = a.slice >= 8 ? 4 : a.warps / 8;
-    if (a.slices > 1)
-      while (a.across > 1 && blocks() / 2 * a.slices >= 4 * sms) a.across /= 2;
-  } else {
-    // Fewer rows: slices of K while a warp keeps two stages to itself and all blocks run at once, two to an SM,
-    // and as x asks for; then smaller blocks where whole ones leave SMs idle.
-    while (a.slices < 8 && a.slices < chunks &&
-           ((a.slice > 4 && blocks() * groups * a.slices <= sms) || smem_of() > kLinSmem))
-      slice(2 * a.slices);
-    if (smem_of() > kLinSmemMost) {
-      a.tokens = 8, groups = (static_cast<int64_t>(M) + 7) / 8;
-    }
-    while (a.warps > 2 && blocks() * groups * a.slices < sms) a.warps /= 2;
-    // SMs idle all the same: more warps to a row tile, as long as each has a stage
-    while (a.warps < 16 && a.slice > 2 * a.across && blocks() * groups * a.slices < sms && smem_of() * 2 < kLinSmemMost)
-      a.warps *= 2, a.across *= 2;
-  }
-  const size_t smem = smem_of();
-  MOE_CHECK(groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
-  // as many blocks as run at once; they take row blocks in turn
-  const int64_t at_once = (a.warps > 8 || kLinSmemSm / (smem + 1024) < 2 ? 1 : 2) * sms / a.slices;
-  const dim3 grid(static_cast<unsigned>((blocks() < at_once ? blocks() : at_once) * a.slices), static_cast<unsigned>(groups));
+  const size_t smem = linear_smem(cut, align);
+  const int n_per = (gated ? 8 : 16) * (cut.warps / cut.across), blocks = (n_out + n_per - 1) / n_per;
+  // as many clusters as run at once; they take row blocks in turn
+  const dim3 grid((blocks < cut.at_once ? blocks : cut.at_once) * cut.slices, static_cast<unsigned>(cut.groups));
   cudaStream_t s = as_stream(stream);
   if (a.tokens <= 8)
     return align == kAlign256  ? launch_linear<1, kAlign256>(a, grid, smem, s)
