@@ -166,9 +166,9 @@ __device__ __forceinline__ float row_lse(float top, float total) {
   return total == 0.0f ? -INFINITY : (top - kPShift + log2f(total)) * kLn2;
 }
 
-// U: runs of 16 tokens in a step of a warp. Two keep the first step's chain short; four spend a quarter
-// less on the maximum, the barrier and the copies of a step: 131071 tokens 35.6 us against 39.6, a full batch
-// 88.5 against 96.2, 16 sequences of up to 4097 tokens 13.9 against 13.3.
+// U: runs of 16 tokens in a step of a warp. Two keep a short run's chain short; four spend less on the
+// maximum, the barrier and the copies: 131071 tokens 34.5 us against 40.3, 64 x 4000 to 8191 89.5 against 96, 16 x
+// 500 to 2000 11.3 against 12.8; 1 x 2000 6.8 either way.
 template <int D, int NT, int U>
 __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : NT <= 3 ? 3 : 2)
     kv_attend_kernel(Cache c, AttendArgs a) {
@@ -562,24 +562,41 @@ Cut cut_attend(int batch, int kv_heads, int head_dim, int rows, int64_t most) {
   const int tiles = (rows + 7) / 8, most_tiles = head_dim == 64 ? 4 : 2;
   k.row_blocks = (tiles + most_tiles - 1) / most_tiles;
   k.row_tiles = (tiles + k.row_blocks - 1) / k.row_blocks;
+  // Runs of 1 to 96 steps of a block, and twice, four times ... that, whose estimated time is least. The estimate (in us):
+  //   a block's steps one after the other, 0.8 each (1.27 with U = 4), half as much again per further row tile, or the
+  //   blocks of an SM, 0.0042 (0.006, 0.005, 0.0125 for 2 to 4 tiles, 9 % less with U = 4) per token and
+  //   0.3 per tile for joining the warps, half of both where D is 64; whichever is longer;
+  //   the blocks of one sequence come in whole rounds; of several, whose lengths are taken to fill 0.8 of the
+  //   table, all but the last tenth of what runs at once is shared evenly where there are more than that;
+  //   2.4 for the join and 1.4e-5 per row and run (half for D = 64).
+  // Constants fitted to 39 shapes from 1 x 500 tokens to 64 x 8191, each timed in every cut: the cut chosen is on
+  // average 4 % off the best (worst 29 %), where runs of at least two steps that filled the SMs once or twice were 11 % off
+  // (worst 42 %): 1 x 60000 tokens of 8 rows on one kv head 15.2 us against 10.9, 16 x 500 to 2000 of 8 x 4 heads 14.2
+  // against 11.4; the other way 3 x 10000 to 20000 of 8 x 8 heads 21.3 against 24.2.
+  const int sms = num_sms();
   const int64_t blocks = static_cast<int64_t>(batch) * kv_heads * k.row_blocks;
-  // A lone sequence is cut into as many runs as run at once; several, of different lengths, into more than
-  // that, and none into runs so long that the last ones to start are waited for.
-  auto runs = [&](int per_sm, int64_t longest, int64_t shortest) {
-    const int64_t want = (static_cast<int64_t>(num_sms()) * per_sm + blocks - 1) / blocks;
-    int64_t chunk = (most + want - 1) / want;
-    if (batch > 1 && chunk > longest) chunk = longest;
-    return chunk > shortest ? chunk : shortest;
-  };
-  // at least two or three steps of a block: joining its warps costs by the rows
-  k.halves = 2;
-  int64_t step = kAttWarps * 32, chunk = runs(batch == 1 ? 4 : 8, 2304, (k.row_tiles == 1 ? 2 : 3) * step);
-  if (k.row_tiles == 1 && chunk >= 1024) {
-    k.halves = 4;
-    step = kAttWarps * 64, chunk = runs(batch == 1 ? 3 : 8, 2304, step);
+  static constexpr float kToken[] = {0.0042f, 0.006f, 0.005f, 0.0125f};
+  const float half = head_dim == 64 ? 0.5f : 1.0f, filled = batch == 1 ? 1.0f : 0.8f;
+  const float of_rows = 1.4e-5f * half * batch * kv_heads * rows;
+  float best = 0.0f;
+  int64_t best_chunk = 0;
+  for (int u = 2; u <= (k.row_tiles == 1 ? 4 : 2); u += 2) {
+    const int per_sm = k.row_tiles == 1 ? (u == 2 ? 4 : 3) : k.row_tiles <= 3 ? 3 : 2;
+    const float token = kToken[k.row_tiles - 1] * half * (u == 4 ? 0.91f : 1.0f);
+    const float step = (u == 4 ? 1.27f : 0.8f) * (1.0f + 0.52f * (k.row_tiles - 1));
+    for (int64_t m = 1;; m += m < 10 ? 1 : m < 20 ? 2 : m < 32 ? 4 : m < 48 ? 8 : m < 64 ? 16 : m < 96 ? 32 : m) {
+      const int64_t chunk = m * 16 * u * kAttWarps, splits = most > chunk ? (most + chunk - 1) / chunk : 1;
+      const int64_t here = most < chunk ? most : chunk;
+      const float one = here * token + 0.3f * half * k.row_tiles;
+      const float turns = blocks * splits * filled / sms;
+      const float shared = turns > per_sm ? (turns + 0.1f * per_sm) * one : ceilf(turns) * one;
+      const float alone = step * ((here + 16 * u * kAttWarps - 1) / (16 * u * kAttWarps));
+      const float time = (alone > shared ? alone : shared) + (splits > 1 ? 2.4f + of_rows * splits : 0.0f);
+      if (best_chunk == 0 || time < best) best = time, best_chunk = chunk, k.halves = u;
+      if (splits == 1) break;
+    }
   }
-  chunk = roundup64(chunk, step);
-  k.chunk = static_cast<int>(chunk < (1 << 30) ? chunk : (1 << 30));
+  k.chunk = static_cast<int>(best_chunk < (1 << 30) ? best_chunk : (1 << 30));
   k.splits = most > 0 ? static_cast<int>((most + k.chunk - 1) / k.chunk) : 1;
   return k;
 }
