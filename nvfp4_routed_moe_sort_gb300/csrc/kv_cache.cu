@@ -78,8 +78,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 // ---------------------------------------------------------------------------
 // attention of a decode step
 // ---------------------------------------------------------------------------
-// One block per (run of a sequence's tokens, kv head and up to 8 * NT of its query rows,
-// sequence). Query rows are q_len * group many per kv head, row = t * group + g. Both
+// One block per (share of a sequence's steps, kv head and up to 8 * NT of its query rows,
+// sequence); each of `splits` blocks takes every splits-th run of `run` steps, so that they share what a sequence
+// has whatever the table's width. Query rows are q_len * group many per kv head, row = t * group + g. Both
 // products run transposed on mma.m16n8k16 (FP16 in, FP32 sums), so that the cached side is
 // the 16-row operand and eight query rows fill its 8 columns:
 //   S^T[token, row] = K[token, :] . Q[row, :]     per 16 tokens, D / 16 steps
@@ -119,7 +120,7 @@ struct AttendArgs {
   float2* part_ml; // [rows, splits]: maximum (base 2) and sum
   int32_t* dev_status;
   int64_t ld_q, ld_table;
-  int q_len, q_heads, group, row_blocks, max_pages, splits, chunk;
+  int q_len, q_heads, group, row_blocks, max_pages, splits, run;
   float scale;
 };
 
@@ -195,12 +196,21 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
   // Everything the block's first copies and its queries wait for is fetched at once; pages past the
   // sequence's end are fetched too and not used.
   const int32_t* table = a.table + b * a.ld_table;
-  const int half = (lane >> 2) & (U - 1), first = split * a.chunk;
-  int tok = first + warp * kGroup;
+  const int half = (lane >> 2) & (U - 1), first = split * a.run * kStep;
+  // this warp's tokens of its present step, of the steps in flight, and of the one whose page is looked up
+  int toks[kAttStages + 2], left = a.run;
+  auto after = [&](int tok) {
+    if (--left > 0) return tok + kStep;
+    left = a.run;
+    return tok + ((a.splits - 1) * a.run + 1) * kStep;
+  };
+  toks[0] = first + warp * kGroup;
+#pragma unroll
+  for (int i = 1; i <= kAttStages; ++i) toks[i] = after(toks[i - 1]);
   int len = a.lens[b], pages[kAttStages + 1];
 #pragma unroll
   for (int i = 0; i <= kAttStages; ++i) {
-    const int at = (tok + i * kStep + 16 * half) >> c.page_shift;
+    const int at = (toks[i] + 16 * half) >> c.page_shift;
     pages[i] = at < a.max_pages ? table[at] : -1;
   }
   uint32_t raw[NT][D / 8];
@@ -231,8 +241,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     }
     return;
   }
-  const int end = min(seen, first + a.chunk);
-  const int all_see = row_limit(a, len, row0);                       // every row sees the tokens before it
+  const int end = seen, all_see = row_limit(a, len, row0);                       // every row sees the tokens before it
 
   // Lane 4u + w copies array w (keys, values, their scales) of the stage's u-th 16 tokens, or (u = 0) of
   // all of them where a page holds them. Copies stay inside a page whatever the sequence's length.
@@ -260,9 +269,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
   };
 #pragma unroll
   for (int i = 0; i < kAttStages; ++i)
-    if (tok + i * kStep < end) issue(i, tok + i * kStep, tok + i * kStep + 16 * half < end ? pages[i] : -1);
+    if (toks[i] < end) issue(i, toks[i], toks[i] + 16 * half < end ? pages[i] : -1);
     else held_next >>= 16;
-  int page = tok + kAttStages * kStep + 16 * half < end ? pages[kAttStages] : -1;
+  int page = toks[kAttStages] + 16 * half < end ? pages[kAttStages] : -1;
 
   // Q^T fragments and each row's factor from raw sums to base-2 scores
   uint32_t q[NT][KS][2];
@@ -296,7 +305,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 
   int stage = 0;
   uint32_t parity = 0;
-  for (; tok < end; tok += kStep) {
+  auto advance = [&] {
+#pragma unroll
+    for (int i = 0; i < kAttStages; ++i) toks[i] = toks[i + 1];
+  };
+  while (toks[0] < end) {
+    const int tok = toks[0];
     if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &abort_flag, a.dev_status, kWaitLimitNs))) break;
     const uint8_t* const st = my_ring + stage * kStage;
     const uint32_t held = held_next & 0xFFFF;
@@ -424,21 +438,26 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
       }
     }
     __syncwarp();  // every lane has read the stage
-    const int next = tok + kAttStages * kStep;
+    const int next = toks[kAttStages];
     if (next < end) {
       issue(stage, next, page);
-      page = page_of(next + kStep);
+      toks[kAttStages + 1] = after(next);
+      page = page_of(toks[kAttStages + 1]);
     } else {
       held_next >>= 16;
+      toks[kAttStages + 1] = next;
     }
+    advance();
+    toks[kAttStages] = toks[kAttStages + 1];
     if (++stage == kAttStages) stage = 0, parity ^= 1;
   }
   // after a wait that gave up: the stages still in flight, before their memory is used again
-  for (int i = 0; i < kAttStages && tok < end; ++i, tok += kStep) {
+  for (int i = 0; i < kAttStages && toks[0] < end; ++i) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(&full[warp][stage], parity) && globaltimer_ns() - t0 < kWaitLimitNs) {
     }
     if (++stage == kAttStages) stage = 0, parity ^= 1;
+    advance();
   }
   __syncthreads();
 
@@ -551,10 +570,17 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, flo
   if (a.lse && d == 0) a.lse[at] = row_lse(top, total);
 }
 
-// How a call is cut: rows of a block, and runs of the sequences. A block takes as many row tiles as
+// Steps that a block takes side by side, where several sequences share the SMs; a lone one's blocks take
+// every so-manieth step. One run for each block would leave most blocks without work where the table is far wider
+// than the sequences (131072 tokens' columns: 16 x 0 to 4097 tokens 34.2 us, one of 2000 16.0), runs of one step
+// spread short sequences over more blocks than they are worth: those two 15.9 and 7.2 us, but 3 % more time on average over
+// 39 shapes with tables as wide as the longest sequence. Runs of 8: 24.8, 7.2, and 2 %.
+constexpr int kAttRun = 8;
+
+// How a call is cut: rows of a block, and blocks of a sequence. A block takes as many row tiles as
 // its registers hold, since all of them share one conversion of the cache.
 struct Cut {
-  int row_tiles, row_blocks, splits, chunk, halves;
+  int row_tiles, row_blocks, splits, run, halves;
 };
 
 Cut cut_attend(int batch, int kv_heads, int head_dim, int rows, int64_t most) {
@@ -562,7 +588,8 @@ Cut cut_attend(int batch, int kv_heads, int head_dim, int rows, int64_t most) {
   const int tiles = (rows + 7) / 8, most_tiles = head_dim == 64 ? 4 : 2;
   k.row_blocks = (tiles + most_tiles - 1) / most_tiles;
   k.row_tiles = (tiles + k.row_blocks - 1) / k.row_blocks;
-  // Runs of 1 to 96 steps of a block, and twice, four times ... that, whose estimated time is least. The estimate (in us):
+  // As many blocks as leave each 1 to 96 steps of the longest sequence, or twice, four times ... that, by the least
+  // estimated time. The estimate (in us):
   //   a block's steps one after the other, 0.8 each (1.27 with U = 4), half as much again per further row tile, or the
   //   blocks of an SM, 0.0042 (0.006, 0.005, 0.0125 for 2 to 4 tiles, 9 % less with U = 4) per token and
   //   0.3 per tile for joining the warps, half of both where D is 64; whichever is longer;
@@ -570,7 +597,7 @@ Cut cut_attend(int batch, int kv_heads, int head_dim, int rows, int64_t most) {
   //   table, all but the last tenth of what runs at once is shared evenly where there are more than that;
   //   2.4 for the join and 1.4e-5 per row and run (half for D = 64).
   // Constants fitted to 39 shapes from 1 x 500 tokens to 64 x 8191, each timed in every cut: the cut chosen is on
-  // average 4 % off the best (worst 29 %), where runs of at least two steps that filled the SMs once or twice were 11 % off
+  // average 6 % off the best (worst 31 %), where runs of at least two steps that filled the SMs once or twice were 11 % off
   // (worst 42 %): 1 x 60000 tokens of 8 rows on one kv head 15.2 us against 10.9, 16 x 500 to 2000 of 8 x 4 heads 14.2
   // against 11.4; the other way 3 x 10000 to 20000 of 8 x 8 heads 21.3 against 24.2.
   const int sms = num_sms();
@@ -579,25 +606,27 @@ Cut cut_attend(int batch, int kv_heads, int head_dim, int rows, int64_t most) {
   const float half = head_dim == 64 ? 0.5f : 1.0f, filled = batch == 1 ? 1.0f : 0.8f;
   const float of_rows = 1.4e-5f * half * batch * kv_heads * rows;
   float best = 0.0f;
-  int64_t best_chunk = 0;
+  k.splits = 0;
   for (int u = 2; u <= (k.row_tiles == 1 ? 4 : 2); u += 2) {
     const int per_sm = k.row_tiles == 1 ? (u == 2 ? 4 : 3) : k.row_tiles <= 3 ? 3 : 2;
     const float token = kToken[k.row_tiles - 1] * half * (u == 4 ? 0.91f : 1.0f);
     const float step = (u == 4 ? 1.27f : 0.8f) * (1.0f + 0.52f * (k.row_tiles - 1));
     for (int64_t m = 1;; m += m < 10 ? 1 : m < 20 ? 2 : m < 32 ? 4 : m < 48 ? 8 : m < 64 ? 16 : m < 96 ? 32 : m) {
       const int64_t chunk = m * 16 * u * kAttWarps, splits = most > chunk ? (most + chunk - 1) / chunk : 1;
+      if (splits > 1 << 17) continue;  // the kernel steps on by splits * run * 256 tokens in 32 bits
       const int64_t here = most < chunk ? most : chunk;
       const float one = here * token + 0.3f * half * k.row_tiles;
       const float turns = blocks * splits * filled / sms;
       const float shared = turns > per_sm ? (turns + 0.1f * per_sm) * one : ceilf(turns) * one;
       const float alone = step * ((here + 16 * u * kAttWarps - 1) / (16 * u * kAttWarps));
       const float time = (alone > shared ? alone : shared) + (splits > 1 ? 2.4f + of_rows * splits : 0.0f);
-      if (best_chunk == 0 || time < best) best = time, best_chunk = chunk, k.halves = u;
+      if (k.splits == 0 || time < best) {
+        best = time, k.splits = static_cast<int>(splits), k.halves = u;
+        k.run = batch == 1 ? 1 : static_cast<int>((m + (m + kAttRun - 1) / kAttRun - 1) / ((m + kAttRun - 1) / kAttRun));
+      }
       if (splits == 1) break;
     }
   }
-  k.chunk = static_cast<int>(best_chunk < (1 << 30) ? best_chunk : (1 << 30));
-  k.splits = most > 0 ? static_cast<int>((most + k.chunk - 1) / k.chunk) : 1;
   return k;
 }
 
@@ -730,7 +759,7 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   float2* part_ml = parts ? reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + roundup64(parts * c.dim * 4, 16))
                           : nullptr;
   const AttendArgs a = {q, page_table, seq_lens, out, lse, part_o, part_ml, dev_status, ld_q, ld_table, q_len,
-                        num_q_heads, num_q_heads / c.heads, cut.row_blocks, max_pages, cut.splits, cut.chunk,
+                        num_q_heads, num_q_heads / c.heads, cut.row_blocks, max_pages, cut.splits, cut.run,
                         softmax_scale};
   const dim3 grid(cut.splits, c.heads * cut.row_blocks, batch);
   decltype(&kv_attend_kernel<64, 1, 2>) kern;

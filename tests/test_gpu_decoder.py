@@ -472,6 +472,21 @@ def test_attend_bad_query_row_stays_alone():
     assert torch.isnan(got[1, 0, 5].float()).all() and torch.isnan(got_lse[1, 0, 5])
 
 
+@pytest.mark.parametrize("B,Hkv,G,T,Dh,page,lens,wide", [(3, 8, 4, 1, 128, 64, (9000, 700, 0), 200000), (6, 2, 3, 4, 64, 16, (5000, 64, 3, 257, 1024, 2049), 60000),
+                                                         (1, 4, 8, 1, 128, 32, (2500,), 1 << 20), (2, 1, 16, 1, 128, 16, (4001, 130), 100000),
+                                                         (64, 8, 2, 1, 128, 64, tuple(range(1, 3201, 50)), 131072)])
+def test_attend_with_a_table_far_wider_than_the_sequences(B, Hkv, G, T, Dh, page, lens, wide):
+    """The work is cut by the table's width: blocks walk a sequence in several runs, or find nothing in it."""
+    p = Pool(sum(-(-n // page) for n in lens), page, Hkv, Dh)
+    table, ln, held = sequences(p, list(lens), seed=B)
+    far = torch.full((B, wide // page), -7, dtype=torch.int32, device=DEV)
+    far[:, :table.shape[1]] = table
+    q = queries(B, T, Hkv * G, Dh)
+    out, lse = p.kv.attend(q, far, ln, softmax_scale=0.2)
+    check_attend(out, lse, q, held, Hkv, 0.2)
+    assert int(p.status[0]) == 0
+
+
 def test_attend_bad_pages_and_lengths():
     lens, page = [200, 70], 16
     p = Pool(30, page, 1, 64)
