@@ -22,7 +22,7 @@ struct Cache {
 };
 
 // One thread per 16-value block of one token's keys (blockIdx.y 0) or values (1): bound by its chain of
-// load, block maximum, two divisions and stores (1.4 us for one token; 64 tokens of 8 heads of 128 the same).
+// load, block maximum, two divisions and stores (1 token of 8 heads of 128 1.3 us, 64 tokens 1.5, 512 tokens 1.7).
 // The held value is code * (scale / g).
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, const uint16_t* __restrict__ k_new,
                                                                    int64_t ld_k, const uint16_t* __restrict__ v_new,
@@ -102,9 +102,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 // sum is FP32. Query rows are scaled by a power of two to a largest value in [2^14, 2^15) so
 // that BF16's exponents fit FP16.
 //
-// Bound by the conversion (ALU pipe 55 %, issue slots 60 % in use; 17.5 instructions per token and kv head), not by
-// HBM: 64 sequences of 4000 to 8191 tokens, 8 kv heads, 86 us (5.1 TB/s; the copies alone 73 us), one of
-// 131071 tokens 34 us. Short ones by the chain of length, pages, first copies, two steps and the join.
+// Bound by the conversion (ALU pipe 54 %, issue slots 61 % in use; 17.8 instructions per token and kv head), not by
+// HBM: 64 sequences of 4000 to 8191 tokens, 8 kv heads, 87 us (5.0 TB/s; the copies alone 73 us), one of
+// 131071 tokens 35 us. Short ones by the chain of length, pages, first copies, steps and the join.
 constexpr int kAttWarps = 4;
 constexpr int kAttStages = 2;
 constexpr float kPShift = 15.0f;
@@ -780,7 +780,8 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   if (smem > 48 * 1024) MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const moe_status_t ran = launch_pdl(kern, grid, dim3(kAttWarps * 32), smem, as_stream(stream), c, a);
   if (ran != MOE_OK || cut.splits == 1) return ran;
-  // a warp to a row while there are rows enough, or too few parts to share
+  // a warp to a row while there are rows enough, or too few parts to share (16 x 4 x 8 rows of 16 parts 0.9 us less than
+  // a block to a row); else the eight warps of a block (64 rows of 57 parts: of 20 us little is left)
   const bool one = cut.splits <= 16 || rows * num_q_heads >= static_cast<size_t>(num_sms()) * 16;
   auto* join = c.dim == 64 ? (one ? kv_join_kernel<64, 1> : kv_join_kernel<64, 8>)
                            : (one ? kv_join_kernel<128, 1> : kv_join_kernel<128, 8>);

@@ -1,7 +1,7 @@
 // A few tokens times one dense NVFP4 matrix: y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]).
 //
-// 9/16 byte per weight, read once per 16 tokens: bound by the weights' conversion, close behind it by HBM. A warp takes 16 rows of w and a run
-// of K: mma.m16n8k16 with the 16 weight rows as one operand and eight tokens as the other. K
+// 9/16 byte per weight, read once per 16 tokens: bound by the weights' conversion, close behind it by
+// HBM. A warp takes 16 rows of w and a run of K: mma.m16n8k16 with the 16 weight rows as one operand and eight tokens as the other. K
 // goes by chunks of 128 values. In a chunk lane (r, c) = (lane / 4, lane % 4) holds the values 32c
 // to 32c + 31 of rows r and r + 8, and MMA step j takes its values 32c + 4j to 32c + 4j + 3.
 //
@@ -24,7 +24,7 @@
 // end. A block goes on to further rows while there are any, their first chunks already in flight.
 //
 // Measured: 4 tokens x 129021 x 4096 57 us (5.2 TB/s; 158 instructions per 16 rows and chunk, 62 % of the
-// issue slots, 64 of them conversions at half rate); 8 x 4096 x 7168 with SwiGLU 8.5 us, 1 x 2048 x 512
+// issue slots, 64 of them conversions at half rate); 8 x 4096 x 7168 with SwiGLU 8.3 us, 1 x 2048 x 512
 // 3.3 us, both chains of launch, loads, sums and barrier.
 #include "cluster.cuh"
 #include "common.cuh"

@@ -244,8 +244,8 @@ template <int V>
 moe_status_t launch_norm(NormArgs a, cudaStream_t s) {
   const int items = (a.H + kItem - 1) / kItem;
   // A warp's items: up to four, its loads in flight together, while that leaves kNormWarps warps to every
-  // SM; fewer, so that a row's chain gets shorter, for fewer rows. A block has at most 32 warps,
-  // or 16 of over two items.
+  // SM; fewer, so that a row's chain gets shorter, for fewer rows (kNormWarps 16, 32, 64: 2000 x 1001 7.1, 6.05, 6.03
+  // us; 777 x 1531 in ones 5.0, in fours 6.8). A block has at most 32 warps, or 16 of over two items.
   int per = 4;
   while (per > 1 && a.M * static_cast<int64_t>((items + per - 1) / per) < kNormWarps * num_sms()) per /= 2;
   while ((items + per - 1) / per > (per > 2 ? 16 : 32)) per *= 2;
