@@ -221,6 +221,32 @@ def test_linear_short_unaligned_rows(M, N, K, act):
     check_linear(got[:, torch.from_numpy(cols).to(DEV)], x, scale, data[rows], sf[rows], alpha, act)
 
 
+# sizes that between them are cut into every kind of block, with and without a cluster, for plain and gated products
+CUTS = {"identity": [(1, 1, 1808), (3, 1, 3088), (4, 1, 528), (4, 1, 1040), (4, 1, 2064), (4, 1, 2320),
+                     (4, 1, 3600), (4, 9743, 272), (4, 14682, 400), (5, 1219, 3632), (6, 1, 2064),
+                     (6, 963, 1824), (6, 1448, 3680), (6, 12163, 400), (7, 1, 528), (7, 1, 1552),
+                     (7, 1, 2064), (8, 1, 1040), (9, 1, 8208), (10, 3555, 784), (11, 1, 528),
+                     (11, 1, 1552), (12, 1, 3088), (12, 1, 8208), (12, 971, 3648), (12, 17025, 16),
+                     (13, 1, 1552), (13, 1, 3088), (15, 1, 272), (15, 1, 400), (15, 1, 2320),
+                     (15, 986, 7280), (15, 3458, 800), (15, 5972, 784), (16, 1690, 1808), (16, 1970, 1808),
+                     (16, 2401, 1808), (16, 2900, 1808), (16, 3527, 1888), (16, 17114, 656)],
+        "swiglu": [(4, 2, 528), (6, 2, 1552), (6, 2, 2064), (6, 1456, 1808), (7, 2, 2064), (8, 2, 1040),
+                   (9, 3458, 1808), (10, 2, 528), (10, 2, 1552), (10, 2, 2320), (10, 2404, 1808),
+                   (10, 34050, 16), (13, 2, 272), (13, 970, 3680), (14, 2, 8208), (14, 2354, 784),
+                   (14, 14598, 16), (15, 5868, 784), (15, 9780, 400), (15, 14658, 656), (16, 2, 3088),
+                   (16, 986, 7184), (16, 1988, 1856), (16, 2976, 1824)]}
+
+
+@pytest.mark.parametrize("act,M,N,K", [(act, *size) for act, sizes in CUTS.items() for size in sizes])
+def test_linear_every_cut(act, M, N, K):
+    x, scale, data, sf, alpha = linear_case(M, N, K, "group" if M % 2 else None)
+    got = run_linear(x, scale, data, sf, alpha, act)
+    n_out = N // 2 if act == "swiglu" else N
+    cols = np.unique(np.r_[0:min(n_out, 150), max(n_out - 150, 0):n_out, np.random.default_rng(1).integers(0, n_out, 100)])
+    rows = np.r_[cols, cols + n_out] if act == "swiglu" else cols
+    check_linear(got[:, torch.from_numpy(cols).to(DEV)], x, scale, data[rows], sf[rows], alpha, act)
+
+
 @pytest.mark.parametrize("M,N,K", [(16, 300, 65536), (9, 40, 65520), (2, 33, 40000), (16, 20000, 32784)])
 def test_linear_longest_k(M, N, K):
     x, scale, data, sf, alpha = linear_case(M, N, K, None)
