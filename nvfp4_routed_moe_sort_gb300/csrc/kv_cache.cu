@@ -596,10 +596,11 @@ Cut cut_attend(int batch, int kv_heads, int head_dim, int rows, int64_t most) {
   //   the blocks of one sequence come in whole rounds; of several, whose lengths are taken to fill 0.8 of the
   //   table, all but the last tenth of what runs at once is shared evenly where there are more than that;
   //   2.4 for the join and 1.4e-5 per row and run (half for D = 64).
-  // Constants fitted to 39 shapes from 1 x 500 tokens to 64 x 8191, each timed in every cut: the cut chosen is on
-  // average 6 % off the best (worst 31 %), where runs of at least two steps that filled the SMs once or twice were 11 % off
-  // (worst 42 %): 1 x 60000 tokens of 8 rows on one kv head 15.2 us against 10.9, 16 x 500 to 2000 of 8 x 4 heads 14.2
-  // against 11.4; the other way 3 x 10000 to 20000 of 8 x 8 heads 21.3 against 24.2.
+  // Constants fitted to 39 shapes from 1 x 500 tokens to 64 x 8191, each timed in every cut. With three draws of the lengths
+  // of the ragged ones the cut chosen is on average 5 % off the best (worst 39 %: the lengths are
+  // not known here); runs of at least two steps that filled the SMs once or twice were 11 % off (worst 42 %): 1 x 60000
+  // tokens of 8 rows on one kv head 15.2 us against 10.9, 16 x 500 to 2000 of 8 x 4 heads 14.2 against 11.4; the other
+  // way 3 x 10000 to 20000 of 8 x 8 heads 21.3 against 24.4.
   const int sms = num_sms();
   const int64_t blocks = static_cast<int64_t>(batch) * kv_heads * k.row_blocks;
   static constexpr float kToken[] = {0.0042f, 0.006f, 0.005f, 0.0125f};
