@@ -781,8 +781,8 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   if (smem > 48 * 1024) MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const moe_status_t ran = launch_pdl(kern, grid, dim3(kAttWarps * 32), smem, as_stream(stream), c, a);
   if (ran != MOE_OK || cut.splits == 1) return ran;
-  // a warp to a row while there are rows enough, or too few parts to share (16 x 4 x 8 rows of 16 parts 0.9 us less than
-  // a block to a row); else the eight warps of a block (64 rows of 57 parts: of 20 us little is left)
+  // a warp to a row while there are rows enough, or too few parts to share (512 rows of 16 parts:
+  // 0.9 us less than a block to a row); else the eight warps of a block (64 rows of 57 parts took a warp each 20 us)
   const bool one = cut.splits <= 16 || rows * num_q_heads >= static_cast<size_t>(num_sms()) * 16;
   auto* join = c.dim == 64 ? (one ? kv_join_kernel<64, 1> : kv_join_kernel<64, 8>)
                            : (one ? kv_join_kernel<128, 1> : kv_join_kernel<128, 8>);
