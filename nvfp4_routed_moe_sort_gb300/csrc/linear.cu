@@ -1,8 +1,8 @@
 // A few tokens times one dense NVFP4 matrix: y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]).
 //
 // 9/16 byte per weight, read once per 16 tokens: bound by the weights' conversion, close behind it by
-// HBM. A warp takes 16 rows of w and a run of K: mma.m16n8k16 with the 16 weight rows as one operand and eight tokens as the other. K
-// goes by chunks of 128 values. In a chunk lane (r, c) = (lane / 4, lane % 4) holds the values 32c
+// HBM. A warp takes 16 rows of w and a run of K: mma.m16n8k16 with the 16 weight rows as one
+// operand and eight tokens as the other. K goes by chunks of 128 values. In a chunk lane (r, c) = (lane / 4, lane % 4) holds the values 32c
 // to 32c + 31 of rows r and r + 8, and MMA step j takes its values 32c + 4j to 32c + 4j + 3.
 //
 // The codes come through a ring in shared memory that belongs to the warp (cp.async; two chunks a
@@ -470,7 +470,8 @@ bool cut_linear(int64_t M, int K, int n_out, bool gated, int align, int sms, Lin
         if (smem > kLinSmem && k.slices == 1) k.buffers = 1, smem = linear_smem(k, align);  // a cluster needs both
         if (smem > kLinSmem) continue;
         const int fit = kLinSmemSm / (smem + 1024), most = kLinWarps / k.warps, per_sm = fit < most ? fit : most;
-        // SMs that clusters of 4 and 8 leave over: 8 and 32 of 152 at one block to an SM, half to a quarter of that otherwise
+        // SMs that clusters of 4 and 8 leave over (the occupancy query's answer): 8 and 32 of 152 at one block to an SM,
+        // half and a quarter of that otherwise
         const int odd = k.slices == 8 ? (per_sm == 1 ? 32 : 8) : k.slices == 4 ? (per_sm == 1 ? 8 : 4) : 0;
         k.at_once = (sms - odd) * per_sm / k.slices;
         if (k.at_once < 1) continue;
