@@ -23,9 +23,9 @@
 // results do not depend on timing. alpha, the activation and the BF16 rounding come once at the
 // end. A block goes on to further rows while there are any, their first chunks already in flight.
 //
-// Measured: 4 tokens x 129021 x 4096 57 us (5.2 TB/s; 158 instructions per 16 rows and chunk, 62 % of the
-// issue slots, 64 of them conversions at half rate); 8 x 4096 x 7168 with SwiGLU 8.3 us, 1 x 2048 x 512
-// 3.3 us, both chains of launch, loads, sums and barrier.
+// Measured: 4 tokens x 129021 x 4096 57.5 us (5.2 TB/s; 158 instructions per 16 rows and chunk, 62 % of the
+// issue slots, 64 of them conversions at half rate); 8 x 4096 x 7168 with SwiGLU 8.4 us, 1 x 2048 x 512
+// 3.4 us, both chains of launch, loads, sums and barrier.
 #include "cluster.cuh"
 #include "common.cuh"
 #include "fp4_mma.cuh"
@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   const int member = a.slices > 1 ? tid : ((tile / own) * a.across + part) * 32 + lane;
   const int members = a.slices > 1 ? threads : a.across * kinds * 32;
   const int m_member = member / cols, col_member = at_col + member - m_member * cols;
+  const int m_members = members / cols, col_members = members - m_members * cols;
   int stage = 0;
   for (int block = blockIdx.x / a.slices; block < blocks; block += stride) {
     float acc[NT][4];
@@ -365,6 +366,23 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
       if (++stage == a.stages) stage = 0;
     }
 
+    // A warp that has all of K and no activation to do has the result: 16 x 60000 x 256 6.4 us against 11.8 through
+    // shared memory. (With the activations here too, their code made every size 0.1 us slower.)
+    if (parts == 1 && a.act == MOE_ACT_IDENTITY) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int col = block * n_per + i0 + r + 8 * h;
+        uint16_t* const to = a.out + static_cast<int64_t>(m0 + 2 * c) * a.n_out + col;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (col < a.n_out && 8 * t + 2 * c + i < M)
+              to[static_cast<int64_t>(8 * t + i) * a.n_out] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(acc[t][2 * h + i] * alpha));
+      }
+      continue;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float* const to_sum = sums + sum_at[h];
@@ -395,8 +413,8 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
         a.out[static_cast<int64_t>(m0 + m) * a.n_out + block * n_per + rank * share + col] =
             __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0] * alpha, y[1] * alpha)));
       }
-      i += members;
-      if (i < cols * M) m = i / cols, col = at_col + i - m * cols;
+      i += members, m += m_members, col += col_members;
+      if (col >= at_col + cols) col -= cols, ++m;
     }
     if (a.buffers == 2) {  // the other buffer is free: what it held was added before the barrier above
       float* const t = sums;
