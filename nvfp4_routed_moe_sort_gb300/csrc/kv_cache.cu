@@ -97,9 +97,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 // kAttStages groups in shared memory (bulk copies of 16 tokens, or of the group where one page holds
 // it, one mbarrier per stage), so the warps of a block never wait for one another before the end.
 //
-// Softmax in base 2 with a running maximum per query row; p = 2^(s - m + 15) is rounded to
-// FP16 for the second product (11 significant bits down to 2^-29 of the largest weight), its
-// sum is FP32. Query rows are scaled by a power of two to a largest value in [2^14, 2^15) so
+// Softmax in base 2 with a running maximum per query row of the raw sums s, which a row's factor f takes to
+// scores; p = 2^((s - m) f + 15) is rounded to FP16 for the second product (11 significant bits down to
+// 2^-29 of the largest weight), its sum is FP32. Subtracting before multiplying makes the largest weight
+// 2^15 whatever the scores' size; the difference of two rounded scores would be off by whole powers of 2
+// from 2^24 on. It costs an instruction a score. Query rows are scaled by a power of two to a largest value in [2^14, 2^15) so
 // that BF16's exponents fit FP16.
 //
 // Bound by the conversion (ALU pipe 54 %, issue slots 61 % in use; 17.8 instructions per token and kv head), not by
@@ -117,7 +119,8 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   float* part_o;   // [rows, splits, D]
-  float2* part_ml; // [rows, splits]: maximum (base 2) and sum
+  float2* part_ml; // [rows, splits]: maximum of the raw sums and sum of the weights
+  float* row_f;    // [rows]: factor from raw sums to base-2 scores
   int32_t* dev_status;
   int64_t ld_q, ld_table;
   int q_len, q_heads, group, row_blocks, max_pages, splits, run;
@@ -163,8 +166,8 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int64_t at, float
   h.w = __bfloat16_as_ushort(__float2bfloat16_rn(v.w * f));
   *reinterpret_cast<ushort4*>(a.out + at) = h;
 }
-__device__ __forceinline__ float row_lse(float top, float total) {
-  return total == 0.0f ? -INFINITY : (top - kPShift + log2f(total)) * kLn2;
+__device__ __forceinline__ float row_lse(float top, float f, float total) {
+  return total == 0.0f ? -INFINITY : (top * f - kPShift + log2f(total)) * kLn2;
 }
 
 // U: runs of 16 tokens in a step of a warp. Two keep a short run's chain short; four spend less on the
@@ -289,7 +292,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
       q[t][i >> 1][i & 1] = pack_f16x2(bf16_lo(raw[t][i]) * up, bf16_hi(raw[t][i]) * up);
-    const float f = fmaxf(fabsf(a.scale) * kLog2e / c.g[0] * down, FLT_MIN);  // above 0: -inf stays -inf
+    // above 0, so that -inf stays -inf; finite, so that no difference stays 0
+    const float f = fminf(fmaxf(fabsf(a.scale) * kLog2e / c.g[0] * down, FLT_MIN), FLT_MAX);
     to_log2[t][0] = __shfl_sync(0xffffffffu, f, 8 * cc);
     to_log2[t][1] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
   }
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     uint32_t p[U][NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float top[2], keep[2], base[2];
+      float top[2], keep[2];
       bool grew = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -383,15 +387,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
         for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][t][i], s[u][t][i + 2]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-        top[i] = fmaxf(m[t][i], x * to_log2[t][i]);
+        top[i] = fmaxf(m[t][i], x);
         grew |= top[i] > m[t][i];
         keep[i] = top[i] == -INFINITY ? 0.0f : top[i];
-        base[i] = kPShift - keep[i];
       }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = ex2(m[t][i] - keep[i]);
+          const float f = ex2((m[t][i] - keep[i]) * to_log2[t][i]);
           l[t][i] *= f;
 #pragma unroll
           for (int j = 0; j < KS; ++j) o[t][j][i] *= f, o[t][j][i + 2] *= f;
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
       for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[u][t][i] = ex2(fmaf(s[u][t][i], to_log2[t][i & 1], base[i & 1]));
+          s[u][t][i] = ex2(fmaf(s[u][t][i] - keep[i & 1], to_log2[t][i & 1], kPShift));
           l[t][i & 1] += s[u][t][i];
         }
         p[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 
   // ---- join the warps
   constexpr int ST = D + 4;
-  __shared__ float sm[kAttWarps][R], sl[kAttWarps][R];
+  __shared__ float sm[kAttWarps][R], sl[kAttWarps][R], sf[R];
   auto so = reinterpret_cast<float(*)[R][ST]>(ring);  // [warp][row][dim]
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -476,6 +479,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
       if (r == 0) {
         sm[warp][row] = m[t][i];
         sl[warp][row] = x;
+        if (warp == 0) sf[row] = to_log2[t][i];
       }
 #pragma unroll
       for (int j = 0; j < KS; ++j)
@@ -484,6 +488,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
   __syncthreads();
   for (int i = tid; i < rows_here * (D / 4); i += kAttWarps * 32) {
     const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
+    const float f_row = sf[row];
     float top = sm[0][row];
 #pragma unroll
     for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sm[w][row]);
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 #pragma unroll
     for (int w = 0; w < kAttWarps; ++w) {
       if (sl[w][row] == 0.0f) continue;  // saw nothing (its maximum may be -inf)
-      const float f = ex2(sm[w][row] - top);
+      const float f = ex2((sm[w][row] - top) * f_row);
       total += sl[w][row] * f;
       const float4 x = *reinterpret_cast<const float4*>(&so[w][row][d]);
       v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
@@ -502,9 +507,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     if (a.splits > 1) {
       *reinterpret_cast<float4*>(a.part_o + (at * a.splits + split) * D + d) = v;
       if (d == 0) a.part_ml[at * a.splits + split] = make_float2(top, total);
+      if (d == 0 && split == 0) a.row_f[at] = f_row;
     } else {
       store_row(a, at * D + d, v, total, c.g[1]);
-      if (a.lse && d == 0) a.lse[at] = row_lse(top, total);
+      if (a.lse && d == 0) a.lse[at] = row_lse(top, f_row, total);
     }
   }
 }
@@ -524,6 +530,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, flo
   const int64_t at = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32 / W) + warp / W;
   const bool row = at < rows;
   const float2* ml = a.part_ml + at * a.splits;
+  const float f_row = row ? a.row_f[at] : 0.0f;
   float top = -INFINITY;
   if (row)
     for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
@@ -536,7 +543,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, flo
     float mine = 0.0f;
     if (row && i0 + lane < a.splits) {
       const float2 x = ml[i0 + lane];
-      if (x.y != 0.0f) mine = ex2(x.x - top);
+      if (x.y != 0.0f) mine = ex2((x.x - top) * f_row);
       total += mine * x.y;
     }
     const int here = min(a.splits - i0, 32);
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, flo
   }
   if (!row || part != 0) return;
   store_row(a, at * D + 4 * d, v, total, g);
-  if (a.lse && d == 0) a.lse[at] = row_lse(top, total);
+  if (a.lse && d == 0) a.lse[at] = row_lse(top, f_row, total);
 }
 
 // Steps that a block takes side by side, where several sequences share the SMs; a lone one's blocks take
@@ -711,7 +718,7 @@ moe_status_t attend_cut(const moe_kv_cache_t* cache, Cache* c, int32_t batch, in
             MOE_ERR_UNSUPPORTED_SHAPE);
   *cut = cut_attend(batch > 0 ? batch : 1, c->heads, c->dim, static_cast<int>(rows), most);
   const int64_t parts = cut->splits > 1 ? static_cast<int64_t>(batch) * q_len * num_q_heads * cut->splits : 0;
-  *bytes = static_cast<size_t>(roundup64(parts * c->dim * 4, 16) + parts * 8);
+  *bytes = static_cast<size_t>(roundup64(parts * c->dim * 4, 16) + parts * 8 + (parts ? parts / cut->splits * 4 : 0));
   return MOE_OK;
 }
 
@@ -759,7 +766,8 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   float* part_o = parts ? static_cast<float*>(workspace) : nullptr;
   float2* part_ml = parts ? reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + roundup64(parts * c.dim * 4, 16))
                           : nullptr;
-  const AttendArgs a = {q, page_table, seq_lens, out, lse, part_o, part_ml, dev_status, ld_q, ld_table, q_len,
+  float* row_f = parts ? reinterpret_cast<float*>(part_ml + parts) : nullptr;
+  const AttendArgs a = {q, page_table, seq_lens, out, lse, part_o, part_ml, row_f, dev_status, ld_q, ld_table, q_len,
                         num_q_heads, num_q_heads / c.heads, cut.row_blocks, max_pages, cut.splits, cut.run,
                         softmax_scale};
   const dim3 grid(cut.splits, c.heads * cut.row_blocks, batch);
