@@ -48,16 +48,38 @@ __device__ __forceinline__ void mma_f16_first(float* d, const uint32_t* a, const
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
 }
 
+// the same in BF16, for BF16 operands whose range does not fit FP16
+__device__ __forceinline__ void mma_bf16(float* d, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// two FP16 values as BF16; a code times its scale keeps its 6 significant bits
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n .reg .b16 h0, h1;\n .reg .f32 f0, f1;\n mov.b32 {h0, h1}, %1;\n cvt.f32.f16 f0, h0;\n cvt.f32.f16 f1, h1;\n"
+      " cvt.rn.bf16x2.f32 %0, f1, f0;\n}\n"
+      : "=r"(r) : "r"(two));
+  return r;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t two) { return __uint_as_float(two << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t two) { return __uint_as_float(two & 0xFFFF0000u); }
 
 // The power of two that takes a largest magnitude `amax` into [2^14, 2^15), and its inverse: BF16
-// values so scaled fit FP16 with their own bits down to 2^-28 of the largest. Zero and the
+// values so scaled are exact in FP16 from 2^-17 on. Zero and the
 // smallest take 2^126; infinity and NaN (whose amax is that of the rest) stay what they are.
 __device__ __forceinline__ void f16_range(float amax, float* up, float* down) {
   const int shift = min(14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127), 126);
   *up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
   *down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+}
+
+// whether a value of these two BF16 lies below what f16_range's factor keeps exact (zero does not)
+__device__ __forceinline__ bool below_f16(uint32_t two, float down) {
+  const uint32_t least = __float_as_uint(0x1p-17f * down) - 1;  // 2^-143 at the smallest
+  return ((two << 16 & 0x7FFFFFFFu) - 1 < least) | ((two & 0x7FFF0000u) - 1 < least);
 }
 
 }  // namespace moe

@@ -13,7 +13,9 @@
 // The block first lays its slice of x out in shared memory as FP16 in fragment order. Each
 // (token, chunk) has an FP32 factor: the tokens' own scales for E4M3 (exact in FP16), a power of two
 // that brings the chunk's values into FP16's range for BF16. A chunk is summed on its own and
-// enters the FP32 sum times its factor.
+// enters the FP32 sum times its factor. Where a chunk's BF16 values span more than FP16 holds exactly (2^31;
+// rare), the block lays x out again as it is and runs on BF16 MMAs, for which the weights take a
+// second conversion: where the largest value's weight is zero, the small ones are all of the sum.
 //
 // Two ways of sharing K. Warps of one block (`across` of them) take neighbouring runs of the same
 // rows, so that a block reads whole rows: DRAM gives 128 rows at a time read along K 4.8 TB/s, whole
@@ -23,9 +25,12 @@
 // results do not depend on timing. alpha, the activation and the BF16 rounding come once at the
 // end. A block goes on to further rows while there are any, their first chunks already in flight.
 //
-// Measured: 4 tokens x 129021 x 4096 57.5 us (5.2 TB/s; 158 instructions per 16 rows and chunk, 62 % of the
-// issue slots, 64 of them conversions at half rate); 8 x 4096 x 7168 with SwiGLU 8.4 us, 1 x 2048 x 512
-// 3.4 us, both chains of launch, loads, sums and barrier.
+// Measured: 4 tokens x 129021 x 4096 58.3 us (5.1 TB/s; 158 instructions per 16 rows and chunk, 62 % of the
+// issue slots, 64 of them conversions at half rate); 8 x 4096 x 7168 with SwiGLU, E4M3 8.1 us, 1 x 2048 x 512
+// 3.6 us, both chains of launch, loads, sums and barrier. (The BF16 MMAs' code costs BF16 calls that do not run it 0.2 to
+// 0.8 us.)
+#include <type_traits>
+
 #include "cluster.cuh"
 #include "common.cuh"
 #include "fp4_mma.cuh"
@@ -99,8 +104,8 @@ __host__ __device__ constexpr int code_row(int align) { return align == kAlign16
 __host__ __device__ constexpr int scale_row(int align) { return align == kAlign256 ? 16 : 48; }
 __host__ __device__ constexpr int stage_bytes(int align) { return 16 * (code_row(align) + scale_row(align)); }
 
-// NT: groups of eight tokens
-template <int NT, int ALIGN>
+// NT: groups of eight tokens; FP8: x is E4M3 with scales, else BF16
+template <int NT, int ALIGN, bool FP8>
 __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
@@ -208,6 +213,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
 
   // x: half a warp per (token, chunk), eight values a lane, four loads in flight
   const int pairs = threads / 16, piece = tid & 15;
+  bool lost = false;  // some value of x is not exact in FP16
   int m_next = chunks ? (tid >> 4) / chunks : M, ch_next = (tid >> 4) - m_next * chunks;
   const int m_step = chunks ? pairs / chunks : 0, ch_step = pairs - m_step * chunks;
   while (m_next < M) {
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
       const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
       raw[u] = make_uint4(0, 0, 0, 0);
       if (m >= M) continue;
-      if (a.x_mode == MOE_FP8_NONE) {
+      if constexpr (!FP8) {
         if (k < a.K) raw[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (m0 + m) * a.ld_x + k);
       } else {
         if (k < a.K) {
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
       if (m >= M) break;
       const uint32_t v[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
       uint4 f;
-      if (a.x_mode == MOE_FP8_NONE) {
+      if constexpr (!FP8) {
         float amax = 0.0f, grow;
 #pragma unroll
         for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(v[j])), fabsf(bf16_hi(v[j]))));
@@ -250,6 +256,8 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half_warp, amax, o));
         f16_range(amax, &grow, &scale[u]);
+        if (amax < INFINITY)  // a sum with an infinity in it needs no other bits
+          lost |= below_f16(v[0], scale[u]) | below_f16(v[1], scale[u]) | below_f16(v[2], scale[u]) | below_f16(v[3], scale[u]);
         f = make_uint4(pack_f16x2(bf16_lo(v[0]) * grow, bf16_hi(v[0]) * grow),
                        pack_f16x2(bf16_lo(v[1]) * grow, bf16_hi(v[1]) * grow),
                        pack_f16x2(bf16_lo(v[2]) * grow, bf16_hi(v[2]) * grow),
@@ -263,7 +271,20 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
       if (piece == 0) factor[ch * 8 * NT + m] = scale[u];
     }
   }
-  __syncthreads();
+  bool wide = false;
+  if constexpr (FP8) __syncthreads();
+  else wide = __syncthreads_or(lost);
+  if (!FP8 && wide) {
+    for (int i = tid >> 4; i < M * chunks; i += pairs) {
+      const int m = i / chunks, ch = i - m * chunks;
+      const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
+      uint4 f = make_uint4(0, 0, 0, 0);
+      if (k < a.K) f = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (m0 + m) * a.ld_x + k);
+      *reinterpret_cast<uint4*>(xs + m * x_row + ch * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16) = f;
+      if (piece == 0) factor[ch * 8 * NT + m] = 1.0f;
+    }
+    __syncthreads();
+  }
 
   const int share = n_per / a.slices, kinds = a.gated ? 2 : 1, parts = a.slices * a.across;
   const float alpha = *a.alpha;
@@ -299,72 +320,86 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
     float acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-    const float* scale_of = factor_lane;
-    int x_at = 0;
-    for (int ch0 = first; ch0 < last; ch0 += 2) {
-      if (a.stages == 3) copies_wait<1>();
-      else copies_wait<0>();
-      __syncwarp();  // every lane's copies of this stage are there, and the stage before it has been read
-      load_stage(stage == 0 ? a.stages - 1 : stage - 1);
-      const uint8_t* const at = ring_at + stage * kStage;
+    auto sweep = [&](auto in_bf16) {
+      constexpr bool kBf16 = decltype(in_bf16)::value;
+      const float* scale_of = factor_lane;
+      int x_at = 0;
+      for (int ch0 = first; ch0 < last; ch0 += 2) {
+        if (a.stages == 3) copies_wait<1>();
+        else copies_wait<0>();
+        __syncwarp();  // every lane's copies of this stage are there, and the stage before it has been read
+        load_stage(stage == 0 ? a.stages - 1 : stage - 1);
+        const uint8_t* const at = ring_at + stage * kStage;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int ch = ch0 + u;
-        if (u == 1 && ch >= last) break;
-        uint32_t codes[2][4], two[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = r + 8 * h;
-          if constexpr (ALIGN == kAlign16) {
-            const uint2* const w = reinterpret_cast<const uint2*>(at + row * kRow + code_at + (4 * u + c) * 16);
-            const uint2 x = w[0], y = w[1];
-            codes[h][0] = x.x, codes[h][1] = x.y, codes[h][2] = y.x, codes[h][3] = y.y;
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4*>(at + row * kRow + ((4 * u + c) ^ (r & 1) << 2) * 16);
-            codes[h][0] = x.x, codes[h][1] = x.y, codes[h][2] = x.z, codes[h][3] = x.w;
-          }
-          const uint8_t* const s = at + 16 * kRow + row * kSfRow + scale_at[h] + 8 * u + 2 * c;
-          if constexpr (ALIGN == kAlign16) two[h] = s[0] | static_cast<uint32_t>(s[1]) << 8;
-          else two[h] = *reinterpret_cast<const uint16_t*>(s);
-          if (ALIGN != kAlign256 && (chunk0 + ch + 1) * kLinChunk > a.K) {  // the next row's may be no numbers
-            const int k = (chunk0 + ch) * kLinChunk + 32 * c;
-            two[h] = k >= a.K ? 0 : k + kBlock >= a.K ? two[h] & 0xFF : two[h];
-          }
-          two[h] = e4m3x2_to_f16x2(two[h]);
-        }
-        float sum[NT][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // a word of either row: two MMA steps
-          uint32_t f[2][4];
+        for (int u = 0; u < 2; ++u) {
+          const int ch = ch0 + u;
+          if (u == 1 && ch >= last) break;
+          uint32_t codes[2][4], two[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t s = __byte_perm(two[h], two[h], j < 2 ? 0x1010 : 0x3232);
-            e2m1x8_to_f16x2(codes[h][j], f[h]);
+            const int row = r + 8 * h;
+            if constexpr (ALIGN == kAlign16) {
+              const uint2* const w = reinterpret_cast<const uint2*>(at + row * kRow + code_at + (4 * u + c) * 16);
+              const uint2 x = w[0], y = w[1];
+              codes[h][0] = x.x, codes[h][1] = x.y, codes[h][2] = y.x, codes[h][3] = y.y;
+            } else {
+              const uint4 x = *reinterpret_cast<const uint4*>(at + row * kRow + ((4 * u + c) ^ (r & 1) << 2) * 16);
+              codes[h][0] = x.x, codes[h][1] = x.y, codes[h][2] = x.z, codes[h][3] = x.w;
+            }
+            const uint8_t* const s = at + 16 * kRow + row * kSfRow + scale_at[h] + 8 * u + 2 * c;
+            if constexpr (ALIGN == kAlign16) two[h] = s[0] | static_cast<uint32_t>(s[1]) << 8;
+            else two[h] = *reinterpret_cast<const uint16_t*>(s);
+            if (ALIGN != kAlign256 && (chunk0 + ch + 1) * kLinChunk > a.K) {  // the next row's may be no numbers
+              const int k = (chunk0 + ch) * kLinChunk + 32 * c;
+              two[h] = k >= a.K ? 0 : k + kBlock >= a.K ? two[h] & 0xFF : two[h];
+            }
+            two[h] = e4m3x2_to_f16x2(two[h]);
+          }
+          float sum[NT][4];
+          if constexpr (kBf16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[h][i] = mul_f16x2(f[h][i], s);
+            for (int t = 0; t < NT; ++t) sum[t][0] = sum[t][1] = sum[t][2] = sum[t][3] = 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // a word of either row: two MMA steps
+            uint32_t f[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t s = __byte_perm(two[h], two[h], j < 2 ? 0x1010 : 0x3232);
+              e2m1x8_to_f16x2(codes[h][j], f[h]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                f[h][i] = mul_f16x2(f[h][i], s);
+                if constexpr (kBf16) f[h][i] = f16x2_to_bf16x2(f[h][i]);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint4 x = *reinterpret_cast<const uint4*>(x_lane[t] + x_at + u * 256 + j * 64);
+              const uint32_t b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t A[4] = {f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1]};
+                if constexpr (kBf16) mma_bf16(sum[t], A, b + 2 * i);
+                else if (j == 0 && i == 0) mma_f16_first(sum[t], A, b);
+                else mma_f16(sum[t], A, b + 2 * i);
+              }
+            }
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const uint4 x = *reinterpret_cast<const uint4*>(x_lane[t] + x_at + u * 256 + j * 64);
-            const uint32_t b[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t A[4] = {f[0][2 * i], f[1][2 * i], f[0][2 * i + 1], f[1][2 * i + 1]};
-              if (j == 0 && i == 0) mma_f16_first(sum[t], A, b);
-              else mma_f16(sum[t], A, b + 2 * i);
-            }
+            const float2 s = *reinterpret_cast<const float2*>(scale_of + (u * NT + t) * 8);
+            acc[t][0] += sum[t][0] * s.x, acc[t][1] += sum[t][1] * s.y;
+            acc[t][2] += sum[t][2] * s.x, acc[t][3] += sum[t][3] * s.y;
           }
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float2 s = *reinterpret_cast<const float2*>(scale_of + (u * NT + t) * 8);
-          acc[t][0] += sum[t][0] * s.x, acc[t][1] += sum[t][1] * s.y;
-          acc[t][2] += sum[t][2] * s.x, acc[t][3] += sum[t][3] * s.y;
-        }
+        x_at += 512, scale_of += 16 * NT;
+        if (++stage == a.stages) stage = 0;
       }
-      x_at += 512, scale_of += 16 * NT;
-      if (++stage == a.stages) stage = 0;
-    }
+    };
+    if constexpr (FP8) sweep(std::false_type{});
+    else if (wide) sweep(std::true_type{});
+    else sweep(std::false_type{});
 
     // A warp that has all of K and no activation to do has the result: 16 x 60000 x 256 6.4 us against 11.8 through
     // shared memory. (With the activations here too, their code made every size 0.1 us slower.)
@@ -428,9 +463,9 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
 
 template <int NT, int ALIGN>
 moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
-  if (smem > 48 * 1024)
-    MOE_CUDA(cudaFuncSetAttribute(linear_kernel<NT, ALIGN>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
-  return launch_clusters(linear_kernel<NT, ALIGN>, a.slices, grid, dim3(32 * a.warps), smem, s, a);
+  auto* const kern = a.x_mode == MOE_FP8_NONE ? linear_kernel<NT, ALIGN, false> : linear_kernel<NT, ALIGN, true>;
+  if (smem > 48 * 1024) MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+  return launch_clusters(kern, a.slices, grid, dim3(32 * a.warps), smem, s, a);
 }
 
 // How a product is cut.

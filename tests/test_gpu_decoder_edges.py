@@ -68,3 +68,55 @@ def test_attend_large_queries_along_one_key():
             want[b, 0, h] = v[top]
     out, _ = p.kv.attend(bf16(q), table, ln)
     assert_within(bf16_np(out), want, np.abs(want) * (2.0 ** -8 + 2.0 ** -18), "out")
+
+
+# -------------------------------------------------------------- linear: range of activations
+def zero_weights(data, ks, rows):
+    """Codes of zero at columns ks of the given rows of packed weights."""
+    for k in ks:
+        data[rows, k // 2] &= 0xF0 if k % 2 == 0 else 0x0F
+
+
+@pytest.mark.parametrize("act", ["identity", "swiglu"])
+@pytest.mark.parametrize("M,N,K", [(1, 32, 128), (3, 50, 144), (5, 1000, 512), (12, 300, 2000), (16, 4096, 1024), (8, 100, 2080),
+                                   (2, 4096, 7168), (16, 40006, 528), (12, 60000, 256), (33, 70, 256), (9, 40, 65520)])
+def test_linear_small_values_beside_an_outlier(M, N, K, act):
+    """One value of each 128 is 2^40 (for every other token 2^90, or 1), and half of the rows have zero for its
+    weight: their results are made of the small values alone."""
+    x, _, data, sf, alpha = linear_case(M, N, K, None)
+    r = np.random.default_rng(K)
+    ks = [min(c + int(r.integers(0, 128)), K - 1) for c in range(0, K, 128)]
+    rows = np.arange(0, N // 2 if act == "swiglu" else N, 2)
+    if act == "swiglu":
+        rows = np.r_[rows, rows + N // 2]
+    zero_weights(data, ks, rows)
+    x[::3, ks] = 2.0 ** 40
+    x[1::3, ks] = 2.0 ** 90
+    if act == "swiglu":
+        x[1::3, ks] = -(2.0 ** 50)                          # products of two sums stay in BF16's range
+    got = run_linear(x, None, data, sf, alpha, act)
+    n_out = N // 2 if act == "swiglu" else N
+    cols = np.unique(np.r_[0:min(n_out, 150), max(n_out - 150, 0):n_out, r.integers(0, n_out, 100)])
+    if K > 60000:
+        cols = cols[::4]
+    at = np.r_[cols, cols + n_out] if act == "swiglu" else cols
+    check_linear(got[:, torch.from_numpy(cols).to(DEV)], x, None, data[at], sf[at], alpha, act)
+
+
+@pytest.mark.parametrize("size,outlier,alpha", [(2.0 ** -100, 1.0, 2.0 ** 100), (2.0 ** -60, 2.0 ** 60, 2.0 ** 60), (1.0, 2.0 ** 110, 1.0)])
+@pytest.mark.parametrize("K", [256, 400])
+def test_linear_far_ranges(K, size, outlier, alpha):
+    x, _, data, sf, _ = linear_case(4, 64, K, None)
+    zero_weights(data, [5, K - 3], np.arange(64))
+    x *= size
+    x[:, 5], x[2:, K - 3] = outlier, -outlier
+    x[3, :128] = outlier
+    x[3, 5:100] = size
+    data[:, : 128 // 2][:, ::2] &= 0x0F                    # and zero weights for every fourth of the first 128
+    data[:, : 128 // 2][:, ::2] &= 0xF0
+    got = bf16_np(run_linear(x, None, data, sf, np.float32(alpha)))
+    want, _, mass = D.linear(f32_np(x), data, sf, alpha)
+    over = np.abs(want) > 3.4e38                             # past BF16's range: infinity is its rounding
+    assert np.array_equal(got[over], np.copysign(np.inf, want[over]))
+    got[over], tol = want[over], (K + 16) * U * mass + np.abs(want) * (2.0 ** -8 + 2.0 ** -18) + 1e-30
+    assert_within(got, want, tol)
