@@ -4,6 +4,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4_mma.cuh"
 #include "host_util.h"
@@ -101,8 +103,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 // scores; p = 2^((s - m) f + 15) is rounded to FP16 for the second product (11 significant bits down to
 // 2^-29 of the largest weight), its sum is FP32. Subtracting before multiplying makes the largest weight
 // 2^15 whatever the scores' size; the difference of two rounded scores would be off by whole powers of 2
-// from 2^24 on. It costs an instruction a score. Query rows are scaled by a power of two to a largest value in [2^14, 2^15) so
-// that BF16's exponents fit FP16.
+// from 2^24 on. It costs an instruction a score.
+// Query rows are scaled by a power of two to a largest value in [2^14, 2^15), which BF16's values fit
+// FP16 with, down to 2^-31 of the largest; a block with a smaller one keeps its queries in BF16 and takes
+// BF16 MMAs for the scores, for which the keys take a second conversion.
 //
 // Bound by the conversion (ALU pipe 54 %, issue slots 61 % in use; 17.8 instructions per token and kv head), not by
 // HBM: 64 sequences of 4000 to 8191 tokens, 8 kv heads, 87 us (5.0 TB/s; the copies alone 73 us), one of
@@ -216,9 +220,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     const int at = (toks[i] + 16 * half) >> c.page_shift;
     pages[i] = at < a.max_pages ? table[at] : -1;
   }
-  uint32_t raw[NT][D / 8];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
+  auto query = [&](int t, uint32_t* to) {  // this lane's share of row 8t + r
     const int row = row0 + 8 * t + r, at = row / a.group, g = row - at * a.group;
     const uint4* src = reinterpret_cast<const uint4*>(
         a.q + (static_cast<int64_t>(b) * a.q_len + at) * a.ld_q + (kvh * a.group + g) * D + cc * (D / 4));
@@ -226,9 +228,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     for (int i = 0; i < D / 32; ++i) {
       uint4 u = make_uint4(0, 0, 0, 0);
       if (8 * t + r < rows_here) u = src[i];
-      raw[t][4 * i] = u.x, raw[t][4 * i + 1] = u.y, raw[t][4 * i + 2] = u.z, raw[t][4 * i + 3] = u.w;
+      to[4 * i] = u.x, to[4 * i + 1] = u.y, to[4 * i + 2] = u.z, to[4 * i + 3] = u.w;
     }
-  }
+  };
+  uint32_t raw[NT][D / 8];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) query(t, raw[t]);
   len = max(len, 0);
   const int64_t most = static_cast<int64_t>(a.max_pages) << c.page_shift;
   if (len > most) {
@@ -279,6 +284,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
   // Q^T fragments and each row's factor from raw sums to base-2 scores
   uint32_t q[NT][KS][2];
   float to_log2[NT][2];
+  bool lost = false;  // some value is not exact in FP16
+  // above 0, so that -inf stays -inf; finite, so that no difference stays 0
+  auto factor = [&](float down) { return fminf(fmaxf(fabsf(a.scale) * kLog2e / c.g[0] * down, FLT_MIN), FLT_MAX); };
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float amax = 0.0f;
@@ -288,14 +296,26 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     float up, down;
     f16_range(amax, &up, &down);
-    if (a.scale < 0.0f) up = -up;  // the factor below is never negative
+    if (a.scale < 0.0f) up = -up;  // the factor is never negative
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < D / 8; ++i) {
       q[t][i >> 1][i & 1] = pack_f16x2(bf16_lo(raw[t][i]) * up, bf16_hi(raw[t][i]) * up);
-    // above 0, so that -inf stays -inf; finite, so that no difference stays 0
-    const float f = fminf(fmaxf(fabsf(a.scale) * kLog2e / c.g[0] * down, FLT_MIN), FLT_MAX);
+      lost |= below_f16(raw[t][i], down) && amax < INFINITY;  // a score with an infinity in it needs no other bits
+    }
+    const float f = factor(down);
     to_log2[t][0] = __shfl_sync(0xffffffffu, f, 8 * cc);
     to_log2[t][1] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
+  }
+  const bool in_bf16 = __any_sync(0xffffffffu, lost);  // the same for every warp of the block
+  if (in_bf16) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t again[D / 8];
+      query(t, again);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) q[t][i >> 1][i & 1] = again[i] ^ (a.scale < 0.0f ? 0x80008000u : 0u);
+      to_log2[t][0] = to_log2[t][1] = factor(1.0f);
+    }
   }
 
   float o[NT][KS][4], m[NT][2], l[NT][2];
@@ -320,35 +340,49 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     const uint32_t held = held_next & 0xFFFF;
     // ---- scores
     float s[U][NT][4];
+    auto scores = [&](auto bf) {
+      constexpr bool kBf16 = decltype(bf)::value;
+      if constexpr (kBf16) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t kw[2][KW], sc[2][2];  // [token r or r + 8][...]; a block's scale in both halves
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * u + 8 * h + r;
-        load_words<KW>(kw[h], st + row * (D / 2) + cc * (D / 8));
-        const uint8_t* f = st + 2 * kData + row * (D / 16) + cc * (D / 64);
-        const uint32_t two = e4m3x2_to_f16x2(D == 128 ? *reinterpret_cast<const uint16_t*>(f) : *f);
-        sc[h][0] = __byte_perm(two, two, 0x1010);
-        sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
+        for (int i = 0; i < U * NT * 4; ++i) s[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
       }
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {  // a word is two steps
-        uint32_t f[2][4];
+      for (int u = 0; u < U; ++u) {
+        uint32_t kw[2][KW], sc[2][2];  // [token r or r + 8][...]; a block's scale in both halves
 #pragma unroll
-        for (int h = 0; h < 2; ++h) e2m1x8_to_f16x2(kw[h][w], f[h]);
+        for (int h = 0; h < 2; ++h) {
+          const int row = 16 * u + 8 * h + r;
+          load_words<KW>(kw[h], st + row * (D / 2) + cc * (D / 8));
+          const uint8_t* f = st + 2 * kData + row * (D / 16) + cc * (D / 64);
+          const uint32_t two = e4m3x2_to_f16x2(D == 128 ? *reinterpret_cast<const uint16_t*>(f) : *f);
+          sc[h][0] = __byte_perm(two, two, 0x1010);
+          sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
+        }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t x[4] = {mul_f16x2(f[0][2 * j], sc[0][w / 2]), mul_f16x2(f[1][2 * j], sc[1][w / 2]),
-                                 mul_f16x2(f[0][2 * j + 1], sc[0][w / 2]), mul_f16x2(f[1][2 * j + 1], sc[1][w / 2])};
+        for (int w = 0; w < KW; ++w) {  // a word is two steps
+          uint32_t f[2][4];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (w == 0 && j == 0) mma_f16_first(s[u][t], x, q[t][0]);
-            else mma_f16(s[u][t], x, q[t][2 * w + j]);
+          for (int h = 0; h < 2; ++h) e2m1x8_to_f16x2(kw[h][w], f[h]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t x[4] = {mul_f16x2(f[0][2 * j], sc[0][w / 2]), mul_f16x2(f[1][2 * j], sc[1][w / 2]),
+                                   mul_f16x2(f[0][2 * j + 1], sc[0][w / 2]), mul_f16x2(f[1][2 * j + 1], sc[1][w / 2])};
+            if constexpr (kBf16) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = f16x2_to_bf16x2(x[i]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if constexpr (kBf16) mma_bf16(s[u][t], x, q[t][2 * w + j]);
+              else if (w == 0 && j == 0) mma_f16_first(s[u][t], x, q[t][0]);
+              else mma_f16(s[u][t], x, q[t][2 * w + j]);
+            }
           }
         }
       }
-    }
+    };
+    if (in_bf16) scores(std::true_type{});
+    else scores(std::false_type{});
     // ---- running maximum, weights
     uint32_t vsf[U][4];
 #pragma unroll

@@ -120,3 +120,30 @@ def test_linear_far_ranges(K, size, outlier, alpha):
     assert np.array_equal(got[over], np.copysign(np.inf, want[over]))
     got[over], tol = want[over], (K + 16) * U * mass + np.abs(want) * (2.0 ** -8 + 2.0 ** -18) + 1e-30
     assert_within(got, want, tol)
+
+
+# ------------------------------------------------------------- attention: range of queries
+@pytest.mark.parametrize("scale", [0.2, -0.2])
+@pytest.mark.parametrize("B,Hkv,G,T,Dh,page,n", [(2, 2, 4, 1, 128, 64, 300), (3, 1, 6, 4, 64, 16, 500), (1, 1, 8, 1, 128, 32, 20000),
+                                               (20, 8, 4, 1, 128, 64, 3000), (1, 1, 16, 1, 128, 16, 5000), (1, 1, 24, 1, 64, 64, 4000),
+                                               (1, 1, 12, 1, 64, 64, 900)])
+def test_attend_small_queries_beside_an_outlier(B, Hkv, G, T, Dh, page, n, scale):
+    """Queries with one dimension of 2^40 (or 2^-90 of its size elsewhere) that every key has a zero in: the
+    scores are made of the small values alone."""
+    lens = [n - 7 * b for b in range(B)]
+    p = Pool(sum(-(-m // page) for m in lens), page, Hkv, Dh, 1.0 if G % 8 else 2.5)
+    table, ln, held = sequences(p, lens, seed=n)
+    r = np.random.default_rng(n)
+    d = r.integers(0, Dh, Hkv)
+    for b in range(B):                                      # the stored codes of dimension d, and the oracle's values
+        for h in range(Hkv):
+            held[b][0][:, h, d[h]] = 0.0
+            p.t[0][table[b][table[b] >= 0].long(), h, :, int(d[h]) // 2] &= 0xF0 if d[h] % 2 == 0 else 0x0F
+    q = queries(B, T, Hkv * G, Dh)
+    for h in range(Hkv * G):
+        if h % 3 != 1:
+            q[:, :, h, int(d[h // G])] = 2.0 ** (40 if h % 3 else 100)
+    out, lse = p.kv.attend(q, table, ln, softmax_scale=scale)
+    check_attend(out, lse, q, held, Hkv, scale)
+    again, lse2 = p.kv.attend(q, table, ln, softmax_scale=scale)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
