@@ -2,6 +2,7 @@
 // attention of a decode step that reads it.
 #include <cuda_fp16.h>
 #include <float.h>
+#include <limits.h>
 #include <math.h>
 
 #include <type_traits>
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     l[t][0] = l[t][1] = 0.0f;
   }
 
-  int stage = 0;
+  int stage = 0, no_number = INT_MAX;  // the first token after all_see whose values this lane keeps out
   uint32_t parity = 0;
   auto advance = [&] {
 #pragma unroll
@@ -407,6 +408,17 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 #pragma unroll
         for (int h = 0; h < 4; ++h)
           if (!here || tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1) >= end) vsf[u][h] = 0;
+      }
+      // Of tokens that only some rows see, a scale that is no number is kept from the others too (the MMA
+      // would give them 0 * NaN): the rows that see the first such token get their NaN after the last step.
+      if (all_see < end) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int at = tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1);
+            if (at >= all_see && (vsf[u][h] & 0x7F) == 0x7F) no_number = min(no_number, at), vsf[u][h] = 0;
+          }
       }
     }
     uint32_t p[U][NT][2];
@@ -497,6 +509,18 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     advance();
   }
   __syncthreads();
+
+  if (__any_sync(0xffffffffu, no_number != INT_MAX)) {
+    no_number = min(no_number, __shfl_xor_sync(0xffffffffu, no_number, 1));  // the lanes of the same dimensions
+    no_number = min(no_number, __shfl_xor_sync(0xffffffffu, no_number, 2));
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (no_number < row_limit(a, len, row0 + 8 * t + 2 * cc + i))
+#pragma unroll
+          for (int j = 0; j < KS; ++j) o[t][j][i] = o[t][j][i + 2] = __int_as_float(0x7FC00000);
+  }
 
   // ---- join the warps
   constexpr int ST = D + 4;

@@ -147,3 +147,24 @@ def test_attend_small_queries_beside_an_outlier(B, Hkv, G, T, Dh, page, n, scale
     check_attend(out, lse, q, held, Hkv, scale)
     again, lse2 = p.kv.attend(q, table, ln, softmax_scale=scale)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("Hkv,G,T,Dh,page,lens", [(2, 4, 4, 128, 64, (300, 65, 64, 4)), (1, 8, 5, 128, 16, (1000, 17, 3)),
+                                                 (2, 6, 3, 64, 16, (130, 2)), (1, 2, 16, 64, 64, (90, 16)), (1, 4, 2, 128, 32, (20000, 9000))])
+def test_attend_no_number_of_a_later_token_reaches_an_earlier_row(Hkv, G, T, Dh, page, lens):
+    """Scales that are no numbers at the place of a step's second new token, for one block of 16 values: the rows
+    before it keep their results bit for bit, those from it on have NaN there and nowhere else."""
+    p = Pool(sum(-(-m // page) for m in lens), page, Hkv, Dh)
+    table, ln, _ = sequences(p, list(lens), seed=T)
+    q = queries(len(lens), T, Hkv * G, Dh)
+    ref, ref_lse = (t.clone() for t in p.kv.attend(q, table, ln))
+    want = ref.clone()
+    for b, n in enumerate(lens):
+        at = n - T + 1                                      # the second new token: row 0 does not see it
+        if at < 0:
+            continue
+        p.t[3][int(table[b, at // page]), Hkv - 1, at % page, 1] = 0x7F if b % 2 else 0xFF
+        want[b, 1:, (Hkv - 1) * G:, 16:32] = float("nan")
+    out, lse = p.kv.attend(q, table, ln)
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(lse, ref_lse)
+    assert torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0))
