@@ -3,8 +3,8 @@
 // These operators run for microseconds at decode sizes. Checked in Python and marshalled by
 // ctypes, a call took 7 to 11 us of host time on a GB300 host, more than the kernel; here it
 // takes about 3, of which the launch is 1.5. Each function checks what the C entry point cannot see
-// (types, shapes, strides, device), then makes the one C call on torch's current stream. A wrong tensor
-// raises ValueError, a refusal by the library its MoEError.
+// (types, shapes, strides, and that every tensor lies on the current device), then makes the one C call on
+// torch's current stream. A wrong tensor raises ValueError, a refusal by the library its MoEError.
 #include <Python.h>
 
 #include <c10/cuda/CUDAStream.h>
@@ -60,6 +60,26 @@ float real(PyObject* o) {
   return static_cast<float>(v);
 }
 
+// a launch runs on the current device: pointers into another one's memory are none there
+void check_device(const char* what, long device, long current) {
+  if (device == current) return;
+  PyErr_Format(PyExc_ValueError, "%s is on cuda:%ld, the call would run on cuda:%ld", what, device, current);
+  throw Raised();
+}
+struct Named {
+  const at::Tensor* t;  // may be null
+  const char* what;
+};
+void on_device(std::initializer_list<Named> tensors, long current) {
+  for (const Named& n : tensors)
+    if (n.t) check_device(n.what, n.t->device().index(), current);
+}
+void on_current_device(std::initializer_list<Named> tensors) {  // the first one is never null
+  const long device = tensors.begin()->t->device().index();
+  on_device(tensors, device);
+  check_device(tensors.begin()->what, device, c10::cuda::current_device());
+}
+
 moe_stream_t stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 
 PyObject* done(moe_status_t st, const char* call) {
@@ -93,6 +113,14 @@ PyObject* set_error(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
+// (what, device, current device): refuses a tensor `what` of another device
+PyObject* refuse_device(PyObject* const* a) {
+  const char* what = PyUnicode_AsUTF8(a[0]);
+  if (!what) throw Raised();
+  check_device(what, integer(a[1]), integer(a[2]));
+  Py_RETURN_NONE;
+}
+
 // (x, weight, residual, eps, fp8_scale, y, residual_out, y8, y8_scale)
 PyObject* add_rms_norm(PyObject* const* a) {
   const at::Tensor& x = tensor(a[0], "x");
@@ -112,6 +140,8 @@ PyObject* add_rms_norm(PyObject* const* a) {
   dense(sc, at::kFloat, {M, groups}, "the scales", "contiguous float32 [M, 1] or [M, ceil(H / 128)] on the GPU");
   if ((y8 != nullptr) != (fp8 != MOE_FP8_NONE) || (sc != nullptr) != (fp8 != MOE_FP8_NONE))
     refuse("the FP8 output and its scales", "given with fp8, and only then");
+  on_current_device({{&x, "x"}, {&w, "weight"}, {r, "residual"}, {y, "the output"}, {ro, "the residual's output"},
+                     {y8, "the FP8 output"}, {sc, "the scales"}});
   return done(moe_add_rmsnorm(static_cast<const uint16_t*>(x.data_ptr()), ld(x, H), static_cast<const uint16_t*>(pointer(r)),
                               r ? ld(*r, H) : H, static_cast<const uint16_t*>(w.data_ptr()), int32_size(M, "x"),
                               int32_size(H, "x"), real(a[3]), static_cast<int32_t>(fp8), static_cast<uint16_t*>(pointer(y)),
@@ -144,6 +174,7 @@ PyObject* fp4_linear(PyObject* const* a) {
   if (gated && N % 2) refuse("w", "of an even number of rows for a gated activation");
   const at::Tensor& out = tensor(a[6], "out");
   dense(&out, kBf16, {M, gated ? N / 2 : N}, "out", "contiguous bf16 [M, N] (gated: [M, N/2]) on the GPU");
+  on_current_device({{&x, "x"}, {xs, "x_scale"}, {&w, "w"}, {&sf, "w_sf"}, {&alpha, "alpha"}, {&out, "out"}});
   return done(moe_linear_fp4(x.data_ptr(), ld(x, K), static_cast<const float*>(pointer(xs)), mode, int32_size(M, "x"),
                              int32_size(K, "x"), static_cast<const uint8_t*>(w.data_ptr()),
                              static_cast<const uint8_t*>(sf.data_ptr()), static_cast<const float*>(alpha.data_ptr()),
@@ -155,6 +186,7 @@ PyObject* fp4_linear(PyObject* const* a) {
 struct Cache {
   moe_kv_cache_t c;
   int32_t* status;
+  long device;
 };
 const char* const kCapsule = "moe_kv_cache";
 
@@ -180,10 +212,12 @@ PyObject* kv_cache(PyObject* const* a) {
                                   "page contiguous, with the same strides for keys and values");
   if (status && (status->scalar_type() != at::kInt || !status->is_cuda() || status->numel() < 1))
     refuse("dev_status", "int32 on the GPU");
+  const long device = k.device().index();
+  on_device({{&ks, "k_sf"}, {&v, "v"}, {&vs, "v_sf"}, {status, "dev_status"}}, device);
   const auto p = [](const at::Tensor& t) { return static_cast<uint8_t*>(t.data_ptr()); };
   auto* c = new Cache{{p(k), p(ks), p(v), p(vs), int32_size(P, "k"), int32_size(S, "k"), int32_size(H, "k"),
                        int32_size(2 * half, "k"), k.stride(0), ks.stride(0), real(a[4]), real(a[5])},
-                      static_cast<int32_t*>(pointer(status))};
+                      static_cast<int32_t*>(pointer(status)), device};
   PyObject* o = PyCapsule_New(c, kCapsule, drop_cache);
   if (!o) {
     delete c;
@@ -204,6 +238,8 @@ PyObject* kv_append(PyObject* const* a) {
   const at::Tensor *ks = maybe(a[4], "seen[0]"), *vs = maybe(a[5], "seen[1]");
   dense(ks, kBf16, {N, H, D}, "seen[0]", "contiguous bf16 of k_new's shape on the GPU");
   dense(vs, kBf16, {N, H, D}, "seen[1]", "contiguous bf16 of k_new's shape on the GPU");
+  on_current_device({{&k, "k_new"}, {&v, "v_new"}, {&slots, "slots"}, {ks, "seen[0]"}, {vs, "seen[1]"}});
+  check_device("the cache", c.device, k.device().index());
   return done(moe_kv_append(&c.c, static_cast<const uint16_t*>(k.data_ptr()), ld(k, H * D),
                             static_cast<const uint16_t*>(v.data_ptr()), ld(v, H * D),
                             static_cast<const int64_t*>(slots.data_ptr()), int32_size(N, "k_new"),
@@ -225,6 +261,8 @@ Queries queries(const Cache& c, const at::Tensor& q, const at::Tensor& table) {
     refuse("q", "of contiguous rows [num_q_heads, head_dim] that are evenly spaced");
   if (table.dim() != 2 || !is(table, at::kInt, {B, table.size(1)}) || (table.stride(1) != 1 && table.size(1) > 1))
     refuse("page_table", "int32 [batch, max_pages] on the GPU, a sequence's pages side by side");
+  on_current_device({{&q, "q"}, {&table, "page_table"}});
+  check_device("the cache", c.device, q.device().index());
   return {int32_size(B, "q"), int32_size(T, "q"), int32_size(H, "q"), int32_size(table.size(1), "page_table"), step,
           ld(table, table.size(1))};
 }
@@ -246,6 +284,7 @@ PyObject* kv_attend(PyObject* const* a) {
   dense(&out, kBf16, {n.batch, n.q_len, n.heads, c.c.head_dim}, "out", "contiguous bf16 of q's shape on the GPU");
   dense(lse, at::kFloat, {n.batch, n.q_len, n.heads}, "lse", "contiguous float32 [batch, q_len, num_q_heads] on the GPU");
   if (ws && !(ws->is_cuda() && ws->is_contiguous())) refuse("workspace", "contiguous on the GPU");
+  on_device({{&lens, "seq_lens"}, {&out, "out"}, {lse, "lse"}, {ws, "workspace"}}, q.device().index());
   return done(moe_kv_attend(&c.c, static_cast<const uint16_t*>(q.data_ptr()), n.ld_q, n.batch, n.q_len, n.heads,
                             static_cast<const int32_t*>(table.data_ptr()), n.ld_table, n.pages,
                             static_cast<const int32_t*>(lens.data_ptr()), real(a[4]), static_cast<uint16_t*>(out.data_ptr()),
@@ -254,7 +293,7 @@ PyObject* kv_attend(PyObject* const* a) {
 }
 
 #define ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(set_error, 1), ENTRY(add_rms_norm, 9), ENTRY(fp4_linear, 7), ENTRY(kv_cache, 7),
+PyMethodDef methods[] = {ENTRY(set_error, 1), ENTRY(refuse_device, 3), ENTRY(add_rms_norm, 9), ENTRY(fp4_linear, 7), ENTRY(kv_cache, 7),
                          ENTRY(kv_append, 6), ENTRY(kv_workspace, 3), ENTRY(kv_attend, 8), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "calls of libmoe_nvfp4 on torch tensors", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,63 @@
+"""The Python layer of the operators around the routed experts: what it checks and keeps on the host."""
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+import nvfp4_routed_moe_sort_gb300 as pkg  # noqa: F401  (the package must be importable without a GPU)
+from nvfp4_routed_moe_sort_gb300 import decoder
+from nvfp4_routed_moe_sort_gb300.build import build
+
+
+@pytest.fixture(scope="module")
+def native():
+    build()
+    return decoder._load()
+
+
+def test_a_tensor_of_another_device_is_refused(native):
+    native.refuse_device("w", 0, 0)
+    native.refuse_device("w", 3, 3)
+    for device, current in ((1, 0), (0, 1), (7, 2)):
+        with pytest.raises(ValueError, match=f"w is on cuda:{device}, the call would run on cuda:{current}"):
+            native.refuse_device("w", device, current)
+
+
+# tensors that say they are on a GPU and have no memory: what is refused never touches them
+host_only = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up devices")
+
+
+def _elsewhere(make, names):
+    """(name, arguments of which that one alone is on cuda:1) for each of `names`; `make(device_of)` makes them."""
+    for name in names:
+        with FakeTensorMode():
+            yield name, make(lambda n, name=name: "cuda:1" if n == name else "cuda:0")
+
+
+@host_only
+def test_tensors_of_two_devices_are_refused(native):
+    bf, f8, f32, u8 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.uint8
+
+    def norm(on):
+        t = lambda name, shape, dtype: torch.empty(shape, dtype=dtype, device=on(name))  # noqa: E731
+        return dict(x=t("x", (4, 256), bf), weight=t("weight", (256,), bf), residual=t("residual", (4, 256), bf), fp8="group",
+                    out=(t("the output", (4, 256), bf), t("the residual's output", (4, 256), bf),
+                         t("the FP8 output", (4, 256), f8), t("the scales", (4, 2), f32)))
+    for name, kw in _elsewhere(norm, ["weight", "residual", "the output", "the residual's output", "the FP8 output", "the scales"]):
+        with pytest.raises(ValueError, match=f"{name} is on cuda:1"):
+            pkg.add_rms_norm(**kw)
+
+    def linear(on):
+        t = lambda name, shape, dtype: torch.empty(shape, dtype=dtype, device=on(name))  # noqa: E731
+        return dict(x=t("x", (4, 256), f8), w=t("w", (32, 128), u8), w_sf=t("w_sf", (32, 16), u8), alpha=t("alpha", (1,), f32),
+                    x_scale=t("x_scale", (4, 2), f32), out=t("out", (4, 32), bf))
+    for name, kw in _elsewhere(linear, ["w", "w_sf", "alpha", "x_scale", "out"]):
+        with pytest.raises(ValueError, match=f"{name} is on cuda:1"):
+            pkg.fp4_linear(**kw)
+
+    def cache(on):
+        t = lambda name, shape, dtype=u8: torch.empty(shape, dtype=dtype, device=on(name))  # noqa: E731
+        return dict(k=t("k", (3, 2, 16, 32)), k_sf=t("k_sf", (3, 2, 16, 4)), v=t("v", (3, 2, 16, 32)), v_sf=t("v_sf", (3, 2, 16, 4)),
+                    dev_status=t("dev_status", (4,), torch.int32))
+    for name, kw in _elsewhere(cache, ["k_sf", "v", "v_sf", "dev_status"]):
+        with pytest.raises(ValueError, match=f"{name} is on cuda:1"):
+            pkg.NVFP4KVCache(**kw)
