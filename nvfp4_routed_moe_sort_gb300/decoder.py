@@ -8,6 +8,7 @@ torch's current stream, and only results that the caller did not bring are alloc
 from __future__ import annotations
 
 import threading
+from operator import attrgetter
 
 import torch
 
@@ -115,13 +116,18 @@ class NVFP4KVCache:
 
     k, v [num_pages, num_kv_heads, page_size, head_dim/2] u8; k_sf, v_sf [..., head_dim/16] u8;
     the pages of k and v (of k_sf and v_sf) have the same stride. k_scale, v_scale: static FP32
-    encode scales. dev_status: an int32 tensor whose first element collects MOE_DEV_* bits.
+    encode scales. dev_status: an int32 tensor whose first element collects MOE_DEV_* bits. All of
+    them stay what they are: other pages or scales are another cache.
     """
 
+    k, k_sf, v, v_sf, k_scale, v_scale, dev_status = (
+        property(attrgetter("_" + name)) for name in ("k", "k_sf", "v", "v_sf", "k_scale", "v_scale", "dev_status"))
+
     def __init__(self, k, k_sf, v, v_sf, k_scale: float = 1.0, v_scale: float = 1.0, dev_status=None):
+        # holds the tensors' addresses, so the tensors are held beside it and never exchanged
         self._native = (_native or _load()).kv_cache(k, k_sf, v, v_sf, k_scale, v_scale, dev_status)
-        self.k, self.k_sf, self.v, self.v_sf, self.dev_status = k, k_sf, v, v_sf, dev_status
-        self.k_scale, self.v_scale = k_scale, v_scale
+        self._k, self._k_sf, self._v, self._v_sf, self._dev_status = k, k_sf, v, v_sf, dev_status
+        self._k_scale, self._v_scale = k_scale, v_scale
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, device="cuda",

@@ -61,3 +61,11 @@ def test_tensors_of_two_devices_are_refused(native):
     for name, kw in _elsewhere(cache, ["k_sf", "v", "v_sf", "dev_status"]):
         with pytest.raises(ValueError, match=f"{name} is on cuda:1"):
             pkg.NVFP4KVCache(**kw)
+
+
+@pytest.mark.parametrize("name", ["k", "k_sf", "v", "v_sf", "k_scale", "v_scale", "dev_status"])
+def test_a_cache_keeps_what_it_was_made_from(name):
+    """The native object has the addresses and scales: exchanging the tensor here would leave it with freed memory."""
+    cache = object.__new__(pkg.NVFP4KVCache)
+    with pytest.raises(AttributeError):
+        setattr(cache, name, torch.zeros(1))
