@@ -5,7 +5,7 @@
  * kernel with the defaults below. The test library holds the same kernels and every
  * entry point of moe_nvfp4.h, plus these calls, which let tests reach paths that normal
  * inputs never take: a GEMM1 with plain epilogues, the decode GEMM's scheduling
- * fallbacks, and the bounded waits of the GEMM kernels running out.
+ * fallbacks, and the bounded waits of the GEMM kernels running out; and the rule that cuts the NVFP4 linear.
  *
  * None of these calls keeps state between calls either: every option is an argument.
  */
@@ -53,6 +53,13 @@ MOE_API moe_status_t moe_test_routed_forward(const uint16_t* x, int32_t M, int64
                                              int32_t* dev_status, void* const* step_events,
                                              int32_t num_step_events, const moe_test_options_t* options,
                                              moe_stream_t stream);
+
+/* The cut that moe_linear_fp4 would take for M tokens and w [N, K] (gated: its rows are [gate; up]) on a GPU
+ * of num_sms SMs; a host function. cut (9 int32 in host memory): tokens of a block, its warps, warps to the same rows,
+ * blocks of a cluster, chunks of 128 values of each, stages of a ring, buffers of sums, clusters that run at
+ * once, groups of tokens. */
+MOE_API moe_status_t moe_test_linear_cut(int32_t M, int32_t K, int32_t N, int32_t gated, int32_t num_sms,
+                                         int32_t* cut);
 
 /* The forward's permute and GEMM1 with a plain epilogue instead of the fused requantiser,
  * so tests can compare GEMM1 with the oracle before the activation and the requantiser.

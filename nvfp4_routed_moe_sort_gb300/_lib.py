@@ -40,7 +40,7 @@ EXPORTED = [
     "moe_add_rmsnorm", "moe_linear_fp4", "moe_kv_append", "moe_kv_attend_workspace_bytes", "moe_kv_attend",
 ]
 # the test build's extra entry points (include/moe_nvfp4_test.h)
-TEST_EXPORTED = ["moe_test_default_options", "moe_test_routed_forward", "moe_test_gemm1"]
+TEST_EXPORTED = ["moe_test_default_options", "moe_test_routed_forward", "moe_test_gemm1", "moe_test_linear_cut"]
 MOE_PLAN_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 
@@ -114,6 +114,7 @@ def _declare(lib, test=False):
         sig.update({
             "moe_test_default_options": (TestOptionsT, []),
             "moe_test_routed_forward": (c_int32, routed + [ctypes.POINTER(TestOptionsT), P]),
+            "moe_test_linear_cut": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, ctypes.POINTER(c_int32)]),
             "moe_test_gemm1": (c_int32, [P, P, c_int32, c_int32, P, P, P, ctypes.POINTER(WeightsT), P,
                                          c_size_t, c_int32, P, P, c_size_t, P, P]),
         })
@@ -383,6 +384,13 @@ def moe_kv_attend(cache: KVCacheT, q, ld_q, page_table, seq_lens, softmax_scale,
         dev_status.data_ptr() if dev_status is not None else None, _stream(stream))
     if st:
         _check(st, "moe_kv_attend")
+
+
+def linear_cut(M, K, N, gated=False, num_sms=152) -> dict:
+    """Test build: how moe_linear_fp4 cuts a product (moe_test_linear_cut)."""
+    out = (c_int32 * 9)()
+    _check(test_lib().moe_test_linear_cut(M, K, N, gated, num_sms, out), "moe_test_linear_cut")
+    return dict(zip(("tokens", "warps", "across", "slices", "slice", "stages", "buffers", "at_once", "groups"), out))
 
 
 def moe_test_gemm1(padded_offsets, row_to_slot, M, top_k, xq, xsf, xs, w: WeightsT, prepared, mode,

@@ -35,13 +35,11 @@
 #include "common.cuh"
 #include "fp4_mma.cuh"
 #include "host_util.h"
+#include "linear_cut.h"
 
 namespace moe {
 namespace {
 
-constexpr int kLinWarps = 16;             // most warps of a block, and of an SM: 128 registers a thread
-constexpr int kLinTokens = 16;
-constexpr int kLinChunk = 128;            // = MOE_FP8_GROUP
 static_assert(kLinChunk == MOE_FP8_GROUP, "one E4M3 scale per chunk");
 
 struct LinArgs {
@@ -95,14 +93,6 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// How rows are aligned: K % 256 == 0 (codes and scales to 16 bytes), K % 32 == 0 (codes to 16, scales to
-// 2), or only K % 16 == 0 (codes to 8, scales to 1). Copies are of 16 aligned bytes; where a row
-// starts inside such a piece, one more of them is copied and the row is read at its offset.
-enum Align : int { kAlign256, kAlign32, kAlign16 };
-__host__ __device__ constexpr int code_row(int align) { return align == kAlign16 ? 144 : 128; }
-__host__ __device__ constexpr int scale_row(int align) { return align == kAlign256 ? 16 : 48; }
-__host__ __device__ constexpr int stage_bytes(int align) { return 16 * (code_row(align) + scale_row(align)); }
 
 // NT: groups of eight tokens; FP8: x is E4M3 with scales, else BF16
 template <int NT, int ALIGN, bool FP8>
@@ -468,16 +458,11 @@ moe_status_t launch_linear(const LinArgs& a, dim3 grid, size_t smem, cudaStream_
   return launch_clusters(kern, a.slices, grid, dim3(32 * a.warps), smem, s, a);
 }
 
-// How a product is cut.
-struct LinCut {
-  int tokens, warps, across, slices, slice, stages, buffers;
-  int at_once;  // clusters that run at once
-  int64_t groups;
-};
+}  // namespace
 
 constexpr int kLinSmem = 227 * 1024, kLinSmemSm = 228 * 1024;  // of a block; of an SM, 1 KB taken by each block
 
-int linear_smem(const LinCut& k, int align) {
+static int linear_smem(const LinCut& k, int align) {
   const int columns = k.tokens > 8 ? 16 : 8;
   return k.tokens * (k.slice * kLinChunk * 2 + 64) + k.slice * columns * 4 + k.buffers * 16 * k.warps * (columns + 1) * 4 +
          k.warps * k.stages * stage_bytes(align);
@@ -523,14 +508,15 @@ bool cut_linear(int64_t M, int K, int n_out, bool gated, int align, int sms, Lin
         if (smem > kLinSmem && k.slices == 1) k.buffers = 1, smem = linear_smem(k, align);  // a cluster needs both
         if (smem > kLinSmem) continue;
         const int fit = kLinSmemSm / (smem + 1024), most = kLinWarps / k.warps, per_sm = fit < most ? fit : most;
-        // SMs that clusters of 4 and 8 leave over (the occupancy query's answer): 8 and 32 of 152 at one block to an SM,
-        // half and a quarter of that otherwise
-        const int odd = k.slices == 8 ? (per_sm == 1 ? 32 : 8) : k.slices == 4 ? (per_sm == 1 ? 8 : 4) : 0;
-        k.at_once = (sms - odd) * per_sm / k.slices;
+        // SMs that clusters of 4 and 8 leave over (the occupancy query's answer for 152): 8 and 32 at one block to an
+        // SM, half and a quarter of that otherwise; the same share of fewer
+        const int alone_over = k.slices == 8 ? sms * 4 / 19 : k.slices == 4 ? sms / 19 : 0;
+        const int over = per_sm == 1 ? alone_over : k.slices == 8 ? sms / 19 : k.slices == 4 ? sms / 38 : 0;
+        k.at_once = (sms - over) * per_sm / k.slices;
         if (k.at_once < 1) continue;
         const int64_t blocks = (static_cast<int64_t>(n_out) + n_per - 1) / n_per * k.groups;
         const int first = static_cast<int>(blocks < k.at_once ? blocks : k.at_once) * k.slices;
-        const int spread = sms - (k.slices == 8 ? 32 : k.slices == 4 ? 8 : 0);
+        const int spread = sms - alone_over;
         const int on_sm = (first + spread - 1) / spread < per_sm ? (first + spread - 1) / spread : per_sm;
         const float turns = static_cast<float>((blocks + k.at_once - 1) / k.at_once);
         int run = ((k.slice + k.across - 1) / k.across + 1) & ~1;
@@ -549,6 +535,8 @@ bool cut_linear(int64_t M, int K, int n_out, bool gated, int align, int sms, Lin
     k.tokens = 8;  // the longest K: x of 16 tokens does not fit
   }
 }
+
+namespace {
 
 // The estimates take 2 us of host time, so a thread keeps the cuts of the sizes it last asked for (a decoder's
 // handful); they follow from the sizes alone.
@@ -590,8 +578,7 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
   MOE_CHECK(aligned16(x) && aligned16(x_scale) && aligned16(w) && aligned16(w_sf) && aligned16(alpha) &&
                 aligned16(out) && ld_x % (fp8 ? 16 : 8) == 0,
             MOE_ERR_MISALIGNED);
-  const int chunks = (K + kLinChunk - 1) / kLinChunk, n_out = gated ? N / 2 : N;
-  const int align = K % 256 == 0 ? kAlign256 : K % 32 == 0 ? kAlign32 : kAlign16;
+  const int chunks = (K + kLinChunk - 1) / kLinChunk, n_out = gated ? N / 2 : N, align = align_of(K);
   LinCut cut;
   MOE_CHECK(cut_of(M, K, n_out, gated, align, num_sms(), &cut) && cut.groups <= 65535, MOE_ERR_UNSUPPORTED_SHAPE);
   const LinArgs a = {x, x_scale, w, w_sf, alpha, out, ld_x, x_scale_mode, M, K, n_out, activation,

@@ -2,11 +2,12 @@
 //
 // They reach paths that normal inputs never take: a standalone GEMM1 with plain epilogues
 // (FP32 pre-activations, BF16 intermediate), the decode GEMM's scheduling fallbacks, and the
-// GEMM kernels' bounded waits running out. Every option is an argument; nothing here keeps
-// state between calls.
+// GEMM kernels' bounded waits running out; and they show the rule that cuts the NVFP4 linear. Every
+// option is an argument; nothing here keeps state between calls.
 #include <string.h>
 
 #include "../../../include/moe_nvfp4_test.h"
+#include "../linear_cut.h"
 #include "gemm_plain.cuh"
 
 namespace moe {
@@ -107,4 +108,16 @@ extern "C" moe_status_t moe_test_gemm1(const int32_t* padded_offsets, const int3
   g1.out = dbg_out;
   g1.out_sf = nullptr;
   return launch_gemm1_plain(g1, s);
+}
+
+extern "C" moe_status_t moe_test_linear_cut(int32_t M, int32_t K, int32_t N, int32_t gated, int32_t num_sms,
+                                            int32_t* cut) {
+  MOE_CHECK(M >= 1 && K >= 16 && K % kBlock == 0 && N >= 1 && (!gated || N % 2 == 0) && num_sms >= 1 && cut != nullptr,
+            MOE_ERR_INVALID_ARGUMENT);
+  LinCut k;
+  MOE_CHECK(cut_linear(M, K, gated ? N / 2 : N, gated != 0, align_of(K), num_sms, &k), MOE_ERR_UNSUPPORTED_SHAPE);
+  const int32_t all[9] = {k.tokens, k.warps, k.across, k.slices, k.slice, k.stages, k.buffers, k.at_once,
+                          static_cast<int32_t>(k.groups)};
+  memcpy(cut, all, sizeof(all));
+  return MOE_OK;
 }

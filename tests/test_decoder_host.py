@@ -69,3 +69,22 @@ def test_a_cache_keeps_what_it_was_made_from(name):
     cache = object.__new__(pkg.NVFP4KVCache)
     with pytest.raises(AttributeError):
         setattr(cache, name, torch.zeros(1))
+
+
+def test_the_linears_cut_on_any_number_of_sms(native):
+    """The rule holds on a part of a GPU too: every cut fits, and clusters that run at once are some."""
+    from nvfp4_routed_moe_sort_gb300._lib import linear_cut
+    sizes = [(1, 16, 1, False), (1, 512, 2048, False), (8, 7168, 4096, True), (13, 2000, 7001, False), (16, 4096, 16384, False),
+             (4, 4096, 129021, False), (2, 40000, 33, False), (16, 32784, 20000, True), (40, 1040, 40006, True), (5, 208, 74, True)]
+    for sms in range(1, 200):
+        for M, K, N, gated in sizes:
+            try:
+                c = linear_cut(M, K, N, gated, sms)
+            except pkg.MoEError:
+                assert sms < 10 and K > 30000, (sms, M, K, N)   # so long an x needs a cluster of up to 8 SMs
+                continue
+            assert 1 <= c["at_once"] <= sms * 16 and c["slices"] in (1, 2, 4, 8) and 2 <= c["warps"] <= 16, (sms, M, K, N, c)
+            assert c["warps"] % c["across"] == 0 and c["slices"] * c["slice"] * 128 >= K and c["groups"] * c["tokens"] >= M
+            assert c["slices"] <= sms * (16 // c["warps"])     # a cluster finds room
+            tiles = c["warps"] // c["across"]
+            assert tiles % (2 if gated else 1) == 0 and (c["slices"] > 1 or tiles // (2 if gated else 1) <= 15)
