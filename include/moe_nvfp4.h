@@ -399,7 +399,8 @@ MOE_API moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ld_x, const uint
  *   x          [M, ld_x] BF16 (x_scale_mode MOE_FP8_NONE; ld_x % 8 == 0) or E4M3 (MOE_FP8_PER_TOKEN
  *              or MOE_FP8_PER_GROUP; ld_x % 16 == 0), first K columns used. The activations are
  *              not rounded any further; E4M3 values are multiplied by their scale in FP32
- *   x_scale    [M] or [M, ceil(K / 128)] FP32, NULL for BF16
+ *   x_scale    [M] or [M, ceil(K / 128)] FP32, NULL for BF16; aligned to 4 bytes (rows of another matrix's
+ *              scales will do)
  *   w, w_sf    [N, K/2] packed E2M1 and [N, K/16] E4M3, linear, as moe_quantize_weights writes them
  *   alpha      device scalar (FP32), the matrix's global decode scale
  *   activation moe_activation_t. The gated kinds take w rows [gate; up] (N even) and write N/2

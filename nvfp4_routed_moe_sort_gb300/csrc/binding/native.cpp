@@ -175,9 +175,11 @@ PyObject* fp4_linear(PyObject* const* a) {
   const at::Tensor& out = tensor(a[6], "out");
   dense(&out, kBf16, {M, gated ? N / 2 : N}, "out", "contiguous bf16 [M, N] (gated: [M, N/2]) on the GPU");
   on_current_device({{&x, "x"}, {xs, "x_scale"}, {&w, "w"}, {&sf, "w_sf"}, {&alpha, "alpha"}, {&out, "out"}});
+  // one of several matrices' scalars lies where it lies; the C entry wants 16-byte alignment, and gets a copy
+  const at::Tensor scalar = reinterpret_cast<uintptr_t>(alpha.data_ptr()) % 16 ? alpha.clone() : alpha;
   return done(moe_linear_fp4(x.data_ptr(), ld(x, K), static_cast<const float*>(pointer(xs)), mode, int32_size(M, "x"),
                              int32_size(K, "x"), static_cast<const uint8_t*>(w.data_ptr()),
-                             static_cast<const uint8_t*>(sf.data_ptr()), static_cast<const float*>(alpha.data_ptr()),
+                             static_cast<const uint8_t*>(sf.data_ptr()), static_cast<const float*>(scalar.data_ptr()),
                              int32_size(N, "w"), static_cast<int32_t>(act), static_cast<uint16_t*>(out.data_ptr()), stream()),
               "moe_linear_fp4");
 }

@@ -575,8 +575,8 @@ extern "C" moe_status_t moe_linear_fp4(const void* x, int64_t ld_x, const float*
   if (M == 0) return MOE_OK;
   const bool fp8 = x_scale_mode != MOE_FP8_NONE;
   MOE_CHECK(x && w && w_sf && alpha && out && fp8 == (x_scale != nullptr), MOE_ERR_INVALID_ARGUMENT);
-  MOE_CHECK(aligned16(x) && aligned16(x_scale) && aligned16(w) && aligned16(w_sf) && aligned16(alpha) &&
-                aligned16(out) && ld_x % (fp8 ? 16 : 8) == 0,
+  MOE_CHECK(aligned16(x) && reinterpret_cast<uintptr_t>(x_scale) % sizeof(float) == 0 && aligned16(w) && aligned16(w_sf) &&
+                aligned16(alpha) && aligned16(out) && ld_x % (fp8 ? 16 : 8) == 0,
             MOE_ERR_MISALIGNED);
   const int chunks = (K + kLinChunk - 1) / kLinChunk, n_out = gated ? N / 2 : N, align = align_of(K);
   LinCut cut;

@@ -84,7 +84,8 @@ def fp4_linear(x: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, alpha: torc
 
     x [M, K]: bf16, or float8_e4m3fn with x_scale f32 [M, 1] or [M, ceil(K / 128)] (as add_rms_norm
     gives them); it may have a row stride. Gated activations take w rows [gate; up]. Returns [M, N]
-    (gated: [M, N / 2]) bf16.
+    (gated: [M, N / 2]) bf16. alpha may be an element of a longer tensor; one that is not 16-byte aligned
+    is copied in every call.
     """
     act = L.ACTIVATIONS.get(activation)
     if act is None:

@@ -168,3 +168,16 @@ def test_attend_no_number_of_a_later_token_reaches_an_earlier_row(Hkv, G, T, Dh,
     out, lse = p.kv.attend(q, table, ln)
     assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(lse, ref_lse)
     assert torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+# ------------------------------------------------------------------- linear: slices
+def test_linear_of_one_of_several_matrices_and_of_some_of_the_tokens():
+    """alpha, x and its scales as slices of what quantize_weights and add_rms_norm give for several."""
+    r = np.random.default_rng(12)
+    w = bf16(r.normal(size=(5, 96, 256)) * (1 + np.arange(5))[:, None, None])
+    data, sf, alpha = pkg.quantize_weights(w)
+    _, _, x8, scale = pkg.add_rms_norm(bf16(r.normal(size=(7, 256))), bf16(np.ones(256)), fp8="group")
+    for e in range(5):
+        lin = pkg.NVFP4Linear(data[e], sf[e], alpha[e:e + 1])
+        for m in range(7):
+            check_linear(lin(x8[m:], scale[m:]), x8[m:], to_np(scale[m:]), to_np(data[e]), to_np(sf[e]), float(alpha[e]))
