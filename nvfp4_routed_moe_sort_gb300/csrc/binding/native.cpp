@@ -74,13 +74,13 @@ void on_device(std::initializer_list<Named> tensors, long current) {
   for (const Named& n : tensors)
     if (n.t) check_device(n.what, n.t->device().index(), current);
 }
-void on_current_device(std::initializer_list<Named> tensors) {  // the first one is never null
-  const long device = tensors.begin()->t->device().index();
+// checks them, and gives torch's current stream on that device; the first one is never null
+moe_stream_t stream_of(std::initializer_list<Named> tensors) {
+  const c10::DeviceIndex device = tensors.begin()->t->device().index();
   on_device(tensors, device);
   check_device(tensors.begin()->what, device, c10::cuda::current_device());
+  return c10::cuda::getCurrentCUDAStream(device).stream();
 }
-
-moe_stream_t stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 
 PyObject* done(moe_status_t st, const char* call) {
   if (st == MOE_OK) Py_RETURN_NONE;
@@ -113,6 +113,16 @@ PyObject* set_error(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
+// () -> what no other stream of this process is ever called, unlike its handle
+PyObject* stream_id(PyObject* const*) {
+  unsigned long long id = 0;
+  if (cudaStreamGetId(c10::cuda::getCurrentCUDAStream().stream(), &id) != cudaSuccess) {
+    PyErr_SetString(PyExc_RuntimeError, "cudaStreamGetId failed");
+    throw Raised();
+  }
+  return PyLong_FromUnsignedLongLong(id);
+}
+
 // (what, device, current device): refuses a tensor `what` of another device
 PyObject* refuse_device(PyObject* const* a) {
   const char* what = PyUnicode_AsUTF8(a[0]);
@@ -140,13 +150,14 @@ PyObject* add_rms_norm(PyObject* const* a) {
   dense(sc, at::kFloat, {M, groups}, "the scales", "contiguous float32 [M, 1] or [M, ceil(H / 128)] on the GPU");
   if ((y8 != nullptr) != (fp8 != MOE_FP8_NONE) || (sc != nullptr) != (fp8 != MOE_FP8_NONE))
     refuse("the FP8 output and its scales", "given with fp8, and only then");
-  on_current_device({{&x, "x"}, {&w, "weight"}, {r, "residual"}, {y, "the output"}, {ro, "the residual's output"},
-                     {y8, "the FP8 output"}, {sc, "the scales"}});
+  const moe_stream_t stream =
+      stream_of({{&x, "x"}, {&w, "weight"}, {r, "residual"}, {y, "the output"}, {ro, "the residual's output"},
+                 {y8, "the FP8 output"}, {sc, "the scales"}});
   return done(moe_add_rmsnorm(static_cast<const uint16_t*>(x.data_ptr()), ld(x, H), static_cast<const uint16_t*>(pointer(r)),
                               r ? ld(*r, H) : H, static_cast<const uint16_t*>(w.data_ptr()), int32_size(M, "x"),
                               int32_size(H, "x"), real(a[3]), static_cast<int32_t>(fp8), static_cast<uint16_t*>(pointer(y)),
                               static_cast<uint16_t*>(pointer(ro)), static_cast<uint8_t*>(pointer(y8)),
-                              static_cast<float*>(pointer(sc)), stream()),
+                              static_cast<float*>(pointer(sc)), stream),
               "moe_add_rmsnorm");
 }
 
@@ -174,13 +185,14 @@ PyObject* fp4_linear(PyObject* const* a) {
   if (gated && N % 2) refuse("w", "of an even number of rows for a gated activation");
   const at::Tensor& out = tensor(a[6], "out");
   dense(&out, kBf16, {M, gated ? N / 2 : N}, "out", "contiguous bf16 [M, N] (gated: [M, N/2]) on the GPU");
-  on_current_device({{&x, "x"}, {xs, "x_scale"}, {&w, "w"}, {&sf, "w_sf"}, {&alpha, "alpha"}, {&out, "out"}});
+  const moe_stream_t stream =
+      stream_of({{&x, "x"}, {xs, "x_scale"}, {&w, "w"}, {&sf, "w_sf"}, {&alpha, "alpha"}, {&out, "out"}});
   // one of several matrices' scalars lies where it lies; the C entry wants 16-byte alignment, and gets a copy
   const at::Tensor scalar = reinterpret_cast<uintptr_t>(alpha.data_ptr()) % 16 ? alpha.clone() : alpha;
   return done(moe_linear_fp4(x.data_ptr(), ld(x, K), static_cast<const float*>(pointer(xs)), mode, int32_size(M, "x"),
                              int32_size(K, "x"), static_cast<const uint8_t*>(w.data_ptr()),
                              static_cast<const uint8_t*>(sf.data_ptr()), static_cast<const float*>(scalar.data_ptr()),
-                             int32_size(N, "w"), static_cast<int32_t>(act), static_cast<uint16_t*>(out.data_ptr()), stream()),
+                             int32_size(N, "w"), static_cast<int32_t>(act), static_cast<uint16_t*>(out.data_ptr()), stream),
               "moe_linear_fp4");
 }
 
@@ -240,12 +252,13 @@ PyObject* kv_append(PyObject* const* a) {
   const at::Tensor *ks = maybe(a[4], "seen[0]"), *vs = maybe(a[5], "seen[1]");
   dense(ks, kBf16, {N, H, D}, "seen[0]", "contiguous bf16 of k_new's shape on the GPU");
   dense(vs, kBf16, {N, H, D}, "seen[1]", "contiguous bf16 of k_new's shape on the GPU");
-  on_current_device({{&k, "k_new"}, {&v, "v_new"}, {&slots, "slots"}, {ks, "seen[0]"}, {vs, "seen[1]"}});
+  const moe_stream_t stream =
+      stream_of({{&k, "k_new"}, {&v, "v_new"}, {&slots, "slots"}, {ks, "seen[0]"}, {vs, "seen[1]"}});
   check_device("the cache", c.device, k.device().index());
   return done(moe_kv_append(&c.c, static_cast<const uint16_t*>(k.data_ptr()), ld(k, H * D),
                             static_cast<const uint16_t*>(v.data_ptr()), ld(v, H * D),
                             static_cast<const int64_t*>(slots.data_ptr()), int32_size(N, "k_new"),
-                            static_cast<uint16_t*>(pointer(ks)), static_cast<uint16_t*>(pointer(vs)), c.status, stream()),
+                            static_cast<uint16_t*>(pointer(ks)), static_cast<uint16_t*>(pointer(vs)), c.status, stream),
               "moe_kv_append");
 }
 
@@ -263,8 +276,6 @@ Queries queries(const Cache& c, const at::Tensor& q, const at::Tensor& table) {
     refuse("q", "of contiguous rows [num_q_heads, head_dim] that are evenly spaced");
   if (table.dim() != 2 || !is(table, at::kInt, {B, table.size(1)}) || (table.stride(1) != 1 && table.size(1) > 1))
     refuse("page_table", "int32 [batch, max_pages] on the GPU, a sequence's pages side by side");
-  on_current_device({{&q, "q"}, {&table, "page_table"}});
-  check_device("the cache", c.device, q.device().index());
   return {int32_size(B, "q"), int32_size(T, "q"), int32_size(H, "q"), int32_size(table.size(1), "page_table"), step,
           ld(table, table.size(1))};
 }
@@ -286,16 +297,18 @@ PyObject* kv_attend(PyObject* const* a) {
   dense(&out, kBf16, {n.batch, n.q_len, n.heads, c.c.head_dim}, "out", "contiguous bf16 of q's shape on the GPU");
   dense(lse, at::kFloat, {n.batch, n.q_len, n.heads}, "lse", "contiguous float32 [batch, q_len, num_q_heads] on the GPU");
   if (ws && !(ws->is_cuda() && ws->is_contiguous())) refuse("workspace", "contiguous on the GPU");
-  on_device({{&lens, "seq_lens"}, {&out, "out"}, {lse, "lse"}, {ws, "workspace"}}, q.device().index());
+  const moe_stream_t stream =
+      stream_of({{&q, "q"}, {&table, "page_table"}, {&lens, "seq_lens"}, {&out, "out"}, {lse, "lse"}, {ws, "workspace"}});
+  check_device("the cache", c.device, q.device().index());
   return done(moe_kv_attend(&c.c, static_cast<const uint16_t*>(q.data_ptr()), n.ld_q, n.batch, n.q_len, n.heads,
                             static_cast<const int32_t*>(table.data_ptr()), n.ld_table, n.pages,
                             static_cast<const int32_t*>(lens.data_ptr()), real(a[4]), static_cast<uint16_t*>(out.data_ptr()),
-                            static_cast<float*>(pointer(lse)), pointer(ws), ws ? ws->nbytes() : 0, c.status, stream()),
+                            static_cast<float*>(pointer(lse)), pointer(ws), ws ? ws->nbytes() : 0, c.status, stream),
               "moe_kv_attend");
 }
 
 #define ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(set_error, 1), ENTRY(refuse_device, 3), ENTRY(add_rms_norm, 9), ENTRY(fp4_linear, 7), ENTRY(kv_cache, 7),
+PyMethodDef methods[] = {ENTRY(set_error, 1), ENTRY(stream_id, 0), ENTRY(refuse_device, 3), ENTRY(add_rms_norm, 9), ENTRY(fp4_linear, 7), ENTRY(kv_cache, 7),
                          ENTRY(kv_append, 6), ENTRY(kv_workspace, 3), ENTRY(kv_attend, 8), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "calls of libmoe_nvfp4 on torch tensors", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -35,7 +35,8 @@ def _load():
     return native
 
 
-_scratch: dict = {}
+_scratch = threading.local()  # .of: (device, stream id) -> tensor; goes with its thread
+_MOST_STREAMS = 8
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor | None:
@@ -45,10 +46,13 @@ def _workspace(nbytes: int, device) -> torch.Tensor | None:
         return None
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=_U8, device=device)
-    key = device, L.current_stream(), threading.get_ident()
-    t = _scratch.get(key)
+    kept = _scratch.__dict__.setdefault("of", {})
+    key = device, _native.stream_id()  # a handle may come back for another stream, an id does not
+    t = kept.get(key)
     if t is None or t.numel() < nbytes:
-        t = _scratch[key] = torch.empty(nbytes, dtype=_U8, device=device)
+        if t is None and len(kept) >= _MOST_STREAMS:
+            kept.clear()
+        t = kept[key] = torch.empty(nbytes, dtype=_U8, device=device)
     return t
 
 

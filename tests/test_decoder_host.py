@@ -1,4 +1,7 @@
 """The Python layer of the operators around the routed experts: what it checks and keeps on the host."""
+import threading
+import weakref
+
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
@@ -88,3 +91,56 @@ def test_the_linears_cut_on_any_number_of_sms(native):
             assert c["slices"] <= sms * (16 // c["warps"])     # a cluster finds room
             tiles = c["warps"] // c["across"]
             assert tiles % (2 if gated else 1) == 0 and (c["slices"] > 1 or tiles // (2 if gated else 1) <= 15)
+
+
+class _Streams:
+    """Stands in for the native module: the current stream's id, while its handle never changes."""
+    id = 1
+
+    def stream_id(self):
+        return self.id
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    s = _Streams()
+    monkeypatch.setattr(decoder, "_native", s)
+    monkeypatch.setattr(decoder.L, "current_stream", lambda: 0x5000)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return s
+
+
+CPU = torch.device("cpu")
+
+
+def test_scratch_is_kept_for_one_stream(streams):
+    assert decoder._workspace(0, CPU) is None
+    a = decoder._workspace(100, CPU)
+    assert a.numel() >= 100 and decoder._workspace(60, CPU) is a
+    assert decoder._workspace(200, CPU).numel() >= 200
+    a = decoder._workspace(200, CPU)
+    streams.id = 2                                          # another stream that got the same handle
+    assert decoder._workspace(200, CPU).data_ptr() != a.data_ptr()
+    streams.id = 1
+    assert decoder._workspace(200, CPU) is a
+
+
+def test_scratch_does_not_grow_with_streams(streams):
+    alive = []
+    for streams.id in range(100, 200):
+        alive.append(weakref.ref(decoder._workspace(64, CPU)))
+    assert sum(r() is not None for r in alive) <= 8
+
+
+def test_scratch_goes_with_its_thread(streams):
+    def work(out):
+        out.append(weakref.ref(decoder._workspace(64, CPU)))
+        out.append(decoder._workspace(64, CPU).data_ptr())
+    mine, others = decoder._workspace(64, CPU), []
+    for _ in range(5):
+        out = []
+        t = threading.Thread(target=work, args=(out,))
+        t.start()
+        t.join()
+        others.append(out)
+    assert all(ref() is None and at != mine.data_ptr() for ref, at in others)

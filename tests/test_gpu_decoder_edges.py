@@ -2,6 +2,8 @@
 numbers that are none, slices, several threads and streams. Tolerances as in test_gpu_decoder.py unless
 a test says otherwise.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -181,3 +183,33 @@ def test_linear_of_one_of_several_matrices_and_of_some_of_the_tokens():
         lin = pkg.NVFP4Linear(data[e], sf[e], alpha[e:e + 1])
         for m in range(7):
             check_linear(lin(x8[m:], scale[m:]), x8[m:], to_np(scale[m:]), to_np(data[e]), to_np(sf[e]), float(alpha[e]))
+
+
+# ------------------------------------------------------------- several threads and streams
+@pytest.mark.parametrize("shared", [False, True])
+def test_attend_from_several_threads_at_once(shared):
+    """Threads with a stream each, or all on one: every call needs scratch for its parts, and none takes
+    another's while it is in use."""
+    lens, page = [9000, 4000], 64
+    p = Pool(300, page, 2, 128)
+    table, ln, _ = sequences(p, lens)
+    qs = [queries(2, 1, 8, 128, seed=s) for s in range(4)]
+    want = [tuple(t.clone() for t in p.kv.attend(q, table, ln)) for q in qs]
+    torch.cuda.synchronize()
+    one, bad, go = torch.cuda.Stream(), [], threading.Barrier(4)
+
+    def work(i):
+        with torch.cuda.stream(one if shared else torch.cuda.Stream()):
+            go.wait(timeout=30)
+            for _ in range(60):
+                got = p.kv.attend(qs[i], table, ln)
+                torch.cuda.current_stream().synchronize()
+                if not (torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1])):
+                    bad.append(i)
+            torch.cuda.current_stream().synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
