@@ -5,7 +5,7 @@
  * kernel with the defaults below. The test library holds the same kernels and every
  * entry point of moe_nvfp4.h, plus these calls, which let tests reach paths that normal
  * inputs never take: a GEMM1 with plain epilogues, the decode GEMM's scheduling
- * fallbacks, and the bounded waits of the GEMM kernels running out; and the rule that cuts the NVFP4 linear.
+ * fallbacks, and the bounded waits of the GEMM and attention kernels running out; and the rule that cuts the NVFP4 linear.
  *
  * None of these calls keeps state between calls either: every option is an argument.
  */
@@ -26,12 +26,13 @@ extern "C" {
  *                    the odd CTAs leave their offered first unit to other CTAs. Results never
  *                    depend on either. Default 0.
  *  wait_limit_ns     limit of every bounded wait in the GEMM kernels (pipeline barriers, GEMM1
- *                    completion counters). Default 2 s.
+ *                    completion counters) and in the attention (its copies). Default 2 s.
  *  withhold_release  nonzero: the GEMM1 tiles of the first 128-row tile (chained GEMMs) or of
  *                    the first active expert (decode GEMMs) never publish their completion, so
  *                    the GEMM2 tiles that read them wait until wait_limit_ns runs out; the kernel
  *                    then ORs MOE_DEV_TIMEOUT into *dev_status and returns, with the outputs of
- *                    the abandoned tiles undefined. Default 0. */
+ *                    the abandoned tiles undefined. Attention: the copies of each sequence's first
+ *                    tokens are not started, so that the warps that wait for them give up. Default 0. */
 typedef struct {
   int32_t decode_hooks;
   int32_t withhold_release;
@@ -60,6 +61,14 @@ MOE_API moe_status_t moe_test_routed_forward(const uint16_t* x, int32_t M, int64
  * once, groups of tokens. */
 MOE_API moe_status_t moe_test_linear_cut(int32_t M, int32_t K, int32_t N, int32_t gated, int32_t num_sms,
                                          int32_t* cut);
+
+/* moe_kv_attend with test options (NULL = the defaults, which is exactly moe_kv_attend). */
+MOE_API moe_status_t moe_test_kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch,
+                                        int32_t q_len, int32_t num_q_heads, const int32_t* page_table,
+                                        int64_t ld_table, int32_t max_pages, const int32_t* seq_lens,
+                                        float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, int32_t* dev_status,
+                                        const moe_test_options_t* options, moe_stream_t stream);
 
 /* The forward's permute and GEMM1 with a plain epilogue instead of the fused requantiser,
  * so tests can compare GEMM1 with the oracle before the activation and the requantiser.

@@ -40,7 +40,8 @@ EXPORTED = [
     "moe_add_rmsnorm", "moe_linear_fp4", "moe_kv_append", "moe_kv_attend_workspace_bytes", "moe_kv_attend",
 ]
 # the test build's extra entry points (include/moe_nvfp4_test.h)
-TEST_EXPORTED = ["moe_test_default_options", "moe_test_routed_forward", "moe_test_gemm1", "moe_test_linear_cut"]
+TEST_EXPORTED = ["moe_test_default_options", "moe_test_routed_forward", "moe_test_gemm1", "moe_test_linear_cut",
+                 "moe_test_kv_attend"]
 MOE_PLAN_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 
@@ -81,6 +82,9 @@ _ROUTED_ARGS = [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_int32, c_int32,
 def _declare(lib, test=False):
     P = c_void_p
     routed = list(_ROUTED_ARGS)
+    # moe_kv_attend's arguments up to the stream
+    attend = [ctypes.POINTER(KVCacheT), P, c_int64, c_int32, c_int32, c_int32, P, c_int64, c_int32, P, c_float, P, P, P,
+              c_size_t, P]
     sig = {
         "moe_status_string": (ctypes.c_char_p, [c_int32]),
         "moe_abi_version": (c_int32, []),
@@ -107,11 +111,11 @@ def _declare(lib, test=False):
         "moe_linear_fp4": (c_int32, [P, c_int64, P, c_int32, c_int32, c_int32, P, P, P, c_int32, c_int32, P, P]),
         "moe_kv_append": (c_int32, [ctypes.POINTER(KVCacheT), P, c_int64, P, c_int64, P, c_int32, P, P, P, P]),
         "moe_kv_attend_workspace_bytes": (c_size_t, [ctypes.POINTER(KVCacheT), c_int32, c_int32, c_int32, c_int32]),
-        "moe_kv_attend": (c_int32, [ctypes.POINTER(KVCacheT), P, c_int64, c_int32, c_int32, c_int32, P, c_int64,
-                                    c_int32, P, c_float, P, P, P, c_size_t, P, P]),
+        "moe_kv_attend": (c_int32, attend + [P]),
     }
     if test:
         sig.update({
+            "moe_test_kv_attend": (c_int32, attend + [ctypes.POINTER(TestOptionsT), P]),
             "moe_test_default_options": (TestOptionsT, []),
             "moe_test_routed_forward": (c_int32, routed + [ctypes.POINTER(TestOptionsT), P]),
             "moe_test_linear_cut": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, ctypes.POINTER(c_int32)]),
@@ -371,17 +375,22 @@ def moe_kv_attend_workspace_bytes(cache: KVCacheT, batch, q_len, num_q_heads, ma
 
 
 def moe_kv_attend(cache: KVCacheT, q, ld_q, page_table, seq_lens, softmax_scale, out, lse, workspace, dev_status,
-                  stream=None):
+                  stream=None, test_options=None):
     """q [batch, q_len, num_q_heads, head_dim] bf16 with ld_q values between rows (b, t) and (b, t + 1) and
-    between the last row of a sequence and the first of the next; page_table [batch, max_pages] int32."""
+    between the last row of a sequence and the first of the next; page_table [batch, max_pages] int32. test_options (a
+    TestOptionsT from test_options()): call the test build's moe_test_kv_attend instead."""
     B, T, Hq, D = q.shape
     pages = page_table.shape[1]
-    st = lib().moe_kv_attend(
+    args = (
         cache, q.data_ptr(), ld_q if B * T > 1 else Hq * D, B, T, Hq, page_table.data_ptr(),
         page_table.stride(0) if B > 1 else pages, pages, seq_lens.data_ptr(), softmax_scale, out.data_ptr(),
         lse.data_ptr() if lse is not None else None, workspace.data_ptr() if workspace is not None else None,
         workspace.numel() * workspace.element_size() if workspace is not None else 0,
-        dev_status.data_ptr() if dev_status is not None else None, _stream(stream))
+        dev_status.data_ptr() if dev_status is not None else None)
+    if test_options is None:
+        st = lib().moe_kv_attend(*args, _stream(stream))
+    else:
+        st = test_lib().moe_test_kv_attend(*args, ctypes.byref(test_options), _stream(stream))
     if st:
         _check(st, "moe_kv_attend")
 

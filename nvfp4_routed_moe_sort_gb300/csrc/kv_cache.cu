@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "fp4_mma.cuh"
 #include "host_util.h"
+#include "layout.h"
 
 namespace moe {
 namespace {
@@ -130,6 +131,8 @@ struct AttendArgs {
   int64_t ld_q, ld_table;
   int q_len, q_heads, group, row_blocks, max_pages, splits, run;
   float scale;
+  uint32_t wait_us;  // limit of every bounded wait (kWaitLimitNs unless a test build shortens it); 64 bits cost 2 %
+  int withhold;      // test build only: the first of the tokens that are never copied, else -1
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     if (lane == 0) mbar_arrive_expect_tx(&full[warp][stage], __popc(held) * (kStage / U));
     __syncwarp();
     const bool all = wide && held == kAll;
-    if (lane < 4 * U && ok && (half == 0 || !all))
+    if (lane < 4 * U && ok && (half == 0 || !all) && tok != a.withhold)
       bulk_load(my_ring + stage * kStage + to, from + page * from_page + ((tok + 16 * half) & ((1 << c.page_shift) - 1)) * row_bytes,
                 (all ? kGroup : 16) * row_bytes, &full[warp][stage]);
   };
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
   };
   while (toks[0] < end) {
     const int tok = toks[0];
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &abort_flag, a.dev_status, kWaitLimitNs))) break;
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &abort_flag, a.dev_status, a.wait_us * uint64_t(1000)))) break;
     const uint8_t* const st = my_ring + stage * kStage;
     const uint32_t held = held_next & 0xFFFF;
     // ---- scores
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
   // after a wait that gave up: the stages still in flight, before their memory is used again
   for (int i = 0; i < kAttStages && toks[0] < end; ++i) {
     const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(&full[warp][stage], parity) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    while (!mbar_try_wait(&full[warp][stage], parity) && globaltimer_ns() - t0 < a.wait_us * uint64_t(1000)) {
     }
     if (++stage == kAttStages) stage = 0, parity ^= 1;
     advance();
@@ -790,11 +793,10 @@ extern "C" size_t moe_kv_attend_workspace_bytes(const moe_kv_cache_t* cache, int
   return attend_cut(cache, &c, batch, q_len, num_q_heads, max_pages, &cut, &bytes) == MOE_OK ? bytes : 0;
 }
 
-extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch,
-                                      int32_t q_len, int32_t num_q_heads, const int32_t* page_table, int64_t ld_table,
-                                      int32_t max_pages, const int32_t* seq_lens, float softmax_scale, uint16_t* out,
-                                      float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
-                                      moe_stream_t stream) {
+moe_status_t moe::kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch, int32_t q_len,
+                            int32_t num_q_heads, const int32_t* page_table, int64_t ld_table, int32_t max_pages,
+                            const int32_t* seq_lens, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, const TestOptions& topt, moe_stream_t stream) {
   Cache c;
   Cut cut;
   size_t need;
@@ -825,9 +827,11 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   float2* part_ml = parts ? reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + roundup64(parts * c.dim * 4, 16))
                           : nullptr;
   float* row_f = parts ? reinterpret_cast<float*>(part_ml + parts) : nullptr;
+  const uint64_t us = (topt.wait_limit_ns + 999) / 1000;
+  const uint32_t wait_us = us < UINT32_MAX ? static_cast<uint32_t>(us) : UINT32_MAX;
   const AttendArgs a = {q, page_table, seq_lens, out, lse, part_o, part_ml, row_f, dev_status, ld_q, ld_table, q_len,
                         num_q_heads, num_q_heads / c.heads, cut.row_blocks, max_pages, cut.splits, cut.run,
-                        softmax_scale};
+                        softmax_scale, wait_us, topt.withhold_release ? 0 : -1};
   const dim3 grid(cut.splits, c.heads * cut.row_blocks, batch);
   decltype(&kv_attend_kernel<64, 1, 2>) kern;
   if (c.dim == 64)
@@ -855,4 +859,13 @@ extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_
   const int64_t all = static_cast<int64_t>(rows) * num_q_heads, per_block = one ? 8 : 1;
   return launch_pdl(join, dim3(static_cast<unsigned>((all + per_block - 1) / per_block)), dim3(kJoinThreads), 0,
                     as_stream(stream), a, c.g[1], all);
+}
+
+extern "C" moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch,
+                                      int32_t q_len, int32_t num_q_heads, const int32_t* page_table, int64_t ld_table,
+                                      int32_t max_pages, const int32_t* seq_lens, float softmax_scale, uint16_t* out,
+                                      float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                      moe_stream_t stream) {
+  return kv_attend(cache, q, ld_q, batch, q_len, num_q_heads, page_table, ld_table, max_pages, seq_lens, softmax_scale,
+                   out, lse, workspace, workspace_bytes, dev_status, TestOptions(), stream);
 }

@@ -135,9 +135,10 @@ constexpr int64_t kDecodeMaxTokens = MOE_DECODE_MAX_TOKENS;
 // Options that only the test build's entry points change; every product entry point passes
 // the defaults. decode_hooks: the decode GEMM's scheduling fallbacks forced (bit 0: every
 // first-unit guess wrong, bit 1: odd CTAs leave their offered unit to others);
-// wait_limit_ns: the limit of every bounded wait in the GEMM kernels; withhold_release: the
+// wait_limit_ns: the limit of every bounded wait in the GEMM and attention kernels; withhold_release: the
 // GEMM1 tiles of the first row tile (chained GEMMs) or of the first active expert (decode
-// GEMMs) never publish their completion, so a GEMM2 wait runs out.
+// GEMMs) never publish their completion, so a GEMM2 wait runs out; in the attention the copies of each
+// sequence's first tokens are not started.
 struct TestOptions {
   int32_t decode_hooks = 0;
   uint64_t wait_limit_ns = kWaitLimitNs;
@@ -227,6 +228,11 @@ moe_status_t check_forward_common(const int32_t* padded_offsets, const int32_t* 
                                   int32_t top_k, const uint8_t* xq, const uint8_t* xsf, const float* xs,
                                   const moe_nvfp4_weights_t* w, const void* prepared, size_t prepared_bytes,
                                   void* workspace, size_t workspace_bytes, int32_t* dev_status, size_t ws_need);
+// moe_kv_attend, and the same with test options (kv_cache.cu)
+moe_status_t kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch, int32_t q_len,
+                       int32_t num_q_heads, const int32_t* page_table, int64_t ld_table, int32_t max_pages,
+                       const int32_t* seq_lens, float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                       size_t workspace_bytes, int32_t* dev_status, const TestOptions& topt, moe_stream_t stream);
 moe_status_t launch_prepare_matrix(const uint8_t* src, const uint8_t* src_sf, int E, int rows, int rows_p, int K,
                                    int gated_inter, uint8_t* dst, uint8_t* dst_sf, cudaStream_t s);
 

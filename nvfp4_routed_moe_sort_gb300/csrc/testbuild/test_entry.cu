@@ -2,7 +2,7 @@
 //
 // They reach paths that normal inputs never take: a standalone GEMM1 with plain epilogues
 // (FP32 pre-activations, BF16 intermediate), the decode GEMM's scheduling fallbacks, and the
-// GEMM kernels' bounded waits running out; and they show the rule that cuts the NVFP4 linear. Every
+// GEMM and attention kernels' bounded waits running out; and they show the rule that cuts the NVFP4 linear. Every
 // option is an argument; nothing here keeps state between calls.
 #include <string.h>
 
@@ -120,4 +120,15 @@ extern "C" moe_status_t moe_test_linear_cut(int32_t M, int32_t K, int32_t N, int
                           static_cast<int32_t>(k.groups)};
   memcpy(cut, all, sizeof(all));
   return MOE_OK;
+}
+
+extern "C" moe_status_t moe_test_kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch,
+                                           int32_t q_len, int32_t num_q_heads, const int32_t* page_table,
+                                           int64_t ld_table, int32_t max_pages, const int32_t* seq_lens,
+                                           float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                                           size_t workspace_bytes, int32_t* dev_status,
+                                           const moe_test_options_t* options, moe_stream_t stream) {
+  MOE_CHECK(options == nullptr || options->wait_limit_ns > 0, MOE_ERR_INVALID_ARGUMENT);
+  return kv_attend(cache, q, ld_q, batch, q_len, num_q_heads, page_table, ld_table, max_pages, seq_lens, softmax_scale,
+                   out, lse, workspace, workspace_bytes, dev_status, to_internal(options), stream);
 }
