@@ -64,17 +64,19 @@ __device__ __forceinline__ float gelu(float x) {
   return __fmul_rn(__fmul_rn(0.5f, x), __fadd_rn(1.0f, erff(__fmul_rn(x, 0.70710678118654752f))));
 }
 
+__device__ __forceinline__ float relu(float x) { return x <= 0.0f ? 0.0f : x; }  // lets a NaN through
+
 // act(g) * u for the gated kinds, act(g) otherwise
 __device__ __forceinline__ float activate(int act, float g, float u) {
   switch (act) {
     case MOE_ACT_SWIGLU: return __fmul_rn(silu(g), u);
     case MOE_ACT_GEGLU: return __fmul_rn(gelu(g), u);
     case MOE_ACT_RELU2: {
-      const float r = fmaxf(g, 0.0f);
+      const float r = relu(g);
       return __fmul_rn(r, r);
     }
     case MOE_ACT_GELU: return gelu(g);
-    case MOE_ACT_RELU: return fmaxf(g, 0.0f);
+    case MOE_ACT_RELU: return relu(g);
     case MOE_ACT_SILU: return silu(g);
     default: return g;
   }

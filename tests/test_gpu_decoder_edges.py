@@ -213,3 +213,14 @@ def test_attend_from_several_threads_at_once(shared):
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("act", ["identity", "swiglu", "geglu", "relu2", "gelu", "relu", "silu"])
+@pytest.mark.parametrize("M,K", [(3, 512), (12, 4096)])
+def test_linear_activations_let_a_nan_through(act, M, K):
+    x, _, data, sf, alpha = linear_case(M, 64, K, None)
+    ref = run_linear(x, None, data, sf, alpha, act).clone()
+    x[1, 77] = float("nan")
+    got = run_linear(x, None, data, sf, alpha, act)
+    rows = [m for m in range(M) if m != 1]
+    assert torch.equal(got[rows], ref[rows]) and torch.isnan(got[1].float()).all()
