@@ -25,10 +25,10 @@
 // results do not depend on timing. alpha, the activation and the BF16 rounding come once at the
 // end. A block goes on to further rows while there are any, their first chunks already in flight.
 //
-// Measured: 4 tokens x 129021 x 4096 58.3 us (5.1 TB/s; 158 instructions per 16 rows and chunk, 62 % of the
+// Measured: 4 tokens x 129021 x 4096 57.4 us (5.2 TB/s; 158 instructions per 16 rows and chunk, 62 % of the
 // issue slots, 64 of them conversions at half rate); 8 x 4096 x 7168 with SwiGLU, E4M3 8.1 us, 1 x 2048 x 512
-// 3.6 us, both chains of launch, loads, sums and barrier. (The BF16 MMAs' code costs BF16 calls that do not run it 0.2 to
-// 0.8 us.)
+// 3.4 us, both chains of launch, loads, sums and barrier. (The loop over rows exists twice: with a
+// choice of the MMA inside it calls that do not run BF16 ones took 0.2 to 1.2 us more.)
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -267,13 +267,16 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   if constexpr (FP8) __syncthreads();
   else wide = __syncthreads_or(lost);
   if (!FP8 && wide) {
-    for (int i = tid >> 4; i < M * chunks; i += pairs) {
-      const int m = i / chunks, ch = i - m * chunks;
+#pragma unroll 1
+    for (int ch = tid >> 4; ch < chunks; ch += pairs) {
       const int64_t k = static_cast<int64_t>(chunk0 + ch) * kLinChunk + 8 * piece;
-      uint4 f = make_uint4(0, 0, 0, 0);
-      if (k < a.K) f = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (m0 + m) * a.ld_x + k);
-      *reinterpret_cast<uint4*>(xs + m * x_row + ch * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16) = f;
-      if (piece == 0) factor[ch * 8 * NT + m] = 1.0f;
+      const uint16_t* from = static_cast<const uint16_t*>(a.x) + m0 * a.ld_x + k;
+      uint8_t* to = xs + ch * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16;
+#pragma unroll 1
+      for (int m = 0; m < M; ++m, from += a.ld_x, to += x_row) {
+        *reinterpret_cast<uint4*>(to) = k < a.K ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
+        if (piece == 0) factor[ch * 8 * NT + m] = 1.0f;
+      }
     }
     __syncthreads();
   }
@@ -308,12 +311,12 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
   const int m_member = member / cols, col_member = at_col + member - m_member * cols;
   const int m_members = members / cols, col_members = members - m_members * cols;
   int stage = 0;
-  for (int block = blockIdx.x / a.slices; block < blocks; block += stride) {
-    float acc[NT][4];
+  auto turns = [&](auto in_bf16) {
+    constexpr bool kBf16 = decltype(in_bf16)::value;
+    for (int block = blockIdx.x / a.slices; block < blocks; block += stride) {
+      float acc[NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-    auto sweep = [&](auto in_bf16) {
-      constexpr bool kBf16 = decltype(in_bf16)::value;
+      for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
       const float* scale_of = factor_lane;
       int x_at = 0;
       for (int ch0 = first; ch0 < last; ch0 += 2) {
@@ -388,69 +391,69 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
         x_at += 512, scale_of += 16 * NT;
         if (++stage == a.stages) stage = 0;
       }
-    };
-    if constexpr (FP8) sweep(std::false_type{});
-    else if (wide) sweep(std::true_type{});
-    else sweep(std::false_type{});
 
-    // A warp that has all of K and no activation to do has the result: 16 x 60000 x 256 6.4 us against 11.8 through
-    // shared memory. (With the activations here too, their code made every size 0.1 us slower.)
-    if (parts == 1 && a.act == MOE_ACT_IDENTITY) {
+      // A warp that has all of K and no activation to do has the result: 16 x 60000 x 256 6.4 us against 11.8 through
+      // shared memory. (With the activations here too, their code made every size 0.1 us slower.)
+      if (parts == 1 && a.act == MOE_ACT_IDENTITY) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = block * n_per + i0 + r + 8 * h;
+          uint16_t* const to = a.out + static_cast<int64_t>(m0 + 2 * c) * a.n_out + col;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (col < a.n_out && 8 * t + 2 * c + i < M)
+                to[static_cast<int64_t>(8 * t + i) * a.n_out] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(acc[t][2 * h + i] * alpha));
+        }
+        continue;
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int col = block * n_per + i0 + r + 8 * h;
-        uint16_t* const to = a.out + static_cast<int64_t>(m0 + 2 * c) * a.n_out + col;
+        float* const to_sum = sums + sum_at[h];
+        const uint32_t to_cluster = a.slices > 1 ? cluster_address(to_sum, owner[h]) : 0;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (col < a.n_out && 8 * t + 2 * c + i < M)
-              to[static_cast<int64_t>(8 * t + i) * a.n_out] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(acc[t][2 * h + i] * alpha));
+          for (int i = 0; i < 2; ++i) {
+            if (a.slices > 1) store_cluster(to_cluster + 4 * (8 * t + i), acc[t][2 * h + i]);
+            else to_sum[8 * t + i] = acc[t][2 * h + i];
+          }
       }
-      continue;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float* const to_sum = sums + sum_at[h];
-      const uint32_t to_cluster = a.slices > 1 ? cluster_address(to_sum, owner[h]) : 0;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (a.slices > 1) store_cluster(to_cluster + 4 * (8 * t + i), acc[t][2 * h + i]);
-          else to_sum[8 * t + i] = acc[t][2 * h + i];
-        }
-    }
-    if (a.slices > 1) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(members) : "memory");
-    }
-    const int left_cols = a.n_out - (block * n_per + rank * share);
-    for (int i = member, m = m_member, col = col_member; i < cols * M;) {
-      if (col < left_cols) {
-        const float* at = sums + col * kSumRow + m;
-        float y[2] = {0.0f, 0.0f};
-        for (int s = 0; s < parts; ++s) {
-          y[0] += *at, at += share * kSumRow;
-          if (a.gated) y[1] += *at, at += share * kSumRow;
-        }
-        a.out[static_cast<int64_t>(m0 + m) * a.n_out + block * n_per + rank * share + col] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0] * alpha, y[1] * alpha)));
+      if (a.slices > 1) {
+        cluster_arrive();
+        cluster_wait();
+      } else {
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(members) : "memory");
       }
-      i += members, m += m_members, col += col_members;
-      if (col >= at_col + cols) col -= cols, ++m;
+      const int left_cols = a.n_out - (block * n_per + rank * share);
+      for (int i = member, m = m_member, col = col_member; i < cols * M;) {
+        if (col < left_cols) {
+          const float* at = sums + col * kSumRow + m;
+          float y[2] = {0.0f, 0.0f};
+          for (int s = 0; s < parts; ++s) {
+            y[0] += *at, at += share * kSumRow;
+            if (a.gated) y[1] += *at, at += share * kSumRow;
+          }
+          a.out[static_cast<int64_t>(m0 + m) * a.n_out + block * n_per + rank * share + col] =
+              __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, y[0] * alpha, y[1] * alpha)));
+        }
+        i += members, m += m_members, col += col_members;
+        if (col >= at_col + cols) col -= cols, ++m;
+      }
+      if (a.buffers == 2) {  // the other buffer is free: what it held was added before the barrier above
+        float* const t = sums;
+        sums = sums_next;
+        sums_next = t;
+      } else {
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(members) : "memory");
+      }
     }
-    if (a.buffers == 2) {  // the other buffer is free: what it held was added before the barrier above
-      float* const t = sums;
-      sums = sums_next;
-      sums_next = t;
-    } else {
-      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(members) : "memory");
-    }
-  }
+  };
+  if constexpr (FP8) turns(std::false_type{});
+  else if (wide) turns(std::true_type{});
+  else turns(std::false_type{});
 }
 
 template <int NT, int ALIGN>
