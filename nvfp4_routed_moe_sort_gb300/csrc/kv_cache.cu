@@ -337,15 +337,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 #pragma unroll
     for (int i = 0; i < kAttStages; ++i) toks[i] = toks[i + 1];
   };
-  while (toks[0] < end) {
-    const int tok = toks[0];
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &abort_flag, a.dev_status, a.wait_us * uint64_t(1000)))) break;
-    const uint8_t* const st = my_ring + stage * kStage;
-    const uint32_t held = held_next & 0xFFFF;
-    // ---- scores
-    float s[U][NT][4];
-    auto scores = [&](auto bf) {
-      constexpr bool kBf16 = decltype(bf)::value;
+  auto steps = [&](auto bf) {
+    constexpr bool kBf16 = decltype(bf)::value;
+    while (toks[0] < end) {
+      const int tok = toks[0];
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &abort_flag, a.dev_status, a.wait_us * uint64_t(1000)))) break;
+      const uint8_t* const st = my_ring + stage * kStage;
+      const uint32_t held = held_next & 0xFFFF;
+      // ---- scores
+      float s[U][NT][4];
       if constexpr (kBf16) {
 #pragma unroll
         for (int i = 0; i < U * NT * 4; ++i) s[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
@@ -384,125 +384,125 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
           }
         }
       }
-    };
-    if (in_bf16) scores(std::true_type{});
-    else scores(std::false_type{});
-    // ---- running maximum, weights
-    uint32_t vsf[U][4];
+      // ---- running maximum, weights
+      uint32_t vsf[U][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        vsf[u][h] = st[2 * kData + kSf + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 16) + r * (D / 16) / 8];
-    if (tok + kGroup > min(all_see, end) || held != kAll) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool here = held >> (4 * u) & 1;
-        if (!here && tok + 16 * u < end && a.dev_status && lane == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = tok + 16 * u + r + 8 * (i >> 1);
-            const int lim = min(end, row_limit(a, len, row0 + 8 * t + 2 * cc + (i & 1)));
-            if (!here || at >= lim) s[u][t][i] = -INFINITY;
-          }
-        // values past the sequence's end may be anything: a zero scale keeps them out
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int h = 0; h < 4; ++h)
-          if (!here || tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1) >= end) vsf[u][h] = 0;
+          vsf[u][h] = st[2 * kData + kSf + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 16) + r * (D / 16) / 8];
+      if (tok + kGroup > min(all_see, end) || held != kAll) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const bool here = held >> (4 * u) & 1;
+          if (!here && tok + 16 * u < end && a.dev_status && lane == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = tok + 16 * u + r + 8 * (i >> 1);
+              const int lim = min(end, row_limit(a, len, row0 + 8 * t + 2 * cc + (i & 1)));
+              if (!here || at >= lim) s[u][t][i] = -INFINITY;
+            }
+          // values past the sequence's end may be anything: a zero scale keeps them out
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if (!here || tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1) >= end) vsf[u][h] = 0;
+        }
+        // Of tokens that only some rows see, a scale that is no number is kept from the others too (the MMA
+        // would give them 0 * NaN): the rows that see the first such token get their NaN after the last step.
+        if (all_see < end) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const int at = tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1);
+              if (at >= all_see && (vsf[u][h] & 0x7F) == 0x7F) no_number = min(no_number, at), vsf[u][h] = 0;
+            }
+        }
       }
-      // Of tokens that only some rows see, a scale that is no number is kept from the others too (the MMA
-      // would give them 0 * NaN): the rows that see the first such token get their NaN after the last step.
-      if (all_see < end) {
+      uint32_t p[U][NT][2];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int at = tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1);
-            if (at >= all_see && (vsf[u][h] & 0x7F) == 0x7F) no_number = min(no_number, at), vsf[u][h] = 0;
-          }
-      }
-    }
-    uint32_t p[U][NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float top[2], keep[2];
-      bool grew = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = fmaxf(s[0][t][i], s[0][t][i + 2]);
-#pragma unroll
-        for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][t][i], s[u][t][i + 2]));
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-        top[i] = fmaxf(m[t][i], x);
-        grew |= top[i] > m[t][i];
-        keep[i] = top[i] == -INFINITY ? 0.0f : top[i];
-      }
-      if (__any_sync(0xffffffffu, grew)) {
+      for (int t = 0; t < NT; ++t) {
+        float top[2], keep[2];
+        bool grew = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = ex2((m[t][i] - keep[i]) * to_log2[t][i]);
-          l[t][i] *= f;
+          float x = fmaxf(s[0][t][i], s[0][t][i + 2]);
 #pragma unroll
-          for (int j = 0; j < KS; ++j) o[t][j][i] *= f, o[t][j][i + 2] *= f;
-          m[t][i] = top[i];
+          for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][t][i], s[u][t][i + 2]));
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          top[i] = fmaxf(m[t][i], x);
+          grew |= top[i] > m[t][i];
+          keep[i] = top[i] == -INFINITY ? 0.0f : top[i];
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float f = ex2((m[t][i] - keep[i]) * to_log2[t][i]);
+            l[t][i] *= f;
+#pragma unroll
+            for (int j = 0; j < KS; ++j) o[t][j][i] *= f, o[t][j][i + 2] *= f;
+            m[t][i] = top[i];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[u][t][i] = ex2(fmaf(s[u][t][i] - keep[i & 1], to_log2[t][i & 1], kPShift));
+            l[t][i & 1] += s[u][t][i];
+          }
+          p[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
+          p[u][t][1] = transpose8x8(pack_f16x2(s[u][t][2], s[u][t][3]));
         }
       }
+
+      // ---- weighted values
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(vsf[u][0], vsf[u][1], 0x0040));
+        const uint32_t s89 = e4m3x2_to_f16x2(__byte_perm(vsf[u][2], vsf[u][3], 0x0040));
+        uint32_t vw[4][VW];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[u][t][i] = ex2(fmaf(s[u][t][i] - keep[i & 1], to_log2[t][i & 1], kPShift));
-          l[t][i & 1] += s[u][t][i];
-        }
-        p[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
-        p[u][t][1] = transpose8x8(pack_f16x2(s[u][t][2], s[u][t][3]));
-      }
-    }
-
-    // ---- weighted values
+        for (int h = 0; h < 4; ++h)
+          load_words<VW>(vw[h], st + kData + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 2) + r * (D / 16));
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(vsf[u][0], vsf[u][1], 0x0040));
-      const uint32_t s89 = e4m3x2_to_f16x2(__byte_perm(vsf[u][2], vsf[u][3], 0x0040));
-      uint32_t vw[4][VW];
+        for (int w = 0; w < VW; ++w) {
+          // bytes that pair one dimension's codes of two neighbouring tokens
+          const uint32_t low = 0x0F0F0F0Fu;
+          uint32_t f[4][4];
+          e2m1x8_to_f16x2((vw[0][w] & low) | (vw[1][w] << 4 & ~low), f[0]);
+          e2m1x8_to_f16x2((vw[0][w] >> 4 & low) | (vw[1][w] & ~low), f[1]);
+          e2m1x8_to_f16x2((vw[2][w] & low) | (vw[3][w] << 4 & ~low), f[2]);
+          e2m1x8_to_f16x2((vw[2][w] >> 4 & low) | (vw[3][w] & ~low), f[3]);
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        load_words<VW>(vw[h], st + kData + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 2) + r * (D / 16));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x[4] = {mul_f16x2(f[0][i], s01), mul_f16x2(f[1][i], s01), mul_f16x2(f[2][i], s89),
+                                   mul_f16x2(f[3][i], s89)};
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        // bytes that pair one dimension's codes of two neighbouring tokens
-        const uint32_t low = 0x0F0F0F0Fu;
-        uint32_t f[4][4];
-        e2m1x8_to_f16x2((vw[0][w] & low) | (vw[1][w] << 4 & ~low), f[0]);
-        e2m1x8_to_f16x2((vw[0][w] >> 4 & low) | (vw[1][w] & ~low), f[1]);
-        e2m1x8_to_f16x2((vw[2][w] & low) | (vw[3][w] << 4 & ~low), f[2]);
-        e2m1x8_to_f16x2((vw[2][w] >> 4 & low) | (vw[3][w] & ~low), f[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x[4] = {mul_f16x2(f[0][i], s01), mul_f16x2(f[1][i], s01), mul_f16x2(f[2][i], s89),
-                                 mul_f16x2(f[3][i], s89)};
-#pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * w + i], x, p[u][t]);
+            for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * w + i], x, p[u][t]);
+          }
         }
       }
+      __syncwarp();  // every lane has read the stage
+      const int next = toks[kAttStages];
+      if (next < end) {
+        issue(stage, next, page);
+        toks[kAttStages + 1] = after(next);
+        page = page_of(toks[kAttStages + 1]);
+      } else {
+        held_next >>= 16;
+        toks[kAttStages + 1] = next;
+      }
+      advance();
+      toks[kAttStages] = toks[kAttStages + 1];
+      if (++stage == kAttStages) stage = 0, parity ^= 1;
     }
-    __syncwarp();  // every lane has read the stage
-    const int next = toks[kAttStages];
-    if (next < end) {
-      issue(stage, next, page);
-      toks[kAttStages + 1] = after(next);
-      page = page_of(toks[kAttStages + 1]);
-    } else {
-      held_next >>= 16;
-      toks[kAttStages + 1] = next;
-    }
-    advance();
-    toks[kAttStages] = toks[kAttStages + 1];
-    if (++stage == kAttStages) stage = 0, parity ^= 1;
-  }
+  };
+  if (in_bf16) steps(std::true_type{});
+  else steps(std::false_type{});
   // after a wait that gave up: the stages still in flight, before their memory is used again
   for (int i = 0; i < kAttStages && toks[0] < end; ++i) {
     const uint64_t t0 = globaltimer_ns();
