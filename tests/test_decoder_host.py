@@ -1,4 +1,6 @@
 """The Python layer of the operators around the routed experts: what it checks and keeps on the host."""
+import math
+import random
 import threading
 import weakref
 
@@ -7,7 +9,9 @@ import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
 import nvfp4_routed_moe_sort_gb300 as pkg  # noqa: F401  (the package must be importable without a GPU)
+from linear_cuts import CUTS, SMS, kinds
 from nvfp4_routed_moe_sort_gb300 import decoder
+from nvfp4_routed_moe_sort_gb300._lib import linear_cut
 from nvfp4_routed_moe_sort_gb300.build import build
 
 
@@ -76,7 +80,6 @@ def test_a_cache_keeps_what_it_was_made_from(name):
 
 def test_the_linears_cut_on_any_number_of_sms(native):
     """The rule holds on a part of a GPU too: every cut fits, and clusters that run at once are some."""
-    from nvfp4_routed_moe_sort_gb300._lib import linear_cut
     sizes = [(1, 16, 1, False), (1, 512, 2048, False), (8, 7168, 4096, True), (13, 2000, 7001, False), (16, 4096, 16384, False),
              (4, 4096, 129021, False), (2, 40000, 33, False), (16, 32784, 20000, True), (40, 1040, 40006, True), (5, 208, 74, True)]
     for sms in range(1, 200):
@@ -144,3 +147,21 @@ def test_scratch_goes_with_its_thread(streams):
         t.join()
         others.append(out)
     assert all(ref() is None and at != mine.data_ptr() for ref, at in others)
+
+
+def test_the_listed_sizes_take_the_cuts_they_are_listed_for_and_every_kind(native):
+    """What tests/test_gpu_linear_cuts.py runs: the table says what the rule chooses, and no kind that ordinary sizes
+    take is missing from it."""
+    listed = set()
+    for gated, M, N, K, warps, across, slices, buffers, stages in CUTS:
+        c = linear_cut(M, K, N, gated, SMS)
+        assert (c["warps"], c["across"], c["slices"], c["buffers"], c["stages"]) == (warps, across, slices, buffers, stages), (M, N, K)
+        listed.update(kinds(gated, M, N, K, c))
+    r = random.Random(5)
+    for _ in range(20000):
+        gated, M, K = r.random() < 0.5, r.randint(1, 16), max(16, int(2 ** r.uniform(4, 14)) // 16 * 16)
+        if r.random() < 0.4:
+            K = max(256, K // 256 * 256)
+        N = max(2, int(2 ** r.uniform(1, min(17.0, 30 - math.log2(K)))) // 2 * 2)
+        missing = set(kinds(gated, M, N, K, linear_cut(M, K, N, gated, SMS))) - listed
+        assert not missing, (gated, M, N, K, missing)
