@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_harness import DEV, bf16_np, pkg, to_np
+from gpu_harness import DEV, F, bf16_np, pkg, to_np
 from oracle import decoder as D
 from test_gpu_decoder import (Pool, U, assert_within, bf16, check_attend, check_linear, f32_np, linear_case, queries,
                               run_linear, sequences)
@@ -224,3 +224,32 @@ def test_linear_activations_let_a_nan_through(act, M, K):
     got = run_linear(x, None, data, sf, alpha, act)
     rows = [m for m in range(M) if m != 1]
     assert torch.equal(got[rows], ref[rows]) and torch.isnan(got[1].float()).all()
+
+
+# ------------------------------------------------------------------- append: no numbers
+@pytest.mark.parametrize("g", [1.0, 2.5])
+@pytest.mark.parametrize("Dh", [64, 128])
+def test_append_stores_only_numbers(Dh, g):
+    """An infinity becomes the largest value of its block's largest scale, a NaN some finite value within its block's;
+    every other value and every other block is what it is without them."""
+    r = np.random.default_rng(Dh)
+    x = torch.from_numpy(r.normal(size=(4, 2, Dh)).astype(np.float32)).bfloat16().float().numpy()
+    bad = x.copy()
+    bad[0, 0, 3], bad[1, 1, 17], bad[2, 0, 40], bad[2, 1, 5] = np.inf, -np.inf, np.nan, np.nan
+    bad[3, 0, 16:32] = np.nan
+    p, slots = Pool(2, 16, 2, Dh, g), torch.tensor([3, 30, 17, 0], device=DEV)
+    seen = tuple(torch.empty(4, 2, Dh, dtype=torch.bfloat16, device=DEV) for _ in "kv")
+    p.kv.append(bf16(bad), bf16(-bad), slots, seen=seen)
+    for sign, s, data, sf in ((1, seen[0], p.t[0], p.t[1]), (-1, seen[1], p.t[2], p.t[3])):
+        got = bf16_np(s)
+        codes, scales = (to_np(a)[slots.cpu().numpy() // 16, :, slots.cpu().numpy() % 16] for a in (data, sf))
+        stored = D.nvfp4_values(codes, scales) / g
+        assert np.isfinite(got).all() and np.isfinite(stored).all()
+        assert_within(got, stored, np.abs(stored) * (2.0 ** -8 + 4 * U) + 1e-37)
+        filled = np.where(np.isnan(bad), 0, bad)
+        want = D.kv_encode(sign * np.where(np.isinf(filled), np.sign(filled) * 3e38, filled), g)[2]
+        same = np.isfinite(bad)
+        assert np.array_equal(stored[same], want[same])
+        assert stored[0, 0, 3] == sign * 6 * 448 / g and stored[1, 1, 17] == -sign * 6 * 448 / g
+        scale = np.repeat(F.e4m3_decode(scales), 16, -1)
+        assert (np.abs(stored) <= 6 * scale / g).all()
