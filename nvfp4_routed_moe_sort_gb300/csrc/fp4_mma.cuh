@@ -6,6 +6,8 @@
 // has 6 significant bits between 2^-10 and 2688: exact in FP16.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace moe {
@@ -76,10 +78,13 @@ __device__ __forceinline__ void f16_range(float amax, float* up, float* down) {
   *down = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
 }
 
-// whether a value of these two BF16 lies below what f16_range's factor keeps exact (zero does not)
-__device__ __forceinline__ bool below_f16(uint32_t two, float down) {
-  const uint32_t least = __float_as_uint(0x1p-17f * down) - 1;  // 2^-143 at the smallest
-  return ((two << 16 & 0x7FFFFFFFu) - 1 < least) | ((two & 0x7FFF0000u) - 1 < least);
+// a mask that is not zero where one of two BF16 values is so small that its FP16 form, scaled by f16_range's
+// factor, may have lost bits of it
+__device__ __forceinline__ uint32_t below_f16(uint32_t two_bf16, uint32_t two_f16) {
+  const __half2 f = *reinterpret_cast<const __half2*>(&two_f16);
+  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&two_bf16);
+  return __hlt2_mask(__habs2(f), __half2half2(__ushort_as_half(0x0080))) &  // 2^-17
+         __hne2_mask(b, __bfloat162bfloat162(__ushort_as_bfloat16(0)));
 }
 
 }  // namespace moe

@@ -101,14 +101,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 // kAttStages groups in shared memory (bulk copies of 16 tokens, or of the group where one page holds
 // it, one mbarrier per stage), so the warps of a block never wait for one another before the end.
 //
-// Softmax in base 2 with a running maximum per query row of the raw sums s, which a row's factor f takes to
-// scores; p = 2^((s - m) f + 15) is rounded to FP16 for the second product (11 significant bits down to
-// 2^-29 of the largest weight), its sum is FP32. Subtracting before multiplying makes the largest weight
-// 2^15 whatever the scores' size; the difference of two rounded scores would be off by whole powers of 2
-// from 2^24 on. It costs an instruction a score.
-// Query rows are scaled by a power of two to a largest value in [2^14, 2^15), which BF16's values fit
-// FP16 with, down to 2^-31 of the largest; a block with a smaller one keeps its queries in BF16 and takes
-// BF16 MMAs for the scores, for which the keys take a second conversion.
+// Softmax in base 2. A row's weights are p = 2^(s f - c), s a raw sum, f the row's factor from raw sums to scores and c
+// the running reference fl(max f - 15), so that p is at most 2^15 but for c's rounding; they are
+// rounded to FP16 for the second product (11 significant bits down to 2^-29 of the largest weight), their sum is
+// FP32. Nothing but c's own rounding is between s f and c (one FMA), and c is what sums of different steps
+// are brought together by. That holds while c is exact to a part of 1: query rows are scaled by a power
+// of two to a largest value in [2^14, 2^15), so no score is above f 2^15 2688 D, and rows for which that is
+// below 2^22 are the plain case. BF16 values so scaled fit FP16 down to 2^-31 of the largest.
+//
+// A block with a row of larger possible scores or of smaller values starts again with its queries in BF16, on BF16
+// MMAs for the scores (the keys take a second conversion), with p = 2^((s - max) f + 15), which is right for
+// scores of any size.
 //
 // Bound by the conversion (ALU pipe 54 %, issue slots 61 % in use; 17.8 instructions per token and kv head), not by
 // HBM: 64 sequences of 4000 to 8191 tokens, 8 kv heads, 87 us (5.0 TB/s; the copies alone 73 us), one of
@@ -116,6 +119,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 constexpr int kAttWarps = 4;
 constexpr int kAttStages = 2;
 constexpr float kPShift = 15.0f;
+constexpr float kMostScore = 0x1p22f;  // of the plain case, in base 2
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttendArgs {
@@ -125,8 +129,8 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   float* part_o;   // [rows, splits, D]
-  float2* part_ml; // [rows, splits]: maximum of the raw sums and sum of the weights
-  float* row_f;    // [rows]: factor from raw sums to base-2 scores
+  float2* part_ml; // [rows, splits]: reference of the weights and their sum
+  float* row_f;    // [rows]: factor from references to base 2
   int32_t* dev_status;
   int64_t ld_q, ld_table;
   int q_len, q_heads, group, row_blocks, max_pages, splits, run;
@@ -175,32 +179,38 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int64_t at, float
   *reinterpret_cast<ushort4*>(a.out + at) = h;
 }
 __device__ __forceinline__ float row_lse(float top, float f, float total) {
-  return total == 0.0f ? -INFINITY : (top * f - kPShift + log2f(total)) * kLn2;
+  return total == 0.0f ? -INFINITY : (top * f + log2f(total)) * kLn2;
 }
 
-// U: runs of 16 tokens in a step of a warp. Two keep a short run's chain short; four spend less on the
-// maximum, the barrier and the copies: 131071 tokens 34.5 us against 40.3, 64 x 4000 to 8191 89.5 against 96, 16 x
-// 500 to 2000 11.3 against 12.8; 1 x 2000 6.8 either way.
-template <int D, int NT, int U>
-__global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : NT <= 3 ? 3 : 2)
-    kv_attend_kernel(Cache c, AttendArgs a) {
+// A block's shared memory beside the ring; the plain case, which comes first, initialises it for both
+template <int NT>
+struct AttendShared {
+  uint64_t full[2][kAttWarps][kAttStages];  // copies' barriers of the plain and the rare case
+  float m[kAttWarps][8 * NT], l[kAttWarps][8 * NT], f[8 * NT];
+  int abort_flag;
+};
+
+// The work of a block. False: its rows are not the plain case; nothing has been written and no copy is in flight.
+template <int D, int NT, int U, bool RARE>
+__device__ __forceinline__ bool attend_block(const Cache& c, const AttendArgs& a, uint8_t* ring, AttendShared<NT>& sh) {
   constexpr int kGroup = 16 * U, kStep = kAttWarps * kGroup;  // tokens of a step of a warp, of the block
   constexpr int KS = D / 16;       // MMA steps of S, MMA tiles of O
   constexpr int KW = D / 32;       // words of one token's keys per lane
   constexpr int VW = D / 64;       // words of one token's values per lane
   constexpr int R = 8 * NT;        // query rows of the block
-  // a stage: keys and values of 32 tokens, then their scales
+  // a stage: keys and values of kGroup tokens, then their scales
   constexpr int kData = kGroup * D / 2, kSf = kGroup * D / 16, kStage = 2 * (kData + kSf);
-  extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage][kStage]; the warps' sums at the end
-  __shared__ __align__(8) uint64_t full[kAttWarps][kAttStages];
-  __shared__ int abort_flag;
+  // ring: [warp][stage][kStage]; the warps' sums at the end
+  uint64_t(&full)[kAttWarps][kAttStages] = sh.full[RARE];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, cc = lane & 3;
-  if (lane < kAttStages) mbar_init(&full[warp][lane], 1);
-  if (tid == 0) abort_flag = 0;
-  fence_mbar_init();
-  __syncthreads();
-  pdl_wait();
-  pdl_trigger();
+  if constexpr (!RARE) {
+    if (lane < 2 * kAttStages) mbar_init(&sh.full[lane / kAttStages][warp][lane % kAttStages], 1);
+    if (tid == 0) sh.abort_flag = 0;
+    fence_mbar_init();
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+  }
   const int split = blockIdx.x, kvh = blockIdx.y / a.row_blocks, b = blockIdx.z;
   const int row0 = (blockIdx.y - kvh * a.row_blocks) * R;
   const int rows_here = min(R, a.q_len * a.group - row0);
@@ -224,7 +234,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     const int at = (toks[i] + 16 * half) >> c.page_shift;
     pages[i] = at < a.max_pages ? table[at] : -1;
   }
-  auto query = [&](int t, uint32_t* to) {  // this lane's share of row 8t + r
+  uint32_t raw[NT][D / 8];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
     const int row = row0 + 8 * t + r, at = row / a.group, g = row - at * a.group;
     const uint4* src = reinterpret_cast<const uint4*>(
         a.q + (static_cast<int64_t>(b) * a.q_len + at) * a.ld_q + (kvh * a.group + g) * D + cc * (D / 4));
@@ -232,12 +244,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     for (int i = 0; i < D / 32; ++i) {
       uint4 u = make_uint4(0, 0, 0, 0);
       if (8 * t + r < rows_here) u = src[i];
-      to[4 * i] = u.x, to[4 * i + 1] = u.y, to[4 * i + 2] = u.z, to[4 * i + 3] = u.w;
+      raw[t][4 * i] = u.x, raw[t][4 * i + 1] = u.y, raw[t][4 * i + 2] = u.z, raw[t][4 * i + 3] = u.w;
     }
-  };
-  uint32_t raw[NT][D / 8];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) query(t, raw[t]);
+  }
   len = max(len, 0);
   const int64_t most = static_cast<int64_t>(a.max_pages) << c.page_shift;
   if (len > most) {
@@ -251,7 +260,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
       const int64_t at = (static_cast<int64_t>(b) * a.q_len + t) * a.q_heads + kvh * a.group + g;
       a.part_ml[at * a.splits + split] = make_float2(-INFINITY, 0.0f);
     }
-    return;
+    return true;
   }
   const int end = seen, all_see = row_limit(a, len, row0);                       // every row sees the tokens before it
 
@@ -288,38 +297,41 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
   // Q^T fragments and each row's factor from raw sums to base-2 scores
   uint32_t q[NT][KS][2];
   float to_log2[NT][2];
-  bool lost = false;  // some value is not exact in FP16
+  bool plain = true;
   // above 0, so that -inf stays -inf; finite, so that no difference stays 0
   auto factor = [&](float down) { return fminf(fmaxf(fabsf(a.scale) * kLog2e / c.g[0] * down, FLT_MIN), FLT_MAX); };
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[t][i])), fabsf(bf16_hi(raw[t][i]))));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    float up, down;
-    f16_range(amax, &up, &down);
-    if (a.scale < 0.0f) up = -up;  // the factor is never negative
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      q[t][i >> 1][i & 1] = pack_f16x2(bf16_lo(raw[t][i]) * up, bf16_hi(raw[t][i]) * up);
-      lost |= below_f16(raw[t][i], down) && amax < INFINITY;  // a score with an infinity in it needs no other bits
-    }
-    const float f = factor(down);
-    to_log2[t][0] = __shfl_sync(0xffffffffu, f, 8 * cc);
-    to_log2[t][1] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
-  }
-  const bool in_bf16 = __any_sync(0xffffffffu, lost);  // the same for every warp of the block
-  if (in_bf16) {
+  if constexpr (RARE) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      uint32_t again[D / 8];
-      query(t, again);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) q[t][i >> 1][i & 1] = again[i] ^ (a.scale < 0.0f ? 0x80008000u : 0u);
+      for (int i = 0; i < D / 8; ++i) q[t][i >> 1][i & 1] = raw[t][i] ^ (a.scale < 0.0f ? 0x80008000u : 0u);
       to_log2[t][0] = to_log2[t][1] = factor(1.0f);
     }
+  } else {
+    uint32_t not_plain = 0;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[t][i])), fabsf(bf16_hi(raw[t][i]))));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      float up, down;
+      f16_range(amax, &up, &down);
+      if (a.scale < 0.0f) up = -up;  // the factor is never negative
+      uint32_t below = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        q[t][i >> 1][i & 1] = pack_f16x2(bf16_lo(raw[t][i]) * up, bf16_hi(raw[t][i]) * up);
+        below |= below_f16(raw[t][i], q[t][i >> 1][i & 1]);
+      }
+      if (amax < INFINITY) not_plain |= below;  // a score with an infinity in it needs no other bits
+      const float f = factor(down);
+      not_plain |= f >= kMostScore / (0x1p15f * 2688.0f * D);
+      to_log2[t][0] = __shfl_sync(0xffffffffu, f, 8 * cc);
+      to_log2[t][1] = __shfl_sync(0xffffffffu, f, 8 * cc + 4);
+    }
+    plain = !__any_sync(0xffffffffu, not_plain != 0);  // the same for every warp of the block, by the same rows
   }
 
   float o[NT][KS][4], m[NT][2], l[NT][2];
@@ -337,181 +349,192 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 #pragma unroll
     for (int i = 0; i < kAttStages; ++i) toks[i] = toks[i + 1];
   };
-  auto steps = [&](auto bf) {
-    constexpr bool kBf16 = decltype(bf)::value;
-    while (toks[0] < end) {
-      const int tok = toks[0];
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &abort_flag, a.dev_status, a.wait_us * uint64_t(1000)))) break;
-      const uint8_t* const st = my_ring + stage * kStage;
-      const uint32_t held = held_next & 0xFFFF;
-      // ---- scores
-      float s[U][NT][4];
-      if constexpr (kBf16) {
+  while (toks[0] < end && (RARE || plain)) {
+    const int tok = toks[0];
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][stage], parity, &sh.abort_flag, a.dev_status, a.wait_us * uint64_t(1000)))) break;
+    const uint8_t* const st = my_ring + stage * kStage;
+    const uint32_t held = held_next & 0xFFFF;
+    // ---- scores
+    float s[U][NT][4];
+    if constexpr (RARE) {
 #pragma unroll
-        for (int i = 0; i < U * NT * 4; ++i) s[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
+      for (int i = 0; i < U * NT * 4; ++i) s[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t kw[2][KW], sc[2][2];  // [token r or r + 8][...]; a block's scale in both halves
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * u + 8 * h + r;
+        load_words<KW>(kw[h], st + row * (D / 2) + cc * (D / 8));
+        const uint8_t* f = st + 2 * kData + row * (D / 16) + cc * (D / 64);
+        const uint32_t two = e4m3x2_to_f16x2(D == 128 ? *reinterpret_cast<const uint16_t*>(f) : *f);
+        sc[h][0] = __byte_perm(two, two, 0x1010);
+        sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t kw[2][KW], sc[2][2];  // [token r or r + 8][...]; a block's scale in both halves
+      for (int w = 0; w < KW; ++w) {  // a word is two steps
+        uint32_t f[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = 16 * u + 8 * h + r;
-          load_words<KW>(kw[h], st + row * (D / 2) + cc * (D / 8));
-          const uint8_t* f = st + 2 * kData + row * (D / 16) + cc * (D / 64);
-          const uint32_t two = e4m3x2_to_f16x2(D == 128 ? *reinterpret_cast<const uint16_t*>(f) : *f);
-          sc[h][0] = __byte_perm(two, two, 0x1010);
-          sc[h][1] = D == 128 ? __byte_perm(two, two, 0x3232) : sc[h][0];
-        }
+        for (int h = 0; h < 2; ++h) e2m1x8_to_f16x2(kw[h][w], f[h]);
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {  // a word is two steps
-          uint32_t f[2][4];
+        for (int j = 0; j < 2; ++j) {
+          uint32_t x[4] = {mul_f16x2(f[0][2 * j], sc[0][w / 2]), mul_f16x2(f[1][2 * j], sc[1][w / 2]),
+                                 mul_f16x2(f[0][2 * j + 1], sc[0][w / 2]), mul_f16x2(f[1][2 * j + 1], sc[1][w / 2])};
+          if constexpr (RARE) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) e2m1x8_to_f16x2(kw[h][w], f[h]);
+            for (int i = 0; i < 4; ++i) x[i] = f16x2_to_bf16x2(x[i]);
+          }
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t x[4] = {mul_f16x2(f[0][2 * j], sc[0][w / 2]), mul_f16x2(f[1][2 * j], sc[1][w / 2]),
-                                   mul_f16x2(f[0][2 * j + 1], sc[0][w / 2]), mul_f16x2(f[1][2 * j + 1], sc[1][w / 2])};
-            if constexpr (kBf16) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x[i] = f16x2_to_bf16x2(x[i]);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              if constexpr (kBf16) mma_bf16(s[u][t], x, q[t][2 * w + j]);
-              else if (w == 0 && j == 0) mma_f16_first(s[u][t], x, q[t][0]);
-              else mma_f16(s[u][t], x, q[t][2 * w + j]);
-            }
+          for (int t = 0; t < NT; ++t) {
+            if constexpr (RARE) mma_bf16(s[u][t], x, q[t][2 * w + j]);
+            else if (w == 0 && j == 0) mma_f16_first(s[u][t], x, q[t][0]);
+            else mma_f16(s[u][t], x, q[t][2 * w + j]);
           }
         }
       }
-      // ---- running maximum, weights
-      uint32_t vsf[U][4];
+    }
+    // ---- running maximum, weights
+    uint32_t vsf[U][4];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        vsf[u][h] = st[2 * kData + kSf + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 16) + r * (D / 16) / 8];
+    if (tok + kGroup > min(all_see, end) || held != kAll) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool here = held >> (4 * u) & 1;
+        if (!here && tok + 16 * u < end && a.dev_status && lane == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = tok + 16 * u + r + 8 * (i >> 1);
+            const int lim = min(end, row_limit(a, len, row0 + 8 * t + 2 * cc + (i & 1)));
+            if (!here || at >= lim) s[u][t][i] = -INFINITY;
+          }
+        // values past the sequence's end may be anything: a zero scale keeps them out
 #pragma unroll
         for (int h = 0; h < 4; ++h)
-          vsf[u][h] = st[2 * kData + kSf + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 16) + r * (D / 16) / 8];
-      if (tok + kGroup > min(all_see, end) || held != kAll) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool here = held >> (4 * u) & 1;
-          if (!here && tok + 16 * u < end && a.dev_status && lane == 0) atomicOr(a.dev_status, MOE_DEV_BAD_INDEX);
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = tok + 16 * u + r + 8 * (i >> 1);
-              const int lim = min(end, row_limit(a, len, row0 + 8 * t + 2 * cc + (i & 1)));
-              if (!here || at >= lim) s[u][t][i] = -INFINITY;
-            }
-          // values past the sequence's end may be anything: a zero scale keeps them out
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            if (!here || tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1) >= end) vsf[u][h] = 0;
-        }
-        // Of tokens that only some rows see, a scale that is no number is kept from the others too (the MMA
-        // would give them 0 * NaN): the rows that see the first such token get their NaN after the last step.
-        if (all_see < end) {
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const int at = tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1);
-              if (at >= all_see && (vsf[u][h] & 0x7F) == 0x7F) no_number = min(no_number, at), vsf[u][h] = 0;
-            }
-        }
+          if (!here || tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1) >= end) vsf[u][h] = 0;
       }
-      uint32_t p[U][NT][2];
+      // Of tokens that only some rows see, a scale that is no number is kept from the others too (the MMA
+      // would give them 0 * NaN): the rows that see the first such token get their NaN after the last step.
+      if (all_see < end) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float top[2], keep[2];
-        bool grew = false;
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int at = tok + 16 * u + 2 * cc + (h & 1) + 8 * (h >> 1);
+            if (at >= all_see && (vsf[u][h] & 0x7F) == 0x7F) no_number = min(no_number, at), vsf[u][h] = 0;
+          }
+      }
+    }
+    uint32_t p[U][NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float top[2], keep[2];
+      bool grew = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = fmaxf(s[0][t][i], s[0][t][i + 2]);
+#pragma unroll
+        for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][t][i], s[u][t][i + 2]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        if constexpr (!RARE) x = fmaf(x, to_log2[t][i], -kPShift);
+        top[i] = fmaxf(m[t][i], x);
+        grew |= top[i] > m[t][i];
+        keep[i] = top[i] == -INFINITY ? 0.0f : top[i];
+      }
+      if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float x = fmaxf(s[0][t][i], s[0][t][i + 2]);
+          const float f = ex2(RARE ? (m[t][i] - keep[i]) * to_log2[t][i] : m[t][i] - keep[i]);
+          l[t][i] *= f;
 #pragma unroll
-          for (int u = 1; u < U; ++u) x = fmaxf(x, fmaxf(s[u][t][i], s[u][t][i + 2]));
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          top[i] = fmaxf(m[t][i], x);
-          grew |= top[i] > m[t][i];
-          keep[i] = top[i] == -INFINITY ? 0.0f : top[i];
-        }
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float f = ex2((m[t][i] - keep[i]) * to_log2[t][i]);
-            l[t][i] *= f;
-#pragma unroll
-            for (int j = 0; j < KS; ++j) o[t][j][i] *= f, o[t][j][i + 2] *= f;
-            m[t][i] = top[i];
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[u][t][i] = ex2(fmaf(s[u][t][i] - keep[i & 1], to_log2[t][i & 1], kPShift));
-            l[t][i & 1] += s[u][t][i];
-          }
-          p[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
-          p[u][t][1] = transpose8x8(pack_f16x2(s[u][t][2], s[u][t][3]));
+          for (int j = 0; j < KS; ++j) o[t][j][i] *= f, o[t][j][i + 2] *= f;
+          m[t][i] = top[i];
         }
       }
-
-      // ---- weighted values
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(vsf[u][0], vsf[u][1], 0x0040));
-        const uint32_t s89 = e4m3x2_to_f16x2(__byte_perm(vsf[u][2], vsf[u][3], 0x0040));
-        uint32_t vw[4][VW];
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          load_words<VW>(vw[h], st + kData + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 2) + r * (D / 16));
+        for (int i = 0; i < 4; ++i) {
+          s[u][t][i] = ex2(RARE ? fmaf(s[u][t][i] - keep[i & 1], to_log2[t][i & 1], kPShift)
+                                 : fmaf(s[u][t][i], to_log2[t][i & 1], -keep[i & 1]));
+          l[t][i & 1] += s[u][t][i];
+        }
+        p[u][t][0] = transpose8x8(pack_f16x2(s[u][t][0], s[u][t][1]));
+        p[u][t][1] = transpose8x8(pack_f16x2(s[u][t][2], s[u][t][3]));
+      }
+    }
+
+    // ---- weighted values
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          // bytes that pair one dimension's codes of two neighbouring tokens
-          const uint32_t low = 0x0F0F0F0Fu;
-          uint32_t f[4][4];
-          e2m1x8_to_f16x2((vw[0][w] & low) | (vw[1][w] << 4 & ~low), f[0]);
-          e2m1x8_to_f16x2((vw[0][w] >> 4 & low) | (vw[1][w] & ~low), f[1]);
-          e2m1x8_to_f16x2((vw[2][w] & low) | (vw[3][w] << 4 & ~low), f[2]);
-          e2m1x8_to_f16x2((vw[2][w] >> 4 & low) | (vw[3][w] & ~low), f[3]);
+    for (int u = 0; u < U; ++u) {
+      const uint32_t s01 = e4m3x2_to_f16x2(__byte_perm(vsf[u][0], vsf[u][1], 0x0040));
+      const uint32_t s89 = e4m3x2_to_f16x2(__byte_perm(vsf[u][2], vsf[u][3], 0x0040));
+      uint32_t vw[4][VW];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x[4] = {mul_f16x2(f[0][i], s01), mul_f16x2(f[1][i], s01), mul_f16x2(f[2][i], s89),
-                                   mul_f16x2(f[3][i], s89)};
+      for (int h = 0; h < 4; ++h)
+        load_words<VW>(vw[h], st + kData + (16 * u + 2 * cc + (h & 1) + 8 * (h >> 1)) * (D / 2) + r * (D / 16));
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * w + i], x, p[u][t]);
-          }
+      for (int w = 0; w < VW; ++w) {
+        // bytes that pair one dimension's codes of two neighbouring tokens
+        const uint32_t low = 0x0F0F0F0Fu;
+        uint32_t f[4][4];
+        e2m1x8_to_f16x2((vw[0][w] & low) | (vw[1][w] << 4 & ~low), f[0]);
+        e2m1x8_to_f16x2((vw[0][w] >> 4 & low) | (vw[1][w] & ~low), f[1]);
+        e2m1x8_to_f16x2((vw[2][w] & low) | (vw[3][w] << 4 & ~low), f[2]);
+        e2m1x8_to_f16x2((vw[2][w] >> 4 & low) | (vw[3][w] & ~low), f[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x[4] = {mul_f16x2(f[0][i], s01), mul_f16x2(f[1][i], s01), mul_f16x2(f[2][i], s89),
+                                 mul_f16x2(f[3][i], s89)};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * w + i], x, p[u][t]);
         }
       }
-      __syncwarp();  // every lane has read the stage
-      const int next = toks[kAttStages];
-      if (next < end) {
-        issue(stage, next, page);
-        toks[kAttStages + 1] = after(next);
-        page = page_of(toks[kAttStages + 1]);
-      } else {
-        held_next >>= 16;
-        toks[kAttStages + 1] = next;
-      }
-      advance();
-      toks[kAttStages] = toks[kAttStages + 1];
-      if (++stage == kAttStages) stage = 0, parity ^= 1;
     }
-  };
-  if (in_bf16) steps(std::true_type{});
-  else steps(std::false_type{});
-  // after a wait that gave up: the stages still in flight, before their memory is used again
+    __syncwarp();  // every lane has read the stage
+    const int next = toks[kAttStages];
+    if (next < end) {
+      issue(stage, next, page);
+      toks[kAttStages + 1] = after(next);
+      page = page_of(toks[kAttStages + 1]);
+    } else {
+      held_next >>= 16;
+      toks[kAttStages + 1] = next;
+    }
+    advance();
+    toks[kAttStages] = toks[kAttStages + 1];
+    if (++stage == kAttStages) stage = 0, parity ^= 1;
+  }
+  if constexpr (RARE) {  // the references are maxima here: 2^15 of the weights go
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[t][i] *= 0x1p-15f;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) o[t][j][i] *= 0x1p-15f, o[t][j][i + 2] *= 0x1p-15f;
+      }
+  }
+  // after a wait that gave up, or where the case is not plain: the stages in flight, before their memory is used again
   for (int i = 0; i < kAttStages && toks[0] < end; ++i) {
     const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(&full[warp][stage], parity) && globaltimer_ns() - t0 < a.wait_us * uint64_t(1000)) {
-    }
+    while (!mbar_try_wait(&full[warp][stage], parity))
+      if (globaltimer_ns() - t0 > a.wait_us * uint64_t(1000)) {
+        if (a.dev_status) atomicOr(a.dev_status, MOE_DEV_TIMEOUT);
+        break;
+      }
     if (++stage == kAttStages) stage = 0, parity ^= 1;
     advance();
   }
   __syncthreads();
+  if (!plain) return false;
 
   if (__any_sync(0xffffffffu, no_number != INT_MAX)) {
     no_number = min(no_number, __shfl_xor_sync(0xffffffffu, no_number, 1));  // the lanes of the same dimensions
@@ -527,7 +550,6 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 
   // ---- join the warps
   constexpr int ST = D + 4;
-  __shared__ float sm[kAttWarps][R], sl[kAttWarps][R], sf[R];
   auto so = reinterpret_cast<float(*)[R][ST]>(ring);  // [warp][row][dim]
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -538,9 +560,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
       for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
       const int row = 8 * t + 2 * cc + i;
       if (r == 0) {
-        sm[warp][row] = m[t][i];
-        sl[warp][row] = x;
-        if (warp == 0) sf[row] = to_log2[t][i];
+        sh.m[warp][row] = m[t][i];
+        sh.l[warp][row] = x;
+        if (RARE && warp == 0) sh.f[row] = to_log2[t][i];
       }
 #pragma unroll
       for (int j = 0; j < KS; ++j)
@@ -549,17 +571,17 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
   __syncthreads();
   for (int i = tid; i < rows_here * (D / 4); i += kAttWarps * 32) {
     const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
-    const float f_row = sf[row];
-    float top = sm[0][row];
+    const float f_row = RARE ? sh.f[row] : 1.0f;
+    float top = sh.m[0][row];
 #pragma unroll
-    for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sm[w][row]);
+    for (int w = 1; w < kAttWarps; ++w) top = fmaxf(top, sh.m[w][row]);
     float total = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kAttWarps; ++w) {
-      if (sl[w][row] == 0.0f) continue;  // saw nothing (its maximum may be -inf)
-      const float f = ex2((sm[w][row] - top) * f_row);
-      total += sl[w][row] * f;
+      if (sh.l[w][row] == 0.0f) continue;  // saw nothing (its maximum may be -inf)
+      const float f = ex2((sh.m[w][row] - top) * f_row);
+      total += sh.l[w][row] * f;
       const float4 x = *reinterpret_cast<const float4*>(&so[w][row][d]);
       v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
     }
@@ -567,13 +589,31 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
     const int64_t at = (static_cast<int64_t>(b) * a.q_len + t) * a.q_heads + kvh * a.group + g;
     if (a.splits > 1) {
       *reinterpret_cast<float4*>(a.part_o + (at * a.splits + split) * D + d) = v;
-      if (d == 0) a.part_ml[at * a.splits + split] = make_float2(top, total);
-      if (d == 0 && split == 0) a.row_f[at] = f_row;
+      if (d == 0) a.part_ml[at * a.splits + split] = make_float2(top, RARE ? -total : total);
+      if (RARE && d == 0 && split == 0) a.row_f[at] = f_row;
     } else {
       store_row(a, at * D + d, v, total, c.g[1]);
       if (a.lse && d == 0) a.lse[at] = row_lse(top, f_row, total);
     }
   }
+  return true;
+}
+
+// a function of its own: in the kernel, its code and registers cost the plain case up to 0.8 us
+template <int D, int NT, int U>
+__device__ __noinline__ void attend_rare(const Cache& c, const AttendArgs& a, uint8_t* ring, AttendShared<NT>& sh) {
+  attend_block<D, NT, U, true>(c, a, ring, sh);
+}
+
+// U: runs of 16 tokens in a step of a warp. Two keep a short run's chain short; four spend less on the
+// maximum, the barrier and the copies: 131071 tokens 34.5 us against 40.3, 64 x 4000 to 8191 89.5 against 96, 16 x
+// 500 to 2000 11.3 against 12.8; 1 x 2000 6.8 either way.
+template <int D, int NT, int U>
+__global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : NT <= 3 ? 3 : 2)
+    kv_attend_kernel(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ AttendShared<NT> sh;
+  if (!attend_block<D, NT, U, false>(c, a, ring, sh)) attend_rare<D, NT, U>(c, a, ring, sh);
 }
 
 // Joins the parts of query rows, W warps to a row. Every warp weighs all parts (a lane a part; those
@@ -591,11 +631,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, flo
   const int64_t at = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32 / W) + warp / W;
   const bool row = at < rows;
   const float2* ml = a.part_ml + at * a.splits;
-  const float f_row = row ? a.row_f[at] : 0.0f;
-  float top = -INFINITY;
+  float top = -INFINITY, f_row = 1.0f;
+  bool raw = false;  // references are raw sums, totals are stored negative
   if (row)
-    for (int i = lane; i < a.splits; i += 32) top = fmaxf(top, ml[i].x);
+    for (int i = lane; i < a.splits; i += 32) {
+      const float2 x = ml[i];
+      top = fmaxf(top, x.x);
+      raw |= signbit(x.y);
+    }
   top = warp_max(top);
+  if (__any_sync(0xffffffffu, raw)) f_row = a.row_f[at];
   const int part = lane / L, d = lane - part * L;
   const float4* po = reinterpret_cast<const float4*>(a.part_o + at * a.splits * D) + d;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -605,7 +650,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, flo
     if (row && i0 + lane < a.splits) {
       const float2 x = ml[i0 + lane];
       if (x.y != 0.0f) mine = ex2((x.x - top) * f_row);
-      total += mine * x.y;
+      total += mine * fabsf(x.y);
     }
     const int here = min(a.splits - i0, 32);
 #pragma unroll 4

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
 
   // x: half a warp per (token, chunk), eight values a lane, four loads in flight
   const int pairs = threads / 16, piece = tid & 15;
-  bool lost = false;  // some value of x is not exact in FP16
+  uint32_t lost = 0;  // not zero: some value of x is not exact in FP16
   int m_next = chunks ? (tid >> 4) / chunks : M, ch_next = (tid >> 4) - m_next * chunks;
   const int m_step = chunks ? pairs / chunks : 0, ch_step = pairs - m_step * chunks;
   while (m_next < M) {
@@ -248,12 +248,12 @@ __global__ void __launch_bounds__(kLinWarps * 32, 1) linear_kernel(LinArgs a) {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half_warp, amax, o));
         f16_range(amax, &grow, &scale[u]);
-        if (amax < INFINITY)  // a sum with an infinity in it needs no other bits
-          lost |= below_f16(v[0], scale[u]) | below_f16(v[1], scale[u]) | below_f16(v[2], scale[u]) | below_f16(v[3], scale[u]);
         f = make_uint4(pack_f16x2(bf16_lo(v[0]) * grow, bf16_hi(v[0]) * grow),
                        pack_f16x2(bf16_lo(v[1]) * grow, bf16_hi(v[1]) * grow),
                        pack_f16x2(bf16_lo(v[2]) * grow, bf16_hi(v[2]) * grow),
                        pack_f16x2(bf16_lo(v[3]) * grow, bf16_hi(v[3]) * grow));
+        if (amax < INFINITY)  // a sum with an infinity in it needs no other bits
+          lost |= below_f16(v[0], f.x) | below_f16(v[1], f.y) | below_f16(v[2], f.z) | below_f16(v[3], f.w);
       } else {
         f = make_uint4(e4m3x2_to_f16x2(v[0] & 0xFFFF), e4m3x2_to_f16x2(v[0] >> 16), e4m3x2_to_f16x2(v[1] & 0xFFFF),
                        e4m3x2_to_f16x2(v[1] >> 16));

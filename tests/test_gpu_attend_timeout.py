@@ -15,15 +15,18 @@ from test_gpu_decoder import Pool, queries, sequences
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("outlier", [False, True])        # queries that a block starts again for
 @pytest.mark.parametrize("lens,Hkv,G,T,Dh,page", [((40, 5), 2, 4, 1, 128, 64),            # one block a sequence
                                                   ((9000, 700, 3), 1, 8, 1, 128, 16),     # split and joined
                                                   ((6000,) * 40, 8, 4, 1, 128, 64),       # four 16-token runs a step
                                                   ((3000, 64), 2, 6, 4, 64, 32)])         # three tiles of rows
-def test_withheld_copies_time_out_and_the_next_call_is_exact(lens, Hkv, G, T, Dh, page):
+def test_withheld_copies_time_out_and_the_next_call_is_exact(lens, Hkv, G, T, Dh, page, outlier):
     p = Pool(sum(-(-n // page) for n in lens), page, Hkv, Dh)
     table, ln, _ = sequences(p, list(lens))
     B, Hq = len(lens), Hkv * G
     q = queries(B, T, Hq, Dh)
+    if outlier:
+        q[..., 0] = 2.0 ** 40
     n = pkg.moe_kv_attend_workspace_bytes(p.kv.c, B, T, Hq, table.shape[1])
     ws = torch.empty(n, dtype=torch.uint8, device=DEV) if n else None
 

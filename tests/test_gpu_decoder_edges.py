@@ -17,9 +17,10 @@ pytestmark = pytest.mark.gpu
 
 
 # ------------------------------------------------------------------ attention: large scores
-def exact_scores_check(out, lse, q, held, Hkv, scale):
+def exact_scores_check(out, lse, q, held, Hkv, scale, smallest=0.0):
     """Against the oracle where every score is exact in 32 bits: only the weights' rounding (2^-10 of the
-    mass) and the result's (2^-8 of the value) are left; the log-sum-exp has 8 roundings of its size."""
+    mass) and the result's (2^-8 of the value) are left; the log-sum-exp has 8 roundings of its size. `smallest`: the
+    error of a weight of any size, of the largest one: FP16 ends at 2^-24, the largest weight is above 2^14, so 2^-39."""
     B, T, Hq, Dh = q.shape
     G = Hq // Hkv
     qf = f32_np(q).astype(np.float64)
@@ -28,7 +29,8 @@ def exact_scores_check(out, lse, q, held, Hkv, scale):
         for h in range(Hkv):
             hs = slice(h * G, (h + 1) * G)
             o, l, mass = D.attend(qf[b, :, hs], k[:, h], v[:, h], scale)
-            assert_within(bf16_np(out)[b, :, hs], o, np.abs(o) * (2.0 ** -8 + 2.0 ** -18) + mass * 2.0 ** -10 + 1e-30, "out")
+            assert_within(bf16_np(out)[b, :, hs], o, np.abs(o) * (2.0 ** -8 + 2.0 ** -18) + mass * 2.0 ** -10 + 1e-30
+                          + smallest * np.abs(v[:, h]).sum(0), "out")
             assert_within(to_np(lse).astype(np.float64)[b, :, hs], l, np.abs(l) * 8 * U + 2.0 ** -20, "lse")
 
 
@@ -253,3 +255,21 @@ def test_append_stores_only_numbers(Dh, g):
         assert stored[0, 0, 3] == sign * 6 * 448 / g and stored[1, 1, 17] == -sign * 6 * 448 / g
         scale = np.repeat(F.e4m3_decode(scales), 16, -1)
         assert (np.abs(stored) <= 6 * scale / g).all()
+
+
+@pytest.mark.parametrize("Hkv,G,T,Dh,page,lens", [(2, 4, 1, 128, 64, (700, 90)), (1, 6, 4, 64, 16, (500, 33)), (1, 8, 1, 128, 32, (20000, 100)),
+                                                 (1, 16, 1, 128, 16, (3000, 1)), (8, 4, 1, 128, 64, (3000,) * 40)])
+def test_attend_scores_of_every_size_in_one_block(Hkv, G, T, Dh, page, lens):
+    """Rows whose possible scores lie below, around and above the size where the weights' reference changes, some of
+    them in one block. Every query value is the same power of two and every key's values share a quantum, so the
+    scores are exact in 32 bits; keys of 500 times a normal value reach a score of 0.3 of the possible."""
+    p = Pool(sum(-(-m // page) for m in lens), page, Hkv, Dh)
+    table, ln, held = sequences(p, list(lens), seed=Dh + T, spread=500.0)
+    r = np.random.default_rng(T)
+    for span in ((-6, -3), (-2, 5), (-14, 18)):
+        sign = r.choice([-1.0, 1.0], size=(len(lens), T, Hkv * G, Dh))
+        q = bf16(sign * 2.0 ** r.integers(*span, size=(len(lens), T, Hkv * G, 1)))
+        out, lse = p.kv.attend(q, table, ln, softmax_scale=1.0)
+        for b in range(len(lens)):                          # the sums' terms are whole multiples of a quantum
+            assert np.abs(held[b][0]).sum(-1).max(initial=0.0) < 2 ** 24 * np.abs(held[b][0][held[b][0] != 0]).min()
+        exact_scores_check(out, lse, q, held, Hkv, 1.0, 2.0 ** -39)
