@@ -395,7 +395,8 @@ MOE_API moe_status_t moe_add_rmsnorm(const uint16_t* x, int64_t ld_x, const uint
 
 /* ----------------------------------------------------------------------------------------
  * moe_linear_fp4 - y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]) for a few tokens, the
- * weights read once per 16 tokens:
+ * weights read once per 16 tokens. Products of finite values are exact whatever their range, sums are FP32,
+ * and a NaN goes through every activation:
  *   x          [M, ld_x] BF16 (x_scale_mode MOE_FP8_NONE; ld_x % 8 == 0) or E4M3 (MOE_FP8_PER_TOKEN
  *              or MOE_FP8_PER_GROUP; ld_x % 16 == 0), first K columns used. The activations are
  *              not rounded any further; E4M3 values are multiplied by their scale in FP32
@@ -465,7 +466,10 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const uint16_t* 
  *   lse = ln sum_j exp(s_j)
  * for query head h with the keys and values of kv head h / (num_q_heads / num_kv_heads). A row
  * that sees nothing gets out = 0 and lse = -inf. Whatever the cache holds past a sequence's
- * end is never used.
+ * end is never used, and no row is changed by what a token that it does not see holds. Queries and cached values enter
+ * the products exactly, whatever their range, and scores may be of any size. Sums are FP32; the weights exp(s_j) are
+ * rounded to 11 significant bits before they meet the values (fewer below 2^-29 of the row's largest, nothing is left
+ * below 2^-39), their sum is not.
  *   q           [batch * q_len, ld_q] BF16, the num_q_heads * head_dim values of a row contiguous;
  *               ld_q % 8 == 0
  *   page_table  [batch, ld_table] int32: page i of sequence b; entries past its length are not
@@ -473,7 +477,7 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const uint16_t* 
  *   max_pages   columns of page_table in use, <= ld_table: lengths above max_pages * page_size
  *               are cut there and set MOE_DEV_BAD_INDEX. The work is cut by max_pages (lengths are not
  *               read on the host): columns far beyond the longest sequence cost time, 64 sequences of
- *               4000 to 8191 tokens 103 us with 131072 tokens' columns against 89
+ *               4000 to 8191 tokens 104 us with 131072 tokens' columns against 92
  *   seq_lens    [batch] int32 (negative: empty)
  *   out         [batch * q_len, num_q_heads, head_dim] BF16;  lse [batch * q_len, num_q_heads]
  *               FP32 or NULL

@@ -1,9 +1,9 @@
-// FP4 operands on mma.m16n8k16 (FP16 in, FP32 sums): the conversions and instructions that the
+// FP4 operands on mma.m16n8k16 (FP16 or BF16 in, FP32 sums): the conversions and instructions that the
 // dense linear and the cache's attention share. Both read each 4-bit value once, for at most 16
 // tokens or 32 query rows, and convert it in registers, where the legacy warp-level MMA takes its
 // operands from. Per two values that is one conversion and one multiplication by the scale, either at
 // half rate; the MMA pipe itself is busy a quarter of the time. An E2M1 code times an E4M3 scale
-// has 6 significant bits between 2^-10 and 2688: exact in FP16.
+// has 6 significant bits between 2^-10 and 2688: exact in FP16, and in BF16.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -113,9 +113,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(Cache c, cons
 // MMAs for the scores (the keys take a second conversion), with p = 2^((s - max) f + 15), which is right for
 // scores of any size.
 //
-// Bound by the conversion (ALU pipe 54 %, issue slots 61 % in use; 17.8 instructions per token and kv head), not by
-// HBM: 64 sequences of 4000 to 8191 tokens, 8 kv heads, 87 us (5.0 TB/s; the copies alone 73 us), one of
-// 131071 tokens 35 us. Short ones by the chain of length, pages, first copies, steps and the join.
+// Bound by latency at three warps a scheduler: no pipe is full (ALU, which converts, 54 %; issue slots 61 %; HMMA
+// 27 %; 18.0 instructions per token and kv head), nor is HBM: 64 sequences of 4000 to 8191 tokens, 8 kv heads, 88 us
+// (5.0 TB/s; the copies alone 73 us), one of 131071 tokens 35 us. Short ones by the chain of length, pages, first
+// copies, steps and the join. Blocks that start again: those 64 sequences 125 us, the one 45.
 constexpr int kAttWarps = 4;
 constexpr int kAttStages = 2;
 constexpr float kPShift = 15.0f;
@@ -606,8 +607,8 @@ __device__ __noinline__ void attend_rare(const Cache& c, const AttendArgs& a, ui
 }
 
 // U: runs of 16 tokens in a step of a warp. Two keep a short run's chain short; four spend less on the
-// maximum, the barrier and the copies: 131071 tokens 34.5 us against 40.3, 64 x 4000 to 8191 89.5 against 96, 16 x
-// 500 to 2000 11.3 against 12.8; 1 x 2000 6.8 either way.
+// maximum, the barrier and the copies: 131071 tokens 35.2 us against 38.9, 64 x 4000 to 8191 91.9 against 102, 16 x
+// 500 to 2000 11.9 against 14.0; 1 x 2000 7.1 either way.
 template <int D, int NT, int U>
 __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : NT <= 3 ? 3 : 2)
     kv_attend_kernel(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a) {
@@ -685,9 +686,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, flo
 
 // Steps that a block takes side by side, where several sequences share the SMs; a lone one's blocks take
 // every so-manieth step. One run for each block would leave most blocks without work where the table is far wider
-// than the sequences (131072 tokens' columns: 16 x 0 to 4097 tokens 34.2 us, one of 2000 16.0), runs of one step
-// spread short sequences over more blocks than they are worth: those two 15.9 and 7.2 us, but 3 % more time on average over
-// 39 shapes with tables as wide as the longest sequence. Runs of 8: 24.8, 7.2, and 2 %.
+// than the sequences, runs of one step spread short sequences over more blocks than they are worth. One run, runs of one and
+// runs of 8, with 131072 tokens' columns: 16 x 0 to 4097 tokens 34.6, 16.0 and 25.1 us, 64 x 4000 to 8191 131, 121 and 104;
+// with the sequences' own: 16 x 500 to 2000 11.9, 14.1 and 11.9, 64 x 4000 to 8191 91.9, 94.1 and 91.9.
 constexpr int kAttRun = 8;
 
 // How a call is cut: rows of a block, and blocks of a sequence. A block takes as many row tiles as
@@ -710,8 +711,8 @@ Cut cut_attend(int batch, int kv_heads, int head_dim, int rows, int64_t most) {
   //   table, all but the last tenth of what runs at once is shared evenly where there are more than that;
   //   2.4 for the join and 1.4e-5 per row and run (half for D = 64).
   // Constants fitted to 39 shapes from 1 x 500 tokens to 64 x 8191, each timed in every cut. With three draws of the lengths
-  // of the ragged ones the cut chosen is on average 5 % off the best (worst 39 %: the lengths are
-  // not known here); runs of at least two steps that filled the SMs once or twice were 11 % off (worst 42 %): 1 x 60000
+  // of the ragged ones the cut chosen is on average 6 % off the best (worst 38 %: the lengths are
+  // not known here); before the fit, runs of at least two steps that filled the SMs once or twice were 11 % off (worst 42 %): 1 x 60000
   // tokens of 8 rows on one kv head 15.2 us against 10.9, 16 x 500 to 2000 of 8 x 4 heads 14.2 against 11.4; the other
   // way 3 x 10000 to 20000 of 8 x 8 heads 21.3 against 24.4.
   const int sms = num_sms();

@@ -1,9 +1,10 @@
 // A few tokens times one dense NVFP4 matrix: y[m, n] = act(alpha * sum_k x[m, k] * w[n, k]).
 //
-// 9/16 byte per weight, read once per 16 tokens: bound by the weights' conversion, close behind it by
-// HBM. A warp takes 16 rows of w and a run of K: mma.m16n8k16 with the 16 weight rows as one
-// operand and eight tokens as the other. K goes by chunks of 128 values. In a chunk lane (r, c) = (lane / 4, lane % 4) holds the values 32c
-// to 32c + 31 of rows r and r + 8, and MMA step j takes its values 32c + 4j to 32c + 4j + 3.
+// 9/16 byte per weight, read once per 16 tokens: bound by latency at four warps a scheduler (issue slots 62 %,
+// the ALU pipe, which converts, 47 %) and by HBM (76 % of the copy rate). A warp takes 16 rows of w and a run
+// of K: mma.m16n8k16 with the 16 weight rows as one operand and eight tokens as the other. K goes by chunks
+// of 128 values. In a chunk lane (r, c) = (lane / 4, lane % 4) holds the values 32c to 32c + 31 of rows r and
+// r + 8, and MMA step j takes its values 32c + 4j to 32c + 4j + 3.
 //
 // The codes come through a ring in shared memory that belongs to the warp (cp.async; two chunks a
 // stage, two or three of them): copied as 128 contiguous bytes per row, a quarter of the L1 lines
@@ -25,10 +26,10 @@
 // results do not depend on timing. alpha, the activation and the BF16 rounding come once at the
 // end. A block goes on to further rows while there are any, their first chunks already in flight.
 //
-// Measured: 4 tokens x 129021 x 4096 57.4 us (5.2 TB/s; 158 instructions per 16 rows and chunk, 62 % of the
-// issue slots, 64 of them conversions at half rate); 8 x 4096 x 7168 with SwiGLU, E4M3 8.1 us, 1 x 2048 x 512
-// 3.4 us, both chains of launch, loads, sums and barrier. (The loop over rows exists twice: with a
-// choice of the MMA inside it calls that do not run BF16 ones took 0.2 to 1.2 us more.)
+// Measured: 4 tokens x 129021 x 4096 57.6 us (5.2 TB/s; 159 instructions per 16 rows and chunk, 64 of them
+// conversions at half rate; on BF16 MMAs 85 us); 8 x 4096 x 7168 with SwiGLU, E4M3 8.1 us, 1 x 2048 x 512
+// 3.4 us, both chains of launch, loads, sums and barrier. The loop over rows exists twice: with the choice of
+// the MMA inside it, calls that do not run BF16 ones took 0.2 to 1.2 us more.
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -482,7 +483,7 @@ static int linear_smem(const LinCut& k, int align) {
 //   where one warp takes a run of K alone and 13 % where two or three do (DRAM: whole rows 5.9 TB/s, one run 4.8).
 // Of that and the weights' bytes at 6 TB/s the longer counts, and a fifth of the shorter. Constants fitted to 61 shapes from
 // 1 x 200 x 8192 to 4 x 129021 x 4096 and 16 x 60000 x 7168, each timed in every cut: the cut chosen is on average 2 %
-// off the best of them (worst 12 %). Halving and doubling blocks and slices until they filled the SMs was 15 %
+// off the best of them (worst 20 %). Before the fit, halving and doubling blocks and slices until they filled the SMs was 15 %
 // off (worst 52 %): 12 x 10240 x 7168 30.2 us against 21.6, 1 x 4096 x 4096 7.2 against 5.7.
 bool cut_linear(int64_t M, int K, int n_out, bool gated, int align, int sms, LinCut* cut) {
   // warps and across: all of a block's to one tile of rows for little work, whole tiles for much
