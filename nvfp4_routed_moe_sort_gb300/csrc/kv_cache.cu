@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, NT == 1 ? (U == 2 ? 4 : 3) : N
 }
 
 // Joins the parts of query rows, W warps to a row. Every warp weighs all parts (a lane a part; those
-// that saw nothing have weight 0 and are not read), then adds every so-manieth part with D / 4 lanes
+// that saw nothing are not read, those of weight 0 are, for they may hold a NaN), then adds every so-manieth part with D / 4 lanes
 // of four dimensions each; the groups of lanes are added in order.
 constexpr int kJoinThreads = 256;
 
@@ -647,17 +647,19 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a, flo
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float total = 0.0f;
   for (int i0 = 0; i0 < a.splits; i0 += 32) {
-    float mine = 0.0f;
+    float mine = -1.0f;
     if (row && i0 + lane < a.splits) {
       const float2 x = ml[i0 + lane];
-      if (x.y != 0.0f) mine = ex2((x.x - top) * f_row);
-      total += mine * fabsf(x.y);
+      if (x.y != 0.0f) {
+        mine = ex2((x.x - top) * f_row);
+        total += mine * fabsf(x.y);
+      }
     }
     const int here = min(a.splits - i0, 32);
 #pragma unroll 4
     for (int j = w * P; j < here; j += W * P) {
       const float f = __shfl_sync(0xffffffffu, mine, (j + part) & 31);
-      if (j + part < here && f != 0.0f) {
+      if (j + part < here && !(f < 0.0f)) {
         const float4 x = po[static_cast<int64_t>(i0 + j + part) * L];
         v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
       }

@@ -273,3 +273,20 @@ def test_attend_scores_of_every_size_in_one_block(Hkv, G, T, Dh, page, lens):
         for b in range(len(lens)):                          # the sums' terms are whole multiples of a quantum
             assert np.abs(held[b][0]).sum(-1).max(initial=0.0) < 2 ** 24 * np.abs(held[b][0][held[b][0] != 0]).min()
         exact_scores_check(out, lse, q, held, Hkv, 1.0, 2.0 ** -39)
+
+
+@pytest.mark.parametrize("n,B", [(30000, 1), (9000, 3)])
+def test_attend_no_number_shows_however_small_its_weight(n, B):
+    """A value that is no number at a token whose weight is 0 in 32 bits, in another part of the sequence than the
+    token that has all of the weight."""
+    p = Pool(-(-n // 64) * B, 64, 1, 128)
+    table, ln, held = sequences(p, [n] * B, seed=n)
+    q = bf16(np.stack([np.tile(100.0 * held[b][0][n - 5], (1, 4, 1)) for b in range(B)]))
+    out, lse = (t.clone() for t in p.kv.attend(q, table, ln))
+    assert torch.isfinite(out.float()).all()
+    p.t[3][int(table[0, 0]), 0, 7, 2] = 0x7F
+    got, got_lse = p.kv.attend(q, table, ln)
+    want = out.clone()
+    want[0, :, :, 32:48] = float("nan")
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got_lse, lse)
+    assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
