@@ -494,6 +494,92 @@ MOE_API moe_status_t moe_kv_attend(const moe_kv_cache_t* cache, const uint16_t* 
                                    float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                    moe_stream_t stream);
 
+/* ----------------------------------------------------------------------------------------
+ * moe_quantize_fp8 - BF16 to E4M3 with FP32 scales, the rule of moe_add_rmsnorm's y8 without its norm:
+ * per scale group scale = amax|x| / 448 (1 when amax is 0), y = e4m3(x * (448 / amax)).
+ *   x           [M, ld_x] BF16 (first K columns used), ld_x >= K
+ *   block_rows  1: a scale per row and MOE_FP8_GROUP columns, as moe_linear_fp8 and moe_linear_fp4 take
+ *               activations; MOE_FP8_GROUP: a scale per 128 x 128 block, as moe_linear_fp8 takes its matrix
+ *   y           [M, K] E4M3 (out);  y_scale [ceil(M / block_rows), ceil(K / 128)] FP32 (out)
+ * Any M and K; K, ld_x multiples of 8 and 16-byte aligned rows are fastest. M == 0 is a no-op. A NaN or
+ * an infinity makes its group's scale and values NaN or infinite, or 0 where finite ones meet an infinity.
+ * ---------------------------------------------------------------------------------------- */
+MOE_API moe_status_t moe_quantize_fp8(const uint16_t* x, int64_t ld_x, int32_t M, int32_t K, int32_t block_rows,
+                                      uint8_t* y, float* y_scale, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * moe_linear_fp8 - any number of tokens times an E4M3 matrix with one scale per 128 x 128 block:
+ *   y[m, n] = act(sum_b x_scale[m, b] * w_scale[n / 128, b] * sum_{k in block b of 128} x[m, k] * w[n, k])
+ *   x             [M, ld_x] E4M3 (first K columns used), ld_x % 16 == 0
+ *   x_scale       [M] (x_scale_mode MOE_FP8_PER_TOKEN) or [M, ceil(K / 128)] (MOE_FP8_PER_GROUP) FP32, as
+ *                 moe_add_rmsnorm and moe_quantize_fp8 write them
+ *   w, w_scale    [N, K] E4M3 and [ceil(N / 128), ceil(K / 128)] FP32, as moe_quantize_fp8 writes them with
+ *                 blocks of 128 rows
+ *   activation    moe_activation_t. The gated kinds take w rows [gate; up], N a multiple of 256 (each half
+ *                 whole blocks), and write N/2 columns; MOE_ACT_IDENTITY is a plain product
+ *   out           [M, N] (gated: [M, N/2]) BF16, contiguous: FP32 sums, one rounding at the end
+ *   dev_status    may be NULL
+ * Products of a block of 128 are summed by the tensor core in FP32, then scaled and added in FP32. NaN codes
+ * make NaN outputs in their row (of x) or column (of w). K % 16 == 0, K <= 65536, M and N <= 2^22.
+ * M == 0 is a no-op.
+ * ---------------------------------------------------------------------------------------- */
+MOE_API moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode,
+                                    int32_t M, int32_t K, const uint8_t* w, const float* w_scale, int32_t N,
+                                    int32_t activation, uint16_t* out, int32_t* dev_status, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * moe_rotary - turns queries and keys by their tokens' positions. Pair i < rotary_dim / 2 of each head of
+ * token n:
+ *   angle = positions[axes[i], n] * inv_freq[i],  (a, b) -> (a cos - b sin, a sin + b cos)
+ * in FP32 with one rounding; the pair is values (i, i + rotary_dim / 2) of the head, or (2 i, 2 i + 1) with
+ * `adjacent`. The head's other values stay. The angle is right to 2^-30 of a turn for positions up to 2^23, and up to
+ * 2^31 as right as a float64 product.
+ *   q           [N, ld_q] BF16, the num_q_heads * head_dim values of a token contiguous; any ld_q from that on
+ *               (slices of one projection's output will do)
+ *   k           the same with num_k_heads, or NULL with num_k_heads 0
+ *   head_dim    up to 1024; rotary_dim even, 2 to head_dim
+ *   positions   [num_axes, ld_positions] int32 or int64 (position_bytes 4 or 8), the first N of a row used; any
+ *               sign
+ *   num_axes    1 to 4: one for text; time, height and width for images and video
+ *   inv_freq    [rotary_dim / 2] float64, finite: radians per position
+ *   axes        [rotary_dim / 2] uint8: the axis of each pair, or NULL with one axis. A pair of an axis
+ *               that is none is not turned and sets MOE_DEV_BAD_INDEX
+ *   q_out, k_out  like q and k, with strides of their own; each may be its input itself (same stride)
+ *   dev_status  may be NULL
+ * Up to 1024 heads each. N == 0 is a no-op. rotary_dim a multiple of 16 and 16-byte aligned tokens are fastest.
+ * ---------------------------------------------------------------------------------------- */
+MOE_API moe_status_t moe_rotary(const uint16_t* q, int64_t ld_q, int32_t num_q_heads, const uint16_t* k, int64_t ld_k,
+                                int32_t num_k_heads, int32_t head_dim, int32_t rotary_dim, int32_t adjacent,
+                                const void* positions, int32_t position_bytes, int64_t ld_positions, int32_t num_axes,
+                                const double* inv_freq, const uint8_t* axes, int32_t N, uint16_t* q_out, int64_t ld_q_out,
+                                uint16_t* k_out, int64_t ld_k_out, int32_t* dev_status, moe_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * moe_sample - one token per row of logits. With a row's tokens in the order of their logits (ties: the
+ * lower index first) and weights w = exp((logit - max) / temperature), these keep a front part of the order:
+ *   top_k    its first k tokens (k <= 0 or >= V: all)
+ *   top_p    the shortest part whose weights reach top_p times the sum of what top_k kept, at least one token
+ *            (>= 1 or NaN: all)
+ *   min_p    the tokens with w >= min_p, those with the largest logit always (<= 0 or NaN: all)
+ * and the token taken is, among the kept ones in the order of their index, the first at which the cumulated
+ * weight passes uniform times their sum. Weights have 36 significant bits (nothing is left below 2^-44 of the largest)
+ * and sums are exact, so that the token is that of exact arithmetic unless uniform lies within about 2^-36 of a border
+ * between two tokens.
+ *   logits       [B, ld_logits] FP32 or BF16 (logits_dtype), first V columns used; V <= 2^18. -infinity masks
+ *                a token, NaN too; a row with nothing else gives -1; +infinity leaves the other tokens no weight
+ *   uniform      [B] FP32 in [0, 1): one random number per row (outside: the nearest one inside; NaN: 0)
+ *   temperature  [B] FP32 or NULL (1). Zero, negative and NaN (and what is below 2^-100): the largest logit's
+ *                lowest index. Above 2^100: as 2^100
+ *   top_k        [B] int32 or NULL;  top_p, min_p [B] FP32 or NULL
+ *   tokens       [B] int32 (out)
+ * B == 0 is a no-op. Results repeat bit for bit, whatever the batch around a row.
+ * ---------------------------------------------------------------------------------------- */
+typedef enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 } moe_logits_dtype_t;
+
+MOE_API moe_status_t moe_sample(const void* logits, int32_t logits_dtype, int64_t ld_logits, int32_t B, int32_t V,
+                                const float* uniform, const float* temperature, const int32_t* top_k, const float* top_p,
+                                const float* min_p, int32_t* tokens, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,7 @@ MOE_IDS_INT32, MOE_IDS_PACKED = 0, 1
 MOE_OUTPUT_UNFINALIZED, MOE_OUTPUT_FINALIZED, MOE_OUTPUT_ACCUMULATE = 0, 1, 2
 MOE_FP8_NONE, MOE_FP8_PER_TOKEN, MOE_FP8_PER_GROUP = 0, 1, 2
 MOE_FP8_GROUP = 128
+MOE_LOGITS_F32, MOE_LOGITS_BF16 = 0, 1
 
 EXPORTED = [
     "moe_status_string", "moe_abi_version", "moe_quantize_input", "moe_plan_capacity",
@@ -38,6 +39,7 @@ EXPORTED = [
     "moe_grouped_fp4_forward", "moe_finalize", "moe_plan_noalloc",
     "moe_routed_forward_workspace_bytes", "moe_routed_forward",
     "moe_add_rmsnorm", "moe_linear_fp4", "moe_kv_append", "moe_kv_attend_workspace_bytes", "moe_kv_attend",
+    "moe_quantize_fp8", "moe_linear_fp8", "moe_rotary", "moe_sample",
 ]
 # the test build's extra entry points (include/moe_nvfp4_test.h)
 TEST_EXPORTED = ["moe_test_default_options", "moe_test_routed_forward", "moe_test_gemm1", "moe_test_linear_cut",
@@ -112,6 +114,11 @@ def _declare(lib, test=False):
         "moe_kv_append": (c_int32, [ctypes.POINTER(KVCacheT), P, c_int64, P, c_int64, P, c_int32, P, P, P, P]),
         "moe_kv_attend_workspace_bytes": (c_size_t, [ctypes.POINTER(KVCacheT), c_int32, c_int32, c_int32, c_int32]),
         "moe_kv_attend": (c_int32, attend + [P]),
+        "moe_quantize_fp8": (c_int32, [P, c_int64, c_int32, c_int32, c_int32, P, P, P]),
+        "moe_linear_fp8": (c_int32, [P, c_int64, P, c_int32, c_int32, c_int32, P, P, c_int32, c_int32, P, P, P]),
+        "moe_rotary": (c_int32, [P, c_int64, c_int32, P, c_int64, c_int32, c_int32, c_int32, c_int32, P, c_int32, c_int64,
+                                 c_int32, P, P, c_int32, P, c_int64, P, c_int64, P, P]),
+        "moe_sample": (c_int32, [P, c_int32, c_int64, c_int32, c_int32, P, P, P, P, P, P, P]),
     }
     if test:
         sig.update({
@@ -393,6 +400,43 @@ def moe_kv_attend(cache: KVCacheT, q, ld_q, page_table, seq_lens, softmax_scale,
         st = test_lib().moe_test_kv_attend(*args, ctypes.byref(test_options), _stream(stream))
     if st:
         _check(st, "moe_kv_attend")
+
+
+def moe_quantize_fp8(x, block_rows, y, y_scale, stream=None):
+    """x [M, K] bf16 may have a row stride; y [M, K] and y_scale [ceil(M / block_rows), ceil(K / 128)] are contiguous."""
+    M, K = x.shape
+    _check(lib().moe_quantize_fp8(_ptr(x), x.stride(0) if M > 1 else K, M, K, block_rows, _ptr(y), _ptr(y_scale),
+                                  _stream(stream)), "moe_quantize_fp8")
+
+
+def moe_linear_fp8(x, x_scale, x_scale_mode, w, w_scale, activation, out, dev_status=None, stream=None):
+    """x [M, K] float8_e4m3fn (it may have a row stride); w [N, K], w_scale [ceil(N / 128), ceil(K / 128)]."""
+    M, K = x.shape
+    _check(lib().moe_linear_fp8(_ptr(x), x.stride(0) if M > 1 else K, _ptr(x_scale), x_scale_mode, M, K, _ptr(w),
+                                _ptr(w_scale), w.shape[0], activation, _ptr(out), _ptr(dev_status), _stream(stream)),
+           "moe_linear_fp8")
+
+
+def moe_rotary(q, k, rotary_dim, adjacent, positions, inv_freq, axes, q_out, k_out, dev_status=None, stream=None):
+    """q, q_out [N, heads, head_dim] bf16 and k, k_out (or None), each with a token stride; positions [num_axes, N]
+    int32 or int64; inv_freq [rotary_dim / 2] float64; axes [rotary_dim / 2] uint8 or None."""
+    N, heads, dim = q.shape
+
+    def ld(t):
+        return 0 if t is None else t.stride(0) if N > 1 else t.shape[1] * dim
+    _check(lib().moe_rotary(_ptr(q), ld(q), heads, _ptr(k), ld(k), 0 if k is None else k.shape[1], dim, rotary_dim,
+                            int(adjacent), _ptr(positions), positions.element_size(), positions.stride(0),
+                            positions.shape[0], _ptr(inv_freq), _ptr(axes), N, _ptr(q_out), ld(q_out), _ptr(k_out),
+                            ld(k_out), _ptr(dev_status), _stream(stream)), "moe_rotary")
+
+
+def moe_sample(logits, uniform, temperature, top_k, top_p, min_p, tokens, stream=None):
+    """logits [B, V] float32 or bf16 (it may have a row stride); the settings are [B] tensors or None."""
+    import torch
+    B, V = logits.shape
+    dtype = MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else MOE_LOGITS_F32
+    _check(lib().moe_sample(_ptr(logits), dtype, logits.stride(0) if B > 1 else V, B, V, _ptr(uniform), _ptr(temperature),
+                            _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(tokens), _stream(stream)), "moe_sample")
 
 
 def linear_cut(M, K, N, gated=False, num_sms=152) -> dict:

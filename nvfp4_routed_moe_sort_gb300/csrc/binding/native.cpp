@@ -307,9 +307,128 @@ PyObject* kv_attend(PyObject* const* a) {
               "moe_kv_attend");
 }
 
+int32_t* status_word(const at::Tensor* t) {
+  if (t && (t->scalar_type() != at::kInt || !t->is_cuda() || t->numel() < 1)) refuse("dev_status", "int32 on the GPU");
+  return static_cast<int32_t*>(pointer(t));
+}
+
+// (x, block_rows, y, scale)
+PyObject* quantize_fp8(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], "x");
+  if (x.dim() != 2) refuse("x", "[M, K]");
+  const int64_t M = x.size(0), K = x.size(1);
+  rows(&x, kBf16, M, K, "x", "bf16 rows on the GPU, their values side by side");
+  const long block = integer(a[1]);
+  if (block != 1 && block != MOE_FP8_GROUP) refuse("rows", "1 or 128");
+  const at::Tensor &y = tensor(a[2], "y"), &sc = tensor(a[3], "the scales");
+  dense(&y, kE4m3, {M, K}, "y", "contiguous float8_e4m3fn [M, K] on the GPU");
+  dense(&sc, at::kFloat, {(M + block - 1) / block, (K + MOE_FP8_GROUP - 1) / MOE_FP8_GROUP}, "the scales",
+        "contiguous float32 [ceil(M / rows), ceil(K / 128)] on the GPU");
+  const moe_stream_t stream = stream_of({{&x, "x"}, {&y, "y"}, {&sc, "the scales"}});
+  return done(moe_quantize_fp8(static_cast<const uint16_t*>(x.data_ptr()), ld(x, K), int32_size(M, "x"), int32_size(K, "x"),
+                               static_cast<int32_t>(block), static_cast<uint8_t*>(y.data_ptr()),
+                               static_cast<float*>(sc.data_ptr()), stream),
+              "moe_quantize_fp8");
+}
+
+// (x, x_scale, w, w_scale, activation, out, dev_status)
+PyObject* fp8_linear(PyObject* const* a) {
+  const at::Tensor &x = tensor(a[0], "x"), &xs = tensor(a[1], "x_scale"), &w = tensor(a[2], "w"), &ws = tensor(a[3], "w_scale");
+  if (x.dim() != 2 || w.dim() != 2) refuse("x and w", "[M, K] and [N, K]");
+  const int64_t M = x.size(0), K = x.size(1), N = w.size(0), groups = (K + MOE_FP8_GROUP - 1) / MOE_FP8_GROUP;
+  rows(&x, kE4m3, M, K, "x", "float8_e4m3fn rows on the GPU, their values side by side");
+  const bool one = xs.dim() == 2 && xs.size(1) == 1;
+  dense(&xs, at::kFloat, {M, one ? 1 : groups}, "x_scale", "contiguous float32 [M, 1] or [M, ceil(K / 128)] on the GPU");
+  dense(&w, kE4m3, {N, K}, "w", "contiguous float8_e4m3fn [N, K] on the GPU");
+  dense(&ws, at::kFloat, {(N + MOE_FP8_GROUP - 1) / MOE_FP8_GROUP, groups}, "w_scale",
+        "contiguous float32 [ceil(N / 128), ceil(K / 128)] on the GPU");
+  const long act = integer(a[4]);
+  const bool gated = act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU;
+  const at::Tensor& out = tensor(a[5], "out");
+  dense(&out, kBf16, {M, gated ? N / 2 : N}, "out", "contiguous bf16 [M, N] (gated: [M, N/2]) on the GPU");
+  const at::Tensor* status = maybe(a[6], "dev_status");
+  int32_t* const word = status_word(status);
+  const moe_stream_t stream = stream_of(
+      {{&x, "x"}, {&xs, "x_scale"}, {&w, "w"}, {&ws, "w_scale"}, {&out, "out"}, {status, "dev_status"}});
+  return done(moe_linear_fp8(static_cast<const uint8_t*>(x.data_ptr()), ld(x, K), static_cast<const float*>(xs.data_ptr()),
+                             one ? MOE_FP8_PER_TOKEN : MOE_FP8_PER_GROUP, int32_size(M, "x"), int32_size(K, "x"),
+                             static_cast<const uint8_t*>(w.data_ptr()), static_cast<const float*>(ws.data_ptr()),
+                             int32_size(N, "w"), static_cast<int32_t>(act), static_cast<uint16_t*>(out.data_ptr()), word, stream),
+              "moe_linear_fp8");
+}
+
+// tokens [N, heads, dim] whose values lie side by side, with a stride between tokens
+void tokens(const at::Tensor* t, int64_t n, int64_t heads, int64_t dim, const char* what) {
+  if (t && !(is(*t, kBf16, {n, heads, dim}) && (t->stride(2) == 1 || dim == 1) && (heads == 1 || t->stride(1) == dim)))
+    refuse(what, "bf16 [N, num_heads, head_dim] on the GPU (an output like its input), each token's values contiguous");
+}
+
+// (q, k, positions, inv_freq, axes, adjacent, q_out, k_out, dev_status)
+PyObject* rotary(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q");
+  const at::Tensor* k = maybe(a[1], "k");
+  if (q.dim() != 3 || (k && k->dim() != 3)) refuse("q and k", "[N, num_heads, head_dim]");
+  const int64_t N = q.size(0), H = q.size(1), D = q.size(2), Hk = k ? k->size(1) : 0;
+  tokens(&q, N, H, D, "q");
+  tokens(k, N, Hk, D, "k");
+  const at::Tensor &pos = tensor(a[2], "positions"), &freq = tensor(a[3], "inv_freq");
+  const int64_t A = pos.dim() == 2 ? pos.size(0) : 1;
+  if (pos.dim() < 1 || pos.dim() > 2 || (pos.scalar_type() != at::kInt && pos.scalar_type() != at::kLong) || !pos.is_cuda() ||
+      pos.size(-1) != N || (pos.stride(-1) != 1 && N > 1))
+    refuse("positions", "int32 or int64 [N] or [num_axes, N] on the GPU, an axis' positions side by side");
+  const int64_t half = freq.dim() == 1 ? freq.size(0) : 0;
+  dense(&freq, at::kDouble, {half}, "inv_freq", "contiguous float64 [rotary_dim / 2] on the GPU");
+  const at::Tensor* axes = maybe(a[4], "axes");
+  dense(axes, at::kByte, {half}, "axes", "contiguous uint8 of inv_freq's size on the GPU");
+  if (!axes && A > 1) refuse("axes", "given where positions has several axes");
+  const int adjacent = PyObject_IsTrue(a[5]);
+  if (adjacent < 0) throw Raised();
+  const at::Tensor &qo = tensor(a[6], "q_out"), *ko = maybe(a[7], "k_out"), *status = maybe(a[8], "dev_status");
+  tokens(&qo, N, H, D, "q_out");
+  tokens(ko, N, Hk, D, "k_out");
+  if ((k != nullptr) != (ko != nullptr)) refuse("k_out", "given with k, and only then");
+  int32_t* const word = status_word(status);
+  const moe_stream_t stream =
+      stream_of({{&q, "q"}, {k, "k"}, {&pos, "positions"}, {&freq, "inv_freq"}, {axes, "axes"}, {&qo, "q_out"}, {ko, "k_out"},
+                 {status, "dev_status"}});
+  return done(moe_rotary(static_cast<const uint16_t*>(q.data_ptr()), ld(q, H * D), int32_size(H, "q"),
+                         static_cast<const uint16_t*>(pointer(k)), k ? ld(*k, Hk * D) : 0, int32_size(Hk, "k"), int32_size(D, "q"),
+                         int32_size(2 * half, "inv_freq"), adjacent, pos.data_ptr(), pos.scalar_type() == at::kInt ? 4 : 8,
+                         A > 1 ? pos.stride(0) : N, int32_size(A, "positions"), static_cast<const double*>(freq.data_ptr()),
+                         static_cast<const uint8_t*>(pointer(axes)), int32_size(N, "q"), static_cast<uint16_t*>(qo.data_ptr()),
+                         ld(qo, H * D), static_cast<uint16_t*>(pointer(ko)), ko ? ld(*ko, Hk * D) : 0, word, stream),
+              "moe_rotary");
+}
+
+// (logits, uniform, temperature, top_k, top_p, min_p, tokens)
+PyObject* sample_tokens(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0], "logits");
+  const bool f32 = x.scalar_type() == at::kFloat;
+  if (x.dim() != 2) refuse("logits", "[B, V]");
+  const int64_t B = x.size(0), V = x.size(1);
+  rows(&x, f32 ? at::kFloat : kBf16, B, V, "logits", "bf16 or float32 rows on the GPU, their values side by side");
+  const at::Tensor& u = tensor(a[1], "uniform");
+  dense(&u, at::kFloat, {B}, "uniform", "contiguous float32 [B] on the GPU");
+  const at::Tensor *t = maybe(a[2], "temperature"), *k = maybe(a[3], "top_k"), *p = maybe(a[4], "top_p"), *m = maybe(a[5], "min_p");
+  dense(t, at::kFloat, {B}, "temperature", "contiguous float32 [B] on the GPU");
+  dense(k, at::kInt, {B}, "top_k", "contiguous int32 [B] on the GPU");
+  dense(p, at::kFloat, {B}, "top_p", "contiguous float32 [B] on the GPU");
+  dense(m, at::kFloat, {B}, "min_p", "contiguous float32 [B] on the GPU");
+  const at::Tensor& out = tensor(a[6], "out");
+  dense(&out, at::kInt, {B}, "out", "contiguous int32 [B] on the GPU");
+  const moe_stream_t stream = stream_of({{&x, "logits"}, {&u, "uniform"}, {t, "temperature"}, {k, "top_k"}, {p, "top_p"},
+                                         {m, "min_p"}, {&out, "out"}});
+  return done(moe_sample(x.data_ptr(), f32 ? MOE_LOGITS_F32 : MOE_LOGITS_BF16, ld(x, V), int32_size(B, "logits"),
+                         int32_size(V, "logits"), static_cast<const float*>(u.data_ptr()), static_cast<const float*>(pointer(t)),
+                         static_cast<const int32_t*>(pointer(k)), static_cast<const float*>(pointer(p)),
+                         static_cast<const float*>(pointer(m)), static_cast<int32_t*>(out.data_ptr()), stream),
+              "moe_sample");
+}
+
 #define ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(set_error, 1), ENTRY(stream_id, 0), ENTRY(refuse_device, 3), ENTRY(add_rms_norm, 9), ENTRY(fp4_linear, 7), ENTRY(kv_cache, 7),
-                         ENTRY(kv_append, 6), ENTRY(kv_workspace, 3), ENTRY(kv_attend, 8), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(kv_append, 6), ENTRY(kv_workspace, 3), ENTRY(kv_attend, 8),
+                         ENTRY(quantize_fp8, 4), ENTRY(fp8_linear, 7), ENTRY(rotary, 9), ENTRY(sample_tokens, 7), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "calls of libmoe_nvfp4 on torch tensors", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

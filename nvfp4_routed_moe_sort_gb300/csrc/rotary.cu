@@ -1,0 +1,149 @@
+// Rotary positions of queries and keys, with one or several position axes.
+//
+// Pair i of a head is turned by the angle positions[axes[i], n] * inv_freq[i]:
+//   (a, b) -> (a cos - b sin, a sin + b cos),
+// the pair being values (i, i + rotary_dim / 2) of a head or (2 i, 2 i + 1). The other values of a
+// head stay as they are.
+//
+// The angle. A position times a frequency in 32 bits is off by a tenth of a radian from a million tokens
+// on. Only the angle's fraction of a full turn counts, so the frequency becomes a 64-bit fixed-point
+// fraction of a turn, inv_freq / (2 pi) * 2^64, and the integer product with the position drops whole
+// turns by overflowing: what is left is exact but for the frequency's own rounding (2^-54 of it, as
+// a float64 product would have). Sine and cosine are those of a float32 in [-1, 1) times pi.
+#include "common.cuh"
+#include "host_util.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxAxes = 4;
+constexpr int kMaxHeadDim = 1024;
+
+struct RotaryArgs {
+  const uint16_t* in[2];  // queries, keys
+  uint16_t* out[2];
+  int64_t ld_in[2], ld_out[2];
+  int heads[2];
+  const void* pos;
+  const double* inv_freq;
+  const uint8_t* axes;
+  int32_t* status;
+  int64_t ld_pos, N;
+  int dim, half, num_axes, pos64, adjacent;
+  int copy[2];  // the values that are not turned go to `out` too (it is not `in`)
+};
+
+// a frequency in turns, as a fraction of 2^64; whole turns per position fall away
+__device__ __forceinline__ uint64_t turns_of(double inv_freq) {
+  double f = inv_freq * 0.15915494309189533577;
+  f -= floor(f);
+  return __double2ull_rz(f * 18446744073709551616.0);
+}
+
+// cosine and sine of pair i of token n; a pair of an axis that is none is not turned
+__device__ __forceinline__ float2 phase_of(const RotaryArgs& a, int64_t n, int i) {
+  const int axis = a.axes ? a.axes[i] : 0;
+  if (axis >= a.num_axes) {
+    if (a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+    return make_float2(1.0f, 0.0f);
+  }
+  const int64_t at = axis * a.ld_pos + n;
+  const int64_t pos = a.pos64 ? static_cast<const int64_t*>(a.pos)[at] : static_cast<const int32_t*>(a.pos)[at];
+  const uint64_t turn = static_cast<uint64_t>(pos) * turns_of(a.inv_freq[i]);
+  float s, c;
+  sincospif(__ll2float_rn(static_cast<int64_t>(turn)) * 0x1p-63f, &s, &c);
+  return make_float2(c, s);
+}
+
+__device__ __forceinline__ float value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+__device__ __forceinline__ uint16_t bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+// one block per token: its phases first, then its heads pair by pair
+__global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a) {
+  __shared__ float2 phase[kMaxHeadDim / 2];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t n = blockIdx.x;
+  for (int i = threadIdx.x; i < a.half; i += blockDim.x) phase[i] = phase_of(a, n, i);
+  __syncthreads();
+  for (int t = 0; t < 2; ++t) {
+    const uint16_t* in = a.in[t] + n * a.ld_in[t];
+    uint16_t* out = a.out[t] + n * a.ld_out[t];
+    for (int j = threadIdx.x; j < a.heads[t] * a.half; j += blockDim.x) {
+      const int h = j / a.half, i = j - h * a.half;
+      const int at = h * a.dim + (a.adjacent ? 2 * i : i), to = at + (a.adjacent ? 1 : a.half);
+      const float x = value(in[at]), y = value(in[to]);
+      const float2 p = phase[i];
+      out[at] = bits(x * p.x - y * p.y);
+      out[to] = bits(x * p.y + y * p.x);
+    }
+    const int rest = a.dim - 2 * a.half;
+    if (a.copy[t])
+      for (int j = threadIdx.x; j < a.heads[t] * rest; j += blockDim.x) {
+        const int at = j / rest * a.dim + 2 * a.half + j % rest;
+        out[at] = in[at];
+      }
+  }
+}
+
+// rows of `width` values every `ld` values; whether two of them share memory. Slices of one wider row do not.
+bool rows_overlap(const uint16_t* a, int64_t lda, int64_t wa, const uint16_t* b, int64_t ldb, int64_t wb, int64_t rows) {
+  if (wa == 0 || wb == 0) return false;
+  if (!overlaps(a, (static_cast<size_t>(rows - 1) * lda + wa) * 2, b, (static_cast<size_t>(rows - 1) * ldb + wb) * 2)) return false;
+  if (lda != ldb) return true;
+  int64_t apart = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(b)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(a))) / 2 % lda;
+  if (apart < 0) apart += lda;
+  return apart < wa || apart + wb > lda;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status_t moe_rotary(const uint16_t* q, int64_t ld_q, int32_t num_q_heads, const uint16_t* k, int64_t ld_k,
+                                   int32_t num_k_heads, int32_t head_dim, int32_t rotary_dim, int32_t adjacent,
+                                   const void* positions, int32_t position_bytes, int64_t ld_positions, int32_t num_axes,
+                                   const double* inv_freq, const uint8_t* axes, int32_t N, uint16_t* q_out, int64_t ld_q_out,
+                                   uint16_t* k_out, int64_t ld_k_out, int32_t* dev_status, moe_stream_t stream) {
+  MOE_CHECK(N >= 0 && num_q_heads > 0 && num_k_heads >= 0 && head_dim > 0 && rotary_dim > 0 && rotary_dim % 2 == 0 &&
+                rotary_dim <= head_dim && num_axes >= 1,
+            MOE_ERR_INVALID_ARGUMENT);
+  MOE_CHECK(position_bytes == 4 || position_bytes == 8, MOE_ERR_INVALID_ARGUMENT);
+  MOE_CHECK(head_dim <= kMaxHeadDim && num_axes <= kMaxAxes && num_q_heads <= 1024 && num_k_heads <= 1024, MOE_ERR_UNSUPPORTED_SHAPE);
+  MOE_CHECK(num_axes == 1 || ld_positions >= N, MOE_ERR_INVALID_ARGUMENT);
+  const int64_t wq = static_cast<int64_t>(num_q_heads) * head_dim, wk = static_cast<int64_t>(num_k_heads) * head_dim;
+  MOE_CHECK(ld_q >= wq && ld_q_out >= wq && (num_k_heads == 0 || (ld_k >= wk && ld_k_out >= wk)), MOE_ERR_INVALID_ARGUMENT);
+  if (N == 0) return MOE_OK;
+  MOE_CHECK(q && q_out && positions && inv_freq && (num_k_heads == 0 || (k && k_out)), MOE_ERR_INVALID_ARGUMENT);
+  MOE_CHECK(num_axes == 1 || axes, MOE_ERR_INVALID_ARGUMENT);
+  MOE_CHECK(((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(q_out) |
+              reinterpret_cast<uintptr_t>(k_out)) & 1) == 0 &&
+                reinterpret_cast<uintptr_t>(positions) % position_bytes == 0 && reinterpret_cast<uintptr_t>(inv_freq) % 8 == 0,
+            MOE_ERR_MISALIGNED);
+  const uint16_t* in[2] = {q, k};
+  uint16_t* out[2] = {q_out, k_out};
+  const int64_t ld_in[2] = {ld_q, ld_k}, ld_out[2] = {ld_q_out, ld_k_out}, width[2] = {wq, wk};
+  for (int i = 0; i < 2; ++i) {
+    for (int j = 0; j < 2; ++j) {
+      if (i == j && in[i] == out[i] && (ld_in[i] == ld_out[i] || N == 1)) continue;  // in place
+      MOE_CHECK(!rows_overlap(out[i], ld_out[i], width[i], in[j], ld_in[j], width[j], N), MOE_ERR_OVERLAP);
+    }
+    const size_t bytes = width[i] ? (static_cast<size_t>(N - 1) * ld_out[i] + width[i]) * 2 : 0;
+    const size_t pos_bytes = (static_cast<size_t>(num_axes - 1) * ld_positions + N) * position_bytes;
+    MOE_CHECK(!overlaps(out[i], bytes, positions, pos_bytes) && !overlaps(out[i], bytes, inv_freq, rotary_dim / 2 * sizeof(double)) &&
+                  !overlaps(out[i], bytes, axes, rotary_dim / 2),
+              MOE_ERR_OVERLAP);
+  }
+  MOE_CHECK(!rows_overlap(q_out, ld_q_out, wq, k_out, ld_k_out, wk, N), MOE_ERR_OVERLAP);
+  RotaryArgs a = {};
+  for (int i = 0; i < 2; ++i) {
+    a.in[i] = in[i], a.out[i] = out[i], a.ld_in[i] = ld_in[i], a.ld_out[i] = ld_out[i];
+    a.copy[i] = in[i] != out[i];
+  }
+  a.heads[0] = num_q_heads, a.heads[1] = num_k_heads;
+  a.pos = positions, a.inv_freq = inv_freq, a.axes = axes, a.status = dev_status;
+  a.ld_pos = ld_positions, a.N = N, a.dim = head_dim, a.half = rotary_dim / 2, a.num_axes = num_axes;
+  a.pos64 = position_bytes == 8, a.adjacent = adjacent != 0;
+  return launch_pdl(rotary_kernel, dim3(static_cast<unsigned>(N)), dim3(256), 0, as_stream(stream), a);
+}

@@ -1,7 +1,8 @@
 """The operators around the routed experts in a decoder layer, on torch tensors.
 
-``add_rms_norm`` (moe_add_rmsnorm), ``fp4_linear`` / ``NVFP4Linear`` (moe_linear_fp4) and
-``NVFP4KVCache`` (moe_kv_append, moe_kv_attend). The calls go through the native module
+``add_rms_norm`` (moe_add_rmsnorm), ``quantize_fp8`` (moe_quantize_fp8), ``fp4_linear`` / ``NVFP4Linear``
+(moe_linear_fp4), ``fp8_linear`` / ``FP8Linear`` (moe_linear_fp8), ``rotary`` (moe_rotary), ``NVFP4KVCache``
+(moe_kv_append, moe_kv_attend) and ``sample_tokens`` (moe_sample). The calls go through the native module
 ``_native`` (csrc/binding/native.cpp), which checks types, shapes, strides and device; they run on
 torch's current stream, and only results that the caller did not bring are allocated.
 """
@@ -114,6 +115,97 @@ class NVFP4Linear:
 
     def __call__(self, x, x_scale=None, out=None):
         return fp4_linear(x, self.w, self.w_sf, self.alpha, self.activation, x_scale, out)
+
+
+def quantize_fp8(x: torch.Tensor, rows: int = 1, out: tuple | None = None):
+    """x [M, K] bf16 to E4M3: (y [M, K] float8_e4m3fn, scale f32 [ceil(M / rows), ceil(K / 128)]).
+
+    rows = 1: a scale per row and 128 columns, as ``fp8_linear`` and ``fp4_linear`` take activations; rows = 128: one
+    per 128 x 128 block, as ``fp8_linear`` takes its matrix. x may have a row stride. ``out``: the two
+    results' own tensors.
+    """
+    if out is None:
+        if x.dim() != 2:
+            raise ValueError("x must be [M, K]")
+        if rows not in (1, L.MOE_FP8_GROUP):
+            raise ValueError("rows must be 1 or 128")
+        (M, K), dev = x.shape, x.device
+        out = (torch.empty(M, K, dtype=_E4M3, device=dev),
+               torch.empty(-(-M // rows), -(-K // L.MOE_FP8_GROUP), dtype=_F32, device=dev))
+    y, scale = out
+    (_native or _load()).quantize_fp8(x, rows, y, scale)
+    return y, scale
+
+
+def fp8_linear(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+               activation: str = "identity", out: torch.Tensor | None = None, dev_status: torch.Tensor | None = None):
+    """act(x W^T) of any number of tokens with one E4M3 matrix: w [N, K] float8_e4m3fn, w_scale f32
+    [ceil(N / 128), ceil(K / 128)].
+
+    x [M, K] float8_e4m3fn with x_scale f32 [M, 1] or [M, ceil(K / 128)] (as ``add_rms_norm`` and ``quantize_fp8``
+    give them); it may have a row stride. K is a multiple of 16. Gated activations take w rows [gate; up], N a
+    multiple of 256. Returns [M, N] (gated: [M, N / 2]) bf16. dev_status: an int32 tensor whose first
+    element collects MOE_DEV_* bits.
+    """
+    act = L.ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(L.ACTIVATIONS)}")
+    if out is None:
+        out = torch.empty(x.shape[0], w.shape[0] // 2 if act in _GATED else w.shape[0], dtype=_BF16, device=x.device)
+    (_native or _load()).fp8_linear(x, x_scale, w, w_scale, act, out, dev_status)
+    return out
+
+
+class FP8Linear:
+    """One dense E4M3 matrix with a scale per 128 x 128 block: a projection of a prompt's or a batch's tokens."""
+
+    def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, activation: str = "identity"):
+        self.w, self.w_scale, self.activation = w, w_scale, activation
+
+    @classmethod
+    def from_bf16(cls, w: torch.Tensor, activation: str = "identity") -> "FP8Linear":
+        """Encodes w [N, K] bf16 with moe_quantize_fp8."""
+        return cls(*quantize_fp8(w, rows=L.MOE_FP8_GROUP), activation)
+
+    def __call__(self, x, x_scale, out=None):
+        return fp8_linear(x, x_scale, self.w, self.w_scale, self.activation, out)
+
+
+def rotary(q: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, k: torch.Tensor | None = None,
+           axes: torch.Tensor | None = None, adjacent: bool = False, out: tuple | None = None,
+           dev_status: torch.Tensor | None = None):
+    """Queries q [N, num_q_heads, head_dim] bf16 and keys k [N, num_k_heads, head_dim] (or None) turned by their
+    tokens' positions: (q_out, k_out).
+
+    positions [N], or [num_axes, N] with up to four axes (time, height and width, say), int32 or int64;
+    inv_freq float64 [rotary_dim / 2], radians per position; axes uint8 [rotary_dim / 2], the axis of each pair (needed
+    with several axes). Pairs are values (i, i + rotary_dim / 2) of a head, or (2 i, 2 i + 1) with ``adjacent``;
+    values past rotary_dim stay. q and k may have a token stride (slices of one projection's output will
+    do). ``out``: the results' own tensors, with a token stride if need be; (q, k) turns them in place.
+    dev_status: an int32 tensor whose first element collects MOE_DEV_* bits.
+    """
+    if out is None:
+        out = torch.empty(q.shape, dtype=_BF16, device=q.device), None if k is None else torch.empty(k.shape, dtype=_BF16, device=k.device)
+    q_out, k_out = out
+    (_native or _load()).rotary(q, k, positions, inv_freq, axes, adjacent, q_out, k_out, dev_status)
+    return q_out, k_out
+
+
+def sample_tokens(logits: torch.Tensor, uniform: torch.Tensor, temperature: torch.Tensor | None = None,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """One token per row of logits [B, V] (bf16 or float32; a row stride is fine): int32 [B].
+
+    uniform f32 [B] in [0, 1): the rows' random numbers. temperature, top_p, min_p f32 [B] and top_k int32 [B], each
+    None or one setting per row: temperature 0 takes the largest logit; top_k <= 0, top_p >= 1 and min_p <= 0 keep all.
+    The filters act in this order on the tokens sorted by logit (ties: the lower index first); the token is, among the
+    kept ones in the order of their index, the first at which the cumulated weight passes uniform times their sum. A row
+    of which every logit is -inf or NaN gives -1.
+    """
+    if out is None:
+        out = torch.empty(logits.shape[0], dtype=torch.int32, device=logits.device)
+    (_native or _load()).sample_tokens(logits, uniform, temperature, top_k, top_p, min_p, out)
+    return out
 
 
 class NVFP4KVCache:
