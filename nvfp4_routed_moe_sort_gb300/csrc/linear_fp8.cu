@@ -3,6 +3,8 @@
 //   y[m, n] = act(sum_b xs[m, b] * ws[n / 128, b] * sum_{k in block b} x[m, k] * w[n, k])
 #include <math.h>
 
+#include <atomic>
+
 #include "cluster.cuh"
 #include "common.cuh"
 #include "host_util.h"
@@ -30,6 +32,24 @@ __device__ __forceinline__ float activate(int act, float g, float u) {
     case MOE_ACT_SILU: return silu(g);
     default: return g;
   }
+}
+
+// mbar_wait that looks at the clock and the flag once in a while only: they cost more than the wait
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status, uint64_t limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, status, limit_ns);
+}
+
+// whether the phase is over, without waiting: the answer's latency is covered by what is done before it is used
+__device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok;
 }
 
 // wait of a block that ends: short, and it gives up without a word
@@ -66,7 +86,7 @@ struct Fp8Args {
   int M, N, K, groups, act;
   int xs_step, xs_ld;  // per 128 columns and per row: 1 and groups, or 0 and 1
   int cols;            // of out: N, or N / 2
-  int slices, m_tiles, x_rows;
+  int slices, m_tiles, x_rows, wide;
 };
 
 constexpr int kRows = 128, kCols = 128;   // of a block's tile
@@ -124,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
       const uint32_t bytes = a.x_rows * 128 + kOperand;
       int stage = 0, phase = 0, issued = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
+        if (!wait_for(&empty[stage], phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
         uint8_t* const st = smem + stage * 2 * kOperand;
         mbar_arrive_expect_tx(&full[stage], bytes);
         tma_load_2d(st, &a.tmap_x, kb * 128, m0, &full[stage]);
@@ -140,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
     if (lane == 0) {
       int stage = 0, phase = 0, buf = 0, buf_phase = 0, last = -1, last_phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&taken[buf], buf_phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
-        if (!mbar_wait(&full[stage], phase, abort_flag, a.status, a.wait_ns)) break;
+        if (!wait_for(&taken[buf], buf_phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
+        if (!wait_for(&full[stage], phase, abort_flag, a.status, a.wait_ns)) break;
         tc_fence_after();
         const uint32_t st = smem_u32(smem + stage * 2 * kOperand);
 #pragma unroll
@@ -172,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
     for (int kb = kb0; kb < kb1; ++kb) {
       const float x = some ? __ldg(xs + static_cast<int64_t>(kb) * a.xs_step) : 0.0f;
       const float s0 = x * __ldg(ws + kb), s1 = GATED ? x * __ldg(ws_up + kb) : s0;
-      ok = __all_sync(0xffffffffu, mbar_wait(&done[buf], buf_phase, abort_flag, a.status, a.wait_ns));
+      ok = __all_sync(0xffffffffu, wait_for(&done[buf], buf_phase, abort_flag, a.status, a.wait_ns));
       if (!ok) break;
       if (some) {
         uint32_t t[64];
@@ -241,6 +261,343 @@ moe_status_t launch_tiles(Fp8Args a, const void* x, int64_t ld_x, const void* w,
   return launch_clusters(kern, a.slices, dim3(static_cast<unsigned>(tiles * a.slices)), dim3(kThreads), kTileSmem, s, a);
 }
 
+// ---------------------------------------------------------------------------------------------------
+// Large products: a pair of blocks (two SMs) to a tile of 256 x 256, the pairs staying for tile after tile.
+// ---------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on both blocks' `bar` once every MMA issued so far by this thread has completed
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// a load into this block's shared memory that completes on a barrier of the pair's first block
+__device__ __forceinline__ void tma_load_pair(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(smem_u32(smem_dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// one lane of a whole warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
+  return yes != 0;
+}
+
+constexpr int kPairStages = 6;
+constexpr int kPairCols = 256;         // of a tile, and of one accumulator
+constexpr int kPairThreads = 512;      // warps: three of copies, four of MMAs, scales, eight of sums
+constexpr int kPairRegs = 208, kPairRegsOther = 48, kPairRegsAtLaunch = 128;
+static_assert(256 * kPairRegs + 256 * kPairRegsOther <= kPairThreads * kPairRegsAtLaunch, "the raise draws on the launch's registers");
+constexpr int kTurnLd = 18;            // of 32 rows of 16 values that a warp turns in shared memory
+constexpr int kScaleRun = 8;           // blocks of K whose scales are fetched together: a sector of x_scale
+constexpr int kPairSmem = 1024 + kPairStages * 2 * kOperand + 8 * 32 * kTurnLd * 2 + 2 * kScaleRun * (128 + 2) * 4 + 256;
+constexpr int kPairGroup = 8;          // row tiles that follow one another before the next column tile
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const __grid_constant__ Fp8Args a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint16_t* const turn = reinterpret_cast<uint16_t*>(smem + kPairStages * 2 * kOperand);
+  float* const x_ring = reinterpret_cast<float*>(turn + 8 * 32 * kTurnLd);  // [2][kScaleRun][128 rows]
+  float* const w_ring = x_ring + 2 * kScaleRun * 128;                        // [2][kScaleRun][halves, or gate and up]
+  uint64_t* const full = reinterpret_cast<uint64_t*>(w_ring + 2 * kScaleRun * 2);
+  uint64_t* const done = full + kPairStages;   // a stage's products are summed, one for each half of its columns
+  uint64_t* const taken = done + 2 * kPairStages;  // ... and read
+  uint64_t* const scales = taken + 4;              // a run of scales is there
+  uint64_t* const scales_free = scales + 2;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(scales_free + 2);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;  // in the pair: rows 0-127 and columns 0-127 of w, or the others
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  constexpr int kOut = GATED ? kPairCols / 2 : kPairCols;
+  const int n_tiles = (a.cols - 1) / kOut + 1, tiles = a.m_tiles * n_tiles;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) mbar_init(&full[i], 1), mbar_init(&done[2 * i], 1), mbar_init(&done[2 * i + 1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&taken[i], 8);
+    for (int i = 0; i < 2; ++i) mbar_init(&scales[i], 1), mbar_init(&scales_free[i], 8);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&a.tmap_x);
+    prefetch_tensormap(&a.tmap_w);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // both blocks' barriers and TMEM are there
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  // tile t: groups of kPairGroup row tiles, column by column
+  const auto place = [&](int t, int& m0, int& n0) {
+    const int group = t / (kPairGroup * n_tiles), first = group * kPairGroup, in = t - group * kPairGroup * n_tiles;
+    const int high = min(kPairGroup, a.m_tiles - first);
+    m0 = (first + in % high) * 256;
+    n0 = in / high * kOut;
+  };
+
+  if (warp < 8) {
+    setmaxnreg_dec<kPairRegsOther>();
+    if (warp == 0 || warp > 5) {
+      if (lane == 0) {
+        // Three warps take the blocks of K by turns: the wait for a stage and its three copies cost a thread more time
+        // than the MMAs leave it.
+        const int all = (tiles - pair + pairs - 1) / pairs * a.groups;  // blocks of K of this pair's tiles
+        int t = pair, kb = warp == 0 ? 0 : warp - 5, last = -1;
+        bool ok = true;
+        for (int i = kb; i < all; i += 3) {
+          while (kb >= a.groups) kb -= a.groups, t += pairs;
+          const int stage = i % kPairStages, phase = i / kPairStages & 1;
+          int m0, n0;
+          place(t, m0, n0);
+          const int y_x = m0 + rank * 128, y_w = n0 + rank * (GATED ? a.cols : 64);
+          uint8_t* const st = smem + stage * 2 * kOperand;
+          const uint32_t bar = cluster_address(&full[stage], 0);
+          ok = wait_for(&done[2 * stage], phase ^ 1, abort_flag, a.status, a.wait_ns) &&
+               wait_for(&done[2 * stage + 1], phase ^ 1, abort_flag, a.status, a.wait_ns);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kOperand);  // both blocks' loads
+          tma_load_pair(st, &a.tmap_x, kb * 128, y_x, bar);
+          tma_load_pair(st + kOperand, &a.tmap_w, kb * 128, y_w, bar);
+          tma_load_pair(st + kOperand + kOperand / 2, &a.tmap_w, kb * 128, y_w + (GATED ? 64 : 128), bar);
+          last = i;
+          kb += 3;
+        }
+        // loads land before the pair ends, even if nothing waited for them
+        if (rank == 0) {
+          for (int i = max(last - 3, 0); i <= last; i += 3) mbar_drain(&full[i % kPairStages], i / kPairStages & 1);
+        } else if (!ok) {
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 1000000ull) {
+          }
+        }
+      }
+    } else if (warp <= 4) {
+      if (rank == 0) {
+        // One warp for each of the four accumulators, so that their waits and commits, which take longer than the MMAs
+        // take the tensor core, go on side by side.
+        const int buf = (warp - 1) & 1, half = (warp - 1) >> 1;
+        const int all = (tiles - pair + pairs - 1) / pairs * a.groups;  // blocks of K of this pair's tiles
+        const uint32_t to = tmem + buf * kPairCols + half * 128;
+        const uint64_t x_desc = sdesc_kmajor_sw128(smem_u32(smem));
+        const uint64_t w_desc = sdesc_kmajor_sw128(smem_u32(smem) + kOperand + half * (kOperand / 2));
+        uint64_t* last = nullptr;
+        int last_phase = 0, stage = buf, phase = 0;
+        for (int i = buf; i < all; i += 2) {
+          // the loads are ahead of the sums: their wait comes first, off the way from sums read to MMAs issued
+          const bool ok = wait_for(&full[stage], phase, abort_flag, a.status, a.wait_ns) &&
+                          wait_for(&taken[2 * buf + half], ((i >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          last = &done[2 * stage + half], last_phase = phase;
+          if (elect_one()) {
+            const uint64_t at = static_cast<uint64_t>(stage * (2 * kOperand >> 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_e4m3_pair(to, x_desc + at + 2 * k, w_desc + at + 2 * k, idesc_e4m3(256, 128), k != 0);
+            tc_commit_pair(last);
+          }
+          __syncwarp();
+          stage += 2;
+          if (stage >= kPairStages) stage -= kPairStages, phase ^= 1;
+        }
+        if (last) mbar_drain(last, last_phase);
+      }
+    } else if (warp == 5) {
+      // The scales of kScaleRun blocks of K at a time, turned so that the threads of a row's sums read them side by
+      // side (read from global memory by those threads, one value a block of K, they cost half of the kernel's time).
+      int run = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        int m0, n0;
+        place(t, m0, n0);
+        const int blocks = (a.N - 1) / kGroup;  // a tile's second half may lie behind the matrix: its sums are not stored
+        const float* const ws = a.ws + static_cast<int64_t>(n0 / kGroup) * a.groups;
+        const float* const ws2 = a.ws + static_cast<int64_t>(min((GATED ? a.cols + n0 : n0 + 128) / kGroup, blocks)) * a.groups;
+        for (int kb = 0; kb < a.groups; kb += kScaleRun, ++run) {
+          ok = __all_sync(0xffffffffu, wait_for(&scales_free[run & 1], ((run >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns));
+          if (!ok) break;
+          float* const x_to = x_ring + (run & 1) * kScaleRun * 128;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float* const xs = a.xs + static_cast<int64_t>(min(m0 + rank * 128 + 32 * j + lane, a.M - 1)) * a.xs_ld;
+            float v[kScaleRun];
+#pragma unroll
+            for (int i = 0; i < kScaleRun; ++i) v[i] = __ldg(xs + min(kb + i, a.groups - 1) * a.xs_step);
+#pragma unroll
+            for (int i = 0; i < kScaleRun; ++i) x_to[i * 128 + 32 * j + lane] = v[i];
+          }
+          if (lane < 2 * kScaleRun)
+            w_ring[(run & 1) * 2 * kScaleRun + lane] = __ldg((lane & 1 ? ws2 : ws) + min(kb + (lane >> 1), a.groups - 1));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scales[run & 1]);
+        }
+      }
+    }
+  } else {
+    setmaxnreg_inc<kPairRegs>();
+    // a warp has 32 rows and a half's 128 columns; gated: 64 of gate and the same 64 of up
+    const int quarter = warp & 3, half = (warp - 8) >> 2;
+    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+    const uint32_t free_bar = cluster_address(&taken[half], 0);
+    int buf = 0, stage = 0, phase = 0, run = 0;
+    uint32_t here = 0;  // the next sums were seen done
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      for (int kb = 0; kb < a.groups; ++kb) {
+        if (kb % kScaleRun == 0)
+          ok = __all_sync(0xffffffffu, wait_for(&scales[run & 1], (run >> 1) & 1, abort_flag, a.status, a.wait_ns));
+        const int in = (run & 1) * kScaleRun + kb % kScaleRun;
+        const float x = x_ring[in * 128 + quarter * 32 + lane];
+        const float s0 = x * w_ring[2 * in + (GATED ? 0 : half)], s1 = GATED ? x * w_ring[2 * in + 1] : s0;
+        if (!__all_sync(0xffffffffu, here))
+          ok = ok && __all_sync(0xffffffffu, wait_for(&done[2 * stage + half], phase, abort_flag, a.status, a.wait_ns));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t from = at + buf * kPairCols;
+        uint32_t v[2][32];
+        tmem_ld32_issue(from, v[0]);
+        if (kb % kScaleRun == kScaleRun - 1 || kb == a.groups - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scales_free[run & 1]);
+          ++run;
+        }
+        tmem_wait_ld<32>(v[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < 3) tmem_ld32_issue(from + (c + 1) * 32, v[(c + 1) & 1]);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(v[c & 1][i]), c < 2 ? s0 : s1, acc[32 * c + i]);
+          if (c < 3) tmem_wait_ld<32>(v[(c + 1) & 1]);
+          if (c == 2) {  // all of it is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(free_bar + 2 * buf * 8);
+            if (++stage == kPairStages) stage = 0, phase ^= 1;
+            here = mbar_test(&done[2 * stage + half], phase);
+          }
+        }
+        buf ^= 1;
+      }
+      if (!ok) break;
+      int m0, n0;
+      place(t, m0, n0);
+      const int first = m0 + rank * 128 + quarter * 32;  // the warp's rows
+      constexpr int kMine = GATED ? 64 : 128;            // columns of out
+      const int c0 = n0 + half * kMine;
+      if (GATED || a.act != MOE_ACT_IDENTITY) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) acc[i] = activate(a.act, acc[i], GATED ? acc[64 + (i & 63)] : 0.0f);
+      }
+      if (a.wide) {  // rows of whole 16-byte pieces
+        if (first + lane < a.M) {
+          uint16_t* const to = a.out + static_cast<int64_t>(first + lane) * a.cols + c0;
+#pragma unroll
+          for (int i = 0; i < kMine / 8; ++i)
+            if (c0 + 8 * i < a.cols)
+              *reinterpret_cast<uint4*>(to + 8 * i) =
+                  make_uint4(bf16x2(acc[8 * i], acc[8 * i + 1]), bf16x2(acc[8 * i + 2], acc[8 * i + 3]),
+                             bf16x2(acc[8 * i + 4], acc[8 * i + 5]), bf16x2(acc[8 * i + 6], acc[8 * i + 7]));
+        }
+      } else {  // 32 x 16 values change hands in shared memory, and the warp writes row by row
+        uint16_t* const mine = turn + (warp - 8) * 32 * kTurnLd;
+#pragma unroll
+        for (int c = 0; c < kMine / 16; ++c) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(mine + lane * kTurnLd + 2 * i) = bf16x2(acc[16 * c + 2 * i], acc[16 * c + 2 * i + 1]);
+          __syncwarp();
+          const int col = c0 + 16 * c + (lane & 15);
+          if (col < a.cols) {
+            uint16_t* const to = a.out + static_cast<int64_t>(first) * a.cols + col;
+            for (int r = lane >> 4; r < min(32, a.M - first); r += 2) to[static_cast<int64_t>(r) * a.cols] = mine[r * kTurnLd + (lane & 15)];
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // neither block goes while the other may still reach into it
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// How many pairs run at once on the current device: looked up once for each.
+template <bool GATED>
+moe_status_t resident_pairs(int& pairs) {
+  const auto kern = linear_fp8_pair_kernel<GATED>;
+  static std::atomic<int> known[64];
+  int dev = 0;
+  MOE_CUDA(cudaGetDevice(&dev));
+  const int i = dev & 63;
+  pairs = known[i].load(std::memory_order_relaxed);
+  if (pairs > 0) return MOE_OK;
+  cudaFuncAttributes fa;
+  MOE_CUDA(cudaFuncGetAttributes(&fa, kern));
+  if (fa.numRegs < kPairRegsAtLaunch) return MOE_ERR_CUDA;  // the raise of the registers would wait forever
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * num_sms());
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MOE_CUDA(cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg));
+  if (pairs < 1) return MOE_ERR_CUDA;
+  known[i].store(pairs, std::memory_order_relaxed);
+  return MOE_OK;
+}
+
+template <bool GATED>
+moe_status_t launch_pairs(Fp8Args a, const void* x, int64_t ld_x, const void* w, cudaStream_t s) {
+  constexpr int kOut = GATED ? kPairCols / 2 : kPairCols;
+  a.m_tiles = (a.M - 1) / 256 + 1;
+  const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.cols - 1) / kOut + 1);
+  MOE_CHECK(tiles <= INT32_MAX / 2, MOE_ERR_UNSUPPORTED_SHAPE);
+  a.wide = a.cols % 8 == 0;
+  if (!encode_rows(&a.tmap_x, x, a.K, a.M, ld_x, 128) || !encode_rows(&a.tmap_w, w, a.K, a.N, a.K, 64)) return MOE_ERR_CUDA;
+  const auto kern = linear_fp8_pair_kernel<GATED>;
+  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
+  int pairs = 0;
+  const moe_status_t known = resident_pairs<GATED>(pairs);
+  if (known != MOE_OK) return known;
+  const unsigned grid = static_cast<unsigned>(tiles < pairs ? tiles : pairs);
+  return launch_clusters(kern, 2, dim3(2 * grid), dim3(kPairThreads), kPairSmem, s, a);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -272,5 +629,7 @@ extern "C" moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const flo
   a.xs = x_scale, a.ws = w_scale, a.out = out, a.status = dev_status, a.wait_ns = kWaitLimitNs;
   a.M = M, a.N = N, a.K = K, a.groups = groups, a.act = activation, a.cols = cols;
   a.xs_step = per_token ? 0 : 1, a.xs_ld = per_token ? 1 : groups;
+  if (M >= 1024 && N >= 1024)
+    return gated ? launch_pairs<true>(a, x, ld_x, w, as_stream(stream)) : launch_pairs<false>(a, x, ld_x, w, as_stream(stream));
   return gated ? launch_tiles<true>(a, x, ld_x, w, as_stream(stream)) : launch_tiles<false>(a, x, ld_x, w, as_stream(stream));
 }
