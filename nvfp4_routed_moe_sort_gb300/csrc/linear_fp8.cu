@@ -14,7 +14,8 @@ namespace moe {
 namespace {
 
 constexpr int kGroup = MOE_FP8_GROUP;
-__device__ __forceinline__ float silu(float g) { return __fdiv_rn(g, __fadd_rn(1.0f, expf(-g))); }
+// within 2^-20 of itself, far below the rounding to BF16 that follows
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 __device__ __forceinline__ float gelu(float x) {
   return __fmul_rn(__fmul_rn(0.5f, x), __fadd_rn(1.0f, erff(__fmul_rn(x, 0.70710678118654752f))));
 }
@@ -76,6 +77,8 @@ __device__ __forceinline__ void store_cluster4(uint32_t at, float a, float b, fl
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
+__host__ __device__ constexpr bool is_gated(int act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
+
 struct Fp8Args {
   CUtensorMap tmap_x, tmap_w;
   const float* xs;
@@ -86,47 +89,128 @@ struct Fp8Args {
   int M, N, K, groups, act;
   int xs_step, xs_ld;  // per 128 columns and per row: 1 and groups, or 0 and 1
   int cols;            // of out: N, or N / 2
-  int slices, m_tiles, x_rows, wide;
+  int slices, m_tiles, x_rows, wide, stages, stage_bytes;
 };
 
+// a += t * s for two values at once
+__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t t0, uint32_t t1, float s) {
+  asm("{\n .reg .b64 a, t, f;\n mov.b64 a, {%0, %1};\n mov.b64 t, {%2, %3};\n mov.b64 f, {%4, %4};\n"
+      " fma.rn.f32x2 a, t, f, a;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "r"(t0), "r"(t1), "f"(s));
+}
+
+// one lane of a whole warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
+  return yes != 0;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 constexpr int kRows = 128, kCols = 128;   // of a block's tile
-constexpr int kStages = 4, kBufs = 4;
-constexpr int kOperand = 128 * 128;       // bytes of a stage's x, and of its w
+constexpr int kMaxStages = 8, kBufs = 4;
+constexpr int kOperand = 128 * 128;       // bytes of a stage's w (and of its x, where rows are 128)
 constexpr int kMaxSlices = 8;
 constexpr int kSumLd = kCols + 4;         // of a row of sums in shared memory: no bank conflicts
-constexpr int kSumRows = kRows + kMaxSlices;
-constexpr int kThreads = 320;             // warps: copies, MMA, eight of sums
-constexpr int kTileSmem = 1024 + kStages * 2 * kOperand + kSumRows * kSumLd * 4 + 256;
+constexpr int kThreads = 384;             // warps: copies, two of MMAs, scales, eight of sums
+constexpr int kTurnLd = 18;               // of 32 rows of 16 values that a warp turns in shared memory
+constexpr int kScaleRun = 8;              // blocks of K whose scales are fetched together: a sector of x_scale
+constexpr int kScaleBytes = 2 * kScaleRun * (128 + 2) * 4;
+constexpr int kBarBytes = 256;
+
+// The scales of kScaleRun blocks of K at a time, turned so that the threads of a row's sums read them side by
+// side (read from global memory by those threads, one value a block of K, they cost half of the kernel's time):
+// x_ring [2][kScaleRun][128 rows], w_ring [2][kScaleRun][2]. One whole warp; `rows` of the tile's rows from m0 on.
+__device__ __forceinline__ void fetch_scales(const Fp8Args& a, int run, int kb, int64_t m0, int rows, const float* ws, const float* ws2,
+                                             float* x_ring, float* w_ring, int lane) {
+  float* const x_to = x_ring + (run & 1) * kScaleRun * 128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (32 * j >= rows) break;
+    const float* const xs = a.xs + (m0 + min(32 * j + lane, rows - 1)) * a.xs_ld;
+    float v[kScaleRun];
+#pragma unroll
+    for (int i = 0; i < kScaleRun; ++i) v[i] = __ldg(xs + min(kb + i, a.groups - 1) * a.xs_step);
+#pragma unroll
+    for (int i = 0; i < kScaleRun; ++i) x_to[i * 128 + 32 * j + lane] = v[i];
+  }
+  if (lane < 2 * kScaleRun)
+    w_ring[(run & 1) * 2 * kScaleRun + lane] = __ldg((lane & 1 ? ws2 : ws) + min(kb + (lane >> 1), a.groups - 1));
+}
+
+// N values of a row (N / 32 warps' worth of columns from c0 on) to out: whole 16-byte pieces where rows are made of
+// them, else 32 x 16 values at a time change hands in shared memory and the warp writes row by row.
+template <int N>
+__device__ __forceinline__ void store_rows(const Fp8Args& a, const float* v, int64_t first, int c0, uint16_t* turn, int lane) {
+  if (a.wide) {
+    if (first + lane < a.M) {
+      uint16_t* const to = a.out + (first + lane) * a.cols + c0;
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i)
+        if (c0 + 8 * i < a.cols)
+          *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(bf16x2(v[8 * i], v[8 * i + 1]), bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                                             bf16x2(v[8 * i + 4], v[8 * i + 5]), bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(turn + lane * kTurnLd + 2 * i) = bf16x2(v[16 * c + 2 * i], v[16 * c + 2 * i + 1]);
+      __syncwarp();
+      const int col = c0 + 16 * c + (lane & 15);
+      if (col < a.cols) {
+        uint16_t* const to = a.out + first * a.cols + col;
+        for (int r = lane >> 4; r < min(int64_t(32), a.M - first); r += 2) to[static_cast<int64_t>(r) * a.cols] = turn[r * kTurnLd + (lane & 15)];
+      }
+      __syncwarp();
+    }
+  }
+}
 
 // One 128 x 128 tile of the product, or one slice of its K. The blocks of a cluster are a tile's slices.
-template <bool GATED>
+template <int ACT>
 __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_constant__ Fp8Args a) {
+  constexpr bool GATED = is_gated(ACT);
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  float* const sums = reinterpret_cast<float*>(smem + kStages * 2 * kOperand);
-  uint64_t* const full = reinterpret_cast<uint64_t*>(sums + kSumRows * kSumLd);
-  uint64_t* const empty = full + kStages;
-  uint64_t* const done = empty + kStages;   // a buffer's block of K is summed
-  uint64_t* const taken = done + kBufs;     // ... and read
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(taken + kBufs);
+  float* const x_ring = reinterpret_cast<float*>(smem + a.stages * a.stage_bytes);
+  float* const w_ring = x_ring + 2 * kScaleRun * 128;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(w_ring + 2 * kScaleRun * 2);
+  uint64_t* const done = full + kMaxStages;    // a stage's products are summed
+  uint64_t* const taken = done + kMaxStages;   // ... and read
+  uint64_t* const scales = taken + kBufs;      // a run of scales is there
+  uint64_t* const scales_free = scales + 2;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(scales_free + 2);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* const sums = reinterpret_cast<float*>(smem + a.stages * a.stage_bytes + kScaleBytes + kBarBytes);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int slice = blockIdx.x % a.slices, tile = blockIdx.x / a.slices;
   const int m0 = tile % a.m_tiles * kRows;
   constexpr int kOut = GATED ? kCols / 2 : kCols;  // columns of out
   const int n0 = tile / a.m_tiles * kOut;
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.groups) * slice / a.slices);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(a.groups) * (slice + 1) / a.slices);
+  const int n = static_cast<int>(static_cast<int64_t>(a.groups) * (slice + 1) / a.slices) - kb0;  // blocks of K
   const int rows = min(kRows, a.M - m0);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < kBufs; ++i) mbar_init(&done[i], 1), mbar_init(&taken[i], 8);
+    for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1), mbar_init(&done[i], 1);
+    for (int i = 0; i < kBufs; ++i) mbar_init(&taken[i], 8);
+    for (int i = 0; i < 2; ++i) mbar_init(&scales[i], 1), mbar_init(&scales_free[i], 8);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&a.tmap_x);
     prefetch_tensormap(&a.tmap_w);
   }
-  if (warp == 1) {
+  __syncwarp();
+  if (warp == 2) {
     tmem_alloc(tmem_slot, kBufs * kCols);
     tmem_relinquish();
   }
@@ -143,122 +227,172 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
     if (lane == 0) {
       const uint32_t bytes = a.x_rows * 128 + kOperand;
       int stage = 0, phase = 0, issued = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_for(&empty[stage], phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
-        uint8_t* const st = smem + stage * 2 * kOperand;
+      for (int i = 0; i < n; ++i) {
+        if (!wait_for(&done[stage], phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
+        uint8_t* const st = smem + stage * a.stage_bytes;
+        const int k = (kb0 + i) * 128;
         mbar_arrive_expect_tx(&full[stage], bytes);
-        tma_load_2d(st, &a.tmap_x, kb * 128, m0, &full[stage]);
-        tma_load_2d(st + kOperand, &a.tmap_w, kb * 128, n0, &full[stage]);
-        if (GATED) tma_load_2d(st + kOperand + kOperand / 2, &a.tmap_w, kb * 128, a.cols + n0, &full[stage]);
+        tma_load_2d(st, &a.tmap_w, k, n0, &full[stage]);
+        if (GATED) tma_load_2d(st + kOperand / 2, &a.tmap_w, k, a.cols + n0, &full[stage]);
+        tma_load_2d(st + kOperand, &a.tmap_x, k, m0, &full[stage]);
         ++issued;
-        if (++stage == kStages) stage = 0, phase ^= 1;
+        if (++stage == a.stages) stage = 0, phase ^= 1;
       }
       // what was issued lands before the block ends, even if nothing waited for it
-      for (int i = max(0, issued - kStages); i < issued; ++i) mbar_drain(&full[i % kStages], i / kStages & 1);
+      for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_drain(&full[i % a.stages], i / a.stages & 1);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, phase = 0, buf = 0, buf_phase = 0, last = -1, last_phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_for(&taken[buf], buf_phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
-        if (!wait_for(&full[stage], phase, abort_flag, a.status, a.wait_ns)) break;
-        tc_fence_after();
-        const uint32_t st = smem_u32(smem + stage * 2 * kOperand);
+  } else if (warp < 3) {
+    // two warps take the blocks of K by turns: what one costs them in waits is more than it costs the tensor core
+    const uint64_t w_desc = sdesc_kmajor_sw128(smem_u32(smem)), x_desc = sdesc_kmajor_sw128(smem_u32(smem) + kOperand);
+    uint64_t* last = nullptr;
+    int last_phase = 0, stage = warp - 1, phase = 0;
+    for (int i = warp - 1; i < n; i += 2) {
+      const int buf = i % kBufs;
+      const bool ok = wait_for(&full[stage], phase, abort_flag, a.status, a.wait_ns) &&
+                      wait_for(&taken[buf], (i / kBufs & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      last = &done[stage], last_phase = phase;
+      if (elect_one()) {
+        const uint64_t at = static_cast<uint64_t>(stage * (a.stage_bytes >> 4));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_e4m3(tmem + buf * kCols, sdesc_kmajor_sw128(st + 32 * k), sdesc_kmajor_sw128(st + kOperand + 32 * k),
-                   idesc_e4m3(kRows, kCols), k != 0);
-        tc_commit(&empty[stage]);
-        tc_commit(&done[buf]);
-        last = buf, last_phase = buf_phase;
-        if (++stage == kStages) stage = 0, phase ^= 1;
-        if (++buf == kBufs) buf = 0, buf_phase ^= 1;
+          mma_e4m3(tmem + buf * kCols, x_desc + at + 2 * k, w_desc + at + 2 * k, idesc_e4m3(kRows, kCols), k != 0);
+        tc_commit(last);
       }
-      if (last >= 0) mbar_drain(&done[last], last_phase);  // no MMA runs when TMEM is released
+      __syncwarp();
+      stage += 2;
+      if (stage >= a.stages) stage -= a.stages, phase ^= 1;
+    }
+    if (last) mbar_drain(last, last_phase);  // no MMA runs when TMEM is released
+  } else if (warp == 3) {
+    const float* const ws = a.ws + static_cast<int64_t>(n0 / kGroup) * a.groups;
+    const float* const ws2 = GATED ? a.ws + static_cast<int64_t>((a.cols + n0) / kGroup) * a.groups : ws;
+    for (int i = 0, run = 0; i < n; i += kScaleRun, ++run) {
+      if (!__all_sync(0xffffffffu, wait_for(&scales_free[run & 1], ((run >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns))) break;
+      fetch_scales(a, run, kb0 + i, m0, rows, ws, ws2, x_ring, w_ring, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&scales[run & 1]);
     }
   } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;  // of the tile's rows and columns
+    const int quarter = warp & 3, half = (warp - 4) >> 2;  // of the tile's rows and columns
     const int r = quarter * 32 + lane;
     const bool some = quarter * 32 < rows;                 // of the warp's rows there are any
     const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * (GATED ? 32 : 64);
-    const float* const xs = a.xs + static_cast<int64_t>(m0 + min(r, rows - 1)) * a.xs_ld;
-    const float* const ws = a.ws + static_cast<int64_t>(n0 / kGroup) * a.groups;
-    const float* const ws_up = GATED ? a.ws + static_cast<int64_t>((a.cols + n0) / kGroup) * a.groups : ws;
     float acc[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-    int buf = 0, buf_phase = 0;
-    bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const float x = some ? __ldg(xs + static_cast<int64_t>(kb) * a.xs_step) : 0.0f;
-      const float s0 = x * __ldg(ws + kb), s1 = GATED ? x * __ldg(ws_up + kb) : s0;
-      ok = __all_sync(0xffffffffu, wait_for(&done[buf], buf_phase, abort_flag, a.status, a.wait_ns));
-      if (!ok) break;
+    int stage = 0, phase = 0, run = 0;
+    for (int i = 0; i < n; ++i) {
+      bool ok = true;
+      if (i % kScaleRun == 0) ok = wait_for(&scales[run & 1], (run >> 1) & 1, abort_flag, a.status, a.wait_ns);
+      const int in = (run & 1) * kScaleRun + i % kScaleRun, buf = i % kBufs;
+      const float x = x_ring[in * 128 + r];
+      const float s0 = x * w_ring[2 * in], s1 = GATED ? x * w_ring[2 * in + 1] : s0;
+      ok = ok && wait_for(&done[stage], phase, abort_flag, a.status, a.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      uint32_t t[64];
       if (some) {
-        uint32_t t[64];
         tc_fence_after();
         tmem_ld32_issue(at + buf * kCols, t);
         tmem_ld32_issue(at + buf * kCols + (GATED ? 64 : 32), t + 32);
         tmem_wait_ld<64>(t);
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&taken[buf]);
-#pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = fmaf(__uint_as_float(t[i]), i < 32 ? s0 : s1, acc[i]);
-      } else if (lane == 0) {
-        mbar_arrive(&taken[buf]);
       }
-      if (++buf == kBufs) buf = 0, buf_phase ^= 1;
-    }
-    if (a.slices > 1) cluster_wait();  // every block of the cluster runs
-    // The rows of the tile are dealt out to its slices, which add up their rows' sums: row r to block r / per.
-    const int per = (rows + a.slices - 1) / a.slices;
-    if (r < rows) {
-      float* const to = sums + (slice * per + r % per) * kSumLd + half * (GATED ? 32 : 64);
-      const uint32_t there = a.slices > 1 ? cluster_address(to, r / per) : smem_u32(to);
+      __syncwarp();
+      if (lane == 0) {
+        arrive_relaxed(&taken[buf]);
+        if (i % kScaleRun == kScaleRun - 1) mbar_arrive(&scales_free[run & 1]);
+      }
+      if (some) {
 #pragma unroll
-      for (int i = 0; i < 64; i += 4)
-        store_cluster4(there + (GATED && i >= 32 ? i + 32 : i) * 4, acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        for (int c = 0; c < 64; c += 2) fma2(acc[c], acc[c + 1], t[c], t[c + 1], c < 32 ? s0 : s1);
+      }
+      if (i % kScaleRun == kScaleRun - 1) ++run;
+      if (++stage == a.stages) stage = 0, phase ^= 1;
+    }
+    if (a.slices == 1) {
+      if constexpr (ACT != MOE_ACT_IDENTITY) {
+#pragma unroll
+        for (int i = 0; i < (GATED ? 32 : 64); ++i) acc[i] = activate(ACT, acc[i], GATED ? acc[32 + (i & 31)] : 0.0f);
+      }
+      store_rows<GATED ? 32 : 64>(a, acc, m0 + quarter * 32, n0 + half * (GATED ? 32 : 64),
+                                  reinterpret_cast<uint16_t*>(sums) + (warp - 4) * 32 * kTurnLd, lane);
+    } else {
+      cluster_wait();  // every block of the cluster runs
+      // The rows of the tile are dealt out to its slices, which add up their rows' sums: row r to block r / per.
+      const int per = (rows + a.slices - 1) / a.slices;
+      if (r < rows) {
+        const uint32_t there = cluster_address(sums + (slice * per + r % per) * kSumLd + half * (GATED ? 32 : 64), r / per);
+#pragma unroll
+        for (int i = 0; i < 64; i += 4)
+          store_cluster4(there + (GATED && i >= 32 ? i + 32 : i) * 4, acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+      }
     }
   }
   __syncwarp();
   if (a.slices > 1) {
-    if (warp < 2) cluster_wait();
+    if (warp < 4) cluster_wait();
     cluster_arrive();
     cluster_wait();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, kBufs * kCols);
   }
+  if (a.slices == 1) return;
   const int per = (rows + a.slices - 1) / a.slices, first = slice * per, mine = min(per, rows - first);
-  for (int i = threadIdx.x; i < mine * kOut; i += kThreads) {
-    const int r = i / kOut, c = i % kOut;
-    if (n0 + c >= a.cols) continue;
-    float g = 0.0f, u = 0.0f;
+  for (int i = threadIdx.x; i < mine * (kOut / 4); i += kThreads) {  // four columns each
+    const int r = i / (kOut / 4), c = i % (kOut / 4) * 4;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < a.slices; ++s) {
-      g += sums[(s * per + r) * kSumLd + c];
-      if (GATED) u += sums[(s * per + r) * kSumLd + kOut + c];
+      const float* const from = sums + (s * per + r) * kSumLd + c;
+      const float4 p = *reinterpret_cast<const float4*>(from);
+      v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+      if (GATED) {
+        const float4 q = *reinterpret_cast<const float4*>(from + kOut);
+        u[0] += q.x, u[1] += q.y, u[2] += q.z, u[3] += q.w;
+      }
     }
-    a.out[static_cast<int64_t>(m0 + first + r) * a.cols + n0 + c] = __bfloat16_as_ushort(__float2bfloat16_rn(activate(a.act, g, u)));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = activate(ACT, v[e], u[e]);
+    uint16_t* const to = a.out + static_cast<int64_t>(m0 + first + r) * a.cols + n0 + c;
+    if (a.wide) {
+      if (n0 + c < a.cols) *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n0 + c + e < a.cols) to[e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
+    }
   }
 }
 
-template <bool GATED>
+template <int ACT>
 moe_status_t launch_tiles(Fp8Args a, const void* x, int64_t ld_x, const void* w, cudaStream_t s) {
-  constexpr int kOut = GATED ? kCols / 2 : kCols;
+  constexpr int kOut = is_gated(ACT) ? kCols / 2 : kCols;
   a.m_tiles = (a.M - 1) / kRows + 1;
   a.x_rows = a.M < kRows ? (a.M + 7) / 8 * 8 : kRows;
   const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.cols - 1) / kOut + 1);
   a.slices = 1;
   while (a.slices < kMaxSlices && tiles * a.slices * 2 <= num_sms() && a.groups >= 4 * a.slices) a.slices *= 2;
   MOE_CHECK(tiles * a.slices <= INT32_MAX, MOE_ERR_UNSUPPORTED_SHAPE);
+  a.wide = a.cols % 8 == 0;
+  const int held = a.M < kRows ? a.M : kRows;
+  int sums = a.slices > 1 ? (held + a.slices - 1) / a.slices * a.slices * kSumLd * 4 : 8 * 32 * kTurnLd * 2;
+  // The MMA reads 128 rows of x where fewer were loaded (what it makes of the others is not used): they lie in the
+  // following stages, and after the last one in what follows the stages.
+  if (sums < kOperand - kScaleBytes - kBarBytes) sums = kOperand - kScaleBytes - kBarBytes;
+  a.stage_bytes = kOperand + (a.x_rows * 128 + 1023) / 1024 * 1024;
+  const int rest = 1024 + kScaleBytes + kBarBytes + sums;
+  a.stages = (227 * 1024 - rest) / a.stage_bytes / 2 * 2;  // even: two warps take them by turns
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  const int smem = rest + a.stages * a.stage_bytes;
   if (!encode_rows(&a.tmap_x, x, a.K, a.M, ld_x, a.x_rows) || !encode_rows(&a.tmap_w, w, a.K, a.N, a.K, kOut)) return MOE_ERR_CUDA;
-  const auto kern = linear_fp8_kernel<GATED>;
-  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem));
-  return launch_clusters(kern, a.slices, dim3(static_cast<unsigned>(tiles * a.slices)), dim3(kThreads), kTileSmem, s, a);
+  const auto kern = linear_fp8_kernel<ACT>;
+  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+  return launch_clusters(kern, a.slices, dim3(static_cast<unsigned>(tiles * a.slices)), dim3(kThreads), smem, s, a);
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -289,30 +423,18 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// one lane of a whole warp
-__device__ __forceinline__ bool elect_one() {
-  uint32_t yes;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(yes));
-  return yes != 0;
-}
-
 constexpr int kPairStages = 6;
+static_assert(kPairStages % 6 == 0, "three warps of copies and two buffers of sums take the stages by turns");
 constexpr int kPairCols = 256;         // of a tile, and of one accumulator
 constexpr int kPairThreads = 512;      // warps: three of copies, four of MMAs, scales, eight of sums
 constexpr int kPairRegs = 208, kPairRegsOther = 48, kPairRegsAtLaunch = 128;
 static_assert(256 * kPairRegs + 256 * kPairRegsOther <= kPairThreads * kPairRegsAtLaunch, "the raise draws on the launch's registers");
-constexpr int kTurnLd = 18;            // of 32 rows of 16 values that a warp turns in shared memory
-constexpr int kScaleRun = 8;           // blocks of K whose scales are fetched together: a sector of x_scale
-constexpr int kPairSmem = 1024 + kPairStages * 2 * kOperand + 8 * 32 * kTurnLd * 2 + 2 * kScaleRun * (128 + 2) * 4 + 256;
+constexpr int kPairSmem = 1024 + kPairStages * 2 * kOperand + 8 * 32 * kTurnLd * 2 + kScaleBytes + kBarBytes;
 constexpr int kPairGroup = 8;          // row tiles that follow one another before the next column tile
 
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-template <bool GATED>
+template <int ACT>
 __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const __grid_constant__ Fp8Args a) {
+  constexpr bool GATED = is_gated(ACT);
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint16_t* const turn = reinterpret_cast<uint16_t*>(smem + kPairStages * 2 * kOperand);
@@ -427,31 +549,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
         if (last) mbar_drain(last, last_phase);
       }
     } else if (warp == 5) {
-      // The scales of kScaleRun blocks of K at a time, turned so that the threads of a row's sums read them side by
-      // side (read from global memory by those threads, one value a block of K, they cost half of the kernel's time).
       int run = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += pairs) {
         int m0, n0;
         place(t, m0, n0);
+        const int row0 = min(m0 + rank * 128, a.M - 1);
         const int blocks = (a.N - 1) / kGroup;  // a tile's second half may lie behind the matrix: its sums are not stored
         const float* const ws = a.ws + static_cast<int64_t>(n0 / kGroup) * a.groups;
         const float* const ws2 = a.ws + static_cast<int64_t>(min((GATED ? a.cols + n0 : n0 + 128) / kGroup, blocks)) * a.groups;
         for (int kb = 0; kb < a.groups; kb += kScaleRun, ++run) {
           ok = __all_sync(0xffffffffu, wait_for(&scales_free[run & 1], ((run >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns));
           if (!ok) break;
-          float* const x_to = x_ring + (run & 1) * kScaleRun * 128;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float* const xs = a.xs + static_cast<int64_t>(min(m0 + rank * 128 + 32 * j + lane, a.M - 1)) * a.xs_ld;
-            float v[kScaleRun];
-#pragma unroll
-            for (int i = 0; i < kScaleRun; ++i) v[i] = __ldg(xs + min(kb + i, a.groups - 1) * a.xs_step);
-#pragma unroll
-            for (int i = 0; i < kScaleRun; ++i) x_to[i * 128 + 32 * j + lane] = v[i];
-          }
-          if (lane < 2 * kScaleRun)
-            w_ring[(run & 1) * 2 * kScaleRun + lane] = __ldg((lane & 1 ? ws2 : ws) + min(kb + (lane >> 1), a.groups - 1));
+          fetch_scales(a, run, kb, row0, max(1, min(128, a.M - row0)), ws, ws2, x_ring, w_ring, lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(&scales[run & 1]);
         }
@@ -493,7 +603,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
         for (int c = 0; c < 4; ++c) {
           if (c < 3) tmem_ld32_issue(from + (c + 1) * 32, v[(c + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(v[c & 1][i]), c < 2 ? s0 : s1, acc[32 * c + i]);
+          for (int i = 0; i < 32; i += 2) fma2(acc[32 * c + i], acc[32 * c + i + 1], v[c & 1][i], v[c & 1][i + 1], c < 2 ? s0 : s1);
           if (c < 3) tmem_wait_ld<32>(v[(c + 1) & 1]);
           if (c == 2) {  // all of it is in registers
             tc_fence_before();
@@ -511,35 +621,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
       const int first = m0 + rank * 128 + quarter * 32;  // the warp's rows
       constexpr int kMine = GATED ? 64 : 128;            // columns of out
       const int c0 = n0 + half * kMine;
-      if (GATED || a.act != MOE_ACT_IDENTITY) {
+      if constexpr (ACT != MOE_ACT_IDENTITY) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) acc[i] = activate(a.act, acc[i], GATED ? acc[64 + (i & 63)] : 0.0f);
+        for (int i = 0; i < kMine; ++i) acc[i] = activate(ACT, acc[i], GATED ? acc[64 + (i & 63)] : 0.0f);
       }
-      if (a.wide) {  // rows of whole 16-byte pieces
-        if (first + lane < a.M) {
-          uint16_t* const to = a.out + static_cast<int64_t>(first + lane) * a.cols + c0;
-#pragma unroll
-          for (int i = 0; i < kMine / 8; ++i)
-            if (c0 + 8 * i < a.cols)
-              *reinterpret_cast<uint4*>(to + 8 * i) =
-                  make_uint4(bf16x2(acc[8 * i], acc[8 * i + 1]), bf16x2(acc[8 * i + 2], acc[8 * i + 3]),
-                             bf16x2(acc[8 * i + 4], acc[8 * i + 5]), bf16x2(acc[8 * i + 6], acc[8 * i + 7]));
-        }
-      } else {  // 32 x 16 values change hands in shared memory, and the warp writes row by row
-        uint16_t* const mine = turn + (warp - 8) * 32 * kTurnLd;
-#pragma unroll
-        for (int c = 0; c < kMine / 16; ++c) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(mine + lane * kTurnLd + 2 * i) = bf16x2(acc[16 * c + 2 * i], acc[16 * c + 2 * i + 1]);
-          __syncwarp();
-          const int col = c0 + 16 * c + (lane & 15);
-          if (col < a.cols) {
-            uint16_t* const to = a.out + static_cast<int64_t>(first) * a.cols + col;
-            for (int r = lane >> 4; r < min(32, a.M - first); r += 2) to[static_cast<int64_t>(r) * a.cols] = mine[r * kTurnLd + (lane & 15)];
-          }
-          __syncwarp();
-        }
-      }
+      store_rows<kMine>(a, acc, first, c0, turn + (warp - 8) * 32 * kTurnLd, lane);
     }
   }
   __syncwarp();
@@ -554,9 +640,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
 }
 
 // How many pairs run at once on the current device: looked up once for each.
-template <bool GATED>
+template <int ACT>
 moe_status_t resident_pairs(int& pairs) {
-  const auto kern = linear_fp8_pair_kernel<GATED>;
+  const auto kern = linear_fp8_pair_kernel<ACT>;
   static std::atomic<int> known[64];
   int dev = 0;
   MOE_CUDA(cudaGetDevice(&dev));
@@ -581,18 +667,30 @@ moe_status_t resident_pairs(int& pairs) {
   return MOE_OK;
 }
 
-template <bool GATED>
+// Pairs, or single blocks with K in slices: the one of less estimated time. A wave of single blocks takes 0.36 us
+// a block of K and 2.5 us around it; one of pairs 0.46 us (for four times the columns and rows) and 1.3, and 4 us once.
+bool use_pairs(int M, int cols, int groups, bool gated) {
+  const int sms = num_sms(), out = gated ? 2 : 1;
+  const double tiles = ceil(M / 128.0) * ceil(cols * out / 128.0), pair_tiles = ceil(M / 256.0) * ceil(cols * out / 256.0);
+  int slices = 1;
+  while (slices < kMaxSlices && tiles * slices * 2 <= sms && groups >= 4 * slices) slices *= 2;
+  const double one = ceil(tiles * slices / sms) * (groups * 0.36 / slices + 2.5);
+  const double two = ceil(pair_tiles / (sms / 2)) * (groups * 0.46 + 1.3) + 4.0;
+  return two < one;
+}
+
+template <int ACT>
 moe_status_t launch_pairs(Fp8Args a, const void* x, int64_t ld_x, const void* w, cudaStream_t s) {
-  constexpr int kOut = GATED ? kPairCols / 2 : kPairCols;
+  constexpr int kOut = is_gated(ACT) ? kPairCols / 2 : kPairCols;
   a.m_tiles = (a.M - 1) / 256 + 1;
   const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.cols - 1) / kOut + 1);
   MOE_CHECK(tiles <= INT32_MAX / 2, MOE_ERR_UNSUPPORTED_SHAPE);
   a.wide = a.cols % 8 == 0;
   if (!encode_rows(&a.tmap_x, x, a.K, a.M, ld_x, 128) || !encode_rows(&a.tmap_w, w, a.K, a.N, a.K, 64)) return MOE_ERR_CUDA;
-  const auto kern = linear_fp8_pair_kernel<GATED>;
+  const auto kern = linear_fp8_pair_kernel<ACT>;
   MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
   int pairs = 0;
-  const moe_status_t known = resident_pairs<GATED>(pairs);
+  const moe_status_t known = resident_pairs<ACT>(pairs);
   if (known != MOE_OK) return known;
   const unsigned grid = static_cast<unsigned>(tiles < pairs ? tiles : pairs);
   return launch_clusters(kern, 2, dim3(2 * grid), dim3(kPairThreads), kPairSmem, s, a);
@@ -629,7 +727,19 @@ extern "C" moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const flo
   a.xs = x_scale, a.ws = w_scale, a.out = out, a.status = dev_status, a.wait_ns = kWaitLimitNs;
   a.M = M, a.N = N, a.K = K, a.groups = groups, a.act = activation, a.cols = cols;
   a.xs_step = per_token ? 0 : 1, a.xs_ld = per_token ? 1 : groups;
-  if (M >= 1024 && N >= 1024)
-    return gated ? launch_pairs<true>(a, x, ld_x, w, as_stream(stream)) : launch_pairs<false>(a, x, ld_x, w, as_stream(stream));
-  return gated ? launch_tiles<true>(a, x, ld_x, w, as_stream(stream)) : launch_tiles<false>(a, x, ld_x, w, as_stream(stream));
+  const bool pairs = use_pairs(M, cols, groups, gated);
+  cudaStream_t s = as_stream(stream);
+#define MOE_FP8_CASE(ACT) \
+  case ACT: return pairs ? launch_pairs<ACT>(a, x, ld_x, w, s) : launch_tiles<ACT>(a, x, ld_x, w, s)
+  switch (activation) {
+    MOE_FP8_CASE(MOE_ACT_SWIGLU);
+    MOE_FP8_CASE(MOE_ACT_RELU2);
+    MOE_FP8_CASE(MOE_ACT_GEGLU);
+    MOE_FP8_CASE(MOE_ACT_GELU);
+    MOE_FP8_CASE(MOE_ACT_RELU);
+    MOE_FP8_CASE(MOE_ACT_SILU);
+    MOE_FP8_CASE(MOE_ACT_IDENTITY);
+  }
+#undef MOE_FP8_CASE
+  return MOE_ERR_INVALID_ARGUMENT;
 }
