@@ -224,23 +224,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
   pdl_trigger();
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t bytes = a.x_rows * 128 + kOperand;
-      int stage = 0, phase = 0, issued = 0;
-      for (int i = 0; i < n; ++i) {
-        if (!wait_for(&done[stage], phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
+    const uint32_t bytes = a.x_rows * 128 + kOperand;
+    int stage = 0, phase = 0, issued = 0;
+    for (int i = 0; i < n; ++i) {
+      if (!__all_sync(0xffffffffu, wait_for(&done[stage], phase ^ 1, abort_flag, a.status, a.wait_ns))) break;
+      if (elect_one()) {
         uint8_t* const st = smem + stage * a.stage_bytes;
         const int k = (kb0 + i) * 128;
         mbar_arrive_expect_tx(&full[stage], bytes);
         tma_load_2d(st, &a.tmap_w, k, n0, &full[stage]);
         if (GATED) tma_load_2d(st + kOperand / 2, &a.tmap_w, k, a.cols + n0, &full[stage]);
         tma_load_2d(st + kOperand, &a.tmap_x, k, m0, &full[stage]);
-        ++issued;
-        if (++stage == a.stages) stage = 0, phase ^= 1;
       }
-      // what was issued lands before the block ends, even if nothing waited for it
-      for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_drain(&full[i % a.stages], i / a.stages & 1);
+      __syncwarp();
+      ++issued;
+      if (++stage == a.stages) stage = 0, phase ^= 1;
     }
+    // what was issued lands before the block ends, even if nothing waited for it
+    for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_drain(&full[i % a.stages], i / a.stages & 1);
   } else if (warp < 3) {
     // two warps take the blocks of K by turns: what one costs them in waits is more than it costs the tensor core
     const uint64_t w_desc = sdesc_kmajor_sw128(smem_u32(smem)), x_desc = sdesc_kmajor_sw128(smem_u32(smem) + kOperand);
@@ -485,37 +486,38 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
   if (warp < 8) {
     setmaxnreg_dec<kPairRegsOther>();
     if (warp == 0 || warp > 5) {
-      if (lane == 0) {
-        // Three warps take the blocks of K by turns: the wait for a stage and its three copies cost a thread more time
-        // than the MMAs leave it.
-        const int all = (tiles - pair + pairs - 1) / pairs * a.groups;  // blocks of K of this pair's tiles
-        int t = pair, kb = warp == 0 ? 0 : warp - 5, last = -1;
-        bool ok = true;
-        for (int i = kb; i < all; i += 3) {
-          while (kb >= a.groups) kb -= a.groups, t += pairs;
-          const int stage = i % kPairStages, phase = i / kPairStages & 1;
-          int m0, n0;
-          place(t, m0, n0);
-          const int y_x = m0 + rank * 128, y_w = n0 + rank * (GATED ? a.cols : 64);
+      // Three warps take the blocks of K by turns: the wait for a stage and its three copies cost one more time
+      // than the MMAs leave it.
+      const int all = (tiles - pair + pairs - 1) / pairs * a.groups;  // blocks of K of this pair's tiles
+      int t = pair, kb = warp == 0 ? 0 : warp - 5, stage = kb, phase = 0, last = -1, m0 = 0, n0 = 0;
+      bool ok = true;
+      for (int i = kb; i < all; i += 3) {
+        while (kb >= a.groups) kb -= a.groups, t += pairs;
+        if (kb < 3) place(t, m0, n0);
+        const int y_x = m0 + rank * 128, y_w = n0 + rank * (GATED ? a.cols : 64);
+        ok = wait_for(&done[2 * stage], phase ^ 1, abort_flag, a.status, a.wait_ns) &&
+             wait_for(&done[2 * stage + 1], phase ^ 1, abort_flag, a.status, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t* const st = smem + stage * 2 * kOperand;
           const uint32_t bar = cluster_address(&full[stage], 0);
-          ok = wait_for(&done[2 * stage], phase ^ 1, abort_flag, a.status, a.wait_ns) &&
-               wait_for(&done[2 * stage + 1], phase ^ 1, abort_flag, a.status, a.wait_ns);
-          if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kOperand);  // both blocks' loads
           tma_load_pair(st, &a.tmap_x, kb * 128, y_x, bar);
           tma_load_pair(st + kOperand, &a.tmap_w, kb * 128, y_w, bar);
           tma_load_pair(st + kOperand + kOperand / 2, &a.tmap_w, kb * 128, y_w + (GATED ? 64 : 128), bar);
-          last = i;
-          kb += 3;
         }
-        // loads land before the pair ends, even if nothing waited for them
-        if (rank == 0) {
-          for (int i = max(last - 3, 0); i <= last; i += 3) mbar_drain(&full[i % kPairStages], i / kPairStages & 1);
-        } else if (!ok) {
-          const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 1000000ull) {
-          }
+        __syncwarp();
+        last = i;
+        kb += 3, stage += 3;
+        if (stage >= kPairStages) stage -= kPairStages, phase ^= 1;
+      }
+      // loads land before the pair ends, even if nothing waited for them
+      if (rank == 0) {
+        for (int i = max(last - 3, 0); i <= last; i += 3) mbar_drain(&full[i % kPairStages], i / kPairStages & 1);
+      } else if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
         }
       }
     } else if (warp <= 4) {
