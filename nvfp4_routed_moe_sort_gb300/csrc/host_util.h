@@ -43,6 +43,20 @@ inline int num_sms() {
   return n;
 }
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1: n / d = (n * mul) >> (32 + shift), mul = ceil(2^(32 + shift) / d) with
+// shift = ceil(log2 d) - 1, so that mul's excess over the true quotient, below d, is at most 2^(shift + 1).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __host__ explicit FastDiv(uint32_t divisor = 1) : d(divisor), mul(0), shift(0) {
+    if (d == 1) return;
+    while ((1ull << (shift + 1)) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << (32 + shift)) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return d == 1 ? n : __umulhi(n, mul) >> shift; }
+#endif
+};
+
 // Launch `kern` on `s` with programmatic stream serialisation, so it may begin while the
 // previous kernel of the stream finishes (it waits with griddepcontrol.wait before using
 // that kernel's results).

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
     const uint32_t bytes = a.x_rows * 128 + kOperand;
     int stage = 0, phase = 0, issued = 0;
     for (int i = 0; i < n; ++i) {
-      if (!__all_sync(0xffffffffu, wait_for(&done[stage], phase ^ 1, abort_flag, a.status, a.wait_ns))) break;
+      if (i >= a.stages && !__all_sync(0xffffffffu, wait_for(&done[stage], phase ^ 1, abort_flag, a.status, a.wait_ns))) break;
       if (elect_one()) {
         uint8_t* const st = smem + stage * a.stage_bytes;
         const int k = (kb0 + i) * 128;

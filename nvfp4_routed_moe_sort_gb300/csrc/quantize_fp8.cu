@@ -36,22 +36,74 @@ struct QuantArgs {
   uint8_t* y;
   float* scale;
   int64_t ld_x;
-  int M, K, groups;
+  uint32_t M, K, groups;
 };
 
-// one warp per scale group, four values a lane
-__global__ void __launch_bounds__(256) quantize_fp8_rows_kernel(QuantArgs a) {
+__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint2 encode8(const float* v, Inverse k) {
+  float t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = __fmul_rn(v[e] * k.up, k.inv);
+  return make_uint2(e4m3x2(t[0], t[1]) | e4m3x2(t[2], t[3]) << 16, e4m3x2(t[4], t[5]) | e4m3x2(t[6], t[7]) << 16);
+}
+
+// Rows of whole 16-byte pieces: half a warp to a scale group, eight neighbouring values a lane, ITEMS groups' loads
+// in flight together.
+template <int ITEMS>
+__global__ void __launch_bounds__(256) quantize_fp8_rows_kernel(QuantArgs a, FastDiv groups) {
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+  const uint32_t all = static_cast<uint32_t>(a.M) * groups.d, first = blockIdx.x * 16 * ITEMS + half;
+  uint4 u[ITEMS];
+  uint32_t row[ITEMS], col[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t g = first + 16 * i;
+    row[i] = groups(g);
+    col[i] = (g - row[i] * groups.d) * kGroup + 8 * lane;
+    u[i] = make_uint4(0, 0, 0, 0);
+    if (g < all && col[i] < a.K) u[i] = __ldcs(reinterpret_cast<const uint4*>(a.x + row[i] * a.ld_x + col[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t g = first + 16 * i;
+    float v[8], top = 0.0f;
+    unpack8(u[i], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(v[e]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (g < all && lane == 0) a.scale[g] = scale_of(top);
+    if (g < all && col[i] < a.K) *reinterpret_cast<uint2*>(a.y + row[i] * static_cast<int64_t>(a.K) + col[i]) = encode8(v, inverse_of(top));
+  }
+}
+
+// Rows of any length and place: one warp per scale group, four values a lane, each by itself.
+__global__ void __launch_bounds__(256) quantize_fp8_odd_rows_kernel(QuantArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (item >= static_cast<int64_t>(a.M) * a.groups) return;
   const int64_t m = item / a.groups;
-  const int col = static_cast<int>(item - m * a.groups) * kGroup;
+  const uint32_t col = static_cast<uint32_t>(item - m * a.groups) * kGroup;
   float v[4], top = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c = col + lane + 32 * i;
+    const uint32_t c = col + lane + 32 * i;
     v[i] = c < a.K ? bf16_at(a.x + m * a.ld_x + c) : 0.0f;
     top = max_nan(top, fabsf(v[i]));
   }
@@ -61,47 +113,81 @@ __global__ void __launch_bounds__(256) quantize_fp8_rows_kernel(QuantArgs a) {
   const Inverse inv = inverse_of(top);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c = col + lane + 32 * i;
+    const uint32_t c = col + lane + 32 * i;
     if (c < a.K) a.y[m * a.K + c] = static_cast<uint8_t>(f32_to_e4m3(__fmul_rn(v[i] * inv.up, inv.inv)));
   }
 }
 
-// one block of 8 warps per 128 x 128 values, 16 rows a warp
+__device__ __forceinline__ float block_max(float top, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = max_nan(top, red[w]);
+  return top;
+}
+
+// One block of 8 warps per 128 x 128 values. V = 8: rows of whole 16-byte pieces, 16 lanes to a row; V = 1: any rows,
+// 16 rows a warp, four values a lane.
+template <int V>
 __global__ void __launch_bounds__(256) quantize_fp8_blocks_kernel(QuantArgs a) {
   __shared__ float red[8];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * kGroup;
   const int64_t row = static_cast<int64_t>(blockIdx.y) * kGroup;
-  float v[16][4], top = 0.0f;
+  float top = 0.0f;
+  if constexpr (V == 8) {
+    const uint32_t col = blockIdx.x * kGroup + 8 * (threadIdx.x & 15), first = threadIdx.x >> 4;
+    uint4 u[8];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int64_t m = row + warp + 8 * r;
+    for (int r = 0; r < 8; ++r) {
+      const int64_t m = row + first + 16 * r;
+      u[r] = make_uint4(0, 0, 0, 0);
+      if (m < a.M && col < a.K) u[r] = __ldcs(reinterpret_cast<const uint4*>(a.x + m * a.ld_x + col));
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = col + lane + 32 * i;
-      v[r][i] = m < a.M && c < a.K ? bf16_at(a.x + m * a.ld_x + c) : 0.0f;
-      top = max_nan(top, fabsf(v[r][i]));
+    for (int r = 0; r < 8; ++r) {
+      float v[8];
+      unpack8(u[r], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(v[e]));
+    }
+    top = block_max(top, red);
+    const Inverse inv = inverse_of(top);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int64_t m = row + first + 16 * r;
+      float v[8];
+      unpack8(u[r], v);
+      if (m < a.M && col < a.K) *reinterpret_cast<uint2*>(a.y + m * a.K + col) = encode8(v, inv);
+    }
+  } else {
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * kGroup;
+    float v[16][4];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int64_t m = row + warp + 8 * r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t c = col + lane + 32 * i;
+        v[r][i] = m < a.M && c < a.K ? bf16_at(a.x + m * a.ld_x + c) : 0.0f;
+        top = max_nan(top, fabsf(v[r][i]));
+      }
+    }
+    top = block_max(top, red);
+    const Inverse inv = inverse_of(top);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int64_t m = row + warp + 8 * r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t c = col + lane + 32 * i;
+        if (m < a.M && c < a.K) a.y[m * a.K + c] = static_cast<uint8_t>(f32_to_e4m3(__fmul_rn(v[r][i] * inv.up, inv.inv)));
+      }
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) red[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) top = max_nan(top, red[w]);
   if (threadIdx.x == 0) a.scale[static_cast<int64_t>(blockIdx.y) * a.groups + blockIdx.x] = scale_of(top);
-  const Inverse inv = inverse_of(top);
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int64_t m = row + warp + 8 * r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = col + lane + 32 * i;
-      if (m < a.M && c < a.K) a.y[m * a.K + c] = static_cast<uint8_t>(f32_to_e4m3(__fmul_rn(v[r][i] * inv.up, inv.inv)));
-    }
-  }
 }
 
 }  // namespace
@@ -124,11 +210,16 @@ extern "C" moe_status_t moe_quantize_fp8(const uint16_t* x, int64_t ld_x, int32_
   MOE_CHECK(!overlaps(y, y_bytes, x, in_bytes) && !overlaps(y_scale, scale_bytes, x, in_bytes) &&
                 !overlaps(y, y_bytes, y_scale, scale_bytes),
             MOE_ERR_OVERLAP);
-  const QuantArgs a = {x, y, y_scale, ld_x, M, K, groups};
+  const QuantArgs a = {x, y, y_scale, ld_x, static_cast<uint32_t>(M), static_cast<uint32_t>(K), static_cast<uint32_t>(groups)};
+  const bool whole = ((K | ld_x) & 7) == 0 && aligned16(x) && (reinterpret_cast<uintptr_t>(y) & 7) == 0;
+  cudaStream_t s = as_stream(stream);
   if (block_rows == 1) {
-    const dim3 grid(static_cast<unsigned>((strips * groups + 7) / 8));
-    return launch_pdl(quantize_fp8_rows_kernel, grid, dim3(256), 0, as_stream(stream), a);
+    const int64_t items = strips * groups;
+    if (!whole || items >= INT32_MAX - 64) return launch_pdl(quantize_fp8_odd_rows_kernel, dim3(static_cast<unsigned>((items + 7) / 8)), dim3(256), 0, s, a);
+    if (items < static_cast<int64_t>(num_sms()) * 16 * 8 * 4)
+      return launch_pdl(quantize_fp8_rows_kernel<1>, dim3(static_cast<unsigned>((items + 15) / 16)), dim3(256), 0, s, a, FastDiv(groups));
+    return launch_pdl(quantize_fp8_rows_kernel<4>, dim3(static_cast<unsigned>((items + 63) / 64)), dim3(256), 0, s, a, FastDiv(groups));
   }
   const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(strips));
-  return launch_pdl(quantize_fp8_blocks_kernel, grid, dim3(256), 0, as_stream(stream), a);
+  return launch_pdl(whole ? quantize_fp8_blocks_kernel<8> : quantize_fp8_blocks_kernel<1>, grid, dim3(256), 0, s, a);
 }

@@ -40,31 +40,42 @@ __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
   return __double2ull_rz(f * 18446744073709551616.0);
 }
 
-// cosine and sine of pair i of token n; a pair of an axis that is none is not turned
-__device__ __forceinline__ float2 phase_of(const RotaryArgs& a, int64_t n, int i) {
-  const int axis = a.axes ? a.axes[i] : 0;
-  if (axis >= a.num_axes) {
-    if (a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
-    return make_float2(1.0f, 0.0f);
-  }
+__device__ __forceinline__ int64_t position_of(const RotaryArgs& a, int64_t n, int axis) {
   const int64_t at = axis * a.ld_pos + n;
-  const int64_t pos = a.pos64 ? static_cast<const int64_t*>(a.pos)[at] : static_cast<const int32_t*>(a.pos)[at];
-  const uint64_t turn = static_cast<uint64_t>(pos) * turns_of(a.inv_freq[i]);
+  return a.pos64 ? static_cast<const int64_t*>(a.pos)[at] : static_cast<const int32_t*>(a.pos)[at];
+}
+
+// cosine and sine of `turns` times a position
+__device__ __forceinline__ float2 phase_of(int64_t position, uint64_t turns) {
+  const uint64_t turn = static_cast<uint64_t>(position) * turns;
   float s, c;
   sincospif(__ll2float_rn(static_cast<int64_t>(turn)) * 0x1p-63f, &s, &c);
   return make_float2(c, s);
 }
 
+// the axis of pair i; a pair of an axis that is none is not turned: axis 0, and its frequency counts as 0
+__device__ __forceinline__ int axis_of(const RotaryArgs& a, int i, uint64_t& turns) {
+  const int axis = a.axes ? a.axes[i] : 0;
+  if (axis < a.num_axes) return axis;
+  if (a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+  turns = 0;
+  return 0;
+}
+
 __device__ __forceinline__ float value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 __device__ __forceinline__ uint16_t bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// one block per token: its phases first, then its heads pair by pair
-__global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a) {
+// Any sizes and places: one block per token, its phases first, then its heads pair by pair.
+__global__ void __launch_bounds__(256) rotary_odd_kernel(RotaryArgs a) {
   __shared__ float2 phase[kMaxHeadDim / 2];
   pdl_wait();
   pdl_trigger();
   const int64_t n = blockIdx.x;
-  for (int i = threadIdx.x; i < a.half; i += blockDim.x) phase[i] = phase_of(a, n, i);
+  for (int i = threadIdx.x; i < a.half; i += blockDim.x) {
+    uint64_t turns = turns_of(a.inv_freq[i]);
+    const int axis = axis_of(a, i, turns);
+    phase[i] = phase_of(position_of(a, n, axis), turns);
+  }
   __syncthreads();
   for (int t = 0; t < 2; ++t) {
     const uint16_t* in = a.in[t] + n * a.ld_in[t];
@@ -84,6 +95,125 @@ __global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a) {
         out[at] = in[at];
       }
   }
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// eight pairs (x[i], y[i]) of two 16-byte pieces, or (x[0], x[1]), (x[2], x[3]) ... of both where neighbours pair
+template <bool ADJACENT>
+__device__ __forceinline__ void turn8(uint4& u, uint4& v, const float2* p) {
+  uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (ADJACENT) {
+      const float a = low(x[i]), b = high(x[i]), c = low(y[i]), d = high(y[i]);
+      const float2 s = p[i], t = p[4 + i];
+      x[i] = bf16x2(a * s.x - b * s.y, a * s.y + b * s.x);
+      y[i] = bf16x2(c * t.x - d * t.y, c * t.y + d * t.x);
+    } else {
+      const float a = low(x[i]), b = high(x[i]), c = low(y[i]), d = high(y[i]);
+      const float2 s = p[2 * i], t = p[2 * i + 1];
+      x[i] = bf16x2(a * s.x - c * s.y, b * t.x - d * t.y);
+      y[i] = bf16x2(a * s.y + c * s.x, b * t.y + d * t.x);
+    }
+  }
+  u = make_uint4(x[0], x[1], x[2], x[3]);
+  v = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+// Heads of whole 16-byte pieces at 16-byte addresses. A block takes runs of `tokens` tokens one after another: their
+// phases go to shared memory, then each thread takes eight pairs of a head at a time, the loads of ITEMS of them in
+// flight together. What is not turned is copied where `out` is not `in`. The frequencies' conversions to turns, in 64 bits,
+// are a block's, not a token's: the card has few units for them.
+template <bool ADJACENT, int ITEMS>
+__global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int tokens, FastDiv per_token, FastDiv per_head, FastDiv halves) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  uint64_t* const turns = reinterpret_cast<uint64_t*>(raw);                    // [half]
+  float2* const phase = reinterpret_cast<float2*>(turns + a.half);             // [tokens][half]
+  uint8_t* const axis = reinterpret_cast<uint8_t*>(phase + tokens * a.half);   // [half]
+  pdl_wait();
+  pdl_trigger();
+  for (int i = threadIdx.x; i < a.half; i += 256) {
+    uint64_t t = turns_of(a.inv_freq[i]);
+    axis[i] = static_cast<uint8_t>(axis_of(a, i, t));
+    turns[i] = t;
+  }
+  const int heads = a.heads[0] + a.heads[1], rest = (a.dim - 2 * a.half) / 8;
+  const bool copy = rest > 0 && (a.copy[0] || a.copy[1]);
+  for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * tokens; n0 < a.N; n0 += static_cast<int64_t>(gridDim.x) * tokens) {
+    const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.N - n0));
+    __syncthreads();
+    for (int i = threadIdx.x; i < here * a.half; i += 256) {
+      const int n = halves(i), f = i - n * a.half;
+      phase[i] = phase_of(position_of(a, n0 + n, axis[f]), turns[f]);
+    }
+    __syncthreads();
+    const int all = here * per_token.d;
+    for (int j0 = threadIdx.x + blockIdx.y * 256 * ITEMS; j0 < all; j0 += 256 * ITEMS * gridDim.y) {
+      uint4 u[ITEMS], v[ITEMS];
+      uint16_t* to[ITEMS];
+      int at[ITEMS];
+      const int apart = ADJACENT ? 8 : a.half;
+#pragma unroll
+      for (int e = 0; e < ITEMS; ++e) {
+        const int j = j0 + 256 * e;
+        if (j < all) {
+          const int n = per_token(j), r = j - n * per_token.d, head = per_head(r), c = r - head * per_head.d;
+          const bool k = head >= a.heads[0];
+          const int place = (k ? head - a.heads[0] : head) * a.dim + c * (ADJACENT ? 16 : 8);
+          const uint16_t* const from = (k ? a.in[1] : a.in[0]) + (n0 + n) * (k ? a.ld_in[1] : a.ld_in[0]) + place;
+          to[e] = (k ? a.out[1] : a.out[0]) + (n0 + n) * (k ? a.ld_out[1] : a.ld_out[0]) + place;
+          at[e] = n * a.half + 8 * c;
+          u[e] = __ldcs(reinterpret_cast<const uint4*>(from));
+          v[e] = __ldcs(reinterpret_cast<const uint4*>(from + apart));
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < ITEMS; ++e) {
+        if (j0 + 256 * e < all) {
+          float2 p[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = reinterpret_cast<const float4*>(phase + at[e])[i];
+          turn8<ADJACENT>(u[e], v[e], p);
+          *reinterpret_cast<uint4*>(to[e]) = u[e];
+          *reinterpret_cast<uint4*>(to[e] + apart) = v[e];
+        }
+      }
+    }
+    if (copy) {
+      for (int j = threadIdx.x + blockIdx.y * 256; j < here * heads * rest; j += 256 * gridDim.y) {
+        const int n = j / (heads * rest), r = j - n * heads * rest, head = r / rest;
+        const int t = head >= a.heads[0];
+        const int64_t place = (t ? head - a.heads[0] : head) * a.dim + 2 * a.half + (r - head * rest) * 8;
+        if (a.copy[t])
+          *reinterpret_cast<uint4*>(a.out[t] + (n0 + n) * a.ld_out[t] + place) =
+              *reinterpret_cast<const uint4*>(a.in[t] + (n0 + n) * a.ld_in[t] + place);
+      }
+    }
+  }
+}
+
+template <bool ADJACENT>
+moe_status_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
+  const int chunks = a.half / 8, per = (a.heads[0] + a.heads[1]) * chunks;  // a token's work, in eight pairs
+  const int64_t sms = num_sms();
+  // many tokens: several to a run, so that it has a thousand pieces of eight pairs, and as many blocks as fit; few
+  // tokens: their heads over several blocks
+  int tokens = 1;
+  while (tokens < 8 && tokens * 2 * a.half <= 2048 && tokens * per < 1024 && a.N >= sms * 4 * tokens) tokens *= 2;
+  const int64_t runs = (a.N + tokens - 1) / tokens, blocks = runs < sms * 8 ? runs : sms * 8;
+  int split = 1;
+  while (split < 16 && blocks * split * 2 <= sms * 2 && per * tokens > 256 * split) split *= 2;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
+  const size_t smem = static_cast<size_t>(a.half) * (sizeof(uint64_t) + tokens * sizeof(float2) + 1);
+  const FastDiv per_token(per), per_head(chunks), halves(a.half);
+  if (per * tokens <= 256 * split) return launch_pdl(rotary_kernel<ADJACENT, 1>, grid, dim3(256), smem, s, a, tokens, per_token, per_head, halves);
+  return launch_pdl(rotary_kernel<ADJACENT, 4>, grid, dim3(256), smem, s, a, tokens, per_token, per_head, halves);
 }
 
 // rows of `width` values every `ld` values; whether two of them share memory. Slices of one wider row do not.
@@ -145,5 +275,9 @@ extern "C" moe_status_t moe_rotary(const uint16_t* q, int64_t ld_q, int32_t num_
   a.pos = positions, a.inv_freq = inv_freq, a.axes = axes, a.status = dev_status;
   a.ld_pos = ld_positions, a.N = N, a.dim = head_dim, a.half = rotary_dim / 2, a.num_axes = num_axes;
   a.pos64 = position_bytes == 8, a.adjacent = adjacent != 0;
-  return launch_pdl(rotary_kernel, dim3(static_cast<unsigned>(N)), dim3(256), 0, as_stream(stream), a);
+  cudaStream_t s = as_stream(stream);
+  const bool whole = rotary_dim % 16 == 0 && head_dim % 8 == 0 && ((ld_q | ld_q_out | ld_k | ld_k_out) & 7) == 0 &&
+                     aligned16(q) && aligned16(k) && aligned16(q_out) && aligned16(k_out);
+  if (!whole) return launch_pdl(rotary_odd_kernel, dim3(static_cast<unsigned>(N)), dim3(256), 0, s, a);
+  return adjacent ? launch_rotary<true>(a, s) : launch_rotary<false>(a, s);
 }
