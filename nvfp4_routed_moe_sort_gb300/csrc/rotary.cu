@@ -8,8 +8,7 @@
 // The angle. A position times a frequency in 32 bits is off by a tenth of a radian from a million tokens
 // on. Only the angle's fraction of a full turn counts, so the frequency becomes a 64-bit fixed-point
 // fraction of a turn, inv_freq / (2 pi) * 2^64, and the integer product with the position drops whole
-// turns by overflowing: what is left is exact but for the frequency's own rounding (2^-54 of it, as
-// a float64 product would have). Sine and cosine are those of a float32 in [-1, 1) times pi.
+// turns by overflowing: what is left is exact but for the frequency's rounding to 2^-64 of a turn. Sine and cosine are those of a float32 in [-1, 1) times pi.
 #include "common.cuh"
 #include "host_util.h"
 
@@ -33,11 +32,20 @@ struct RotaryArgs {
   int copy[2];  // the values that are not turned go to `out` too (it is not `in`)
 };
 
-// a frequency in turns, as a fraction of 2^64; whole turns per position fall away
+// A frequency in turns, as a fraction of 2^64: m 2^(e - 1075) / (2 pi) with the 53-bit m of a float64, in whole numbers
+// (2 / pi in 64 bits), as the card has few units for float64. Whole turns per position fall away at the top.
 __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
-  double f = inv_freq * 0.15915494309189533577;
-  f -= floor(f);
-  return __double2ull_rz(f * 18446744073709551616.0);
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(inv_freq));
+  const int e = static_cast<int>(b >> 52) & 0x7FF;
+  const uint64_t m = (b & 0xFFFFFFFFFFFFFull) | (e ? 1ull << 52 : 0);
+  constexpr uint64_t k2OverPi = 0xA2F9836E4E441529ull;
+  const uint64_t hi = __umul64hi(m, k2OverPi), lo = m * k2OverPi;
+  const int down = 1077 - (e ? e : 1);
+  uint64_t t;
+  if (down >= 64) t = down < 128 ? hi >> (down - 64) : 0;
+  else if (down > 0) t = hi << (64 - down) | lo >> down;
+  else t = down > -64 ? lo << -down : 0;
+  return b >> 63 ? 0 - t : t;
 }
 
 __device__ __forceinline__ int64_t position_of(const RotaryArgs& a, int64_t n, int axis) {
@@ -126,74 +134,75 @@ __device__ __forceinline__ void turn8(uint4& u, uint4& v, const float2* p) {
   v = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-// Heads of whole 16-byte pieces at 16-byte addresses. A block takes runs of `tokens` tokens one after another: their
-// phases go to shared memory, then each thread takes eight pairs of a head at a time, the loads of ITEMS of them in
-// flight together. What is not turned is copied where `out` is not `in`. The frequencies' conversions to turns, in 64 bits,
-// are a block's, not a token's: the card has few units for them.
-template <bool ADJACENT, int ITEMS>
-__global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int tokens, FastDiv per_token, FastDiv per_head, FastDiv halves) {
+// Heads of whole 16-byte pieces at 16-byte addresses. A block has a run of `tokens` tokens: their phases go to shared
+// memory, and each thread takes eight pairs of a head at a time, the first ones fetched before the phases are computed.
+// What is not turned is copied where `out` is not `in`. More pieces in flight a thread cost more in resident warps than
+// they gain (4: 110 -> 115 us for the long prompt, 16 -> 20 for the images).
+template <bool ADJACENT>
+__global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens, FastDiv per_token, FastDiv per_head, FastDiv halves) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint64_t* const turns = reinterpret_cast<uint64_t*>(raw);                    // [half]
   float2* const phase = reinterpret_cast<float2*>(turns + a.half);             // [tokens][half]
   uint8_t* const axis = reinterpret_cast<uint8_t*>(phase + tokens * a.half);   // [half]
   pdl_wait();
   pdl_trigger();
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.N - n0));
+  const int all = here * per_token.d, step = 256 * gridDim.y, apart = ADJACENT ? 8 : a.half;
+  int j = threadIdx.x + blockIdx.y * 256;
+  uint4 u, v;
+  // piece j: its place in the queries (0) or keys (1), and its first phase
+  const auto place = [&](int& t, int64_t& n, int& at) {
+    const int token = per_token(j), r = j - token * per_token.d, head = per_head(r), c = r - head * per_head.d;
+    t = head >= a.heads[0];
+    n = n0 + token;
+    at = token * a.half + 8 * c;
+    return (t ? head - a.heads[0] : head) * a.dim + c * (ADJACENT ? 16 : 8);
+  };
+  const auto fetch = [&] {
+    int t, at;
+    int64_t n;
+    const int in = place(t, n, at);
+    const uint16_t* const from = (t ? a.in[1] : a.in[0]) + n * (t ? a.ld_in[1] : a.ld_in[0]) + in;
+    u = __ldcs(reinterpret_cast<const uint4*>(from));
+    v = __ldcs(reinterpret_cast<const uint4*>(from + apart));
+  };
+  if (j < all) fetch();
   for (int i = threadIdx.x; i < a.half; i += 256) {
     uint64_t t = turns_of(a.inv_freq[i]);
     axis[i] = static_cast<uint8_t>(axis_of(a, i, t));
     turns[i] = t;
   }
-  const int heads = a.heads[0] + a.heads[1], rest = (a.dim - 2 * a.half) / 8;
-  const bool copy = rest > 0 && (a.copy[0] || a.copy[1]);
-  for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * tokens; n0 < a.N; n0 += static_cast<int64_t>(gridDim.x) * tokens) {
-    const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.N - n0));
-    __syncthreads();
-    for (int i = threadIdx.x; i < here * a.half; i += 256) {
-      const int n = halves(i), f = i - n * a.half;
-      phase[i] = phase_of(position_of(a, n0 + n, axis[f]), turns[f]);
-    }
-    __syncthreads();
-    const int all = here * per_token.d;
-    for (int j0 = threadIdx.x + blockIdx.y * 256 * ITEMS; j0 < all; j0 += 256 * ITEMS * gridDim.y) {
-      uint4 u[ITEMS], v[ITEMS];
-      uint16_t* to[ITEMS];
-      int at[ITEMS];
-      const int apart = ADJACENT ? 8 : a.half;
+  __syncthreads();
+  for (int i = threadIdx.x; i < here * a.half; i += 256) {
+    const int n = halves(i), f = i - n * a.half;
+    phase[i] = phase_of(position_of(a, n0 + n, axis[f]), turns[f]);
+  }
+  __syncthreads();
+  while (j < all) {
+    int t, at;
+    int64_t n;
+    const int in = place(t, n, at);
+    uint16_t* const to = (t ? a.out[1] : a.out[0]) + n * (t ? a.ld_out[1] : a.ld_out[0]) + in;
+    float2 p[8];
 #pragma unroll
-      for (int e = 0; e < ITEMS; ++e) {
-        const int j = j0 + 256 * e;
-        if (j < all) {
-          const int n = per_token(j), r = j - n * per_token.d, head = per_head(r), c = r - head * per_head.d;
-          const bool k = head >= a.heads[0];
-          const int place = (k ? head - a.heads[0] : head) * a.dim + c * (ADJACENT ? 16 : 8);
-          const uint16_t* const from = (k ? a.in[1] : a.in[0]) + (n0 + n) * (k ? a.ld_in[1] : a.ld_in[0]) + place;
-          to[e] = (k ? a.out[1] : a.out[0]) + (n0 + n) * (k ? a.ld_out[1] : a.ld_out[0]) + place;
-          at[e] = n * a.half + 8 * c;
-          u[e] = __ldcs(reinterpret_cast<const uint4*>(from));
-          v[e] = __ldcs(reinterpret_cast<const uint4*>(from + apart));
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < ITEMS; ++e) {
-        if (j0 + 256 * e < all) {
-          float2 p[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = reinterpret_cast<const float4*>(phase + at[e])[i];
-          turn8<ADJACENT>(u[e], v[e], p);
-          *reinterpret_cast<uint4*>(to[e]) = u[e];
-          *reinterpret_cast<uint4*>(to[e] + apart) = v[e];
-        }
-      }
-    }
-    if (copy) {
-      for (int j = threadIdx.x + blockIdx.y * 256; j < here * heads * rest; j += 256 * gridDim.y) {
-        const int n = j / (heads * rest), r = j - n * heads * rest, head = r / rest;
-        const int t = head >= a.heads[0];
-        const int64_t place = (t ? head - a.heads[0] : head) * a.dim + 2 * a.half + (r - head * rest) * 8;
-        if (a.copy[t])
-          *reinterpret_cast<uint4*>(a.out[t] + (n0 + n) * a.ld_out[t] + place) =
-              *reinterpret_cast<const uint4*>(a.in[t] + (n0 + n) * a.ld_in[t] + place);
-      }
+    for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = reinterpret_cast<const float4*>(phase + at)[i];
+    turn8<ADJACENT>(u, v, p);
+    *reinterpret_cast<uint4*>(to) = u;
+    *reinterpret_cast<uint4*>(to + apart) = v;
+    j += step;
+    if (j < all) fetch();
+  }
+  const int rest = (a.dim - 2 * a.half) / 8;
+  if (rest > 0 && (a.copy[0] || a.copy[1])) {
+    const int heads = a.heads[0] + a.heads[1];
+    for (int i = threadIdx.x + blockIdx.y * 256; i < here * heads * rest; i += step) {
+      const int n = i / (heads * rest), r = i - n * heads * rest, head = r / rest;
+      const int t = head >= a.heads[0];
+      const int64_t place = (t ? head - a.heads[0] : head) * a.dim + 2 * a.half + (r - head * rest) * 8;
+      if (a.copy[t])
+        *reinterpret_cast<uint4*>(a.out[t] + (n0 + n) * a.ld_out[t] + place) =
+            *reinterpret_cast<const uint4*>(a.in[t] + (n0 + n) * a.ld_in[t] + place);
     }
   }
 }
@@ -202,18 +211,16 @@ template <bool ADJACENT>
 moe_status_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
   const int chunks = a.half / 8, per = (a.heads[0] + a.heads[1]) * chunks;  // a token's work, in eight pairs
   const int64_t sms = num_sms();
-  // many tokens: several to a run, so that it has a thousand pieces of eight pairs, and as many blocks as fit; few
-  // tokens: their heads over several blocks
+  // many tokens: several to a block, while it has less than one and a half pieces a thread (30000 tokens of five heads of
+  // 64: 34 us with one, 10 with eight); few tokens: their heads over several blocks
   int tokens = 1;
-  while (tokens < 8 && tokens * 2 * a.half <= 2048 && tokens * per < 1024 && a.N >= sms * 4 * tokens) tokens *= 2;
-  const int64_t runs = (a.N + tokens - 1) / tokens, blocks = runs < sms * 8 ? runs : sms * 8;
+  while (tokens < 32 && tokens * 2 * a.half <= 2048 && tokens * per < 384 && a.N >= sms * 4 * tokens) tokens *= 2;
+  const int64_t blocks = (a.N + tokens - 1) / tokens;
   int split = 1;
   while (split < 16 && blocks * split * 2 <= sms * 2 && per * tokens > 256 * split) split *= 2;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
   const size_t smem = static_cast<size_t>(a.half) * (sizeof(uint64_t) + tokens * sizeof(float2) + 1);
-  const FastDiv per_token(per), per_head(chunks), halves(a.half);
-  if (per * tokens <= 256 * split) return launch_pdl(rotary_kernel<ADJACENT, 1>, grid, dim3(256), smem, s, a, tokens, per_token, per_head, halves);
-  return launch_pdl(rotary_kernel<ADJACENT, 4>, grid, dim3(256), smem, s, a, tokens, per_token, per_head, halves);
+  return launch_pdl(rotary_kernel<ADJACENT>, grid, dim3(256), smem, s, a, tokens, FastDiv(per), FastDiv(chunks), FastDiv(a.half));
 }
 
 // rows of `width` values every `ld` values; whether two of them share memory. Slices of one wider row do not.
