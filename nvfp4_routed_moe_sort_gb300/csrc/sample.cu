@@ -6,20 +6,22 @@
 // w >= min_p. The token taken is, among the kept ones in the order of their INDEX, the first at which the
 // cumulated weight passes u times their sum.
 //
-// So a row needs no sort, only the last kept logit and how many of the tokens that share it are kept. It
-// is found by histograms over all values: 2048 bins of 1/64 in (max - l) / temperature, then the keys (the
-// logits' bits in their order) of the bin in which the count or the weight is reached, 2048 ways a pass, until
-// one key is left. BF16 logits mostly share one key by then.
+// So a row needs no sort, only the last kept logit and how many of the tokens that share it are kept. It is found by
+// histograms: 2048 bins of 1/64 in (max - l) / temperature, then the keys (the logits' bits in their order) of the bin in
+// which the count or the weight is reached, 2048 ways a pass, until one key is left. BF16 logits mostly share one key by
+// then. Only tokens that can matter are counted: of the threads' largest logits the k-th, taken down to its bin's end, is
+// no larger than the k-th of all, and tokens below the part 1 - top_p of the mean weight cannot all together
+// reach that part of the sum. What is above such a bound goes to a list in shared memory, if it fits.
 //
 // Weights are whole numbers, 2^44 for the largest logit, so that sums are exact in any order and every
-// block of a row sees the same ones. A weight is right to 2^-36 of itself and to a unit: of 131072 tokens of like
-// weight the border at which one token follows the next moves by less than 2^-19 of a token's width. (With
+// block of a row sees the same ones. A weight is right to 2^-34 of itself (2^-37 on average) and to a unit: of 131072
+// tokens of like weight the border at which one token follows the next moves by less than 2^-18 of a token's width. (With
 // float32 exponentials it moves by hundredths, and now and then another token is taken than in exact
-// arithmetic.) exp2 in pieces: 4096 steps from a table, a polynomial of degree 2 for the rest, the argument
+// arithmetic.) exp2 in pieces: 1024 steps from a table, a polynomial of degree 2 for the rest, the argument
 // carried as two floats.
 //
-// A row is spread over a cluster of blocks, each holding its part in shared memory; histograms and
-// totals meet in distributed shared memory.
+// A row is spread over a cluster of blocks; histograms and totals meet in distributed shared memory. The row
+// is read from L2 again for each pass over all of it: two where top_k is set, three for top_p alone, two for neither.
 #include <math.h>
 
 #include "cluster.cuh"
@@ -29,16 +31,18 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = 32;
 constexpr int kBins = 2048;
+constexpr int kMaxWarps = 16;
 constexpr int kMaxBlocks = 8;
 constexpr int kMaxVocab = 1 << 18;
+constexpr int kList = 4096;
 constexpr uint32_t kNone = 0x007FFFFFu;  // the key of -infinity: such a token is never taken
 constexpr uint64_t kOne = 1ull << 44;    // the weight of the largest logit
+constexpr int kStepBits = 10;            // of the table of powers
 
-// 2^(-j / 4096) in units of 2^-44, by products of repeated square roots of 1/2 in 63-bit fixed point
+// 2^(-j / 1024) in units of 2^-44, by products of repeated square roots of 1/2 in 63-bit fixed point
 struct Powers {
-  uint64_t t[4096];
+  uint64_t t[1 << kStepBits];
   static constexpr uint64_t mul(uint64_t a, uint64_t b) {  // a * b / 2^63
     const uint64_t al = a & 0xFFFFFFFFu, ah = a >> 32, bl = b & 0xFFFFFFFFu, bh = b >> 32;
     const uint64_t mid = ah * bl + ((al * bl) >> 32), mid2 = al * bh + (mid & 0xFFFFFFFFu);
@@ -52,16 +56,16 @@ struct Powers {
     return x;
   }
   constexpr Powers() : t() {
-    uint64_t r[12] = {};  // r[b] = 2^(-2^b / 4096)
+    uint64_t r[kStepBits] = {};  // r[b] = 2^(-2^b / 1024)
     uint64_t v = 1ull << 62;
-    for (int b = 11; b >= 0; --b) r[b] = v = root(v);
+    for (int b = kStepBits - 1; b >= 0; --b) r[b] = v = root(v);
     t[0] = 1ull << 63;
-    for (int j = 1; j < 4096; ++j) {
+    for (int j = 1; j < 1 << kStepBits; ++j) {
       int b = 0;
       while (!((j >> b) & 1)) ++b;
       t[j] = mul(t[j & (j - 1)], r[b]);
     }
-    for (int j = 0; j < 4096; ++j) t[j] = (t[j] + (1ull << 18)) >> 19;
+    for (int j = 0; j < 1 << kStepBits; ++j) t[j] = (t[j] + (1ull << 18)) >> 19;
     t[0] = kOne - 1;  // its upper half fits 31 bits, as the product below needs
   }
 };
@@ -76,19 +80,43 @@ struct SampleArgs {
   int V, blocks;
 };
 
+// BF16 logits take few values. Those of magnitude 2^-8 to 2^7 have a bin each, in descending order, zero one between
+// the positive and the negative ones; the few nonzero ones nearer to zero (rare) are listed and count with zero.
+constexpr uint32_t kSmallest = 0x3B80, kSide = 15 * 128;  // bits of 2^-8; values of a sign
+constexpr int kZeroBin = kSide, kValues = 2 * kBins;
+__device__ __forceinline__ int value_bin(uint32_t b) {    // of BF16 bits; below 0: not one of them
+  const uint32_t m = b & 0x7FFFu, off = m - kSmallest;
+  if (off < kSide) return b & 0x8000u ? kSide + 1 + off : kSide - 1 - off;
+  return m == 0 ? kZeroBin : -1;
+}
+__device__ __forceinline__ float bin_value(int bin) {
+  if (bin == kZeroBin || bin > 2 * static_cast<int>(kSide)) return bin == kZeroBin ? 0.0f : -INFINITY;
+  const uint32_t b = bin < kZeroBin ? kSmallest + (kSide - 1 - bin) : 0x8000u + kSmallest + (bin - kSide - 1);
+  return __uint_as_float(b << 16);
+}
+
 struct Shared {
-  uint64_t power[4096];
-  uint64_t total[kBins];  // of every block's histogram
-  uint32_t lo[kBins], hi[kBins];
-  uint64_t warp_a[kWarps];
-  uint32_t warp_b[kWarps], warp_c[kWarps];
+  uint64_t power[1 << kStepBits];
+  uint64_t weight[kValues];    // of each of a BF16 logit's values
+  union {
+    uint64_t total[kBins];     // of every block's histogram
+    uint32_t counts[kValues];  // ... of values
+  };
+  union {
+    struct {
+      uint32_t lo[kBins], hi[kBins];
+    };
+    uint32_t count[kValues];
+  };
+  uint32_t list[kList];        // keys that may be kept; rare values
+  uint64_t warp_a[32];
+  uint32_t warp_b[32], warp_c[32];
   // what each block of the row has to tell, written by them; one array for each meeting, since blocks may be one apart
-  uint64_t peer_best[kMaxBlocks], peer_sum[kMaxBlocks];
-  uint32_t peer_low[kMaxBlocks], peer_high[kMaxBlocks], peer_same[kMaxBlocks];
-  uint64_t before, sum, target;
-  double below;  // temperature * ln(min_p), -infinity without one
-  float ch, cl, step;
-  int bin;
+  uint64_t peer_total[kMaxBlocks], peer_sum[kMaxBlocks], peer_rare[kMaxBlocks];
+  uint32_t peer_others[kMaxBlocks], peer_below[kMaxBlocks];
+  uint32_t peer_top[kMaxBlocks], peer_far[kMaxBlocks], peer_rares[kMaxBlocks], peer_low[kMaxBlocks], peer_high[kMaxBlocks], peer_same[kMaxBlocks];
+  uint64_t before, target;
+  int bin, listed;
 };
 
 // logits' bits in the order of their values; both zeros are one value
@@ -145,17 +173,49 @@ __device__ __forceinline__ uint64_t part_of(float v, uint64_t n, bool& rest) {
   return (hi << (64 - shift)) | (lo >> shift);
 }
 
-// One row's block. All members but data, count and rank are the same in all threads of all its blocks.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A 16-byte piece of a row of V values that begins at value `at`: places outside the row, and NaN, are -infinity.
+template <typename T>
+__device__ __noinline__ uint4 odd_piece(const T* row, int V, int at) {
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int e = 0; e < 16 / static_cast<int>(sizeof(T)); ++e) {
+    uint32_t b = sizeof(T) == 2 ? 0xFF80u : 0xFF800000u;
+    if (at + e >= 0 && at + e < V) {
+      const uint32_t l = row[at + e];
+      if (!isnan(__uint_as_float(sizeof(T) == 2 ? l << 16 : l))) b = l;
+    }
+    if constexpr (sizeof(T) == 2) w[e / 2] |= b << (e % 2 * 16);
+    else w[e] = b;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One row's block. All members but v0, count and rank are the same in all threads of all its blocks.
 template <typename T>
 struct Row {
   static constexpr int kVec = 16 / sizeof(T);
   Shared& s;
-  const uint4* data;  // this block's vectors
-  int count, rank, blocks;
-  float top;          // the largest logit
-  uint32_t tau;       // kept: keys above tau, and the first `ties` tokens of key tau
+  const T* row;
+  int V, skew;            // the row begins `skew` values into a 16-byte piece
+  int v0, count;          // this block's pieces, from the one in which the row begins
+  int rank, blocks;
+  float top;              // the largest logit
+  float ch, cl, step;     // log2(e) / temperature as two floats; bins per unit
+  uint32_t tau;           // kept: keys above tau, and the first `ties` tokens of key tau
   uint32_t ties;
   uint64_t tie_weight;
+  bool listed;            // what may be kept of this block's tokens is in the list
 
   __device__ __forceinline__ void sync() const {
     __syncwarp();
@@ -179,51 +239,118 @@ struct Row {
       }
     }
   }
+  __device__ __forceinline__ static float most(const uint4& u) {  // NaN if there is one
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(u.x, u.y), max_nan_bf16x2(u.z, u.w));
+      return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    } else {
+      return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)), max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+    }
+  }
 
-  // vectors of this warp: [first, last), a run of neighbours, a warp's width at a time
+  __device__ __forceinline__ uint4 raw(int i) const {
+    // pieces that lie inside the row are read whole, its ends by the value
+    const int at = (v0 + i) * kVec - skew;
+    if (at >= 0 && at + kVec <= V) return __ldg(reinterpret_cast<const uint4*>(row + at));
+    return odd_piece(row, V, at);
+  }
+  __device__ __forceinline__ void clean(int i, uint4& u, float& m) const {
+    m = most(u);
+    if (isnan(m)) {
+      u = odd_piece(row, V, (v0 + i) * kVec - skew);
+      m = most(u);
+    }
+  }
+
+  // pieces of a warp: [first, last), a run of neighbours, a warp's width at a time
   __device__ __forceinline__ void segment(int warp, int& first, int& last) const {
-    const int per = ((count + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int warps = blockDim.x >> 5, per = ((count + warps - 1) / warps + 31) / 32 * 32;
     first = min(count, warp * per);
     last = min(count, first + per);
   }
-
+  // f(piece, its largest value) for this thread's pieces, four of them in flight
   template <typename F>
-  __device__ __forceinline__ void each(F&& f) const {
+  __device__ __forceinline__ void pieces(F&& f) const {
     int first, last;
     segment(threadIdx.x >> 5, first, last);
-    for (int i = first + (threadIdx.x & 31); i < last; i += 32) {
+    int i = first + (threadIdx.x & 31);
+    for (; i + 96 < last; i += 128) {
+      uint4 u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = raw(i + 32 * e);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float m;
+        clean(i + 32 * e, u[e], m);
+        f(u[e], m);
+      }
+    }
+    for (; i < last; i += 32) {
+      uint4 u = raw(i);
+      float m;
+      clean(i, u, m);
+      f(u, m);
+    }
+  }
+  // f(logit, key) for every token that may be kept
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    if (listed) {
+      for (int i = threadIdx.x; i < s.listed; i += blockDim.x) f(value_of(s.list[i]), s.list[i]);
+      return;
+    }
+    pieces([&](const uint4& u, float) {
       float v[kVec];
-      unpack(data[i], v);
+      unpack(u, v);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) f(v[e], key_of(v[e]));
-    }
+    });
+  }
+
+  // This block's tokens from `least` on, in the list; none is if they are too many.
+  __device__ __forceinline__ void gather(float least) {
+    if (threadIdx.x == 0) s.listed = 0;
+    __syncthreads();
+    pieces([&](const uint4& u, float m) {
+      if (!(m >= least) || m == -INFINITY) return;
+      float v[kVec];
+      unpack(u, v);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (v[e] >= least && v[e] > -INFINITY) {
+          const int at = atomicAdd(&s.listed, 1);
+          if (at < kList) s.list[at] = key_of(v[e]);
+        }
+    });
+    __syncthreads();
+    listed = s.listed <= kList;
   }
 
   __device__ __forceinline__ uint64_t weight(float l) const {
     if (l == top) return kOne;
     const float d = top - l;
-    const float p = d * s.ch;
+    const float p = d * ch;
     if (!(p < 46.0f)) return 0;
     // what d and p lost by rounding
     const float back = top - d;
     const float dl = (top - (d + back)) + (back - l);
-    float e = fmaf(d, s.ch, -p);
-    e = fmaf(d, s.cl, e);
-    e = fmaf(dl, s.ch, e);
-    const float magic = 0x1.8p11f;  // rounds to multiples of 2^-12
+    float e = fmaf(d, ch, -p);
+    e = fmaf(d, cl, e);
+    e = fmaf(dl, ch, e);
+    const float magic = 0x1.8p13f;  // rounds to multiples of 2^-10
     const float k = p + magic;
     const int steps = static_cast<int>(__float_as_uint(k) - __float_as_uint(magic));
     const float z = (p - (k - magic)) + e;
-    // 2^-z - 1, |z| <= 2^-13 and a bit: the cubic term is below 2^-43
+    // 2^-z - 1, |z| <= 2^-11 and a bit: the cubic term is below 2^-37
     const float x = z * fmaf(z, 0.240226507f, -0.693147181f);
-    const int part = __float2int_rn(x * 0x1p44f);
-    const uint64_t t = s.power[steps & 4095];
-    const int64_t w = static_cast<int64_t>(t) + ((static_cast<int64_t>(static_cast<int32_t>(t >> 13)) * part) >> 31);
-    return static_cast<uint64_t>(w) >> (steps >> 12);
+    const int part = __float2int_rn(x * 0x1p42f);
+    const uint64_t t = s.power[steps & ((1 << kStepBits) - 1)];
+    const int64_t w = static_cast<int64_t>(t) + ((static_cast<int64_t>(static_cast<int32_t>(t >> 13)) * part) >> 29);
+    return static_cast<uint64_t>(w) >> (steps >> kStepBits);
   }
 
   __device__ __forceinline__ int bin_of(float l) const {
-    return min(kBins - 1, static_cast<int>(fminf((top - l) * s.step, 4096.0f)));
+    return min(kBins - 1, static_cast<int>(fminf((top - l) * step, 4096.0f)));
   }
 
   template <bool WEIGHTS>
@@ -241,8 +368,16 @@ struct Row {
   // Adds the blocks' histograms up in every block's `total` and clears them.
   __device__ __forceinline__ void meet() const {
     sync();
+    if (blocks == 1) {
+      for (int i = threadIdx.x; i < kBins; i += blockDim.x) {
+        s.total[i] = static_cast<uint64_t>(s.hi[i]) << 32 | s.lo[i];
+        s.lo[i] = s.hi[i] = 0;
+      }
+      __syncthreads();
+      return;
+    }
     const int slice = kBins / blocks;
-    for (int i = rank * slice + threadIdx.x; i < (rank + 1) * slice; i += kThreads) {
+    for (int i = rank * slice + threadIdx.x; i < (rank + 1) * slice; i += blockDim.x) {
       uint64_t sum = 0;
       for (int p = 0; p < blocks; ++p)
         sum += (static_cast<uint64_t>(load_cluster(cluster_address(&s.hi[i], p))) << 32) +
@@ -250,50 +385,166 @@ struct Row {
       for (int p = 0; p < blocks; ++p) store_cluster(cluster_address(&s.total[i], p), sum);
     }
     sync();
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += blockDim.x) s.lo[i] = s.hi[i] = 0;
   }
 
   // The first bin at which the cumulated total reaches the target (that number, or the part `p` of everything,
   // at least 1): bin, before and target in shared memory; bin -1 where it is never reached.
-  __device__ __forceinline__ void reach(uint64_t target, const float* p) const {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t a = s.total[2 * threadIdx.x], b = s.total[2 * threadIdx.x + 1];
-    const uint64_t upto = warp_scan(a + b, lane);
+  __device__ __forceinline__ void reach(uint64_t target, const float* p, bool others) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, own = kBins / blockDim.x;
+    uint64_t mine = 0;
+    for (int i = 0; i < own; ++i) mine += s.total[own * threadIdx.x + i];
+    const uint64_t upto = warp_scan(mine, lane);
     if (lane == 31) s.warp_a[warp] = upto;
     if (threadIdx.x == 0) s.bin = -1;
     __syncthreads();
-    const uint64_t warps = warp_scan(s.warp_a[lane], lane);
-    const uint64_t all = __shfl_sync(0xffffffffu, warps, 31);
-    const uint64_t prior = __shfl_sync(0xffffffffu, warps, warp == 0 ? 0 : warp - 1);
-    if (p) {
-      bool rest;
-      target = part_of(*p, all, rest);
-      target += rest;
-      if (target == 0) target = 1;
+    const uint64_t sums = warp_scan(lane < warps ? s.warp_a[lane] : 0, lane);
+    const uint64_t all = __shfl_sync(0xffffffffu, sums, 31);
+    const uint64_t prior = __shfl_sync(0xffffffffu, sums, warp == 0 ? 0 : warp - 1);
+    if (p) target = front_of(*p, all, others);
+    uint64_t x = (warp == 0 ? 0 : prior) + upto - mine;
+    if (x < target && target <= x + mine) {
+      int bin = own * threadIdx.x;
+      while (x + s.total[bin] < target) x += s.total[bin++];
+      s.bin = bin, s.before = x, s.target = target;
     }
-    const uint64_t x = (warp == 0 ? 0 : prior) + upto - (a + b);
-    if (x < target && target <= x + a) {
-      s.bin = 2 * threadIdx.x, s.before = x, s.target = target;
-    } else if (x + a < target && target <= x + a + b) {
-      s.bin = 2 * threadIdx.x + 1, s.before = x + a, s.target = target;
+    __syncthreads();
+  }
+  // The least whole number that is at least p times `all`, and 1. Where there are `others` than the largest logit, their
+  // weights were rounded down, the true sum is a little more than `all`, and a product without a rest is passed.
+  __device__ __forceinline__ static uint64_t front_of(float p, uint64_t all, bool others) {
+    bool rest;
+    const uint64_t part = part_of(p, all, rest);
+    return part + (rest || others) ? part + (rest || others) : 1;
+  }
+
+  // Counts this thread's pieces' values; rare ones go to the list. `far`: the largest value of magnitude 2^7 or more.
+  __device__ __forceinline__ void count_values(const uint4& u, float& far) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu;
+      const int bin = value_bin(b);
+      if (bin >= 0) {
+        atomicAdd(&s.count[bin], 1u);
+      } else if ((b & 0x7FFFu) < kSmallest) {
+        const int at = atomicAdd(&s.listed, 1);
+        if (at < kList) s.list[at] = b << 16;
+      } else {
+        far = fmaxf(far, __uint_as_float(b << 16));
+      }
+    }
+  }
+
+  // The first value's bin at which the cumulated count (or weight) of the tokens kept so far, those before `end` and
+  // `end_count` of it, reaches the target, as reach() does; the rare ones count with zero. `far`: there are tokens that
+  // were not counted.
+  template <bool WEIGHTS>
+  __device__ __forceinline__ void reach_value(uint64_t target, const float* p, int end, uint32_t end_count, uint32_t rares,
+                                              uint64_t rare_weight, bool far) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, own = kValues / blockDim.x;
+    const auto amount = [&](int bin) -> uint64_t {
+      if (bin > end) return 0;
+      const uint64_t w = s.weight[bin];
+      const uint32_t n = bin == end ? end_count : s.counts[bin];
+      uint64_t x = WEIGHTS ? n * w : (w ? n : 0);
+      if (bin == kZeroBin && bin < end) x += WEIGHTS ? rare_weight : rare_weight ? rares : 0;
+      return x;
+    };
+    uint64_t mine = 0;
+    bool other = far && end == kValues;  // than the largest logit
+    for (int i = 0; i < own; ++i) {
+      const int bin = own * threadIdx.x + i;
+      mine += amount(bin);
+      other = other || (bin <= end && bin_value(bin) != top && (s.counts[bin] || (bin == kZeroBin && bin < end && rares)));
+    }
+    const uint64_t upto = warp_scan(mine, lane);
+    if (lane == 31) s.warp_a[warp] = upto;
+    if (threadIdx.x == 0) s.bin = -1;
+    other = __syncthreads_or(other);
+    const uint64_t sums = warp_scan(lane < warps ? s.warp_a[lane] : 0, lane);
+    const uint64_t all = __shfl_sync(0xffffffffu, sums, 31);
+    const uint64_t prior = __shfl_sync(0xffffffffu, sums, warp == 0 ? 0 : warp - 1);
+    if (p) target = front_of(*p, all, other);
+    uint64_t x = (warp == 0 ? 0 : prior) + upto - mine;
+    if (x < target && target <= x + mine) {
+      int bin = own * threadIdx.x;
+      while (x + amount(bin) < target) x += amount(bin++);
+      s.bin = bin, s.before = x, s.target = target;
     }
     __syncthreads();
   }
 
+  // top-k and top-p by the counts of values. False: the cut lies among the rare ones, and nothing was done.
+  __device__ __forceinline__ bool cut_values(uint32_t k, const float* p, bool far) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    uint64_t rare_weight = 0;
+    uint32_t rares = s.listed;
+    for (int i = threadIdx.x; i < s.listed; i += blockDim.x) rare_weight += weight(__uint_as_float(s.list[i]));
+    rare_weight = warp_sum(rare_weight);
+    if (lane == 0) s.warp_a[warp] = rare_weight;
+    __syncthreads();
+    rare_weight = warp_sum(lane < warps ? s.warp_a[lane] : 0);
+    if (blocks > 1) {
+      if (threadIdx.x < blocks) {
+        store_cluster(cluster_address(&s.peer_rare[rank], threadIdx.x), rare_weight);
+        store_cluster(cluster_address(&s.peer_rares[rank], threadIdx.x), rares);
+      }
+      sync();
+      rare_weight = 0, rares = 0;
+      for (int q = 0; q < blocks; ++q) rare_weight += s.peer_rare[q], rares += s.peer_rares[q];
+      const int slice = kValues / blocks;
+      for (int i = rank * slice + threadIdx.x; i < (rank + 1) * slice; i += blockDim.x) {
+        uint32_t sum = 0;
+        for (int q = 0; q < blocks; ++q) sum += load_cluster(cluster_address(&s.count[i], q));
+        for (int q = 0; q < blocks; ++q) store_cluster(cluster_address(&s.counts[i], q), sum);
+      }
+      sync();
+    } else {
+      for (int i = threadIdx.x; i < kValues; i += blockDim.x) s.counts[i] = s.count[i];
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < kValues; i += blockDim.x) s.count[i] = 0;
+    int end = kValues;
+    uint32_t end_count = 0;
+    if (k) {
+      reach_value<false>(k, nullptr, end, end_count, rares, rare_weight, far);
+      if (s.bin >= 0) end = s.bin, end_count = static_cast<uint32_t>(s.target - s.before);
+      if (end == kZeroBin && rares) return false;
+    }
+    if (p) {
+      __syncthreads();  // s.bin and its company are read
+      reach_value<true>(0, p, end, end_count, rares, rare_weight, far);
+      end = s.bin;
+      if (end == kZeroBin && rares) return false;
+      end_count = static_cast<uint32_t>((s.target - s.before + s.weight[end] - 1) / s.weight[end]);
+    }
+    if (end < kValues) tau = key_of(bin_value(end)), ties = end_count, tie_weight = s.weight[end];
+    return true;
+  }
+
   // Cuts the kept tokens to the shortest front part whose count or weight reaches the target.
   template <bool WEIGHTS>
-  __device__ void cut(uint64_t target, const float* p) {
+  __device__ __forceinline__ void cut(uint64_t target, const float* p) {
     const bool group = WEIGHTS && ties > 0;            // kept tokens of key tau,
     const bool mine = group && rank == 0 && threadIdx.x == 0;  // added by one thread
     const uint64_t group_weight = ties * tie_weight;
+    bool others = group && value_of(tau) != top;       // than the largest logit
     each([&](float l, uint32_t key) {
       if (key <= tau) return;
+      others = others || l != top;
       const uint64_t w = WEIGHTS ? weight(l) : 1;
       if (!WEIGHTS || w) add<WEIGHTS>(bin_of(l), w);
     });
     if (mine) add<WEIGHTS>(bin_of(value_of(tau)), group_weight);
+    if (WEIGHTS && p) {
+      others = __syncthreads_or(others);
+      if (blocks > 1 && threadIdx.x < blocks) store_cluster(cluster_address(&s.peer_others[rank], threadIdx.x), others ? 1u : 0u);
+    }
     meet();
-    reach(target, p);
+    if (WEIGHTS && p && blocks > 1)
+      for (int q = 0; q < blocks; ++q) others = others || s.peer_others[q];
+    reach(target, p, others);
     if (s.bin < 0) return;
     const int bin = s.bin;
     uint64_t left = s.target - s.before;
@@ -304,16 +555,19 @@ struct Row {
     if (mine && bin_of(value_of(tau)) == bin) low = min(low, tau), high = max(high, tau);
     low = __reduce_min_sync(0xffffffffu, low);
     high = __reduce_max_sync(0xffffffffu, high);
-    if ((threadIdx.x & 31) == 0) s.warp_b[threadIdx.x >> 5] = low, s.warp_c[threadIdx.x >> 5] = high;
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) s.warp_b[threadIdx.x >> 5] = low, s.warp_c[threadIdx.x >> 5] = high;
     __syncthreads();
-    low = __reduce_min_sync(0xffffffffu, s.warp_b[threadIdx.x & 31]);
-    high = __reduce_max_sync(0xffffffffu, s.warp_c[threadIdx.x & 31]);
-    if (threadIdx.x < blocks) {
-      store_cluster(cluster_address(&s.peer_low[rank], threadIdx.x), low);
-      store_cluster(cluster_address(&s.peer_high[rank], threadIdx.x), high);
+    low = __reduce_min_sync(0xffffffffu, lane < warps ? s.warp_b[lane] : 0xFFFFFFFFu);
+    high = __reduce_max_sync(0xffffffffu, lane < warps ? s.warp_c[lane] : 0);
+    if (blocks > 1) {
+      if (threadIdx.x < blocks) {
+        store_cluster(cluster_address(&s.peer_low[rank], threadIdx.x), low);
+        store_cluster(cluster_address(&s.peer_high[rank], threadIdx.x), high);
+      }
+      sync();
+      for (int q = 0; q < blocks; ++q) low = min(low, s.peer_low[q]), high = max(high, s.peer_high[q]);
     }
-    sync();
-    for (int q = 0; q < blocks; ++q) low = min(low, s.peer_low[q]), high = max(high, s.peer_high[q]);
     while (low < high) {
       const int shift = max(0, 32 - __clz(high - low) - 11);
       each([&](float l, uint32_t key) {
@@ -323,7 +577,7 @@ struct Row {
       });
       if (mine && tau >= low && tau <= high) add<WEIGHTS>(static_cast<int>((high - tau) >> shift), group_weight);
       meet();
-      reach(left, nullptr);
+      reach(left, nullptr, false);
       left -= s.before;
       high -= static_cast<uint32_t>(s.bin) << shift;
       const uint32_t span = (1u << shift) - 1u;
@@ -332,153 +586,200 @@ struct Row {
     tau = low;
     tie_weight = weight(value_of(tau));
     ties = static_cast<uint32_t>(WEIGHTS ? (left + tie_weight - 1) / max(tie_weight, uint64_t(1)) : left);
+    __syncthreads();
   }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(32 * kMaxWarps, 2) sample_kernel(SampleArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
-  uint4* const data = reinterpret_cast<uint4*>(raw + sizeof(Shared));
   constexpr int kVec = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t b = blockIdx.x / a.blocks;
   const int rank = static_cast<int>(blockIdx.x % a.blocks);
-  for (int i = threadIdx.x; i < 2048; i += kThreads)
+  for (int i = threadIdx.x; i < 1 << (kStepBits - 1); i += blockDim.x)
     reinterpret_cast<uint4*>(s.power)[i] = reinterpret_cast<const uint4*>(kPowers.t)[i];
-  for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
+  for (int i = threadIdx.x; i < kBins; i += blockDim.x) s.lo[i] = s.hi[i] = 0;
+  if (threadIdx.x == 0) s.listed = 0;
   pdl_wait();
   pdl_trigger();
-  const float t = a.temperature ? a.temperature[b] : 1.0f;
-  const bool greedy = !(t >= 0x1p-100f);
-  if (threadIdx.x == kThreads - 1) {
-    const double c = 1.4426950408889634074 / fmin(static_cast<double>(t), 0x1p100);
-    s.ch = static_cast<float>(c);
-    s.cl = static_cast<float>(c - s.ch);
-    s.step = s.ch * 44.3614196f;  // 64 ln 2: 64 bins where the weight falls by e
-    const float q = a.min_p ? a.min_p[b] : 0.0f;
-    s.below = q > 0.0f ? fmin(static_cast<double>(t), 0x1p100) * log(static_cast<double>(q)) : -INFINITY;
-  }
-  // This block's part of the row, from the 16-byte piece in which the row begins: places outside the row and
-  // NaN become -infinity. Vectors that lie inside are read whole, the row's ends by the value.
   const T* const row = static_cast<const T*>(a.logits) + b * a.ld;
   const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T) % kVec);
-  const int vectors = (skew + a.V + kVec - 1) / kVec, per = (vectors + a.blocks - 1) / a.blocks;
-  const int v0 = min(vectors, rank * per), count = min(vectors, v0 + per) - v0;
-  uint64_t best = 0;  // key, then the lower index
-  for (int i = threadIdx.x; i < count; i += kThreads) {
-    const int64_t at = static_cast<int64_t>(v0 + i) * kVec - skew;  // the vector's first token
-    uint4 u;
-    if (at >= 0 && at + kVec <= a.V) {
-      u = __ldg(reinterpret_cast<const uint4*>(row + at));
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 2) {
-          const uint32_t l = at + 2 * e >= 0 && at + 2 * e < a.V ? row[at + 2 * e] : 0xFF80u;
-          const uint32_t h = at + 2 * e + 1 >= 0 && at + 2 * e + 1 < a.V ? row[at + 2 * e + 1] : 0xFF80u;
-          w[e] = l | h << 16;
-        } else {
-          w[e] = at + e >= 0 && at + e < a.V ? row[at + e] : 0xFF800000u;
-        }
-      }
-      u = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    float v[kVec];
-    Row<T>::unpack(u, v);
-    bool nan = false;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      if (isnan(v[e])) {
-        nan = true;
-        v[e] = -INFINITY;
-      }
-      const uint64_t k = static_cast<uint64_t>(key_of(v[e])) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(at + e));
-      best = k > best ? k : best;
-    }
-    if (nan) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 2)
-          w[e] = __float_as_uint(v[2 * e]) >> 16 | (__float_as_uint(v[2 * e + 1]) & 0xFFFF0000u);
-        else
-          w[e] = __float_as_uint(v[e]);
-      }
-      u = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    data[i] = u;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t k = __shfl_xor_sync(0xffffffffu, best, o);
-    best = k > best ? k : best;
-  }
-  if (lane == 0) s.warp_a[warp] = best;
+  const int all = (skew + a.V + kVec - 1) / kVec, per = (all + a.blocks - 1) / a.blocks;
+  const int v0 = min(all, rank * per), count = min(all, v0 + per) - v0;
+  Row<T> r = {s, row, a.V, skew, v0, count, rank, a.blocks, 0.0f, 0.0f, 0.0f, 0.0f, kNone, 0, 0, false};
+  const float t = a.temperature ? a.temperature[b] : 1.0f;
+  const int k = a.top_k ? a.top_k[b] : 0;
+  const float p = a.top_p ? a.top_p[b] : 1.0f, q = a.min_p ? a.min_p[b] : 0.0f;
+  float u = a.uniform[b];
+  const bool top_k = k > 0 && k < a.V, top_p = p < 1.0f, greedy = !(t >= 0x1p-100f);
+  float own = -INFINITY;  // this thread's largest logit
+  float away = -INFINITY;
+  const bool counted = sizeof(T) == 2 && !greedy && (top_k || top_p);
+  if (counted) __syncthreads();  // the counts are 0
+  r.pieces([&](const uint4& w, float m) {
+    own = fmaxf(own, m);
+    if constexpr (sizeof(T) == 2)
+      if (counted) r.count_values(w, away);
+  });
+  uint32_t best = __reduce_max_sync(0xffffffffu, key_of(own)), far = __reduce_max_sync(0xffffffffu, key_of(away));
+  if (lane == 0) s.warp_b[warp] = best, s.warp_c[warp] = far;
   __syncthreads();
-  Row<T> r = {s, data, count, rank, a.blocks, 0.0f, kNone, 0, 0};
-  if (warp == 0) {
-    best = s.warp_a[lane];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t k = __shfl_xor_sync(0xffffffffu, best, o);
-      best = k > best ? k : best;
+  best = __reduce_max_sync(0xffffffffu, lane < warps ? s.warp_b[lane] : 0);
+  far = __reduce_max_sync(0xffffffffu, lane < warps ? s.warp_c[lane] : 0);
+  if (s.listed > kList) far = 0xFFFFFFFFu;  // too many rare ones
+  if (a.blocks > 1) {
+    if (threadIdx.x < a.blocks) {
+      store_cluster(cluster_address(&s.peer_top[rank], threadIdx.x), best);
+      store_cluster(cluster_address(&s.peer_far[rank], threadIdx.x), far);
     }
-    if (lane < a.blocks) store_cluster(cluster_address(&s.peer_best[rank], lane), best);
+    r.sync();
+    for (int i = 0; i < a.blocks; ++i) best = max(best, s.peer_top[i]), far = max(far, s.peer_far[i]);
+  } else {
+    __syncthreads();
   }
-  r.sync();
-  best = 0;
-  for (int q = 0; q < a.blocks; ++q) best = s.peer_best[q] > best ? s.peer_best[q] : best;
-  const uint32_t top_key = static_cast<uint32_t>(best >> 32);
-  if (top_key <= kNone || greedy) {
-    if (rank == 0 && threadIdx.x == 0)
-      a.tokens[b] = top_key <= kNone ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
+  if (best <= kNone) {
+    if (rank == 0 && threadIdx.x == 0) a.tokens[b] = -1;
     return;
   }
-  r.top = value_of(top_key);
-
-  const int k = a.top_k ? a.top_k[b] : 0;
-  if (k > 0 && k < a.V) r.template cut<false>(static_cast<uint64_t>(k), nullptr);
-  const float p = a.top_p ? fmaxf(a.top_p[b], 0.0f) : 1.0f;
-  if (a.top_p && a.top_p[b] < 1.0f) r.template cut<true>(0, &p);
-  if (s.below > -INFINITY) {
-    const double least = fmin(static_cast<double>(r.top) + s.below, static_cast<double>(r.top));
-    const uint32_t key = key_of(__double2float_ru(least));
-    if (key > r.tau) r.tau = key - 1, r.ties = 0;
+  r.top = value_of(best);
+  uint64_t least = 0;  // weight of a kept token
+  bool valued = false;  // the weights of values are there
+  if (greedy) {
+    r.tau = best, r.ties = 1, r.tie_weight = kOne;
+  } else {
+    const float limited = fminf(t, 0x1p100f);
+    const float high = 1.44269502f, low = 1.92596299e-8f;  // log2(e)
+    r.ch = high / limited;
+    r.cl = (fmaf(-r.ch, limited, high) + low) / limited;
+    r.step = r.ch * 44.3614196f;  // 64 ln 2: 64 bins where the weight falls by e
+    // a bound is a little lower than its arithmetic in 32 bits says
+    const auto below = [&](float units, float scale) { return r.top - units / scale * 1.0001f - fabsf(r.top) * 0x1p-20f; };
+    const float part = fmaxf(p, 0.0f);
+    bool cut = false;
+    if constexpr (sizeof(T) == 2) {
+      // values of magnitude 2^7 and more are not counted: none may have a weight
+      valued = isfinite(r.top) && far != 0xFFFFFFFFu && !((r.top - value_of(far)) * r.ch < 46.0f);
+      if (valued) {
+        for (int i = threadIdx.x; i < kValues; i += blockDim.x) s.weight[i] = bin_value(i) > r.top ? 0 : r.weight(bin_value(i));
+        __syncthreads();
+      }
+      if (counted && valued) {
+        cut = r.cut_values(top_k ? k : 0, top_p ? &part : nullptr, far > kNone);
+      } else if (counted) {
+        for (int i = threadIdx.x; i < kValues; i += blockDim.x) s.count[i] = 0;
+      }
+      if (counted) __syncthreads();
+    }
+    if (!cut) {
+      if (top_k) {
+        // a row's blocks have like numbers of tokens, and agree on what they do together
+        if (per * kVec <= kList) {
+          r.gather(-INFINITY);
+        } else if (k <= a.blocks * static_cast<int>(blockDim.x) / 2) {
+          if (own > -INFINITY) r.template add<false>(r.bin_of(own), 1);
+          r.meet();
+          r.reach(k, nullptr, false);
+          const int bin = s.bin;
+          if (bin >= 0 && bin < kBins - 1 && isfinite(r.top)) r.gather(below(bin + 1.0f, r.step));
+        }
+        r.template cut<false>(k, nullptr);
+      }
+      if (top_p) {
+        uint64_t sum = 0, front = 0;
+        if (top_k || per * kVec <= kList) {
+          if (!top_k) r.gather(-INFINITY);
+        } else {
+          bool others = false;
+          r.pieces([&](const uint4& w, float m) {
+            others = others || (m > -INFINITY && m < r.top);
+            if (!((r.top - m) * r.ch < 46.0f) && m != r.top) return;
+            float v[kVec];
+            Row<T>::unpack(w, v);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+              sum += r.weight(v[e]);
+              others = others || (v[e] > -INFINITY && v[e] < r.top);
+            }
+          });
+          sum = warp_sum(sum);
+          if (lane == 0) s.warp_a[warp] = sum;
+          others = __syncthreads_or(others);
+          sum = warp_sum(lane < warps ? s.warp_a[lane] : 0);
+          if (a.blocks > 1) {
+            if (threadIdx.x < a.blocks) {
+              store_cluster(cluster_address(&s.peer_total[rank], threadIdx.x), sum);
+              store_cluster(cluster_address(&s.peer_below[rank], threadIdx.x), others ? 1u : 0u);
+            }
+            r.sync();
+            sum = 0;
+            for (int i = 0; i < a.blocks; ++i) sum += s.peer_total[i], others = others || s.peer_below[i];
+          } else {
+            __syncthreads();
+          }
+          const float bits = __log2f(__ull2float_rn(sum) * 0x1p-44f * a.V / (1.0f - part)) + 0.01f;
+          if (isfinite(r.top)) r.gather(below(bits, r.ch));
+          front = Row<T>::front_of(part, sum, others);
+        }
+        r.template cut<true>(front, front ? nullptr : &part);
+      }
+    }
+    if (q > 0.0f) {
+      bool rest;
+      const float kept = fminf(q, 1.0f);
+      least = kept == 1.0f ? kOne : part_of(kept, kOne, rest) + rest;
+      if (r.tie_weight < least) r.ties = 0;
+    }
   }
 
   // the kept weight of every warp's segment, without the tokens of key tau; how many of these it has
+  const float last_kept = value_of(r.tau);
   uint64_t sum = 0;
   uint32_t same = 0;
-  r.each([&](float l, uint32_t key) {
-    if (key > r.tau) sum += r.weight(l);
-    same += key == r.tau;
+  r.pieces([&](const uint4& w, float m) {
+    if (!(m >= last_kept) || m == -INFINITY) return;
+    float v[kVec];
+    Row<T>::unpack(w, v);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      if (v[e] > last_kept) {
+        uint64_t x;
+        const int bin = sizeof(T) == 2 && valued ? value_bin(__float_as_uint(v[e]) >> 16) : -1;
+        if (bin >= 0) x = s.weight[bin];
+        else x = r.weight(v[e]);
+        if (x >= least) sum += x;
+      }
+      same += v[e] == last_kept;
+    }
   });
   sum = warp_sum(sum);
   same = warp_sum(same);
-  __syncthreads();
   if (lane == 0) s.warp_a[warp] = sum, s.warp_b[warp] = same;
   __syncthreads();
-  sum = s.warp_a[lane], same = s.warp_b[lane];
+  sum = lane < warps ? s.warp_a[lane] : 0, same = lane < warps ? s.warp_b[lane] : 0;
   const uint64_t block_sum = warp_sum(sum);
   const uint32_t block_same = warp_sum(same);
-  if (threadIdx.x < a.blocks) {
-    store_cluster(cluster_address(&s.peer_sum[rank], threadIdx.x), block_sum);
-    store_cluster(cluster_address(&s.peer_same[rank], threadIdx.x), block_same);
-  }
-  r.sync();
-  if (warp != 0) return;
   uint64_t total = 0, prior = 0;
   uint32_t seen = 0, seen_prior = 0;
-  for (int q = 0; q < a.blocks; ++q) {
-    if (q == rank) prior = total, seen_prior = seen;
-    const uint32_t here = min(s.peer_same[q], r.ties - min(r.ties, seen));
-    seen += here;
-    total += s.peer_sum[q] + here * r.tie_weight;
+  if (a.blocks > 1) {
+    if (threadIdx.x < a.blocks) {
+      store_cluster(cluster_address(&s.peer_sum[rank], threadIdx.x), block_sum);
+      store_cluster(cluster_address(&s.peer_same[rank], threadIdx.x), block_same);
+    }
+    r.sync();
+    if (warp != 0) return;
+    for (int i = 0; i < a.blocks; ++i) {
+      if (i == rank) prior = total, seen_prior = seen;
+      const uint32_t here = min(s.peer_same[i], r.ties - min(r.ties, seen));
+      seen += here;
+      total += s.peer_sum[i] + here * r.tie_weight;
+    }
+  } else {
+    if (warp != 0) return;
+    total = block_sum + min(block_same, r.ties) * r.tie_weight;
   }
   bool rest;
-  float u = a.uniform[b];
   u = u >= 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f;
   uint64_t target = part_of(u, total, rest) + 1;
   if (target <= prior) return;
@@ -498,26 +799,30 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a) {
   r.segment(w, first, last);
   for (int i0 = first; i0 < last; i0 += 32) {
     const int i = i0 + lane;
-    float v[kVec];
-    uint32_t n = 0;
+    float v[kVec], m = -INFINITY;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) v[e] = -INFINITY;
-    if (i < last) Row<T>::unpack(data[i], v);
+    if (i < last) {
+      uint4 piece = r.raw(i);
+      r.clean(i, piece, m);
+      Row<T>::unpack(piece, v);
+    }
+    uint32_t n = 0;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) n += key_of(v[e]) == r.tau;
+    for (int e = 0; e < kVec; ++e) n += v[e] == last_kept;
     const uint32_t n_upto = warp_scan(n, lane);
     uint32_t free = free_ties - min(free_ties, n_upto - n);
-    uint64_t part[kVec], own = 0;
+    uint64_t part[kVec], whole = 0;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-      const uint32_t key = key_of(v[e]);
-      part[e] = key > r.tau ? r.weight(v[e]) : 0;
-      if (key == r.tau && free > 0) part[e] = r.tie_weight, --free;
-      own += part[e];
+      part[e] = v[e] > last_kept ? r.weight(v[e]) : 0;
+      if (part[e] < least) part[e] = 0;
+      if (v[e] == last_kept && free > 0) part[e] = r.tie_weight, --free;
+      whole += part[e];
     }
-    const uint64_t own_upto = warp_scan(own, lane);
-    if (own_upto >= target && own_upto - own < target) {
-      uint64_t x = own_upto - own;
+    const uint64_t whole_upto = warp_scan(whole, lane);
+    if (whole_upto >= target && whole_upto - whole < target) {
+      uint64_t x = whole_upto - whole;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         if (x < target && target <= x + part[e])
@@ -525,30 +830,26 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(SampleArgs a) {
         x += part[e];
       }
     }
-    const uint64_t all = __shfl_sync(0xffffffffu, own_upto, 31);
-    if (all >= target) return;
-    target -= all;
+    const uint64_t sums = __shfl_sync(0xffffffffu, whole_upto, 31);
+    if (sums >= target) return;
+    target -= sums;
     free_ties -= min(free_ties, __shfl_sync(0xffffffffu, n_upto, 31));
   }
 }
 
-// Blocks of a row: enough that its part fits shared memory, and more while blocks are fewer than SMs
-// and parts longer than 8192 tokens.
-int blocks_of(int B, int V, int size) {
+// Blocks of a row: more while they all fit the SMs twice and their parts are longer than 4096 tokens.
+int blocks_of(int B, int V) {
   int n = 1;
-  while (n < kMaxBlocks && ((static_cast<int64_t>(V) + 8) * size > n * int64_t(144 << 10) ||
-                            (static_cast<int64_t>(B) * n * 2 <= num_sms() && V > 8192 * n)))
-    n *= 2;
+  while (n < kMaxBlocks && static_cast<int64_t>(B) * n * 2 <= 2 * num_sms() && V > 4096 * n) n *= 2;
   return n;
 }
 
 template <typename T>
 moe_status_t launch_sample(SampleArgs a, int B, cudaStream_t s) {
-  constexpr int kVec = 16 / sizeof(T);
-  a.blocks = blocks_of(B, a.V, sizeof(T));
-  const size_t smem = sizeof(Shared) + static_cast<size_t>((a.V + 2 * kVec - 2) / kVec / a.blocks + 1) * 16;
-  MOE_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
-  return launch_clusters(sample_kernel<T>, a.blocks, dim3(static_cast<unsigned>(B) * a.blocks), dim3(kThreads), smem, s, a);
+  a.blocks = blocks_of(B, a.V);
+  const int threads = a.V / a.blocks > 2048 ? 32 * kMaxWarps : 256;
+  MOE_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared)));
+  return launch_clusters(sample_kernel<T>, a.blocks, dim3(static_cast<unsigned>(B) * a.blocks), dim3(threads), sizeof(Shared), s, a);
 }
 
 }  // namespace

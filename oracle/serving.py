@@ -3,6 +3,8 @@ matrix in scaled blocks, rotary positions, and sampling.
 """
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
 
 from . import formats as F
@@ -58,6 +60,26 @@ def rotary(x, positions, inv_freq, axes=None, adjacent: bool = False):
     return out, size, angle
 
 
+def _front(w, part: float) -> int:
+    """How many of the descending weights reach that part of their sum. Near a border the float64 sums say nothing (two equal
+    weights and a 1e-20 make 2.0): there, in rational numbers, a weight that underflowed counting as less than any."""
+    sums = np.cumsum(w)
+    reached = sums >= part * sums[-1]
+    j = int(np.argmax(reached))
+    near = np.flatnonzero(np.abs(sums - part * sums[-1]) <= 1e-9 * sums[-1])
+    if not len(near):
+        return j + 1
+    exact = [Fraction(float(v)) if v > 0 else Fraction(1, 10 ** 400) for v in w]
+    target = Fraction(part) * sum(exact)
+    first = int(near[0])
+    upto = sum(exact[:first])
+    while True:
+        upto += exact[first]
+        first += 1
+        if upto >= target or first == len(exact):
+            return first
+
+
 def sample(logits, uniform: float, temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0) -> int:
     """One row's token, by the filters as they are defined on the sorted tokens."""
     l = np.asarray(logits, np.float64)
@@ -74,8 +96,7 @@ def sample(logits, uniform: float, temperature: float = 1.0, top_k: int = 0, top
     w = np.exp(z)
     n = len(order) if top_k <= 0 else min(top_k, len(order))
     if top_p < 1.0:
-        sums = np.cumsum(w[:n])
-        n = 1 + next(j for j in range(n) if sums[j] >= max(top_p, 0.0) * sums[-1])
+        n = _front(w[:n], max(float(top_p), 0.0))
     if min_p > 0:
         n = max(1, sum(1 for j in range(n) if w[j] >= min_p or z[j] == 0.0))
     kept = sorted(zip(order[:n], w[:n]))

@@ -422,6 +422,28 @@ def test_sample_masked_and_infinite_logits():
                 assert sample(rows, [u] * len(rows), dtype, **kw) == want, (kw, u)
 
 
+@pytest.mark.parametrize("V", [900, 30000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample_logits_of_any_size(V, dtype):
+    """Logits so near to zero, so large or so far apart that none of a fast way's assumptions holds, and mixtures."""
+    r = np.random.default_rng(V)
+    base = r.normal(size=(8, V))
+    tiny, some = base * 1e-3, r.random((8, V)) < 0.02
+    kinds = [tiny, base * 1e-6, base * 60, base * 1e4, base * 1e30, np.where(some, base, tiny), np.where(some, tiny, base), np.where(some, base * 200, base),
+             np.where(some, -1e4, base), np.where(some, -np.inf, tiny), base - 100, base + 127.5, -np.abs(base) * 1e-3, np.where(some, 0.0, tiny),
+             np.where(some, 0.0, base * 1e-40)]
+    u = r.random(8).astype(np.float32)
+    for x in kinds:
+        x = torch.from_numpy(x.astype(np.float32)).to(dtype)
+        for kw in ({}, dict(top_k=V // 20), dict(top_p=0.7), dict(top_k=V // 3, top_p=0.9, min_p=0.05), dict(temperature=0.01, top_k=30, top_p=0.8),
+                   dict(temperature=50.0, top_p=0.5)):
+            kw = {n: np.full(8, v, np.int32 if n == "top_k" else np.float32) for n, v in kw.items()}
+            got = pkg.sample_tokens(x.to(DEV), up(u), **{n: up(v) for n, v in kw.items()}).tolist()
+            some_rows = range(8) if V < 1000 else (0, 5)
+            host = x.float().numpy()
+            assert [got[b] for b in some_rows] == [S.sample(host[b], u[b], **{n: v[b] for n, v in kw.items()}) for b in some_rows], kw
+
+
 def test_sample_settings_outside_their_range():
     r = np.random.default_rng(8)
     rows = [r.normal(size=50).astype(np.float32)] * 6

@@ -71,6 +71,9 @@ def test_sampling_by_hand():
     assert S.sample(l, 0.999, top_p=0.0) == 1
     # of the front three, 2 / (2 + 1 / e) = 0.8446 of the weight lies on the first two
     assert S.sample(l, 0.45, top_k=3, top_p=0.84) == 1 and S.sample(l, 0.45, top_k=3, top_p=0.85) == 2
+    # two equal weights are half of the sum each only if nothing else has any
+    assert S.sample([5.0, 5.0, -np.inf], 0.9, top_p=0.5) == 0 and S.sample([5.0, 5.0, -60.0], 0.9, top_p=0.5) == 1
+    assert S.sample([5.0, 5.0, -2000.0], 0.9, top_p=0.5) == 1
     assert S.sample(l, 0.0, min_p=0.3) == 1 and S.sample(l, 0.0, min_p=0.1) == 0
     assert S.sample(l, 0.0, min_p=5.0) == 1 and S.sample(l, 0.999, min_p=5.0) == 3
     assert S.sample([-np.inf, np.nan], 0.5) == -1
