@@ -32,7 +32,7 @@ namespace moe {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kMaxWarps = 16;
+constexpr int kThreads = 512, kWarps = 16;
 constexpr int kMaxBlocks = 8;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kList = 4096;
@@ -264,7 +264,7 @@ struct Row {
 
   // pieces of a warp: [first, last), a run of neighbours, a warp's width at a time
   __device__ __forceinline__ void segment(int warp, int& first, int& last) const {
-    const int warps = blockDim.x >> 5, per = ((count + warps - 1) / warps + 31) / 32 * 32;
+    const int per = ((count + kWarps - 1) / kWarps + 31) / 32 * 32;
     first = min(count, warp * per);
     last = min(count, first + per);
   }
@@ -296,7 +296,7 @@ struct Row {
   template <typename F>
   __device__ __forceinline__ void each(F&& f) const {
     if (listed) {
-      for (int i = threadIdx.x; i < s.listed; i += blockDim.x) f(value_of(s.list[i]), s.list[i]);
+      for (int i = threadIdx.x; i < s.listed; i += kThreads) f(value_of(s.list[i]), s.list[i]);
       return;
     }
     pieces([&](const uint4& u, float) {
@@ -369,7 +369,7 @@ struct Row {
   __device__ __forceinline__ void meet() const {
     sync();
     if (blocks == 1) {
-      for (int i = threadIdx.x; i < kBins; i += blockDim.x) {
+      for (int i = threadIdx.x; i < kBins; i += kThreads) {
         s.total[i] = static_cast<uint64_t>(s.hi[i]) << 32 | s.lo[i];
         s.lo[i] = s.hi[i] = 0;
       }
@@ -377,7 +377,7 @@ struct Row {
       return;
     }
     const int slice = kBins / blocks;
-    for (int i = rank * slice + threadIdx.x; i < (rank + 1) * slice; i += blockDim.x) {
+    for (int i = rank * slice + threadIdx.x; i < (rank + 1) * slice; i += kThreads) {
       uint64_t sum = 0;
       for (int p = 0; p < blocks; ++p)
         sum += (static_cast<uint64_t>(load_cluster(cluster_address(&s.hi[i], p))) << 32) +
@@ -385,20 +385,21 @@ struct Row {
       for (int p = 0; p < blocks; ++p) store_cluster(cluster_address(&s.total[i], p), sum);
     }
     sync();
-    for (int i = threadIdx.x; i < kBins; i += blockDim.x) s.lo[i] = s.hi[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
   }
 
   // The first bin at which the cumulated total reaches the target (that number, or the part `p` of everything,
   // at least 1): bin, before and target in shared memory; bin -1 where it is never reached.
   __device__ __forceinline__ void reach(uint64_t target, const float* p, bool others) const {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, own = kBins / blockDim.x;
+    constexpr int own = kBins / kThreads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t mine = 0;
     for (int i = 0; i < own; ++i) mine += s.total[own * threadIdx.x + i];
     const uint64_t upto = warp_scan(mine, lane);
     if (lane == 31) s.warp_a[warp] = upto;
     if (threadIdx.x == 0) s.bin = -1;
     __syncthreads();
-    const uint64_t sums = warp_scan(lane < warps ? s.warp_a[lane] : 0, lane);
+    const uint64_t sums = warp_scan(lane < kWarps ? s.warp_a[lane] : 0, lane);
     const uint64_t all = __shfl_sync(0xffffffffu, sums, 31);
     const uint64_t prior = __shfl_sync(0xffffffffu, sums, warp == 0 ? 0 : warp - 1);
     if (p) target = front_of(*p, all, others);
@@ -436,55 +437,45 @@ struct Row {
     }
   }
 
-  // The first value's bin at which the cumulated count (or weight) of the tokens kept so far, those before `end` and
-  // `end_count` of it, reaches the target, as reach() does; the rare ones count with zero. `far`: there are tokens that
-  // were not counted.
-  template <bool WEIGHTS>
-  __device__ __forceinline__ void reach_value(uint64_t target, const float* p, int end, uint32_t end_count, uint32_t rares,
-                                              uint64_t rare_weight, bool far) const {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, own = kValues / blockDim.x;
-    const auto amount = [&](int bin) -> uint64_t {
-      if (bin > end) return 0;
-      const uint64_t w = s.weight[bin];
-      const uint32_t n = bin == end ? end_count : s.counts[bin];
-      uint64_t x = WEIGHTS ? n * w : (w ? n : 0);
-      if (bin == kZeroBin && bin < end) x += WEIGHTS ? rare_weight : rare_weight ? rares : 0;
-      return x;
-    };
+  static constexpr int kOwn = kValues / kThreads;  // neighbouring bins of a thread
+
+  // The first of all threads' amounts, in order, at which their sum reaches the target (that number, or the part `p` of
+  // everything), as reach() finds bins.
+  __device__ __forceinline__ void reach_value(const uint64_t (&part)[kOwn], uint64_t target, const float* p, bool other) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t mine = 0;
-    bool other = far && end == kValues;  // than the largest logit
-    for (int i = 0; i < own; ++i) {
-      const int bin = own * threadIdx.x + i;
-      mine += amount(bin);
-      other = other || (bin <= end && bin_value(bin) != top && (s.counts[bin] || (bin == kZeroBin && bin < end && rares)));
-    }
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) mine += part[i];
     const uint64_t upto = warp_scan(mine, lane);
     if (lane == 31) s.warp_a[warp] = upto;
     if (threadIdx.x == 0) s.bin = -1;
     other = __syncthreads_or(other);
-    const uint64_t sums = warp_scan(lane < warps ? s.warp_a[lane] : 0, lane);
+    const uint64_t sums = warp_scan(lane < kWarps ? s.warp_a[lane] : 0, lane);
     const uint64_t all = __shfl_sync(0xffffffffu, sums, 31);
     const uint64_t prior = __shfl_sync(0xffffffffu, sums, warp == 0 ? 0 : warp - 1);
     if (p) target = front_of(*p, all, other);
     uint64_t x = (warp == 0 ? 0 : prior) + upto - mine;
     if (x < target && target <= x + mine) {
-      int bin = own * threadIdx.x;
-      while (x + amount(bin) < target) x += amount(bin++);
-      s.bin = bin, s.before = x, s.target = target;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        if (x < target && target <= x + part[i]) s.bin = kOwn * threadIdx.x + i, s.before = x, s.target = target;
+        x += part[i];
+      }
     }
     __syncthreads();
   }
 
-  // top-k and top-p by the counts of values. False: the cut lies among the rare ones, and nothing was done.
+  // top-k and top-p by the counts of values; the rare ones count with zero. `far`: there are tokens that were not counted.
+  // False: the cut lies among the rare ones, and nothing was done.
   __device__ __forceinline__ bool cut_values(uint32_t k, const float* p, bool far) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t rare_weight = 0;
     uint32_t rares = s.listed;
-    for (int i = threadIdx.x; i < s.listed; i += blockDim.x) rare_weight += weight(__uint_as_float(s.list[i]));
+    for (int i = threadIdx.x; i < rares; i += kThreads) rare_weight += weight(__uint_as_float(s.list[i]));
     rare_weight = warp_sum(rare_weight);
     if (lane == 0) s.warp_a[warp] = rare_weight;
     __syncthreads();
-    rare_weight = warp_sum(lane < warps ? s.warp_a[lane] : 0);
+    rare_weight = warp_sum(lane < kWarps ? s.warp_a[lane] : 0);
     if (blocks > 1) {
       if (threadIdx.x < blocks) {
         store_cluster(cluster_address(&s.peer_rare[rank], threadIdx.x), rare_weight);
@@ -494,27 +485,57 @@ struct Row {
       rare_weight = 0, rares = 0;
       for (int q = 0; q < blocks; ++q) rare_weight += s.peer_rare[q], rares += s.peer_rares[q];
       const int slice = kValues / blocks;
-      for (int i = rank * slice + threadIdx.x; i < (rank + 1) * slice; i += blockDim.x) {
+      for (int i = rank * slice + threadIdx.x; i < (rank + 1) * slice; i += kThreads) {
         uint32_t sum = 0;
         for (int q = 0; q < blocks; ++q) sum += load_cluster(cluster_address(&s.count[i], q));
         for (int q = 0; q < blocks; ++q) store_cluster(cluster_address(&s.counts[i], q), sum);
       }
       sync();
-    } else {
-      for (int i = threadIdx.x; i < kValues; i += blockDim.x) s.counts[i] = s.count[i];
-      __syncthreads();
     }
-    for (int i = threadIdx.x; i < kValues; i += blockDim.x) s.count[i] = 0;
+    // from here on a thread's bins are in its registers
+    uint32_t n[kOwn];
+    uint64_t w[kOwn], part[kOwn];
+    const uint32_t* const from = (blocks > 1 ? s.counts : s.count) + kOwn * threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) n[i] = from[i], s.count[kOwn * threadIdx.x + i] = 0;
+    bool other = far;  // than the largest logit
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const float value = bin_value(kOwn * threadIdx.x + i);
+      w[i] = 0;
+      if (n[i]) {
+        s.weight[kOwn * threadIdx.x + i] = w[i] = weight(value);
+        other = other || value != top;
+      }
+    }
+    constexpr int zero_thread = kZeroBin / kOwn, zero_at = kZeroBin % kOwn;
+    const bool zero = threadIdx.x == zero_thread && rares;
+    other = other || zero;
     int end = kValues;
     uint32_t end_count = 0;
     if (k) {
-      reach_value<false>(k, nullptr, end, end_count, rares, rare_weight, far);
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) part[i] = (w[i] ? n[i] : 0) + (zero && i == zero_at && rare_weight ? rares : 0);
+      reach_value(part, k, nullptr, false);
       if (s.bin >= 0) end = s.bin, end_count = static_cast<uint32_t>(s.target - s.before);
       if (end == kZeroBin && rares) return false;
+      if (end < kValues) {
+        other = false;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          const int bin = kOwn * threadIdx.x + i;
+          if (bin > end) n[i] = 0;
+          if (bin == end) n[i] = end_count;
+          other = other || (n[i] && bin_value(bin) != top);
+        }
+        other = other || (zero && kZeroBin < end);
+      }
     }
     if (p) {
-      __syncthreads();  // s.bin and its company are read
-      reach_value<true>(0, p, end, end_count, rares, rare_weight, far);
+      if (k) __syncthreads();  // s.bin and its company are read
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) part[i] = n[i] * w[i] + (zero && i == zero_at && kZeroBin < end ? rare_weight : 0);
+      reach_value(part, 0, p, other);
       end = s.bin;
       if (end == kZeroBin && rares) return false;
       end_count = static_cast<uint32_t>((s.target - s.before + s.weight[end] - 1) / s.weight[end]);
@@ -555,11 +576,11 @@ struct Row {
     if (mine && bin_of(value_of(tau)) == bin) low = min(low, tau), high = max(high, tau);
     low = __reduce_min_sync(0xffffffffu, low);
     high = __reduce_max_sync(0xffffffffu, high);
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31;
     if (lane == 0) s.warp_b[threadIdx.x >> 5] = low, s.warp_c[threadIdx.x >> 5] = high;
     __syncthreads();
-    low = __reduce_min_sync(0xffffffffu, lane < warps ? s.warp_b[lane] : 0xFFFFFFFFu);
-    high = __reduce_max_sync(0xffffffffu, lane < warps ? s.warp_c[lane] : 0);
+    low = __reduce_min_sync(0xffffffffu, lane < kWarps ? s.warp_b[lane] : 0xFFFFFFFFu);
+    high = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.warp_c[lane] : 0);
     if (blocks > 1) {
       if (threadIdx.x < blocks) {
         store_cluster(cluster_address(&s.peer_low[rank], threadIdx.x), low);
@@ -591,16 +612,16 @@ struct Row {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kMaxWarps, 2) sample_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared& s = *reinterpret_cast<Shared*>(raw);
   constexpr int kVec = 16 / sizeof(T);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t b = blockIdx.x / a.blocks;
   const int rank = static_cast<int>(blockIdx.x % a.blocks);
-  for (int i = threadIdx.x; i < 1 << (kStepBits - 1); i += blockDim.x)
+  for (int i = threadIdx.x; i < 1 << (kStepBits - 1); i += kThreads)
     reinterpret_cast<uint4*>(s.power)[i] = reinterpret_cast<const uint4*>(kPowers.t)[i];
-  for (int i = threadIdx.x; i < kBins; i += blockDim.x) s.lo[i] = s.hi[i] = 0;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
   if (threadIdx.x == 0) s.listed = 0;
   pdl_wait();
   pdl_trigger();
@@ -626,8 +647,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) sample_kernel(SampleArgs a)
   uint32_t best = __reduce_max_sync(0xffffffffu, key_of(own)), far = __reduce_max_sync(0xffffffffu, key_of(away));
   if (lane == 0) s.warp_b[warp] = best, s.warp_c[warp] = far;
   __syncthreads();
-  best = __reduce_max_sync(0xffffffffu, lane < warps ? s.warp_b[lane] : 0);
-  far = __reduce_max_sync(0xffffffffu, lane < warps ? s.warp_c[lane] : 0);
+  best = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.warp_b[lane] : 0);
+  far = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.warp_c[lane] : 0);
   if (s.listed > kList) far = 0xFFFFFFFFu;  // too many rare ones
   if (a.blocks > 1) {
     if (threadIdx.x < a.blocks) {
@@ -661,14 +682,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) sample_kernel(SampleArgs a)
     if constexpr (sizeof(T) == 2) {
       // values of magnitude 2^7 and more are not counted: none may have a weight
       valued = isfinite(r.top) && far != 0xFFFFFFFFu && !((r.top - value_of(far)) * r.ch < 46.0f);
-      if (valued) {
-        for (int i = threadIdx.x; i < kValues; i += blockDim.x) s.weight[i] = bin_value(i) > r.top ? 0 : r.weight(bin_value(i));
-        __syncthreads();
-      }
-      if (counted && valued) {
+      if (!counted) {  // without counts, a table of all values pays for long rows only
+        valued = valued && per * kVec > 2 * kValues;
+        if (valued) {
+          for (int i = threadIdx.x; i < kValues; i += kThreads) s.weight[i] = bin_value(i) > r.top ? 0 : r.weight(bin_value(i));
+          __syncthreads();
+        }
+      } else if (valued) {
         cut = r.cut_values(top_k ? k : 0, top_p ? &part : nullptr, far > kNone);
-      } else if (counted) {
-        for (int i = threadIdx.x; i < kValues; i += blockDim.x) s.count[i] = 0;
+      } else {
+        for (int i = threadIdx.x; i < kValues; i += kThreads) s.count[i] = 0;
       }
       if (counted) __syncthreads();
     }
@@ -677,7 +700,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) sample_kernel(SampleArgs a)
         // a row's blocks have like numbers of tokens, and agree on what they do together
         if (per * kVec <= kList) {
           r.gather(-INFINITY);
-        } else if (k <= a.blocks * static_cast<int>(blockDim.x) / 2) {
+        } else if (k <= a.blocks * kThreads / 2) {
           if (own > -INFINITY) r.template add<false>(r.bin_of(own), 1);
           r.meet();
           r.reach(k, nullptr, false);
@@ -706,7 +729,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) sample_kernel(SampleArgs a)
           sum = warp_sum(sum);
           if (lane == 0) s.warp_a[warp] = sum;
           others = __syncthreads_or(others);
-          sum = warp_sum(lane < warps ? s.warp_a[lane] : 0);
+          sum = warp_sum(lane < kWarps ? s.warp_a[lane] : 0);
           if (a.blocks > 1) {
             if (threadIdx.x < a.blocks) {
               store_cluster(cluster_address(&s.peer_total[rank], threadIdx.x), sum);
@@ -757,7 +780,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) sample_kernel(SampleArgs a)
   same = warp_sum(same);
   if (lane == 0) s.warp_a[warp] = sum, s.warp_b[warp] = same;
   __syncthreads();
-  sum = lane < warps ? s.warp_a[lane] : 0, same = lane < warps ? s.warp_b[lane] : 0;
+  sum = lane < kWarps ? s.warp_a[lane] : 0, same = lane < kWarps ? s.warp_b[lane] : 0;
   const uint64_t block_sum = warp_sum(sum);
   const uint32_t block_same = warp_sum(same);
   uint64_t total = 0, prior = 0;
@@ -847,9 +870,8 @@ int blocks_of(int B, int V) {
 template <typename T>
 moe_status_t launch_sample(SampleArgs a, int B, cudaStream_t s) {
   a.blocks = blocks_of(B, a.V);
-  const int threads = a.V / a.blocks > 2048 ? 32 * kMaxWarps : 256;
   MOE_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared)));
-  return launch_clusters(sample_kernel<T>, a.blocks, dim3(static_cast<unsigned>(B) * a.blocks), dim3(threads), sizeof(Shared), s, a);
+  return launch_clusters(sample_kernel<T>, a.blocks, dim3(static_cast<unsigned>(B) * a.blocks), dim3(kThreads), sizeof(Shared), s, a);
 }
 
 }  // namespace
