@@ -184,6 +184,34 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// exp((l - top) / temperature) in units of 2^-44, ch + cl = log2(e) / temperature
+__device__ __forceinline__ uint64_t weight_of(const uint64_t* power, float top, float ch, float cl, float l) {
+  if (l == top) return kOne;
+  const float d = top - l;
+  const float p = d * ch;
+  if (!(p < 46.0f)) return 0;
+  // what d and p lost by rounding
+  const float back = top - d;
+  const float dl = (top - (d + back)) + (back - l);
+  float e = fmaf(d, ch, -p);
+  e = fmaf(d, cl, e);
+  e = fmaf(dl, ch, e);
+  const float magic = 0x1.8p13f;  // rounds to multiples of 2^-10
+  const float k = p + magic;
+  const int steps = static_cast<int>(__float_as_uint(k) - __float_as_uint(magic));
+  const float z = (p - (k - magic)) + e;
+  // 2^-z - 1, |z| <= 2^-11 and a bit: the cubic term is below 2^-37
+  const float x = z * fmaf(z, 0.240226507f, -0.693147181f);
+  const int part = __float2int_rn(x * 0x1p42f);
+  const uint64_t t = power[steps & ((1 << kStepBits) - 1)];
+  const int64_t w = static_cast<int64_t>(t) + ((static_cast<int64_t>(static_cast<int32_t>(t >> 13)) * part) >> 29);
+  return static_cast<uint64_t>(w) >> (steps >> kStepBits);
+}
+// the same as a call: most of this kernel's code runs once a row and is slow to fetch, so there is to be little of it
+__device__ __noinline__ uint64_t weight_call(const uint64_t* power, float top, float ch, float cl, float l) {
+  return weight_of(power, top, ch, cl, l);
+}
+
 // A 16-byte piece of a row of V values that begins at value `at`: places outside the row, and NaN, are -infinity.
 template <typename T>
 __device__ __noinline__ uint4 odd_piece(const T* row, int V, int at) {
@@ -268,25 +296,19 @@ struct Row {
     first = min(count, warp * per);
     last = min(count, first + per);
   }
-  // f(piece, its largest value) for this thread's pieces, four of them in flight
+  // f(piece, its largest value) for this thread's pieces, the next one in flight
   template <typename F>
   __device__ __forceinline__ void pieces(F&& f) const {
     int first, last;
     segment(threadIdx.x >> 5, first, last);
     int i = first + (threadIdx.x & 31);
-    for (; i + 96 < last; i += 128) {
-      uint4 u[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = raw(i + 32 * e);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float m;
-        clean(i + 32 * e, u[e], m);
-        f(u[e], m);
-      }
-    }
+    if (i >= last) return;
+    uint4 next = raw(i), then = i + 32 < last ? raw(i + 32) : next;
+#pragma unroll 1
     for (; i < last; i += 32) {
-      uint4 u = raw(i);
+      uint4 u = next;
+      next = then;
+      if (i + 64 < last) then = raw(i + 64);
       float m;
       clean(i, u, m);
       f(u, m);
@@ -327,26 +349,7 @@ struct Row {
   }
 
   __device__ __forceinline__ uint64_t weight(float l) const {
-    if (l == top) return kOne;
-    const float d = top - l;
-    const float p = d * ch;
-    if (!(p < 46.0f)) return 0;
-    // what d and p lost by rounding
-    const float back = top - d;
-    const float dl = (top - (d + back)) + (back - l);
-    float e = fmaf(d, ch, -p);
-    e = fmaf(d, cl, e);
-    e = fmaf(dl, ch, e);
-    const float magic = 0x1.8p13f;  // rounds to multiples of 2^-10
-    const float k = p + magic;
-    const int steps = static_cast<int>(__float_as_uint(k) - __float_as_uint(magic));
-    const float z = (p - (k - magic)) + e;
-    // 2^-z - 1, |z| <= 2^-11 and a bit: the cubic term is below 2^-37
-    const float x = z * fmaf(z, 0.240226507f, -0.693147181f);
-    const int part = __float2int_rn(x * 0x1p42f);
-    const uint64_t t = s.power[steps & ((1 << kStepBits) - 1)];
-    const int64_t w = static_cast<int64_t>(t) + ((static_cast<int64_t>(static_cast<int32_t>(t >> 13)) * part) >> 29);
-    return static_cast<uint64_t>(w) >> (steps >> kStepBits);
+    return sizeof(T) == 2 ? weight_call(s.power, top, ch, cl, l) : weight_of(s.power, top, ch, cl, l);
   }
 
   __device__ __forceinline__ int bin_of(float l) const {
@@ -492,22 +495,27 @@ struct Row {
       }
       sync();
     }
-    // from here on a thread's bins are in its registers
-    uint32_t n[kOwn];
-    uint64_t w[kOwn], part[kOwn];
-    const uint32_t* const from = (blocks > 1 ? s.counts : s.count) + kOwn * threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) n[i] = from[i], s.count[kOwn * threadIdx.x + i] = 0;
+    // weights of the values that occur, neighbouring bins by turns to the warps: few values lie in few runs of bins
+    const uint32_t* const counts = blocks > 1 ? s.counts : s.count;
     bool other = far;  // than the largest logit
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const float value = bin_value(kOwn * threadIdx.x + i);
-      w[i] = 0;
-      if (n[i]) {
-        s.weight[kOwn * threadIdx.x + i] = w[i] = weight(value);
+#pragma unroll 1
+    for (int bin = threadIdx.x; bin < kValues; bin += kThreads) {
+      if (counts[bin]) {
+        const float value = bin_value(bin);
+        s.weight[bin] = weight(value);
         other = other || value != top;
       }
     }
+    __syncthreads();
+    // from here on a thread's bins are in its registers
+    uint32_t n[kOwn];
+    uint64_t w[kOwn], part[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) n[i] = counts[kOwn * threadIdx.x + i];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) w[i] = n[i] ? s.weight[kOwn * threadIdx.x + i] : 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) s.count[kOwn * threadIdx.x + i] = 0;
     constexpr int zero_thread = kZeroBin / kOwn, zero_at = kZeroBin % kOwn;
     const bool zero = threadIdx.x == zero_thread && rares;
     other = other || zero;
@@ -722,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
             Row<T>::unpack(w, v);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
-              sum += r.weight(v[e]);
+              sum += weight_of(s.power, r.top, r.ch, r.cl, v[e]);
               others = others || (v[e] > -INFINITY && v[e] < r.top);
             }
           });
@@ -756,14 +764,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
     }
   }
 
-  // the kept weight of every warp's segment, without the tokens of key tau; how many of these it has
+  // the kept weight of a piece, without the tokens of key tau; how many of these it has
   const float last_kept = value_of(r.tau);
-  uint64_t sum = 0;
-  uint32_t same = 0;
-  r.pieces([&](const uint4& w, float m) {
+  const auto kept = [&](const uint4& piece, float m, uint64_t& sum, uint32_t& same) {
     if (!(m >= last_kept) || m == -INFINITY) return;
     float v[kVec];
-    Row<T>::unpack(w, v);
+    Row<T>::unpack(piece, v);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       if (v[e] > last_kept) {
@@ -775,7 +781,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
       }
       same += v[e] == last_kept;
     }
-  });
+  };
+  // of every warp's segment
+  uint64_t sum = 0;
+  uint32_t same = 0;
+  r.pieces([&](const uint4& piece, float m) { kept(piece, m, sum, same); });
   sum = warp_sum(sum);
   same = warp_sum(same);
   if (lane == 0) s.warp_a[warp] = sum, s.warp_b[warp] = same;
@@ -791,7 +801,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
       store_cluster(cluster_address(&s.peer_same[rank], threadIdx.x), block_same);
     }
     r.sync();
-    if (warp != 0) return;
     for (int i = 0; i < a.blocks; ++i) {
       if (i == rank) prior = total, seen_prior = seen;
       const uint32_t here = min(s.peer_same[i], r.ties - min(r.ties, seen));
@@ -799,7 +808,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
       total += s.peer_sum[i] + here * r.tie_weight;
     }
   } else {
-    if (warp != 0) return;
     total = block_sum + min(block_same, r.ties) * r.tie_weight;
   }
   bool rest;
@@ -808,55 +816,75 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   if (target <= prior) return;
   target -= prior;
   uint32_t free_ties = r.ties - min(r.ties, seen_prior);  // kept tokens of key tau from here on
-  // the warp's segment in which it lies
-  const uint32_t upto_same = warp_scan(same, lane), before_same = upto_same - same;
-  sum += min(same, free_ties - min(free_ties, before_same)) * r.tie_weight;
-  const uint64_t upto = warp_scan(sum, lane);
-  const unsigned reached = __ballot_sync(0xffffffffu, upto >= target);
-  if (!reached) return;  // another block's
-  const int w = __ffs(reached) - 1;
-  target -= __shfl_sync(0xffffffffu, upto - sum, w);
-  const uint32_t gone = __shfl_sync(0xffffffffu, before_same, w);
-  free_ties -= min(free_ties, gone);
+  // Of 32 runs' sums and ties in order, a run a lane: the one in which the target lies, or -1; the target and the free ties
+  // become those from that run, or from behind all of them, on.
+  const auto find = [&](uint64_t run_sum, uint32_t run_same) {
+    const uint32_t upto_same = warp_scan(run_same, lane), before_same = upto_same - run_same;
+    run_sum += min(run_same, free_ties - min(free_ties, before_same)) * r.tie_weight;
+    const uint64_t upto = warp_scan(run_sum, lane);
+    const unsigned reached = __ballot_sync(0xffffffffu, upto >= target);
+    const int at = reached ? __ffs(reached) - 1 : 31;
+    target -= __shfl_sync(0xffffffffu, reached ? upto - run_sum : upto, at);
+    const uint32_t gone = __shfl_sync(0xffffffffu, reached ? before_same : upto_same, at);
+    free_ties -= min(free_ties, gone);
+    return reached ? at : -1;
+  };
+  const int w = find(sum, same);
+  if (w < 0) return;  // another block's
+  // The segment's rounds of 32 pieces are dealt out to the warps, and the first of them looks into the one it is.
   int first, last;
   r.segment(w, first, last);
-  for (int i0 = first; i0 < last; i0 += 32) {
-    const int i = i0 + lane;
-    float v[kVec], m = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) v[e] = -INFINITY;
-    if (i < last) {
-      uint4 piece = r.raw(i);
-      r.clean(i, piece, m);
-      Row<T>::unpack(piece, v);
-    }
+  const int rounds = (last - first + 31) / 32;
+  uint64_t* const round_sum = s.total;
+  uint32_t* const round_same = s.lo;
+  for (int i = warp; i < rounds; i += kWarps) {
+    uint64_t x = 0;
     uint32_t n = 0;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) n += v[e] == last_kept;
-    const uint32_t n_upto = warp_scan(n, lane);
-    uint32_t free = free_ties - min(free_ties, n_upto - n);
-    uint64_t part[kVec], whole = 0;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      part[e] = v[e] > last_kept ? r.weight(v[e]) : 0;
-      if (part[e] < least) part[e] = 0;
-      if (v[e] == last_kept && free > 0) part[e] = r.tie_weight, --free;
-      whole += part[e];
+    const int at = first + 32 * i + lane;
+    if (at < last) {
+      uint4 piece = r.raw(at);
+      float m;
+      r.clean(at, piece, m);
+      kept(piece, m, x, n);
     }
-    const uint64_t whole_upto = warp_scan(whole, lane);
-    if (whole_upto >= target && whole_upto - whole < target) {
-      uint64_t x = whole_upto - whole;
+    x = warp_sum(x);
+    n = warp_sum(n);
+    if (lane == 0) round_sum[i] = x, round_same[i] = n;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  int round = -1;
+  for (int i = 0; round < 0 && i < rounds; i += 32) {
+    const int at = find(i + lane < rounds ? round_sum[i + lane] : 0, i + lane < rounds ? round_same[i + lane] : 0);
+    if (at >= 0) round = i + at;
+  }
+  if (round < 0) return;
+  const int i = first + 32 * round + lane;
+  float v[kVec], m = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        if (x < target && target <= x + part[e])
-          a.tokens[b] = static_cast<int32_t>(static_cast<int64_t>(v0 + i) * kVec - skew + e);
-        x += part[e];
-      }
-    }
-    const uint64_t sums = __shfl_sync(0xffffffffu, whole_upto, 31);
-    if (sums >= target) return;
-    target -= sums;
-    free_ties -= min(free_ties, __shfl_sync(0xffffffffu, n_upto, 31));
+  for (int e = 0; e < kVec; ++e) v[e] = -INFINITY;
+  if (i < last) {
+    uint4 piece = r.raw(i);
+    r.clean(i, piece, m);
+    Row<T>::unpack(piece, v);
+  }
+  uint32_t n = 0;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) n += v[e] == last_kept;
+  uint32_t free = free_ties - min(free_ties, warp_scan(n, lane) - n);
+  uint64_t part[kVec], whole = 0;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    part[e] = v[e] > last_kept ? r.weight(v[e]) : 0;
+    if (part[e] < least) part[e] = 0;
+    if (v[e] == last_kept && free > 0) part[e] = r.tie_weight, --free;
+    whole += part[e];
+  }
+  uint64_t x = warp_scan(whole, lane) - whole;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    if (x < target && target <= x + part[e]) a.tokens[b] = static_cast<int32_t>(static_cast<int64_t>(v0 + i) * kVec - skew + e);
+    x += part[e];
   }
 }
 
