@@ -62,6 +62,13 @@ MOE_API moe_status_t moe_test_routed_forward(const uint16_t* x, int32_t M, int64
 MOE_API moe_status_t moe_test_linear_cut(int32_t M, int32_t K, int32_t N, int32_t gated, int32_t num_sms,
                                          int32_t* cut);
 
+/* moe_linear_fp8 with test options (NULL = the defaults, which is exactly moe_linear_fp8). withhold_release: the
+ * copies of the first tiles' first block of K are not started. */
+MOE_API moe_status_t moe_test_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode,
+                                         int32_t M, int32_t K, const uint8_t* w, const float* w_scale, int32_t N,
+                                         int32_t activation, uint16_t* out, int32_t* dev_status,
+                                         const moe_test_options_t* options, moe_stream_t stream);
+
 /* moe_kv_attend with test options (NULL = the defaults, which is exactly moe_kv_attend). */
 MOE_API moe_status_t moe_test_kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t ld_q, int32_t batch,
                                         int32_t q_len, int32_t num_q_heads, const int32_t* page_table,

@@ -43,7 +43,7 @@ EXPORTED = [
 ]
 # the test build's extra entry points (include/moe_nvfp4_test.h)
 TEST_EXPORTED = ["moe_test_default_options", "moe_test_routed_forward", "moe_test_gemm1", "moe_test_linear_cut",
-                 "moe_test_kv_attend"]
+                 "moe_test_kv_attend", "moe_test_linear_fp8"]
 MOE_PLAN_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 
@@ -123,6 +123,8 @@ def _declare(lib, test=False):
     if test:
         sig.update({
             "moe_test_kv_attend": (c_int32, attend + [ctypes.POINTER(TestOptionsT), P]),
+            "moe_test_linear_fp8": (c_int32, [P, c_int64, P, c_int32, c_int32, c_int32, P, P, c_int32, c_int32, P, P,
+                                              ctypes.POINTER(TestOptionsT), P]),
             "moe_test_default_options": (TestOptionsT, []),
             "moe_test_routed_forward": (c_int32, routed + [ctypes.POINTER(TestOptionsT), P]),
             "moe_test_linear_cut": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, ctypes.POINTER(c_int32)]),
@@ -409,12 +411,16 @@ def moe_quantize_fp8(x, block_rows, y, y_scale, stream=None):
                                   _stream(stream)), "moe_quantize_fp8")
 
 
-def moe_linear_fp8(x, x_scale, x_scale_mode, w, w_scale, activation, out, dev_status=None, stream=None):
-    """x [M, K] float8_e4m3fn (it may have a row stride); w [N, K], w_scale [ceil(N / 128), ceil(K / 128)]."""
+def moe_linear_fp8(x, x_scale, x_scale_mode, w, w_scale, activation, out, dev_status=None, stream=None, test_options=None):
+    """x [M, K] float8_e4m3fn (it may have a row stride); w [N, K], w_scale [ceil(N / 128), ceil(K / 128)]. test_options (a
+    TestOptionsT from test_options()): call the test build's moe_test_linear_fp8 instead."""
     M, K = x.shape
-    _check(lib().moe_linear_fp8(_ptr(x), x.stride(0) if M > 1 else K, _ptr(x_scale), x_scale_mode, M, K, _ptr(w),
-                                _ptr(w_scale), w.shape[0], activation, _ptr(out), _ptr(dev_status), _stream(stream)),
-           "moe_linear_fp8")
+    args = (_ptr(x), x.stride(0) if M > 1 else K, _ptr(x_scale), x_scale_mode, M, K, _ptr(w), _ptr(w_scale), w.shape[0],
+            activation, _ptr(out), _ptr(dev_status))
+    if test_options is None:
+        _check(lib().moe_linear_fp8(*args, _stream(stream)), "moe_linear_fp8")
+    else:
+        _check(test_lib().moe_test_linear_fp8(*args, ctypes.byref(test_options), _stream(stream)), "moe_test_linear_fp8")
 
 
 def moe_rotary(q, k, rotary_dim, adjacent, positions, inv_freq, axes, q_out, k_out, dev_status=None, stream=None):

@@ -384,9 +384,9 @@ PyObject* rotary(PyObject* const* a) {
   const int adjacent = PyObject_IsTrue(a[5]);
   if (adjacent < 0) throw Raised();
   const at::Tensor &qo = tensor(a[6], "q_out"), *ko = maybe(a[7], "k_out"), *status = maybe(a[8], "dev_status");
+  if ((k != nullptr) != (ko != nullptr)) refuse("k_out", "given with k, and only then");
   tokens(&qo, N, H, D, "q_out");
   tokens(ko, N, Hk, D, "k_out");
-  if ((k != nullptr) != (ko != nullptr)) refuse("k_out", "given with k, and only then");
   int32_t* const word = status_word(status);
   const moe_stream_t stream =
       stream_of({{&q, "q"}, {k, "k"}, {&pos, "positions"}, {&freq, "inv_freq"}, {axes, "axes"}, {&qo, "q_out"}, {ko, "k_out"},

@@ -233,6 +233,11 @@ moe_status_t kv_attend(const moe_kv_cache_t* cache, const uint16_t* q, int64_t l
                        int32_t num_q_heads, const int32_t* page_table, int64_t ld_table, int32_t max_pages,
                        const int32_t* seq_lens, float softmax_scale, uint16_t* out, float* lse, void* workspace,
                        size_t workspace_bytes, int32_t* dev_status, const TestOptions& topt, moe_stream_t stream);
+
+// moe_linear_fp8 with test options (linear_fp8.cu)
+moe_status_t linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode, int32_t M, int32_t K,
+                        const uint8_t* w, const float* w_scale, int32_t N, int32_t activation, uint16_t* out,
+                        int32_t* dev_status, const TestOptions& topt, moe_stream_t stream);
 moe_status_t launch_prepare_matrix(const uint8_t* src, const uint8_t* src_sf, int E, int rows, int rows_p, int K,
                                    int gated_inter, uint8_t* dst, uint8_t* dst_sf, cudaStream_t s);
 

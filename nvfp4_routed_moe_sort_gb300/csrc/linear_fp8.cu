@@ -8,6 +8,7 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "host_util.h"
+#include "layout.h"
 #include "tensor_map.h"
 
 namespace moe {
@@ -90,6 +91,7 @@ struct Fp8Args {
   int xs_step, xs_ld;  // per 128 columns and per row: 1 and groups, or 0 and 1
   int cols;            // of out: N, or N / 2
   int slices, m_tiles, x_rows, wide, stages, stage_bytes;
+  int withhold;        // test build: the first block of K of a tile's first copies never comes
 };
 
 // a += t * s for two values at once
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
     int stage = 0, phase = 0, issued = 0;
     for (int i = 0; i < n; ++i) {
       if (i >= a.stages && !__all_sync(0xffffffffu, wait_for(&done[stage], phase ^ 1, abort_flag, a.status, a.wait_ns))) break;
-      if (elect_one()) {
+      if (!(a.withhold && i == 0) && elect_one()) {
         uint8_t* const st = smem + stage * a.stage_bytes;
         const int k = (kb0 + i) * 128;
         mbar_arrive_expect_tx(&full[stage], bytes);
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
       if (++stage == a.stages) stage = 0, phase ^= 1;
     }
     // what was issued lands before the block ends, even if nothing waited for it
-    for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_drain(&full[i % a.stages], i / a.stages & 1);
+    for (int i = max(a.withhold ? 1 : 0, issued - a.stages); i < issued; ++i) mbar_drain(&full[i % a.stages], i / a.stages & 1);
   } else if (warp < 3) {
     // two warps take the blocks of K by turns: what one costs them in waits is more than it costs the tensor core
     const uint64_t w_desc = sdesc_kmajor_sw128(smem_u32(smem)), x_desc = sdesc_kmajor_sw128(smem_u32(smem) + kOperand);
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
              wait_for(&done[2 * stage + 1], phase ^ 1, abort_flag, a.status, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (elect_one()) {
+        if (!(a.withhold && i == 0) && elect_one()) {
           uint8_t* const st = smem + stage * 2 * kOperand;
           const uint32_t bar = cluster_address(&full[stage], 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 4 * kOperand);  // both blocks' loads
@@ -514,7 +516,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
       }
       // loads land before the pair ends, even if nothing waited for them
       if (rank == 0) {
-        for (int i = max(last - 3, 0); i <= last; i += 3) mbar_drain(&full[i % kPairStages], i / kPairStages & 1);
+        for (int i = last >= 3 ? last - 3 : last; i >= 0 && i <= last; i += 3)
+          if (!(a.withhold && i == 0)) mbar_drain(&full[i % kPairStages], i / kPairStages & 1);
       } else if (!ok) {
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 1000000ull) {
@@ -703,9 +706,11 @@ moe_status_t launch_pairs(Fp8Args a, const void* x, int64_t ld_x, const void* w,
 
 using namespace moe;
 
-extern "C" moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode,
-                                       int32_t M, int32_t K, const uint8_t* w, const float* w_scale, int32_t N,
-                                       int32_t activation, uint16_t* out, int32_t* dev_status, moe_stream_t stream) {
+namespace moe {
+
+moe_status_t linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode, int32_t M, int32_t K,
+                        const uint8_t* w, const float* w_scale, int32_t N, int32_t activation, uint16_t* out,
+                        int32_t* dev_status, const TestOptions& topt, moe_stream_t stream) {
   MOE_CHECK(M >= 0 && K > 0 && N > 0 && ld_x >= K, MOE_ERR_INVALID_ARGUMENT);
   MOE_CHECK(x_scale_mode == MOE_FP8_PER_TOKEN || x_scale_mode == MOE_FP8_PER_GROUP, MOE_ERR_INVALID_ARGUMENT);
   MOE_CHECK(activation >= MOE_ACT_SWIGLU && activation <= MOE_ACT_IDENTITY, MOE_ERR_INVALID_ARGUMENT);
@@ -726,7 +731,8 @@ extern "C" moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const flo
                 !overlaps(out, out_bytes, w_scale, static_cast<size_t>((N - 1) / kGroup + 1) * groups * 4),
             MOE_ERR_OVERLAP);
   Fp8Args a = {};
-  a.xs = x_scale, a.ws = w_scale, a.out = out, a.status = dev_status, a.wait_ns = kWaitLimitNs;
+  a.xs = x_scale, a.ws = w_scale, a.out = out, a.status = dev_status, a.wait_ns = topt.wait_limit_ns;
+  a.withhold = topt.withhold_release;
   a.M = M, a.N = N, a.K = K, a.groups = groups, a.act = activation, a.cols = cols;
   a.xs_step = per_token ? 0 : 1, a.xs_ld = per_token ? 1 : groups;
   const bool pairs = use_pairs(M, cols, groups, gated);
@@ -744,4 +750,12 @@ extern "C" moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const flo
   }
 #undef MOE_FP8_CASE
   return MOE_ERR_INVALID_ARGUMENT;
+}
+
+}  // namespace moe
+
+extern "C" moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode,
+                                       int32_t M, int32_t K, const uint8_t* w, const float* w_scale, int32_t N,
+                                       int32_t activation, uint16_t* out, int32_t* dev_status, moe_stream_t stream) {
+  return linear_fp8(x, ld_x, x_scale, x_scale_mode, M, K, w, w_scale, N, activation, out, dev_status, TestOptions(), stream);
 }

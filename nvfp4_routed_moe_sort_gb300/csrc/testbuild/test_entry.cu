@@ -110,6 +110,15 @@ extern "C" moe_status_t moe_test_gemm1(const int32_t* padded_offsets, const int3
   return launch_gemm1_plain(g1, s);
 }
 
+extern "C" moe_status_t moe_test_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode,
+                                            int32_t M, int32_t K, const uint8_t* w, const float* w_scale, int32_t N,
+                                            int32_t activation, uint16_t* out, int32_t* dev_status,
+                                            const moe_test_options_t* options, moe_stream_t stream) {
+  MOE_CHECK(options == nullptr || options->wait_limit_ns > 0, MOE_ERR_INVALID_ARGUMENT);
+  return linear_fp8(x, ld_x, x_scale, x_scale_mode, M, K, w, w_scale, N, activation, out, dev_status, to_internal(options),
+                    stream);
+}
+
 extern "C" moe_status_t moe_test_linear_cut(int32_t M, int32_t K, int32_t N, int32_t gated, int32_t num_sms,
                                             int32_t* cut) {
   MOE_CHECK(M >= 1 && K >= 16 && K % kBlock == 0 && N >= 1 && (!gated || N % 2 == 0) && num_sms >= 1 && cut != nullptr,
