@@ -1,11 +1,12 @@
 """One decoder layer's decode step on NVFP4 weights and an NVFP4 key/value cache, in one CUDA graph.
 
-    x -> norm (E4M3) -> q, k, v projection -> append -> attention -> output projection
+    x -> norm (E4M3) -> q, k, v projection (-> rotary positions) -> append -> attention -> output projection
       -> residual addition + norm (BF16 and E4M3) -> shared expert (SwiGLU, E4M3 in)
       -> + routed experts (NVFP4RoutedMoE, from the BF16 norm) -> residual addition
 
 Every product, norm and attention is a call of this library; torch allocates, computes the router's
-logits and top-k, and captures the graph. Position encodings are left to the caller. Run it
+logits and top-k, and captures the graph. ``rope_base`` turns queries and keys by their positions; without it position
+encodings are left to the caller. A head over the layer's output would go on with ``sample_tokens``. Run it
 (`python examples/decode_layer.py`) for the time of a step of a 2048-wide layer.
 """
 from __future__ import annotations
@@ -23,7 +24,7 @@ class DecodeLayer:
     """Weights of one layer (random here) and the buffers of a batch of single new tokens."""
 
     def __init__(self, batch, hidden=2048, heads=16, kv_heads=4, head_dim=128, experts=128, top_k=10, inter=512,
-                 shared_inter=512, pages=256, page_size=64, max_pages=32, seed=0, device="cuda"):
+                 shared_inter=512, pages=256, page_size=64, max_pages=32, seed=0, device="cuda", rope_base=None):
         gen = torch.Generator(device=device).manual_seed(seed)
 
         def normal(*shape):
@@ -53,6 +54,9 @@ class DecodeLayer:
         self.page_table = torch.zeros(batch, max_pages, dtype=torch.int32, device=device)
         self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=device)            # new tokens included
         self.slots = torch.full((batch,), -1, dtype=torch.int64, device=device)         # of the new tokens
+        self.positions = torch.zeros(batch, dtype=torch.int64, device=device)           # of the new tokens, with rope_base
+        half = torch.arange(head_dim // 2, dtype=torch.float64, device=device) / (head_dim // 2)
+        self.inv_freq = None if rope_base is None else rope_base ** -half
         self.graph = self.result = None
 
     def step(self) -> torch.Tensor:
@@ -61,6 +65,8 @@ class DecodeLayer:
         _, _, x8, scale = moe.add_rms_norm(self.x, self.w["norm1"], fp8="group")
         qkv = self.qkv(x8, scale).view(B, -1, self.head_dim)
         q, k, v = qkv.split((self.heads, self.kv_heads, self.kv_heads), 1)
+        if self.inv_freq is not None:
+            moe.rotary(q, self.positions, self.inv_freq, k=k, out=(q, k))  # in place, in the projection's output
         self.cache.append(k, v, self.slots)
         o, _ = self.cache.attend(q.unsqueeze(1), self.page_table, self.seq_lens)
         o = self.out(o.view(B, -1))
@@ -86,7 +92,7 @@ class DecodeLayer:
 
 def main():
     batch, steps, page = 8, 50, 64
-    layer = DecodeLayer(batch)
+    layer = DecodeLayer(batch, rope_base=10000.0)
     layer.x.copy_(torch.randn(layer.x.shape, device="cuda"))
     layer.page_table.copy_(torch.randperm(256, device="cuda").view(batch, 32).int())
     graph = layer.capture()
@@ -95,6 +101,7 @@ def main():
     times = []
     for t in range(steps):  # each sequence grows by one token a step
         layer.seq_lens.fill_(t + 1)
+        layer.positions.fill_(t)
         layer.slots.copy_(layer.page_table[place, t // page].long() * page + t % page)
         begin.record()
         graph.replay()

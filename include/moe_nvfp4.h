@@ -532,8 +532,7 @@ MOE_API moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const float*
  * token n:
  *   angle = positions[axes[i], n] * inv_freq[i],  (a, b) -> (a cos - b sin, a sin + b cos)
  * in FP32 with one rounding; the pair is values (i, i + rotary_dim / 2) of the head, or (2 i, 2 i + 1) with
- * `adjacent`. The head's other values stay. The angle is right to 2^-30 of a turn for positions up to 2^23, and up to
- * 2^31 as right as a float64 product.
+ * `adjacent`. The head's other values stay. The angle is right to 2^-24 of a turn for positions up to 2^38.
  *   q           [N, ld_q] BF16, the num_q_heads * head_dim values of a token contiguous; any ld_q from that on
  *               (slices of one projection's output will do)
  *   k           the same with num_k_heads, or NULL with num_k_heads 0

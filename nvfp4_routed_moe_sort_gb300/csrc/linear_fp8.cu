@@ -1,6 +1,24 @@
 // Products of E4M3 activations with an E4M3 matrix that has one FP32 scale per 128 x 128 block.
 //
 //   y[m, n] = act(sum_b xs[m, b] * ws[n / 128, b] * sum_{k in block b} x[m, k] * w[n, k])
+//
+// The products of a block b of K run on tcgen05 (kind::f8f6f4, FP32 sums in TMEM). Its scales are arbitrary FP32
+// numbers, so that its sums leave TMEM every 128 of K: warps of sums read them into registers, free the accumulator at
+// once, and add them times their scale to the tile's sums there, while the tensor core makes the next blocks'.
+//
+// What bounds it. Few tokens: the bytes of w, and a chain of launch, first load, sums and the slices' meeting of about
+// 4 us. Many: the way of an accumulator from MMA to MMA. All of TMEM is accumulators, 512 columns; from a block's MMAs over
+// commit, wait, read-out and release to the next ones into the same columns takes 1200 to 1500 cycles where 1024 would
+// keep the tensor core busy. What shortened that way, 8192 x 7168 x 7168: a relaxed arrival where a releasing one waited
+// for the scales' loads (780 -> 460 us); halves of the columns as accumulators of their own and a warp of MMAs for each of
+// the four (-> 440); scales through shared memory by a warp of their own, read before the wait; copies by three warps; the
+// loads' barrier waited for before the accumulator's, whole warps that elect a lane for the MMAs (-> 332); packed
+// FP32 multiply-adds (-> 314); the last 64 columns' reads under the first ones' additions (-> 307).
+//
+// Measured (us, in a graph): 4 x 2048 x 512 3.3, 16 x 4096 x 4096 6.7, 48 x 4096 x 7168 with SwiGLU 9.6, 256 x 4096 x 4096
+// 12.3, 333 x 7001 x 2000 15.7, 512 x 4096 x 4096 14.8, 1024 x 4096 x 4096 20 (1.7 PFLOP/s), 4096 x 4096 x 7168 with SwiGLU
+// 94 (2.55), 8192 x 7168 x 7168 305 to 320 (2.6 to 2.75). With nothing read out, loaded or varied (a timing copy), the
+// MMAs alone reach 3.8 PFLOP/s at 4096 x 4096 x 16384, whose tiles fill 84 % of the pairs' turns.
 #include <math.h>
 
 #include <atomic>
@@ -114,6 +132,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// as arrive_cluster() does, in this block
 __device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -178,7 +197,8 @@ __device__ __forceinline__ void store_rows(const Fp8Args& a, const float* v, int
   }
 }
 
-// One 128 x 128 tile of the product, or one slice of its K. The blocks of a cluster are a tile's slices.
+// One 128 x 128 tile of the product, or one slice of its K. The blocks of a cluster are a tile's slices: their sums meet in
+// distributed shared memory in the slices' order, so that results repeat.
 template <int ACT>
 __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_constant__ Fp8Args a) {
   constexpr bool GATED = is_gated(ACT);
@@ -226,24 +246,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
   pdl_trigger();
 
   if (warp == 0) {
-    const uint32_t bytes = a.x_rows * 128 + kOperand;
-    int stage = 0, phase = 0, issued = 0;
-    for (int i = 0; i < n; ++i) {
-      if (i >= a.stages && !__all_sync(0xffffffffu, wait_for(&done[stage], phase ^ 1, abort_flag, a.status, a.wait_ns))) break;
-      if (!(a.withhold && i == 0) && elect_one()) {
-        uint8_t* const st = smem + stage * a.stage_bytes;
-        const int k = (kb0 + i) * 128;
-        mbar_arrive_expect_tx(&full[stage], bytes);
-        tma_load_2d(st, &a.tmap_w, k, n0, &full[stage]);
-        if (GATED) tma_load_2d(st + kOperand / 2, &a.tmap_w, k, a.cols + n0, &full[stage]);
-        tma_load_2d(st + kOperand, &a.tmap_x, k, m0, &full[stage]);
+    if (lane == 0) {  // (the whole warp waiting, one of its lanes issuing, takes 5 to 10 % longer)
+      const uint32_t bytes = a.x_rows * 128 + kOperand;
+      int stage = 0, phase = 0, issued = 0;
+      for (int i = 0; i < n; ++i) {
+        if (!wait_for(&done[stage], phase ^ 1, abort_flag, a.status, a.wait_ns)) break;
+        if (!(a.withhold && i == 0)) {
+          uint8_t* const st = smem + stage * a.stage_bytes;
+          const int k = (kb0 + i) * 128;
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          tma_load_2d(st, &a.tmap_w, k, n0, &full[stage]);
+          if (GATED) tma_load_2d(st + kOperand / 2, &a.tmap_w, k, a.cols + n0, &full[stage]);
+          tma_load_2d(st + kOperand, &a.tmap_x, k, m0, &full[stage]);
+        }
+        ++issued;
+        if (++stage == a.stages) stage = 0, phase ^= 1;
       }
-      __syncwarp();
-      ++issued;
-      if (++stage == a.stages) stage = 0, phase ^= 1;
+      // what was issued lands before the block ends, even if nothing waited for it
+      for (int i = max(a.withhold ? 1 : 0, issued - a.stages); i < issued; ++i) mbar_drain(&full[i % a.stages], i / a.stages & 1);
     }
-    // what was issued lands before the block ends, even if nothing waited for it
-    for (int i = max(a.withhold ? 1 : 0, issued - a.stages); i < issued; ++i) mbar_drain(&full[i % a.stages], i / a.stages & 1);
   } else if (warp < 3) {
     // two warps take the blocks of K by turns: what one costs them in waits is more than it costs the tensor core
     const uint64_t w_desc = sdesc_kmajor_sw128(smem_u32(smem)), x_desc = sdesc_kmajor_sw128(smem_u32(smem) + kOperand);
@@ -422,10 +443,14 @@ __device__ __forceinline__ void tma_load_pair(void* smem_dst, const CUtensorMap*
       ::"r"(smem_u32(smem_dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// Sums were read (tcgen05.wait::ld came before) and nothing else is told: with a release the arrival would wait for every
+// load of the thread that is under way.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// 256 x 256 columns to two SMs, since each then loads 32 KB a block of K and not 48: at the tensor core's rate one SM's tiles
+// of 128 x 256 would want 27 TB/s from L2.
 constexpr int kPairStages = 6;
 static_assert(kPairStages % 6 == 0, "three warps of copies and two buffers of sums take the stages by turns");
 constexpr int kPairCols = 256;         // of a tile, and of one accumulator
@@ -597,27 +622,30 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
         tc_fence_after();
         const uint32_t from = at + buf * kPairCols;
         uint32_t v[2][32];
+        const auto add = [&](int c) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) fma2(acc[32 * c + i], acc[32 * c + i + 1], v[c & 1][i], v[c & 1][i + 1], c < 2 ? s0 : s1);
+        };
         tmem_ld32_issue(from, v[0]);
+        tmem_ld32_issue(from + 32, v[1]);
         if (kb % kScaleRun == kScaleRun - 1 || kb == a.groups - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&scales_free[run & 1]);
           ++run;
         }
-        tmem_wait_ld<32>(v[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < 3) tmem_ld32_issue(from + (c + 1) * 32, v[(c + 1) & 1]);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) fma2(acc[32 * c + i], acc[32 * c + i + 1], v[c & 1][i], v[c & 1][i + 1], c < 2 ? s0 : s1);
-          if (c < 3) tmem_wait_ld<32>(v[(c + 1) & 1]);
-          if (c == 2) {  // all of it is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(free_bar + 2 * buf * 8);
-            if (++stage == kPairStages) stage = 0, phase ^= 1;
-            here = mbar_test(&done[2 * stage + half], phase);
-          }
-        }
+        tmem_wait_ld<64>(&v[0][0]);
+        add(0);
+        tmem_ld32_issue(from + 64, v[0]);
+        add(1);
+        tmem_ld32_issue(from + 96, v[1]);
+        tmem_wait_ld<64>(&v[0][0]);  // all of it is in registers
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(free_bar + 2 * buf * 8);
+        if (++stage == kPairStages) stage = 0, phase ^= 1;
+        here = mbar_test(&done[2 * stage + half], phase);
+        add(2);
+        add(3);
         buf ^= 1;
       }
       if (!ok) break;

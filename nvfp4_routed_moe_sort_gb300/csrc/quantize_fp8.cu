@@ -3,6 +3,11 @@
 //
 // Per scale group scale = amax|x| / 448 (1 when amax is 0), y = e4m3(x * (448 / amax)): the rule of the
 // norm's E4M3 output.
+//
+// Bound by HBM (3 bytes a value): a group stays in the registers of its half warp between its one read and its one
+// write, four groups' loads a thread in flight where rows are many (one where they are few). A group's row by
+// multiplication: with a 64-bit division 77 us, without 65. Measured: 8 x 2048 2.4 us, 16384 x 7160 65 us (5.5 TB/s, 80 %
+// of the copy rate). Rows at odd addresses go by the value.
 #include <math.h>
 
 #include "common.cuh"

