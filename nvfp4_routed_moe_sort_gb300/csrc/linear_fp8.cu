@@ -147,6 +147,7 @@ constexpr int kTurnLd = 18;               // of 32 rows of 16 values that a warp
 constexpr int kScaleRun = 8;              // blocks of K whose scales are fetched together: a sector of x_scale
 constexpr int kScaleBytes = 2 * kScaleRun * (128 + 2) * 4;
 constexpr int kBarBytes = 256;
+constexpr int kTileSmem = 227 * 1024;     // at most
 
 // The scales of kScaleRun blocks of K at a time, turned so that the threads of a row's sums read them side by
 // side (read from global memory by those threads, one value a block of K, they cost half of the kernel's time):
@@ -172,7 +173,21 @@ __device__ __forceinline__ void fetch_scales(const Fp8Args& a, int run, int kb, 
 // them, else 32 x 16 values at a time change hands in shared memory and the warp writes row by row.
 template <int N>
 __device__ __forceinline__ void store_rows(const Fp8Args& a, const float* v, int64_t first, int c0, uint16_t* turn, int lane) {
-  if (a.wide) {
+  if (a.wide == 2) {  // whole sectors
+    if (first + lane < a.M) {
+      uint16_t* const to = a.out + (first + lane) * a.cols + c0;
+#pragma unroll
+      for (int i = 0; i < N / 16; ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = bf16x2(v[16 * i + 2 * e], v[16 * i + 2 * e + 1]);
+        if (c0 + 16 * i < a.cols)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * i), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                       "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                       : "memory");
+      }
+    }
+  } else if (a.wide) {
     if (first + lane < a.M) {
       uint16_t* const to = a.out + (first + lane) * a.cols + c0;
 #pragma unroll
@@ -393,16 +408,63 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
   }
 }
 
+// rows of out: 2 whole 32-byte sectors, 1 whole 16-byte pieces, 0 neither
+int row_pieces(const Fp8Args& a) {
+  return a.cols % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 32 == 0 ? 2 : a.cols % 8 == 0;
+}
+
+// How many clusters of `size` blocks of a kernel run at once on the current device: looked up once for each size.
+moe_status_t resident(const void* kern, int size, int threads, int smem, std::atomic<int>* known, int& clusters) {
+  int dev = 0;
+  MOE_CUDA(cudaGetDevice(&dev));
+  std::atomic<int>& here = known[(dev & 63) * kMaxSlices + size - 1];
+  clusters = here.load(std::memory_order_relaxed);
+  if (clusters > 0) return MOE_OK;
+  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size * num_sms());
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MOE_CUDA(cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg));
+  if (clusters < 1) return MOE_ERR_CUDA;
+  here.store(clusters, std::memory_order_relaxed);
+  return MOE_OK;
+}
+
+// Single blocks: in how many slices K is cut, by the least estimated time. A wave of blocks takes 3 us and 0.26 us a block of
+// K, up to 0.10 more where all SMs load 128 rows of x; the slices' meeting 0.4 us and 3 more for 128 rows. The clusters
+// that run at once are fewer than their blocks would let one think (of eight blocks 15 on 152 SMs, not 19).
+moe_status_t cut_tiles(int M, int groups, int64_t tiles, int& slices, double& time) {
+  static std::atomic<int> known[64 * kMaxSlices];
+  const double rows = (M < kRows ? M : kRows) / static_cast<double>(kRows);
+  time = -1.0;
+  for (int n = 1; n <= kMaxSlices && (n == 1 || groups >= 2 * n); ++n) {
+    int clusters = 0;
+    const moe_status_t st = resident(reinterpret_cast<const void*>(linear_fp8_kernel<MOE_ACT_IDENTITY>), n, kThreads, kTileSmem, known, clusters);
+    if (st != MOE_OK) return st;
+    const double waves = ceil(static_cast<double>(tiles) / clusters), busy = fmin(1.0, static_cast<double>(tiles) / clusters);
+    const double t = waves * (3.0 + ceil(static_cast<double>(groups) / n) * (0.26 + 0.10 * busy * rows)) + (n > 1 ? 0.4 + 3.0 * rows : 0.0);
+    if (time < 0.0 || t < time) time = t, slices = n;
+  }
+  return MOE_OK;
+}
+
 template <int ACT>
 moe_status_t launch_tiles(Fp8Args a, const void* x, int64_t ld_x, const void* w, cudaStream_t s) {
   constexpr int kOut = is_gated(ACT) ? kCols / 2 : kCols;
   a.m_tiles = (a.M - 1) / kRows + 1;
   a.x_rows = a.M < kRows ? (a.M + 7) / 8 * 8 : kRows;
   const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.cols - 1) / kOut + 1);
-  a.slices = 1;
-  while (a.slices < kMaxSlices && tiles * a.slices * 2 <= num_sms() && a.groups >= 4 * a.slices) a.slices *= 2;
+  double time = 0.0;
+  const moe_status_t cut = cut_tiles(a.M, a.groups, tiles, a.slices, time);
+  if (cut != MOE_OK) return cut;
   MOE_CHECK(tiles * a.slices <= INT32_MAX, MOE_ERR_UNSUPPORTED_SHAPE);
-  a.wide = a.cols % 8 == 0;
+  a.wide = row_pieces(a);
   const int held = a.M < kRows ? a.M : kRows;
   int sums = a.slices > 1 ? (held + a.slices - 1) / a.slices * a.slices * kSumLd * 4 : 8 * 32 * kTurnLd * 2;
   // The MMA reads 128 rows of x where fewer were loaded (what it makes of the others is not used): they lie in the
@@ -410,12 +472,12 @@ moe_status_t launch_tiles(Fp8Args a, const void* x, int64_t ld_x, const void* w,
   if (sums < kOperand - kScaleBytes - kBarBytes) sums = kOperand - kScaleBytes - kBarBytes;
   a.stage_bytes = kOperand + (a.x_rows * 128 + 1023) / 1024 * 1024;
   const int rest = 1024 + kScaleBytes + kBarBytes + sums;
-  a.stages = (227 * 1024 - rest) / a.stage_bytes / 2 * 2;  // even: two warps take them by turns
+  a.stages = (kTileSmem - rest) / a.stage_bytes / 2 * 2;  // even: two warps take them by turns
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const int smem = rest + a.stages * a.stage_bytes;
   if (!encode_rows(&a.tmap_x, x, a.K, a.M, ld_x, a.x_rows) || !encode_rows(&a.tmap_w, w, a.K, a.N, a.K, kOut)) return MOE_ERR_CUDA;
   const auto kern = linear_fp8_kernel<ACT>;
-  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+  MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem));
   return launch_clusters(kern, a.slices, dim3(static_cast<unsigned>(tiles * a.slices)), dim3(kThreads), smem, s, a);
 }
 
@@ -672,44 +734,33 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
   }
 }
 
-// How many pairs run at once on the current device: looked up once for each.
+// How many pairs run at once on the current device.
 template <int ACT>
 moe_status_t resident_pairs(int& pairs) {
-  const auto kern = linear_fp8_pair_kernel<ACT>;
-  static std::atomic<int> known[64];
-  int dev = 0;
-  MOE_CUDA(cudaGetDevice(&dev));
-  const int i = dev & 63;
-  pairs = known[i].load(std::memory_order_relaxed);
-  if (pairs > 0) return MOE_OK;
-  cudaFuncAttributes fa;
-  MOE_CUDA(cudaFuncGetAttributes(&fa, kern));
-  if (fa.numRegs < kPairRegsAtLaunch) return MOE_ERR_CUDA;  // the raise of the registers would wait forever
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * num_sms());
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPairSmem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  MOE_CUDA(cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg));
-  if (pairs < 1) return MOE_ERR_CUDA;
-  known[i].store(pairs, std::memory_order_relaxed);
-  return MOE_OK;
+  static std::atomic<int> known[64 * kMaxSlices];
+  static std::atomic<bool> checked;
+  if (!checked.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa;
+    MOE_CUDA(cudaFuncGetAttributes(&fa, linear_fp8_pair_kernel<ACT>));
+    if (fa.numRegs < kPairRegsAtLaunch) return MOE_ERR_CUDA;  // the raise of the registers would wait forever
+    checked.store(true, std::memory_order_relaxed);
+  }
+  return resident(reinterpret_cast<const void*>(linear_fp8_pair_kernel<ACT>), 2, kPairThreads, kPairSmem, known, pairs);
 }
 
-// Pairs, or single blocks with K in slices: the one of less estimated time. A wave of single blocks takes 0.36 us
-// a block of K and 2.5 us around it; one of pairs 0.46 us (for four times the columns and rows) and 1.3, and 4 us once.
-bool use_pairs(int M, int cols, int groups, bool gated) {
-  const int sms = num_sms(), out = gated ? 2 : 1;
-  const double tiles = ceil(M / 128.0) * ceil(cols * out / 128.0), pair_tiles = ceil(M / 256.0) * ceil(cols * out / 256.0);
-  int slices = 1;
-  while (slices < kMaxSlices && tiles * slices * 2 <= sms && groups >= 4 * slices) slices *= 2;
-  const double one = ceil(tiles * slices / sms) * (groups * 0.36 / slices + 2.5);
-  const double two = ceil(pair_tiles / (sms / 2)) * (groups * 0.46 + 1.3) + 4.0;
-  return two < one;
+// Pairs, or single blocks: the one of less estimated time. A wave of pairs takes 0.46 us a block of K (for four times the
+// rows and columns of a single block), 1.3 around it, and all of them 4 once.
+moe_status_t use_pairs(int M, int cols, int groups, bool gated, bool& pairs) {
+  const int out = gated ? 2 : 1;
+  const auto tiles = [&](int side) { return (M + side - 1ll) / side * ((static_cast<int64_t>(cols) * out + side - 1) / side); };
+  int slices = 1, at_once = 0;
+  double one = 0.0;
+  moe_status_t st = cut_tiles(M, groups, tiles(128), slices, one);
+  if (st != MOE_OK) return st;
+  st = resident_pairs<MOE_ACT_IDENTITY>(at_once);
+  if (st != MOE_OK) return st;
+  pairs = ceil(static_cast<double>(tiles(256)) / at_once) * (groups * 0.46 + 1.3) + 4.0 < one;
+  return MOE_OK;
 }
 
 template <int ACT>
@@ -718,7 +769,7 @@ moe_status_t launch_pairs(Fp8Args a, const void* x, int64_t ld_x, const void* w,
   a.m_tiles = (a.M - 1) / 256 + 1;
   const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.cols - 1) / kOut + 1);
   MOE_CHECK(tiles <= INT32_MAX / 2, MOE_ERR_UNSUPPORTED_SHAPE);
-  a.wide = a.cols % 8 == 0;
+  a.wide = row_pieces(a);
   if (!encode_rows(&a.tmap_x, x, a.K, a.M, ld_x, 128) || !encode_rows(&a.tmap_w, w, a.K, a.N, a.K, 64)) return MOE_ERR_CUDA;
   const auto kern = linear_fp8_pair_kernel<ACT>;
   MOE_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
@@ -763,7 +814,9 @@ moe_status_t linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, in
   a.withhold = topt.withhold_release;
   a.M = M, a.N = N, a.K = K, a.groups = groups, a.act = activation, a.cols = cols;
   a.xs_step = per_token ? 0 : 1, a.xs_ld = per_token ? 1 : groups;
-  const bool pairs = use_pairs(M, cols, groups, gated);
+  bool pairs = false;
+  const moe_status_t st = use_pairs(M, cols, groups, gated, pairs);
+  if (st != MOE_OK) return st;
   cudaStream_t s = as_stream(stream);
 #define MOE_FP8_CASE(ACT) \
   case ACT: return pairs ? launch_pairs<ACT>(a, x, ld_x, w, s) : launch_tiles<ACT>(a, x, ld_x, w, s)
