@@ -9,9 +9,9 @@
 // So a row needs no sort, only the last kept logit and how many of the tokens that share it are kept. It is found by
 // histograms: 2048 bins of 1/64 in (max - l) / temperature, then the keys (the logits' bits in their order) of the bin in
 // which the count or the weight is reached, 2048 ways a pass, until one key is left. BF16 logits mostly share one key by
-// then. Only tokens that can matter are counted: of the threads' largest logits the k-th, taken down to its bin's end, is
-// no larger than the k-th of all, and tokens below the part 1 - top_p of the mean weight cannot all together
-// reach that part of the sum. What is above such a bound goes to a list in shared memory, if it fits.
+// then. For top_k only tokens that can matter are counted: of the threads' largest logits the k-th, taken down to its bin's
+// end, is no larger than the k-th of all. What is above that bound, what short rows have, and what a bin has goes to a list
+// in shared memory, if it fits. Long rows of BF16 logits are counted by their values instead, which are few.
 //
 // Weights are whole numbers, 2^44 for the largest logit, so that sums are exact in any order and every
 // block of a row sees the same ones. A weight is right to 2^-34 of itself (2^-37 on average) and to a unit: of 131072
@@ -21,7 +21,8 @@
 // carried as two floats.
 //
 // A row is spread over a cluster of blocks; histograms and totals meet in distributed shared memory. The row
-// is read from L2 again for each pass over all of it: two where top_k is set, three for top_p alone, two for neither.
+// is read from L2 again for each pass over all of it: two where BF16 logits are counted by their values or no filter is
+// set, three or four else.
 #include <math.h>
 
 #include "cluster.cuh"
@@ -80,14 +81,17 @@ struct SampleArgs {
   int V, blocks;
 };
 
-// BF16 logits take few values. Those of magnitude 2^-8 to 2^7 have a bin each, in descending order, zero one between
-// the positive and the negative ones; the few nonzero ones nearer to zero (rare) are listed and count with zero.
+// BF16 logits take few values. Those of magnitude 2^-8 to 2^7 have a place each in tables, by their bits: the positive ones
+// in the first half, the negative ones in the second, zero last. In descending order they are the bins 0 to 2 * kSide, zero
+// in the middle; the few nonzero ones nearer to zero (rare) are listed and count with zero.
 constexpr uint32_t kSmallest = 0x3B80, kSide = 15 * 128;  // bits of 2^-8; values of a sign
-constexpr int kZeroBin = kSide, kValues = 2 * kBins;
-__device__ __forceinline__ int value_bin(uint32_t b) {    // of BF16 bits; below 0: not one of them
-  const uint32_t m = b & 0x7FFFu, off = m - kSmallest;
-  if (off < kSide) return b & 0x8000u ? kSide + 1 + off : kSide - 1 - off;
-  return m == 0 ? kZeroBin : -1;
+constexpr int kZeroBin = kSide, kValues = 2 * kBins, kZeroPlace = kValues - 1;
+__device__ __forceinline__ int value_place(uint32_t b) {  // of BF16 bits; below 0: not one of them, or zero
+  const uint32_t off = (b & 0x7FFFu) - kSmallest;
+  return off < kSide ? static_cast<int>(off + ((b & 0x8000u) >> 4)) : -1;
+}
+__device__ __forceinline__ int bin_place(int bin) {
+  return bin < kZeroBin ? kSide - 1 - bin : bin == kZeroBin ? kZeroPlace : bin <= 2 * static_cast<int>(kSide) ? kBins + bin - kZeroBin - 1 : kSide;
 }
 __device__ __forceinline__ float bin_value(int bin) {
   if (bin == kZeroBin || bin > 2 * static_cast<int>(kSide)) return bin == kZeroBin ? 0.0f : -INFINITY;
@@ -112,8 +116,8 @@ struct Shared {
   uint64_t warp_a[32];
   uint32_t warp_b[32], warp_c[32];
   // what each block of the row has to tell, written by them; one array for each meeting, since blocks may be one apart
-  uint64_t peer_total[kMaxBlocks], peer_sum[kMaxBlocks], peer_rare[kMaxBlocks];
-  uint32_t peer_others[kMaxBlocks], peer_below[kMaxBlocks];
+  uint64_t peer_sum[kMaxBlocks], peer_rare[kMaxBlocks];
+  uint32_t peer_others[kMaxBlocks];
   uint32_t peer_top[kMaxBlocks], peer_far[kMaxBlocks], peer_rares[kMaxBlocks], peer_low[kMaxBlocks], peer_high[kMaxBlocks], peer_same[kMaxBlocks];
   uint64_t before, target;
   int bin, listed;
@@ -428,12 +432,16 @@ struct Row {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint32_t b = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu;
-      const int bin = value_bin(b);
-      if (bin >= 0) {
-        atomicAdd(&s.count[bin], 1u);
+      const int place = value_place(b);
+      if (place >= 0) {
+        atomicAdd(&s.count[place], 1u);
       } else if ((b & 0x7FFFu) < kSmallest) {
-        const int at = atomicAdd(&s.listed, 1);
-        if (at < kList) s.list[at] = b << 16;
+        if ((b & 0x7FFFu) == 0) {
+          atomicAdd(&s.count[kZeroPlace], 1u);
+        } else {
+          const int at = atomicAdd(&s.listed, 1);
+          if (at < kList) s.list[at] = b << 16;
+        }
       } else {
         far = fmaxf(far, __uint_as_float(b << 16));
       }
@@ -499,10 +507,11 @@ struct Row {
     const uint32_t* const counts = blocks > 1 ? s.counts : s.count;
     bool other = far;  // than the largest logit
 #pragma unroll 1
-    for (int bin = threadIdx.x; bin < kValues; bin += kThreads) {
-      if (counts[bin]) {
+    for (int bin = threadIdx.x; bin <= 2 * kSide; bin += kThreads) {
+      const int at = bin_place(bin);
+      if (counts[at]) {
         const float value = bin_value(bin);
-        s.weight[bin] = weight(value);
+        s.weight[at] = weight(value);
         other = other || value != top;
       }
     }
@@ -511,11 +520,11 @@ struct Row {
     uint32_t n[kOwn];
     uint64_t w[kOwn], part[kOwn];
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) n[i] = counts[kOwn * threadIdx.x + i];
+    for (int i = 0; i < kOwn; ++i) n[i] = counts[bin_place(kOwn * threadIdx.x + i)];  // place kSide, for those past the last, is empty
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) w[i] = n[i] ? s.weight[kOwn * threadIdx.x + i] : 0;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) s.count[kOwn * threadIdx.x + i] = 0;
+    for (int i = 0; i < kOwn; ++i) w[i] = n[i] ? s.weight[bin_place(kOwn * threadIdx.x + i)] : 0;
+    __syncthreads();  // the counts are read
+    for (int i = threadIdx.x; i < kValues; i += kThreads) s.count[i] = 0;
     constexpr int zero_thread = kZeroBin / kOwn, zero_at = kZeroBin % kOwn;
     const bool zero = threadIdx.x == zero_thread && rares;
     other = other || zero;
@@ -546,15 +555,20 @@ struct Row {
       reach_value(part, 0, p, other);
       end = s.bin;
       if (end == kZeroBin && rares) return false;
-      end_count = static_cast<uint32_t>((s.target - s.before + s.weight[end] - 1) / s.weight[end]);
+      const uint64_t each = s.weight[bin_place(end)];
+      end_count = static_cast<uint32_t>((s.target - s.before + each - 1) / each);
     }
-    if (end < kValues) tau = key_of(bin_value(end)), ties = end_count, tie_weight = s.weight[end];
+    if (end < kValues) {
+      tau = key_of(bin_value(end)), ties = end_count, tie_weight = s.weight[bin_place(end)];
+      __syncthreads();  // ... and from here on the table holds what tokens above tau weigh
+      for (int bin = end + threadIdx.x; bin <= 2 * static_cast<int>(kSide); bin += kThreads) s.weight[bin_place(bin)] = 0;
+    }
     return true;
   }
 
   // Cuts the kept tokens to the shortest front part whose count or weight reaches the target.
   template <bool WEIGHTS>
-  __device__ __forceinline__ void cut(uint64_t target, const float* p) {
+  __device__ __forceinline__ void cut(const float* p, uint64_t target = 0) {
     const bool group = WEIGHTS && ties > 0;            // kept tokens of key tau,
     const bool mine = group && rank == 0 && threadIdx.x == 0;  // added by one thread
     const uint64_t group_weight = ties * tie_weight;
@@ -578,8 +592,20 @@ struct Row {
     const int bin = s.bin;
     uint64_t left = s.target - s.before;
     uint32_t low = 0xFFFFFFFFu, high = 0;
+    // the bin's keys go to the list, if it is free and they are not too many
+    const bool had = listed;
+    if (!had) {
+      if (threadIdx.x == 0) s.listed = 0;
+      __syncthreads();
+    }
     each([&](float l, uint32_t key) {
-      if (key > tau && bin_of(l) == bin) low = min(low, key), high = max(high, key);
+      if (key > tau && bin_of(l) == bin) {
+        low = min(low, key), high = max(high, key);
+        if (!had) {
+          const int at = atomicAdd(&s.listed, 1);
+          if (at < kList) s.list[at] = key;
+        }
+      }
     });
     if (mine && bin_of(value_of(tau)) == bin) low = min(low, tau), high = max(high, tau);
     low = __reduce_min_sync(0xffffffffu, low);
@@ -587,6 +613,7 @@ struct Row {
     const int lane = threadIdx.x & 31;
     if (lane == 0) s.warp_b[threadIdx.x >> 5] = low, s.warp_c[threadIdx.x >> 5] = high;
     __syncthreads();
+    listed = had || s.listed <= kList;
     low = __reduce_min_sync(0xffffffffu, lane < kWarps ? s.warp_b[lane] : 0xFFFFFFFFu);
     high = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.warp_c[lane] : 0);
     if (blocks > 1) {
@@ -612,6 +639,7 @@ struct Row {
       const uint32_t span = (1u << shift) - 1u;
       if (high - low > span) low = high - span;
     }
+    listed = had;
     tau = low;
     tie_weight = weight(value_of(tau));
     ties = static_cast<uint32_t>(WEIGHTS ? (left + tie_weight - 1) / max(tie_weight, uint64_t(1)) : left);
@@ -645,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   const bool top_k = k > 0 && k < a.V, top_p = p < 1.0f, greedy = !(t >= 0x1p-100f);
   float own = -INFINITY;  // this thread's largest logit
   float away = -INFINITY;
-  const bool counted = sizeof(T) == 2 && !greedy && (top_k || top_p);
+  const bool counted = sizeof(T) == 2 && !greedy && (top_k || top_p) && per * kVec > kList;
   if (counted) __syncthreads();  // the counts are 0
   r.pieces([&](const uint4& w, float m) {
     own = fmaxf(own, m);
@@ -674,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   }
   r.top = value_of(best);
   uint64_t least = 0;  // weight of a kept token
-  bool valued = false;  // the weights of values are there
+  bool valued = false, table = false;  // the weights of values are there; and those of no others than are kept
   if (greedy) {
     r.tau = best, r.ties = 1, r.tie_weight = kOne;
   } else {
@@ -693,7 +721,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
       if (!counted) {  // without counts, a table of all values pays for long rows only
         valued = valued && per * kVec > 2 * kValues;
         if (valued) {
-          for (int i = threadIdx.x; i < kValues; i += kThreads) s.weight[i] = bin_value(i) > r.top ? 0 : r.weight(bin_value(i));
+          for (int i = threadIdx.x; i <= 2 * static_cast<int>(kSide); i += kThreads)
+            s.weight[bin_place(i)] = bin_value(i) > r.top ? 0 : r.weight(bin_value(i));
           __syncthreads();
         }
       } else if (valued) {
@@ -703,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
       }
       if (counted) __syncthreads();
     }
+    table = valued && (cut || !counted);
     if (!cut) {
       if (top_k) {
         // a row's blocks have like numbers of tokens, and agree on what they do together
@@ -715,45 +745,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
           const int bin = s.bin;
           if (bin >= 0 && bin < kBins - 1 && isfinite(r.top)) r.gather(below(bin + 1.0f, r.step));
         }
-        r.template cut<false>(k, nullptr);
+        r.template cut<false>(nullptr, k);
       }
       if (top_p) {
-        uint64_t sum = 0, front = 0;
-        if (top_k || per * kVec <= kList) {
-          if (!top_k) r.gather(-INFINITY);
-        } else {
-          bool others = false;
-          r.pieces([&](const uint4& w, float m) {
-            others = others || (m > -INFINITY && m < r.top);
-            if (!((r.top - m) * r.ch < 46.0f) && m != r.top) return;
-            float v[kVec];
-            Row<T>::unpack(w, v);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-              sum += weight_of(s.power, r.top, r.ch, r.cl, v[e]);
-              others = others || (v[e] > -INFINITY && v[e] < r.top);
-            }
-          });
-          sum = warp_sum(sum);
-          if (lane == 0) s.warp_a[warp] = sum;
-          others = __syncthreads_or(others);
-          sum = warp_sum(lane < kWarps ? s.warp_a[lane] : 0);
-          if (a.blocks > 1) {
-            if (threadIdx.x < a.blocks) {
-              store_cluster(cluster_address(&s.peer_total[rank], threadIdx.x), sum);
-              store_cluster(cluster_address(&s.peer_below[rank], threadIdx.x), others ? 1u : 0u);
-            }
-            r.sync();
-            sum = 0;
-            for (int i = 0; i < a.blocks; ++i) sum += s.peer_total[i], others = others || s.peer_below[i];
-          } else {
-            __syncthreads();
-          }
-          const float bits = __log2f(__ull2float_rn(sum) * 0x1p-44f * a.V / (1.0f - part)) + 0.01f;
-          if (isfinite(r.top)) r.gather(below(bits, r.ch));
-          front = Row<T>::front_of(part, sum, others);
-        }
-        r.template cut<true>(front, front ? nullptr : &part);
+        if (!top_k && per * kVec <= kList) r.gather(-INFINITY);
+        r.template cut<true>(&part);
       }
     }
     if (q > 0.0f) {
@@ -761,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
       const float kept = fminf(q, 1.0f);
       least = kept == 1.0f ? kOne : part_of(kept, kOne, rest) + rest;
       if (r.tie_weight < least) r.ties = 0;
+      table = false;
     }
   }
 
@@ -768,14 +765,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   const float last_kept = value_of(r.tau);
   const auto kept = [&](const uint4& piece, float m, uint64_t& sum, uint32_t& same) {
     if (!(m >= last_kept) || m == -INFINITY) return;
+    if constexpr (sizeof(T) == 2) {
+      if (table && last_kept != 0.0f) {  // by the table alone
+        const uint32_t tie = __float_as_uint(last_kept) >> 16;
+        const uint32_t w[4] = {piece.x, piece.y, piece.z, piece.w};
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const uint32_t b = e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu;
+          const int place = value_place(b);
+          if (place >= 0) sum += s.weight[place];
+          else if (__uint_as_float(b << 16) > last_kept) sum += r.weight(__uint_as_float(b << 16));
+          same += b == tie;
+        }
+        return;
+      }
+    }
     float v[kVec];
     Row<T>::unpack(piece, v);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       if (v[e] > last_kept) {
+        const int place = sizeof(T) == 2 && valued ? value_place(__float_as_uint(v[e]) >> 16) : -1;
         uint64_t x;
-        const int bin = sizeof(T) == 2 && valued ? value_bin(__float_as_uint(v[e]) >> 16) : -1;
-        if (bin >= 0) x = s.weight[bin];
+        if (place >= 0) x = s.weight[place];
         else x = r.weight(v[e]);
         if (x >= least) sum += x;
       }
