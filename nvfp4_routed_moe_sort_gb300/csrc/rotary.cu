@@ -147,7 +147,9 @@ template <bool ADJACENT>
 __global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens, FastDiv per_token, FastDiv per_head, FastDiv halves) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint64_t* const turns = reinterpret_cast<uint64_t*>(raw);                    // [half]
-  float2* const phase = reinterpret_cast<float2*>(turns + a.half);             // [tokens][half]
+  // [tokens][half], two neighbouring pairs of each eight after the other: threads side by side read side by side (eight
+  // pairs in a row cost four times the shared memory's turns, and 2 us of 10)
+  float2* const phase = reinterpret_cast<float2*>(turns + a.half);
   uint8_t* const axis = reinterpret_cast<uint8_t*>(phase + tokens * a.half);   // [half]
   pdl_wait();
   pdl_trigger();
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens
     const int token = per_token(j), r = j - token * per_token.d, head = per_head(r), c = r - head * per_head.d;
     t = head >= a.heads[0];
     n = n0 + token;
-    at = token * a.half + 8 * c;
+    at = token * a.half + 2 * c;
     return (t ? head - a.heads[0] : head) * a.dim + c * (ADJACENT ? 16 : 8);
   };
   const auto fetch = [&] {
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens
   __syncthreads();
   for (int i = threadIdx.x; i < here * a.half; i += 256) {
     const int n = halves(i), f = i - n * a.half;
-    phase[i] = phase_of(position_of(a, n0 + n, axis[f]), turns[f]);
+    phase[n * a.half + ((f >> 1 & 3) * per_head.d + (f >> 3)) * 2 + (f & 1)] = phase_of(position_of(a, n0 + n, axis[f]), turns[f]);
   }
   __syncthreads();
   while (j < all) {
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens
     uint16_t* const to = (t ? a.out[1] : a.out[0]) + n * (t ? a.ld_out[1] : a.ld_out[0]) + in;
     float2 p[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = reinterpret_cast<const float4*>(phase + at)[i];
+    for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = *reinterpret_cast<const float4*>(phase + at + i * 2 * per_head.d);
     turn8<ADJACENT>(u, v, p);
     *reinterpret_cast<uint4*>(to) = u;
     *reinterpret_cast<uint4*>(to + apart) = v;
