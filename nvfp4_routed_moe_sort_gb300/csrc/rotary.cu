@@ -144,7 +144,8 @@ __device__ __forceinline__ void turn8(uint4& u, uint4& v, const float2* p) {
 // What is not turned is copied where `out` is not `in`. More pieces in flight a thread cost more in resident warps than
 // they gain (4: 110 -> 115 us for the long prompt, 16 -> 20 for the images).
 template <bool ADJACENT>
-__global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens, FastDiv per_token, FastDiv per_head, FastDiv halves) {
+__global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens, FastDiv per_token, FastDiv per_head, FastDiv halves,
+                                                        FastDiv rest_token, FastDiv rest_head) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint64_t* const turns = reinterpret_cast<uint64_t*>(raw);                    // [half]
   // [tokens][half], two neighbouring pairs of each eight after the other: threads side by side read side by side (eight
@@ -175,6 +176,18 @@ __global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens
     v = __ldcs(reinterpret_cast<const uint4*>(from + apart));
   };
   if (j < all) fetch();
+  // what is not turned, while the phases wait for their inputs
+  const int rest = rest_head.d;
+  if (a.copy[0] || a.copy[1]) {
+    for (int i = threadIdx.x + blockIdx.y * 256; i < here * rest_token.d; i += step) {
+      const int n = rest_token(i), r = i - n * rest_token.d, head = rest_head(r);
+      const int t = head >= a.heads[0];
+      const int64_t place = (t ? head - a.heads[0] : head) * a.dim + 2 * a.half + (r - head * rest) * 8;
+      if (t ? a.copy[1] : a.copy[0])
+        *reinterpret_cast<uint4*>((t ? a.out[1] : a.out[0]) + (n0 + n) * (t ? a.ld_out[1] : a.ld_out[0]) + place) =
+            __ldcs(reinterpret_cast<const uint4*>((t ? a.in[1] : a.in[0]) + (n0 + n) * (t ? a.ld_in[1] : a.ld_in[0]) + place));
+    }
+  }
   for (int i = threadIdx.x; i < a.half; i += 256) {
     uint64_t t = turns_of(a.inv_freq[i]);
     axis[i] = static_cast<uint8_t>(axis_of(a, i, t));
@@ -200,18 +213,6 @@ __global__ void __launch_bounds__(256, 8) rotary_kernel(RotaryArgs a, int tokens
     j += step;
     if (j < all) fetch();
   }
-  const int rest = (a.dim - 2 * a.half) / 8;
-  if (rest > 0 && (a.copy[0] || a.copy[1])) {
-    const int heads = a.heads[0] + a.heads[1];
-    for (int i = threadIdx.x + blockIdx.y * 256; i < here * heads * rest; i += step) {
-      const int n = i / (heads * rest), r = i - n * heads * rest, head = r / rest;
-      const int t = head >= a.heads[0];
-      const int64_t place = (t ? head - a.heads[0] : head) * a.dim + 2 * a.half + (r - head * rest) * 8;
-      if (a.copy[t])
-        *reinterpret_cast<uint4*>(a.out[t] + (n0 + n) * a.ld_out[t] + place) =
-            *reinterpret_cast<const uint4*>(a.in[t] + (n0 + n) * a.ld_in[t] + place);
-    }
-  }
 }
 
 template <bool ADJACENT>
@@ -227,7 +228,11 @@ moe_status_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
   while (split < 16 && blocks * split * 2 <= sms * 2 && per * tokens > 256 * split) split *= 2;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
   const size_t smem = static_cast<size_t>(a.half) * (sizeof(uint64_t) + tokens * sizeof(float2) + 1);
-  return launch_pdl(rotary_kernel<ADJACENT>, grid, dim3(256), smem, s, a, tokens, FastDiv(per), FastDiv(chunks), FastDiv(a.half));
+  RotaryArgs b = a;
+  const int rest = (a.dim - 2 * a.half) / 8, left = rest > 0 ? rest : 1;
+  if (rest == 0) b.copy[0] = b.copy[1] = 0;
+  return launch_pdl(rotary_kernel<ADJACENT>, grid, dim3(256), smem, s, b, tokens, FastDiv(per), FastDiv(chunks), FastDiv(a.half),
+                    FastDiv((a.heads[0] + a.heads[1]) * left), FastDiv(left));
 }
 
 // rows of `width` values every `ld` values; whether two of them share memory. Slices of one wider row do not.
