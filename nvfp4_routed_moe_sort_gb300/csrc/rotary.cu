@@ -12,8 +12,9 @@
 // cosine are those of a float32 in [-1, 1) times pi.
 //
 // Bound by HBM (4 bytes a turned value): a piece of 16 bytes is read once and written once, each thread fetching its
-// next one before it writes. Measured: 8 tokens of 20 heads of 128 2.7 us, 4099 tokens of 32 heads, three quarters of each
-// turned, 16 us (4.2 TB/s with what is copied), 16384 tokens of 72 heads 109 us (5.5 TB/s, 82 % of the copy rate).
+// next one before it writes; what is not turned is copied while the phases are made. Measured: 8 tokens of 20 heads of
+// 128 2.7 us (a launch), 4099 tokens of 32 heads, three quarters of each turned, 14 us (4.7 TB/s with what is copied),
+// 16384 tokens of 72 heads 93 us (6.5 TB/s, 95 % of the copy rate; 109 with phases that met in shared memory's banks).
 #include "common.cuh"
 #include "host_util.h"
 

@@ -23,6 +23,10 @@
 // A row is spread over a cluster of blocks; histograms and totals meet in distributed shared memory. The row
 // is read from L2 again for each pass over all of it: two where BF16 logits are counted by their values or no filter is
 // set, three or four else.
+//
+// Bound by the chain of passes and meetings where rows are few (one row of 129021 BF16 logits: all tokens 14 us, top-k 18,
+// top-p 20), by the shared-memory additions and the instructions around them where they are many (128 such rows: 35, 37 and
+// 49 us; FP32 logits 60, 48 and 134). One row of 1001 FP32 logits: 5 to 12 us.
 #include <math.h>
 
 #include "cluster.cuh"
