@@ -542,7 +542,7 @@ MOE_API moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const float*
  *   num_axes    1 to 4: one for text; time, height and width for images and video
  *   inv_freq    [rotary_dim / 2] float64, finite: radians per position
  *   axes        [rotary_dim / 2] uint8: the axis of each pair, or NULL with one axis. A pair of an axis
- *               that is none is not turned and sets MOE_DEV_BAD_INDEX
+ *               that is none is turned by the angle 0 and sets MOE_DEV_BAD_INDEX
  *   q_out, k_out  like q and k, with strides of their own; each may be its input itself (same stride)
  *   dev_status  may be NULL
  * Up to 1024 heads each. N == 0 is a no-op. rotary_dim a multiple of 16 and 16-byte aligned tokens are fastest.

@@ -659,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t b = blockIdx.x / a.blocks;
   const int rank = static_cast<int>(blockIdx.x % a.blocks);
+  if (a.blocks > 1) cluster_arrive();  // this block has started: its shared memory may be written
   for (int i = threadIdx.x; i < 1 << (kStepBits - 1); i += kThreads)
     reinterpret_cast<uint4*>(s.power)[i] = reinterpret_cast<const uint4*>(kPowers.t)[i];
   for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = 0;
@@ -691,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   far = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.warp_c[lane] : 0);
   if (s.listed > kList) far = 0xFFFFFFFFu;  // too many rare ones
   if (a.blocks > 1) {
+    cluster_wait();
     if (threadIdx.x < a.blocks) {
       store_cluster(cluster_address(&s.peer_top[rank], threadIdx.x), best);
       store_cluster(cluster_address(&s.peer_far[rank], threadIdx.x), far);
