@@ -134,6 +134,13 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// 32 bytes at a multiple of 32
+__device__ __forceinline__ void store_sector(uint16_t* to, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // as arrive_cluster() does, in this block
 __device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -145,7 +152,6 @@ constexpr int kOperand = 128 * 128;       // bytes of a stage's w (and of its x,
 constexpr int kMaxSlices = 8;
 constexpr int kSumLd = kCols + 4;         // of a row of sums in shared memory: no bank conflicts
 constexpr int kThreads = 384;             // warps: copies, two of MMAs, scales, eight of sums
-constexpr int kTurnLd = 18;               // of 32 rows of 16 values that a warp turns in shared memory
 constexpr int kScaleRun = 8;              // blocks of K whose scales are fetched together: a sector of x_scale
 constexpr int kScaleBytes = 2 * kScaleRun * (128 + 2) * 4;
 constexpr int kBarBytes = 256;
@@ -171,46 +177,90 @@ __device__ __forceinline__ void fetch_scales(const Fp8Args& a, int run, int kb, 
     w_ring[(run & 1) * 2 * kScaleRun + lane] = __ldg((lane & 1 ? ws2 : ws) + min(kb + (lane >> 1), a.groups - 1));
 }
 
-// N values of a row (N / 32 warps' worth of columns from c0 on) to out: whole 16-byte pieces where rows are made of
-// them, else 32 x 16 values at a time change hands in shared memory and the warp writes row by row.
+// N neighbouring values, a pair to a word, to any place in a row: `some` of them, the others lie behind the row. The ones
+// before the first whole sector go in pieces of 1, 2, 4 and 8 values, each at a multiple of its size, and what follows
+// moves up by as many; so do the ones behind the last. (Through shared memory, value by value in row order, 2048 x 129021 x
+// 512 took twice the time of 2048 x 129024 x 512.)
 template <int N>
-__device__ __forceinline__ void store_rows(const Fp8Args& a, const float* v, int64_t first, int c0, uint16_t* turn, int lane) {
-  if (a.wide == 2) {  // whole sectors
-    if (first + lane < a.M) {
-      uint16_t* const to = a.out + (first + lane) * a.cols + c0;
+__device__ __forceinline__ void store_odd(uint32_t (&w)[N / 2], uint16_t* to, int some) {
+  if (some < 16) {
 #pragma unroll
-      for (int i = 0; i < N / 16; ++i) {
-        uint32_t w[8];
+    for (int i = 0; i < 15; ++i)
+      if (i < some) to[i] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+    return;
+  }
+  const uint32_t head = (0 - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to) >> 1)) & 15;
+  const auto up = [&](int words) {  // moves all of them by `words`
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = bf16x2(v[16 * i + 2 * e], v[16 * i + 2 * e + 1]);
-        if (c0 + 16 * i < a.cols)
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * i), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                       "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                       : "memory");
-      }
-    }
-  } else if (a.wide) {
-    if (first + lane < a.M) {
-      uint16_t* const to = a.out + (first + lane) * a.cols + c0;
+    for (int i = 0; i < N / 2; ++i) w[i] = i + words < N / 2 ? w[i + words] : 0;
+  };
+  if (head & 1) *to = static_cast<uint16_t>(w[0]);
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i)
-        if (c0 + 8 * i < a.cols)
-          *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(bf16x2(v[8 * i], v[8 * i + 1]), bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                                             bf16x2(v[8 * i + 4], v[8 * i + 5]), bf16x2(v[8 * i + 6], v[8 * i + 7]));
-    }
+  for (int i = 0; i < N / 2; ++i) w[i] = __funnelshift_r(w[i], i + 1 < N / 2 ? w[i + 1] : 0, (head & 1) * 16);
+  to += head & 1;
+  if (head & 2) {
+    *reinterpret_cast<uint32_t*>(to) = w[0];
+    up(1);
+  }
+  to += head & 2;
+  if (head & 4) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+    up(2);
+  }
+  to += head & 4;
+  if (head & 8) {
+    *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    up(4);
+  }
+  to += head & 8;
+  const int left = some - static_cast<int>(head), whole = left >> 4;
+  uint32_t z[8];  // what is behind the whole sectors
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = 0;
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) {
+    if (i < whole) store_sector(to + 16 * i, w + 8 * i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = i == whole ? w[8 * i + e] : z[e];
+  }
+  to += 16 * whole;
+  if (left & 8) {
+    *reinterpret_cast<uint4*>(to) = make_uint4(z[0], z[1], z[2], z[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = z[e + 4];
+  }
+  to += left & 8;
+  if (left & 4) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(z[0], z[1]);
+    z[0] = z[2], z[1] = z[3];
+  }
+  to += left & 4;
+  if (left & 2) {
+    *reinterpret_cast<uint32_t*>(to) = z[0];
+    z[0] = z[1];
+  }
+  to += left & 2;
+  if (left & 1) *to = static_cast<uint16_t>(z[0]);
+}
+
+// N values of a thread's row, from column c0 on, to out
+template <int N, bool GATED>
+__device__ __forceinline__ void store_row(const Fp8Args& a, const float* v, int64_t row, int c0) {
+  if (row >= a.M || c0 >= a.cols) return;
+  uint16_t* const to = a.out + row * a.cols + c0;
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+  if (a.wide == 2) {
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i)
+      if (c0 + 16 * i < a.cols) store_sector(to + 16 * i, w + 8 * i);
+  } else if (GATED || a.wide) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i)
+      if (c0 + 8 * i < a.cols) *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   } else {
-#pragma unroll
-    for (int c = 0; c < N / 16; ++c) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(turn + lane * kTurnLd + 2 * i) = bf16x2(v[16 * c + 2 * i], v[16 * c + 2 * i + 1]);
-      __syncwarp();
-      const int col = c0 + 16 * c + (lane & 15);
-      if (col < a.cols) {
-        uint16_t* const to = a.out + first * a.cols + col;
-        for (int r = lane >> 4; r < min(int64_t(32), a.M - first); r += 2) to[static_cast<int64_t>(r) * a.cols] = turn[r * kTurnLd + (lane & 15)];
-      }
-      __syncwarp();
-    }
+    store_odd<N>(w, to, min(N, a.cols - c0));
   }
 }
 
@@ -357,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < (GATED ? 32 : 64); ++i) acc[i] = activate(ACT, acc[i], GATED ? acc[32 + (i & 31)] : 0.0f);
       }
-      store_rows<GATED ? 32 : 64>(a, acc, m0 + quarter * 32, n0 + half * (GATED ? 32 : 64),
-                                  reinterpret_cast<uint16_t*>(sums) + (warp - 4) * 32 * kTurnLd, lane);
+      store_row<GATED ? 32 : 64, GATED>(a, acc, static_cast<int64_t>(m0) + r, n0 + half * (GATED ? 32 : 64));
     } else {
       cluster_wait();  // every block of the cluster runs
       // The rows of the tile are dealt out to its slices, which add up their rows' sums: row r to block r / per.
@@ -385,6 +434,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
   }
   if (a.slices == 1) return;
   const int per = (rows + a.slices - 1) / a.slices, first = slice * per, mine = min(per, rows - first);
+  if (!GATED && !a.wide) {  // columns side by side to threads side by side
+    for (int i = threadIdx.x; i < mine * kOut; i += kThreads) {
+      const int r = i / kOut, c = i % kOut;
+      if (n0 + c >= a.cols) continue;
+      float v = 0.0f;
+      for (int s = 0; s < a.slices; ++s) v += sums[(s * per + r) * kSumLd + c];
+      a.out[static_cast<int64_t>(m0 + first + r) * a.cols + n0 + c] = __bfloat16_as_ushort(__float2bfloat16_rn(activate(ACT, v, 0.0f)));
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < mine * (kOut / 4); i += kThreads) {  // four columns each
     const int r = i / (kOut / 4), c = i % (kOut / 4) * 4;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -400,13 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = activate(ACT, v[e], u[e]);
     uint16_t* const to = a.out + static_cast<int64_t>(m0 + first + r) * a.cols + n0 + c;
-    if (a.wide) {
-      if (n0 + c < a.cols) *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n0 + c + e < a.cols) to[e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
-    }
+    if (n0 + c < a.cols) *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
   }
 }
 
@@ -468,7 +521,7 @@ moe_status_t launch_tiles(Fp8Args a, const void* x, int64_t ld_x, const void* w,
   MOE_CHECK(tiles * a.slices <= INT32_MAX, MOE_ERR_UNSUPPORTED_SHAPE);
   a.wide = row_pieces(a);
   const int held = a.M < kRows ? a.M : kRows;
-  int sums = a.slices > 1 ? (held + a.slices - 1) / a.slices * a.slices * kSumLd * 4 : 8 * 32 * kTurnLd * 2;
+  int sums = a.slices > 1 ? (held + a.slices - 1) / a.slices * a.slices * kSumLd * 4 : 0;
   // The MMA reads 128 rows of x where fewer were loaded (what it makes of the others is not used): they lie in the
   // following stages, and after the last one in what follows the stages.
   if (sums < kOperand - kScaleBytes - kBarBytes) sums = kOperand - kScaleBytes - kBarBytes;
@@ -521,7 +574,7 @@ constexpr int kPairCols = 256;         // of a tile, and of one accumulator
 constexpr int kPairThreads = 512;      // warps: three of copies, four of MMAs, scales, eight of sums
 constexpr int kPairRegs = 208, kPairRegsOther = 48, kPairRegsAtLaunch = 128;
 static_assert(256 * kPairRegs + 256 * kPairRegsOther <= kPairThreads * kPairRegsAtLaunch, "the raise draws on the launch's registers");
-constexpr int kPairSmem = 1024 + kPairStages * 2 * kOperand + 8 * 32 * kTurnLd * 2 + kScaleBytes + kBarBytes;
+constexpr int kPairSmem = 1024 + kPairStages * 2 * kOperand + kScaleBytes + kBarBytes;
 constexpr int kPairGroup = 8;          // row tiles that follow one another before the next column tile
 
 template <int ACT>
@@ -529,8 +582,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
   constexpr bool GATED = is_gated(ACT);
   extern __shared__ uint8_t raw[];
   uint8_t* const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint16_t* const turn = reinterpret_cast<uint16_t*>(smem + kPairStages * 2 * kOperand);
-  float* const x_ring = reinterpret_cast<float*>(turn + 8 * 32 * kTurnLd);  // [2][kScaleRun][128 rows]
+  float* const x_ring = reinterpret_cast<float*>(smem + kPairStages * 2 * kOperand);  // [2][kScaleRun][128 rows]
   float* const w_ring = x_ring + 2 * kScaleRun * 128;                        // [2][kScaleRun][halves, or gate and up]
   uint64_t* const full = reinterpret_cast<uint64_t*>(w_ring + 2 * kScaleRun * 2);
   uint64_t* const done = full + kPairStages;   // a stage's products are summed, one for each half of its columns
@@ -715,14 +767,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
       if (!ok) break;
       int m0, n0;
       place(t, m0, n0);
-      const int first = m0 + rank * 128 + quarter * 32;  // the warp's rows
       constexpr int kMine = GATED ? 64 : 128;            // columns of out
       const int c0 = n0 + half * kMine;
       if constexpr (ACT != MOE_ACT_IDENTITY) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i) acc[i] = activate(ACT, acc[i], GATED ? acc[64 + (i & 63)] : 0.0f);
       }
-      store_rows<kMine>(a, acc, first, c0, turn + (warp - 8) * 32 * kTurnLd, lane);
+      store_row<kMine, GATED>(a, acc, static_cast<int64_t>(m0) + rank * 128 + quarter * 32 + lane, c0);
     }
   }
   __syncwarp();
