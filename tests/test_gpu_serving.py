@@ -169,6 +169,19 @@ def test_linear_many_tiles(M, N, K, mode):
     assert_within(bf16_np(got[torch.from_numpy(rows)])[:, cols], out[:, cols], tol[:, cols])
 
 
+@pytest.mark.parametrize("M,K,columns", [(40, 128, range(113, 147)), (5, 1024, (113, 127, 129, 130, 132, 136, 145)),
+                                         (2600, 128, (898, 1025, 1026, 1028, 1037, 1039, 1041, 1042, 1151))])
+def test_linear_rows_at_every_place(M, K, columns):
+    """Rows of out that begin anywhere within a sector, and last tiles of any width."""
+    for N in columns:
+        c = linear_case(M, N, K)
+        g = Guarded(16)
+        out = g((M, N), torch.bfloat16)
+        pkg.fp8_linear(*c, out=out)
+        assert g.intact(), N
+        check_linear(out, *c)
+
+
 @pytest.mark.parametrize("M", [5, 200])
 def test_linear_slices_and_nothing_else(M):
     N, K = 300, 400
