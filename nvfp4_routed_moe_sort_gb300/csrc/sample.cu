@@ -24,10 +24,12 @@
 // is read from L2 again for each pass over all of it: two where BF16 logits are counted by their values or no filter is
 // set, three or four else.
 //
-// Bound by the chain of passes and meetings where rows are few (one row of 129021 BF16 logits: all tokens 14 us, top-k 18,
-// top-p 20), by the shared-memory additions and the instructions around them where they are many (128 such rows: 35, 37 and
+// Bound by the chain of passes and meetings where rows are few (one row of 129021 BF16 logits: all tokens 13 us, top-k 17,
+// top-p 18), by the shared-memory additions and the instructions around them where they are many (128 such rows: 35, 37 and
 // 49 us; FP32 logits 60, 48 and 134). One row of 1001 FP32 logits: 5 to 12 us.
 #include <math.h>
+
+#include <atomic>
 
 #include "cluster.cuh"
 #include "common.cuh"
@@ -38,7 +40,7 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kThreads = 512, kWarps = 16;
-constexpr int kMaxBlocks = 8;
+constexpr int kMaxBlocks = 16;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kList = 4096;
 constexpr uint32_t kNone = 0x007FFFFFu;  // the key of -infinity: such a token is never taken
@@ -906,17 +908,54 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   }
 }
 
-// Blocks of a row: more while they all fit the SMs twice and their parts are longer than 4096 tokens.
-int blocks_of(int B, int V) {
-  int n = 1;
-  while (n < kMaxBlocks && static_cast<int64_t>(B) * n * 2 <= 2 * num_sms() && V > 4096 * n) n *= 2;
-  return n;
+// Whether the current device runs clusters of kMaxBlocks, more than every device does: looked up once.
+template <typename T>
+moe_status_t large_clusters(bool& run) {
+  static std::atomic<int> known[64];  // 0: not asked yet, 1: no, 2: yes
+  int dev = 0;
+  MOE_CUDA(cudaGetDevice(&dev));
+  int answer = known[dev & 63].load(std::memory_order_relaxed);
+  if (answer == 0) {
+    MOE_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxBlocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxBlocks, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    MOE_CUDA(cudaOccupancyMaxActiveClusters(&clusters, reinterpret_cast<const void*>(sample_kernel<T>), &cfg));
+    answer = clusters >= 4 ? 2 : 1;
+    known[dev & 63].store(answer, std::memory_order_relaxed);
+  }
+  run = answer == 2;
+  return MOE_OK;
+}
+
+// Blocks of a row: more while they all fit the SMs twice and their parts are longer than 4096 tokens; 16 where few rows leave
+// half of the SMs free (129021 BF16 logits by top-p: one to four rows 20.4 -> 18.4 us, eight 20.6 -> 24.2; 40000 logits,
+// of which a block then has too few to count them by value, 17.0 -> 19.3).
+template <typename T>
+moe_status_t blocks_of(int B, int V, int& n) {
+  n = 1;
+  while (n < 8 && static_cast<int64_t>(B) * n * 2 <= 2 * num_sms() && V > 4096 * n) n *= 2;
+  if (n == 8 && B * kMaxBlocks <= num_sms() / 2 && V > 4096 * kMaxBlocks) {
+    bool large = false;
+    const moe_status_t st = large_clusters<T>(large);
+    if (st != MOE_OK) return st;
+    if (large) n = kMaxBlocks;
+  }
+  return MOE_OK;
 }
 
 template <typename T>
 moe_status_t launch_sample(SampleArgs a, int B, cudaStream_t s) {
-  a.blocks = blocks_of(B, a.V);
   MOE_CUDA(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared)));
+  const moe_status_t cut = blocks_of<T>(B, a.V, a.blocks);
+  if (cut != MOE_OK) return cut;
   return launch_clusters(sample_kernel<T>, a.blocks, dim3(static_cast<unsigned>(B) * a.blocks), dim3(kThreads), sizeof(Shared), s, a);
 }
 
