@@ -14,12 +14,12 @@
 // the four (-> 440); scales through shared memory by a warp of their own, read before the wait; copies by three warps; the
 // loads' barrier waited for before the accumulator's, whole warps that elect a lane for the MMAs (-> 332); packed
 // FP32 multiply-adds (-> 314); the last 64 columns' reads under the first ones' additions (-> 307); results stored by
-// whole 32-byte sectors (-> 290).
+// whole 32-byte sectors (-> 290), packed before any of them is (-> 282).
 //
 // Measured (us, in a graph): 4 x 2048 x 512 3.3, 16 x 4096 x 4096 6.7, 48 x 4096 x 7168 with SwiGLU 9.0, 256 x 4096 x 4096
-// 12.3, 333 x 7001 x 2000 15.5, 512 x 4096 x 4096 14.8, 1024 x 4096 x 4096 20 (1.7 PFLOP/s), 4096 x 4096 x 7168 with SwiGLU
-// 94 (2.55), 8192 x 7168 x 7168 290 (2.9; one after another for seconds the card's power limit lowers the clock to 1.7 GHz,
-// and it takes 320). With nothing read out, loaded or varied (a timing copy), the
+// 12.3, 333 x 7001 x 2000 13.4, 512 x 4096 x 4096 14.8, 1024 x 4096 x 4096 20 (1.7 PFLOP/s), 4096 x 4096 x 7168 with SwiGLU
+// 94 (2.55), 8192 x 7168 x 7168 282 (3.0; one after another for seconds the card's power limit lowers the clock to 1.7 GHz,
+// and it takes 320 to 330). With nothing read out, loaded or varied (a timing copy), the
 // MMAs alone reach 3.8 PFLOP/s at 4096 x 4096 x 16384, whose tiles fill 84 % of the pairs' turns.
 #include <math.h>
 
