@@ -457,6 +457,25 @@ def test_sample_logits_of_any_size(V, dtype):
             assert [got[b] for b in some_rows] == [S.sample(host[b], u[b], **{n: v[b] for n, v in kw.items()}) for b in some_rows], kw
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample_one_row_as_in_a_batch(dtype):
+    """A row's token does not depend on how many blocks share it: 1, 4, 20, 80 and 320 rows at a time."""
+    V, B = 70001, 320
+    r = np.random.default_rng(5)
+    x = r.normal(size=(8, V)).astype(np.float32) * np.array([[2.5], [1e-3], [60.0], [0.3], [2.5], [2.5], [0.0], [8.0]], np.float32)
+    x[4, r.random(V) < 0.9] = -np.inf
+    x[5, r.random(V) < 0.001] = np.nan
+    x = torch.from_numpy(x).to(dtype).to(DEV).repeat(B // 8, 1)
+    u = up(r.random(B).astype(np.float32))
+    kw = dict(temperature=r.choice([0.0, 0.7, 1.0, 3.0], B).astype(np.float32), top_k=r.choice([0, 1, 40, 5000, 69999], B).astype(np.int32),
+              top_p=r.choice([1.0, 0.9, 0.3], B).astype(np.float32), min_p=r.choice([0.0, 0.02], B).astype(np.float32))
+    kw = {n: up(v) for n, v in kw.items()}
+    want = pkg.sample_tokens(x, u, **kw)
+    for n in (1, 4, 20, 80):
+        got = [pkg.sample_tokens(x[i:i + n], u[i:i + n], **{k: v[i:i + n] for k, v in kw.items()}) for i in range(0, B, n)]
+        assert torch.equal(torch.cat(got), want), n
+
+
 def test_sample_settings_outside_their_range():
     r = np.random.default_rng(8)
     rows = [r.normal(size=50).astype(np.float32)] * 6
