@@ -194,25 +194,27 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// exp((l - top) / temperature) in units of 2^-44, ch + cl = log2(e) / temperature
+// exp((l - top) / temperature) in units of 2^-44, ch + cl = log2(e) / temperature. Every step rounds by itself, whatever the
+// compiler may contract: a multiply-add in place of p's product and a difference would count p's rounding twice (2^-19 of a
+// weight), and the places of this function have to agree to the bit.
 __device__ __forceinline__ uint64_t weight_of(const uint64_t* power, float top, float ch, float cl, float l) {
   if (l == top) return kOne;
-  const float d = top - l;
-  const float p = d * ch;
+  const float d = __fsub_rn(top, l);
+  const float p = __fmul_rn(d, ch);
   if (!(p < 46.0f)) return 0;
   // what d and p lost by rounding
-  const float back = top - d;
-  const float dl = (top - (d + back)) + (back - l);
-  float e = fmaf(d, ch, -p);
-  e = fmaf(d, cl, e);
-  e = fmaf(dl, ch, e);
+  const float back = __fsub_rn(top, d);
+  const float dl = __fadd_rn(__fsub_rn(top, __fadd_rn(d, back)), __fsub_rn(back, l));
+  float e = __fmaf_rn(d, ch, -p);
+  e = __fmaf_rn(d, cl, e);
+  e = __fmaf_rn(dl, ch, e);
   const float magic = 0x1.8p13f;  // rounds to multiples of 2^-10
-  const float k = p + magic;
+  const float k = __fadd_rn(p, magic);
   const int steps = static_cast<int>(__float_as_uint(k) - __float_as_uint(magic));
-  const float z = (p - (k - magic)) + e;
+  const float z = __fadd_rn(__fsub_rn(p, __fsub_rn(k, magic)), e);
   // 2^-z - 1, |z| <= 2^-11 and a bit: the cubic term is below 2^-37
-  const float x = z * fmaf(z, 0.240226507f, -0.693147181f);
-  const int part = __float2int_rn(x * 0x1p42f);
+  const float x = __fmul_rn(z, __fmaf_rn(z, 0.240226507f, -0.693147181f));
+  const int part = __float2int_rn(__fmul_rn(x, 0x1p42f));
   const uint64_t t = power[steps & ((1 << kStepBits) - 1)];
   const int64_t w = static_cast<int64_t>(t) + ((static_cast<int64_t>(static_cast<int32_t>(t >> 13)) * part) >> 29);
   return static_cast<uint64_t>(w) >> (steps >> kStepBits);
@@ -716,8 +718,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
   } else {
     const float limited = fminf(t, 0x1p100f);
     const float high = 1.44269502f, low = 1.92596299e-8f;  // log2(e)
-    r.ch = high / limited;
-    r.cl = (fmaf(-r.ch, limited, high) + low) / limited;
+    r.ch = __fdiv_rn(high, limited);
+    r.cl = __fdiv_rn(__fadd_rn(__fmaf_rn(-r.ch, limited, high), low), limited);
     r.step = r.ch * 44.3614196f;  // 64 ln 2: 64 bins where the weight falls by e
     // a bound is a little lower than its arithmetic in 32 bits says
     const auto below = [&](float units, float scale) { return r.top - units / scale * 1.0001f - fabsf(r.top) * 0x1p-20f; };
