@@ -763,9 +763,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a) {
       }
     }
     if (q > 0.0f) {
-      bool rest;
-      const float kept = fminf(q, 1.0f);
-      least = kept == 1.0f ? kOne : part_of(kept, kOne, rest) + rest;
+      bool rest = false;
+      least = kOne;
+      if (q < 1.0f) least = part_of(q, kOne, rest);
+      least += rest;  // the least whole number that is at least min_p
       if (r.tie_weight < least) r.ties = 0;
       table = false;
     }

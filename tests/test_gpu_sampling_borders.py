@@ -131,3 +131,27 @@ def test_min_p_beside_a_border(V, n, dtype):
         for setting, taken in ((low, 0), (high, V - 1)):
             values.append({0: l, V - 1: top}), m.append(setting), t.append(temp), want.append(taken)
     assert pkg.sample_tokens(rows(values, V, dtype), column([0.0] * len(m)), temperature=column(t), min_p=column(m)).tolist() == want
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [3, 9001])
+def test_min_p_of_every_size(V, dtype):
+    """From 2^-43 of the largest weight up: a third of min_p's weight is not kept, three times it is. (Such settings are no whole
+    numbers of 2^-44, and are rounded up.)"""
+    values, m, u, want = [], [], [], []
+    for e in range(1, 44):
+        for f in (1.0, 1.0 + 2.0 ** -23, 1.5, 2.0 - 2.0 ** -23):
+            setting = np.float32(f * 2.0 ** -e)
+            for part, taken in ((1 / 3, 0), (3.0, V - 1)):
+                if setting * part < 0.9:  # tokens 1 and 0 of weight 1, the last of min_p's weight times `part`
+                    values.append({0: 0.0, V - 1: math.log(float(setting) * part)})
+                    m.append(setting), u.append(1.0 - 2.0 ** -24), want.append(taken)
+    u = column(u)
+    got = pkg.sample_tokens(rows(values, V, dtype), u, min_p=column(m)).tolist()
+    # the last token's own weight is drawn only where it is at least 2^-24 of the sum
+    seen = [i for i, v in enumerate(values) if v[V - 1] > -16.0 or want[i] == 0]
+    assert [got[i] for i in seen] == [want[i] for i in seen]
+    # reversed, it comes first and is drawn by u = 0
+    back = [{0: v[V - 1], V - 1: v[0]} for v in values]
+    got = pkg.sample_tokens(rows(back, V, dtype), torch.zeros_like(u), min_p=column(m)).tolist()
+    assert got == [V - 1 if w == 0 else 0 for w in want]
