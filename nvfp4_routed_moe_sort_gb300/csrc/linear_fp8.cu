@@ -35,8 +35,50 @@ namespace moe {
 namespace {
 
 constexpr int kGroup = MOE_FP8_GROUP;
-// within 2^-20 of itself, far below the rounding to BF16 that follows
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// 2^x to 2^-22 of itself, 0 where that is no normal number; 1 / x to 2^-23 for 1 <= x <= 2
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two values an instruction
+struct Two {
+  float x, y;
+};
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+// g / (1 + e^-g) by e = e^-|g|, which cannot overflow: the square of a power of two, whose exponent's rounding is made good, so
+// that e is right where it is no normal number any more. Within 2^-19 of itself down to g = -87, and to 2^-148 |g| below, far
+// under the rounding to BF16 that follows. 4096 x 4096 x 1024 with SwiGLU: 24.2 us; with expf and an IEEE quotient 35, one value an
+// instruction 24.9.
+__device__ __forceinline__ Two silu(Two g) {
+  constexpr float kHigh = 0.5f * 1.44269502f, kLow = 0.5f * 1.92596299e-8f;  // log2(e) / 2 as two floats
+  const Two a = {fminf(fabsf(g.x), 256.0f), fminf(fabsf(g.y), 256.0f)};      // an infinity would leave no rest of its own
+  const Two p = mul2(a, {-kHigh, -kHigh}), rest = fma2(a, {kLow, kLow}, fma2(a, {kHigh, kHigh}, p));
+  Two h = {exp2_approx(p.x), exp2_approx(p.y)};
+  h = fma2(h, mul2(rest, {-0.693147181f, -0.693147181f}), h);
+  const Two ge = mul2(g, mul2(h, h)), d = fma2(h, h, {1.0f, 1.0f});
+  return mul2({g.x < 0.0f ? ge.x : g.x, g.y < 0.0f ? ge.y : g.y}, {rcp_approx(d.x), rcp_approx(d.y)});
+}
+__device__ __forceinline__ float silu(float g) { return silu(Two{g, g}).x; }
 __device__ __forceinline__ float gelu(float x) {
   return __fmul_rn(__fmul_rn(0.5f, x), __fadd_rn(1.0f, erff(__fmul_rn(x, 0.70710678118654752f))));
 }
@@ -99,6 +141,22 @@ __device__ __forceinline__ void store_cluster4(uint32_t at, float a, float b, fl
 }
 
 __host__ __device__ constexpr bool is_gated(int act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
+
+// a thread's N results from its sums; of the gated kinds from N of gate and, behind them, N of up
+template <int ACT, int N>
+__device__ __forceinline__ void activate_all(float* v) {
+  if constexpr (ACT == MOE_ACT_SWIGLU || ACT == MOE_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      Two y = silu(Two{v[i], v[i + 1]});
+      if constexpr (ACT == MOE_ACT_SWIGLU) y = mul2(y, {v[N + i], v[N + i + 1]});
+      v[i] = y.x, v[i + 1] = y.y;
+    }
+  } else if constexpr (ACT != MOE_ACT_IDENTITY) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = activate(ACT, v[i], is_gated(ACT) ? v[N + i] : 0.0f);
+  }
+}
 
 struct Fp8Args {
   CUtensorMap tmap_x, tmap_w;
@@ -403,10 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_kernel(const __grid_co
       if (++stage == a.stages) stage = 0, phase ^= 1;
     }
     if (a.slices == 1) {
-      if constexpr (ACT != MOE_ACT_IDENTITY) {
-#pragma unroll
-        for (int i = 0; i < (GATED ? 32 : 64); ++i) acc[i] = activate(ACT, acc[i], GATED ? acc[32 + (i & 31)] : 0.0f);
-      }
+      activate_all<ACT, GATED ? 32 : 64>(acc);
       store_row<GATED ? 32 : 64, GATED>(a, acc, static_cast<int64_t>(m0) + r, n0 + half * (GATED ? 32 : 64));
     } else {
       cluster_wait();  // every block of the cluster runs
@@ -769,10 +824,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_fp8_pair_kernel(const 
       place(t, m0, n0);
       constexpr int kMine = GATED ? 64 : 128;            // columns of out
       const int c0 = n0 + half * kMine;
-      if constexpr (ACT != MOE_ACT_IDENTITY) {
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) acc[i] = activate(ACT, acc[i], GATED ? acc[64 + (i & 63)] : 0.0f);
-      }
+      activate_all<ACT, kMine>(acc);
       store_row<kMine, GATED>(a, acc, static_cast<int64_t>(m0) + rank * 128 + quarter * 32 + lane, c0);
     }
   }
