@@ -519,8 +519,10 @@ MOE_API moe_status_t moe_quantize_fp8(const uint16_t* x, int64_t ld_x, int32_t M
  *                 whole blocks), and write N/2 columns; MOE_ACT_IDENTITY is a plain product
  *   out           [M, N] (gated: [M, N/2]) BF16, contiguous: FP32 sums, one rounding at the end
  *   dev_status    may be NULL
- * Products of a block of 128 are summed by the tensor core in FP32, then scaled and added in FP32. NaN codes
- * make NaN outputs in their row (of x) or column (of w). K % 16 == 0, K <= 65536, M and N <= 2^22.
+ * Products of a block of 128 are summed by the tensor core in FP32, then scaled and added in FP32, by the FP32 product of the
+ * block's two scales: that product is to be 0 or a normal number (2^-126 to 2^128; a larger one counts as infinite and makes NaN of a
+ * sum of 0, a smaller one has fewer bits). NaN codes make NaN outputs in their row (of x) or column (of w). K % 16 == 0,
+ * K <= 65536, M and N <= 2^22.
  * M == 0 is a no-op.
  * ---------------------------------------------------------------------------------------- */
 MOE_API moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int32_t x_scale_mode,

@@ -144,8 +144,8 @@ def fp8_linear(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
 
     x [M, K] float8_e4m3fn with x_scale f32 [M, 1] or [M, ceil(K / 128)] (as ``add_rms_norm`` and ``quantize_fp8``
     give them); it may have a row stride. K is a multiple of 16. Gated activations take w rows [gate; up], N a
-    multiple of 256. Returns [M, N] (gated: [M, N / 2]) bf16. dev_status: an int32 tensor whose first
-    element collects MOE_DEV_* bits.
+    multiple of 256. The product of a block's two scales is 0 or a normal float32 number. Returns [M, N] (gated:
+    [M, N / 2]) bf16. dev_status: an int32 tensor whose first element collects MOE_DEV_* bits.
     """
     act = L.ACTIVATIONS.get(activation)
     if act is None:

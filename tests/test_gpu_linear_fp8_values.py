@@ -5,9 +5,11 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_harness import DEV, bf16_np, pkg
+from gpu_harness import DEV, bf16_np, pkg, to_np
 from oracle import formats as F
-from test_gpu_serving import F8, up
+from oracle import serving as S
+from test_gpu_decoder import assert_within, f32_np
+from test_gpu_serving import F8, U, up
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +79,29 @@ def test_silu_of_gates_without_bounds(act):
         want = F.bf16_round(g.astype(np.float64) / (1 + np.exp(-g.astype(np.float64))) * (g if act == "swiglu" else 1.0))
     assert np.array_equal(got[:11], want[:11])
     assert got[11] == np.inf and np.isnan(got[12:]).all()
+
+
+@pytest.mark.parametrize("kind", ["high", "low"])
+@pytest.mark.parametrize("M,N,K", [(5, 300, 1024), (130, 140, 512), (20000, 300, 512)])  # slices, whole tiles, pairs
+def test_scales_at_the_ends_of_their_range(M, N, K, kind):
+    """Products of two scales up to 2^126 and down to 2^-126, the scales themselves far beyond: against float64 by the bound of a 32-bit
+    sum of 128 + K / 128 terms, half a BF16 step, and half of BF16's smallest step for what is below the normal numbers."""
+    r = np.random.default_rng(M + 3 * N + K)
+    groups = -(-K // 128)
+    xs, ws = r.uniform(1, 2, (M, groups)), r.uniform(1, 2, (-(-N // 128), groups))
+    x, w = r.choice([-1.0, 0.0, 1.0], (M, K)), r.choice([-1.0, 0.0, 1.0], (N, K))
+    one, other = r.random((1, groups)) < 0.5, np.exp2(np.where(r.random((M, 1)) < 0.5, 0, 3 if kind == "low" else -3))
+    if kind == "high":  # codes of 2^-9 and 2^-6
+        x, w = x * 2.0 ** -9, w * 2.0 ** -6
+        xs, ws = xs * np.where(one, 2.0 ** 120, 2.0 ** 4) * other, ws * np.where(one, 2.0 ** 4, 2.0 ** 120)
+    else:
+        x, w = x * 448, w * 448
+        xs, ws = xs * np.where(one, 2.0 ** -126, 1.0) * other, ws * np.where(one, 1.0, 2.0 ** -126)
+    xs, ws = xs.astype(np.float32), ws.astype(np.float32)
+    product = xs.astype(np.float64)[:, :, None] * ws.astype(np.float64).T[None]
+    assert product.max() < 2.0 ** 127 if kind == "high" else product.min() >= 2.0 ** -126
+    c = up(x.astype(np.float32), F8), up(xs), up(w.astype(np.float32), F8), up(ws)
+    at = np.unique(np.r_[0:min(M, 200), max(0, M - 60):M])
+    out, _, mass = S.fp8_linear(f32_np(c[0][at]), xs[at], f32_np(c[2]), ws)
+    tol = np.abs(out) * 2.0 ** -8 + mass * (128 + groups + 8) * U + 2.0 ** -134
+    assert_within(bf16_np(pkg.fp8_linear(*c)[torch.from_numpy(at).to(DEV)]), out, tol, kind)
