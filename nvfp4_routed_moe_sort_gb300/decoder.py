@@ -157,18 +157,23 @@ def fp8_linear(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale:
 
 
 class FP8Linear:
-    """One dense E4M3 matrix with a scale per 128 x 128 block: a projection of a prompt's or a batch's tokens."""
+    """One dense E4M3 matrix with a scale per 128 x 128 block: a projection of a prompt's or a batch's tokens.
 
-    def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, activation: str = "identity"):
+    dev_status: an int32 tensor whose first element collects the calls' MOE_DEV_* bits, the layer's own where none is given.
+    A result is whole as long as it is 0: layers may share one, and a program looks at it where it waits for the GPU anyway.
+    """
+
+    def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, activation: str = "identity", dev_status: torch.Tensor | None = None):
         self.w, self.w_scale, self.activation = w, w_scale, activation
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=w.device) if dev_status is None else dev_status
 
     @classmethod
-    def from_bf16(cls, w: torch.Tensor, activation: str = "identity") -> "FP8Linear":
+    def from_bf16(cls, w: torch.Tensor, activation: str = "identity", dev_status: torch.Tensor | None = None) -> "FP8Linear":
         """Encodes w [N, K] bf16 with moe_quantize_fp8."""
-        return cls(*quantize_fp8(w, rows=L.MOE_FP8_GROUP), activation)
+        return cls(*quantize_fp8(w, rows=L.MOE_FP8_GROUP), activation, dev_status)
 
     def __call__(self, x, x_scale, out=None):
-        return fp8_linear(x, x_scale, self.w, self.w_scale, self.activation, out)
+        return fp8_linear(x, x_scale, self.w, self.w_scale, self.activation, out, self.dev_status)
 
 
 def rotary(q: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, k: torch.Tensor | None = None,

@@ -105,3 +105,23 @@ def test_scales_at_the_ends_of_their_range(M, N, K, kind):
     out, _, mass = S.fp8_linear(f32_np(c[0][at]), xs[at], f32_np(c[2]), ws)
     tol = np.abs(out) * 2.0 ** -8 + mass * (128 + groups + 8) * U + 2.0 ** -134
     assert_within(bf16_np(pkg.fp8_linear(*c)[torch.from_numpy(at).to(DEV)]), out, tol, kind)
+
+
+def test_a_layers_status_word():
+    """Calls of every kind that end as they should leave it 0, also in a captured graph; a word elsewhere is refused."""
+    word = torch.zeros(2, dtype=torch.int32, device=DEV)
+    r = np.random.default_rng(3)
+    layers = [pkg.FP8Linear.from_bf16(up(r.normal(size=s).astype(np.float32)).bfloat16(), dev_status=word if i else None)
+              for i, s in enumerate(((300, 1024), (1024, 300 // 16 * 16), (40, 1024)))]
+    inputs = [pkg.quantize_fp8(up(r.normal(size=(M, layer.w.shape[1])).astype(np.float32)).bfloat16()) for M, layer in zip((5, 20000, 200), layers)]
+    for layer, x in zip(layers, inputs):
+        layer(*x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        results = [layer(*x) for layer, x in zip(layers, inputs)]
+    graph.replay()
+    assert all(torch.equal(y, layer(*x)) for y, layer, x in zip(results, layers, inputs))
+    assert layers[1].dev_status is word and layers[0].dev_status is not word
+    assert not word.any() and not layers[0].dev_status.any()
+    with pytest.raises(ValueError, match="dev_status must be int32"):
+        pkg.FP8Linear(layers[0].w, layers[0].w_scale, dev_status=word.cpu())(*inputs[0])
