@@ -540,7 +540,7 @@ MOE_API moe_status_t moe_linear_fp8(const uint8_t* x, int64_t ld_x, const float*
  *   k           the same with num_k_heads, or NULL with num_k_heads 0
  *   head_dim    up to 1024; rotary_dim even, 2 to head_dim
  *   positions   [num_axes, ld_positions] int32 or int64 (position_bytes 4 or 8), the first N of a row used; any
- *               sign
+ *               sign. ld_positions >= N, or 0: all axes read one row (text, to a model of several axes)
  *   num_axes    1 to 4: one for text; time, height and width for images and video
  *   inv_freq    [rotary_dim / 2] float64, finite: radians per position
  *   axes        [rotary_dim / 2] uint8: the axis of each pair, or NULL with one axis. A pair of an axis

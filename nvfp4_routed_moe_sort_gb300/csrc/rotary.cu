@@ -261,7 +261,7 @@ extern "C" moe_status_t moe_rotary(const uint16_t* q, int64_t ld_q, int32_t num_
             MOE_ERR_INVALID_ARGUMENT);
   MOE_CHECK(position_bytes == 4 || position_bytes == 8, MOE_ERR_INVALID_ARGUMENT);
   MOE_CHECK(head_dim <= kMaxHeadDim && num_axes <= kMaxAxes && num_q_heads <= 1024 && num_k_heads <= 1024, MOE_ERR_UNSUPPORTED_SHAPE);
-  MOE_CHECK(num_axes == 1 || ld_positions >= N, MOE_ERR_INVALID_ARGUMENT);
+  MOE_CHECK(num_axes == 1 || ld_positions >= N || ld_positions == 0, MOE_ERR_INVALID_ARGUMENT);  // 0: one row for every axis
   const int64_t wq = static_cast<int64_t>(num_q_heads) * head_dim, wk = static_cast<int64_t>(num_k_heads) * head_dim;
   MOE_CHECK(ld_q >= wq && ld_q_out >= wq && (num_k_heads == 0 || (ld_k >= wk && ld_k_out >= wk)), MOE_ERR_INVALID_ARGUMENT);
   if (N == 0) return MOE_OK;

@@ -182,8 +182,8 @@ def rotary(q: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, k: 
     """Queries q [N, num_q_heads, head_dim] bf16 and keys k [N, num_k_heads, head_dim] (or None) turned by their
     tokens' positions: (q_out, k_out).
 
-    positions [N], or [num_axes, N] with up to four axes (time, height and width, say), int32 or int64;
-    inv_freq float64 [rotary_dim / 2], radians per position; axes uint8 [rotary_dim / 2], the axis of each pair (needed
+    positions [N], or [num_axes, N] with up to four axes (time, height and width, say; one row expanded to all of them
+    will do), int32 or int64; inv_freq float64 [rotary_dim / 2], radians per position; axes uint8 [rotary_dim / 2], the axis of each pair (needed
     with several axes). Pairs are values (i, i + rotary_dim / 2) of a head, or (2 i, 2 i + 1) with ``adjacent``;
     values past rotary_dim stay. q and k may have a token stride (slices of one projection's output will
     do). ``out``: the results' own tensors, with a token stride if need be; (q, k) turns them in place.
