@@ -563,9 +563,10 @@ MOE_API moe_status_t moe_rotary(const uint16_t* q, int64_t ld_q, int32_t num_q_h
  *            (>= 1 or NaN: all)
  *   min_p    the tokens with w >= min_p, those with the largest logit always (<= 0 or NaN: all)
  * and the token taken is, among the kept ones in the order of their index, the first at which the cumulated
- * weight passes uniform times their sum. Weights have 34 significant bits (nothing is left below 2^-44 of the largest)
- * and sums are exact, so that the token is that of exact arithmetic unless uniform or a filter's setting lies within about
- * 2^-34 of a border between two tokens.
+ * weight passes uniform times their sum. A weight is right to 2^-34 of itself and rounded down to a whole number of 2^-44 of the
+ * largest one (below that it is 0); sums are exact. So the token is that of exact arithmetic unless uniform or top_p lies within
+ * 2^-33 of a border between two tokens (as parts of the sum) and, for each token that may be kept, 2^-44 more: 2^-26 in all where 2^18
+ * tokens have weights of a few 2^-44; for min_p the border is a weight, right to the same 2^-34 and 2^-44.
  *   logits       [B, ld_logits] FP32 or BF16 (logits_dtype), first V columns used; V <= 2^18. -infinity masks
  *                a token, NaN too; a row with nothing else gives -1; +infinity leaves the other tokens no weight
  *   uniform      [B] FP32 in [0, 1): one random number per row (outside: the nearest one inside; NaN: 0)

@@ -14,9 +14,10 @@
 // in shared memory, if it fits. Long rows of BF16 logits are counted by their values instead, which are few.
 //
 // Weights are whole numbers, 2^44 for the largest logit, so that sums are exact in any order and every
-// block of a row sees the same ones. A weight is right to 2^-34 of itself (2^-37 on average) and to a unit: of 131072
-// tokens of like weight the border at which one token follows the next moves by less than 2^-18 of a token's width. (With
-// float32 exponentials it moves by hundredths, and now and then another token is taken than in exact
+// block of a row sees the same ones. A weight is right to 2^-34 of itself (2^-37 on average) and rounded down to a unit. Of 131072
+// tokens of like weight the border at which one token follows the next moves by less than 2^-18 of a token's width; the units that
+// many small weights lose move it by 2^-44 of the largest each, 2^-26 where 2^18 weights are a unit or two. (With
+// float32 exponentials it moves by hundredths of a token, and now and then another token is taken than in exact
 // arithmetic.) exp2 in pieces: 1024 steps from a table, a polynomial of degree 2 for the rest, the argument
 // carried as two floats.
 //

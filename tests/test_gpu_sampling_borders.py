@@ -155,3 +155,29 @@ def test_min_p_of_every_size(V, dtype):
     back = [{0: v[V - 1], V - 1: v[0]} for v in values]
     got = pkg.sample_tokens(rows(back, V, dtype), torch.zeros_like(u), min_p=column(m)).tolist()
     assert got == [V - 1 if w == 0 else 0 for w in want]
+
+
+@pytest.mark.parametrize("units", [1.02, 1.5, 1.99, 3.99, 100.9])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [3000, 1 << 18])
+def test_a_long_tail_of_weights_of_a_few_units(V, dtype, units):
+    """Many tokens of `units` times 2^-44, then one of 2^-12, then one of weight 1. Each may lose a unit: the borders lie within
+    V units and 2^-33 of the exact ones, and beyond that the token is the exact one's; nothing is drawn that has no weight."""
+    logits = torch.full((V,), math.log(units * 2.0 ** -44))
+    logits[-2], logits[-1] = math.log(2.0 ** -12), 0.0
+    logits = logits.to(dtype)
+    w = np.exp(logits.double().numpy())
+    ends = np.cumsum(w) / w.sum()
+    before, middle = ends[-3], ends[-2]
+    bound = V * 2.0 ** -44 + 2.0 ** -33 + units * 2.0 ** -43  # and the one that top_k takes out
+    u = [middle + bound, middle - bound, before + bound, 0.999]
+    want = [V - 1, V - 2, V - 2, V - 1]
+    if before > bound:
+        u.append(before - bound)
+    u = np.float32(u)
+    u[0], u[1], u[2] = np.nextafter(u[0], np.float32(1)), np.nextafter(u[1], np.float32(0)), np.nextafter(u[2], np.float32(1))
+    x = logits.to(DEV).expand(len(u), V).contiguous()
+    for kw in ({}, dict(top_k=column([V - 1] * len(u), torch.int32))):
+        got = pkg.sample_tokens(x, column(u), **kw).tolist()
+        assert got[:4] == want
+        assert all(0 <= t < V - 2 for t in got[4:])
