@@ -166,7 +166,7 @@ struct Fp8Args {
   uint16_t* out;
   int32_t* status;
   uint64_t wait_ns;
-  int M, N, K, groups, act;
+  int M, N, K, groups;
   int xs_step, xs_ld;  // per 128 columns and per row: 1 and groups, or 0 and 1
   int cols;            // of out: N, or N / 2
   int slices, m_tiles, x_rows, wide, stages, stage_bytes;
@@ -918,7 +918,7 @@ moe_status_t linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, in
   Fp8Args a = {};
   a.xs = x_scale, a.ws = w_scale, a.out = out, a.status = dev_status, a.wait_ns = topt.wait_limit_ns;
   a.withhold = topt.withhold_release;
-  a.M = M, a.N = N, a.K = K, a.groups = groups, a.act = activation, a.cols = cols;
+  a.M = M, a.N = N, a.K = K, a.groups = groups, a.cols = cols;
   a.xs_step = per_token ? 0 : 1, a.xs_ld = per_token ? 1 : groups;
   bool pairs = false;
   const moe_status_t st = use_pairs(M, cols, groups, gated, pairs);
