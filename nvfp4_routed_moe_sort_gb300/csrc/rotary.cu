@@ -15,6 +15,10 @@
 // next one before it writes; what is not turned is copied while the phases are made. Measured: 8 tokens of 20 heads of
 // 128 2.7 us (a launch), 4099 tokens of 32 heads, three quarters of each turned, 14 us (4.7 TB/s with what is copied),
 // 16384 tokens of 72 heads 93 us (6.5 TB/s, 95 % of the copy rate; 109 with phases that met in shared memory's banks).
+//
+// Where rotary_dim is not of 16, head_dim or a stride not of 8, or an address not of 16 bytes, pairs go by the value (two loads and
+// stores of two bytes, a division for the pair's head): of those 16384 tokens with 124 of 128 values turned 178 us, with 62
+// 234 (64: 97), with 62 of heads of 127 186; 8 tokens of 20 heads 3.6 us (1.9 aligned, one call after another).
 #include "common.cuh"
 #include "host_util.h"
 
@@ -79,7 +83,8 @@ __device__ __forceinline__ int axis_of(const RotaryArgs& a, int i, uint64_t& tur
 __device__ __forceinline__ float value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 __device__ __forceinline__ uint16_t bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// Any sizes and places: one block per token, its phases first, then its heads pair by pair.
+// Any sizes and places, at two to two and a half times the aligned ones' time: one block per token, its phases first, then its
+// heads pair by pair.
 __global__ void __launch_bounds__(256) rotary_odd_kernel(RotaryArgs a) {
   __shared__ float2 phase[kMaxHeadDim / 2];
   pdl_wait();
