@@ -3,8 +3,8 @@
 //   y[m, n] = act(sum_b xs[m, b] * ws[n / 128, b] * sum_{k in block b} x[m, k] * w[n, k])
 //
 // The products of a block b of K run on tcgen05 (kind::f8f6f4, FP32 sums in TMEM). Its scales are any FP32
-// numbers whose product is one (a look at every product's size, and a factor for the sums where it is none, costs 2 to 6 % of all
-// calls), so that its sums leave TMEM every 128 of K: warps of sums read them into registers, free the accumulator at
+// numbers whose product is a normal one or 0 (to carry those where it is not costs 2 to 6 % of every call's time), so that its
+// sums leave TMEM every 128 of K: warps of sums read them into registers, free the accumulator at
 // once, and add them times their scale to the tile's sums there, while the tensor core makes the next blocks'.
 //
 // What bounds it. Few tokens: the bytes of w, and a chain of launch, first load, sums and the slices' meeting of about

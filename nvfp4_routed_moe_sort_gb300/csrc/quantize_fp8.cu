@@ -10,8 +10,9 @@
 // launch), 16384 x 7160 55 us (60; 6.4 TB/s, 95 % of the copy rate; 70 with each lane making every group's divisions),
 // 7168 x 16384 in blocks 52 us (58).
 //
-// Rows of odd lengths or at odd addresses go by the value, two bytes in and one out: a row's 16-byte pieces do not lie at multiples of 16. That is
-// bound by the number of loads and stores: 16384 x 7161 145 us, 7168 x 16383 in blocks 412 us, 8 x 2047 1.5 us.
+// Rows of odd lengths or at odd addresses go by the value, two bytes in and one out: a row's 16-byte pieces do not lie at
+// multiples of 16. That is bound by the number of loads and stores: 16384 x 7161 145 us, 7168 x 16383 in blocks 412 us,
+// 8 x 2047 1.5 us.
 #include <math.h>
 
 #include "common.cuh"

@@ -183,10 +183,10 @@ def rotary(q: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, k: 
     tokens' positions: (q_out, k_out).
 
     positions [N], or [num_axes, N] with up to four axes (time, height and width, say; one row expanded to all of them
-    will do), int32 or int64; inv_freq float64 [rotary_dim / 2], radians per position; axes uint8 [rotary_dim / 2], the axis of each pair (needed
-    with several axes). Pairs are values (i, i + rotary_dim / 2) of a head, or (2 i, 2 i + 1) with ``adjacent``;
-    values past rotary_dim stay. q and k may have a token stride (slices of one projection's output will
-    do). ``out``: the results' own tensors, with a token stride if need be; (q, k) turns them in place.
+    will do), int32 or int64; inv_freq float64 [rotary_dim / 2], radians per position; axes uint8 [rotary_dim / 2], the
+    axis of each pair (needed with several axes). Pairs are values (i, i + rotary_dim / 2) of a head, or (2 i, 2 i + 1)
+    with ``adjacent``; values past rotary_dim stay. q and k may have a token stride (slices of one projection's output
+    will do). ``out``: the results' own tensors, with a token stride if need be; (q, k) turns them in place.
     dev_status: an int32 tensor whose first element collects MOE_DEV_* bits.
     """
     if out is None:
